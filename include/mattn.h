@@ -247,6 +247,145 @@ attn_status attn_combine(const void* o_parts, const float* lse_parts, int n_part
 attn_status attn_doc_ids_from_seqlens(const int* cu_seqlens, int n, int total, int* doc_id,
                                       struct CUstream_st* stream);
 
+/* A [B, H, S, D] tensor of any strides (in elements), D contiguous. `data`
+ * is 16-byte aligned and every stride of a dimension longer than 1 is a
+ * multiple of 16 bytes, >= 0. */
+typedef struct attn_view {
+  void* data;
+  long long stride_b, stride_h, stride_s;
+} attn_view;
+
+/* Page tables and slot maps of a serving step, from the requests' lengths.
+ * Request b (of B) holds cached_lens[b] tokens in the first
+ * ceil(cached / page_size) entries of page_table[b] and gets new_lens[b] more
+ * (0 for an empty place of the batch; a negative length counts as 0). Pages it
+ * then needs beyond those are taken from free_pages in order, request by
+ * request, and written to its next entries; other entries stay as they are.
+ *   seq_lens   int32 [B]          cached + new
+ *   cu_new     int32 [B + 1]      cumulative new lengths (cu_new[0] = 0)
+ *   slots      int64 [max_tokens] page * page_size + position % page_size of
+ *                                 each new token, packed request by request
+ *   positions  int32 [max_tokens] its position in its sequence
+ *   seq_ids    int32 [max_tokens] its request
+ *   info       int32 [4]          new tokens, pages taken, pages lacking,
+ *                                 requests longer than their table
+ * Entries past the last new token are -1 (attn_qk_norm_rope and the cache
+ * calls skip them, so a captured graph may keep max_tokens fixed); new tokens
+ * past max_tokens are dropped. A page that free_pages cannot give is entered
+ * as -1, and tokens without a page (that one, or past pages_per_seq) get slot
+ * -1: info tells. page_size 16, 32, 64 or 128; B <= 16384 (else
+ * ATTN_ERR_UNSUPPORTED). No two arguments may overlap. Asynchronous on
+ * `stream`, one launch. */
+attn_status attn_page_plan(const int* cached_lens, const int* new_lens, int B, int* page_table,
+                           int pages_per_seq, int page_size, const int* free_pages, int num_free,
+                           int* seq_lens, int* cu_new, long long* slots, int* positions,
+                           int* seq_ids, int max_tokens, int* info, struct CUstream_st* stream);
+
+/* Parameters of the norm and rotation of queries and keys (host struct). */
+typedef struct attn_rope_params {
+  int dtype;              /* ATTN_BF16 or ATTN_F32: type of the tensors */
+  float eps;              /* >= 0, added to the mean of squares */
+  const float* q_weight;  /* device fp32 [D], or NULL: no norm of the queries */
+  const float* k_weight;  /* device fp32 [D], or NULL: no norm of the keys */
+  const float* cos_sin;   /* device fp32 [max_pos][rot_dim], 16-byte aligned: rot_dim / 2
+                             cosines, then as many sines; NULL: no rotation */
+  int max_pos;
+  int rot_dim;            /* leading channels that are rotated: a multiple of 16, <= D */
+  int interleaved;        /* pairs (2i, 2i + 1) if nonzero, else (i, i + rot_dim / 2) */
+  const int* positions;   /* device int32 [B][S], or NULL: position s */
+} attn_rope_params;
+
+/* Per-head RMS norm and position rotation of queries and keys, one pass:
+ *   y = x / sqrt(mean(x^2) + eps) * weight,
+ *   out[c] = y[c] cos_i - y[c'] sin_i,  out[c'] = y[c'] cos_i + y[c] sin_i
+ * for the i-th channel pair (c, c') and row `position` of cos_sin; channels
+ * from rot_dim on are y. q and q_out are [B, Hq, S, D], k and k_out
+ * [B, Hkv, S, D], each with strides of its own: the inputs may be slices of a
+ * projection's output, the outputs what attn_fwd takes. Hq or Hkv may be 0
+ * (its tensors are then not used). q_out may be q itself with the same strides
+ * (k likewise); no other overlap. With cos_sin, a row whose position lies
+ * outside [0, max_pos) is not written (places of a padded batch). D is 64 or
+ * 128. Sums are fp32; each output is rounded once. Asynchronous on `stream`. */
+attn_status attn_qk_norm_rope(const attn_view* q, const attn_view* k, const attn_view* q_out,
+                              const attn_view* k_out, int B, int Hq, int Hkv, int S, int D,
+                              const attn_rope_params* p, struct CUstream_st* stream);
+
+/* Bytes of workspace attn_qk_norm_rope_bwd() needs (the weights' partial sums). */
+size_t attn_qk_norm_rope_bwd_workspace_bytes(int D);
+
+/* Gradient of attn_qk_norm_rope: from its inputs q, k and the gradients
+ * dq_out, dk_out of its outputs computes dq, dk (rows that the forward did not
+ * write are not written and add nothing) and dq_weight, dk_weight (device fp32
+ * [D], summed over every row; NULL: not wanted, and invalid for a weight that
+ * is NULL). q (k) is not read and may be NULL when its weight is NULL. dq may
+ * be dq_out itself with the same strides. No atomics: results are bitwise
+ * reproducible. The workspace is 256-byte aligned device memory whose contents
+ * need not be kept between calls. */
+attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view* k, const attn_view* dq_out,
+                                  const attn_view* dk_out, const attn_view* dq,
+                                  const attn_view* dk, float* dq_weight, float* dk_weight,
+                                  void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                                  int S, int D, const attn_rope_params* p,
+                                  struct CUstream_st* stream);
+
+/* The 4-bit paged key/value cache. A pool is num_pages * Hkv records, record
+ * (page, head) being
+ *   K codes  [page_size][D / 2]   bytes: channel 2b in the low nibble of byte
+ *   V codes  [page_size][D / 2]   b, channel 2b + 1 in the high one
+ *   K scales [page_size][D / 32]  bf16, one per 32 consecutive channels
+ *   V scales [page_size][D / 32]  bf16
+ * and a code n stands for (n - 8) * scale (4.5 bits an element). D is 64 or
+ * 128, page_size 16, 32, 64 or 128. The pool is 16-byte aligned. */
+size_t attn_cache_q4_bytes(int num_pages, int Hkv, int page_size, int D);
+
+/* Writes K and V rows (bf16 [B, Hkv, S, D], strides of their own) to slots
+ * (device int64 [B][S]; page = slot / page_size). Per 32 channels
+ * scale = bf16(max|x| / 7) and code = clamp(rint(x / scale), -8, 7) + 8, ties
+ * to even; a zero scale stores code 8, and a group with an infinity or NaN
+ * gets scale NaN (it reads back as NaN). A slot outside
+ * [0, num_pages * page_size) is skipped. The slots of one call must differ:
+ * what two tokens write to the same slot is unspecified. Asynchronous on
+ * `stream`. */
+attn_status attn_cache_store_q4(const attn_view* k, const attn_view* v, const long long* slots,
+                                void* pool, int num_pages, int page_size, int B, int Hkv, int S,
+                                int D, struct CUstream_st* stream);
+
+/* Reads the rows at `slots` back as bf16 (one rounding), e.g. a cached
+ * prefix that attn_fwd attends to as a packed batch. A slot outside the pool
+ * reads as zeros; slots may repeat. */
+attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
+                               const long long* slots, const attn_view* k, const attn_view* v,
+                               int B, int Hkv, int S, int D, struct CUstream_st* stream);
+
+/* attn_decode over a 4-bit paged cache and sequences of their own lengths.
+ * q, o [B, Hq, Sq, D] bf16 and lse fp32 [B, Hq, Sq] as for attn_decode, with
+ * (Hq / Hkv) * Sq <= 16. seq_lens (device int32 [B]) counts each sequence's
+ * keys, its Sq query rows' own tokens included: row r sits at absolute
+ * position i = seq_lens[b] - Sq + r and key j at j. max_len bounds seq_lens
+ * on the host (a length outside [0, max_len] counts as the nearest bound) and
+ * p->pages_per_seq * page_size must hold it. p gives dtype (ATTN_BF16), scale,
+ * window, softcap, alibi_slopes, page_table, page_size, pages_per_seq and
+ * num_pages; its other fields are not used, except that offsets must be 0.
+ * Variant: ATTN_MASK_CAUSAL, ATTN_MASK_WINDOW, ATTN_SCORE_ALIBI and
+ * ATTN_SCORE_SOFTCAP in any combination (others: ATTN_ERR_UNSUPPORTED), and
+ * with a window the first `sink` keys stay visible:
+ *   keep(i, j) = j < seq_len AND i >= 0 AND (CAUSAL: j <= i)
+ *                AND (WINDOW: i - j < window OR j < sink)
+ * Keys that no row sees are not read, and what a masked key's record holds,
+ * NaN included, changes nothing. A row without a key (an empty place of the
+ * batch) gets O = 0, LSE = -inf. A page index outside [0, num_pages) reads as
+ * zeros. `workspace` as for attn_decode: 256-byte aligned,
+ * attn_decode_q4_workspace_bytes() for the full split count, less or NULL
+ * means fewer splits; its contents need not be kept between calls. */
+attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B, int Hq,
+                           int Hkv, int Sq, int max_len, int D, unsigned variant,
+                           const attn_params* p, const int* seq_lens, int sink, void* workspace,
+                           size_t workspace_bytes, struct CUstream_st* stream);
+
+/* Bytes of workspace attn_decode_q4() uses for its full split count on the
+ * current device (0 when it does not split the keys). */
+size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D);
+
 /* Bytes of device buffer build_block_mask() needs (256-byte aligned pieces). */
 size_t attn_block_mask_bytes(int B, int Sq, int Skv, int transposed);
 

@@ -28,6 +28,9 @@ __all__ = [
     "build_block_mask", "attn_block_mask_bytes", "attn_bwd_workspace_bytes", "attn_bwd_noalloc",
     "attn_check_status", "attn_status_str", "attn_last_cuda_error", "attn_combine", "lib",
     "LIB_PATH", "LIB_DEBUG_PATH", "debug_record", "debug_selftest",
+    "attn_page_plan", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
+    "attn_qk_norm_rope_bwd_workspace_bytes", "attn_cache_q4_bytes", "attn_cache_store_q4",
+    "attn_cache_load_q4", "attn_decode_q4", "attn_decode_q4_workspace_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmattn.so")
@@ -66,6 +69,18 @@ class attn_params(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("pages_per_seq", ctypes.c_int),
                 ("num_pages", ctypes.c_int), ("q_offset", ctypes.c_int),
                 ("kv_offset", ctypes.c_int), ("doc_len", ctypes.c_int)]
+
+
+class attn_view(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("stride_s", ctypes.c_longlong)]
+
+
+class attn_rope_params(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("positions", ctypes.c_void_p)]
 
 
 class attn_debug_info(ctypes.Structure):
@@ -114,6 +129,25 @@ def lib() -> ctypes.CDLL:
         L.attn_decode_workspace_bytes.restype = sz
         L.attn_combine.argtypes = [vp, vp, i, ctypes.c_longlong, i, i, vp, vp, vp]
         L.attn_combine.restype = i
+        V, R = ctypes.POINTER(attn_view), ctypes.POINTER(attn_rope_params)
+        L.attn_page_plan.argtypes = [vp, vp, i, vp, i, i, vp, i, vp, vp, vp, vp, vp, i, vp, vp]
+        L.attn_page_plan.restype = i
+        L.attn_qk_norm_rope.argtypes = [V, V, V, V, i, i, i, i, i, R, vp]
+        L.attn_qk_norm_rope.restype = i
+        L.attn_qk_norm_rope_bwd_workspace_bytes.argtypes = [i]
+        L.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
+        L.attn_qk_norm_rope_bwd.argtypes = [V, V, V, V, V, V, vp, vp, vp, sz, i, i, i, i, i, R, vp]
+        L.attn_qk_norm_rope_bwd.restype = i
+        L.attn_cache_q4_bytes.argtypes = [i, i, i, i]
+        L.attn_cache_q4_bytes.restype = sz
+        L.attn_cache_store_q4.argtypes = [V, V, vp, vp, i, i, i, i, i, i, vp]
+        L.attn_cache_store_q4.restype = i
+        L.attn_cache_load_q4.argtypes = [vp, i, i, vp, V, V, i, i, i, i, vp]
+        L.attn_cache_load_q4.restype = i
+        L.attn_decode_q4.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, u, P, vp, i, vp, sz, vp]
+        L.attn_decode_q4.restype = i
+        L.attn_decode_q4_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.attn_decode_q4_workspace_bytes.restype = sz
         L.attn_check_status.argtypes = [vp, vp]
         L.attn_check_status.restype = i
         L.attn_status_str.argtypes = [i]
@@ -450,6 +484,236 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, variant: int = 0, *,
                                 _ptr(dq), _ptr(dk), _ptr(dv), B, Hq, Hkv, Sq, Skv, D, variant,
                                 ctypes.byref(p), _stream(stream))
     _check(st, "attn_bwd_noalloc")
+
+
+def _tensor(where: str, name: str, x, dtype, device, shape=None):
+    """Checks a tensor argument; contiguous when a shape is given."""
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise ValueError(f"{where}: {name} must be a tensor")
+    if x.dtype != dtype:
+        raise ValueError(f"{where}: {name} must be {dtype}, not {x.dtype}")
+    if x.device != device or not x.is_cuda:
+        raise ValueError(f"{where}: {name} is on {x.device}, not on one CUDA device with the rest")
+    if shape is not None:
+        if tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not "
+                             f"{tuple(x.shape)}")
+        if not x.is_contiguous():
+            raise ValueError(f"{where}: {name} must be contiguous")
+    return x.data_ptr()
+
+
+def _view(where: str, name: str, x, dtype, device, shape) -> attn_view:
+    """A [B, H, S, D] tensor of any strides with contiguous D."""
+    p = _tensor(where, name, x, dtype, device)
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    sb, sh, ss, sd = x.stride()
+    if sd != 1:
+        raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
+    return attn_view(p, sb, sh, ss)
+
+
+def _run(where: str, fn, device, stream, *args) -> None:
+    """Calls fn(*args, stream) on the tensors' device (its current stream unless given)."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, where)
+
+
+def attn_page_plan(cached_lens, new_lens, page_table, free_pages, seq_lens, cu_new, slots,
+                   positions, seq_ids, info, *, page_size: int, stream=None) -> None:
+    """Page tables and slot maps of a serving step, on the device, from the
+    requests' lengths: ``cached_lens`` [B] tokens are held in the pages of
+    ``page_table`` [B, pages_per_seq], ``new_lens`` [B] more come; pages they
+    need are taken from ``free_pages`` in order and entered. Writes ``seq_lens``
+    [B], ``cu_new`` [B + 1], per new token ``slots`` (int64), ``positions`` and
+    ``seq_ids`` [max_tokens] (-1 past the last one), and ``info`` [4]: new
+    tokens, pages taken, pages lacking, requests longer than their table. All
+    int32 but ``slots``. See include/mattn.h."""
+    import torch
+    w, dev, i32 = "attn_page_plan", cached_lens.device, torch.int32
+    B, per = page_table.shape
+    n = slots.shape[0]
+    _run(w, lib().attn_page_plan, dev, stream, _tensor(w, "cached_lens", cached_lens, i32, dev, (B,)),
+         _tensor(w, "new_lens", new_lens, i32, dev, (B,)), B,
+         _tensor(w, "page_table", page_table, i32, dev, (B, per)), per, page_size,
+         _tensor(w, "free_pages", free_pages, i32, dev, (free_pages.numel(),)), free_pages.numel(),
+         _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)),
+         _tensor(w, "cu_new", cu_new, i32, dev, (B + 1,)),
+         _tensor(w, "slots", slots, torch.int64, dev, (n,)),
+         _tensor(w, "positions", positions, i32, dev, (n,)),
+         _tensor(w, "seq_ids", seq_ids, i32, dev, (n,)), n, _tensor(w, "info", info, i32, dev, (4,)))
+
+
+def _rope_params(w: str, x, B, S, D, q_weight, k_weight, eps, cos_sin, positions,
+                 interleaved) -> attn_rope_params:
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{w}: tensors must be bfloat16 or float32, not {x.dtype}")
+    dev, f32 = x.device, torch.float32
+    p = attn_rope_params()
+    p.dtype = F32 if x.dtype == f32 else BF16
+    p.eps = eps
+    if q_weight is not None:
+        p.q_weight = _tensor(w, "q_weight", q_weight, f32, dev, (D,))
+    if k_weight is not None:
+        p.k_weight = _tensor(w, "k_weight", k_weight, f32, dev, (D,))
+    if cos_sin is not None:
+        p.max_pos, p.rot_dim = cos_sin.shape
+        p.cos_sin = _tensor(w, "cos_sin", cos_sin, f32, dev, cos_sin.shape)
+    if positions is not None:
+        p.positions = _tensor(w, "positions", positions, torch.int32, dev, positions.shape)
+        if positions.numel() != B * S:
+            raise ValueError(f"{w}: positions must have {B * S} entries ([B, S])")
+    p.interleaved = int(bool(interleaved))
+    return p
+
+
+def attn_qk_norm_rope(q, k, q_out, k_out, *, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      cos_sin=None, positions=None, interleaved: bool = False,
+                      stream=None) -> None:
+    """Per-head RMS norm of queries and keys and their position rotation, in
+    one pass. ``q``, ``q_out`` [B, Hq, S, D] and ``k``, ``k_out`` [B, Hkv, S,
+    D], bf16 or fp32, of any strides with contiguous D (slices of a fused
+    projection in, the attention's layout out; in place with equal strides);
+    ``k`` and ``k_out`` may be None. ``q_weight``, ``k_weight`` fp32 [D] (None:
+    no norm), ``cos_sin`` fp32 [max_pos, rot_dim] (rot_dim / 2 cosines, then
+    the sines; None: no rotation), ``positions`` int32 [B, S] (None: 0..S-1;
+    rows whose position is outside the table are not written)."""
+    w = "attn_qk_norm_rope"
+    B, Hq, S, D = q.shape
+    Hkv = k.shape[1] if k is not None else 0
+    p = _rope_params(w, q, B, S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
+    v = [ctypes.byref(_view(w, n, x, q.dtype, q.device, (B, H, S, D))) if H else None
+         for n, x, H in (("q", q, Hq), ("k", k, Hkv), ("q_out", q_out, Hq), ("k_out", k_out, Hkv))]
+    _run(w, lib().attn_qk_norm_rope, q.device, stream, *v, B, Hq, Hkv, S, D, ctypes.byref(p))
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
+    return int(lib().attn_qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, *, dq_weight=None, dk_weight=None,
+                          workspace, q_weight=None, k_weight=None, eps: float = 1e-6,
+                          cos_sin=None, positions=None, interleaved: bool = False,
+                          stream=None) -> None:
+    """Gradient of ``attn_qk_norm_rope``: from its inputs ``q``, ``k`` (not
+    read, and may be None, without a norm) and the gradients ``dq_out``,
+    ``dk_out`` of its outputs writes ``dq``, ``dk`` and the weights' gradients
+    ``dq_weight``, ``dk_weight`` (fp32 [D]; None: not wanted). ``workspace``:
+    a CUDA tensor of ``attn_qk_norm_rope_bwd_workspace_bytes(D)`` bytes."""
+    import torch
+    w = "attn_qk_norm_rope_bwd"
+    B, Hq, S, D = dq_out.shape
+    Hkv = dk_out.shape[1] if dk_out is not None else 0
+    dt, dev = dq_out.dtype, dq_out.device
+    p = _rope_params(w, dq_out, B, S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
+    v = [ctypes.byref(_view(w, n, x, dt, dev, (B, H, S, D))) if H and x is not None else None
+         for n, x, H in (("q", q, Hq), ("k", k, Hkv), ("dq_out", dq_out, Hq),
+                         ("dk_out", dk_out, Hkv), ("dq", dq, Hq), ("dk", dk, Hkv))]
+    dw = [None if g is None else _tensor(w, n, g, torch.float32, dev, (D,))
+          for n, g in (("dq_weight", dq_weight), ("dk_weight", dk_weight))]
+    ws = _tensor(w, "workspace", workspace, workspace.dtype, dev, workspace.shape)
+    _run(w, lib().attn_qk_norm_rope_bwd, dev, stream, *v, *dw, ws,
+         workspace.numel() * workspace.element_size(), B, Hq, Hkv, S, D, ctypes.byref(p))
+
+
+def attn_cache_q4_bytes(num_pages: int, Hkv: int, page_size: int, D: int) -> int:
+    """Bytes of a 4-bit cache pool; as a tensor: uint8 [num_pages, Hkv, bytes
+    per record]."""
+    return int(lib().attn_cache_q4_bytes(num_pages, Hkv, page_size, D))
+
+
+def _pool_q4(w: str, pool, Hkv: int, page_size: int, D: int, device):
+    import torch
+    if pool.dim() != 3:
+        raise ValueError(f"{w}: pool must be uint8 [num_pages, Hkv, record bytes]")
+    record = attn_cache_q4_bytes(1, 1, page_size, D)
+    if not record:
+        raise AttnError(ATTN_ERR_UNSUPPORTED, w)
+    return _tensor(w, "pool", pool, torch.uint8, device, (pool.shape[0], Hkv, record))
+
+
+def _cache_q4(w: str, k, v, slots, pool, page_size: int):
+    import torch
+    B, Hkv, S, D = k.shape
+    dev = k.device
+    views = [ctypes.byref(_view(w, n, x, torch.bfloat16, dev, k.shape))
+             for n, x in (("k", k), ("v", v))]
+    ps = _tensor(w, "slots", slots, torch.int64, dev, slots.shape)
+    if slots.numel() != B * S:
+        raise ValueError(f"{w}: slots must have {B * S} entries ([B, S])")
+    return views, ps, _pool_q4(w, pool, Hkv, page_size, D, dev), (B, Hkv, S, D)
+
+
+def attn_cache_store_q4(k, v, slots, pool, *, page_size: int, stream=None) -> None:
+    """Quantises ``k``, ``v`` (bf16 [B, Hkv, S, D], any strides with contiguous
+    D) into the 4-bit ``pool`` (uint8 [num_pages, Hkv, record bytes]) at
+    ``slots`` (int64 [B, S], page * page_size + row, each at most once; a slot
+    outside the pool is skipped). Record layout and rounding: include/mattn.h."""
+    w = "attn_cache_store_q4"
+    views, ps, pp, shape = _cache_q4(w, k, v, slots, pool, page_size)
+    _run(w, lib().attn_cache_store_q4, k.device, stream, *views, ps, pp, pool.shape[0], page_size,
+         *shape)
+
+
+def attn_cache_load_q4(pool, slots, k, v, *, page_size: int, stream=None) -> None:
+    """Reads the rows at ``slots`` of the 4-bit ``pool`` into ``k``, ``v``
+    (bf16 [B, Hkv, S, D], any strides with contiguous D); a slot outside the
+    pool reads as zeros."""
+    w = "attn_cache_load_q4"
+    views, ps, pp, shape = _cache_q4(w, k, v, slots, pool, page_size)
+    _run(w, lib().attn_cache_load_q4, k.device, stream, pp, pool.shape[0], page_size, ps, *views,
+         *shape)
+
+
+def attn_decode_q4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, max_len: int,
+                                   D: int) -> int:
+    return int(lib().attn_decode_q4_workspace_bytes(B, Hq, Hkv, Sq, max_len, D))
+
+
+def attn_decode_q4(q, pool, o, lse, variant: int = 0, *, page_table, page_size: int, seq_lens,
+                   max_len: Optional[int] = None, workspace=None, scale: float = 0.0,
+                   window: int = 0, sink: int = 0, softcap: float = 0.0, alibi_slopes=None,
+                   stream=None) -> None:
+    """Decode over a 4-bit paged cache: ``q`` [B, Hq, Sq, D] bf16 (the last Sq
+    tokens of each sequence, (Hq/Hkv) * Sq <= 16) against the ``seq_lens`` [B]
+    int32 tokens that ``page_table`` [B, pages_per_seq] places in ``pool``
+    (uint8 [num_pages, Hkv, record bytes]). ``max_len`` (default: all the
+    table holds) bounds seq_lens. With ``MASK_WINDOW`` the first ``sink`` keys
+    stay visible. Writes ``o`` (bf16, like q) and ``lse`` fp32 [B, Hq, Sq].
+    ``workspace``: optional CUDA tensor (``attn_decode_q4_workspace_bytes``)."""
+    import torch
+    w, dev = "attn_decode_q4", q.device
+    B, Hq, Sq, D = q.shape
+    pages, Hkv = pool.shape[:2]
+    p = attn_params()
+    p.dtype, p.scale, p.window, p.softcap = BF16, scale, window, softcap
+    if alibi_slopes is not None:
+        p.alibi_slopes = _tensor(w, "alibi_slopes", alibi_slopes, torch.float32, dev, (Hq,))
+    per = page_table.shape[1]
+    p.page_table = _tensor(w, "page_table", page_table, torch.int32, dev, (B, per))
+    p.page_size, p.pages_per_seq, p.num_pages = page_size, per, pages
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws = _tensor(w, "workspace", workspace, workspace.dtype, dev, workspace.shape)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _run(w, lib().attn_decode_q4, dev, stream,
+         _tensor(w, "q", q, torch.bfloat16, dev, q.shape),
+         _pool_q4(w, pool, Hkv, page_size, D, dev),
+         _tensor(w, "o", o, torch.bfloat16, dev, q.shape),
+         _tensor(w, "lse", lse, torch.float32, dev, (B, Hq, Sq)), B, Hq, Hkv, Sq,
+         per * page_size if max_len is None else max_len, D, variant, ctypes.byref(p),
+         _tensor(w, "seq_lens", seq_lens, torch.int32, dev, (B,)), sink, ws, ws_bytes)
 
 
 def attn_check_status(status=None, stream=None) -> int:

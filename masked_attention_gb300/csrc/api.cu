@@ -578,6 +578,10 @@ const DebugTu kDebugTus[] = {
     {debug_fetch_decode, debug_clear_decode},
     {debug_fetch_combine, debug_clear_combine},
     {debug_fetch_mask_build, debug_clear_mask_build},
+    {debug_fetch_page_plan, debug_clear_page_plan},
+    {debug_fetch_norm_rope, debug_clear_norm_rope},
+    {debug_fetch_cache_q4, debug_clear_cache_q4},
+    {debug_fetch_decode_q4, debug_clear_decode_q4},
 };
 
 }  // namespace
@@ -630,6 +634,11 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSiteF32: return "fp32 forward: list entry, document id or bias entry";
     case kSiteMaskBuild: return "block-mask builder: document id or order entry";
     case kSiteSelfTest: return "self-test: planted index";
+    case kSitePlan: return "page plan: page-table or free-list entry";
+    case kSiteRope: return "norm and rotation: row";
+    case kSiteCacheRow: return "4-bit cache: bf16 row";
+    case kSiteQ4Q: return "4-bit decode: query row";
+    case kSiteQ4Out: return "4-bit decode: output or split partial store";
   }
   return "unknown";
 }

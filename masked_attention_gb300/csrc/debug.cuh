@@ -37,6 +37,11 @@ enum DebugSite : int {
   kSiteF32 = 17,          // any access of the fp32 forward
   kSiteMaskBuild = 18,    // block-mask list written by the builder
   kSiteSelfTest = 19,     // the planted index of attn_debug_selftest
+  kSitePlan = 20,         // page-table or free-list entry of the page plan
+  kSiteRope = 21,         // row read or written by the norm and rotation
+  kSiteCacheRow = 22,     // bf16 row of the 4-bit cache's write or read
+  kSiteQ4Q = 23,          // query row of the 4-bit decode
+  kSiteQ4Out = 24,        // output or split partial of the 4-bit decode
   kSiteCount
 };
 

@@ -1,0 +1,696 @@
+// Decode attention over the 4-bit paged cache (record layout: cache_q4.cuh):
+// a few new query rows per sequence against sequences of their own lengths.
+//
+//   O = softmax(mask(mod(scale q K^T))) V,   K[j][c] = (n - 8) sK[j][c / 32],
+//   V likewise. With group g's channels summed apart,
+//   q . K[j] = sum_g sK[j][g] (q . (n - 8))_g,
+// so the products run on the codes themselves, which bf16 and fp16 hold
+// exactly, and the scales multiply fp32 sums (K) and the probabilities (V):
+// no dequantised value is ever rounded.
+//
+// HBM is the floor: every visible record row is read once for all query rows
+// of its key/value head (4.5 bits an element: 144 bytes a token at D = 128),
+// 3.6 times less than the bf16 cache; so the instructions that unpack the
+// codes are the near bound, and the layout of the products is chosen for them:
+//  - scores are computed transposed, S^T = K q^T (mma m16n8k16: 16 keys, 8
+//    query rows), and so is O^T = V^T P^T. The codes are then the A operand
+//    (the 16-wide one), and up to 8 query rows cost one product, 9 to 16 two
+//    that share the unpacked codes.
+//  - ldmatrix on the packed bytes puts a key's 8 channels of one 32-channel
+//    group into a lane (K), and with .trans four channels of two neighbouring
+//    keys (V): both are what the A fragments need up to the order of the
+//    channels, which q's fragments and O's rows follow.
+//  - a code n becomes a value by one AND/OR into the mantissa of 128 (bf16),
+//    1024 or 64 (fp16): 128 + n. For K the offset 136 sum(q) is the product's
+//    initial accumulator; for V it is subtracted (exactly) before the product,
+//    since O can be far smaller than the offset's share.
+//  - P^T comes out of S^T's accumulators by movmatrix.
+// P is rounded to fp16 after the V scale multiplied it: with y = score +
+// log2(scale of the key's largest V group), the running reference m keeps
+// 2^(y - m) <= 2^15 and at 2^8 for the largest key when m last moved, so fp16's
+// 11 bits hold over 22 binades below the largest weight. m moves (and O and l
+// are rescaled) only when a key passes that bound, which one vote per 32 keys
+// decides. Sums are fp32.
+//
+// A CTA takes one (sequence, key/value head) and a run of 32-key tiles; its
+// four warps stream every fourth tile through buffers of their own (cp.async,
+// rows padded by 16 bytes so the ldmatrix rows hit distinct banks). Their
+// states meet in shared memory, and the CTAs' in the workspace (fp32), joined
+// by the online-softmax merge. With a window the tiles are those of the first
+// `sink` keys, then those of the window.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include "cache_q4.cuh"
+#include "host_util.h"
+#include "launch.h"
+
+#define MATTN_API extern "C" __attribute__((visibility("default")))
+
+namespace mattn {
+namespace {
+
+constexpr int kQ4Threads = 128;
+constexpr int kQ4Warps = 4;
+constexpr int kQ4Tile = 32;    // keys per warp step
+constexpr int kQ4Stages = 2;   // per-warp tile buffers
+constexpr int kQ4MaxRows = 16;
+constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
+constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
+
+struct Q4Problem {
+  const void* q;
+  const uint8_t* pool;
+  void* o;
+  float* lse;
+  const int* seq_lens;
+  const int* table;
+  const float* slopes;
+  int B, Hq, Hkv, Sq, max_len;
+  int pages_per_seq, num_pages, shift;
+  unsigned variant;
+  int window, sink;
+  float scale2;       // scale * log2 e
+  float softcap2;     // softcap * log2 e
+  int splits, chunk;  // tiles per split
+  float* ws_o;        // [splits][rows][D], or nullptr (one split)
+  float* ws_lse;      // [splits][rows]
+};
+
+template <int D>
+struct Q4Cfg {
+  static constexpr int G = D / kQ4Group;                  // scales per row
+  static constexpr int kRow = D / 2 + 16;                 // padded row of codes
+  static constexpr int kCodes = kQ4Tile * kRow;
+  static constexpr int kScales = kQ4Tile * G * 2;
+  static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
+  static constexpr int kWarp = kQ4Stages * kStage;
+  static_assert(kWarp >= (2 * 16 + 16 * D) * 4, "merge state fits the warp area");
+  static constexpr int kSmem = kQ4Warps * kWarp;
+};
+
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// d = A (16x16) B (16x8) + c, fp32 accumulators
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0,
+                                         float c1, float c2, float c3) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Nibbles i and i + 4 of w as the bf16 pair (128 + n_i, 128 + n_{i+4}).
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i) {
+  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+}
+
+// Nibble j of both halves of w as the exact fp16 pair (n - 8, n' - 8).
+__device__ __forceinline__ uint32_t v_pair(uint32_t w, int j) {
+  const uint32_t x = j & 2 ? w >> 8 : w;
+  const uint32_t raw = j & 1 ? (x & 0x00f000f0u) | 0x54005400u    // 64 + n
+                             : (x & 0x000f000fu) | 0x64006400u;   // 1024 + n
+  const uint32_t off = j & 1 ? 0x54805480u : 0x64086408u;         // 72, 1032
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&raw),
+                            *reinterpret_cast<const __half2*>(&off));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The G bf16 scales of one row, as floats.
+template <int G>
+__device__ __forceinline__ void row_scales(const uint8_t* p, float (&s)[G]) {
+  uint32_t w[G / 2];
+  if constexpr (G == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+#pragma unroll
+  for (int i = 0; i < G / 2; ++i) {
+    s[2 * i] = __uint_as_float(w[i] << 16);
+    s[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+template <int D, int NT, int SCORE>
+__global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p) {
+  using C = Q4Cfg<D>;
+  constexpr int G = C::G;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;  // fragment coordinates
+  const int split = blockIdx.x;
+  const int b = blockIdx.y / p.Hkv, hkv = blockIdx.y % p.Hkv;
+  const int group = p.Hq / p.Hkv;
+  const int R = group * p.Sq;
+  const size_t row0 = (size_t)(b * p.Hq + hkv * group) * p.Sq;
+  const size_t total_rows = (size_t)p.B * p.Hq * p.Sq;
+  const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+
+  // the sequence's keys, and its tiles: those of the sinks, then the window's
+  const long long held = (long long)p.pages_per_seq << p.shift;
+  const int len = max(0, min(p.seq_lens[b], (int)min((long long)p.max_len, held)));
+  const int first_pos = len - p.Sq;  // absolute position of query row 0
+  int win_tile = 0, sink_tiles = 0;
+  if (windowed) {
+    const int w0 = (int)max(0ll, (long long)first_pos - p.window + 1);
+    win_tile = w0 / kQ4Tile;
+    sink_tiles = min(win_tile, (min(p.sink, len) + kQ4Tile - 1) / kQ4Tile);
+  }
+  const int last_tile = (len + kQ4Tile - 1) / kQ4Tile;
+  const int tiles = sink_tiles + max(0, last_tile - win_tile);
+  const int v_begin = split * p.chunk, v_end = min(tiles, v_begin + p.chunk);
+  if (v_begin >= v_end && p.ws_o) {  // nothing here: the merge skips this part
+    if (threadIdx.x < R && MATTN_IN_BOUNDS(kSiteQ4Out, row0 + threadIdx.x, total_rows))
+      p.ws_lse[(size_t)split * total_rows + row0 + threadIdx.x] = -INFINITY;
+    return;
+  }
+
+  // q^T fragments (B operand) and the offset 136 sum(q) of each group, as the
+  // products' initial accumulators; rows past R are 0. Channel order of a
+  // group's 8 channels per lane: pairs (0, 4), (1, 5) | (2, 6), (3, 7).
+  const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
+  uint32_t qb[NT][G][4];
+  float corr[NT][G][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g;
+#pragma unroll
+    for (int a = 0; a < G; ++a) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
+        x = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
+      // x.x = channels 0, 1; .y = 2, 3; .z = 4, 5; .w = 6, 7
+      qb[nt][a][0] = __byte_perm(x.x, x.z, 0x5410);
+      qb[nt][a][1] = __byte_perm(x.x, x.z, 0x7632);
+      qb[nt][a][2] = __byte_perm(x.y, x.w, 0x5410);
+      qb[nt][a][3] = __byte_perm(x.y, x.w, 0x7632);
+      float sum = 0.0f;
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        sum += __uint_as_float(u[i] << 16) + __uint_as_float(u[i] & 0xffff0000u);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);  // of row g; wanted: rows 2t and 2t + 1
+      corr[nt][a][0] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t);
+      corr[nt][a][1] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+    }
+  }
+  // the lane's query rows (columns 2t, 2t + 1 of each 8): position and slope
+  int pos[NT][2];
+  float slope2[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * t + e;
+      const int hg = r < R ? r / p.Sq : 0;
+      pos[nt][e] = first_pos + (r < R ? r % p.Sq : 0);
+      const int h = hkv * group + hg;
+      slope2[nt][e] =
+          (SCORE & 1) ? (p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq))) * kLog2e
+                      : 0.0f;
+    }
+
+  // tiles through the warp's buffers
+  const Q4Layout L{D, 1 << p.shift};
+  const uint32_t area = smem_u32(smem) + warp * C::kWarp;
+  const uint8_t* area_ptr = smem + warp * C::kWarp;
+  auto tile_of = [&](int v) { return v < sink_tiles ? v : v - sink_tiles + win_tile; };
+  auto page_of = [&](int v, int half) -> int {  // page of a tile's 16-key half, or -1
+    if (v >= v_end) return -1;
+    const int lp = (tile_of(v) * kQ4Tile + 16 * half) >> p.shift;
+    if (lp >= p.pages_per_seq) return -1;
+    const int pg = p.table[(size_t)b * p.pages_per_seq + lp];
+    return pg >= 0 && pg < p.num_pages ? pg : -1;
+  };
+  auto load_tile = [&](int v, int stage, int pg0, int pg1) {
+    const uint32_t dst = area + stage * C::kStage;
+    const int key0 = tile_of(v) * kQ4Tile;
+    const uint8_t* rec0 = p.pool + ((size_t)max(pg0, 0) * p.Hkv + hkv) * L.bytes();
+    const uint8_t* rec1 = p.pool + ((size_t)max(pg1, 0) * p.Hkv + hkv) * L.bytes();
+    const int in0 = key0 & (L.page - 1), in1 = (key0 + 16) & (L.page - 1);
+    const uint32_t bytes0 = pg0 >= 0 ? 16u : 0u, bytes1 = pg1 >= 0 ? 16u : 0u;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {  // a row's codes are G chunks of 16 bytes
+      const bool h = i >= G / 2;   // half of the tile
+      const int r = (32 * i + lane) % (16 * G) / G, q = lane % G;
+      const uint8_t* src = (h ? rec1 : rec0) + ((h ? in1 : in0) + r) * L.code_row() + q * 16;
+      const uint32_t d = dst + (16 * h + r) * C::kRow + q * 16;
+      cp_async16z(d, src, h ? bytes1 : bytes0);
+      cp_async16z(d + C::kCodes, src + L.v_codes(), h ? bytes1 : bytes0);
+    }
+    constexpr int kChunks = C::kScales / 16;  // 16-byte chunks of K (and V) scales per tile
+    if (lane < 2 * kChunks) {
+      const int kv = lane / kChunks, c = lane % kChunks;
+      const bool h = c >= kChunks / 2;
+      const uint8_t* src = (h ? rec1 : rec0) + (kv ? L.v_scales() : L.k_scales()) +
+                           (h ? in1 : in0) * L.scale_row() + (c % (kChunks / 2)) * 16;
+      cp_async16z(dst + 2 * C::kCodes + kv * C::kScales + c * 16, src, h ? bytes1 : bytes0);
+    }
+    cp_async_commit();
+  };
+
+  float o[G][2][NT][4];  // [group][channel pair] x (channel, row) of each 8 rows
+#pragma unroll
+  for (int a = 0; a < G; ++a)
+#pragma unroll
+    for (int jp = 0; jp < 2; ++jp)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        o[a][jp][nt][0] = o[a][jp][nt][1] = o[a][jp][nt][2] = o[a][jp][nt][3] = 0.0f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.0f;
+  }
+
+  // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
+  auto process = [&](const int stage, const int key0, auto mask_tag) {
+    constexpr bool kMask = decltype(mask_tag)::value;
+    const uint32_t buf = area + stage * C::kStage;
+    const uint8_t* scales = area_ptr + stage * C::kStage + 2 * C::kCodes;
+    float x[2][NT][4], lsv[2][2];
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {  // 16 keys: rows g and g + 8 of the fragments
+      uint32_t w[2][G];  // a lane's 8 channels of each group, for its two keys
+      if constexpr (G == 4) {
+        ldsm4(buf + (16 * mt + (lane & 7)) * C::kRow + (lane >> 3) * 16, w[0]);
+        ldsm4(buf + (16 * mt + 8 + (lane & 7)) * C::kRow + (lane >> 3) * 16, w[1]);
+      } else {
+        uint32_t u[4];
+        ldsm4(buf + (16 * mt + (lane >> 4) * 8 + (lane & 7)) * C::kRow + ((lane >> 3) & 1) * 16, u);
+        w[0][0] = u[0];
+        w[0][1] = u[1];
+        w[1][0] = u[2];
+        w[1][1] = u[3];
+      }
+      float sk[2][G], sv[2][G];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        row_scales<G>(scales + (16 * mt + 8 * e + g) * 2 * G, sk[e]);
+        row_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[e]);
+        float big = 1e-27f;  // keeps the weights of tiny scales within fp32
+#pragma unroll
+        for (int a = 0; a < G; ++a) big = fmaxf(big, fabsf(sv[e][a]));
+        lsv[mt][e] = __log2f(big);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.0f;
+#pragma unroll
+      for (int a = 0; a < G; ++a) {
+        uint32_t f[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[0][i] = k_pair(w[0][a], i);
+          f[1][i] = k_pair(w[1][a], i);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float d[4];
+          mma_bf16(d, f[0][0], f[1][0], f[0][1], f[1][1], qb[nt][a][0], qb[nt][a][1],
+                   corr[nt][a][0], corr[nt][a][1], corr[nt][a][0], corr[nt][a][1]);
+          mma_bf16(d, f[0][2], f[1][2], f[0][3], f[1][3], qb[nt][a][2], qb[nt][a][3], d[0], d[1],
+                   d[2], d[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[mt][nt][e] = fmaf(sk[e >> 1][a], d[e], x[mt][nt][e]);
+        }
+      }
+    }
+    // score modification and mask, in log2 units
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = key0 + 16 * mt + 8 * (e >> 1) + g, i = pos[nt][e & 1];
+          float s = x[mt][nt][e] * p.scale2;
+          if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
+          if constexpr ((SCORE & 2) != 0) s = p.softcap2 * tanhf(s / p.softcap2);
+          if constexpr (kMask) {
+            bool keep = j < len && i >= 0;
+            if (causal) keep = keep && j <= i;
+            if (windowed) keep = keep && (i - j < p.window || j < p.sink);
+            s = keep ? s : -INFINITY;
+          }
+          x[mt][nt][e] = s;
+        }
+    // the reference follows keys that pass its bound
+    float top[NT][2];
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = x[0][nt][e] + lsv[0][0];
+        y = fmaxf(y, x[0][nt][e + 2] + lsv[0][1]);
+        y = fmaxf(y, x[1][nt][e] + lsv[1][0]);
+        y = fmaxf(y, x[1][nt][e + 2] + lsv[1][1]);
+        top[nt][e] = y;
+        over = over || y > m[nt][e] + kQ4Head;
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float y = top[nt][e];
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          // each row by itself: its result does not depend on the others'
+          const float m_new = y > m[nt][e] + kQ4Head ? y - kQ4Start : m[nt][e];
+          const float c = m_new == -INFINITY ? 1.0f : ex2_approx(m[nt][e] - m_new);  // -inf -> 0
+          m[nt][e] = m_new;
+          l[nt][e] *= c;
+#pragma unroll
+          for (int a = 0; a < G; ++a)
+#pragma unroll
+            for (int jp = 0; jp < 2; ++jp) {
+              o[a][jp][nt][e] *= c;
+              o[a][jp][nt][e + 2] *= c;
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
+        float sum = 0.0f;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float& s = x[mt][nt][e + 2 * k];
+            s = ex2_approx(s - ref);
+            sum += s;
+          }
+        l[nt][e] += sum;
+      }
+    // O^T += V^T P^T
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      float sv[2][G];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        row_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[e]);
+#pragma unroll
+      for (int a2 = 0; a2 < G; a2 += 2) {  // two groups: keys 0-7 and 8-15 of each
+        uint32_t w[4];
+        ldsm4_t(buf + C::kCodes + (16 * mt + ((lane >> 3) & 1) * 8 + (lane & 7)) * C::kRow +
+                    (a2 + (lane >> 4)) * 16,
+                w);
+#pragma unroll
+        for (int da = 0; da < 2; ++da) {
+          const int a = a2 + da;
+          uint32_t f[2][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[0][j] = v_pair(w[2 * da], j);
+            f[1][j] = v_pair(w[2 * da + 1], j);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float pv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pv[e] = x[mt][nt][e] * sv[e >> 1][a];
+              // a masked key adds nothing, whatever its scale holds
+              if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
+            }
+            const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
+            const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
+            mma_f16(o[a][0][nt], f[0][0], f[0][1], f[1][0], f[1][1], b0, b1);
+            mma_f16(o[a][1][nt], f[0][2], f[0][3], f[1][2], f[1][3], b0, b1);
+          }
+        }
+      }
+    }
+  };
+
+  const int v_first = v_begin + warp;
+  if (v_first < v_end) load_tile(v_first, 0, page_of(v_first, 0), page_of(v_first, 1));
+  if (v_first + kQ4Warps < v_end)
+    load_tile(v_first + kQ4Warps, 1, page_of(v_first + kQ4Warps, 0), page_of(v_first + kQ4Warps, 1));
+  int stage = 0;
+  for (int v = v_first; v < v_end; v += kQ4Warps, stage ^= 1) {
+    const int next = v + 2 * kQ4Warps;
+    const int pg0 = page_of(next, 0), pg1 = page_of(next, 1);
+    if (v + kQ4Warps < v_end) cp_async_wait<1>();
+    else cp_async_wait<0>();
+    __syncwarp();
+    const int key0 = tile_of(v) * kQ4Tile, key_end = key0 + kQ4Tile;
+    const bool whole = key_end <= len && first_pos >= 0 && (!causal || key_end - 1 <= first_pos) &&
+                       (!windowed || len - 1 - key0 < p.window || key_end <= p.sink);
+    if (whole) process(stage, key0, std::false_type{});
+    else process(stage, key0, std::true_type{});
+    __syncwarp();
+    if (next < v_end) load_tile(next, stage, pg0, pg1);
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+
+  // the warps' states meet in shared memory: m, l (16 each), O [16][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+    }
+  float* wm = reinterpret_cast<float*>(smem + warp * C::kWarp);
+  float* wl = wm + 16;
+  float* wo = wm + 32;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (g == 0) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        wm[nt * 8 + 2 * t + e] = m[nt][e];
+        wl[nt * 8 + 2 * t + e] = l[nt][e];
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < G; ++a)
+#pragma unroll
+      for (int jp = 0; jp < 2; ++jp)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(wo + (nt * 8 + 2 * t + e) * D + 32 * a + 4 * g + 2 * jp) =
+              make_float2(o[a][jp][nt][e], o[a][jp][nt][e + 2]);
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < R * D; idx += kQ4Threads) {
+    const int r = idx / D, c = idx % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kQ4Warps; ++w)
+      M = fmaxf(M, reinterpret_cast<const float*>(smem + w * C::kWarp)[r]);
+    float Ls = 0.0f, acc = 0.0f;
+    if (M != -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kQ4Warps; ++w) {
+        const float* st = reinterpret_cast<const float*>(smem + w * C::kWarp);
+        const float wt = ex2_approx(st[r] - M);  // -inf -> 0
+        Ls += wt * st[16 + r];
+        acc += wt * st[32 + r * D + c];
+      }
+    }
+    // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
+    const float out = M != -INFINITY ? acc / Ls : 0.0f;
+    const float lse = M != -INFINITY ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
+    if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
+    if (p.ws_o) {
+      if (!MATTN_IN_BOUNDS(kSiteQ4Out, split, p.splits)) continue;
+      p.ws_o[((size_t)split * total_rows + row0 + r) * D + c] = out;
+      if (c == 0) p.ws_lse[(size_t)split * total_rows + row0 + r] = lse;
+    } else {
+      static_cast<__nv_bfloat16*>(p.o)[(row0 + r) * D + c] = __float2bfloat16_rn(out);
+      if (c == 0) p.lse[row0 + r] = lse;
+    }
+  }
+}
+
+template <int D, int NT, int SCORE>
+cudaError_t launch_typed(const Q4Problem& p, cudaStream_t stream) {
+  using C = Q4Cfg<D>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(decode_q4_kernel<D, NT, SCORE>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  decode_q4_kernel<D, NT, SCORE><<<dim3(p.splits, p.B * p.Hkv), kQ4Threads, C::kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int NT>
+cudaError_t launch_score(const Q4Problem& p, cudaStream_t s) {
+  switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
+    case 0: return launch_typed<D, NT, 0>(p, s);
+    case 1: return launch_typed<D, NT, 1>(p, s);
+    case 2: return launch_typed<D, NT, 2>(p, s);
+    default: return launch_typed<D, NT, 3>(p, s);
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Most splits that a call over `tiles` 32-key tiles uses: about eight CTAs
+// per SM, at least one tile per warp. Does not fall when `tiles` grows.
+int q4_most_splits(int B, int Hkv, long long tiles) {
+  const long long ctas = (long long)B * Hkv;
+  const long long want = std::min((8LL * sm_count() + ctas - 1) / ctas,
+                                  (tiles + kQ4Warps - 1) / kQ4Warps);
+  return (int)std::max(1LL, std::min(want, 64LL));
+}
+
+size_t q4_ws_per_split(int B, int Hq, int Sq, int D) {
+  const size_t rows = (size_t)B * Hq * Sq;
+  return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+}  // namespace
+}  // namespace mattn
+
+MATTN_API size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || max_len < 1 || (D != 64 && D != 128)) return 0;
+  const int splits = mattn::q4_most_splits(B, Hkv, ((long long)max_len + mattn::kQ4Tile - 1) /
+                                                       mattn::kQ4Tile);
+  return splits > 1 ? (size_t)splits * mattn::q4_ws_per_split(B, Hq, Sq, D) : 0;
+}
+
+MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B,
+                                     int Hq, int Hkv, int Sq, int max_len, int D, unsigned variant,
+                                     const attn_params* p, const int* seq_lens, int sink,
+                                     void* workspace, size_t workspace_bytes,
+                                     struct CUstream_st* stream) {
+  using namespace mattn;
+  if (!p || B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || max_len < 0 || sink < 0 || Hq % Hkv)
+    return ATTN_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || p->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (variant & ~(ATTN_MASK_BITS | ATTN_SCORE_BITS)) return ATTN_ERR_INVALID_ARG;
+  if (variant & ~(unsigned)(ATTN_MASK_CAUSAL | ATTN_MASK_WINDOW | ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP))
+    return ATTN_ERR_UNSUPPORTED;
+  if ((variant & ATTN_MASK_WINDOW) && p->window < 1) return ATTN_ERR_INVALID_ARG;
+  if ((variant & ATTN_SCORE_SOFTCAP) && !(p->softcap > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || p->scale < 0.0f) return ATTN_ERR_INVALID_ARG;
+  if (p->q_offset || p->kv_offset) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)(Hq / Hkv) * Sq > kQ4MaxRows || (long long)B * Hkv > 65535)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!q4_page_ok(p->page_size)) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Sq == 0) return ATTN_OK;
+  if (p->num_pages < 1 || p->pages_per_seq < 1 ||
+      (long long)p->pages_per_seq * p->page_size < (long long)max_len)
+    return ATTN_ERR_INVALID_ARG;
+  if (!q || !pool || !o || !lse || !seq_lens || !p->page_table) return ATTN_ERR_INVALID_ARG;
+  const void* vecs[] = {q, pool, o};
+  for (const void* x : vecs)
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return ATTN_ERR_MISALIGNED;
+  const void* words[] = {lse, seq_lens, p->page_table, p->alibi_slopes};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return ATTN_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_ERR_MISALIGNED;
+
+  Q4Problem f{};
+  f.q = q;
+  f.pool = static_cast<const uint8_t*>(pool);
+  f.o = o;
+  f.lse = lse;
+  f.seq_lens = seq_lens;
+  f.table = p->page_table;
+  f.slopes = p->alibi_slopes;
+  f.B = B;
+  f.Hq = Hq;
+  f.Hkv = Hkv;
+  f.Sq = Sq;
+  f.max_len = max_len;
+  f.pages_per_seq = p->pages_per_seq;
+  f.num_pages = p->num_pages;
+  f.shift = 4;
+  while ((1 << f.shift) != p->page_size) ++f.shift;
+  f.variant = variant;
+  f.window = p->window;
+  f.sink = sink;
+  f.scale2 = (p->scale != 0.0f ? p->scale : 1.0f / std::sqrt((float)D)) * kLog2e;
+  f.softcap2 = p->softcap * kLog2e;
+
+  // most tiles that a sequence can have: its whole length, or sinks and window
+  long long tiles = ((long long)max_len + kQ4Tile - 1) / kQ4Tile;
+  if (variant & ATTN_MASK_WINDOW)
+    tiles = std::min(tiles, ((long long)sink + kQ4Tile - 1) / kQ4Tile +
+                                ((long long)p->window + Sq - 1 + 2 * kQ4Tile - 2) / kQ4Tile);
+  int splits = q4_most_splits(B, Hkv, tiles);
+  const size_t fit = workspace ? workspace_bytes / q4_ws_per_split(B, Hq, Sq, D) : 0;
+  if ((size_t)splits > fit) splits = fit >= 2 ? (int)fit : 1;  // as many as the workspace holds
+  f.chunk = (int)std::max(1LL, (tiles + splits - 1) / splits);
+  f.splits = splits = (int)std::max(1LL, (tiles + f.chunk - 1) / f.chunk);
+  const long long rows = (long long)B * Hq * Sq;
+  if (splits > 1) {
+    f.ws_o = static_cast<float*>(workspace);
+    f.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align256((size_t)rows * D * sizeof(float)) * splits);
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool two = (Hq / Hkv) * Sq > 8;
+  cudaError_t e;
+  if (D == 64) e = two ? launch_score<64, 2>(f, s) : launch_score<64, 1>(f, s);
+  else e = two ? launch_score<128, 2>(f, s) : launch_score<128, 1>(f, s);
+  attn_status st = cuda_status(e);
+  if (st != ATTN_OK || splits == 1) return st;
+  return cuda_status(launch_combine_f32_bf16(f.ws_o, f.ws_lse, splits, rows, D, o, lse, s));
+}
+
+namespace mattn {
+MATTN_DEBUG_RECORD_ACCESSORS(decode_q4)
+}  // namespace mattn
