@@ -20,10 +20,11 @@
 //    group into a lane (K), and with .trans four channels of two neighbouring
 //    keys (V): both are what the A fragments need up to the order of the
 //    channels, which q's fragments and O's rows follow.
-//  - a code n becomes a value by one AND/OR into the mantissa of 128 (bf16),
-//    1024 or 64 (fp16): 128 + n. For K the offset 136 sum(q) is the product's
-//    initial accumulator; for V it is subtracted (exactly) before the product,
-//    since O can be far smaller than the offset's share.
+//  - a code n becomes the exact fp16 value n - 8 by one AND/OR into the mantissa
+//    of 1024 or 64 and one packed subtraction, two codes at a time. (The bits
+//    alone, as fp16 subnormals, need no subtraction, but the products then keep
+//    about 14 bits below the largest: their sums are aligned to the exponents of
+//    the operands as encoded. O was up to 2 % off.)
 //  - P^T comes out of S^T's accumulators by movmatrix.
 // P is rounded to fp16 after the V scale multiplied it: with y = score +
 // log2(scale of the key's largest V group), the running reference m keeps
@@ -61,6 +62,8 @@ constexpr int kQ4Stages = 2;   // per-warp tile buffers
 constexpr int kQ4MaxRows = 16;
 constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
+constexpr uint32_t kQ4Tiny = 0x12801280u;  // bf16 2^-90, twice: smaller V scales count as this,
+                                           // so that unscaled weights stay within fp32
 
 struct Q4Problem {
   const void* q;
@@ -76,6 +79,7 @@ struct Q4Problem {
   int window, sink;
   float scale2;       // scale * log2 e
   float softcap2;     // softcap * log2 e
+  float softcap_e;    // 2 / softcap: e^(2 s / softcap) from s in log2 units
   int splits, chunk;  // tiles per split
   float* ws_o;        // [splits][rows][D], or nullptr (one split)
   float* ws_lse;      // [splits][rows]
@@ -117,17 +121,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// d = A (16x16) B (16x8) + c, fp32 accumulators
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1, float c0,
-                                         float c1, float c2, float c3) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%12,%13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
+// c += A (16x16) B (16x8), fp32 accumulators
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -137,20 +131,26 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Nibbles i and i + 4 of w as the bf16 pair (128 + n_i, 128 + n_{i+4}).
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+// (x & mask) | bits in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
 }
 
-// Nibble j of both halves of w as the exact fp16 pair (n - 8, n' - 8).
-__device__ __forceinline__ uint32_t v_pair(uint32_t w, int j) {
-  const uint32_t x = j & 2 ? w >> 8 : w;
-  const uint32_t raw = j & 1 ? (x & 0x00f000f0u) | 0x54005400u    // 64 + n
-                             : (x & 0x000f000fu) | 0x64006400u;   // 1024 + n
-  const uint32_t off = j & 1 ? 0x54805480u : 0x64086408u;         // 72, 1032
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&raw),
-                            *reinterpret_cast<const __half2*>(&off));
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Nibbles 0 to 3 of both halves of w as exact fp16 pairs (n - 8, n' - 8): the
+// nibble's bits in the mantissa of 1024 or, one nibble up, of 64.
+__device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t x = j & 2 ? w >> 8 : w;
+    const uint32_t raw = j & 1 ? and_or(x, 0x00f000f0u, 0x54005400u)    // 64 + n
+                               : and_or(x, 0x000f000fu, 0x64006400u);   // 1024 + n
+    const uint32_t off = j & 1 ? 0x54805480u : 0x64086408u;         // 72, 1032
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&raw),
+                              *reinterpret_cast<const __half2*>(&off));
+    f[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -158,10 +158,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The G bf16 scales of one row, as floats.
+// The G bf16 scales of one row, two to a word.
 template <int G>
-__device__ __forceinline__ void row_scales(const uint8_t* p, float (&s)[G]) {
-  uint32_t w[G / 2];
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&w)[G / 2]) {
   if constexpr (G == 4) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     w[0] = u.x;
@@ -169,11 +168,10 @@ __device__ __forceinline__ void row_scales(const uint8_t* p, float (&s)[G]) {
   } else {
     w[0] = *reinterpret_cast<const uint32_t*>(p);
   }
-#pragma unroll
-  for (int i = 0; i < G / 2; ++i) {
-    s[2 * i] = __uint_as_float(w[i] << 16);
-    s[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+}
+
+__device__ __forceinline__ float scale_of(uint32_t w, int i) {  // i = 0 or 1
+  return __uint_as_float(i ? w & 0xffff0000u : w << 16);
 }
 
 template <int D, int NT, int SCORE>
@@ -210,34 +208,44 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
     return;
   }
 
-  // q^T fragments (B operand) and the offset 136 sum(q) of each group, as the
-  // products' initial accumulators; rows past R are 0. Channel order of a
-  // group's 8 channels per lane: pairs (0, 4), (1, 5) | (2, 6), (3, 7).
+  // q^T fragments (B operand), fp16: a row is scaled by a power of two that
+  // brings its largest channel to [2^14, 2^15), so bf16's 8 bits are exact
+  // (channels 2^28 times smaller lose bits below 2^-39 of the largest). Channel
+  // order of a lane's 8 per group: pairs (0, 4), (1, 5) | (2, 6), (3, 7). Rows past
+  // R are 0.
   const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
   uint32_t qb[NT][G][4];
-  float corr[NT][G][2];
+  float unit[NT][2];  // scores per product unit, log2
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int r = nt * 8 + g;
+    uint4 x[G];
+    float big = 0.0f;
 #pragma unroll
     for (int a = 0; a < G; ++a) {
-      uint4 x = make_uint4(0, 0, 0, 0);
+      x[a] = make_uint4(0, 0, 0, 0);
       if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
-        x = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
-      // x.x = channels 0, 1; .y = 2, 3; .z = 4, 5; .w = 6, 7
-      qb[nt][a][0] = __byte_perm(x.x, x.z, 0x5410);
-      qb[nt][a][1] = __byte_perm(x.x, x.z, 0x7632);
-      qb[nt][a][2] = __byte_perm(x.y, x.w, 0x5410);
-      qb[nt][a][3] = __byte_perm(x.y, x.w, 0x7632);
-      float sum = 0.0f;
-      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+        x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
+      const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        sum += __uint_as_float(u[i] << 16) + __uint_as_float(u[i] & 0xffff0000u);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);  // of row g; wanted: rows 2t and 2t + 1
-      corr[nt][a][0] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t);
-      corr[nt][a][1] = -136.0f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        big = fmaxf(big, fmaxf(fabsf(scale_of(u[i], 0)), fabsf(scale_of(u[i], 1))));
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+    const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
+    const float up = __uint_as_float((uint32_t)(127 + min(14 - ex, 127)) << 23);
+    const float down = exp2f((float)(ex - 14)) * p.scale2;
+    unit[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);      // rows 2t and 2t + 1
+    unit[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+    for (int a = 0; a < G; ++a) {
+      const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+      float c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = scale_of(u[i / 2], i & 1) * up;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qb[nt][a][i] = pack_f16x2(c[i], c[i + 4]);
     }
   }
   // the lane's query rows (columns 2t, 2t + 1 of each 8): position and slope
@@ -256,42 +264,70 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
                       : 0.0f;
     }
 
-  // tiles through the warp's buffers
+  // The warp's tiles: v_begin + warp, every kQ4Warps-th. Their pages are looked
+  // up 16 tiles at a time, lane 2i + h the page of tile i's 16-key half h (or
+  // -1), one batch ahead.
   const Q4Layout L{D, 1 << p.shift};
   const uint32_t area = smem_u32(smem) + warp * C::kWarp;
   const uint8_t* area_ptr = smem + warp * C::kWarp;
-  auto tile_of = [&](int v) { return v < sink_tiles ? v : v - sink_tiles + win_tile; };
-  auto page_of = [&](int v, int half) -> int {  // page of a tile's 16-key half, or -1
-    if (v >= v_end) return -1;
-    const int lp = (tile_of(v) * kQ4Tile + 16 * half) >> p.shift;
+  const int v_first = v_begin + warp;
+  const int n_tiles = v_first < v_end ? (v_end - v_first + kQ4Warps - 1) / kQ4Warps : 0;
+  auto key_of = [&](int i) {  // first key of the warp's tile i
+    const int v = v_first + i * kQ4Warps;
+    return (v < sink_tiles ? v : v - sink_tiles + win_tile) * kQ4Tile;
+  };
+  auto look_up = [&](int i0) -> int {
+    const int i = i0 + (lane >> 1);
+    if (i >= n_tiles) return -1;
+    const int lp = (key_of(i) + 16 * (lane & 1)) >> p.shift;
     if (lp >= p.pages_per_seq) return -1;
     const int pg = p.table[(size_t)b * p.pages_per_seq + lp];
     return pg >= 0 && pg < p.num_pages ? pg : -1;
   };
-  auto load_tile = [&](int v, int stage, int pg0, int pg1) {
-    const uint32_t dst = area + stage * C::kStage;
-    const int key0 = tile_of(v) * kQ4Tile;
-    const uint8_t* rec0 = p.pool + ((size_t)max(pg0, 0) * p.Hkv + hkv) * L.bytes();
-    const uint8_t* rec1 = p.pool + ((size_t)max(pg1, 0) * p.Hkv + hkv) * L.bytes();
-    const int in0 = key0 & (L.page - 1), in1 = (key0 + 16) & (L.page - 1);
-    const uint32_t bytes0 = pg0 >= 0 ? 16u : 0u, bytes1 = pg1 >= 0 ? 16u : 0u;
+  int pages = -1, pages_next = look_up(0);
+  const uint8_t* head_pool = p.pool + (size_t)hkv * L.bytes() + lane * 16;
+  const uint32_t page_stride = (uint32_t)p.Hkv * L.bytes();
+  constexpr int kScaleChunks = C::kScales / 32;  // 16-byte chunks of K (or V) scales per half
+  // lane's chunk of the scales: half, K or V, place
+  const bool sc_half = lane / kScaleChunks & 1;
+  const int sc_src = (lane / (2 * kScaleChunks) ? L.v_scales() : L.k_scales()) +
+                     (lane % kScaleChunks) * 16 - lane * 16;
+  const uint32_t sc_dst = 2 * C::kCodes + (lane / kScaleChunks) % 2 * (C::kScales / 2) +
+                          lane / (2 * kScaleChunks) * C::kScales + lane % kScaleChunks * 16;
+  auto load_tile = [&](int i) {  // into buffer i % kQ4Stages; called with i = 0, 1, 2, ...
+    if ((i & 15) == 0) {
+      pages = pages_next;
+      pages_next = look_up(i + 16);
+    }
+    const uint32_t dst = area + (i & (kQ4Stages - 1)) * C::kStage;
+    const int key0 = key_of(i);
+    const uint8_t* src[2];
+    uint32_t bytes[2];
+    int in_page[2];
 #pragma unroll
-    for (int i = 0; i < G; ++i) {  // a row's codes are G chunks of 16 bytes
-      const bool h = i >= G / 2;   // half of the tile
-      const int r = (32 * i + lane) % (16 * G) / G, q = lane % G;
-      const uint8_t* src = (h ? rec1 : rec0) + ((h ? in1 : in0) + r) * L.code_row() + q * 16;
-      const uint32_t d = dst + (16 * h + r) * C::kRow + q * 16;
-      cp_async16z(d, src, h ? bytes1 : bytes0);
-      cp_async16z(d + C::kCodes, src + L.v_codes(), h ? bytes1 : bytes0);
+    for (int h = 0; h < 2; ++h) {
+      const int pg = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + h);
+      bytes[h] = pg >= 0 ? 16u : 0u;
+      src[h] = head_pool + (size_t)(uint32_t)max(pg, 0) * page_stride;
+      in_page[h] = (key0 + 16 * h) & (L.page - 1);
     }
-    constexpr int kChunks = C::kScales / 16;  // 16-byte chunks of K (and V) scales per tile
-    if (lane < 2 * kChunks) {
-      const int kv = lane / kChunks, c = lane % kChunks;
-      const bool h = c >= kChunks / 2;
-      const uint8_t* src = (h ? rec1 : rec0) + (kv ? L.v_scales() : L.k_scales()) +
-                           (h ? in1 : in0) * L.scale_row() + (c % (kChunks / 2)) * 16;
-      cp_async16z(dst + 2 * C::kCodes + kv * C::kScales + c * 16, src, h ? bytes1 : bytes0);
+    // a half's codes are 8 D consecutive bytes of the record: D / 64 chunks per lane
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* k = src[h] + in_page[h] * L.code_row();
+      const uint8_t* v = k + L.v_codes();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint32_t d = dst + (16 * h + c * (32 / G) + lane / G) * C::kRow + lane % G * 16;
+        cp_async16z(d, k + c * 512, bytes[h]);
+        cp_async16z(d + C::kCodes, v + c * 512, bytes[h]);
+      }
     }
+    if (lane < 4 * kScaleChunks)
+      cp_async16z(dst + sc_dst,
+                  (sc_half ? src[1] + in_page[1] * L.scale_row() : src[0] + in_page[0] * L.scale_row()) +
+                      sc_src,
+                  sc_half ? bytes[1] : bytes[0]);
     cp_async_commit();
   };
 
@@ -311,11 +347,12 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
   }
 
   // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
-  auto process = [&](const int stage, const int key0, auto mask_tag) {
+  auto process = [&](const uint32_t stage_off, const int key0, auto mask_tag) {
     constexpr bool kMask = decltype(mask_tag)::value;
-    const uint32_t buf = area + stage * C::kStage;
-    const uint8_t* scales = area_ptr + stage * C::kStage + 2 * C::kCodes;
-    float x[2][NT][4], lsv[2][2];
+    const uint32_t buf = area + stage_off;
+    const uint8_t* scales = area_ptr + stage_off + 2 * C::kCodes;
+    float x[2][NT][4];
+    uint32_t sv[2][2][G / 2];
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {  // 16 keys: rows g and g + 8 of the fragments
       uint32_t w[2][G];  // a lane's 8 channels of each group, for its two keys
@@ -330,40 +367,32 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
         w[1][0] = u[2];
         w[1][1] = u[3];
       }
-      float sk[2][G], sv[2][G];
+      uint32_t sk[2][G / 2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        row_scales<G>(scales + (16 * mt + 8 * e + g) * 2 * G, sk[e]);
-        row_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[e]);
-        float big = 1e-27f;  // keeps the weights of tiny scales within fp32
-#pragma unroll
-        for (int a = 0; a < G; ++a) big = fmaxf(big, fabsf(sv[e][a]));
-        lsv[mt][e] = __log2f(big);
+        load_scales<G>(scales + (16 * mt + 8 * e + g) * 2 * G, sk[e]);
+        load_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[mt][e]);
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        x[mt][nt][0] = x[mt][nt][1] = x[mt][nt][2] = x[mt][nt][3] = 0.0f;
 #pragma unroll
       for (int a = 0; a < G; ++a) {
         uint32_t f[2][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[0][i] = k_pair(w[0][a], i);
-          f[1][i] = k_pair(w[1][a], i);
-        }
+        nibble_pairs(w[0][a], f[0]);
+        nibble_pairs(w[1][a], f[1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float d[4];
-          mma_bf16(d, f[0][0], f[1][0], f[0][1], f[1][1], qb[nt][a][0], qb[nt][a][1],
-                   corr[nt][a][0], corr[nt][a][1], corr[nt][a][0], corr[nt][a][1]);
-          mma_bf16(d, f[0][2], f[1][2], f[0][3], f[1][3], qb[nt][a][2], qb[nt][a][3], d[0], d[1],
-                   d[2], d[3]);
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qb[nt][a][0], qb[nt][a][1]);
+          mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qb[nt][a][2], qb[nt][a][3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[mt][nt][e] = fmaf(sk[e >> 1][a], d[e], x[mt][nt][e]);
+          for (int e = 0; e < 4; ++e) {
+            const float s = scale_of(sk[e >> 1][a / 2], a & 1);
+            x[mt][nt][e] = a == 0 ? s * d[e] : fmaf(s, d[e], x[mt][nt][e]);
+          }
         }
       }
     }
-    // score modification and mask, in log2 units
+    // score modification and mask. Without a modification the scores stay in
+    // the products' units and `unit` enters with the exponent.
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -371,9 +400,13 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int j = key0 + 16 * mt + 8 * (e >> 1) + g, i = pos[nt][e & 1];
-          float s = x[mt][nt][e] * p.scale2;
+          float s = x[mt][nt][e];
+          if constexpr (SCORE != 0) s *= unit[nt][e & 1];
           if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
-          if constexpr ((SCORE & 2) != 0) s = p.softcap2 * tanhf(s / p.softcap2);
+          // cap tanh(s / cap) as cap - 2 cap / (1 + e^(2 s / cap)): off by at
+          // most 2^-22 cap, and exact at both ends
+          if constexpr ((SCORE & 2) != 0)
+            s = fmaf(-p.softcap2, __fdividef(2.0f, 1.0f + ex2_approx(s * p.softcap_e)), p.softcap2);
           if constexpr (kMask) {
             bool keep = j < len && i >= 0;
             if (causal) keep = keep && j <= i;
@@ -382,26 +415,46 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
           }
           x[mt][nt][e] = s;
         }
-    // the reference follows keys that pass its bound
-    float top[NT][2];
+    auto log2_of = [&](float s, int nt, int e) { return SCORE ? s : s * unit[nt][e]; };
+    // The reference follows keys that pass its bound. First a quick bound: the
+    // lane's largest score with its largest V scale, rounded up to a power of
+    // two (a negative or NaN scale counts as huge).
+    uint32_t sm = kQ4Tiny;
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < G / 2; ++i) sm = __vmaxu2(sm, sv[mt][e][i]);
+    sm = max(sm, sm << 16);
+    const float lsm = (float)(int)(sm >> 23) - 126.0f;
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float y = x[0][nt][e] + lsv[0][0];
-        y = fmaxf(y, x[0][nt][e + 2] + lsv[0][1]);
-        y = fmaxf(y, x[1][nt][e] + lsv[1][0]);
-        y = fmaxf(y, x[1][nt][e + 2] + lsv[1][1]);
-        top[nt][e] = y;
-        over = over || y > m[nt][e] + kQ4Head;
+        const float y = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
+        over = over || log2_of(y, nt, e) + lsm > m[nt][e] + kQ4Head;
       }
     if (__any_sync(0xffffffffu, over)) {
+      float lsv[2][2];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float big = __uint_as_float(kQ4Tiny & 0xffff0000u);
+#pragma unroll
+          for (int a = 0; a < G; ++a) big = fmaxf(big, fabsf(scale_of(sv[mt][e][a / 2], a & 1)));
+          lsv[mt][e] = __log2f(big);
+        }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float y = top[nt][e];
+          float y = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y = fmaxf(y, log2_of(x[k >> 1][nt][e + 2 * (k & 1)], nt, e) + lsv[k >> 1][k & 1]);
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
@@ -424,24 +477,16 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-        float sum = 0.0f;
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float& s = x[mt][nt][e + 2 * k];
-            s = ex2_approx(s - ref);
-            sum += s;
-          }
-        l[nt][e] += sum;
+        for (int k = 0; k < 4; ++k) {
+          float& s = x[k >> 1][nt][e + 2 * (k & 1)];
+          s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
+          l[nt][e] += s;
+        }
       }
     // O^T += V^T P^T
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      float sv[2][G];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        row_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[e]);
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
       for (int a2 = 0; a2 < G; a2 += 2) {  // two groups: keys 0-7 and 8-15 of each
         uint32_t w[4];
@@ -452,48 +497,42 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
         for (int da = 0; da < 2; ++da) {
           const int a = a2 + da;
           uint32_t f[2][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[0][j] = v_pair(w[2 * da], j);
-            f[1][j] = v_pair(w[2 * da + 1], j);
-          }
+          nibble_pairs(w[2 * da], f[0]);
+          nibble_pairs(w[2 * da + 1], f[1]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float pv[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              pv[e] = x[mt][nt][e] * sv[e >> 1][a];
+              pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
               // a masked key adds nothing, whatever its scale holds
               if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
             }
             const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
             const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
-            mma_f16(o[a][0][nt], f[0][0], f[0][1], f[1][0], f[1][1], b0, b1);
-            mma_f16(o[a][1][nt], f[0][2], f[0][3], f[1][2], f[1][3], b0, b1);
+#pragma unroll
+            for (int jp = 0; jp < 2; ++jp)
+              mma_f16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp], f[1][2 * jp + 1],
+                      b0, b1);
           }
         }
       }
-    }
   };
 
-  const int v_first = v_begin + warp;
-  if (v_first < v_end) load_tile(v_first, 0, page_of(v_first, 0), page_of(v_first, 1));
-  if (v_first + kQ4Warps < v_end)
-    load_tile(v_first + kQ4Warps, 1, page_of(v_first + kQ4Warps, 0), page_of(v_first + kQ4Warps, 1));
-  int stage = 0;
-  for (int v = v_first; v < v_end; v += kQ4Warps, stage ^= 1) {
-    const int next = v + 2 * kQ4Warps;
-    const int pg0 = page_of(next, 0), pg1 = page_of(next, 1);
-    if (v + kQ4Warps < v_end) cp_async_wait<1>();
+  if (n_tiles > 0) load_tile(0);
+  if (n_tiles > 1) load_tile(1);
+  for (int i = 0; i < n_tiles; ++i) {
+    if (i + 1 < n_tiles) cp_async_wait<1>();
     else cp_async_wait<0>();
     __syncwarp();
-    const int key0 = tile_of(v) * kQ4Tile, key_end = key0 + kQ4Tile;
+    const int key0 = key_of(i), key_end = key0 + kQ4Tile;
     const bool whole = key_end <= len && first_pos >= 0 && (!causal || key_end - 1 <= first_pos) &&
                        (!windowed || len - 1 - key0 < p.window || key_end <= p.sink);
-    if (whole) process(stage, key0, std::false_type{});
-    else process(stage, key0, std::true_type{});
+    const uint32_t stage_off = (i & (kQ4Stages - 1)) * C::kStage;
+    if (whole) process(stage_off, key0, std::false_type{});
+    else process(stage_off, key0, std::true_type{});
     __syncwarp();
-    if (next < v_end) load_tile(next, stage, pg0, pg1);
+    if (i + 2 < n_tiles) load_tile(i + 2);
   }
   cp_async_wait<0>();
   __syncwarp();
@@ -664,6 +703,7 @@ MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, f
   f.sink = sink;
   f.scale2 = (p->scale != 0.0f ? p->scale : 1.0f / std::sqrt((float)D)) * kLog2e;
   f.softcap2 = p->softcap * kLog2e;
+  f.softcap_e = 2.0f / p->softcap;
 
   // most tiles that a sequence can have: its whole length, or sinks and window
   long long tiles = ((long long)max_len + kQ4Tile - 1) / kQ4Tile;
