@@ -374,16 +374,18 @@ attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
  * Keys that no row sees are not read, and what a masked key's record holds,
  * NaN included, changes nothing. A row without a key (an empty place of the
  * batch) gets O = 0, LSE = -inf. A page index outside [0, num_pages) reads as
- * zeros. `workspace` as for attn_decode: 256-byte aligned,
- * attn_decode_q4_workspace_bytes() for the full split count, less or NULL
- * means fewer splits; its contents need not be kept between calls. */
+ * zeros. With a workspace the keys of all sequences are shared out evenly over
+ * the SMs, and results of sequences that several CTAs share are joined from it:
+ * 256-byte aligned device memory, attn_decode_q4_workspace_bytes() for the full
+ * spread, less or NULL means fewer CTAs (one per sequence and key/value head
+ * with NULL); its contents need not be kept between calls. */
 attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B, int Hq,
                            int Hkv, int Sq, int max_len, int D, unsigned variant,
                            const attn_params* p, const int* seq_lens, int sink, void* workspace,
                            size_t workspace_bytes, struct CUstream_st* stream);
 
-/* Bytes of workspace attn_decode_q4() uses for its full split count on the
- * current device (0 when it does not split the keys). */
+/* Bytes of workspace attn_decode_q4() uses for its full spread on the current
+ * device (0 when a sequence's keys are too few to share out). */
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D);
 
 /* Bytes of device buffer build_block_mask() needs (256-byte aligned pieces). */

@@ -19,7 +19,8 @@
 //  - ldmatrix on the packed bytes puts a key's 8 channels of one 32-channel
 //    group into a lane (K), and with .trans four channels of two neighbouring
 //    keys (V): both are what the A fragments need up to the order of the
-//    channels, which q's fragments and O's rows follow.
+//    channels, which q's fragments and O's rows follow. q's fragments stay in
+//    shared memory: the registers go to more warps.
 //  - a code n becomes the exact fp16 value n - 8 by one AND/OR into the mantissa
 //    of 1024 or 64 and one packed subtraction, two codes at a time. (The bits
 //    alone, as fp16 subnormals, need no subtraction, but the products then keep
@@ -33,15 +34,21 @@
 // are rescaled) only when a key passes that bound, which one vote per 32 keys
 // decides. Sums are fp32.
 //
-// A CTA takes one (sequence, key/value head) and a run of 32-key tiles; its
-// four warps stream every fourth tile through buffers of their own (cp.async,
-// rows padded by 16 bytes so the ldmatrix rows hit distinct banks). Their
-// states meet in shared memory, and the CTAs' in the workspace (fp32), joined
-// by the online-softmax merge. With a window the tiles are those of the first
-// `sink` keys, then those of the window.
+// The tiles of 32 keys of all (sequence, key/value head) pairs, one after the
+// other, are dealt out evenly: CTA c of C takes tiles [c N / C, (c + 1) N / C), so
+// ragged lengths and few sequences load the SMs alike and the grid is one
+// resident wave (16 sequences x 8 heads in equal splits of 8 CTAs per SM ran 2.1
+// waves: 135 us against 125). A pair that lies within one CTA is written at once; one that
+// is cut leaves fp32 partial results in the workspace, which a second, small
+// kernel joins by the online-softmax merge. Within a CTA four warps stream every
+// fourth tile through buffers of their own (cp.async, 16-byte chunks swizzled for
+// ldmatrix) and their states meet in shared memory.
+// With a window the tiles are those of the first `sink` keys, then those of the
+// window.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <mutex>
 #include <type_traits>
@@ -80,22 +87,56 @@ struct Q4Problem {
   float scale2;       // scale * log2 e
   float softcap2;     // softcap * log2 e
   float softcap_e;    // 2 / softcap: e^(2 s / softcap) from s in log2 units
-  int splits, chunk;  // tiles per split
-  float* ws_o;        // [splits][rows][D], or nullptr (one split)
-  float* ws_lse;      // [splits][rows]
+  // Workspace, or nullptr: then one CTA per pair. Partial results by slot: CTA +
+  // pair (both ascend along the tiles, so each cut has its own).
+  int2* ws_meta;   // [pairs]: first and last CTA of a cut pair; first = -1: done
+  float* ws_lse;   // [slots][R], log2
+  float* ws_o;     // [slots][R][D]
 };
 
-template <int D>
+// A sequence's tiles: those of the sinks, then those from win_tile on.
+struct Q4Range {
+  int len, win_tile, sink_tiles, tiles;
+};
+
+__device__ __forceinline__ Q4Range q4_range(const Q4Problem& p, int b) {
+  Q4Range r;
+  const long long held = (long long)p.pages_per_seq << p.shift;
+  r.len = max(0, min(p.seq_lens[b], (int)min((long long)p.max_len, held)));
+  r.win_tile = r.sink_tiles = 0;
+  if (p.variant & ATTN_MASK_WINDOW) {
+    const int w0 = (int)max(0ll, (long long)r.len - p.Sq - p.window + 1);
+    r.win_tile = w0 / kQ4Tile;
+    r.sink_tiles = min(r.win_tile, (min(p.sink, r.len) + kQ4Tile - 1) / kQ4Tile);
+  }
+  r.tiles = r.sink_tiles + max(0, (r.len + kQ4Tile - 1) / kQ4Tile - r.win_tile);
+  return r;
+}
+
+template <int D, int NT>
 struct Q4Cfg {
   static constexpr int G = D / kQ4Group;                  // scales per row
-  static constexpr int kRow = D / 2 + 16;                 // padded row of codes
+  static constexpr int kRow = D / 2;                      // bytes of a row of codes
   static constexpr int kCodes = kQ4Tile * kRow;
   static constexpr int kScales = kQ4Tile * G * 2;
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
   static constexpr int kWarp = kQ4Stages * kStage;
-  static_assert(kWarp >= (2 * 16 + 16 * D) * 4, "merge state fits the warp area");
-  static constexpr int kSmem = kQ4Warps * kWarp;
+  static constexpr int kState = 8 * NT * (2 + D) * 4;      // a warp's m, l, O at the end
+  static constexpr int kArea = kWarp > kState ? kWarp : kState;
+  static constexpr int kQ = NT * G * 512;                  // q fragments, 16 bytes per lane
+  static constexpr int kSmem = kQ4Warps * kArea + kQ + NT * 8 * 4;
+  // Rows of codes are D / 2 bytes; chunk c (16 bytes) of row r stands at place
+  // c ^ swz(r), so that the 8 rows of an ldmatrix matrix hit distinct banks.
+  static __device__ __forceinline__ int swz(int row) {
+    return D == 128 ? (row >> 1) & 3 : (row >> 2) & 1;
+  }
 };
+
+// CTAs per SM that the registers are cut to.
+template <int D, int NT>
+constexpr int q4_per_sm() {
+  return D == 128 ? (NT == 1 ? 4 : 2) : (NT == 1 ? 5 : 3);
+}
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
@@ -114,6 +155,17 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
+
+// Programmatic dependent launch: lets the next kernel of the stream be set up
+// early; that kernel's wait returns when this one has ended and its writes show.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -174,102 +226,32 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) {  // i = 0 or 1
   return __uint_as_float(i ? w & 0xffff0000u : w << 16);
 }
 
+// Tiles [v_begin, v_end) of one pair, by the whole CTA: into the partial slot,
+// or (slot < 0: they are all of the pair's) into o and lse.
 template <int D, int NT, int SCORE>
-__global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p) {
-  using C = Q4Cfg<D>;
+__device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem, int b, int hkv,
+                                               const Q4Range& rg, int v_begin, int v_end,
+                                               long long slot) {
+  using C = Q4Cfg<D, NT>;
   constexpr int G = C::G;
-  extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;  // fragment coordinates
-  const int split = blockIdx.x;
-  const int b = blockIdx.y / p.Hkv, hkv = blockIdx.y % p.Hkv;
   const int group = p.Hq / p.Hkv;
   const int R = group * p.Sq;
   const size_t row0 = (size_t)(b * p.Hq + hkv * group) * p.Sq;
   const size_t total_rows = (size_t)p.B * p.Hq * p.Sq;
   const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
-
-  // the sequence's keys, and its tiles: those of the sinks, then the window's
-  const long long held = (long long)p.pages_per_seq << p.shift;
-  const int len = max(0, min(p.seq_lens[b], (int)min((long long)p.max_len, held)));
+  const int len = rg.len, sink_tiles = rg.sink_tiles, win_tile = rg.win_tile;
   const int first_pos = len - p.Sq;  // absolute position of query row 0
-  int win_tile = 0, sink_tiles = 0;
-  if (windowed) {
-    const int w0 = (int)max(0ll, (long long)first_pos - p.window + 1);
-    win_tile = w0 / kQ4Tile;
-    sink_tiles = min(win_tile, (min(p.sink, len) + kQ4Tile - 1) / kQ4Tile);
-  }
-  const int last_tile = (len + kQ4Tile - 1) / kQ4Tile;
-  const int tiles = sink_tiles + max(0, last_tile - win_tile);
-  const int v_begin = split * p.chunk, v_end = min(tiles, v_begin + p.chunk);
-  if (v_begin >= v_end && p.ws_o) {  // nothing here: the merge skips this part
-    if (threadIdx.x < R && MATTN_IN_BOUNDS(kSiteQ4Out, row0 + threadIdx.x, total_rows))
-      p.ws_lse[(size_t)split * total_rows + row0 + threadIdx.x] = -INFINITY;
-    return;
-  }
-
-  // q^T fragments (B operand), fp16: a row is scaled by a power of two that
-  // brings its largest channel to [2^14, 2^15), so bf16's 8 bits are exact
-  // (channels 2^28 times smaller lose bits below 2^-39 of the largest). Channel
-  // order of a lane's 8 per group: pairs (0, 4), (1, 5) | (2, 6), (3, 7). Rows past
-  // R are 0.
-  const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
-  uint32_t qb[NT][G][4];
-  float unit[NT][2];  // scores per product unit, log2
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    uint4 x[G];
-    float big = 0.0f;
-#pragma unroll
-    for (int a = 0; a < G; ++a) {
-      x[a] = make_uint4(0, 0, 0, 0);
-      if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
-        x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
-      const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        big = fmaxf(big, fmaxf(fabsf(scale_of(u[i], 0)), fabsf(scale_of(u[i], 1))));
-    }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
-    const float up = __uint_as_float((uint32_t)(127 + min(14 - ex, 127)) << 23);
-    const float down = exp2f((float)(ex - 14)) * p.scale2;
-    unit[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);      // rows 2t and 2t + 1
-    unit[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-#pragma unroll
-    for (int a = 0; a < G; ++a) {
-      const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-      float c[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) c[i] = scale_of(u[i / 2], i & 1) * up;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qb[nt][a][i] = pack_f16x2(c[i], c[i + 4]);
-    }
-  }
-  // the lane's query rows (columns 2t, 2t + 1 of each 8): position and slope
-  int pos[NT][2];
-  float slope2[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * t + e;
-      const int hg = r < R ? r / p.Sq : 0;
-      pos[nt][e] = first_pos + (r < R ? r % p.Sq : 0);
-      const int h = hkv * group + hg;
-      slope2[nt][e] =
-          (SCORE & 1) ? (p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq))) * kLog2e
-                      : 0.0f;
-    }
 
   // The warp's tiles: v_begin + warp, every kQ4Warps-th. Their pages are looked
   // up 16 tiles at a time, lane 2i + h the page of tile i's 16-key half h (or
   // -1), one batch ahead.
   const Q4Layout L{D, 1 << p.shift};
-  const uint32_t area = smem_u32(smem) + warp * C::kWarp;
-  const uint8_t* area_ptr = smem + warp * C::kWarp;
+  const uint32_t area = smem_u32(smem) + warp * C::kArea;
+  const uint8_t* area_ptr = smem + warp * C::kArea;
+  uint4* qs = reinterpret_cast<uint4*>(smem + kQ4Warps * C::kArea);   // [NT][G][32 lanes]
+  float* units = reinterpret_cast<float*>(smem + kQ4Warps * C::kArea + C::kQ);  // [NT * 8]
   const int v_first = v_begin + warp;
   const int n_tiles = v_first < v_end ? (v_end - v_first + kQ4Warps - 1) / kQ4Warps : 0;
   auto key_of = [&](int i) {  // first key of the warp's tile i
@@ -318,7 +300,8 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
       const uint8_t* v = k + L.v_codes();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const uint32_t d = dst + (16 * h + c * (32 / G) + lane / G) * C::kRow + lane % G * 16;
+        const uint32_t d = dst + (16 * h + c * (32 / G) + lane / G) * C::kRow +
+                           (lane % G ^ C::swz(lane / G)) * 16;
         cp_async16z(d, k + c * 512, bytes[h]);
         cp_async16z(d + C::kCodes, v + c * 512, bytes[h]);
       }
@@ -330,6 +313,66 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
                   sc_half ? bytes[1] : bytes[0]);
     cp_async_commit();
   };
+
+  if (n_tiles > 0) load_tile(0);
+  if (n_tiles > 1) load_tile(1);
+
+  // Meanwhile warp 0 prepares q^T's fragments (B operand) in shared memory, in
+  // fp16: a row is scaled by a power of two that brings its largest channel to
+  // [2^14, 2^15), so bf16's 8 bits are exact (channels 2^28 times smaller lose
+  // bits below 2^-39 of the largest). Channel order of a lane's 8 per group: pairs
+  // (0, 4), (1, 5) | (2, 6), (3, 7). Rows past R are 0.
+  if (warp == 0) {
+    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      uint4 x[G];
+      float big = 0.0f;
+#pragma unroll
+      for (int a = 0; a < G; ++a) {
+        x[a] = make_uint4(0, 0, 0, 0);
+        if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
+          x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
+        const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          big = fmaxf(big, fmaxf(fabsf(scale_of(u[i], 0)), fabsf(scale_of(u[i], 1))));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
+      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+      if (t == 0) units[r] = exp2f((float)(ex - 14)) * p.scale2;  // scores per product, log2
+#pragma unroll
+      for (int a = 0; a < G; ++a) {
+        const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+        float c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = scale_of(u[i / 2], i & 1) * up;
+        qs[(nt * G + a) * 32 + lane] = make_uint4(pack_f16x2(c[0], c[4]), pack_f16x2(c[1], c[5]),
+                                                  pack_f16x2(c[2], c[6]), pack_f16x2(c[3], c[7]));
+      }
+    }
+  }
+  __syncthreads();
+
+  // the lane's query rows (columns 2t, 2t + 1 of each 8)
+  float unit[NT][2], slope2[NT][2];
+  int pos[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * t + e;
+      unit[nt][e] = units[r];
+      const int hg = r < R ? r / p.Sq : 0;
+      pos[nt][e] = first_pos + (r < R ? r % p.Sq : 0);
+      const int h = hkv * group + hg;
+      slope2[nt][e] =
+          (SCORE & 1) ? (p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq))) * kLog2e
+                      : 0.0f;
+    }
 
   float o[G][2][NT][4];  // [group][channel pair] x (channel, row) of each 8 rows
 #pragma unroll
@@ -349,48 +392,44 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
   // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
   auto process = [&](const uint32_t stage_off, const int key0, auto mask_tag) {
     constexpr bool kMask = decltype(mask_tag)::value;
-    const uint32_t buf = area + stage_off;
+    // an ldmatrix row is a key: the lane's, with the place of chunk 0
+    const uint32_t rows = area + stage_off + lane * C::kRow + C::swz(lane) * 16;
     const uint8_t* scales = area_ptr + stage_off + 2 * C::kCodes;
     float x[2][NT][4];
-    uint32_t sv[2][2][G / 2];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {  // 16 keys: rows g and g + 8 of the fragments
-      uint32_t w[2][G];  // a lane's 8 channels of each group, for its two keys
-      if constexpr (G == 4) {
-        ldsm4(buf + (16 * mt + (lane & 7)) * C::kRow + (lane >> 3) * 16, w[0]);
-        ldsm4(buf + (16 * mt + 8 + (lane & 7)) * C::kRow + (lane >> 3) * 16, w[1]);
-      } else {
-        uint32_t u[4];
-        ldsm4(buf + (16 * mt + (lane >> 4) * 8 + (lane & 7)) * C::kRow + ((lane >> 3) & 1) * 16, u);
-        w[0][0] = u[0];
-        w[0][1] = u[1];
-        w[1][0] = u[2];
-        w[1][1] = u[3];
-      }
-      uint32_t sk[2][G / 2];
+    for (int a = 0; a < G; ++a) {
+      uint32_t w[4];  // the lane's 8 channels of group a, for keys g, g + 8, g + 16, g + 24
+      ldsm4(rows ^ (a * 16), w);
+      float sk[4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        load_scales<G>(scales + (16 * mt + 8 * e + g) * 2 * G, sk[e]);
-        load_scales<G>(scales + C::kScales + (16 * mt + 8 * e + g) * 2 * G, sv[mt][e]);
-      }
+      for (int i = 0; i < 4; ++i)
+        sk[i] = scale_of(*reinterpret_cast<const uint32_t*>(scales + (8 * i + g) * 2 * G + (a / 2) * 4),
+                         a & 1);
+      uint4 qf[NT];
 #pragma unroll
-      for (int a = 0; a < G; ++a) {
+      for (int nt = 0; nt < NT; ++nt) qf[nt] = qs[(nt * G + a) * 32 + lane];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
         uint32_t f[2][4];
-        nibble_pairs(w[0][a], f[0]);
-        nibble_pairs(w[1][a], f[1]);
+        nibble_pairs(w[2 * mt], f[0]);
+        nibble_pairs(w[2 * mt + 1], f[1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qb[nt][a][0], qb[nt][a][1]);
-          mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qb[nt][a][2], qb[nt][a][3]);
+          mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qf[nt].x, qf[nt].y);
+          mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qf[nt].z, qf[nt].w);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float s = scale_of(sk[e >> 1][a / 2], a & 1);
+            const float s = sk[2 * mt + (e >> 1)];
             x[mt][nt][e] = a == 0 ? s * d[e] : fmaf(s, d[e], x[mt][nt][e]);
           }
         }
       }
     }
+    uint32_t sv[2][2][G / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      load_scales<G>(scales + C::kScales + (8 * i + g) * 2 * G, sv[i >> 1][i & 1]);
     // score modification and mask. Without a modification the scores stay in
     // the products' units and `unit` enters with the exponent.
 #pragma unroll
@@ -486,41 +525,34 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
       }
     // O^T += V^T P^T
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+    for (int a = 0; a < G; ++a) {
+      uint32_t w[4];  // 4 channels of group a for key pairs 2t, 2t + 1 of each 8 keys
+      ldsm4_t((rows ^ (a * 16)) + C::kCodes, w);
 #pragma unroll
-      for (int a2 = 0; a2 < G; a2 += 2) {  // two groups: keys 0-7 and 8-15 of each
-        uint32_t w[4];
-        ldsm4_t(buf + C::kCodes + (16 * mt + ((lane >> 3) & 1) * 8 + (lane & 7)) * C::kRow +
-                    (a2 + (lane >> 4)) * 16,
-                w);
+      for (int mt = 0; mt < 2; ++mt) {
+        uint32_t f[2][4];
+        nibble_pairs(w[2 * mt], f[0]);
+        nibble_pairs(w[2 * mt + 1], f[1]);
 #pragma unroll
-        for (int da = 0; da < 2; ++da) {
-          const int a = a2 + da;
-          uint32_t f[2][4];
-          nibble_pairs(w[2 * da], f[0]);
-          nibble_pairs(w[2 * da + 1], f[1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          float pv[4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float pv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
-              // a masked key adds nothing, whatever its scale holds
-              if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
-            }
-            const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
-            const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
-#pragma unroll
-            for (int jp = 0; jp < 2; ++jp)
-              mma_f16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp], f[1][2 * jp + 1],
-                      b0, b1);
+          for (int e = 0; e < 4; ++e) {
+            pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
+            // a masked key adds nothing, whatever its scale holds
+            if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
           }
+          const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
+          const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
+#pragma unroll
+          for (int jp = 0; jp < 2; ++jp)
+            mma_f16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp], f[1][2 * jp + 1],
+                    b0, b1);
         }
       }
+    }
   };
 
-  if (n_tiles > 0) load_tile(0);
-  if (n_tiles > 1) load_tile(1);
   for (int i = 0; i < n_tiles; ++i) {
     if (i + 1 < n_tiles) cp_async_wait<1>();
     else cp_async_wait<0>();
@@ -537,7 +569,7 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
   cp_async_wait<0>();
   __syncwarp();
 
-  // the warps' states meet in shared memory: m, l (16 each), O [16][D]
+  // the warps' states meet in shared memory: m, l (8 NT each), O [8 NT][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -546,9 +578,10 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
       l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
       l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
     }
-  float* wm = reinterpret_cast<float*>(smem + warp * C::kWarp);
-  float* wl = wm + 16;
-  float* wo = wm + 32;
+  constexpr int kR = 8 * NT;
+  float* wm = reinterpret_cast<float*>(smem + warp * C::kArea);
+  float* wl = wm + kR;
+  float* wo = wl + kR;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     if (g == 0) {
@@ -573,70 +606,280 @@ __global__ void __launch_bounds__(kQ4Threads) decode_q4_kernel(const Q4Problem p
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kQ4Warps; ++w)
-      M = fmaxf(M, reinterpret_cast<const float*>(smem + w * C::kWarp)[r]);
+      M = fmaxf(M, reinterpret_cast<const float*>(smem + w * C::kArea)[r]);
     float Ls = 0.0f, acc = 0.0f;
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < kQ4Warps; ++w) {
-        const float* st = reinterpret_cast<const float*>(smem + w * C::kWarp);
+        const float* st = reinterpret_cast<const float*>(smem + w * C::kArea);
         const float wt = ex2_approx(st[r] - M);  // -inf -> 0
-        Ls += wt * st[16 + r];
-        acc += wt * st[32 + r * D + c];
+        Ls += wt * st[kR + r];
+        acc += wt * st[2 * kR + r * D + c];
       }
     }
     // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
     const float out = M != -INFINITY ? acc / Ls : 0.0f;
-    const float lse = M != -INFINITY ? (M + __log2f(Ls)) * kLn2 : -INFINITY;
+    const float lse2 = M != -INFINITY ? M + __log2f(Ls) : -INFINITY;
     if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
-    if (p.ws_o) {
-      if (!MATTN_IN_BOUNDS(kSiteQ4Out, split, p.splits)) continue;
-      p.ws_o[((size_t)split * total_rows + row0 + r) * D + c] = out;
-      if (c == 0) p.ws_lse[(size_t)split * total_rows + row0 + r] = lse;
+    if (slot >= 0) {
+      p.ws_o[((size_t)slot * R + r) * D + c] = out;
+      if (c == 0) p.ws_lse[(size_t)slot * R + r] = lse2;
     } else {
       static_cast<__nv_bfloat16*>(p.o)[(row0 + r) * D + c] = __float2bfloat16_rn(out);
-      if (c == 0) p.lse[row0 + r] = lse;
+      if (c == 0) p.lse[row0 + r] = lse2 * kLn2;
     }
   }
+  __syncthreads();  // the next segment's tiles overwrite the states
 }
 
 template <int D, int NT, int SCORE>
-cudaError_t launch_typed(const Q4Problem& p, cudaStream_t stream) {
-  using C = Q4Cfg<D>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(decode_q4_kernel<D, NT, SCORE>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
-  decode_q4_kernel<D, NT, SCORE><<<dim3(p.splits, p.B * p.Hkv), kQ4Threads, C::kSmem, stream>>>(p);
-  return cudaGetLastError();
-}
+__global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
+    decode_q4_kernel(const Q4Problem p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31;
+  launch_dependents();  // the merge may be set up; it waits for this grid's end
 
-template <int D, int NT>
-cudaError_t launch_score(const Q4Problem& p, cudaStream_t s) {
-  switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
-    case 0: return launch_typed<D, NT, 0>(p, s);
-    case 1: return launch_typed<D, NT, 1>(p, s);
-    case 2: return launch_typed<D, NT, 2>(p, s);
-    default: return launch_typed<D, NT, 3>(p, s);
+  // this CTA's first pair and tiles [lo, hi) of all
+  int b = blockIdx.x / p.Hkv, hkv = blockIdx.x % p.Hkv;
+  long long lo = 0, hi = LLONG_MAX, seq_start = 0;
+  bool last_cta = false;
+  if (p.ws_meta) {
+    long long total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32)
+      total += warp_sum(b0 + lane < p.B ? q4_range(p, b0 + lane).tiles : 0);
+    total *= p.Hkv;
+    // CTAs that take part: each has a tile for every warp, on the average
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, (total + kQ4Warps - 1) / kQ4Warps));
+    if (blockIdx.x >= ctas) return;
+    last_cta = blockIdx.x == ctas - 1;
+    lo = total * blockIdx.x / ctas;
+    hi = total * (blockIdx.x + 1) / ctas;
+    // the first sequence that ends past lo, or starts there without tiles
+    b = p.B;
+    long long before = 0;
+    for (int b0 = 0; b0 < p.B && b == p.B; b0 += 32) {
+      const int n = b0 + lane < p.B ? q4_range(p, b0 + lane).tiles : 0;
+      int end = n;  // inclusive scan
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, end, d);
+        if (lane >= d) end += v;
+      }
+      const long long e = before + (long long)end * p.Hkv, s0 = e - (long long)n * p.Hkv;
+      const unsigned hit = __ballot_sync(0xffffffffu, b0 + lane < p.B && (e > lo || s0 >= lo));
+      if (hit) {
+        const int f = __ffs(hit) - 1;
+        b = b0 + f;
+        seq_start = __shfl_sync(0xffffffffu, s0, f);
+      }
+      before = __shfl_sync(0xffffffffu, e, 31);
+    }
+    hkv = 0;
+  }
+
+  for (; b < p.B; ++b, hkv = 0) {
+    const Q4Range rg = q4_range(p, b);
+    if (p.ws_meta) {
+      if (seq_start >= hi && !(last_cta && rg.tiles == 0)) break;
+      if (rg.tiles > 0) hkv = max(0, (int)((lo - seq_start) / rg.tiles));
+    }
+    for (; hkv < p.Hkv; ++hkv) {
+      int v_begin = 0, v_end = rg.tiles;
+      const long long start = seq_start + (long long)hkv * rg.tiles;
+      if (p.ws_meta && rg.tiles > 0) {
+        if (start >= hi) break;
+        v_begin = (int)max(0ll, lo - start);
+        v_end = (int)min((long long)rg.tiles, hi - start);
+      }
+      const bool cut = v_begin > 0 || v_end < rg.tiles;
+      const int pair = b * p.Hkv + hkv;
+      if (p.ws_meta && threadIdx.x == 0) {
+        if (v_begin == 0) p.ws_meta[pair].x = cut ? (int)blockIdx.x : -1;
+        if (v_end == rg.tiles) p.ws_meta[pair].y = (int)blockIdx.x;
+      }
+      decode_segment<D, NT, SCORE>(p, smem, b, hkv, rg, v_begin, v_end,
+                                   cut ? (long long)blockIdx.x + pair : -1);
+      if (!p.ws_meta) return;
+    }
+    seq_start += (long long)rg.tiles * p.Hkv;
   }
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Most splits that a call over `tiles` 32-key tiles uses: about eight CTAs
-// per SM, at least one tile per warp. Does not fall when `tiles` grows.
-int q4_most_splits(int B, int Hkv, long long tiles) {
-  const long long ctas = (long long)B * Hkv;
-  const long long want = std::min((8LL * sm_count() + ctas - 1) / ctas,
-                                  (tiles + kQ4Warps - 1) / kQ4Warps);
-  return (int)std::max(1LL, std::min(want, 64LL));
+// Joins the partial results of the pairs that several CTAs share: W warps per
+// row of o take its parts in turn (a fixed order), each lane D / 32 channels.
+// Bound by latency: two dependent loads, then the parts' rows from the L2.
+template <int D, int W>
+__global__ void __launch_bounds__(kQ4Threads) q4_merge_kernel(const Q4Problem p) {
+  constexpr int V = D / 32;
+  __shared__ float sh[kQ4Warps][D + 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long rows = (long long)p.B * p.Hq * p.Sq;
+  const long long row = (long long)blockIdx.x * (kQ4Warps / W) + warp / W;
+  wait_for_primary();
+  float M = -INFINITY, L = 0.0f, acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+  bool mine = false;
+  if (row < rows) {
+    const int group = p.Hq / p.Hkv, R = group * p.Sq;
+    const long long bh = row / p.Sq;
+    const int h = (int)(bh % p.Hq);
+    const long long pair = bh / p.Hq * p.Hkv + h / group;
+    const int r = h % group * p.Sq + (int)(row % p.Sq);
+    const int2 ctas = p.ws_meta[pair];
+    mine = ctas.x >= 0;
+    if (mine) {
+      for (int c0 = ctas.x + warp % W; c0 <= ctas.y; c0 += 32 * W) {  // 32 parts at a time
+        const int c = c0 + lane * W;
+        const float lse = c <= ctas.y ? p.ws_lse[(c + pair) * R + r] : -INFINITY;
+        float m = lse;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float m_new = fmaxf(M, m);
+        const float ref = m_new == -INFINITY ? 0.0f : m_new;
+        const float w = ex2_approx(lse - ref), fix = ex2_approx(M - ref);  // -inf -> 0
+        L *= fix;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] *= fix;
+        M = m_new;
+        const int n = min(32, (ctas.y - c0) / W + 1);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const float wk = __shfl_sync(0xffffffffu, w, k);
+          const float* part = p.ws_o + ((c0 + (long long)k * W + pair) * R + r) * D + lane * V;
+          float x[V];
+          if constexpr (V == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(part);
+            x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(part);
+            x[0] = f.x, x[1] = f.y;
+          }
+          L += wk;
+#pragma unroll
+          for (int i = 0; i < V; ++i) acc[i] += wk * x[i];
+        }
+      }
+    }
+  }
+  if constexpr (W > 1) {  // W = the block's warps: one row
+    sh[warp][D] = M;
+    sh[warp][D + 1] = L;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sh[warp][lane * V + i] = acc[i];
+    __syncthreads();
+    if (warp) return;
+#pragma unroll
+    for (int k = 1; k < W; ++k) M = fmaxf(M, sh[k][D]);
+    L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float w = M == -INFINITY ? 0.0f : ex2_approx(sh[k][D] - M);
+      L += w * sh[k][D + 1];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += w * sh[k][lane * V + i];
+    }
+  }
+  if (!mine || !MATTN_IN_BOUNDS(kSiteQ4Out, row, rows)) return;
+  const bool any = M != -INFINITY;  // else no key in any part
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t*>(out + i) =
+        any ? pack_bf16x2(acc[i] / L, acc[i + 1] / L) : 0u;
+  if (lane == 0) p.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
 }
 
-size_t q4_ws_per_split(int B, int Hq, int Sq, int D) {
-  const size_t rows = (size_t)B * Hq * Sq;
-  return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
+template <int D>
+cudaError_t launch_merge(const Q4Problem& p, int ctas, cudaStream_t stream) {
+  const long long rows = (long long)p.B * p.Hq * p.Sq;
+  // One warp per row where a pair is cut into few parts; a whole block where
+  // the CTAs are at least eight times the pairs.
+  const bool wide = ctas >= 8LL * p.B * p.Hkv;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + kQ4Warps - 1) / kQ4Warps));
+  cfg.blockDim = dim3(kQ4Threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return wide ? cudaLaunchKernelEx(&cfg, q4_merge_kernel<D, kQ4Warps>, p)
+              : cudaLaunchKernelEx(&cfg, q4_merge_kernel<D, 1>, p);
+}
+
+constexpr int kQ4CtasPerSm = 5;  // most resident CTAs that a call uses
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// CTAs that share `tiles` tiles: a resident wave, or one per four tiles (a
+// warp each) where there are fewer.
+int q4_ctas(long long tiles, int resident) {
+  return (int)std::max(1LL, std::min<long long>(resident, (tiles + kQ4Warps - 1) / kQ4Warps));
+}
+
+struct Q4Workspace {
+  size_t lse, o, total;  // meta at 0
+};
+
+Q4Workspace q4_workspace(long long pairs, int ctas, int R, int D) {
+  const size_t slots = (size_t)(pairs + ctas);
+  Q4Workspace w;
+  w.lse = align256(pairs * sizeof(int2));
+  w.o = w.lse + align256(slots * R * sizeof(float));
+  w.total = w.o + align256(slots * R * D * sizeof(float));
+  return w;
+}
+
+template <int D, int NT, int SCORE>
+cudaError_t launch_typed(Q4Problem& p, long long tiles, void* ws, size_t ws_bytes,
+                         cudaStream_t stream) {
+  using C = Q4Cfg<D, NT>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  static int per_sm = 1;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(decode_q4_kernel<D, NT, SCORE>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (attr_err == cudaSuccess)
+      attr_err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+          &per_sm, decode_q4_kernel<D, NT, SCORE>, kQ4Threads, C::kSmem);
+    per_sm = std::max(1, std::min(per_sm, kQ4CtasPerSm));
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  const long long pairs = (long long)p.B * p.Hkv;
+  const int R = p.Hq / p.Hkv * p.Sq;
+  // As many CTAs as the workspace has slots for; one per pair, writing o and
+  // lse at once, where that is no fewer or a pair has no more tiles than a CTA
+  // warps.
+  int ctas = q4_ctas(tiles * pairs, per_sm * sm_count());
+  const int want = ctas;
+  while (ctas > 1 && q4_workspace(pairs, ctas, R, D).total > ws_bytes) ctas /= 2;
+  const bool split = ws && tiles > kQ4Warps && ctas > 1 && (ctas == want || ctas > pairs);
+  if (!split) {
+    decode_q4_kernel<D, NT, SCORE><<<(unsigned)pairs, kQ4Threads, C::kSmem, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const Q4Workspace w = q4_workspace(pairs, ctas, R, D);
+  p.ws_meta = static_cast<int2*>(ws);
+  p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + w.lse);
+  p.ws_o = reinterpret_cast<float*>(static_cast<char*>(ws) + w.o);
+  decode_q4_kernel<D, NT, SCORE><<<ctas, kQ4Threads, C::kSmem, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_merge<D>(p, ctas, stream);
+}
+
+template <int D, int NT>
+cudaError_t launch_score(Q4Problem& p, long long tiles, void* ws, size_t n, cudaStream_t s) {
+  switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
+    case 0: return launch_typed<D, NT, 0>(p, tiles, ws, n, s);
+    case 1: return launch_typed<D, NT, 1>(p, tiles, ws, n, s);
+    case 2: return launch_typed<D, NT, 2>(p, tiles, ws, n, s);
+    default: return launch_typed<D, NT, 3>(p, tiles, ws, n, s);
+  }
 }
 
 }  // namespace
@@ -644,9 +887,12 @@ size_t q4_ws_per_split(int B, int Hq, int Sq, int D) {
 
 MATTN_API size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || max_len < 1 || (D != 64 && D != 128)) return 0;
-  const int splits = mattn::q4_most_splits(B, Hkv, ((long long)max_len + mattn::kQ4Tile - 1) /
-                                                       mattn::kQ4Tile);
-  return splits > 1 ? (size_t)splits * mattn::q4_ws_per_split(B, Hq, Sq, D) : 0;
+  using namespace mattn;
+  const long long pairs = (long long)B * Hkv;
+  const long long tiles = ((long long)max_len + kQ4Tile - 1) / kQ4Tile;
+  if (tiles <= kQ4Warps || Hq % Hkv) return 0;
+  return q4_workspace(pairs, q4_ctas(tiles * pairs, kQ4CtasPerSm * sm_count()),
+                      Hq / Hkv * Sq, D).total;
 }
 
 MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B,
@@ -710,25 +956,13 @@ MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, f
   if (variant & ATTN_MASK_WINDOW)
     tiles = std::min(tiles, ((long long)sink + kQ4Tile - 1) / kQ4Tile +
                                 ((long long)p->window + Sq - 1 + 2 * kQ4Tile - 2) / kQ4Tile);
-  int splits = q4_most_splits(B, Hkv, tiles);
-  const size_t fit = workspace ? workspace_bytes / q4_ws_per_split(B, Hq, Sq, D) : 0;
-  if ((size_t)splits > fit) splits = fit >= 2 ? (int)fit : 1;  // as many as the workspace holds
-  f.chunk = (int)std::max(1LL, (tiles + splits - 1) / splits);
-  f.splits = splits = (int)std::max(1LL, (tiles + f.chunk - 1) / f.chunk);
-  const long long rows = (long long)B * Hq * Sq;
-  if (splits > 1) {
-    f.ws_o = static_cast<float*>(workspace);
-    f.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        align256((size_t)rows * D * sizeof(float)) * splits);
-  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool two = (Hq / Hkv) * Sq > 8;
-  cudaError_t e;
-  if (D == 64) e = two ? launch_score<64, 2>(f, s) : launch_score<64, 1>(f, s);
-  else e = two ? launch_score<128, 2>(f, s) : launch_score<128, 1>(f, s);
-  attn_status st = cuda_status(e);
-  if (st != ATTN_OK || splits == 1) return st;
-  return cuda_status(launch_combine_f32_bf16(f.ws_o, f.ws_lse, splits, rows, D, o, lse, s));
+  if (D == 64)
+    return cuda_status(two ? launch_score<64, 2>(f, tiles, workspace, workspace_bytes, s)
+                           : launch_score<64, 1>(f, tiles, workspace, workspace_bytes, s));
+  return cuda_status(two ? launch_score<128, 2>(f, tiles, workspace, workspace_bytes, s)
+                         : launch_score<128, 1>(f, tiles, workspace, workspace_bytes, s));
 }
 
 namespace mattn {

@@ -127,17 +127,15 @@ def test_lengths(D, page, heads):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D,heads", [(64, (4, 2, 2)), (128, (8, 1, 1)), (128, (12, 1, 1))])
-@pytest.mark.parametrize("ws", ["full", "none", "two"])
+@pytest.mark.parametrize("ws", ["full", "none", "third", 256])
 def test_long_and_split(D, heads, ws):
-    """Keys split over CTAs, over none, and over as many as a small workspace holds."""
+    """Keys shared by many CTAs, by none, and by as many as a small workspace allows."""
     import masked_attention_gb300 as M
     Hq, Hkv, Sq = heads
     c = Cache([1500, 7, 0, 900], Hkv, D, 32, seed=3)
-    if ws == "two":
+    if ws == "third":
         full = M.attn_decode_q4_workspace_bytes(4, Hq, Hkv, Sq, c.table.shape[1] * 32, D)
-        per = (4 * Hq * Sq * D * 4 + 255) // 256 * 256 + (4 * Hq * Sq * 4 + 255) // 256 * 256
-        assert full >= 2 * per
-        ws = 2 * per + 17
+        ws = full // 3 + 17
     check(c, queries(4, Hq, Sq, D), ws)
 
 
