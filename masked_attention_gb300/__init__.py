@@ -486,47 +486,83 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, variant: int = 0, *,
     _check(st, "attn_bwd_noalloc")
 
 
-def _tensor(where: str, name: str, x, dtype, device, shape=None):
-    """Checks a tensor argument; contiguous when a shape is given."""
-    import torch
-    if not isinstance(x, torch.Tensor):
+# The calls below run once per layer of a decode step, where the host's time is
+# what counts, so their checks are few attribute reads per tensor; what a refusal
+# says is worked out only once one fails.
+_torch = None
+
+
+def _lazy_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _refuse(where: str, name: str, x, dtype, dev: int, shape=None) -> None:
+    """Raises what is wrong with a tensor argument (shape: contiguous of that shape)."""
+    if not isinstance(x, _torch.Tensor):
         raise ValueError(f"{where}: {name} must be a tensor")
-    if x.dtype != dtype:
+    if x.dtype is not dtype:
         raise ValueError(f"{where}: {name} must be {dtype}, not {x.dtype}")
-    if x.device != device or not x.is_cuda:
+    if not x.is_cuda or x.get_device() != dev:
         raise ValueError(f"{where}: {name} is on {x.device}, not on one CUDA device with the rest")
-    if shape is not None:
-        if tuple(x.shape) != tuple(shape):
-            raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not "
-                             f"{tuple(x.shape)}")
-        if not x.is_contiguous():
-            raise ValueError(f"{where}: {name} must be contiguous")
-    return x.data_ptr()
-
-
-def _view(where: str, name: str, x, dtype, device, shape) -> attn_view:
-    """A [B, H, S, D] tensor of any strides with contiguous D."""
-    p = _tensor(where, name, x, dtype, device)
-    if tuple(x.shape) != tuple(shape):
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{where}: {name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
-    sb, sh, ss, sd = x.stride()
-    if sd != 1:
-        raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
-    return attn_view(p, sb, sh, ss)
+    if shape is not None and not x.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    raise ValueError(f"{where}: the last dimension of {name} must be contiguous")
 
 
-def _run(where: str, fn, device, stream, *args) -> None:
-    """Calls fn(*args, stream) on the tensors' device (its current stream unless given)."""
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
+def _tensor(where: str, name: str, x, dtype, dev: int, shape) -> int:
+    """Address of a contiguous tensor argument, checked."""
+    try:
+        if (x.dtype is dtype and x.get_device() == dev and x.shape == shape and dev >= 0
+                and x.is_contiguous()):
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(where, name, x, dtype, dev, shape)
+
+
+def _view(where: str, name: str, x, dtype, dev: int, shape):
+    """A [B, H, S, D] tensor of any strides with contiguous D, checked."""
+    try:
+        if x.dtype is dtype and x.get_device() == dev and x.shape == shape and dev >= 0:
+            sb, sh, ss, sd = x.stride()
+            if sd == 1 or shape[3] == 1:
+                return ctypes.byref(attn_view(x.data_ptr(), sb, sh, ss))
+            _refuse(where, name, x, dtype, dev)
+    except AttributeError:
+        pass
+    _refuse(where, name, x, dtype, dev, shape)
+
+
+def _device(where: str, name: str, x) -> int:
+    """Index of the CUDA device that a call's tensors are on."""
+    _lazy_torch()
+    if not isinstance(x, _torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{where}: {name} must be a CUDA tensor")
+    return x.get_device()
+
+
+def _run(where: str, fn, dev: int, stream, *args) -> None:
+    """Calls fn(*args, stream) on device `dev` (on its current stream unless given)."""
+    stream = _current_stream(dev) if stream is None else _stream(stream)
+    if dev == _torch.cuda.current_device():
+        st = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
+        with _torch.cuda.device(dev):
+            st = fn(*args, stream)
     if st != ATTN_OK:
         raise AttnError(st, where)
+
+
+def _current_stream(dev: int) -> int:
+    # the handle alone; torch.cuda.current_stream builds a Stream object around it
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else _torch.cuda.current_stream(dev).cuda_stream
 
 
 def attn_page_plan(cached_lens, new_lens, page_table, free_pages, seq_lens, cu_new, slots,
@@ -539,43 +575,42 @@ def attn_page_plan(cached_lens, new_lens, page_table, free_pages, seq_lens, cu_n
     ``seq_ids`` [max_tokens] (-1 past the last one), and ``info`` [4]: new
     tokens, pages taken, pages lacking, requests longer than their table. All
     int32 but ``slots``. See include/mattn.h."""
-    import torch
-    w, dev, i32 = "attn_page_plan", cached_lens.device, torch.int32
+    w = "attn_page_plan"
+    dev = _device(w, "cached_lens", cached_lens)
+    i32 = _torch.int32
     B, per = page_table.shape
-    n = slots.shape[0]
+    n, n_free = slots.numel(), free_pages.numel()
     _run(w, lib().attn_page_plan, dev, stream, _tensor(w, "cached_lens", cached_lens, i32, dev, (B,)),
          _tensor(w, "new_lens", new_lens, i32, dev, (B,)), B,
          _tensor(w, "page_table", page_table, i32, dev, (B, per)), per, page_size,
-         _tensor(w, "free_pages", free_pages, i32, dev, (free_pages.numel(),)), free_pages.numel(),
+         _tensor(w, "free_pages", free_pages, i32, dev, (n_free,)), n_free,
          _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)),
          _tensor(w, "cu_new", cu_new, i32, dev, (B + 1,)),
-         _tensor(w, "slots", slots, torch.int64, dev, (n,)),
+         _tensor(w, "slots", slots, _torch.int64, dev, (n,)),
          _tensor(w, "positions", positions, i32, dev, (n,)),
          _tensor(w, "seq_ids", seq_ids, i32, dev, (n,)), n, _tensor(w, "info", info, i32, dev, (4,)))
 
 
-def _rope_params(w: str, x, B, S, D, q_weight, k_weight, eps, cos_sin, positions,
-                 interleaved) -> attn_rope_params:
-    import torch
-    if x.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"{w}: tensors must be bfloat16 or float32, not {x.dtype}")
-    dev, f32 = x.device, torch.float32
-    p = attn_rope_params()
-    p.dtype = F32 if x.dtype == f32 else BF16
-    p.eps = eps
+def _rope_params(w: str, dt, dev: int, tokens: int, D: int, q_weight, k_weight, eps, cos_sin,
+                 positions, interleaved):
+    if dt is not _torch.bfloat16 and dt is not _torch.float32:
+        raise ValueError(f"{w}: tensors must be bfloat16 or float32, not {dt}")
+    f32 = _torch.float32
+    max_pos = rot_dim = 0
+    qw = kw = table = pos = None
     if q_weight is not None:
-        p.q_weight = _tensor(w, "q_weight", q_weight, f32, dev, (D,))
+        qw = _tensor(w, "q_weight", q_weight, f32, dev, (D,))
     if k_weight is not None:
-        p.k_weight = _tensor(w, "k_weight", k_weight, f32, dev, (D,))
+        kw = _tensor(w, "k_weight", k_weight, f32, dev, (D,))
     if cos_sin is not None:
-        p.max_pos, p.rot_dim = cos_sin.shape
-        p.cos_sin = _tensor(w, "cos_sin", cos_sin, f32, dev, cos_sin.shape)
+        max_pos, rot_dim = cos_sin.shape
+        table = _tensor(w, "cos_sin", cos_sin, f32, dev, (max_pos, rot_dim))
     if positions is not None:
-        p.positions = _tensor(w, "positions", positions, torch.int32, dev, positions.shape)
-        if positions.numel() != B * S:
-            raise ValueError(f"{w}: positions must have {B * S} entries ([B, S])")
-    p.interleaved = int(bool(interleaved))
-    return p
+        pos = _tensor(w, "positions", positions, _torch.int32, dev, positions.shape)
+        if positions.numel() != tokens:
+            raise ValueError(f"{w}: positions must have {tokens} entries ([B, S])")
+    return ctypes.byref(attn_rope_params(F32 if dt is f32 else BF16, eps, qw, kw, table, max_pos,
+                                         rot_dim, 1 if interleaved else 0, pos))
 
 
 def attn_qk_norm_rope(q, k, q_out, k_out, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -590,12 +625,18 @@ def attn_qk_norm_rope(q, k, q_out, k_out, *, q_weight=None, k_weight=None, eps: 
     the sines; None: no rotation), ``positions`` int32 [B, S] (None: 0..S-1;
     rows whose position is outside the table are not written)."""
     w = "attn_qk_norm_rope"
-    B, Hq, S, D = q.shape
-    Hkv = k.shape[1] if k is not None else 0
-    p = _rope_params(w, q, B, S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
-    v = [ctypes.byref(_view(w, n, x, q.dtype, q.device, (B, H, S, D))) if H else None
-         for n, x, H in (("q", q, Hq), ("k", k, Hkv), ("q_out", q_out, Hq), ("k_out", k_out, Hkv))]
-    _run(w, lib().attn_qk_norm_rope, q.device, stream, *v, B, Hq, Hkv, S, D, ctypes.byref(p))
+    dev = _device(w, "q", q)
+    B, Hq, S, D = shape = q.shape
+    dt = q.dtype
+    p = _rope_params(w, dt, dev, B * S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
+    kv = ko = None
+    Hkv = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        kv = _view(w, "k", k, dt, dev, (B, Hkv, S, D))
+        ko = _view(w, "k_out", k_out, dt, dev, (B, Hkv, S, D))
+    _run(w, lib().attn_qk_norm_rope, dev, stream, _view(w, "q", q, dt, dev, shape), kv,
+         _view(w, "q_out", q_out, dt, dev, shape), ko, B, Hq, Hkv, S, D, p)
 
 
 def attn_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
@@ -611,20 +652,30 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, *, dq_weight=None, dk_we
     ``dk_out`` of its outputs writes ``dq``, ``dk`` and the weights' gradients
     ``dq_weight``, ``dk_weight`` (fp32 [D]; None: not wanted). ``workspace``:
     a CUDA tensor of ``attn_qk_norm_rope_bwd_workspace_bytes(D)`` bytes."""
-    import torch
     w = "attn_qk_norm_rope_bwd"
-    B, Hq, S, D = dq_out.shape
+    dev = _device(w, "dq_out", dq_out)
+    B, Hq, S, D = qs = dq_out.shape
     Hkv = dk_out.shape[1] if dk_out is not None else 0
-    dt, dev = dq_out.dtype, dq_out.device
-    p = _rope_params(w, dq_out, B, S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
-    v = [ctypes.byref(_view(w, n, x, dt, dev, (B, H, S, D))) if H and x is not None else None
-         for n, x, H in (("q", q, Hq), ("k", k, Hkv), ("dq_out", dq_out, Hq),
-                         ("dk_out", dk_out, Hkv), ("dq", dq, Hq), ("dk", dk, Hkv))]
-    dw = [None if g is None else _tensor(w, n, g, torch.float32, dev, (D,))
-          for n, g in (("dq_weight", dq_weight), ("dk_weight", dk_weight))]
-    ws = _tensor(w, "workspace", workspace, workspace.dtype, dev, workspace.shape)
-    _run(w, lib().attn_qk_norm_rope_bwd, dev, stream, *v, *dw, ws,
-         workspace.numel() * workspace.element_size(), B, Hq, Hkv, S, D, ctypes.byref(p))
+    ks = (B, Hkv, S, D)
+    dt, f32 = dq_out.dtype, _torch.float32
+    p = _rope_params(w, dt, dev, B * S, D, q_weight, k_weight, eps, cos_sin, positions, interleaved)
+    _run(w, lib().attn_qk_norm_rope_bwd, dev, stream,
+         _view(w, "q", q, dt, dev, qs) if q is not None else None,
+         _view(w, "k", k, dt, dev, ks) if Hkv and k is not None else None,
+         _view(w, "dq_out", dq_out, dt, dev, qs),
+         _view(w, "dk_out", dk_out, dt, dev, ks) if Hkv else None,
+         _view(w, "dq", dq, dt, dev, qs), _view(w, "dk", dk, dt, dev, ks) if Hkv else None,
+         None if dq_weight is None else _tensor(w, "dq_weight", dq_weight, f32, dev, (D,)),
+         None if dk_weight is None else _tensor(w, "dk_weight", dk_weight, f32, dev, (D,)),
+         *_workspace(w, workspace, dev), B, Hq, Hkv, S, D, p)
+
+
+def _workspace(w: str, x, dev: int) -> tuple:
+    """(address, bytes) of a workspace tensor of any type, or (None, 0)."""
+    if x is None:
+        return None, 0
+    return (_tensor(w, "workspace", x, getattr(x, "dtype", None), dev, getattr(x, "shape", None)),
+            x.numel() * x.element_size())
 
 
 def attn_cache_q4_bytes(num_pages: int, Hkv: int, page_size: int, D: int) -> int:
@@ -633,26 +684,23 @@ def attn_cache_q4_bytes(num_pages: int, Hkv: int, page_size: int, D: int) -> int
     return int(lib().attn_cache_q4_bytes(num_pages, Hkv, page_size, D))
 
 
-def _pool_q4(w: str, pool, Hkv: int, page_size: int, D: int, device):
-    import torch
-    if pool.dim() != 3:
-        raise ValueError(f"{w}: pool must be uint8 [num_pages, Hkv, record bytes]")
-    record = attn_cache_q4_bytes(1, 1, page_size, D)
-    if not record:
-        raise AttnError(ATTN_ERR_UNSUPPORTED, w)
-    return _tensor(w, "pool", pool, torch.uint8, device, (pool.shape[0], Hkv, record))
-
-
-def _cache_q4(w: str, k, v, slots, pool, page_size: int):
-    import torch
-    B, Hkv, S, D = k.shape
-    dev = k.device
-    views = [ctypes.byref(_view(w, n, x, torch.bfloat16, dev, k.shape))
-             for n, x in (("k", k), ("v", v))]
-    ps = _tensor(w, "slots", slots, torch.int64, dev, slots.shape)
+def _cache_q4(w: str, load: bool, k, v, slots, pool, page_size: int, stream) -> None:
+    dev = _device(w, "k", k)
+    B, Hkv, S, D = shape = k.shape
+    bf16 = _torch.bfloat16
+    pages = pool.shape[0]
+    vk, vv = _view(w, "k", k, bf16, dev, shape), _view(w, "v", v, bf16, dev, shape)
+    ps = _tensor(w, "slots", slots, _torch.int64, dev, slots.shape)
     if slots.numel() != B * S:
         raise ValueError(f"{w}: slots must have {B * S} entries ([B, S])")
-    return views, ps, _pool_q4(w, pool, Hkv, page_size, D, dev), (B, Hkv, S, D)
+    # codes and scales of a token and head: D + D / 8 bytes (include/mattn.h)
+    pp = _tensor(w, "pool", pool, _torch.uint8, dev, (pages, Hkv, page_size * (D + D // 8)))
+    if load:
+        _run(w, lib().attn_cache_load_q4, dev, stream, pp, pages, page_size, ps, vk, vv, B, Hkv, S,
+             D)
+    else:
+        _run(w, lib().attn_cache_store_q4, dev, stream, vk, vv, ps, pp, pages, page_size, B, Hkv,
+             S, D)
 
 
 def attn_cache_store_q4(k, v, slots, pool, *, page_size: int, stream=None) -> None:
@@ -660,20 +708,14 @@ def attn_cache_store_q4(k, v, slots, pool, *, page_size: int, stream=None) -> No
     D) into the 4-bit ``pool`` (uint8 [num_pages, Hkv, record bytes]) at
     ``slots`` (int64 [B, S], page * page_size + row, each at most once; a slot
     outside the pool is skipped). Record layout and rounding: include/mattn.h."""
-    w = "attn_cache_store_q4"
-    views, ps, pp, shape = _cache_q4(w, k, v, slots, pool, page_size)
-    _run(w, lib().attn_cache_store_q4, k.device, stream, *views, ps, pp, pool.shape[0], page_size,
-         *shape)
+    _cache_q4("attn_cache_store_q4", False, k, v, slots, pool, page_size, stream)
 
 
 def attn_cache_load_q4(pool, slots, k, v, *, page_size: int, stream=None) -> None:
     """Reads the rows at ``slots`` of the 4-bit ``pool`` into ``k``, ``v``
     (bf16 [B, Hkv, S, D], any strides with contiguous D); a slot outside the
     pool reads as zeros."""
-    w = "attn_cache_load_q4"
-    views, ps, pp, shape = _cache_q4(w, k, v, slots, pool, page_size)
-    _run(w, lib().attn_cache_load_q4, k.device, stream, pp, pool.shape[0], page_size, ps, *views,
-         *shape)
+    _cache_q4("attn_cache_load_q4", True, k, v, slots, pool, page_size, stream)
 
 
 def attn_decode_q4_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, max_len: int,
@@ -692,28 +734,25 @@ def attn_decode_q4(q, pool, o, lse, variant: int = 0, *, page_table, page_size: 
     table holds) bounds seq_lens. With ``MASK_WINDOW`` the first ``sink`` keys
     stay visible. Writes ``o`` (bf16, like q) and ``lse`` fp32 [B, Hq, Sq].
     ``workspace``: optional CUDA tensor (``attn_decode_q4_workspace_bytes``)."""
-    import torch
-    w, dev = "attn_decode_q4", q.device
-    B, Hq, Sq, D = q.shape
+    w = "attn_decode_q4"
+    dev = _device(w, "q", q)
+    bf16, i32, f32 = _torch.bfloat16, _torch.int32, _torch.float32
+    B, Hq, Sq, D = shape = q.shape
     pages, Hkv = pool.shape[:2]
-    p = attn_params()
-    p.dtype, p.scale, p.window, p.softcap = BF16, scale, window, softcap
-    if alibi_slopes is not None:
-        p.alibi_slopes = _tensor(w, "alibi_slopes", alibi_slopes, torch.float32, dev, (Hq,))
     per = page_table.shape[1]
-    p.page_table = _tensor(w, "page_table", page_table, torch.int32, dev, (B, per))
-    p.page_size, p.pages_per_seq, p.num_pages = page_size, per, pages
-    ws, ws_bytes = None, 0
-    if workspace is not None:
-        ws = _tensor(w, "workspace", workspace, workspace.dtype, dev, workspace.shape)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _run(w, lib().attn_decode_q4, dev, stream,
-         _tensor(w, "q", q, torch.bfloat16, dev, q.shape),
-         _pool_q4(w, pool, Hkv, page_size, D, dev),
-         _tensor(w, "o", o, torch.bfloat16, dev, q.shape),
-         _tensor(w, "lse", lse, torch.float32, dev, (B, Hq, Sq)), B, Hq, Hkv, Sq,
-         per * page_size if max_len is None else max_len, D, variant, ctypes.byref(p),
-         _tensor(w, "seq_lens", seq_lens, torch.int32, dev, (B,)), sink, ws, ws_bytes)
+    p = attn_params(BF16, scale, window, softcap)
+    if alibi_slopes is not None:
+        p.alibi_slopes = _tensor(w, "alibi_slopes", alibi_slopes, f32, dev, (Hq,))
+    p.page_table = _tensor(w, "page_table", page_table, i32, dev, (B, per))
+    p.page_size = page_size
+    p.pages_per_seq = per
+    p.num_pages = pages
+    ws, ws_bytes = _workspace(w, workspace, dev)
+    _run(w, lib().attn_decode_q4, dev, stream, _tensor(w, "q", q, bf16, dev, shape),
+         _tensor(w, "pool", pool, _torch.uint8, dev, (pages, Hkv, page_size * (D + D // 8))),
+         _tensor(w, "o", o, bf16, dev, shape), _tensor(w, "lse", lse, f32, dev, (B, Hq, Sq)),
+         B, Hq, Hkv, Sq, per * page_size if max_len is None else max_len, D, variant,
+         ctypes.byref(p), _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)), sink, ws, ws_bytes)
 
 
 def attn_check_status(status=None, stream=None) -> int:
