@@ -14,10 +14,11 @@
 // written once (gradient). A lane holds 16 bytes of a row, so a row takes 8
 // to 32 lanes and the row sums are a few shuffles; the rotation's partner
 // channels are in a lane rot_dim/2 away (shuffle) or, interleaved, in the same
-// lane. A warp takes a unit of up to kRows rows per lane group from one token,
-// with all their loads in flight at once, and keeps the token's cos and sin in
-// registers from unit to unit. All arithmetic is fp32; each output is rounded
-// once.
+// lane. A block's 8 warps take 8 consecutive tokens (fewer tokens: the heads of
+// one), a warp kRows rows per lane group with all their loads in flight at once;
+// a token's cos and sin stay in registers from one such item to the next. Queries
+// and keys are two passes over the tokens, so that one set of weights is held
+// at a time. All arithmetic is fp32; each output is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -35,9 +36,23 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRows = 4;           // rows in flight per lane group
-constexpr int kRopeBwdBlocks = 608;  // most blocks of the gradient (4 per SM of 152): the
-                                     // workspace holds one partial weight gradient each
+#ifndef ROWSF
+#define ROWSF 4
+#define ROWSB 2
+#endif
+#ifndef MINF
+#define MINF 4
+#endif
+#ifndef MINB
+#define MINB 3
+#endif
+constexpr int kMinFwd = MINF, kMinBwd = MINB;  // blocks per SM
+// row steps (a row of each lane group) per item: one item is computed while the
+// next one's rows arrive in shared memory
+template <bool kBwd>
+constexpr int rope_rows() { return kBwd ? ROWSB : ROWSF; }
+constexpr int kRopeMaxBlocks = 912;  // most blocks: the gradient's workspace holds one partial
+                                     // weight gradient of each
 
 struct View {
   char* p;
@@ -53,9 +68,11 @@ struct RopeArgs {
   float* part;             // gradient: [blocks][2][D]
   float eps;
   int S, H[2], rot, max_pos;
-  int blocks_q, blocks_all;  // head blocks of q, and of q and k together, per token
-  int per_block;             // heads per block
-  long long units;           // tokens * blocks_all
+  int together;         // warps of a block with tokens of their own: 8 or 1
+  int per_item;         // heads per item
+  int items[2];         // items per token
+  long long groups;     // ceil(tokens / together)
+  int B;
 };
 
 template <bool kBf16>
@@ -63,95 +80,94 @@ struct Chunk {  // 16 bytes of a row
   static constexpr int N = kBf16 ? 8 : 4;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ void unpack(const uint4& v, float* f) {
+// Channel pairs, for the packed fp32 instructions (two lanes each).
+template <bool kBf16, int P>
+__device__ __forceinline__ void unpack(const uint4& v, float2 (&f)[P]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kBf16) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    } else {
-      f[i] = __uint_as_float(u[i]);
-    }
+  for (int i = 0; i < P; ++i) {
+    if constexpr (kBf16)
+      f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    else
+      f[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
   }
 }
 
-template <bool kBf16>
-__device__ __forceinline__ uint4 pack(const float* f) {
+template <bool kBf16, int P>
+__device__ __forceinline__ uint4 pack(const float2 (&f)[P]) {
   uint32_t u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kBf16) u[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    else u[i] = __float_as_uint(f[i]);
+  for (int i = 0; i < P; ++i) {
+    if constexpr (kBf16) {
+      u[i] = pack_bf16x2(f[i].x, f[i].y);
+    } else {
+      u[2 * i] = __float_as_uint(f[i].x);
+      u[2 * i + 1] = __float_as_uint(f[i].y);
+    }
   }
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // A token's rotation as the lane's channels see it: z = c y + e y', y' the
 // partner channel (e = -sin for the first of a pair, +sin for the second).
-// The transpose is the same with e negated. Interleaved: c and e of pair i.
+// The transpose is the same with e negated.
 template <int N, bool kInter>
 struct Rotation {
-  static constexpr int M = kInter ? N / 2 : N;
-  float c[M], e[M];
-  int mate;  // partner lane
+  float2 c[N / 2], e[N / 2];
+  int mate;  // partner lane; interleaved: unused, the partner is channel i ^ 1
 
   __device__ __forceinline__ void load(const RopeArgs& a, int pos, int chunk, int lane) {
     const int ch = chunk * N, half = a.rot / 2;
     mate = lane;
     if (!a.table || ch >= a.rot) {
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        c[i] = 1.0f;
-        e[i] = 0.0f;
+      for (int i = 0; i < N / 2; ++i) {
+        c[i] = both(1.0f);
+        e[i] = both(0.0f);
       }
       return;
     }
     const float* row = a.table + (size_t)pos * a.rot;
     if constexpr (kInter) {
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        c[i] = row[ch / 2 + i];
-        e[i] = row[half + ch / 2 + i];
+      for (int i = 0; i < N / 2; ++i) {
+        const float cs = row[ch / 2 + i], sn = row[half + ch / 2 + i];
+        c[i] = both(cs);
+        e[i] = make_float2(-sn, sn);
       }
     } else {
       const bool second = ch >= half;
       const int at = second ? ch - half : ch;
       mate = second ? lane - half / N : lane + half / N;
+      const float2 sign = both(second ? 1.0f : -1.0f);
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         const float4 cv = *reinterpret_cast<const float4*>(row + at + i);
         const float4 sv = *reinterpret_cast<const float4*>(row + half + at + i);
-        const float cs[4] = {cv.x, cv.y, cv.z, cv.w}, sn[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[i + j] = cs[j];
-          e[i + j] = second ? sn[j] : -sn[j];
-        }
+        c[i / 2] = make_float2(cv.x, cv.y);
+        c[i / 2 + 1] = make_float2(cv.z, cv.w);
+        e[i / 2] = fmul2(sign, make_float2(sv.x, sv.y));
+        e[i / 2 + 1] = fmul2(sign, make_float2(sv.z, sv.w));
       }
     }
   }
 
-  // sign 1: rotate, -1: the transpose
-  __device__ __forceinline__ void apply(float* y, float sign) const {
-    if constexpr (kInter) {
+  // The partner channels' values.
+  __device__ __forceinline__ void partner(const float2 (&x)[N / 2], float2 (&y)[N / 2]) const {
 #pragma unroll
-      for (int i = 0; i < M; ++i) {
-        const float s = sign * e[i], a = y[2 * i], b = y[2 * i + 1];
-        y[2 * i] = a * c[i] - b * s;
-        y[2 * i + 1] = b * c[i] + a * s;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float o = __shfl_sync(0xffffffffu, y[i], mate);
-        y[i] = y[i] * c[i] + (sign * e[i]) * o;
-      }
+    for (int i = 0; i < N / 2; ++i) {
+      if constexpr (kInter)
+        y[i] = make_float2(x[i].y, x[i].x);
+      else
+        y[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, mate),
+                           __shfl_sync(0xffffffffu, x[i].y, mate));
     }
   }
 };
 
+// Sum over the LANES lanes of a row.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
@@ -159,137 +175,187 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// 16-byte asynchronous copy into the thread's own place of shared memory.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src))
+               : "memory");
+}
+
 template <int D, bool kBf16, bool kInter, bool kBwd>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const RopeArgs a) {
-  constexpr int N = Chunk<kBf16>::N;
+__global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
+    norm_rope_kernel(const RopeArgs a) {
+  constexpr int N = Chunk<kBf16>::N, P = N / 2;
   constexpr int LANES = D / N;        // lanes per row
   constexpr int SUBS = 32 / LANES;    // rows side by side in a warp
+  constexpr int kRows = rope_rows<kBwd>();
+  constexpr int kSlots = kBwd ? 2 : 1;  // x, and the gradient's dz
+  __shared__ uint4 ring[2][kRows][kSlots][kRopeThreads];  // a thread's own chunks
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = lane % LANES, sub = lane / LANES;
+  const int apart = warp / a.together;       // head item within the group
+  const int spread = kRopeWarps / a.together;
 
-  float w[2][N], dw[2][N];
+  for (int t = 0; t < 2; ++t) {
+    if (a.H[t] == 0) continue;
+    const bool norm = a.w[t] != nullptr;
+    float2 w[P], dw[P];  // the gradient's weights and sums
+    if constexpr (kBwd) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w[t][i] = a.w[t] ? a.w[t][chunk * N + i] : 1.0f;
-      dw[t][i] = 0.0f;
+      for (int i = 0; i < P; ++i) {
+        w[i] = norm ? make_float2(a.w[t][chunk * N + 2 * i], a.w[t][chunk * N + 2 * i + 1]) : both(1.0f);
+        dw[i] = both(0.0f);
+      }
     }
-
-  // a warp's run of consecutive units: the same token again and again
-  const long long nw = (long long)gridDim.x * kRopeWarps;
-  const long long wid = (long long)blockIdx.x * kRopeWarps + warp;
-  long long u = a.units * wid / nw;
-  const long long u_end = a.units * (wid + 1) / nw;
-  long long token = u / a.blocks_all;
-  int blk = (int)(u - token * a.blocks_all);
-  int b = (int)(token / a.S), s = (int)(token - (long long)b * a.S);
-  Rotation<N, kInter> rot;
-  bool live = false, fresh = true;
-
-  for (; u < u_end; ++u) {
-    if (fresh) {
-      const int pos = !a.table ? 0 : a.pos ? a.pos[(size_t)b * a.S + s] : s;
-      live = !a.table || (pos >= 0 && pos < a.max_pos);
-      if (live) rot.load(a, pos, chunk, lane);
-      fresh = false;
-    }
-    if (live) {
-      auto rows = [&](const int t, float (&wt)[N], float (&dwt)[N], int h_begin) {
-        const View& xv = a.x[t];
-        const View& zv = a.z[t];
-        const bool norm = a.w[t] != nullptr;
-        const int h_end = min(a.H[t], h_begin + a.per_block);
-        const char* xp = xv.p + b * xv.sb + s * xv.ss + chunk * 16;
-        char* zp = zv.p + b * zv.sb + s * zv.ss + chunk * 16;
-        char* dp = kBwd ? a.dx[t].p + b * a.dx[t].sb + s * a.dx[t].ss + chunk * 16 : nullptr;
-        for (int h0 = h_begin; h0 < h_end; h0 += SUBS * kRows) {
-          uint4 xr[kRows], gr[kRows];
+    // the block's run of items, the head items of a token group one after the other
+    const int per_group = (a.items[t] + spread - 1) / spread;
+    const long long n = a.groups * per_group;
+    const long long u0 = n * blockIdx.x / gridDim.x;
+    const int count = (int)(n * (blockIdx.x + 1) / gridDim.x - u0);
+    // the next item's token (b, s) and head item
+    const long long token0 = u0 / per_group * a.together + warp % a.together;
+    int b = (int)(token0 / a.S), s = (int)(token0 - (long long)b * a.S);
+    int it = (int)(u0 % per_group);
+    int pos_next = -1;
+    const View &xv = a.x[t], &zv = a.z[t], &ov = kBwd ? a.dx[t] : a.z[t];
+    const char *x_at = nullptr, *z_at = nullptr;  // its first row of this lane, head 0
+    char *o_at = nullptr, *o_next = nullptr;
+    auto enter_token = [&]() {
+      if (b >= a.B) return;
+      const long long c = chunk * 16;
+      x_at = xv.p + b * xv.sb + s * xv.ss + sub * xv.sh + c;
+      if constexpr (kBwd) z_at = zv.p + b * zv.sb + s * zv.ss + sub * zv.sh + c;
+      o_next = ov.p + b * ov.sb + s * ov.ss + sub * ov.sh + c;
+      pos_next = !a.table ? 0 : a.pos ? a.pos[(size_t)b * a.S + s] : s;
+    };
+    auto head_of = [&](int item) { return (item * spread + apart) * a.per_item; };
+    // heads of an item (the same for the whole warp), and row steps of SUBS of them
+    auto heads_of = [&](int item) { return min(a.H[t] - head_of(item), a.per_item); };
+    const long long x_step = SUBS * xv.sh, z_step = SUBS * zv.sh, o_step = SUBS * ov.sh;
+    auto fetch = [&](int buf) {
+      if (b < a.B) {
+        const int heads = heads_of(it) - sub;
+        const char* x = x_at + head_of(it) * xv.sh;
+        const char* z = kBwd ? z_at + head_of(it) * zv.sh : nullptr;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const int h = h0 + r * SUBS + sub;
-            xr[r] = gr[r] = make_uint4(0, 0, 0, 0);
-            if (h < h_end) {
-              const long long at = h * xv.sh;
-              if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, xp + at - xv.p, xv.bytes))
-                xr[r] = *reinterpret_cast<const uint4*>(xp + at);
-              if (kBwd && MATTN_IN_BOUNDS(kSiteRope, zp + h * zv.sh - zv.p, zv.bytes))
-                gr[r] = *reinterpret_cast<const uint4*>(zp + h * zv.sh);
-            }
+        for (int r = 0; r < kRows; ++r) {
+          if (r * SUBS < heads) {
+            if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, x - xv.p, xv.bytes))
+              cp_async16(&ring[buf][r][0][threadIdx.x], x);
+            if (kBwd && MATTN_IN_BOUNDS(kSiteRope, z - zv.p, zv.bytes))
+              cp_async16(&ring[buf][r][1][threadIdx.x], z);
           }
+          x += x_step;
+          if constexpr (kBwd) z += z_step;
+        }
+      }
+      cp_async_commit();
+    };
+
+    Rotation<N, kInter> rot;
+    bool live = false;
+    enter_token();
+    if (count > 0) fetch(0);
+    for (int i = 0; i < count; ++i) {
+      const int item = it, pos = pos_next;
+      const bool there = b < a.B;
+      o_at = o_next;
+      if (++it == per_group) {
+        it = 0;
+        for (s += a.together; s >= a.S; s -= a.S) ++b;
+        enter_token();
+      }
+      if (i + 1 < count) fetch((i + 1) & 1);
+      if (item == 0 || i == 0) {  // another token
+        live = there && (!a.table || (pos >= 0 && pos < a.max_pos));
+        if (live) {
+          rot.load(a, pos, chunk, lane);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (h0 + r * SUBS >= h_end) break;  // the whole warp is past the last head
-            const int h = h0 + r * SUBS + sub;
-            float x[N], y[N];
-            unpack<kBf16>(xr[r], x);
-            float ri = 1.0f;
-            if (norm) {
-              float ss = 0.0f;
-#pragma unroll
-              for (int i = 0; i < N; ++i) ss += x[i] * x[i];
-              ri = rsqrtf(row_sum<LANES>(ss) * (1.0f / D) + a.eps);
-              if (h >= h_end) ri = 0.0f;  // no row: adds nothing, eps = 0 included
-            }
-            if constexpr (!kBwd) {
-#pragma unroll
-              for (int i = 0; i < N; ++i) y[i] = x[i] * ri * wt[i];
-              rot.apply(y, 1.0f);
-              if (h < h_end && MATTN_IN_BOUNDS(kSiteRope, zp + h * zv.sh - zv.p, zv.bytes))
-                *reinterpret_cast<uint4*>(zp + h * zv.sh) = pack<kBf16>(y);
-            } else {
-              unpack<kBf16>(gr[r], y);
-              rot.apply(y, -1.0f);  // dy
-              if (norm) {
-                float dot = 0.0f;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                  x[i] *= ri;                    // n
-                  dwt[i] += y[i] * x[i];
-                  y[i] *= wt[i];                 // dn
-                  dot += y[i] * x[i];
-                }
-                dot = row_sum<LANES>(dot) * (1.0f / D);
-#pragma unroll
-                for (int i = 0; i < N; ++i) y[i] = ri * (y[i] - x[i] * dot);
+          for (int j = 0; j < P; ++j) {
+            if constexpr (kBwd) {  // the transpose
+              rot.e[j] = fmul2(rot.e[j], both(-1.0f));
+            } else if (norm) {  // z = r (x (w c) + x' (w' e))
+              const float* own = a.w[t] + chunk * N + 2 * j;
+              const float2 wo = make_float2(own[0], own[1]);
+              rot.c[j] = fmul2(rot.c[j], wo);
+              if constexpr (kInter) {
+                rot.e[j] = fmul2(rot.e[j], make_float2(wo.y, wo.x));
+              } else {
+                const float* other = a.w[t] + (rot.mate % LANES) * N + 2 * j;
+                rot.e[j] = fmul2(rot.e[j], make_float2(other[0], other[1]));
               }
-              if (h < h_end &&
-                  MATTN_IN_BOUNDS(kSiteRope, dp + h * a.dx[t].sh - a.dx[t].p, a.dx[t].bytes))
-                *reinterpret_cast<uint4*>(dp + h * a.dx[t].sh) = pack<kBf16>(y);
             }
           }
         }
-      };
-      if (blk < a.blocks_q) rows(0, w[0], dw[0], blk * a.per_block);
-      else rows(1, w[1], dw[1], (blk - a.blocks_q) * a.per_block);
-    }
-    if (++blk == a.blocks_all) {
-      blk = 0;
-      fresh = true;
-      if (++s == a.S) {
-        s = 0;
-        ++b;
+      }
+      if (i + 1 < count) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      const int heads = live ? heads_of(item) : 0;
+      char* out = o_at + head_of(item) * ov.sh;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r, out += o_step) {
+        if (r * SUBS >= heads) break;
+        const bool here = r * SUBS + sub < heads;
+        float2 x[P], y[P];
+        float ri = 1.0f;
+        if (!kBwd || norm) {
+          unpack<kBf16>(ring[i & 1][r][0][threadIdx.x], x);
+          if (norm) {
+            float2 q = fmul2(x[0], x[0]);
+#pragma unroll
+            for (int j = 1; j < P; ++j) q = ffma2(x[j], x[j], q);
+            ri = rsqrtf(row_sum<LANES>(q.x + q.y) * (1.0f / D) + a.eps);
+          }
+        }
+        if constexpr (!kBwd) {
+          rot.partner(x, y);
+#pragma unroll
+          for (int j = 0; j < P; ++j)
+            y[j] = fmul2(both(ri), ffma2(x[j], rot.c[j], fmul2(y[j], rot.e[j])));
+        } else {
+          float2 g[P];
+          unpack<kBf16>(ring[i & 1][r][1][threadIdx.x], g);
+          rot.partner(g, y);
+#pragma unroll
+          for (int j = 0; j < P; ++j) y[j] = ffma2(g[j], rot.c[j], fmul2(y[j], rot.e[j]));  // dy
+          if (norm) {
+            float2 q = both(0.0f);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              x[j] = fmul2(x[j], both(ri));       // n
+              const float2 yn = fmul2(y[j], x[j]);
+              if (here) dw[j] = fadd2(dw[j], yn);
+              q = ffma2(yn, w[j], q);
+            }
+            const float2 k = both(row_sum<LANES>(q.x + q.y) * (-1.0f / D));
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+              y[j] = fmul2(both(ri), ffma2(x[j], k, fmul2(y[j], w[j])));
+          }
+        }
+        if (here && MATTN_IN_BOUNDS(kSiteRope, out - ov.p, ov.bytes))
+          *reinterpret_cast<uint4*>(out) = pack<kBf16>(y);
       }
     }
-  }
 
-  if constexpr (kBwd) {  // the block's weight gradients, always in the same order
-    __shared__ float sh[kRopeWarps][2][D];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
+    if constexpr (kBwd) {  // the block's weight gradient, always in the same order
+      float* sh = reinterpret_cast<float*>(ring);  // [warps][D]
+      __syncthreads();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float v = dw[t][i];
+        float v = i & 1 ? dw[i / 2].y : dw[i / 2].x;
 #pragma unroll
         for (int d = LANES; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (sub == 0) sh[warp][t][chunk * N + i] = v;
+        if (sub == 0) sh[warp * D + chunk * N + i] = v;
       }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * D; c += kRopeThreads) {
-      float v = 0.0f;
+      __syncthreads();
+      for (int c = threadIdx.x; c < D; c += kRopeThreads) {
+        float v = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kRopeWarps; ++k) v += sh[k][c / D][c % D];
-      a.part[(size_t)blockIdx.x * 2 * D + c] = v;
+        for (int k = 0; k < kRopeWarps; ++k) v += sh[k * D + c];
+        a.part[(size_t)blockIdx.x * 2 * D + t * D + c] = v;
+      }
+      __syncthreads();
     }
   }
 }
@@ -315,23 +381,23 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n,
 template <int D, bool kBf16, bool kBwd>
 cudaError_t launch_typed(RopeArgs& a, bool inter, int B, float* const* dw, cudaStream_t stream) {
   constexpr int kSubs = 32 / (D / Chunk<kBf16>::N);
+  a.B = B;
   const long long tokens = (long long)B * a.S;
-  const int blocks_max = kBwd ? std::min(kRopeBwdBlocks, 4 * sm_count()) : 4 * sm_count();
-  // Heads per unit: as many as a warp has in flight, but fewer where the
-  // tokens alone do not give every warp of the grid one unit (a decode step's
-  // few tokens: one row per lane group and unit, so the rows spread over the SMs).
-  a.per_block = kSubs * kRows;
-  auto count = [&](int per) {
-    a.per_block = per;
-    a.blocks_q = (a.H[0] + per - 1) / per;
-    a.blocks_all = a.blocks_q + (a.H[1] + per - 1) / per;
-    a.units = tokens * a.blocks_all;
-  };
-  for (int per = kSubs * kRows; per >= kSubs; per >>= 1) {
-    count(per);
-    if (a.units >= (long long)blocks_max * kRopeWarps) break;
+  const int resident = (kBwd ? kMinBwd : kMinFwd) * sm_count();
+  // 8 tokens per block where they give every resident block some; a decode
+  // step's few tokens: one per block, and one row per lane group and item, so that
+  // the heads spread over the warps.
+  const bool many = tokens >= (long long)kRopeWarps * resident;
+  a.together = many ? kRopeWarps : 1;
+  a.per_item = many ? kSubs * rope_rows<kBwd>() : kSubs;
+  a.groups = (tokens + a.together - 1) / a.together;
+  long long items = 0;
+  for (int t = 0; t < 2; ++t) {
+    a.items[t] = (a.H[t] + a.per_item - 1) / a.per_item;
+    items += a.items[t];
   }
-  const int blocks = (int)std::min<long long>(blocks_max, (a.units + kRopeWarps - 1) / kRopeWarps);
+  const long long all = many ? a.groups * items : a.groups * ((items + kRopeWarps - 1) / kRopeWarps);
+  const int blocks = (int)std::min<long long>(std::min(resident, kRopeMaxBlocks), all);
   if (inter) norm_rope_kernel<D, kBf16, true, kBwd><<<blocks, kRopeThreads, 0, stream>>>(a);
   else norm_rope_kernel<D, kBf16, false, kBwd><<<blocks, kRopeThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
@@ -417,7 +483,7 @@ MATTN_API attn_status attn_qk_norm_rope(const attn_view* q, const attn_view* k,
 }
 
 MATTN_API size_t attn_qk_norm_rope_bwd_workspace_bytes(int D) {
-  return D == 64 || D == 128 ? sizeof(float) * 2 * D * mattn::kRopeBwdBlocks : 0;
+  return D == 64 || D == 128 ? sizeof(float) * 2 * D * mattn::kRopeMaxBlocks : 0;
 }
 
 MATTN_API attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view* k,
