@@ -170,6 +170,15 @@ __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// Programmatic dependent launch: lets the next kernel of the stream be set up
+// early; that kernel's wait returns when this one has ended and its writes show.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor) and fences.
 // ---------------------------------------------------------------------------

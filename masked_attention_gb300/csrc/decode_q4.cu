@@ -156,15 +156,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 
-// Programmatic dependent launch: lets the next kernel of the stream be set up
-// early; that kernel's wait returns when this one has ended and its writes show.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_primary() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {

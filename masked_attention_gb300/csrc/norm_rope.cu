@@ -11,20 +11,26 @@
 //   dx = r (dn - n mean(dn n))
 //
 // Bound by HBM: a row is read and written once (forward), or read twice and
-// written once (gradient). A lane holds 16 bytes of a row, so a row takes 8
-// to 32 lanes and the row sums are a few shuffles; the rotation's partner
-// channels are in a lane rot_dim/2 away (shuffle) or, interleaved, in the same
-// lane. A block's 8 warps take 8 consecutive tokens (fewer tokens: the heads of
-// one), a warp kRows rows per lane group with all their loads in flight at once;
-// a token's cos and sin stay in registers from one such item to the next. Queries
-// and keys are two passes over the tokens, so that one set of weights is held
-// at a time. All arithmetic is fp32; each output is rounded once.
+// written once (gradient); what competes are the instructions per row. A lane
+// holds 32 bytes of a row, two 16-byte chunks that are each other's rotation
+// partners (or, past rot_dim and interleaved, any two), so a rotation needs no
+// exchange between lanes, a row takes 4 to 16 lanes, and its sums two to four
+// shuffles; the arithmetic is on packed fp32 pairs. (With one chunk per lane and the
+// partner's by shuffle: 128 instead of 95 instructions per two rows of
+// 128 bf16 channels, and 245 instead of 185 in the gradient.) A block's 8 warps take
+// 8 consecutive tokens (fewer tokens: the heads of one). An item is kRows rows per lane
+// group; the next item's rows arrive in shared memory (asynchronous copies, each
+// thread its own) while one is computed, and a token's cos and sin stay in
+// registers from one item to the next. Queries and keys are two passes over the
+// tokens, so that one set of weights is held at a time. All arithmetic is fp32;
+// each output is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "host_util.h"
 #include "launch.h"
@@ -36,22 +42,14 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-#ifndef ROWSF
-#define ROWSF 4
-#define ROWSB 2
-#endif
-#ifndef MINF
-#define MINF 4
-#endif
-#ifndef MINB
-#define MINB 3
-#endif
-constexpr int kMinFwd = MINF, kMinBwd = MINB;  // blocks per SM
-// row steps (a row of each lane group) per item: one item is computed while the
-// next one's rows arrive in shared memory
+constexpr int kRopePerSm = 2;  // blocks per SM: 3, with 80 registers, spilled (69 against 63 us
+                               // on 16384 tokens x 40 heads of 128 bf16 channels)
+// Row steps (a row of each lane group) per item. The gradient needs more rows in
+// flight at its 128 registers: 3 against 1 is 149 against 158 us on the training
+// shape (B 8, 16 + 16 heads, S 4096, D 128); the forward 64 against 63.
 template <bool kBwd>
-constexpr int rope_rows() { return kBwd ? ROWSB : ROWSF; }
-constexpr int kRopeMaxBlocks = 912;  // most blocks: the gradient's workspace holds one partial
+constexpr int rope_rows() { return kBwd ? 3 : 2; }
+constexpr int kRopeMaxBlocks = 608;  // most blocks: the gradient's workspace holds one partial
                                      // weight gradient of each
 
 struct View {
@@ -110,60 +108,60 @@ __device__ __forceinline__ uint4 pack(const float2 (&f)[P]) {
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// A token's rotation as the lane's channels see it: z = c y + e y', y' the
-// partner channel (e = -sin for the first of a pair, +sin for the second).
-// The transpose is the same with e negated.
+// The two chunks of a row that a lane holds: partners of the rotation where
+// they lie below rot_dim.
+template <int N>
+__device__ __forceinline__ void lane_chunks(const RopeArgs& a, bool inter, int part, int (&ch)[2]) {
+  const int pairs = a.table && !inter ? a.rot / (2 * N) : 0;  // lanes with partners
+  ch[0] = part < pairs ? part * N : (2 * part) * N;
+  ch[1] = part < pairs ? part * N + a.rot / 2 : (2 * part + 1) * N;
+}
+
+// A token's rotation as the lane's channels see it:
+//   z0 = c0 y0 + e0 y0',  z1 = c1 y1 + e1 y1'
+// with y' the other chunk or, interleaved, the neighbouring channel. The transpose
+// is the same with e negated.
 template <int N, bool kInter>
 struct Rotation {
-  float2 c[N / 2], e[N / 2];
-  int mate;  // partner lane; interleaved: unused, the partner is channel i ^ 1
+  float2 c[2][N / 2], e[2][N / 2];
 
-  __device__ __forceinline__ void load(const RopeArgs& a, int pos, int chunk, int lane) {
-    const int ch = chunk * N, half = a.rot / 2;
-    mate = lane;
-    if (!a.table || ch >= a.rot) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        c[i] = both(1.0f);
-        e[i] = both(0.0f);
-      }
-      return;
-    }
+  __device__ __forceinline__ void load(const RopeArgs& a, int pos, const int (&ch)[2]) {
     const float* row = a.table + (size_t)pos * a.rot;
-    if constexpr (kInter) {
+    const int half = a.rot / 2;
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const float cs = row[ch / 2 + i], sn = row[half + ch / 2 + i];
-        c[i] = both(cs);
-        e[i] = make_float2(-sn, sn);
-      }
-    } else {
-      const bool second = ch >= half;
-      const int at = second ? ch - half : ch;
-      mate = second ? lane - half / N : lane + half / N;
-      const float2 sign = both(second ? 1.0f : -1.0f);
+    for (int k = 0; k < 2; ++k) {
+      if (!a.table || ch[k] >= a.rot) {
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        const float4 cv = *reinterpret_cast<const float4*>(row + at + i);
-        const float4 sv = *reinterpret_cast<const float4*>(row + half + at + i);
-        c[i / 2] = make_float2(cv.x, cv.y);
-        c[i / 2 + 1] = make_float2(cv.z, cv.w);
-        e[i / 2] = fmul2(sign, make_float2(sv.x, sv.y));
-        e[i / 2 + 1] = fmul2(sign, make_float2(sv.z, sv.w));
+        for (int i = 0; i < N / 2; ++i) {
+          c[k][i] = both(1.0f);
+          e[k][i] = both(0.0f);
+        }
+      } else if constexpr (kInter) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          const float cs = row[ch[k] / 2 + i], sn = row[half + ch[k] / 2 + i];
+          c[k][i] = both(cs);
+          e[k][i] = make_float2(-sn, sn);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 cv = *reinterpret_cast<const float4*>(row + ch[0] + i);
+          const float4 sv = *reinterpret_cast<const float4*>(row + half + ch[0] + i);
+          c[k][i / 2] = make_float2(cv.x, cv.y);
+          c[k][i / 2 + 1] = make_float2(cv.z, cv.w);
+          const float2 sign = both(k ? 1.0f : -1.0f);
+          e[k][i / 2] = fmul2(sign, make_float2(sv.x, sv.y));
+          e[k][i / 2 + 1] = fmul2(sign, make_float2(sv.z, sv.w));
+        }
       }
     }
   }
 
-  // The partner channels' values.
-  __device__ __forceinline__ void partner(const float2 (&x)[N / 2], float2 (&y)[N / 2]) const {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      if constexpr (kInter)
-        y[i] = make_float2(x[i].y, x[i].x);
-      else
-        y[i] = make_float2(__shfl_sync(0xffffffffu, x[i].x, mate),
-                           __shfl_sync(0xffffffffu, x[i].y, mate));
-    }
+  // c y + e y'
+  __device__ __forceinline__ float2 turn(const float2 (&y)[2][N / 2], int k, int i) const {
+    const float2 other = kInter ? make_float2(y[k][i].y, y[k][i].x) : y[1 - k][i];
+    return ffma2(y[k][i], c[k][i], fmul2(other, e[k][i]));
   }
 };
 
@@ -183,29 +181,41 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 }
 
 template <int D, bool kBf16, bool kInter, bool kBwd>
-__global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
+__global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
     norm_rope_kernel(const RopeArgs a) {
   constexpr int N = Chunk<kBf16>::N, P = N / 2;
-  constexpr int LANES = D / N;        // lanes per row
+  constexpr int LANES = D / (2 * N);  // lanes per row
   constexpr int SUBS = 32 / LANES;    // rows side by side in a warp
   constexpr int kRows = rope_rows<kBwd>();
-  constexpr int kSlots = kBwd ? 2 : 1;  // x, and the gradient's dz
-  __shared__ uint4 ring[2][kRows][kSlots][kRopeThreads];  // a thread's own chunks
+  constexpr int kSlots = kBwd ? 4 : 2;  // two chunks of x, and of the gradient's dz
+  extern __shared__ uint4 ring[];       // [2][kRows][kSlots][threads]: a thread's own chunks
+  auto place = [&](int buf, int r, int slot) -> uint4& {
+    return ring[((buf * kRows + r) * kSlots + slot) * kRopeThreads + threadIdx.x];
+  };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int chunk = lane % LANES, sub = lane / LANES;
+  const int sub = lane / LANES;
+  if constexpr (kBwd) launch_dependents();  // the sum over blocks waits for this grid's end
   const int apart = warp / a.together;       // head item within the group
   const int spread = kRopeWarps / a.together;
+  int ch[2];
+  lane_chunks<N>(a, kInter, lane % LANES, ch);
+  const int c0 = ch[0] * (16 / N), c1 = ch[1] * (16 / N);  // bytes
 
   for (int t = 0; t < 2; ++t) {
     if (a.H[t] == 0) continue;
     const bool norm = a.w[t] != nullptr;
-    float2 w[P], dw[P];  // the gradient's weights and sums
+    auto weight = [&](int k, int i) {
+      return norm ? make_float2(a.w[t][ch[k] + 2 * i], a.w[t][ch[k] + 2 * i + 1]) : both(1.0f);
+    };
+    float2 w[2][P], dw[2][P];  // the gradient's weights and sums
     if constexpr (kBwd) {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        w[i] = norm ? make_float2(a.w[t][chunk * N + 2 * i], a.w[t][chunk * N + 2 * i + 1]) : both(1.0f);
-        dw[i] = both(0.0f);
-      }
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          w[k][i] = weight(k, i);
+          dw[k][i] = both(0.0f);
+        }
     }
     // the block's run of items, the head items of a token group one after the other
     const int per_group = (a.items[t] + spread - 1) / spread;
@@ -222,14 +232,13 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
     char *o_at = nullptr, *o_next = nullptr;
     auto enter_token = [&]() {
       if (b >= a.B) return;
-      const long long c = chunk * 16;
-      x_at = xv.p + b * xv.sb + s * xv.ss + sub * xv.sh + c;
-      if constexpr (kBwd) z_at = zv.p + b * zv.sb + s * zv.ss + sub * zv.sh + c;
-      o_next = ov.p + b * ov.sb + s * ov.ss + sub * ov.sh + c;
+      x_at = xv.p + b * xv.sb + s * xv.ss + sub * xv.sh;
+      if constexpr (kBwd) z_at = zv.p + b * zv.sb + s * zv.ss + sub * zv.sh;
+      o_next = ov.p + b * ov.sb + s * ov.ss + sub * ov.sh;
       pos_next = !a.table ? 0 : a.pos ? a.pos[(size_t)b * a.S + s] : s;
     };
     auto head_of = [&](int item) { return (item * spread + apart) * a.per_item; };
-    // heads of an item (the same for the whole warp), and row steps of SUBS of them
+    // heads of an item (the same for the whole warp)
     auto heads_of = [&](int item) { return min(a.H[t] - head_of(item), a.per_item); };
     const long long x_step = SUBS * xv.sh, z_step = SUBS * zv.sh, o_step = SUBS * ov.sh;
     auto fetch = [&](int buf) {
@@ -240,10 +249,14 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           if (r * SUBS < heads) {
-            if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, x - xv.p, xv.bytes))
-              cp_async16(&ring[buf][r][0][threadIdx.x], x);
-            if (kBwd && MATTN_IN_BOUNDS(kSiteRope, z - zv.p, zv.bytes))
-              cp_async16(&ring[buf][r][1][threadIdx.x], z);
+            if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, x - xv.p, xv.bytes)) {
+              cp_async16(&place(buf, r, 0), x + c0);
+              cp_async16(&place(buf, r, 1), x + c1);
+            }
+            if (kBwd && MATTN_IN_BOUNDS(kSiteRope, z - zv.p, zv.bytes)) {
+              cp_async16(&place(buf, r, 2), z + c0);
+              cp_async16(&place(buf, r, 3), z + c1);
+            }
           }
           x += x_step;
           if constexpr (kBwd) z += z_step;
@@ -269,23 +282,19 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
       if (item == 0 || i == 0) {  // another token
         live = there && (!a.table || (pos >= 0 && pos < a.max_pos));
         if (live) {
-          rot.load(a, pos, chunk, lane);
+          rot.load(a, pos, ch);
 #pragma unroll
-          for (int j = 0; j < P; ++j) {
-            if constexpr (kBwd) {  // the transpose
-              rot.e[j] = fmul2(rot.e[j], both(-1.0f));
-            } else if (norm) {  // z = r (x (w c) + x' (w' e))
-              const float* own = a.w[t] + chunk * N + 2 * j;
-              const float2 wo = make_float2(own[0], own[1]);
-              rot.c[j] = fmul2(rot.c[j], wo);
-              if constexpr (kInter) {
-                rot.e[j] = fmul2(rot.e[j], make_float2(wo.y, wo.x));
-              } else {
-                const float* other = a.w[t] + (rot.mate % LANES) * N + 2 * j;
-                rot.e[j] = fmul2(rot.e[j], make_float2(other[0], other[1]));
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              if constexpr (kBwd) {  // the transpose
+                rot.e[k][j] = fmul2(rot.e[k][j], both(-1.0f));
+              } else if (norm) {  // z = r (x (w c) + x' (w' e))
+                const float2 own = weight(k, j);
+                rot.c[k][j] = fmul2(rot.c[k][j], own);
+                rot.e[k][j] = fmul2(rot.e[k][j], kInter ? make_float2(own.y, own.x) : weight(1 - k, j));
               }
             }
-          }
         }
       }
       if (i + 1 < count) cp_async_wait<1>();
@@ -296,45 +305,58 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
       for (int r = 0; r < kRows; ++r, out += o_step) {
         if (r * SUBS >= heads) break;
         const bool here = r * SUBS + sub < heads;
-        float2 x[P], y[P];
+        float2 x[2][P], y[2][P];
         float ri = 1.0f;
         if (!kBwd || norm) {
-          unpack<kBf16>(ring[i & 1][r][0][threadIdx.x], x);
+          unpack<kBf16>(place(i & 1, r, 0), x[0]);
+          unpack<kBf16>(place(i & 1, r, 1), x[1]);
           if (norm) {
-            float2 q = fmul2(x[0], x[0]);
+            float2 q = fmul2(x[0][0], x[0][0]), q1 = fmul2(x[1][0], x[1][0]);
 #pragma unroll
-            for (int j = 1; j < P; ++j) q = ffma2(x[j], x[j], q);
+            for (int j = 1; j < P; ++j) {
+              q = ffma2(x[0][j], x[0][j], q);
+              q1 = ffma2(x[1][j], x[1][j], q1);
+            }
+            q = fadd2(q, q1);
             ri = rsqrtf(row_sum<LANES>(q.x + q.y) * (1.0f / D) + a.eps);
           }
         }
         if constexpr (!kBwd) {
-          rot.partner(x, y);
 #pragma unroll
-          for (int j = 0; j < P; ++j)
-            y[j] = fmul2(both(ri), ffma2(x[j], rot.c[j], fmul2(y[j], rot.e[j])));
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < P; ++j) y[k][j] = fmul2(both(ri), rot.turn(x, k, j));
         } else {
-          float2 g[P];
-          unpack<kBf16>(ring[i & 1][r][1][threadIdx.x], g);
-          rot.partner(g, y);
+          float2 g[2][P];
+          unpack<kBf16>(place(i & 1, r, 2), g[0]);
+          unpack<kBf16>(place(i & 1, r, 3), g[1]);
 #pragma unroll
-          for (int j = 0; j < P; ++j) y[j] = ffma2(g[j], rot.c[j], fmul2(y[j], rot.e[j]));  // dy
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < P; ++j) y[k][j] = rot.turn(g, k, j);  // dy
           if (norm) {
             float2 q = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-              x[j] = fmul2(x[j], both(ri));       // n
-              const float2 yn = fmul2(y[j], x[j]);
-              if (here) dw[j] = fadd2(dw[j], yn);
-              q = ffma2(yn, w[j], q);
-            }
-            const float2 k = both(row_sum<LANES>(q.x + q.y) * (-1.0f / D));
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < P; ++j)
-              y[j] = fmul2(both(ri), ffma2(x[j], k, fmul2(y[j], w[j])));
+              for (int j = 0; j < P; ++j) {
+                x[k][j] = fmul2(x[k][j], both(ri));  // n
+                const float2 yn = fmul2(y[k][j], x[k][j]);
+                if (here) dw[k][j] = fadd2(dw[k][j], yn);
+                q = ffma2(yn, w[k][j], q);
+              }
+            const float2 m = both(row_sum<LANES>(q.x + q.y) * (-1.0f / D));
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < P; ++j)
+                y[k][j] = fmul2(both(ri), ffma2(x[k][j], m, fmul2(y[k][j], w[k][j])));
           }
         }
-        if (here && MATTN_IN_BOUNDS(kSiteRope, out - ov.p, ov.bytes))
-          *reinterpret_cast<uint4*>(out) = pack<kBf16>(y);
+        if (here && MATTN_IN_BOUNDS(kSiteRope, out - ov.p, ov.bytes)) {
+          *reinterpret_cast<uint4*>(out + c0) = pack<kBf16>(y[0]);
+          *reinterpret_cast<uint4*>(out + c1) = pack<kBf16>(y[1]);
+        }
       }
     }
 
@@ -342,12 +364,14 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
       float* sh = reinterpret_cast<float*>(ring);  // [warps][D]
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float v = i & 1 ? dw[i / 2].y : dw[i / 2].x;
+      for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int d = LANES; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-        if (sub == 0) sh[warp * D + chunk * N + i] = v;
-      }
+        for (int i = 0; i < N; ++i) {
+          float v = i & 1 ? dw[k][i / 2].y : dw[k][i / 2].x;
+#pragma unroll
+          for (int d = LANES; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (sub == 0) sh[warp * D + ch[k] + i] = v;
+        }
       __syncthreads();
       for (int c = threadIdx.x; c < D; c += kRopeThreads) {
         float v = 0.0f;
@@ -364,6 +388,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwd ? kMinBwd : kMinFwd)
 // 32 columns, 32 rows of threads each taking every 32nd partial.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n, int D, float* dwq,
                                                        float* dwk) {
+  wait_for_primary();
   __shared__ float sh[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
   float v = 0.0f;
@@ -380,10 +405,10 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n,
 
 template <int D, bool kBf16, bool kBwd>
 cudaError_t launch_typed(RopeArgs& a, bool inter, int B, float* const* dw, cudaStream_t stream) {
-  constexpr int kSubs = 32 / (D / Chunk<kBf16>::N);
+  constexpr int kSubs = 32 / (D / (2 * Chunk<kBf16>::N));
   a.B = B;
   const long long tokens = (long long)B * a.S;
-  const int resident = (kBwd ? kMinBwd : kMinFwd) * sm_count();
+  const int resident = kRopePerSm * sm_count();
   // 8 tokens per block where they give every resident block some; a decode
   // step's few tokens: one per block, and one row per lane group and item, so that
   // the heads spread over the warps.
@@ -398,12 +423,32 @@ cudaError_t launch_typed(RopeArgs& a, bool inter, int B, float* const* dw, cudaS
   }
   const long long all = many ? a.groups * items : a.groups * ((items + kRopeWarps - 1) / kRopeWarps);
   const int blocks = (int)std::min<long long>(std::min(resident, kRopeMaxBlocks), all);
-  if (inter) norm_rope_kernel<D, kBf16, true, kBwd><<<blocks, kRopeThreads, 0, stream>>>(a);
-  else norm_rope_kernel<D, kBf16, false, kBwd><<<blocks, kRopeThreads, 0, stream>>>(a);
+  constexpr int kSmem = 2 * rope_rows<kBwd>() * (kBwd ? 4 : 2) * kRopeThreads * (int)sizeof(uint4);
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(norm_rope_kernel<D, kBf16, true, kBwd>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (attr_err == cudaSuccess)
+      attr_err = cudaFuncSetAttribute(norm_rope_kernel<D, kBf16, false, kBwd>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  if (attr_err != cudaSuccess) return attr_err;
+  if (inter) norm_rope_kernel<D, kBf16, true, kBwd><<<blocks, kRopeThreads, kSmem, stream>>>(a);
+  else norm_rope_kernel<D, kBf16, false, kBwd><<<blocks, kRopeThreads, kSmem, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !kBwd || (!dw[0] && !dw[1])) return e;
-  rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, stream>>>(a.part, blocks, D, dw[0], dw[1]);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_dw_kernel, static_cast<const float*>(a.part), blocks, D,
+                            dw[0], dw[1]);
 }
 
 template <bool kBwd>
