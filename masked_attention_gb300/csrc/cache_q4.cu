@@ -5,17 +5,18 @@
 //   s = bf16(max|x| / 7),  code = clamp(rint(x / s), -8, 7) + 8
 //
 // rint rounds ties to even; s = 0 stores code 8 throughout; a group that holds
-// an infinity or NaN gets s = NaN, so it reads back as NaN. x / s and the tie
-// are decided exactly, so the codes do not depend on how the quotient is
-// computed: c = rint(x / s) from an approximate reciprocal, then the
-// remainder x - c s (exact in fp32: x and s have 8 significant bits, c three)
-// tells whether the exact quotient could have rounded elsewhere, and only
-// then the group's lane divides.
+// an infinity or NaN gets s = NaN, so it reads back as NaN. The quotient is
+// x times an approximate reciprocal, corrected once by its exact remainder:
+// q = q0 + (x - q0 s) / s. A tie, an exact k + 1/2, comes out exactly (the error
+// of q0, 2^-22, is squared), and since x and s have 8 significant bits every other
+// quotient is at least 2^-9 away from a tie; so the codes are those of exact
+// division.
 //
-// Bound by HBM (a bf16 element is 2 bytes, a stored one 0.5625). A lane
-// holds 8 channels of a row: 16 bytes of bf16, one 4-byte word of codes; a
-// scale's 32 channels are four neighbouring lanes. K and V rows of a token and
-// head are handled together, several rows per lane in flight.
+// Bound by HBM (a bf16 element is 2 bytes, a stored one 0.5625), with the
+// quantiser's instructions close behind. A lane holds 16 channels of a row (32 bytes
+// of bf16, 8 of codes), half of a scale's, so the largest magnitude takes one
+// shuffle. A warp takes a batch of a token's K and V rows, with the slot (read:
+// and the codes) of its next batch on the way.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,43 +34,44 @@ namespace mattn {
 namespace {
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheRows = 2;  // (K, V) row pairs in flight per lane group
+constexpr int kCacheWarps = kCacheThreads / 32;
+constexpr int kCacheRows = 4;   // rows in flight per lane group
+constexpr int kCachePerSm = 3;  // blocks per SM. 16384 tokens x 8 heads of 128 channels, write and
+                                // read: 38 us; 2 rows at 4 blocks 42 us, 1 row at 6 blocks 46 us
 
 struct CacheArgs {
   char* x[2];            // K and V rows (store: read, load: written)
   long long sb[2], sh[2], ss[2], span[2];  // bytes
   uint8_t* pool;
   const long long* slots;  // [B][S]
-  int Hkv, S, num_pages, shift;
-  long long units;  // row pairs: tokens * heads
+  int B, Hkv, S, num_pages, shift;
+  int batches;             // batches of rows per token
+  bool wide;               // rows are 32-byte aligned
 };
 
-// The eight codes of a lane, exactly: the definition itself.
-__device__ __noinline__ uint32_t encode_exact(const float* x, float s) {
+// The eight codes of a word, exactly: the definition itself.
+__device__ __noinline__ uint32_t encode_exact(uint4 v, float s) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    const float x = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
     int c = 0;
-    if (s > 0.0f) c = (int)fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -8.0f), 7.0f);
+    if (s > 0.0f) c = (int)fminf(fmaxf(rintf(__fdiv_rn(x, s)), -8.0f), 7.0f);
     word |= (uint32_t)(c + 8) << (4 * i);
   }
   return word;
 }
 
-// Quantises a lane's 8 channels (four lanes share a scale): the code word and
-// the scale's bf16 bits.
-__device__ __forceinline__ void encode(const uint4& v, uint32_t& word, uint32_t& scale) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  float x[8];
-  uint32_t m = 0;  // largest |x| as bits: orders like the values, NaN last
+// Quantises a lane's 16 channels (two neighbouring lanes share a scale): the
+// code words and the scale's bf16 bits.
+__device__ __forceinline__ void encode(const uint4 (&v)[2], uint32_t (&word)[2], uint32_t& scale) {
+  const uint32_t u[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  uint32_t m2 = 0;  // largest |x| as bits, two at a time: ordered like the values, NaN last
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    m = max(m, max((u[i] << 16) & 0x7fff0000u, u[i] & 0x7fff0000u));
-  }
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  for (int i = 0; i < 8; ++i) m2 = __vmaxu2(m2, u[i] & 0x7fff7fffu);
+  m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+  const uint32_t m = max(m2 & 0xffff0000u, m2 << 16);
   float s = 0.0f;
   if (m >= 0x7f800000u) {
     scale = 0x7fffu;
@@ -78,110 +80,213 @@ __device__ __forceinline__ void encode(const uint4& v, uint32_t& word, uint32_t&
     scale = *reinterpret_cast<const unsigned short*>(&b);
     s = __bfloat162float(b);
   }
-  // fast form: kMagic + c is a float whose low mantissa bits hold c
+  // kMagic + q is a float whose low mantissa bits hold rint(q)
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
   const float inv = __fdividef(1.0f, s);
-  float worst = s > 1e-30f ? 0.0f : INFINITY;  // tiny, zero, NaN scales: the exact form
-  word = 0;
+  const float2 inv2 = make_float2(inv, inv), s2 = make_float2(-s, -s);
+  const float2 up = make_float2(kMagic, kMagic);
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float t = fmaf(x[i], inv, kMagic);
-    const float c = t - kMagic;
-    worst = fmaxf(worst, fabsf(fmaf(-c, s, x[i])));
-    word = word * 16u + (__float_as_uint(t) - 0x4b400000u + 8u);
+  for (int k = 0; k < 2; ++k) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const uint32_t p = u[4 * k + i];
+      const float2 x = make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+      const float2 q = fmul2(x, inv2);
+      const float2 t = fadd2(ffma2(ffma2(q, s2, x), inv2, q), up);
+      w = w * 16u + __float_as_uint(t.y);
+      w = w * 16u + __float_as_uint(t.x);
+    }
+    word[k] = w - (0x4b400000u - 8u) * 0x11111111u;  // the magic's bits, off all eight
   }
-  // |remainder| below s/2 by more than the reciprocal's error: c is right
-  if (!(worst < s * (0.5f - 1e-5f))) word = encode_exact(x, s);
+  // zero, NaN and tiny scales, where the remainder or the reciprocal leaves
+  // fp32's normal range
+  if (!(s > 1e-30f)) {
+    word[0] = encode_exact(v[0], s);
+    word[1] = encode_exact(v[1], s);
+  }
+}
+
+// The eight values of a word, (n - 8) * scale rounded once to bf16: 128 + n has
+// n's bits in its mantissa, n - 8 is exact, and the packed product rounds.
+__device__ __forceinline__ uint4 decode(uint32_t w, uint32_t scale) {
+  const uint32_t s2 = scale | scale << 16, off = 0x43084308u;  // 136
+  uint32_t p[4];  // pairs (i, i + 4)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t raw = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&raw),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&off));
+    const __nv_bfloat162 x = __hmul2(n, *reinterpret_cast<const __nv_bfloat162*>(&s2));
+    p[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                    __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+}
+
+// 32 bytes of a row: one access where its rows are aligned to that (`wide`),
+// else two, which then leave every 32-byte sector to two instructions.
+__device__ __forceinline__ void load32(const uint4* p, bool wide, uint4 (&v)[2]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                   "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                 : "l"(p));
+  } else {
+    v[0] = p[0];
+    v[1] = p[1];
+  }
+}
+
+__device__ __forceinline__ void store32(uint4* p, bool wide, const uint4& a, const uint4& b) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    p[0] = a;
+    p[1] = b;
+  }
+}
+
+// Units (token, batch of its K and V rows), the batch first; a warp takes every
+// stride-th. Where a unit is, kept without divisions.
+struct Cursor {
+  long long u, token;
+  int batch, b, s;
+};
+
+template <int D, bool kLoad>
+__global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
+    cache_q4_kernel(const CacheArgs a) {
+  constexpr int R = kCacheRows;
+  constexpr int LANES = D / 16;     // lanes per row
+  constexpr int SUBS = 32 / LANES;  // rows side by side in a warp
+  const int lane = threadIdx.x & 31, part = lane % LANES, sub = lane / LANES;
+  const Q4Layout L{D, 1 << a.shift};
+  const long long units = (long long)a.B * a.S * a.batches;
+  const long long stride = (long long)gridDim.x * kCacheWarps;
+  Cursor c;
+  c.u = (long long)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
+  if (c.u >= units) return;
+  c.token = c.u / a.batches;
+  c.batch = (int)(c.u % a.batches);
+  c.b = (int)(c.token / a.S);
+  c.s = (int)(c.token % a.S);
+  const long long dt = stride / a.batches;
+  const int dbatch = (int)(stride % a.batches), db = (int)(dt / a.S), ds = (int)(dt % a.S);
+  const long long page_bytes = (long long)a.Hkv * L.bytes();
+  const int rows = 2 * a.Hkv;  // K rows of all heads, then V rows
+  auto advance = [&](Cursor& k) {
+    k.u += stride;
+    k.batch += dbatch;
+    const int carry = k.batch >= a.batches;
+    k.batch -= carry ? a.batches : 0;
+    k.token += dt + carry;
+    k.s += ds + carry;
+    k.b += db;
+    if (k.s >= a.S) {
+      k.s -= a.S;
+      ++k.b;
+    }
+  };
+  auto slot_of = [&](const Cursor& k) { return k.u < units ? a.slots[k.token] : -1; };
+  // row r of the unit for this lane group: K or V, head; nullptr: past the last
+  auto bf16_row = [&](const Cursor& k, int r) -> uint4* {
+    const int rr = k.batch * SUBS * R + r * SUBS + sub;
+    const int v = rr >= a.Hkv ? 1 : 0, h = rr - v * a.Hkv;
+    const long long at = v ? k.b * a.sb[1] + k.s * a.ss[1] + h * a.sh[1]
+                           : k.b * a.sb[0] + k.s * a.ss[0] + h * a.sh[0];
+    if (rr >= rows || !MATTN_IN_BOUNDS(kSiteCacheRow, at + part * 32, a.span[v] - 31)) return nullptr;
+    return reinterpret_cast<uint4*>((v ? a.x[1] : a.x[0]) + at + part * 32);
+  };
+  // its codes and scale in the record, for a slot of the pool; nullptr: none
+  auto code_row = [&](const Cursor& k, int r, long long slot, uint8_t*& scale) -> uint8_t* {
+    const int rr = k.batch * SUBS * R + r * SUBS + sub;
+    const int v = rr >= a.Hkv ? 1 : 0, h = rr - v * a.Hkv;
+    const long long page = slot >> a.shift;
+    if (rr >= rows || slot < 0 || page >= a.num_pages) return nullptr;
+    uint8_t* rec = a.pool + page * page_bytes + (long long)h * L.bytes();
+    const int row = (int)(slot & (L.page - 1));
+    scale = rec + (v ? L.v_scales() : L.k_scales()) + row * L.scale_row() + part / 2 * 2;
+    return rec + (v ? L.v_codes() : 0) + row * L.code_row() + part * 8;
+  };
+
+  if constexpr (!kLoad) {
+    long long slot = slot_of(c);
+    while (c.u < units) {
+      uint4 raw[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint4* x = bf16_row(c, r);
+        raw[r][0] = raw[r][1] = make_uint4(0, 0, 0, 0);
+        if (x) load32(x, a.wide, raw[r]);
+      }
+      const Cursor now = c;
+      advance(c);
+      const long long slot_next = slot_of(c);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        uint32_t word[2], sc;
+        encode(raw[r], word, sc);
+        uint8_t* scale;
+        uint8_t* code = code_row(now, r, slot, scale);
+        if (!code) continue;
+        *reinterpret_cast<uint2*>(code) = make_uint2(word[0], word[1]);
+        if (part % 2 == 0) *reinterpret_cast<unsigned short*>(scale) = (unsigned short)sc;
+      }
+      slot = slot_next;
+    }
+  } else {
+    // the codes of the next unit, and the slot of the one after it, are on
+    // their way while a unit is written
+    auto fetch = [&](const Cursor& k, long long slot, uint2 (&word)[R], uint32_t (&sc)[R]) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        uint8_t* scale;
+        const uint8_t* code = code_row(k, r, slot, scale);
+        word[r] = code ? *reinterpret_cast<const uint2*>(code) : make_uint2(0x88888888u, 0x88888888u);
+        sc[r] = code ? *reinterpret_cast<const unsigned short*>(scale) : 0u;
+      }
+    };
+    uint2 word[R];
+    uint32_t sc[R];
+    fetch(c, slot_of(c), word, sc);
+    Cursor ahead = c;
+    advance(ahead);
+    long long slot = slot_of(ahead);
+    while (c.u < units) {
+      uint2 word_next[R];
+      uint32_t sc_next[R];
+      const Cursor next = ahead;
+      if (next.u < units) fetch(next, slot, word_next, sc_next);
+      advance(ahead);
+      slot = slot_of(ahead);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        uint4* x = bf16_row(c, r);
+        if (!x) continue;
+        store32(x, a.wide, decode(word[r].x, sc[r]), decode(word[r].y, sc[r]));
+      }
+      c = next;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        word[r] = word_next[r];
+        sc[r] = sc_next[r];
+      }
+    }
+  }
 }
 
 template <int D, bool kLoad>
-__global__ void __launch_bounds__(kCacheThreads) cache_q4_kernel(const CacheArgs a) {
-  constexpr int LANES = D / 8;      // lanes per row
-  constexpr int SUBS = 32 / LANES;  // rows side by side in a warp
-  const int lane = threadIdx.x & 31, chunk = lane % LANES, sub = lane / LANES;
-  const Q4Layout L{D, 1 << a.shift};
-  const long long warp = (long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
-  const long long step = (long long)gridDim.x * (kCacheThreads / 32) * SUBS * kCacheRows;
-  for (long long u0 = warp * SUBS * kCacheRows; u0 < a.units; u0 += step) {
-    long long at[kCacheRows][2];       // byte offset of the row's chunk in K and V
-    uint8_t* rec[kCacheRows];          // the row's page record, nullptr: no slot
-    int row[kCacheRows];               // its row in the page
-    bool have[kCacheRows];
-    uint4 raw[kCacheRows][2];
-    uint32_t code[kCacheRows][2], sc[kCacheRows][2];
-#pragma unroll
-    for (int r = 0; r < kCacheRows; ++r) {
-      const long long u = u0 + r * SUBS + sub;
-      have[r] = u < a.units;
-      rec[r] = nullptr;
-      row[r] = 0;
-      at[r][0] = at[r][1] = 0;
-      if (!have[r]) continue;
-      const long long token = u / a.Hkv;
-      const int h = (int)(u - token * a.Hkv);
-      const long long b = token / a.S, s = token - b * a.S;
-      const long long slot = a.slots[token];
-      const long long page = slot >> a.shift;
-      if (slot >= 0 && page < a.num_pages) {
-        rec[r] = a.pool + ((size_t)page * a.Hkv + h) * L.bytes();
-        row[r] = (int)(slot & (L.page - 1));
-      }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        at[r][t] = b * a.sb[t] + h * a.sh[t] + s * a.ss[t] + chunk * 16;
-        if (!MATTN_IN_BOUNDS(kSiteCacheRow, at[r][t], a.span[t] - 15)) have[r] = false;
-      }
-    }
-    if constexpr (!kLoad) {
-#pragma unroll
-      for (int r = 0; r < kCacheRows; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          raw[r][t] = have[r] && rec[r] ? *reinterpret_cast<const uint4*>(a.x[t] + at[r][t])
-                                        : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < kCacheRows; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          encode(raw[r][t], code[r][t], sc[r][t]);
-          if (!have[r] || !rec[r]) continue;
-          *reinterpret_cast<uint32_t*>(rec[r] + (t ? L.v_codes() : 0) + row[r] * L.code_row() +
-                                       chunk * 4) = code[r][t];
-          if (chunk % 4 == 0)
-            *reinterpret_cast<unsigned short*>(rec[r] + (t ? L.v_scales() : L.k_scales()) +
-                                               row[r] * L.scale_row() + chunk / 4 * 2) =
-                (unsigned short)sc[r][t];
-        }
-    } else {
-#pragma unroll
-      for (int r = 0; r < kCacheRows; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          code[r][t] = 0;
-          sc[r][t] = 0;  // no slot: (0 - 8) * 0, stored as zeros below
-          if (!have[r] || !rec[r]) continue;
-          code[r][t] = *reinterpret_cast<const uint32_t*>(
-              rec[r] + (t ? L.v_codes() : 0) + row[r] * L.code_row() + chunk * 4);
-          sc[r][t] = *reinterpret_cast<const unsigned short*>(
-              rec[r] + (t ? L.v_scales() : L.k_scales()) + row[r] * L.scale_row() + chunk / 4 * 2);
-        }
-#pragma unroll
-      for (int r = 0; r < kCacheRows; ++r)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!have[r]) continue;
-          const float s = __uint_as_float(sc[r][t] << 16);
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float lo = (float)(int)((code[r][t] >> (8 * i)) & 15u) - 8.0f;
-            const float hi = (float)(int)((code[r][t] >> (8 * i + 4)) & 15u) - 8.0f;
-            o[i] = rec[r] ? pack_bf16x2(lo * s, hi * s) : 0u;
-          }
-          *reinterpret_cast<uint4*>(a.x[t] + at[r][t]) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-    }
-  }
+cudaError_t launch_cache(CacheArgs& a, cudaStream_t stream) {
+  constexpr int kBatch = 32 / (D / 16) * kCacheRows;
+  a.batches = (2 * a.Hkv + kBatch - 1) / kBatch;
+  const long long units = (long long)a.B * a.S * a.batches;
+  const int blocks = (int)std::min<long long>(kCachePerSm * sm_count(),
+                                              (units + kCacheWarps - 1) / kCacheWarps);
+  cache_q4_kernel<D, kLoad><<<blocks, kCacheThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const long long* slots,
@@ -207,6 +312,9 @@ attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const l
   }
   if ((reinterpret_cast<uintptr_t>(pool) & 15u) || (reinterpret_cast<uintptr_t>(slots) & 7u))
     return ATTN_ERR_MISALIGNED;
+  a.wide = true;
+  for (int t = 0; t < 2; ++t)
+    a.wide = a.wide && !((reinterpret_cast<uintptr_t>(a.x[t]) | a.sb[t] | a.sh[t] | a.ss[t]) & 31);
   a.pool = static_cast<uint8_t*>(pool);
   a.slots = slots;
   a.Hkv = Hkv;
@@ -214,17 +322,9 @@ attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const l
   a.num_pages = num_pages;
   a.shift = 4;
   while ((1 << a.shift) != page_size) ++a.shift;
-  a.units = (long long)B * S * Hkv;
-  const long long per_block = (long long)(kCacheThreads / 32) * (32 / (D / 8)) * kCacheRows;
-  const int blocks = (int)std::min<long long>(8LL * sm_count(), (a.units + per_block - 1) / per_block);
-  if (load) {
-    if (D == 64) cache_q4_kernel<64, true><<<blocks, kCacheThreads, 0, stream>>>(a);
-    else cache_q4_kernel<128, true><<<blocks, kCacheThreads, 0, stream>>>(a);
-  } else {
-    if (D == 64) cache_q4_kernel<64, false><<<blocks, kCacheThreads, 0, stream>>>(a);
-    else cache_q4_kernel<128, false><<<blocks, kCacheThreads, 0, stream>>>(a);
-  }
-  return cuda_status(cudaGetLastError());
+  a.B = B;
+  if (load) return cuda_status(D == 64 ? launch_cache<64, true>(a, stream) : launch_cache<128, true>(a, stream));
+  return cuda_status(D == 64 ? launch_cache<64, false>(a, stream) : launch_cache<128, false>(a, stream));
 }
 
 }  // namespace

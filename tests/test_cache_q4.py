@@ -69,6 +69,35 @@ def test_store_and_load(D, page, B, H, S):
 
 
 @pytest.mark.gpu
+def test_half_aligned_rows():
+    """Rows that start on 16 but not on 32 bytes (slices of an odd projection)."""
+    import masked_attention_gb300 as M
+    D, page, S = 128, 16, 21
+    k, v = rows(1, 2, S, D, 8), rows(1, 2, S, D, 9)
+    slots = np.random.default_rng(5).permutation(3 * page)[:S].astype(np.int64)
+    ref = oracle_pool(k, v, slots, 3, page)
+    for pad in (8, 24):
+        dev = []
+        for x in (k, v):
+            wide = torch.full((1, S, 2, D + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+            buf = torch.full((wide.numel() + pad,), 3.0, dtype=torch.bfloat16, device="cuda")
+            t = buf[pad:].view(wide.shape)[..., :D].transpose(1, 2)
+            t.copy_(x.cuda())
+            dev.append((t, buf))
+        pool = torch.full(ref.shape, 0xCC, dtype=torch.uint8, device="cuda")
+        ds = torch.from_numpy(slots).cuda()
+        M.attn_cache_store_q4(dev[0][0], dev[1][0], ds, pool, page_size=page)
+        assert np.array_equal(pool.cpu().numpy(), ref)
+        plain = [torch.empty(1, 2, S, D, dtype=torch.bfloat16, device="cuda") for _ in (0, 1)]
+        M.attn_cache_load_q4(pool, ds, *plain, page_size=page)
+        M.attn_cache_load_q4(pool, ds, dev[0][0], dev[1][0], page_size=page)
+        for (t, buf), x in zip(dev, plain):
+            assert torch.equal(t, x)
+            t.fill_(3.0)
+            assert (buf == 3.0).all()   # nothing between the rows was touched
+
+
+@pytest.mark.gpu
 def test_values_at_the_edges():
     """Ties, tiny and huge magnitudes, signed zeros, infinities and NaN."""
     D, page = 64, 16
@@ -90,8 +119,16 @@ def test_values_at_the_edges():
     k = k.to(torch.bfloat16)
     v = k.flip(2)
     slots = np.arange(16, dtype=np.int64)
-    assert np.array_equal(store(k, v, slots, 1, page).cpu().numpy(),
-                          oracle_pool(k, v, slots, 1, page))
+    pool = store(k, v, slots, 1, page)
+    assert np.array_equal(pool.cpu().numpy(), oracle_pool(k, v, slots, 1, page))
+    # and read back: subnormal scales, NaN groups
+    import masked_attention_gb300 as M
+    out = [torch.empty(1, 1, 16, D, dtype=torch.bfloat16, device="cuda") for _ in (0, 1)]
+    M.attn_cache_load_q4(pool, torch.from_numpy(slots).cuda(), *out, page_size=page)
+    for row in range(16):
+        for got, ref in zip(out, q4_row(pool.cpu().numpy(), row, 0, page, D)):
+            got = got[0, 0, row].double().cpu().numpy()
+            assert np.array_equal(got, bf16_value(bf16_bits(ref)), equal_nan=True)
 
 
 @pytest.mark.gpu
