@@ -67,6 +67,10 @@ constexpr int kQ4Warps = 4;
 constexpr int kQ4Tile = 32;    // keys per warp step
 constexpr int kQ4Stages = 2;   // per-warp tile buffers
 constexpr int kQ4MaxRows = 16;
+#ifndef SEGC
+#define SEGC 4
+#endif
+constexpr int kQ4SegmentCost = SEGC;
 constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
 constexpr uint32_t kQ4Tiny = 0x12801280u;  // bf16 2^-90, twice: smaller V scales count as this,
@@ -97,6 +101,9 @@ struct Q4Problem {
 // A sequence's tiles: those of the sinks, then those from win_tile on.
 struct Q4Range {
   int len, win_tile, sink_tiles, tiles;
+  // What a pair counts for in the dealing out: its tiles, and the start and
+  // end of a segment as so many more.
+  __device__ __forceinline__ int cost() const { return tiles ? tiles + kQ4SegmentCost : 0; }
 };
 
 __device__ __forceinline__ Q4Range q4_range(const Q4Problem& p, int b) {
@@ -124,7 +131,8 @@ struct Q4Cfg {
   static constexpr int kState = 8 * NT * (2 + D) * 4;      // a warp's m, l, O at the end
   static constexpr int kArea = kWarp > kState ? kWarp : kState;
   static constexpr int kQ = NT * G * 512;                  // q fragments, 16 bytes per lane
-  static constexpr int kSmem = kQ4Warps * kArea + kQ + NT * 8 * 4;
+  static constexpr int kOff = NT * G * 64;                 // the scores' offsets, 16 bytes per t
+  static constexpr int kSmem = kQ4Warps * kArea + kQ + kOff + NT * 8 * 4;
   // Rows of codes are D / 2 bytes; chunk c (16 bytes) of row r stands at place
   // c ^ swz(r), so that the 8 rows of an ldmatrix matrix hit distinct banks.
   static __device__ __forceinline__ int swz(int row) {
@@ -182,13 +190,19 @@ __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t b
 }
 
 // Nibbles 0 to 3 of both halves of w as exact fp16 pairs (n - 8, n' - 8): the
-// nibble's bits in the mantissa of 1024 or, one nibble up, of 64.
+// nibble's bits in the mantissa of 1024 or, one nibble up, of 64. kOdd false:
+// nibbles 1 and 3 keep the offset, 64 + n.
+template <bool kOdd>
 __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&f)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t x = j & 2 ? w >> 8 : w;
     const uint32_t raw = j & 1 ? and_or(x, 0x00f000f0u, 0x54005400u)    // 64 + n
                                : and_or(x, 0x000f000fu, 0x64006400u);   // 1024 + n
+    if ((j & 1) && !kOdd) {
+      f[j] = raw;
+      continue;
+    }
     const uint32_t off = j & 1 ? 0x54805480u : 0x64086408u;         // 72, 1032
     const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&raw),
                               *reinterpret_cast<const __half2*>(&off));
@@ -242,7 +256,8 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
   const uint32_t area = smem_u32(smem) + warp * C::kArea;
   const uint8_t* area_ptr = smem + warp * C::kArea;
   uint4* qs = reinterpret_cast<uint4*>(smem + kQ4Warps * C::kArea);   // [NT][G][32 lanes]
-  float* units = reinterpret_cast<float*>(smem + kQ4Warps * C::kArea + C::kQ);  // [NT * 8]
+  float4* offs = reinterpret_cast<float4*>(smem + kQ4Warps * C::kArea + C::kQ);  // [NT][G][4]
+  float* units = reinterpret_cast<float*>(smem + kQ4Warps * C::kArea + C::kQ + C::kOff);  // [NT * 8]
   const int v_first = v_begin + warp;
   const int n_tiles = v_first < v_end ? (v_end - v_first + kQ4Warps - 1) / kQ4Warps : 0;
   auto key_of = [&](int i) {  // first key of the warp's tile i
@@ -274,34 +289,37 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
     }
     const uint32_t dst = area + (i & (kQ4Stages - 1)) * C::kStage;
     const int key0 = key_of(i);
-    const uint8_t* src[2];
-    uint32_t bytes[2];
-    int in_page[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int pg = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + h);
-      bytes[h] = pg >= 0 ? 16u : 0u;
-      src[h] = head_pool + (size_t)(uint32_t)max(pg, 0) * page_stride;
-      in_page[h] = (key0 + 16 * h) & (L.page - 1);
-    }
-    // a half's codes are 8 D consecutive bytes of the record: D / 64 chunks per lane
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint8_t* k = src[h] + in_page[h] * L.code_row();
+    const uint32_t lane_dst = dst + lane / G * C::kRow + (lane % G ^ C::swz(lane / G)) * 16;
+    auto half_codes = [&](int h, const uint8_t* k, uint32_t bytes) {  // 16 keys, K and V
       const uint8_t* v = k + L.v_codes();
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const uint32_t d = dst + (16 * h + c * (32 / G) + lane / G) * C::kRow +
-                           (lane % G ^ C::swz(lane / G)) * 16;
-        cp_async16z(d, k + c * 512, bytes[h]);
-        cp_async16z(d + C::kCodes, v + c * 512, bytes[h]);
+        const uint32_t d = lane_dst + (16 * h + c * (32 / G)) * C::kRow;
+        cp_async16z(d, k + c * 512, bytes);
+        cp_async16z(d + C::kCodes, v + c * 512, bytes);
+      }
+    };
+    const int pg0 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15));
+    const uint8_t* rec0 = head_pool + (size_t)(uint32_t)max(pg0, 0) * page_stride;
+    const int in0 = key0 & (L.page - 1);
+    const uint32_t bytes0 = pg0 >= 0 ? 16u : 0u;
+    const uint8_t* k0 = rec0 + in0 * L.code_row();
+    half_codes(0, k0, bytes0);
+    const uint8_t* sc = rec0 + in0 * L.scale_row() + sc_src;
+    uint32_t sc_bytes = bytes0;
+    if (L.page >= kQ4Tile) {  // the whole tile lies in one page
+      half_codes(1, k0 + 16 * L.code_row(), bytes0);
+      if (sc_half) sc += 16 * L.scale_row();
+    } else {
+      const int pg1 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + 1);
+      const uint8_t* rec1 = head_pool + (size_t)(uint32_t)max(pg1, 0) * page_stride;
+      half_codes(1, rec1, pg1 >= 0 ? 16u : 0u);
+      if (sc_half) {
+        sc = rec1 + sc_src;
+        sc_bytes = pg1 >= 0 ? 16u : 0u;
       }
     }
-    if (lane < 4 * kScaleChunks)
-      cp_async16z(dst + sc_dst,
-                  (sc_half ? src[1] + in_page[1] * L.scale_row() : src[0] + in_page[0] * L.scale_row()) +
-                      sc_src,
-                  sc_half ? bytes[1] : bytes[0]);
+    if (lane < 4 * kScaleChunks) cp_async16z(dst + sc_dst, sc, sc_bytes);
     cp_async_commit();
   };
 
@@ -320,6 +338,7 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
       const int r = nt * 8 + g;
       uint4 x[G];
       float big = 0.0f;
+      bool odd = false;  // a NaN, which fmaxf passes over
 #pragma unroll
       for (int a = 0; a < G; ++a) {
         x[a] = make_uint4(0, 0, 0, 0);
@@ -328,21 +347,33 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
         const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          big = fmaxf(big, fmaxf(fabsf(scale_of(u[i], 0)), fabsf(scale_of(u[i], 1))));
+          for (int e = 0; e < 2; ++e) {
+            big = fmaxf(big, fabsf(scale_of(u[i], e)));
+            odd = odd || isnan(scale_of(u[i], e));
+          }
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      odd = __ballot_sync(0xffffffffu, odd) & (0xfu << (lane & 28));
+      const bool fine = big < INFINITY && !odd;
       const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
       const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-      if (t == 0) units[r] = exp2f((float)(ex - 14)) * p.scale2;  // scores per product, log2
+      // scores per product, log2; a row with an infinity or NaN scores NaN
+      if (t == 0) units[r] = fine ? exp2f((float)(ex - 14)) * p.scale2 : NAN;
 #pragma unroll
       for (int a = 0; a < G; ++a) {
         const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-        float c[8];
+        float c[8], sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = scale_of(u[i / 2], i & 1) * up;
+        for (int i = 0; i < 8; ++i) c[i] = fine ? scale_of(u[i / 2], i & 1) * up : 0.0f;
         qs[(nt * G + a) * 32 + lane] = make_uint4(pack_f16x2(c[0], c[4]), pack_f16x2(c[1], c[5]),
                                                   pack_f16x2(c[2], c[6]), pack_f16x2(c[3], c[7]));
+        // -72 sum(q) over the nibbles that keep their offset: per lane channels
+        // 1, 3, 5, 7; of row g, stored for the lane t that holds columns 2t, 2t + 1
+        sum = c[1] + c[3] + c[5] + c[7];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (t < 2) reinterpret_cast<float*>(offs + (nt * G + a) * 4 + g / 2)[g % 2 + 2 * t] = -72.0f * sum;
       }
     }
   }
@@ -387,31 +418,33 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
     const uint32_t rows = area + stage_off + lane * C::kRow + C::swz(lane) * 16;
     const uint8_t* scales = area_ptr + stage_off + 2 * C::kCodes;
     float x[2][NT][4];
+    uint32_t sk[4][G / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_scales<G>(scales + (8 * i + g) * 2 * G, sk[i]);
 #pragma unroll
     for (int a = 0; a < G; ++a) {
       uint32_t w[4];  // the lane's 8 channels of group a, for keys g, g + 8, g + 16, g + 24
       ldsm4(rows ^ (a * 16), w);
-      float sk[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sk[i] = scale_of(*reinterpret_cast<const uint32_t*>(scales + (8 * i + g) * 2 * G + (a / 2) * 4),
-                         a & 1);
       uint4 qf[NT];
+      float4 off[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) qf[nt] = qs[(nt * G + a) * 32 + lane];
+      for (int nt = 0; nt < NT; ++nt) {
+        qf[nt] = qs[(nt * G + a) * 32 + lane];
+        off[nt] = offs[(nt * G + a) * 4 + t];
+      }
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t f[2][4];
-        nibble_pairs(w[2 * mt], f[0]);
-        nibble_pairs(w[2 * mt + 1], f[1]);
+        nibble_pairs<false>(w[2 * mt], f[0]);
+        nibble_pairs<false>(w[2 * mt + 1], f[1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          float d[4] = {off[nt].x, off[nt].y, off[nt].z, off[nt].w};
           mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qf[nt].x, qf[nt].y);
           mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qf[nt].z, qf[nt].w);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float s = sk[2 * mt + (e >> 1)];
+            const float s = scale_of(sk[2 * mt + (e >> 1)][a / 2], a & 1);
             x[mt][nt][e] = a == 0 ? s * d[e] : fmaf(s, d[e], x[mt][nt][e]);
           }
         }
@@ -522,8 +555,8 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt) {
         uint32_t f[2][4];
-        nibble_pairs(w[2 * mt], f[0]);
-        nibble_pairs(w[2 * mt + 1], f[1]);
+        nibble_pairs<true>(w[2 * mt], f[0]);
+        nibble_pairs<true>(w[2 * mt + 1], f[1]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float pv[4];
@@ -599,18 +632,16 @@ __device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem
     for (int w = 0; w < kQ4Warps; ++w)
       M = fmaxf(M, reinterpret_cast<const float*>(smem + w * C::kArea)[r]);
     float Ls = 0.0f, acc = 0.0f;
-    if (M != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kQ4Warps; ++w) {
-        const float* st = reinterpret_cast<const float*>(smem + w * C::kArea);
-        const float wt = ex2_approx(st[r] - M);  // -inf -> 0
-        Ls += wt * st[kR + r];
-        acc += wt * st[2 * kR + r * D + c];
-      }
+    for (int w = 0; w < kQ4Warps; ++w) {
+      const float* st = reinterpret_cast<const float*>(smem + w * C::kArea);
+      const float wt = M != -INFINITY ? ex2_approx(st[r] - M) : 1.0f;  // -inf -> 0
+      Ls += wt * st[kR + r];
+      acc += wt * st[2 * kR + r * D + c];
     }
     // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
-    const float out = M != -INFINITY ? acc / Ls : 0.0f;
-    const float lse2 = M != -INFINITY ? M + __log2f(Ls) : -INFINITY;
+    const float out = Ls == 0.0f ? 0.0f : acc / Ls;
+    const float lse2 = Ls == 0.0f ? -INFINITY : M + __log2f(Ls);
     if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
     if (slot >= 0) {
       p.ws_o[((size_t)slot * R + r) * D + c] = out;
@@ -637,7 +668,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
   if (p.ws_meta) {
     long long total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32)
-      total += warp_sum(b0 + lane < p.B ? q4_range(p, b0 + lane).tiles : 0);
+      total += warp_sum(b0 + lane < p.B ? q4_range(p, b0 + lane).cost() : 0);
     total *= p.Hkv;
     // CTAs that take part: each has a tile for every warp, on the average
     const int ctas = (int)max(1ll, min((long long)gridDim.x, (total + kQ4Warps - 1) / kQ4Warps));
@@ -649,7 +680,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     b = p.B;
     long long before = 0;
     for (int b0 = 0; b0 < p.B && b == p.B; b0 += 32) {
-      const int n = b0 + lane < p.B ? q4_range(p, b0 + lane).tiles : 0;
+      const int n = b0 + lane < p.B ? q4_range(p, b0 + lane).cost() : 0;
       int end = n;  // inclusive scan
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -670,20 +701,23 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
 
   for (; b < p.B; ++b, hkv = 0) {
     const Q4Range rg = q4_range(p, b);
+    const int cost = rg.cost();
     if (p.ws_meta) {
-      if (seq_start >= hi && !(last_cta && rg.tiles == 0)) break;
-      if (rg.tiles > 0) hkv = max(0, (int)((lo - seq_start) / rg.tiles));
+      if (seq_start >= hi && !(last_cta && cost == 0)) break;
+      if (cost > 0) hkv = max(0, (int)((lo - seq_start) / cost));
     }
     for (; hkv < p.Hkv; ++hkv) {
       int v_begin = 0, v_end = rg.tiles;
-      const long long start = seq_start + (long long)hkv * rg.tiles;
-      if (p.ws_meta && rg.tiles > 0) {
+      const int pair = b * p.Hkv + hkv;
+      if (p.ws_meta && cost > 0) {
+        // the pair's tiles follow its own cost
+        const long long start = seq_start + (long long)hkv * cost + kQ4SegmentCost;
         if (start >= hi) break;
         v_begin = (int)max(0ll, lo - start);
         v_end = (int)min((long long)rg.tiles, hi - start);
+        if (v_begin >= rg.tiles) continue;
       }
       const bool cut = v_begin > 0 || v_end < rg.tiles;
-      const int pair = b * p.Hkv + hkv;
       if (p.ws_meta && threadIdx.x == 0) {
         if (v_begin == 0) p.ws_meta[pair].x = cut ? (int)blockIdx.x : -1;
         if (v_end == rg.tiles) p.ws_meta[pair].y = (int)blockIdx.x;
@@ -692,7 +726,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
                                    cut ? (long long)blockIdx.x + pair : -1);
       if (!p.ws_meta) return;
     }
-    seq_start += (long long)rg.tiles * p.Hkv;
+    seq_start += (long long)cost * p.Hkv;
   }
 }
 
@@ -767,14 +801,14 @@ __global__ void __launch_bounds__(kQ4Threads) q4_merge_kernel(const Q4Problem p)
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-      const float w = M == -INFINITY ? 0.0f : ex2_approx(sh[k][D] - M);
+      const float w = M == -INFINITY ? 1.0f : ex2_approx(sh[k][D] - M);
       L += w * sh[k][D + 1];
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[i] += w * sh[k][lane * V + i];
     }
   }
   if (!mine || !MATTN_IN_BOUNDS(kSiteQ4Out, row, rows)) return;
-  const bool any = M != -INFINITY;  // else no key in any part
+  const bool any = !(L == 0.0f);  // else no key in any part
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V;
 #pragma unroll
   for (int i = 0; i < V; i += 2)

@@ -238,6 +238,32 @@ def test_nan_in_a_visible_record_shows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ws", ["full", "none"])
+def test_infinities_and_nan_in_queries(D, ws):
+    """Such a row is NaN, as its scores are; the others keep their bits. Channels
+    far apart in size, and the largest finite ones, are ordinary."""
+    import masked_attention_gb300 as M
+    c = Cache([400, 3], 2, D, 16, seed=23)
+    q = queries(2, 4, 2, D)
+    ref = run(c, q, M.MASK_CAUSAL, ws)
+    bad = q.clone()
+    bad[0, 1, 0, 5] = float("inf")
+    bad[1, 3, 1, D - 1] = float("nan")
+    bad[0, 2, 1, :2] = torch.tensor([float("inf"), -float("inf")])
+    o, lse = run(c, bad, M.MASK_CAUSAL, ws)
+    hit = torch.zeros(2, 4, 2, dtype=torch.bool)
+    hit[0, 1, 0] = hit[1, 3, 1] = hit[0, 2, 1] = True
+    hit = hit.numpy()
+    assert np.isnan(o[hit]).all() and np.isnan(lse[hit]).all()
+    assert np.array_equal(o[~hit], ref[0][~hit]) and np.array_equal(lse[~hit], ref[1][~hit])
+    q[0, 0] *= torch.logspace(-12, 0, D, base=10.0)
+    q[0, 1] = 0
+    q[1, 2] *= 1e-30
+    check(c, q, ws)
+
+
+@pytest.mark.gpu
 def test_pages_outside_the_pool_read_zeros():
     """Bad table entries: their keys have K = V = 0 (as attn_decode reads them)."""
     c = Cache([100, 64], 2, 64, 16, seed=18)
