@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
   const long long stride = (long long)gridDim.x * kCacheWarps;
   Cursor c;
   c.u = (long long)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
+  early_start();
   if (c.u >= units) return;
   c.token = c.u / a.batches;
   c.batch = (int)(c.u % a.batches);
@@ -285,8 +286,7 @@ cudaError_t launch_cache(CacheArgs& a, cudaStream_t stream) {
   const long long units = (long long)a.B * a.S * a.batches;
   const int blocks = (int)std::min<long long>(kCachePerSm * sm_count(),
                                               (units + kCacheWarps - 1) / kCacheWarps);
-  cache_q4_kernel<D, kLoad><<<blocks, kCacheThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(cache_q4_kernel<D, kLoad>, blocks, kCacheThreads, 0, stream, a);
 }
 
 attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const long long* slots,

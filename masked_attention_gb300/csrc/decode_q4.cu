@@ -40,7 +40,8 @@
 // resident wave (16 sequences x 8 heads in equal splits of 8 CTAs per SM ran 2.1
 // waves: 135 us against 125). A pair that lies within one CTA is written at once; one that
 // is cut leaves fp32 partial results in the workspace, which a second, small
-// kernel joins by the online-softmax merge. Within a CTA four warps stream every
+// kernel joins by the online-softmax merge (its start is programmatic: it is set
+// up while the first one ends). Within a CTA four warps stream every
 // fourth tile through buffers of their own (cp.async, 16-byte chunks swizzled for
 // ldmatrix) and their states meet in shared memory.
 // With a window the tiles are those of the first `sink` keys, then those of the
@@ -67,10 +68,9 @@ constexpr int kQ4Warps = 4;
 constexpr int kQ4Tile = 32;    // keys per warp step
 constexpr int kQ4Stages = 2;   // per-warp tile buffers
 constexpr int kQ4MaxRows = 16;
-#ifndef SEGC
-#define SEGC 4
-#endif
-constexpr int kQ4SegmentCost = SEGC;
+// What a segment's start and end cost beside its tiles (61 ragged sequences of up to 15001
+// keys: 0: 151 us, 4: 140, 8: 131, 16: 124, 24: 127)
+constexpr int kQ4SegmentCost = 16;
 constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
 constexpr uint32_t kQ4Tiny = 0x12801280u;  // bf16 2^-90, twice: smaller V scales count as this,
@@ -129,10 +129,9 @@ struct Q4Cfg {
   static constexpr int kStage = 2 * kCodes + 2 * kScales;  // K, V codes, K, V scales
   static constexpr int kWarp = kQ4Stages * kStage;
   static constexpr int kState = 8 * NT * (2 + D) * 4;      // a warp's m, l, O at the end
-  static constexpr int kArea = kWarp > kState ? kWarp : kState;
   static constexpr int kQ = NT * G * 512;                  // q fragments, 16 bytes per lane
   static constexpr int kOff = NT * G * 64;                 // the scores' offsets, 16 bytes per t
-  static constexpr int kSmem = kQ4Warps * kArea + kQ + kOff + NT * 8 * 4;
+  static constexpr int kSmem = kQ4Warps * (kWarp + kState) + kQ + kOff + NT * 8 * 4;
   // Rows of codes are D / 2 bytes; chunk c (16 bytes) of row r stands at place
   // c ^ swz(r), so that the 8 rows of an ldmatrix matrix hit distinct banks.
   static __device__ __forceinline__ int swz(int row) {
@@ -140,10 +139,13 @@ struct Q4Cfg {
   }
 };
 
-// CTAs per SM that the registers are cut to.
+// CTAs per SM that the registers are cut to. What is measured is issue, not
+// latency: one more CTA at fewer registers spills and is slower (16 x 32768 keys,
+// D = 128: 123 us, with four 134; one product of 16 query rows: 102 with two, 106 with three;
+// D = 64: 80 with four, 86 with five).
 template <int D, int NT>
 constexpr int q4_per_sm() {
-  return D == 128 ? (NT == 1 ? 4 : 2) : (NT == 1 ? 5 : 3);
+  return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
 }
 
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, uint32_t bytes) {
@@ -231,435 +233,27 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) {  // i = 0 or 1
   return __uint_as_float(i ? w & 0xffff0000u : w << 16);
 }
 
-// Tiles [v_begin, v_end) of one pair, by the whole CTA: into the partial slot,
-// or (slot < 0: they are all of the pair's) into o and lse.
-template <int D, int NT, int SCORE>
-__device__ __forceinline__ void decode_segment(const Q4Problem& p, uint8_t* smem, int b, int hkv,
-                                               const Q4Range& rg, int v_begin, int v_end,
-                                               long long slot) {
-  using C = Q4Cfg<D, NT>;
-  constexpr int G = C::G;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;  // fragment coordinates
-  const int group = p.Hq / p.Hkv;
-  const int R = group * p.Sq;
-  const size_t row0 = (size_t)(b * p.Hq + hkv * group) * p.Sq;
-  const size_t total_rows = (size_t)p.B * p.Hq * p.Sq;
-  const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
-  const int len = rg.len, sink_tiles = rg.sink_tiles, win_tile = rg.win_tile;
-  const int first_pos = len - p.Sq;  // absolute position of query row 0
-
-  // The warp's tiles: v_begin + warp, every kQ4Warps-th. Their pages are looked
-  // up 16 tiles at a time, lane 2i + h the page of tile i's 16-key half h (or
-  // -1), one batch ahead.
-  const Q4Layout L{D, 1 << p.shift};
-  const uint32_t area = smem_u32(smem) + warp * C::kArea;
-  const uint8_t* area_ptr = smem + warp * C::kArea;
-  uint4* qs = reinterpret_cast<uint4*>(smem + kQ4Warps * C::kArea);   // [NT][G][32 lanes]
-  float4* offs = reinterpret_cast<float4*>(smem + kQ4Warps * C::kArea + C::kQ);  // [NT][G][4]
-  float* units = reinterpret_cast<float*>(smem + kQ4Warps * C::kArea + C::kQ + C::kOff);  // [NT * 8]
-  const int v_first = v_begin + warp;
-  const int n_tiles = v_first < v_end ? (v_end - v_first + kQ4Warps - 1) / kQ4Warps : 0;
-  auto key_of = [&](int i) {  // first key of the warp's tile i
-    const int v = v_first + i * kQ4Warps;
-    return (v < sink_tiles ? v : v - sink_tiles + win_tile) * kQ4Tile;
-  };
-  auto look_up = [&](int i0) -> int {
-    const int i = i0 + (lane >> 1);
-    if (i >= n_tiles) return -1;
-    const int lp = (key_of(i) + 16 * (lane & 1)) >> p.shift;
-    if (lp >= p.pages_per_seq) return -1;
-    const int pg = p.table[(size_t)b * p.pages_per_seq + lp];
-    return pg >= 0 && pg < p.num_pages ? pg : -1;
-  };
-  int pages = -1, pages_next = look_up(0);
-  const uint8_t* head_pool = p.pool + (size_t)hkv * L.bytes() + lane * 16;
-  const uint32_t page_stride = (uint32_t)p.Hkv * L.bytes();
-  constexpr int kScaleChunks = C::kScales / 32;  // 16-byte chunks of K (or V) scales per half
-  // lane's chunk of the scales: half, K or V, place
-  const bool sc_half = lane / kScaleChunks & 1;
-  const int sc_src = (lane / (2 * kScaleChunks) ? L.v_scales() : L.k_scales()) +
-                     (lane % kScaleChunks) * 16 - lane * 16;
-  const uint32_t sc_dst = 2 * C::kCodes + (lane / kScaleChunks) % 2 * (C::kScales / 2) +
-                          lane / (2 * kScaleChunks) * C::kScales + lane % kScaleChunks * 16;
-  auto load_tile = [&](int i) {  // into buffer i % kQ4Stages; called with i = 0, 1, 2, ...
-    if ((i & 15) == 0) {
-      pages = pages_next;
-      pages_next = look_up(i + 16);
-    }
-    const uint32_t dst = area + (i & (kQ4Stages - 1)) * C::kStage;
-    const int key0 = key_of(i);
-    const uint32_t lane_dst = dst + lane / G * C::kRow + (lane % G ^ C::swz(lane / G)) * 16;
-    auto half_codes = [&](int h, const uint8_t* k, uint32_t bytes) {  // 16 keys, K and V
-      const uint8_t* v = k + L.v_codes();
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint32_t d = lane_dst + (16 * h + c * (32 / G)) * C::kRow;
-        cp_async16z(d, k + c * 512, bytes);
-        cp_async16z(d + C::kCodes, v + c * 512, bytes);
-      }
-    };
-    const int pg0 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15));
-    const uint8_t* rec0 = head_pool + (size_t)(uint32_t)max(pg0, 0) * page_stride;
-    const int in0 = key0 & (L.page - 1);
-    const uint32_t bytes0 = pg0 >= 0 ? 16u : 0u;
-    const uint8_t* k0 = rec0 + in0 * L.code_row();
-    half_codes(0, k0, bytes0);
-    const uint8_t* sc = rec0 + in0 * L.scale_row() + sc_src;
-    uint32_t sc_bytes = bytes0;
-    if (L.page >= kQ4Tile) {  // the whole tile lies in one page
-      half_codes(1, k0 + 16 * L.code_row(), bytes0);
-      if (sc_half) sc += 16 * L.scale_row();
-    } else {
-      const int pg1 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + 1);
-      const uint8_t* rec1 = head_pool + (size_t)(uint32_t)max(pg1, 0) * page_stride;
-      half_codes(1, rec1, pg1 >= 0 ? 16u : 0u);
-      if (sc_half) {
-        sc = rec1 + sc_src;
-        sc_bytes = pg1 >= 0 ? 16u : 0u;
-      }
-    }
-    if (lane < 4 * kScaleChunks) cp_async16z(dst + sc_dst, sc, sc_bytes);
-    cp_async_commit();
-  };
-
-  if (n_tiles > 0) load_tile(0);
-  if (n_tiles > 1) load_tile(1);
-
-  // Meanwhile warp 0 prepares q^T's fragments (B operand) in shared memory, in
-  // fp16: a row is scaled by a power of two that brings its largest channel to
-  // [2^14, 2^15), so bf16's 8 bits are exact (channels 2^28 times smaller lose
-  // bits below 2^-39 of the largest). Channel order of a lane's 8 per group: pairs
-  // (0, 4), (1, 5) | (2, 6), (3, 7). Rows past R are 0.
-  if (warp == 0) {
-    const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int r = nt * 8 + g;
-      uint4 x[G];
-      float big = 0.0f;
-      bool odd = false;  // a NaN, which fmaxf passes over
-#pragma unroll
-      for (int a = 0; a < G; ++a) {
-        x[a] = make_uint4(0, 0, 0, 0);
-        if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
-          x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
-        const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          for (int e = 0; e < 2; ++e) {
-            big = fmaxf(big, fabsf(scale_of(u[i], e)));
-            odd = odd || isnan(scale_of(u[i], e));
-          }
-      }
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      odd = __ballot_sync(0xffffffffu, odd) & (0xfu << (lane & 28));
-      const bool fine = big < INFINITY && !odd;
-      const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
-      const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
-      // scores per product, log2; a row with an infinity or NaN scores NaN
-      if (t == 0) units[r] = fine ? exp2f((float)(ex - 14)) * p.scale2 : NAN;
-#pragma unroll
-      for (int a = 0; a < G; ++a) {
-        const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
-        float c[8], sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = fine ? scale_of(u[i / 2], i & 1) * up : 0.0f;
-        qs[(nt * G + a) * 32 + lane] = make_uint4(pack_f16x2(c[0], c[4]), pack_f16x2(c[1], c[5]),
-                                                  pack_f16x2(c[2], c[6]), pack_f16x2(c[3], c[7]));
-        // -72 sum(q) over the nibbles that keep their offset: per lane channels
-        // 1, 3, 5, 7; of row g, stored for the lane t that holds columns 2t, 2t + 1
-        sum = c[1] + c[3] + c[5] + c[7];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (t < 2) reinterpret_cast<float*>(offs + (nt * G + a) * 4 + g / 2)[g % 2 + 2 * t] = -72.0f * sum;
-      }
-    }
-  }
-  __syncthreads();
-
-  // the lane's query rows (columns 2t, 2t + 1 of each 8)
-  float unit[NT][2], slope2[NT][2];
-  int pos[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * t + e;
-      unit[nt][e] = units[r];
-      const int hg = r < R ? r / p.Sq : 0;
-      pos[nt][e] = first_pos + (r < R ? r % p.Sq : 0);
-      const int h = hkv * group + hg;
-      slope2[nt][e] =
-          (SCORE & 1) ? (p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq))) * kLog2e
-                      : 0.0f;
-    }
-
-  float o[G][2][NT][4];  // [group][channel pair] x (channel, row) of each 8 rows
-#pragma unroll
-  for (int a = 0; a < G; ++a)
-#pragma unroll
-    for (int jp = 0; jp < 2; ++jp)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        o[a][jp][nt][0] = o[a][jp][nt][1] = o[a][jp][nt][2] = o[a][jp][nt][3] = 0.0f;
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.0f;
-  }
-
-  // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
-  auto process = [&](const uint32_t stage_off, const int key0, auto mask_tag) {
-    constexpr bool kMask = decltype(mask_tag)::value;
-    // an ldmatrix row is a key: the lane's, with the place of chunk 0
-    const uint32_t rows = area + stage_off + lane * C::kRow + C::swz(lane) * 16;
-    const uint8_t* scales = area_ptr + stage_off + 2 * C::kCodes;
-    float x[2][NT][4];
-    uint32_t sk[4][G / 2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load_scales<G>(scales + (8 * i + g) * 2 * G, sk[i]);
-#pragma unroll
-    for (int a = 0; a < G; ++a) {
-      uint32_t w[4];  // the lane's 8 channels of group a, for keys g, g + 8, g + 16, g + 24
-      ldsm4(rows ^ (a * 16), w);
-      uint4 qf[NT];
-      float4 off[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        qf[nt] = qs[(nt * G + a) * 32 + lane];
-        off[nt] = offs[(nt * G + a) * 4 + t];
-      }
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t f[2][4];
-        nibble_pairs<false>(w[2 * mt], f[0]);
-        nibble_pairs<false>(w[2 * mt + 1], f[1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[4] = {off[nt].x, off[nt].y, off[nt].z, off[nt].w};
-          mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qf[nt].x, qf[nt].y);
-          mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qf[nt].z, qf[nt].w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s = scale_of(sk[2 * mt + (e >> 1)][a / 2], a & 1);
-            x[mt][nt][e] = a == 0 ? s * d[e] : fmaf(s, d[e], x[mt][nt][e]);
-          }
-        }
-      }
-    }
-    uint32_t sv[2][2][G / 2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_scales<G>(scales + C::kScales + (8 * i + g) * 2 * G, sv[i >> 1][i & 1]);
-    // score modification and mask. Without a modification the scores stay in
-    // the products' units and `unit` enters with the exponent.
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = key0 + 16 * mt + 8 * (e >> 1) + g, i = pos[nt][e & 1];
-          float s = x[mt][nt][e];
-          if constexpr (SCORE != 0) s *= unit[nt][e & 1];
-          if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
-          // cap tanh(s / cap) as cap - 2 cap / (1 + e^(2 s / cap)): off by at
-          // most 2^-22 cap, and exact at both ends
-          if constexpr ((SCORE & 2) != 0)
-            s = fmaf(-p.softcap2, __fdividef(2.0f, 1.0f + ex2_approx(s * p.softcap_e)), p.softcap2);
-          if constexpr (kMask) {
-            bool keep = j < len && i >= 0;
-            if (causal) keep = keep && j <= i;
-            if (windowed) keep = keep && (i - j < p.window || j < p.sink);
-            s = keep ? s : -INFINITY;
-          }
-          x[mt][nt][e] = s;
-        }
-    auto log2_of = [&](float s, int nt, int e) { return SCORE ? s : s * unit[nt][e]; };
-    // The reference follows keys that pass its bound. First a quick bound: the
-    // lane's largest score with its largest V scale, rounded up to a power of
-    // two (a negative or NaN scale counts as huge).
-    uint32_t sm = kQ4Tiny;
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < G / 2; ++i) sm = __vmaxu2(sm, sv[mt][e][i]);
-    sm = max(sm, sm << 16);
-    const float lsm = (float)(int)(sm >> 23) - 126.0f;
-    bool over = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float y = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
-        over = over || log2_of(y, nt, e) + lsm > m[nt][e] + kQ4Head;
-      }
-    if (__any_sync(0xffffffffu, over)) {
-      float lsv[2][2];
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float big = __uint_as_float(kQ4Tiny & 0xffff0000u);
-#pragma unroll
-          for (int a = 0; a < G; ++a) big = fmaxf(big, fabsf(scale_of(sv[mt][e][a / 2], a & 1)));
-          lsv[mt][e] = __log2f(big);
-        }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float y = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y = fmaxf(y, log2_of(x[k >> 1][nt][e + 2 * (k & 1)], nt, e) + lsv[k >> 1][k & 1]);
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-          // each row by itself: its result does not depend on the others'
-          const float m_new = y > m[nt][e] + kQ4Head ? y - kQ4Start : m[nt][e];
-          const float c = m_new == -INFINITY ? 1.0f : ex2_approx(m[nt][e] - m_new);  // -inf -> 0
-          m[nt][e] = m_new;
-          l[nt][e] *= c;
-#pragma unroll
-          for (int a = 0; a < G; ++a)
-#pragma unroll
-            for (int jp = 0; jp < 2; ++jp) {
-              o[a][jp][nt][e] *= c;
-              o[a][jp][nt][e + 2] *= c;
-            }
-        }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& s = x[k >> 1][nt][e + 2 * (k & 1)];
-          s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
-          l[nt][e] += s;
-        }
-      }
-    // O^T += V^T P^T
-#pragma unroll
-    for (int a = 0; a < G; ++a) {
-      uint32_t w[4];  // 4 channels of group a for key pairs 2t, 2t + 1 of each 8 keys
-      ldsm4_t((rows ^ (a * 16)) + C::kCodes, w);
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint32_t f[2][4];
-        nibble_pairs<true>(w[2 * mt], f[0]);
-        nibble_pairs<true>(w[2 * mt + 1], f[1]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float pv[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
-            // a masked key adds nothing, whatever its scale holds
-            if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
-          }
-          const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
-          const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
-#pragma unroll
-          for (int jp = 0; jp < 2; ++jp)
-            mma_f16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp], f[1][2 * jp + 1],
-                    b0, b1);
-        }
-      }
-    }
-  };
-
-  for (int i = 0; i < n_tiles; ++i) {
-    if (i + 1 < n_tiles) cp_async_wait<1>();
-    else cp_async_wait<0>();
-    __syncwarp();
-    const int key0 = key_of(i), key_end = key0 + kQ4Tile;
-    const bool whole = key_end <= len && first_pos >= 0 && (!causal || key_end - 1 <= first_pos) &&
-                       (!windowed || len - 1 - key0 < p.window || key_end <= p.sink);
-    const uint32_t stage_off = (i & (kQ4Stages - 1)) * C::kStage;
-    if (whole) process(stage_off, key0, std::false_type{});
-    else process(stage_off, key0, std::true_type{});
-    __syncwarp();
-    if (i + 2 < n_tiles) load_tile(i + 2);
-  }
-  cp_async_wait<0>();
-  __syncwarp();
-
-  // the warps' states meet in shared memory: m, l (8 NT each), O [8 NT][D]
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
-      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
-      l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
-    }
-  constexpr int kR = 8 * NT;
-  float* wm = reinterpret_cast<float*>(smem + warp * C::kArea);
-  float* wl = wm + kR;
-  float* wo = wl + kR;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (g == 0) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        wm[nt * 8 + 2 * t + e] = m[nt][e];
-        wl[nt * 8 + 2 * t + e] = l[nt][e];
-      }
-    }
-#pragma unroll
-    for (int a = 0; a < G; ++a)
-#pragma unroll
-      for (int jp = 0; jp < 2; ++jp)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float2*>(wo + (nt * 8 + 2 * t + e) * D + 32 * a + 4 * g + 2 * jp) =
-              make_float2(o[a][jp][nt][e], o[a][jp][nt][e + 2]);
-  }
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < R * D; idx += kQ4Threads) {
-    const int r = idx / D, c = idx % D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kQ4Warps; ++w)
-      M = fmaxf(M, reinterpret_cast<const float*>(smem + w * C::kArea)[r]);
-    float Ls = 0.0f, acc = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kQ4Warps; ++w) {
-      const float* st = reinterpret_cast<const float*>(smem + w * C::kArea);
-      const float wt = M != -INFINITY ? ex2_approx(st[r] - M) : 1.0f;  // -inf -> 0
-      Ls += wt * st[kR + r];
-      acc += wt * st[2 * kR + r * D + c];
-    }
-    // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
-    const float out = Ls == 0.0f ? 0.0f : acc / Ls;
-    const float lse2 = Ls == 0.0f ? -INFINITY : M + __log2f(Ls);
-    if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
-    if (slot >= 0) {
-      p.ws_o[((size_t)slot * R + r) * D + c] = out;
-      if (c == 0) p.ws_lse[(size_t)slot * R + r] = lse2;
-    } else {
-      static_cast<__nv_bfloat16*>(p.o)[(row0 + r) * D + c] = __float2bfloat16_rn(out);
-      if (c == 0) p.lse[row0 + r] = lse2 * kLn2;
-    }
-  }
-  __syncthreads();  // the next segment's tiles overwrite the states
-}
+// A run of tiles of one pair: the CTA's share of it.
+struct Q4Segment {
+  int b, hkv;
+  int len, win_tile, sink_tiles;
+  int v_first, n_tiles;  // this warp's first tile and its count (every kQ4Warps-th)
+  long long slot;        // partial result, or -1: all of the pair's tiles
+};
 
 template <int D, int NT, int SCORE>
 __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     decode_q4_kernel(const Q4Problem p) {
+  using C = Q4Cfg<D, NT>;
+  constexpr int G = C::G;
   extern __shared__ __align__(128) uint8_t smem[];
-  const int lane = threadIdx.x & 31;
-  launch_dependents();  // the merge may be set up; it waits for this grid's end
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;  // fragment coordinates
+  const int group = p.Hq / p.Hkv;
+  const int R = group * p.Sq;
+  [[maybe_unused]] const size_t total_rows = (size_t)p.B * p.Hq * p.Sq;
+  const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+  early_start();
 
   // this CTA's first pair and tiles [lo, hi) of all
   int b = blockIdx.x / p.Hkv, hkv = blockIdx.x % p.Hkv;
@@ -699,34 +293,477 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     hkv = 0;
   }
 
-  for (; b < p.B; ++b, hkv = 0) {
-    const Q4Range rg = q4_range(p, b);
-    const int cost = rg.cost();
-    if (p.ws_meta) {
-      if (seq_start >= hi && !(last_cta && cost == 0)) break;
-      if (cost > 0) hkv = max(0, (int)((lo - seq_start) / cost));
-    }
-    for (; hkv < p.Hkv; ++hkv) {
-      int v_begin = 0, v_end = rg.tiles;
-      const int pair = b * p.Hkv + hkv;
-      if (p.ws_meta && cost > 0) {
-        // the pair's tiles follow its own cost
-        const long long start = seq_start + (long long)hkv * cost + kQ4SegmentCost;
-        if (start >= hi) break;
-        v_begin = (int)max(0ll, lo - start);
-        v_end = (int)min((long long)rg.tiles, hi - start);
-        if (v_begin >= rg.tiles) continue;
+  // The CTA's next segment, false at the end. Sequences without tiles on the
+  // way get their empty rows.
+  Q4Range rg;
+  int rg_of = -1;
+  auto next_segment = [&](Q4Segment& sg) -> bool {
+    for (; b < p.B; ++b, hkv = 0) {
+      if (rg_of != b) {
+        rg = q4_range(p, b);
+        rg_of = b;
+        const int cost = rg.cost();
+        if (p.ws_meta && cost > 0) hkv = max(0, (int)((lo - seq_start) / cost));
       }
-      const bool cut = v_begin > 0 || v_end < rg.tiles;
-      if (p.ws_meta && threadIdx.x == 0) {
-        if (v_begin == 0) p.ws_meta[pair].x = cut ? (int)blockIdx.x : -1;
-        if (v_end == rg.tiles) p.ws_meta[pair].y = (int)blockIdx.x;
+      const int cost = rg.cost();
+      if (p.ws_meta && seq_start >= hi && !(last_cta && cost == 0)) return false;
+      if (p.ws_meta && cost == 0) {
+        const size_t row0 = (size_t)b * p.Hq * p.Sq;
+        for (int i = threadIdx.x; i < p.Hq * p.Sq * (D / 2); i += kQ4Threads)
+          if (MATTN_IN_BOUNDS(kSiteQ4Out, row0 + i / (D / 2), total_rows))
+            static_cast<uint32_t*>(p.o)[row0 * (D / 2) + i] = 0u;
+        for (int i = threadIdx.x; i < p.Hq * p.Sq; i += kQ4Threads) p.lse[row0 + i] = -INFINITY;
+        for (int i = threadIdx.x; i < p.Hkv; i += kQ4Threads)
+          p.ws_meta[(size_t)b * p.Hkv + i].x = -1;
+        continue;
       }
-      decode_segment<D, NT, SCORE>(p, smem, b, hkv, rg, v_begin, v_end,
-                                   cut ? (long long)blockIdx.x + pair : -1);
-      if (!p.ws_meta) return;
+      for (; hkv < p.Hkv; ++hkv) {
+        int v_begin = 0, v_end = rg.tiles;
+        if (p.ws_meta) {
+          // the pair's tiles follow its own cost
+          const long long start = seq_start + (long long)hkv * cost + kQ4SegmentCost;
+          if (start >= hi) return false;
+          v_begin = (int)max(0ll, lo - start);
+          v_end = (int)min((long long)rg.tiles, hi - start);
+          if (v_begin >= rg.tiles) continue;
+        }
+        const bool cut = v_begin > 0 || v_end < rg.tiles;
+        const int pair = b * p.Hkv + hkv;
+        if (p.ws_meta && threadIdx.x == 0) {
+          if (v_begin == 0) p.ws_meta[pair].x = cut ? (int)blockIdx.x : -1;
+          if (v_end == rg.tiles) p.ws_meta[pair].y = (int)blockIdx.x;
+        }
+        sg.b = b;
+        sg.hkv = hkv;
+        sg.len = rg.len;
+        sg.win_tile = rg.win_tile;
+        sg.sink_tiles = rg.sink_tiles;
+        sg.v_first = v_begin + warp;
+        sg.n_tiles = sg.v_first < v_end ? (v_end - sg.v_first + kQ4Warps - 1) / kQ4Warps : 0;
+        sg.slot = cut ? (long long)blockIdx.x + pair : -1;
+        ++hkv;
+        if (!p.ws_meta) b = p.B;  // one pair per CTA
+        return true;
+      }
+      seq_start += (long long)cost * p.Hkv;
     }
-    seq_start += (long long)cost * p.Hkv;
+    return false;
+  };
+
+  // A segment's tiles through the warp's buffers. Their pages are looked up 16
+  // tiles at a time, lane 2i + h the page of tile i's 16-key half h (or -1), one
+  // batch ahead.
+  const Q4Layout L{D, 1 << p.shift};
+  const uint32_t area = smem_u32(smem) + warp * C::kWarp;
+  const uint8_t* area_ptr = smem + warp * C::kWarp;
+  float* states = reinterpret_cast<float*>(smem + kQ4Warps * C::kWarp);
+  uint4* qs = reinterpret_cast<uint4*>(smem + kQ4Warps * (C::kWarp + C::kState));  // [NT][G][32 lanes]
+  float4* offs = reinterpret_cast<float4*>(qs + C::kQ / 16);                        // [NT][G][4]
+  float* units = reinterpret_cast<float*>(offs + C::kOff / 16);                     // [NT * 8]
+  auto key_of = [&](const Q4Segment& sg, int i) {  // first key of the warp's tile i
+    const int v = sg.v_first + i * kQ4Warps;
+    return (v < sg.sink_tiles ? v : v - sg.sink_tiles + sg.win_tile) * kQ4Tile;
+  };
+  auto look_up = [&](const Q4Segment& sg, int i0) -> int {
+    const int i = i0 + (lane >> 1);
+    if (i >= sg.n_tiles) return -1;
+    const int lp = (key_of(sg, i) + 16 * (lane & 1)) >> p.shift;
+    if (lp >= p.pages_per_seq) return -1;
+    const int pg = p.table[(size_t)sg.b * p.pages_per_seq + lp];
+    return pg >= 0 && pg < p.num_pages ? pg : -1;
+  };
+  int pages = -1, pages_next = -1;
+  const uint32_t page_stride = (uint32_t)p.Hkv * L.bytes();
+  constexpr int kScaleChunks = C::kScales / 32;  // 16-byte chunks of K (or V) scales per half
+  // lane's chunk of the scales: half, K or V, place
+  const bool sc_half = lane / kScaleChunks & 1;
+  const int sc_src = (lane / (2 * kScaleChunks) ? L.v_scales() : L.k_scales()) +
+                     (lane % kScaleChunks) * 16 - lane * 16;
+  const uint32_t sc_dst = 2 * C::kCodes + (lane / kScaleChunks) % 2 * (C::kScales / 2) +
+                          lane / (2 * kScaleChunks) * C::kScales + lane % kScaleChunks * 16;
+  auto load_tile = [&](const Q4Segment& sg, int i) {  // into buffer i % kQ4Stages; i = 0, 1, 2, ...
+    if ((i & 15) == 0) {
+      pages = pages_next;
+      pages_next = look_up(sg, i + 16);
+    }
+    const uint32_t dst = area + (i & (kQ4Stages - 1)) * C::kStage;
+    const int key0 = key_of(sg, i);
+    const uint8_t* head_pool = p.pool + (size_t)sg.hkv * L.bytes() + lane * 16;
+    const uint32_t lane_dst = dst + lane / G * C::kRow + (lane % G ^ C::swz(lane / G)) * 16;
+    auto half_codes = [&](int h, const uint8_t* k, uint32_t bytes) {  // 16 keys, K and V
+      const uint8_t* v = k + L.v_codes();
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint32_t d = lane_dst + (16 * h + c * (32 / G)) * C::kRow;
+        cp_async16z(d, k + c * 512, bytes);
+        cp_async16z(d + C::kCodes, v + c * 512, bytes);
+      }
+    };
+    const int pg0 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15));
+    const uint8_t* rec0 = head_pool + (size_t)(uint32_t)max(pg0, 0) * page_stride;
+    const int in0 = key0 & (L.page - 1);
+    const uint32_t bytes0 = pg0 >= 0 ? 16u : 0u;
+    const uint8_t* k0 = rec0 + in0 * L.code_row();
+    half_codes(0, k0, bytes0);
+    const uint8_t* sc = rec0 + in0 * L.scale_row() + sc_src;
+    uint32_t sc_bytes = bytes0;
+    if (L.page >= kQ4Tile) {  // the whole tile lies in one page
+      half_codes(1, k0 + 16 * L.code_row(), bytes0);
+      if (sc_half) sc += 16 * L.scale_row();
+    } else {
+      const int pg1 = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + 1);
+      const uint8_t* rec1 = head_pool + (size_t)(uint32_t)max(pg1, 0) * page_stride;
+      half_codes(1, rec1, pg1 >= 0 ? 16u : 0u);
+      if (sc_half) {
+        sc = rec1 + sc_src;
+        sc_bytes = pg1 >= 0 ? 16u : 0u;
+      }
+    }
+    if (lane < 4 * kScaleChunks) cp_async16z(dst + sc_dst, sc, sc_bytes);
+    cp_async_commit();
+  };
+  auto start_loads = [&](const Q4Segment& sg) {
+    pages_next = look_up(sg, 0);
+    if (sg.n_tiles > 0) load_tile(sg, 0);
+    if (sg.n_tiles > 1) load_tile(sg, 1);
+  };
+
+  Q4Segment cur;
+  if (!next_segment(cur)) return;
+  start_loads(cur);
+  for (;;) {
+    const int len = cur.len, first_pos = len - p.Sq;  // absolute position of query row 0
+    const size_t row0 = (size_t)(cur.b * p.Hq + cur.hkv * group) * p.Sq;
+
+    // Meanwhile warp 0 prepares q^T's fragments (B operand) in shared memory, in
+    // fp16: a row is scaled by a power of two that brings its largest channel to
+    // [2^14, 2^15), so bf16's 8 bits are exact (channels 2^28 times smaller lose
+    // bits below 2^-39 of the largest). Channel order of a lane's 8 per group: pairs
+    // (0, 4), (1, 5) | (2, 6), (3, 7). Rows past R are 0.
+    if (warp == 0) {
+      const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g;
+        uint4 x[G];
+        float big = 0.0f;
+        bool odd = false;  // a NaN, which fmaxf passes over
+#pragma unroll
+        for (int a = 0; a < G; ++a) {
+          x[a] = make_uint4(0, 0, 0, 0);
+          if (r < R && MATTN_IN_BOUNDS(kSiteQ4Q, row0 + r, total_rows))
+            x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
+          const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 2; ++e) {
+              big = fmaxf(big, fabsf(scale_of(u[i], e)));
+              odd = odd || isnan(scale_of(u[i], e));
+            }
+        }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        odd = __ballot_sync(0xffffffffu, odd) & (0xfu << (lane & 28));
+        const bool fine = big < INFINITY && !odd;
+        const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
+        const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        // scores per product, log2; a row with an infinity or NaN scores NaN
+        if (t == 0) units[r] = fine ? exp2f((float)(ex - 14)) * p.scale2 : NAN;
+#pragma unroll
+        for (int a = 0; a < G; ++a) {
+          const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+          float c[8], sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) c[i] = fine ? scale_of(u[i / 2], i & 1) * up : 0.0f;
+          qs[(nt * G + a) * 32 + lane] = make_uint4(pack_f16x2(c[0], c[4]), pack_f16x2(c[1], c[5]),
+                                                    pack_f16x2(c[2], c[6]), pack_f16x2(c[3], c[7]));
+          // -72 sum(q) over the nibbles that keep their offset: per lane channels
+          // 1, 3, 5, 7; of row g, stored for the lane t that holds columns 2t, 2t + 1
+          sum = c[1] + c[3] + c[5] + c[7];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if (t < 2) reinterpret_cast<float*>(offs + (nt * G + a) * 4 + g / 2)[g % 2 + 2 * t] = -72.0f * sum;
+        }
+      }
+    }
+    __syncthreads();
+
+    // the lane's query rows (columns 2t, 2t + 1 of each 8)
+    float unit[NT][2], slope2[NT][2];
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+        unit[nt][e] = units[r];
+        const int hg = r < R ? r / p.Sq : 0;
+        pos[nt][e] = first_pos + (r < R ? r % p.Sq : 0);
+        const int h = cur.hkv * group + hg;
+        slope2[nt][e] =
+            (SCORE & 1) ? (p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq))) * kLog2e
+                        : 0.0f;
+      }
+
+    float o[G][2][NT][4];  // [group][channel pair] x (channel, row) of each 8 rows
+#pragma unroll
+    for (int a = 0; a < G; ++a)
+#pragma unroll
+      for (int jp = 0; jp < 2; ++jp)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          o[a][jp][nt][0] = o[a][jp][nt][1] = o[a][jp][nt][2] = o[a][jp][nt][3] = 0.0f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+
+    // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
+    auto process = [&](const uint32_t stage_off, const int key0, auto mask_tag) {
+      constexpr bool kMask = decltype(mask_tag)::value;
+      // an ldmatrix row is a key: the lane's, with the place of chunk 0
+      const uint32_t rows = area + stage_off + lane * C::kRow + C::swz(lane) * 16;
+      const uint8_t* scales = area_ptr + stage_off + 2 * C::kCodes;
+      float x[2][NT][4];
+      uint32_t sk[4][G / 2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) load_scales<G>(scales + (8 * i + g) * 2 * G, sk[i]);
+#pragma unroll
+      for (int a = 0; a < G; ++a) {
+        uint32_t w[4];  // the lane's 8 channels of group a, for keys g, g + 8, g + 16, g + 24
+        ldsm4(rows ^ (a * 16), w);
+        uint4 qf[NT];
+        float4 off[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          qf[nt] = qs[(nt * G + a) * 32 + lane];
+          off[nt] = offs[(nt * G + a) * 4 + t];
+        }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t f[2][4];
+          nibble_pairs<false>(w[2 * mt], f[0]);
+          nibble_pairs<false>(w[2 * mt + 1], f[1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float d[4] = {off[nt].x, off[nt].y, off[nt].z, off[nt].w};
+            mma_f16(d, f[0][0], f[1][0], f[0][1], f[1][1], qf[nt].x, qf[nt].y);
+            mma_f16(d, f[0][2], f[1][2], f[0][3], f[1][3], qf[nt].z, qf[nt].w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float s = scale_of(sk[2 * mt + (e >> 1)][a / 2], a & 1);
+              x[mt][nt][e] = a == 0 ? s * d[e] : fmaf(s, d[e], x[mt][nt][e]);
+            }
+          }
+        }
+      }
+      uint32_t sv[2][2][G / 2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        load_scales<G>(scales + C::kScales + (8 * i + g) * 2 * G, sv[i >> 1][i & 1]);
+      // score modification and mask. Without a modification the scores stay in
+      // the products' units and `unit` enters with the exponent.
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = key0 + 16 * mt + 8 * (e >> 1) + g, i = pos[nt][e & 1];
+            float s = x[mt][nt][e];
+            if constexpr (SCORE != 0) s *= unit[nt][e & 1];
+            if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
+            // cap tanh(s / cap) as cap - 2 cap / (1 + e^(2 s / cap)): off by at
+            // most 2^-22 cap, and exact at both ends
+            if constexpr ((SCORE & 2) != 0)
+              s = fmaf(-p.softcap2, __fdividef(2.0f, 1.0f + ex2_approx(s * p.softcap_e)), p.softcap2);
+            if constexpr (kMask) {
+              bool keep = j < len && i >= 0;
+              if (causal) keep = keep && j <= i;
+              if (windowed) keep = keep && (i - j < p.window || j < p.sink);
+              s = keep ? s : -INFINITY;
+            }
+            x[mt][nt][e] = s;
+          }
+      auto log2_of = [&](float s, int nt, int e) { return SCORE ? s : s * unit[nt][e]; };
+      // The reference follows keys that pass its bound. First a quick bound: the
+      // lane's largest score with its largest V scale, rounded up to a power of
+      // two (a negative or NaN scale counts as huge).
+      uint32_t sm = kQ4Tiny;
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < G / 2; ++i) sm = __vmaxu2(sm, sv[mt][e][i]);
+      sm = max(sm, sm << 16);
+      const float lsm = (float)(int)(sm >> 23) - 126.0f;
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
+          over = over || log2_of(y, nt, e) + lsm > m[nt][e] + kQ4Head;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+        float lsv[2][2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float big = __uint_as_float(kQ4Tiny & 0xffff0000u);
+#pragma unroll
+            for (int a = 0; a < G; ++a) big = fmaxf(big, fabsf(scale_of(sv[mt][e][a / 2], a & 1)));
+            lsv[mt][e] = __log2f(big);
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y = fmaxf(y, log2_of(x[k >> 1][nt][e + 2 * (k & 1)], nt, e) + lsv[k >> 1][k & 1]);
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+            // each row by itself: its result does not depend on the others'
+            const float m_new = y > m[nt][e] + kQ4Head ? y - kQ4Start : m[nt][e];
+            const float c = m_new == -INFINITY ? 1.0f : ex2_approx(m[nt][e] - m_new);  // -inf -> 0
+            m[nt][e] = m_new;
+            l[nt][e] *= c;
+#pragma unroll
+            for (int a = 0; a < G; ++a)
+#pragma unroll
+              for (int jp = 0; jp < 2; ++jp) {
+                o[a][jp][nt][e] *= c;
+                o[a][jp][nt][e + 2] *= c;
+              }
+          }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float& s = x[k >> 1][nt][e + 2 * (k & 1)];
+            s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
+            l[nt][e] += s;
+          }
+        }
+      // O^T += V^T P^T
+#pragma unroll
+      for (int a = 0; a < G; ++a) {
+        uint32_t w[4];  // 4 channels of group a for key pairs 2t, 2t + 1 of each 8 keys
+        ldsm4_t((rows ^ (a * 16)) + C::kCodes, w);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          uint32_t f[2][4];
+          nibble_pairs<true>(w[2 * mt], f[0]);
+          nibble_pairs<true>(w[2 * mt + 1], f[1]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float pv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
+              // a masked key adds nothing, whatever its scale holds
+              if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
+            }
+            const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
+            const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));
+#pragma unroll
+            for (int jp = 0; jp < 2; ++jp)
+              mma_f16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp], f[1][2 * jp + 1],
+                      b0, b1);
+          }
+        }
+      }
+    };
+
+    for (int i = 0; i < cur.n_tiles; ++i) {
+      if (i + 1 < cur.n_tiles) cp_async_wait<1>();
+      else cp_async_wait<0>();
+      __syncwarp();
+      const int key0 = key_of(cur, i), key_end = key0 + kQ4Tile;
+      const bool whole = key_end <= len && first_pos >= 0 && (!causal || key_end - 1 <= first_pos) &&
+                         (!windowed || len - 1 - key0 < p.window || key_end <= p.sink);
+      const uint32_t stage_off = (i & (kQ4Stages - 1)) * C::kStage;
+      if (whole) process(stage_off, key0, std::false_type{});
+      else process(stage_off, key0, std::true_type{});
+      __syncwarp();
+      if (i + 2 < cur.n_tiles) load_tile(cur, i + 2);
+    }
+    // the next segment's first tiles are on their way during this one's end
+    Q4Segment nxt;
+    const bool more = next_segment(nxt);
+    if (more) start_loads(nxt);
+
+    // the warps' states meet in shared memory: m, l (8 NT each), O [8 NT][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], 16);
+      }
+    constexpr int kR = 8 * NT;
+    float* wm = states + warp * (C::kState / 4);
+    float* wl = wm + kR;
+    float* wo = wl + kR;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (g == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          wm[nt * 8 + 2 * t + e] = m[nt][e];
+          wl[nt * 8 + 2 * t + e] = l[nt][e];
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < G; ++a)
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float2*>(wo + (nt * 8 + 2 * t + e) * D + 32 * a + 4 * g + 2 * jp) =
+                make_float2(o[a][jp][nt][e], o[a][jp][nt][e + 2]);
+    }
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < R * D; idx += kQ4Threads) {
+      const int r = idx / D, c = idx % D;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kQ4Warps; ++w)
+        M = fmaxf(M, states[w * (C::kState / 4) + r]);
+      float Ls = 0.0f, acc = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kQ4Warps; ++w) {
+        const float* st = states + w * (C::kState / 4);
+        const float wt = M != -INFINITY ? ex2_approx(st[r] - M) : 1.0f;  // -inf -> 0
+        Ls += wt * st[kR + r];
+        acc += wt * st[2 * kR + r * D + c];
+      }
+      // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
+      const float out = Ls == 0.0f ? 0.0f : acc / Ls;
+      const float lse2 = Ls == 0.0f ? -INFINITY : M + __log2f(Ls);
+      if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
+      if (cur.slot >= 0) {
+        p.ws_o[((size_t)cur.slot * R + r) * D + c] = out;
+        if (c == 0) p.ws_lse[(size_t)cur.slot * R + r] = lse2;
+      } else {
+        static_cast<__nv_bfloat16*>(p.o)[(row0 + r) * D + c] = __float2bfloat16_rn(out);
+        if (c == 0) p.lse[row0 + r] = lse2 * kLn2;
+      }
+    }
+    if (!more) break;
+    cur = nxt;
   }
 }
 
@@ -740,7 +777,7 @@ __global__ void __launch_bounds__(kQ4Threads) q4_merge_kernel(const Q4Problem p)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long rows = (long long)p.B * p.Hq * p.Sq;
   const long long row = (long long)blockIdx.x * (kQ4Warps / W) + warp / W;
-  wait_for_primary();
+  early_start();
   float M = -INFINITY, L = 0.0f, acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -823,20 +860,12 @@ cudaError_t launch_merge(const Q4Problem& p, int ctas, cudaStream_t stream) {
   // One warp per row where a pair is cut into few parts; a whole block where
   // the CTAs are at least eight times the pairs.
   const bool wide = ctas >= 8LL * p.B * p.Hkv;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + kQ4Warps - 1) / kQ4Warps));
-  cfg.blockDim = dim3(kQ4Threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, q4_merge_kernel<D, kQ4Warps>, p)
-              : cudaLaunchKernelEx(&cfg, q4_merge_kernel<D, 1>, p);
+  const unsigned grid = (unsigned)(wide ? rows : (rows + kQ4Warps - 1) / kQ4Warps);
+  return wide ? launch_early(q4_merge_kernel<D, kQ4Warps>, grid, kQ4Threads, 0, stream, p)
+              : launch_early(q4_merge_kernel<D, 1>, grid, kQ4Threads, 0, stream, p);
 }
 
-constexpr int kQ4CtasPerSm = 5;  // most resident CTAs that a call uses
+constexpr int kQ4CtasPerSm = 4;  // most resident CTAs that a call uses
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -885,15 +914,13 @@ cudaError_t launch_typed(Q4Problem& p, long long tiles, void* ws, size_t ws_byte
   while (ctas > 1 && q4_workspace(pairs, ctas, R, D).total > ws_bytes) ctas /= 2;
   const bool split = ws && tiles > kQ4Warps && ctas > 1 && (ctas == want || ctas > pairs);
   if (!split) {
-    decode_q4_kernel<D, NT, SCORE><<<(unsigned)pairs, kQ4Threads, C::kSmem, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(decode_q4_kernel<D, NT, SCORE>, (unsigned)pairs, kQ4Threads, C::kSmem, stream, p);
   }
   const Q4Workspace w = q4_workspace(pairs, ctas, R, D);
   p.ws_meta = static_cast<int2*>(ws);
   p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + w.lse);
   p.ws_o = reinterpret_cast<float*>(static_cast<char*>(ws) + w.o);
-  decode_q4_kernel<D, NT, SCORE><<<ctas, kQ4Threads, C::kSmem, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_early(decode_q4_kernel<D, NT, SCORE>, ctas, kQ4Threads, C::kSmem, stream, p);
   return e != cudaSuccess ? e : launch_merge<D>(p, ctas, stream);
 }
 

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
   };
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LANES;
-  if constexpr (kBwd) launch_dependents();  // the sum over blocks waits for this grid's end
+  early_start();
   const int apart = warp / a.together;       // head item within the group
   const int spread = kRopeWarps / a.together;
   int ch[2];
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 // 32 columns, 32 rows of threads each taking every 32nd partial.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int n, int D, float* dwq,
                                                        float* dwk) {
-  wait_for_primary();
+  early_start();
   __shared__ float sh[32][33];
   const int col = blockIdx.x * 32 + threadIdx.x;  // of 2 D
   float v = 0.0f;
@@ -434,21 +434,11 @@ cudaError_t launch_typed(RopeArgs& a, bool inter, int B, float* const* dw, cudaS
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (attr_err != cudaSuccess) return attr_err;
-  if (inter) norm_rope_kernel<D, kBf16, true, kBwd><<<blocks, kRopeThreads, kSmem, stream>>>(a);
-  else norm_rope_kernel<D, kBf16, false, kBwd><<<blocks, kRopeThreads, kSmem, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      inter ? launch_early(norm_rope_kernel<D, kBf16, true, kBwd>, blocks, kRopeThreads, kSmem, stream, a)
+            : launch_early(norm_rope_kernel<D, kBf16, false, kBwd>, blocks, kRopeThreads, kSmem, stream, a);
   if (e != cudaSuccess || !kBwd || (!dw[0] && !dw[1])) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(32, 32);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_dw_kernel, static_cast<const float*>(a.part), blocks, D,
-                            dw[0], dw[1]);
+  return launch_early(rope_dw_kernel, 2 * D / 32, dim3(32, 32), 0, stream, a.part, blocks, D, dw[0], dw[1]);
 }
 
 template <bool kBwd>

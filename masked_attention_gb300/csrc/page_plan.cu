@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   __shared__ int over;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) over = 0;
+  early_start();
 
   // exclusive scan: a thread sums its run of requests, warps scan the sums
   const int run = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -210,9 +211,8 @@ MATTN_API attn_status attn_page_plan(const int* cached_lens, const int* new_lens
                    shift, seq_lens, cu_new, slots, positions, seq_ids, max_tokens, info};
   const int blocks = std::max(1, std::min(2 * sm_count(),
                                           (max_tokens + kPlanTokens - 1) / kPlanTokens));
-  page_plan_kernel<<<blocks, kPlanThreads, 2 * (B + 1) * sizeof(int),
-                     reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_early(page_plan_kernel, blocks, kPlanThreads, 2 * (B + 1) * sizeof(int),
+                                  reinterpret_cast<cudaStream_t>(stream), a));
 }
 
 namespace mattn {
