@@ -51,7 +51,6 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "cache_q4.cuh"
@@ -166,8 +165,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "r"(addr));
 }
 
-__device__ __forceinline__ int warp_sum(int x) { return __reduce_add_sync(0xffffffffu, x); }
-
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -260,9 +257,30 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
   long long lo = 0, hi = LLONG_MAX, seq_start = 0;
   bool last_cta = false;
   if (p.ws_meta) {
+    // A thread adds up a run of sequences; a scan over the block places the runs.
+    __shared__ long long sums[kQ4Warps];
+    __shared__ long long found_start;
+    __shared__ int found;
+    const int run = (p.B + kQ4Threads - 1) / kQ4Threads;
+    const int r0 = min((int)threadIdx.x * run, p.B), r1 = min(r0 + run, p.B);
+    long long mine = 0;
+    int last_cost = 0;
+    for (int i = r0; i < r1; ++i) mine += last_cost = q4_range(p, i).cost();
+    long long upto = mine;  // inclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    if (threadIdx.x == 0) found = p.B;
+    __syncthreads();
     long long total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32)
-      total += warp_sum(b0 + lane < p.B ? q4_range(p, b0 + lane).cost() : 0);
+#pragma unroll
+    for (int w = 0; w < kQ4Warps; ++w) {
+      if (w < warp) upto += sums[w];
+      total += sums[w];
+    }
     total *= p.Hkv;
     // CTAs that take part: each has a tile for every warp, on the average
     const int ctas = (int)max(1ll, min((long long)gridDim.x, (total + kQ4Warps - 1) / kQ4Warps));
@@ -271,25 +289,22 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     lo = total * blockIdx.x / ctas;
     hi = total * (blockIdx.x + 1) / ctas;
     // the first sequence that ends past lo, or starts there without tiles
-    b = p.B;
-    long long before = 0;
-    for (int b0 = 0; b0 < p.B && b == p.B; b0 += 32) {
-      const int n = b0 + lane < p.B ? q4_range(p, b0 + lane).cost() : 0;
-      int end = n;  // inclusive scan
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, end, d);
-        if (lane >= d) end += v;
+    if (r0 < r1 && (upto * p.Hkv > lo || (upto - last_cost) * p.Hkv >= lo)) atomicMin(&found, r0);
+    __syncthreads();
+    if (r0 < r1 && found == r0) {
+      long long at = upto - mine;
+      int i = r0;
+      for (; i < r1 - 1; ++i) {
+        const int c = q4_range(p, i).cost();
+        if ((at + c) * p.Hkv > lo || at * p.Hkv >= lo) break;
+        at += c;
       }
-      const long long e = before + (long long)end * p.Hkv, s0 = e - (long long)n * p.Hkv;
-      const unsigned hit = __ballot_sync(0xffffffffu, b0 + lane < p.B && (e > lo || s0 >= lo));
-      if (hit) {
-        const int f = __ffs(hit) - 1;
-        b = b0 + f;
-        seq_start = __shfl_sync(0xffffffffu, s0, f);
-      }
-      before = __shfl_sync(0xffffffffu, e, 31);
+      found_start = at * p.Hkv;
+      sums[0] = i;
     }
+    __syncthreads();
+    b = found < p.B ? (int)sums[0] : p.B;
+    seq_start = found_start;
     hkv = 0;
   }
 
@@ -892,18 +907,15 @@ template <int D, int NT, int SCORE>
 cudaError_t launch_typed(Q4Problem& p, long long tiles, void* ws, size_t ws_bytes,
                          cudaStream_t stream) {
   using C = Q4Cfg<D, NT>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int per_sm = 1;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(decode_q4_kernel<D, NT, SCORE>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-          &per_sm, decode_q4_kernel<D, NT, SCORE>, kQ4Threads, C::kSmem);
-    per_sm = std::max(1, std::min(per_sm, kQ4CtasPerSm));
-  });
-  if (attr_err != cudaSuccess) return attr_err;
+  static DeviceOnce ready;
+  const cudaError_t err = ready.allow_smem(decode_q4_kernel<D, NT, SCORE>, C::kSmem);
+  if (err != cudaSuccess) return err;
+  static const int per_sm = [] {
+    int n = 1;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_q4_kernel<D, NT, SCORE>, kQ4Threads,
+                                                  C::kSmem);
+    return std::max(1, std::min(n, kQ4CtasPerSm));
+  }();
   const long long pairs = (long long)p.B * p.Hkv;
   const int R = p.Hq / p.Hkv * p.Sq;
   // As many CTAs as the workspace has slots for; one per pair, writing o and
@@ -966,6 +978,7 @@ MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, f
   if ((long long)(Hq / Hkv) * Sq > kQ4MaxRows || (long long)B * Hkv > 65535)
     return ATTN_ERR_UNSUPPORTED;
   if (!q4_page_ok(p->page_size)) return ATTN_ERR_UNSUPPORTED;
+  if (max_len > INT_MAX - 255) return ATTN_ERR_UNSUPPORTED;  // tile ends are int
   if (B == 0 || Sq == 0) return ATTN_OK;
   if (p->num_pages < 1 || p->pages_per_seq < 1 ||
       (long long)p->pages_per_seq * p->page_size < (long long)max_len)

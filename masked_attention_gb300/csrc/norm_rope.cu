@@ -30,7 +30,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 
 #include "host_util.h"
 #include "launch.h"
@@ -424,18 +423,11 @@ cudaError_t launch_typed(RopeArgs& a, bool inter, int B, float* const* dw, cudaS
   const long long all = many ? a.groups * items : a.groups * ((items + kRopeWarps - 1) / kRopeWarps);
   const int blocks = (int)std::min<long long>(std::min(resident, kRopeMaxBlocks), all);
   constexpr int kSmem = 2 * rope_rows<kBwd>() * (kBwd ? 4 : 2) * kRopeThreads * (int)sizeof(uint4);
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(norm_rope_kernel<D, kBf16, true, kBwd>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(norm_rope_kernel<D, kBf16, false, kBwd>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  });
-  if (attr_err != cudaSuccess) return attr_err;
-  const cudaError_t e =
-      inter ? launch_early(norm_rope_kernel<D, kBf16, true, kBwd>, blocks, kRopeThreads, kSmem, stream, a)
+  static DeviceOnce ready[2];
+  cudaError_t e = inter ? ready[1].allow_smem(norm_rope_kernel<D, kBf16, true, kBwd>, kSmem)
+                        : ready[0].allow_smem(norm_rope_kernel<D, kBf16, false, kBwd>, kSmem);
+  if (e != cudaSuccess) return e;
+  e = inter ? launch_early(norm_rope_kernel<D, kBf16, true, kBwd>, blocks, kRopeThreads, kSmem, stream, a)
             : launch_early(norm_rope_kernel<D, kBf16, false, kBwd>, blocks, kRopeThreads, kSmem, stream, a);
   if (e != cudaSuccess || !kBwd || (!dw[0] && !dw[1])) return e;
   return launch_early(rope_dw_kernel, 2 * D / 32, dim3(32, 32), 0, stream, a.part, blocks, D, dw[0], dw[1]);

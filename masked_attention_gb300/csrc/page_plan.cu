@@ -19,7 +19,6 @@
 #include <algorithm>
 #include <climits>
 #include <cstdint>
-#include <mutex>
 
 #include "host_util.h"
 #include "launch.h"
@@ -200,13 +199,9 @@ MATTN_API attn_status attn_page_plan(const int* cached_lens, const int* new_lens
   for (const void* x : ints)
     if (reinterpret_cast<uintptr_t>(x) & 3) return ATTN_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(slots) & 7) return ATTN_ERR_MISALIGNED;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    2 * (kPlanMaxB + 1) * (int)sizeof(int));
-  });
-  if (attr_err != cudaSuccess) return cuda_status(attr_err);
+  static DeviceOnce ready;
+  const cudaError_t err = ready.allow_smem(page_plan_kernel, 2 * (kPlanMaxB + 1) * (int)sizeof(int));
+  if (err != cudaSuccess) return cuda_status(err);
   const PlanArgs a{cached_lens, new_lens, B, page_table, pages_per_seq, free_pages, num_free,
                    shift, seq_lens, cu_new, slots, positions, seq_ids, max_tokens, info};
   const int blocks = std::max(1, std::min(2 * sm_count(),

@@ -139,6 +139,24 @@ def test_long_and_split(D, heads, ws):
     check(c, queries(4, Hq, Sq, D), ws)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,heads,seed", [(64, (2, 1, 1), 0), (128, (4, 2, 2), 1), (64, (9, 1, 1), 2)])
+def test_large_ragged_batches(D, heads, seed):
+    """Hundreds of sequences, many of them empty or short, one long: the dealing
+    out over CTAs has runs of sequences per thread and segments of every kind."""
+    Hq, Hkv, Sq = heads
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, 40, 331) * (rng.random(331) < 0.7)
+    lens[rng.integers(0, 331, 4)] = [700, 1300, 260, 129]
+    lens[:7] = 0
+    lens[-5:] = 0
+    c = Cache(lens, Hkv, D, 16, seed=seed, per=90)
+    check(c, queries(331, Hq, Sq, D), "full")
+    c.lens[:] = 0    # no sequence at all
+    o, lse = run(c, queries(331, Hq, Sq, D), 1, "full")
+    assert (o == 0).all() and np.isneginf(lse).all()
+
+
 MASKS = [dict(window=1), dict(window=20), dict(window=20, sink=1), dict(window=33, sink=40),
          dict(window=64, sink=4), dict(window=500, sink=4), dict(window=5, sink=1000),
          dict(causal=False), dict(causal=False, window=50, sink=3)]
@@ -387,6 +405,7 @@ def test_refusals():
     assert dec(1 << 5) == inv
     assert dec(M.MASK_WINDOW) == dec(M.SCORE_SOFTCAP) == dec(scale=float("inf")) == inv
     assert dec(q_offset=3) == dec(kv_offset=3) == uns
+    assert dec(max_len=2 ** 31 - 1, pages_per_seq=2 ** 27) == uns
     assert dec(max_len=113) == dec(num_pages=0) == dec(pages_per_seq=0) == inv
     for n in ("q", "pool", "o", "lse", "lens"):
         assert dec(**{n: None}) == inv and dec(**{n: 0x1002}) == mis, n
