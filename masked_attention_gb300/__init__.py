@@ -489,13 +489,20 @@ def attn_bwd_noalloc(q, k, v, o, lse, do, dq, dk, dv, variant: int = 0, *,
 # The calls below run once per layer of a decode step, where the host's time is
 # what counts, so their checks are few attribute reads per tensor; what a refusal
 # says is worked out only once one fails.
-_torch = None
+_torch = _current_device = _current_stream = None
 
 
 def _lazy_torch():
-    global _torch
+    """torch and two of its getters; the direct ones where this torch has them
+    (torch.cuda.current_stream builds a Stream object around the handle)."""
+    global _torch, _current_device, _current_stream
     if _torch is None:
         import torch
+        direct = torch._C
+        _current_device = getattr(direct, "_cuda_getDevice", torch.cuda.current_device)
+        _current_stream = getattr(direct, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        torch.cuda.init()
         _torch = torch
     return _torch
 
@@ -518,7 +525,7 @@ def _refuse(where: str, name: str, x, dtype, dev: int, shape=None) -> None:
 def _tensor(where: str, name: str, x, dtype, dev: int, shape) -> int:
     """Address of a contiguous tensor argument, checked."""
     try:
-        if (x.dtype is dtype and x.get_device() == dev and x.shape == shape and dev >= 0
+        if (x.dtype is dtype and x.get_device() == dev and x.shape == shape
                 and x.is_contiguous()):
             return x.data_ptr()
     except AttributeError:
@@ -529,7 +536,7 @@ def _tensor(where: str, name: str, x, dtype, dev: int, shape) -> int:
 def _view(where: str, name: str, x, dtype, dev: int, shape):
     """A [B, H, S, D] tensor of any strides with contiguous D, checked."""
     try:
-        if x.dtype is dtype and x.get_device() == dev and x.shape == shape and dev >= 0:
+        if x.dtype is dtype and x.get_device() == dev and x.shape == shape:
             sb, sh, ss, sd = x.stride()
             if sd == 1 or shape[3] == 1:
                 return ctypes.byref(attn_view(x.data_ptr(), sb, sh, ss))
@@ -541,28 +548,23 @@ def _view(where: str, name: str, x, dtype, dev: int, shape):
 
 def _device(where: str, name: str, x) -> int:
     """Index of the CUDA device that a call's tensors are on."""
-    _lazy_torch()
-    if not isinstance(x, _torch.Tensor) or not x.is_cuda:
+    if getattr(x, "is_cuda", False) is not True:
         raise ValueError(f"{where}: {name} must be a CUDA tensor")
+    if _torch is None:
+        _lazy_torch()
     return x.get_device()
 
 
 def _run(where: str, fn, dev: int, stream, *args) -> None:
     """Calls fn(*args, stream) on device `dev` (on its current stream unless given)."""
     stream = _current_stream(dev) if stream is None else _stream(stream)
-    if dev == _torch.cuda.current_device():
+    if dev == _current_device():
         st = fn(*args, stream)
     else:
         with _torch.cuda.device(dev):
             st = fn(*args, stream)
     if st != ATTN_OK:
         raise AttnError(st, where)
-
-
-def _current_stream(dev: int) -> int:
-    # the handle alone; torch.cuda.current_stream builds a Stream object around it
-    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw is not None else _torch.cuda.current_stream(dev).cuda_stream
 
 
 def attn_page_plan(cached_lens, new_lens, page_table, free_pages, seq_lens, cu_new, slots,

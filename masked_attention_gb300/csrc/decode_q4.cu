@@ -880,6 +880,10 @@ cudaError_t launch_merge(const Q4Problem& p, int ctas, cudaStream_t stream) {
               : launch_early(q4_merge_kernel<D, 1>, grid, kQ4Threads, 0, stream, p);
 }
 
+// Up to this many tiles a pair is one CTA's, whatever the workspace: sharing it out
+// costs the merge, a launch (1 sequence x 8 heads, 1100 keys, 35 tiles: 11 us alone
+// and 12 shared; 2000 keys, 63 tiles: 17 and 12).
+constexpr int kQ4DirectTiles = 40;
 constexpr int kQ4CtasPerSm = 4;  // most resident CTAs that a call uses
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -919,12 +923,11 @@ cudaError_t launch_typed(Q4Problem& p, long long tiles, void* ws, size_t ws_byte
   const long long pairs = (long long)p.B * p.Hkv;
   const int R = p.Hq / p.Hkv * p.Sq;
   // As many CTAs as the workspace has slots for; one per pair, writing o and
-  // lse at once, where that is no fewer or a pair has no more tiles than a CTA
-  // warps.
+  // lse at once, where that is no fewer or pairs are short.
   int ctas = q4_ctas(tiles * pairs, per_sm * sm_count());
   const int want = ctas;
   while (ctas > 1 && q4_workspace(pairs, ctas, R, D).total > ws_bytes) ctas /= 2;
-  const bool split = ws && tiles > kQ4Warps && ctas > 1 && (ctas == want || ctas > pairs);
+  const bool split = ws && tiles > kQ4DirectTiles && ctas > 1 && (ctas == want || ctas > pairs);
   if (!split) {
     return launch_early(decode_q4_kernel<D, NT, SCORE>, (unsigned)pairs, kQ4Threads, C::kSmem, stream, p);
   }
@@ -954,7 +957,7 @@ MATTN_API size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, 
   using namespace mattn;
   const long long pairs = (long long)B * Hkv;
   const long long tiles = ((long long)max_len + kQ4Tile - 1) / kQ4Tile;
-  if (tiles <= kQ4Warps || Hq % Hkv) return 0;
+  if (tiles <= kQ4DirectTiles || Hq % Hkv) return 0;
   return q4_workspace(pairs, q4_ctas(tiles * pairs, kQ4CtasPerSm * sm_count()),
                       Hq / Hkv * Sq, D).total;
 }

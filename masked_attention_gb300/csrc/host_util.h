@@ -101,9 +101,12 @@ cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, dim3 block, s
 }
 
 inline int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (n > 0 && dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n > 0 ? n : 1;
 }
 

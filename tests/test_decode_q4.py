@@ -173,6 +173,16 @@ def test_windows_and_sinks(D, heads, mask):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mask", [dict(window=1400, sink=4), dict(window=1300, sink=100),
+                                  dict(window=2500), dict(window=1400, sink=4, alibi=True)])
+@pytest.mark.parametrize("ws", ["full", "none"])
+def test_long_windows(mask, ws):
+    """Windows long enough to be shared by several CTAs."""
+    c = Cache([2900, 1500, 0, 50], 1, 64, 32, seed=24)
+    check(c, queries(4, 4, 2, 64), ws, **mask)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("heads", [(8, 2, 2), (12, 1, 1)])
 @pytest.mark.parametrize("kw", [dict(softcap=30.0), dict(softcap=1.5), dict(alibi=True),
@@ -345,10 +355,12 @@ def test_graphs_streams_and_a_shared_workspace():
     """Two captured graphs on one workspace, replayed in turn and again; then
     calls on a side stream: same bits as eager calls."""
     import masked_attention_gb300 as M
-    cs = [Cache([800, 30, 0], 2, 128, 16, seed=21), Cache([33, 700, 1], 2, 128, 16, seed=22)]
+    cs = [Cache([800, 30, 0], 2, 128, 16, seed=21, per=100),
+          Cache([33, 700, 1], 2, 128, 16, seed=22, per=100)]
     q = queries(3, 8, 1, 128).cuda()
     refs = [run(c, q.cpu(), M.MASK_CAUSAL, "full") for c in cs]
     n = max(M.attn_decode_q4_workspace_bytes(3, 8, 2, 1, c.table.shape[1] * 16, 128) for c in cs)
+    assert n > 0   # the tables are wide enough that the keys are shared out
     ws = torch.empty(n, dtype=torch.uint8, device="cuda")
     outs = [(torch.empty_like(q), torch.empty(3, 8, 1, device="cuda")) for _ in cs]
     dev = [(torch.from_numpy(c.pool).cuda(), torch.from_numpy(c.table).cuda(),
