@@ -367,8 +367,8 @@ attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
  * window, softcap, alibi_slopes, page_table, page_size, pages_per_seq and
  * num_pages; its other fields are not used, except that offsets must be 0.
  * Variant: ATTN_MASK_CAUSAL, ATTN_MASK_WINDOW, ATTN_SCORE_ALIBI and
- * ATTN_SCORE_SOFTCAP in any combination (others: ATTN_ERR_UNSUPPORTED), and
- * with a window the first `sink` keys stay visible:
+ * ATTN_SCORE_SOFTCAP (a finite softcap >= 1e-38) in any combination (others:
+ * ATTN_ERR_UNSUPPORTED), and with a window the first `sink` keys stay visible:
  *   keep(i, j) = j < seq_len AND i >= 0 AND (CAUSAL: j <= i)
  *                AND (WINDOW: i - j < window OR j < sink)
  * Keys that no row sees are not read, and what a masked key's record holds,

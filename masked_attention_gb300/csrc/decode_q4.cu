@@ -119,6 +119,19 @@ __device__ __forceinline__ Q4Range q4_range(const Q4Problem& p, int b) {
   return r;
 }
 
+// cap tanh(s / cap), s and cap in log2 units, inv = 2 / cap (natural), as
+// cap - 2 cap / (1 + e^(2 s / cap)): off by at most 2^-22 cap. Where |s / cap| < 1/8
+// that would be many times the score's own rounding (a cap of 10^6: 0.2), so there it
+// is s (1 - x^2/3 + 2 x^4/15 - 17 x^6/315), x = s / cap, off by 2^-29 s.
+__device__ __forceinline__ float soft_cap(float s, float cap2, float inv) {
+  const float y = s * inv;  // x = y ln 2 / 2
+  const float far = fmaf(-cap2, __fdividef(2.0f, 1.0f + ex2_approx(y)), cap2);
+  constexpr float kX2 = 0.25f * 0.69314718f * 0.69314718f;
+  const float x2 = kX2 * y * y;
+  const float near = s + s * x2 * fmaf(x2, fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f);
+  return x2 < 1.0f / 64.0f ? near : far;
+}
+
 template <int D, int NT>
 struct Q4Cfg {
   static constexpr int G = D / kQ4Group;                  // scales per row
@@ -590,10 +603,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
             float s = x[mt][nt][e];
             if constexpr (SCORE != 0) s *= unit[nt][e & 1];
             if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
-            // cap tanh(s / cap) as cap - 2 cap / (1 + e^(2 s / cap)): off by at
-            // most 2^-22 cap, and exact at both ends
-            if constexpr ((SCORE & 2) != 0)
-              s = fmaf(-p.softcap2, __fdividef(2.0f, 1.0f + ex2_approx(s * p.softcap_e)), p.softcap2);
+            if constexpr ((SCORE & 2) != 0) s = soft_cap(s, p.softcap2, p.softcap_e);
             if constexpr (kMask) {
               bool keep = j < len && i >= 0;
               if (causal) keep = keep && j <= i;
@@ -975,7 +985,9 @@ MATTN_API attn_status attn_decode_q4(const void* q, const void* pool, void* o, f
   if (variant & ~(unsigned)(ATTN_MASK_CAUSAL | ATTN_MASK_WINDOW | ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP))
     return ATTN_ERR_UNSUPPORTED;
   if ((variant & ATTN_MASK_WINDOW) && p->window < 1) return ATTN_ERR_INVALID_ARG;
-  if ((variant & ATTN_SCORE_SOFTCAP) && !(p->softcap > 0.0f)) return ATTN_ERR_INVALID_ARG;
+  if ((variant & ATTN_SCORE_SOFTCAP) &&
+      !(p->softcap > 0.0f && std::isfinite(p->softcap) && std::isfinite(2.0f / p->softcap)))
+    return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(p->scale) || p->scale < 0.0f) return ATTN_ERR_INVALID_ARG;
   if (p->q_offset || p->kv_offset) return ATTN_ERR_UNSUPPORTED;
   if ((long long)(Hq / Hkv) * Sq > kQ4MaxRows || (long long)B * Hkv > 65535)

@@ -198,6 +198,29 @@ def test_scores(D, heads, kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [6.0, 40.0, 1e6, 1e30, 3e38])
+@pytest.mark.parametrize("heads", [(8, 2, 2), (12, 1, 1)])
+def test_caps_far_above_the_scores(cap, heads):
+    """A cap that the scores do not come near leaves them as they are: its
+    rounding has to count against the score, not against the cap."""
+    Hq, Hkv, Sq = heads
+    c = Cache([130, 33], Hkv, 128, 16, seed=22)
+    check(c, queries(2, Hq, Sq, 128), softcap=cap)
+    check(c, queries(2, Hq, Sq, 128, size=1e-3), softcap=cap)
+
+
+def test_caps_that_fp32_cannot_hold_are_refused():
+    import masked_attention_gb300 as M
+    p = M.attn_params()
+    p.dtype, p.page_table, p.page_size, p.pages_per_seq, p.num_pages = 0, 0x6000, 16, 7, 9
+    for cap in (float("inf"), float("nan"), 0.0, -1.0, 1e-39):
+        p.softcap = cap
+        assert M.lib().attn_decode_q4(0x1000, 0x2000, 0x3000, 0x4000, 1, 4, 2, 1, 100, 64,
+                                      M.SCORE_SOFTCAP, ctypes.byref(p), 0x5000, 0, None, 0,
+                                      None) == M.ATTN_ERR_INVALID_ARG, cap
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_scores_that_jump(D):
     """Scores of several hundred, the largest late in the key order: the
