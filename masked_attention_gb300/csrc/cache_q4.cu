@@ -304,6 +304,9 @@ attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const l
     if ((reinterpret_cast<uintptr_t>(w.data) & 15u) || (B > 1 && w.stride_b % 8) ||
         (Hkv > 1 && w.stride_h % 8) || (S > 1 && w.stride_s % 8))
       return ATTN_ERR_MISALIGNED;
+    // rows that are written have to be distinct places
+    if (load && ((B > 1 && !w.stride_b) || (Hkv > 1 && !w.stride_h) || (S > 1 && !w.stride_s)))
+      return ATTN_ERR_INVALID_ARG;
     a.x[t] = static_cast<char*>(w.data);
     a.sb[t] = B > 1 ? w.stride_b * 2 : 0;
     a.sh[t] = Hkv > 1 ? w.stride_h * 2 : 0;

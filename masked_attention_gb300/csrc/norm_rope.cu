@@ -444,8 +444,10 @@ cudaError_t launch_rope(RopeArgs& a, const attn_rope_params* p, int B, int D, fl
                  : launch_typed<128, false, kBwd>(a, inter, B, dw, s);
 }
 
-// Checks one tensor and turns its strides into bytes.
-attn_status take_view(View& v, const attn_view* t, int B, int H, int S, int D, int elem) {
+// Checks one tensor and turns its strides into bytes. An output's rows have to be
+// distinct places (no stride of 0); `from` is the input that it may be itself.
+attn_status take_view(View& v, const attn_view* t, int B, int H, int S, int D, int elem,
+                      bool output = false, const View* from = nullptr) {
   if (!t || !t->data) return ATTN_ERR_INVALID_ARG;
   if (t->stride_b < 0 || t->stride_h < 0 || t->stride_s < 0) return ATTN_ERR_INVALID_ARG;
   const long long unit = 16 / elem;
@@ -457,6 +459,9 @@ attn_status take_view(View& v, const attn_view* t, int B, int H, int S, int D, i
   v.sh = H > 1 ? t->stride_h * elem : 0;
   v.ss = S > 1 ? t->stride_s * elem : 0;
   v.bytes = (B - 1) * v.sb + (H - 1) * v.sh + (S - 1) * v.ss + (long long)D * elem;
+  if (output && ((B > 1 && !v.sb) || (H > 1 && !v.sh) || (S > 1 && !v.ss))) return ATTN_ERR_INVALID_ARG;
+  if (from && from->p == v.p && (from->sb != v.sb || from->sh != v.sh || from->ss != v.ss))
+    return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
 
@@ -504,7 +509,7 @@ MATTN_API attn_status attn_qk_norm_rope(const attn_view* q, const attn_view* k,
   for (int t = 0; t < 2; ++t) {
     if (a.H[t] == 0) continue;
     if ((st = take_view(a.x[t], in[t], B, a.H[t], S, D, elem)) != ATTN_OK) return st;
-    if ((st = take_view(a.z[t], out[t], B, a.H[t], S, D, elem)) != ATTN_OK) return st;
+    if ((st = take_view(a.z[t], out[t], B, a.H[t], S, D, elem, true, &a.x[t])) != ATTN_OK) return st;
   }
   return cuda_status(launch_rope<false>(a, p, B, D, nullptr, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -536,7 +541,7 @@ MATTN_API attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view*
       if (a.H[t] == 0) continue;
       if (a.w[t] && (st = take_view(a.x[t], in[t], B, a.H[t], S, D, elem)) != ATTN_OK) return st;
       if ((st = take_view(a.z[t], dz[t], B, a.H[t], S, D, elem)) != ATTN_OK) return st;
-      if ((st = take_view(a.dx[t], dx[t], B, a.H[t], S, D, elem)) != ATTN_OK) return st;
+      if ((st = take_view(a.dx[t], dx[t], B, a.H[t], S, D, elem, true, &a.z[t])) != ATTN_OK) return st;
     }
   }
   if (!workspace) return ATTN_ERR_INVALID_ARG;

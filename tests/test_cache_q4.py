@@ -199,6 +199,16 @@ def test_oracle_rounding():
     assert bits[0, 0] == 0x3f80 and n[0, :5].tolist() == [15, 1, 10, 12, 8]
 
 
+def test_loads_into_broadcast_tensors_are_refused():
+    import masked_attention_gb300 as M
+    good = ctypes.byref(M.attn_view(0x1000, 4096, 1024, 128))
+    for strides in ((0, 1024, 128), (4096, 0, 128), (4096, 1024, 0)):
+        bad = ctypes.byref(M.attn_view(0x1000, *strides))
+        for k, v in ((good, bad), (bad, good)):
+            assert M.lib().attn_cache_load_q4(0x10000, 4, 16, 0x8000, k, v, 2, 2, 3, 128,
+                                              None) == M.ATTN_ERR_INVALID_ARG
+
+
 def test_refusals():
     import masked_attention_gb300 as M
     L = M.lib()

@@ -300,6 +300,30 @@ def test_oracle_rotation_keeps_relative_position():
         assert abs(s[0] - s[1]) < 1e-5 * abs(q).sum()   # the table itself is fp32
 
 
+def test_outputs_whose_rows_share_a_place_are_refused():
+    """A broadcast tensor is an input only, and an output that starts where its
+    input does has its strides."""
+    import ctypes
+    import masked_attention_gb300 as M
+    L = M.lib()
+    good, other = (4096, 1024, 128), (8192, 1024, 128)
+
+    def call(fn, out, x=good, data=0x100000, B=2, H=4):
+        p = M.attn_rope_params(M.BF16, 1e-6, None, None, 0x9000, 64, 128, 0, None)
+        i, o = ctypes.byref(M.attn_view(0x1000, *x)), ctypes.byref(M.attn_view(data, *out))
+        if fn == "fwd":
+            return L.attn_qk_norm_rope(i, None, o, None, B, H, 0, 8, 128, ctypes.byref(p), None)
+        return L.attn_qk_norm_rope_bwd(None, None, i, None, o, None, None, None, 0x200000,
+                                       M.attn_qk_norm_rope_bwd_workspace_bytes(128), B, H, 0, 8,
+                                       128, ctypes.byref(p), None)
+
+    for fn in ("fwd", "bwd"):
+        for out in ((0, 1024, 128), (4096, 0, 128), (4096, 1024, 0)):
+            assert call(fn, out) == M.ATTN_ERR_INVALID_ARG, (fn, out)
+        assert call(fn, other, data=0x1000) == M.ATTN_ERR_INVALID_ARG
+        assert call(fn, good, x=(0, 1024, 128), data=0x1000) == M.ATTN_ERR_INVALID_ARG
+
+
 def test_refusals():
     import ctypes
     import masked_attention_gb300 as M
