@@ -249,7 +249,7 @@ attn_status attn_doc_ids_from_seqlens(const int* cu_seqlens, int n, int total, i
 
 /* A [B, H, S, D] tensor of any strides (in elements), D contiguous. `data`
  * is 16-byte aligned and every stride of a dimension longer than 1 is a
- * multiple of 16 bytes, >= 0. */
+ * multiple of 16 bytes, >= 0, and in a tensor that is written > 0. */
 typedef struct attn_view {
   void* data;
   long long stride_b, stride_h, stride_s;
@@ -274,8 +274,9 @@ typedef struct attn_view {
  * past max_tokens are dropped. A page that free_pages cannot give is entered
  * as -1, and tokens without a page (that one, or past pages_per_seq) get slot
  * -1: info tells. page_size 16, 32, 64 or 128; B <= 16384 (else
- * ATTN_ERR_UNSUPPORTED). No two arguments may overlap. Asynchronous on
- * `stream`, one launch. */
+ * ATTN_ERR_UNSUPPORTED). What is written (page_table and the outputs) may
+ * overlap no other argument (ATTN_ERR_INVALID_ARG): seq_lens is not
+ * cached_lens. Asynchronous on `stream`, one launch. */
 attn_status attn_page_plan(const int* cached_lens, const int* new_lens, int B, int* page_table,
                            int pages_per_seq, int page_size, const int* free_pages, int num_free,
                            int* seq_lens, int* cu_new, long long* slots, int* positions,
@@ -320,7 +321,8 @@ size_t attn_qk_norm_rope_bwd_workspace_bytes(int D);
  * is NULL). q (k) is not read and may be NULL when its weight is NULL. dq may
  * be dq_out itself with the same strides. No atomics: results are bitwise
  * reproducible. The workspace is 256-byte aligned device memory whose contents
- * need not be kept between calls. */
+ * need not be kept between calls; calls that may run at the same time need
+ * one each. */
 attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view* k, const attn_view* dq_out,
                                   const attn_view* dk_out, const attn_view* dq,
                                   const attn_view* dk, float* dq_weight, float* dk_weight,
@@ -378,7 +380,9 @@ attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
  * the SMs, and results of sequences that several CTAs share are joined from it:
  * 256-byte aligned device memory, attn_decode_q4_workspace_bytes() for the full
  * spread, less or NULL means fewer CTAs (one per sequence and key/value head
- * with NULL); its contents need not be kept between calls. */
+ * with NULL); its contents need not be kept between calls, and calls that may
+ * run at the same time need one each. ATTN_ERR_UNSUPPORTED for B * Hkv > 65535 or
+ * max_len > INT_MAX - 255. */
 attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B, int Hq,
                            int Hkv, int Sq, int max_len, int D, unsigned variant,
                            const attn_params* p, const int* seq_lens, int sink, void* workspace,

@@ -199,15 +199,33 @@ MATTN_API attn_status attn_page_plan(const int* cached_lens, const int* new_lens
   for (const void* x : ints)
     if (reinterpret_cast<uintptr_t>(x) & 3) return ATTN_ERR_MISALIGNED;
   if (reinterpret_cast<uintptr_t>(slots) & 7) return ATTN_ERR_MISALIGNED;
+  // Every block reads the lengths, the free list and the table while others write:
+  // what is written overlaps nothing.
+  struct Range {
+    const void* at;
+    long long bytes;
+  };
+  const long long tokens = max_tokens, entries = (long long)B * pages_per_seq;
+  const Range ranges[] = {{seq_lens, 4LL * B}, {cu_new, 4LL * B + 4}, {slots, 8 * tokens},
+                          {positions, 4 * tokens}, {seq_ids, 4 * tokens}, {info, 16},
+                          {page_table, 4 * entries}, {cached_lens, 4LL * B}, {new_lens, 4LL * B},
+                          {free_pages, 4LL * num_free}};
+  constexpr int kWritten = 7, kRanges = sizeof(ranges) / sizeof(ranges[0]);
+  for (int i = 0; i < kWritten; ++i)
+    for (int j = i + 1; j < kRanges; ++j) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(ranges[i].at);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(ranges[j].at);
+      if (a < b + ranges[j].bytes && b < a + ranges[i].bytes) return ATTN_ERR_INVALID_ARG;
+    }
   static DeviceOnce ready;
   const cudaError_t err = ready.allow_smem(page_plan_kernel, 2 * (kPlanMaxB + 1) * (int)sizeof(int));
   if (err != cudaSuccess) return cuda_status(err);
-  const PlanArgs a{cached_lens, new_lens, B, page_table, pages_per_seq, free_pages, num_free,
+  const PlanArgs args{cached_lens, new_lens, B, page_table, pages_per_seq, free_pages, num_free,
                    shift, seq_lens, cu_new, slots, positions, seq_ids, max_tokens, info};
   const int blocks = std::max(1, std::min(2 * sm_count(),
                                           (max_tokens + kPlanTokens - 1) / kPlanTokens));
   return cuda_status(launch_early(page_plan_kernel, blocks, kPlanThreads, 2 * (B + 1) * sizeof(int),
-                                  reinterpret_cast<cudaStream_t>(stream), a));
+                                  reinterpret_cast<cudaStream_t>(stream), args));
 }
 
 namespace mattn {

@@ -148,6 +148,30 @@ def test_oracle_plan_by_hand():
     assert tab.tolist() == [[8, 2, -7], [5, 6, 9]] and info.tolist() == [5, 2, 0, 0]
 
 
+def test_overlapping_arguments_are_refused():
+    """The lengths in place, the natural mistake, and neighbours that run into
+    one another."""
+    import masked_attention_gb300 as M
+    names = ("cached", "new", "table", "free", "lens", "cu", "slots", "pos", "ids", "info")
+    size = dict(cached=8, new=8, table=32, free=12, lens=8, cu=12, slots=64, pos=32, ids=32, info=16)
+
+    def plan(**kw):
+        a = {n: 0x1000 * (i + 1) for i, n in enumerate(names)}
+        a.update(kw)
+        return M.lib().attn_page_plan(a["cached"], a["new"], 2, a["table"], 4, 16, a["free"], 3,
+                                      a["lens"], a["cu"], a["slots"], a["pos"], a["ids"], 8,
+                                      a["info"], None)
+
+    for out in ("table", "lens", "cu", "slots", "pos", "ids", "info"):
+        for i, other in enumerate(names):
+            if other == out:
+                continue
+            at = 0x1000 * (i + 1)
+            assert plan(**{out: at}) == M.ATTN_ERR_INVALID_ARG, (out, other)
+            last = at + (size[other] - 1) // 8 * 8      # inside it, aligned for all types
+            assert plan(**{out: last}) == M.ATTN_ERR_INVALID_ARG, (out, other)
+
+
 def test_refusals():
     import masked_attention_gb300 as M
     L = M.lib()
