@@ -16,7 +16,8 @@
 // quantiser's instructions close behind. A lane holds 16 channels of a row (32 bytes
 // of bf16, 8 of codes), half of a scale's, so the largest magnitude takes one
 // shuffle. A warp takes a batch of a token's K and V rows, with the slot (read:
-// and the codes) of its next batch on the way.
+// and the codes) of its next batch on the way; where a token's rows do not fill
+// batches, the rows of all tokens in a line are cut into batches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,6 +39,7 @@ constexpr int kCacheWarps = kCacheThreads / 32;
 constexpr int kCacheRows = 4;   // rows in flight per lane group
 constexpr int kCachePerSm = 3;  // blocks per SM. 16384 tokens x 8 heads of 128 channels, write and
                                 // read: 38 us; 2 rows at 4 blocks 42 us, 1 row at 6 blocks 46 us
+                                // (before their starts were programmatic: 33 us)
 
 struct CacheArgs {
   char* x[2];            // K and V rows (store: read, load: written)
@@ -45,7 +47,8 @@ struct CacheArgs {
   uint8_t* pool;
   const long long* slots;  // [B][S]
   int B, Hkv, S, num_pages, shift;
-  int batches;             // batches of rows per token
+  int period;              // batches of rows per token; packed: rows per token
+  uint32_t per_row, per_s;  // packed: ceil(2^32 / rows per token), ceil(2^32 / S)
   bool wide;               // rows are 32-byte aligned
 };
 
@@ -149,14 +152,16 @@ __device__ __forceinline__ void store32(uint4* p, bool wide, const uint4& a, con
   }
 }
 
-// Units (token, batch of its K and V rows), the batch first; a warp takes every
-// stride-th. Where a unit is, kept without divisions.
+// Units of a batch of rows (kCacheRows per lane group); a warp takes every
+// stride-th. A unit is a batch of one token's K and V rows, the batch first, or
+// (packed) the next rows of all tokens' in a line. Where a unit begins, kept without
+// divisions: batch is the batch or (packed) the row of its token.
 struct Cursor {
   long long u, token;
   int batch, b, s;
 };
 
-template <int D, bool kLoad>
+template <int D, bool kLoad, bool kPacked>
 __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
     cache_q4_kernel(const CacheArgs a) {
   constexpr int R = kCacheRows;
@@ -164,25 +169,27 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
   constexpr int SUBS = 32 / LANES;  // rows side by side in a warp
   const int lane = threadIdx.x & 31, part = lane % LANES, sub = lane / LANES;
   const Q4Layout L{D, 1 << a.shift};
-  const long long units = (long long)a.B * a.S * a.batches;
+  const int rows = 2 * a.Hkv;  // K rows of all heads, then V rows
+  const long long tokens = (long long)a.B * a.S;
+  const long long units = kPacked ? (tokens * rows + SUBS * R - 1) / (SUBS * R) : tokens * a.period;
   const long long stride = (long long)gridDim.x * kCacheWarps;
   Cursor c;
   c.u = (long long)blockIdx.x * kCacheWarps + (threadIdx.x >> 5);
   early_start();
   if (c.u >= units) return;
-  c.token = c.u / a.batches;
-  c.batch = (int)(c.u % a.batches);
+  constexpr int kStep = kPacked ? SUBS * R : 1;
+  c.token = c.u * kStep / a.period;
+  c.batch = (int)(c.u * kStep % a.period);
   c.b = (int)(c.token / a.S);
   c.s = (int)(c.token % a.S);
-  const long long dt = stride / a.batches;
-  const int dbatch = (int)(stride % a.batches), db = (int)(dt / a.S), ds = (int)(dt % a.S);
+  const long long dt = stride * kStep / a.period;
+  const int dbatch = (int)(stride * kStep % a.period), db = (int)(dt / a.S), ds = (int)(dt % a.S);
   const long long page_bytes = (long long)a.Hkv * L.bytes();
-  const int rows = 2 * a.Hkv;  // K rows of all heads, then V rows
   auto advance = [&](Cursor& k) {
     k.u += stride;
     k.batch += dbatch;
-    const int carry = k.batch >= a.batches;
-    k.batch -= carry ? a.batches : 0;
+    const int carry = k.batch >= a.period;
+    k.batch -= carry ? a.period : 0;
     k.token += dt + carry;
     k.s += ds + carry;
     k.b += db;
@@ -191,30 +198,60 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
       ++k.b;
     }
   };
-  auto slot_of = [&](const Cursor& k) { return k.u < units ? a.slots[k.token] : -1; };
-  // row r of the unit for this lane group: K or V, head; nullptr: past the last
+  // Row r of a unit for this lane group: its token (`ahead` of the unit's first; -1: no
+  // row) and its row there.
+  auto place = [&](const Cursor& k, int r, int& row) -> int {
+    row = (kPacked ? k.batch : k.batch * SUBS * R) + r * SUBS + sub;
+    if constexpr (!kPacked) return row < rows ? 0 : -1;
+    const int ahead = (int)__umulhi(row, a.per_row);
+    row -= ahead * rows;
+    return k.token + ahead < tokens ? ahead : -1;
+  };
+  constexpr int kSlots = kPacked ? R : 1;  // slots of a unit: one token's, or each row's
+  auto slots_of = [&](const Cursor& k, long long (&slot)[kSlots]) {
+#pragma unroll
+    for (int r = 0; r < kSlots; ++r) {
+      int row, ahead = 0;
+      if constexpr (kPacked) ahead = place(k, r, row);
+      slot[r] = k.u < units && ahead >= 0 ? a.slots[k.token + ahead] : -1;
+    }
+  };
+  // its bf16 row; nullptr: none
   auto bf16_row = [&](const Cursor& k, int r) -> uint4* {
-    const int rr = k.batch * SUBS * R + r * SUBS + sub;
-    const int v = rr >= a.Hkv ? 1 : 0, h = rr - v * a.Hkv;
-    const long long at = v ? k.b * a.sb[1] + k.s * a.ss[1] + h * a.sh[1]
-                           : k.b * a.sb[0] + k.s * a.ss[0] + h * a.sh[0];
-    if (rr >= rows || !MATTN_IN_BOUNDS(kSiteCacheRow, at + part * 32, a.span[v] - 31)) return nullptr;
+    int row;
+    const int ahead = place(k, r, row);
+    if (ahead < 0) return nullptr;
+    int b = k.b, s = k.s;
+    if constexpr (kPacked) {  // over the sequence's end; a unit has at most 16 tokens
+      s += ahead;
+      const int over = a.S > 16 ? s >= a.S : (int)__umulhi(s, a.per_s);
+      b += over;
+      s -= over * a.S;
+    }
+    const int v = row >= a.Hkv ? 1 : 0, h = row - v * a.Hkv;
+    const long long at = v ? b * a.sb[1] + s * a.ss[1] + h * a.sh[1]
+                           : b * a.sb[0] + s * a.ss[0] + h * a.sh[0];
+    if (!MATTN_IN_BOUNDS(kSiteCacheRow, at + part * 32, a.span[v] - 31)) return nullptr;
     return reinterpret_cast<uint4*>((v ? a.x[1] : a.x[0]) + at + part * 32);
   };
   // its codes and scale in the record, for a slot of the pool; nullptr: none
-  auto code_row = [&](const Cursor& k, int r, long long slot, uint8_t*& scale) -> uint8_t* {
-    const int rr = k.batch * SUBS * R + r * SUBS + sub;
-    const int v = rr >= a.Hkv ? 1 : 0, h = rr - v * a.Hkv;
+  auto code_row = [&](const Cursor& k, int r, const long long (&slots)[kSlots],
+                      uint8_t*& scale) -> uint8_t* {
+    int row;
+    const int ahead = place(k, r, row);
+    const long long slot = slots[kPacked ? r : 0];
     const long long page = slot >> a.shift;
-    if (rr >= rows || slot < 0 || page >= a.num_pages) return nullptr;
+    if (ahead < 0 || slot < 0 || page >= a.num_pages) return nullptr;
+    const int v = row >= a.Hkv ? 1 : 0, h = row - v * a.Hkv;
     uint8_t* rec = a.pool + page * page_bytes + (long long)h * L.bytes();
-    const int row = (int)(slot & (L.page - 1));
-    scale = rec + (v ? L.v_scales() : L.k_scales()) + row * L.scale_row() + part / 2 * 2;
-    return rec + (v ? L.v_codes() : 0) + row * L.code_row() + part * 8;
+    const int in_page = (int)(slot & (L.page - 1));
+    scale = rec + (v ? L.v_scales() : L.k_scales()) + in_page * L.scale_row() + part / 2 * 2;
+    return rec + (v ? L.v_codes() : 0) + in_page * L.code_row() + part * 8;
   };
 
   if constexpr (!kLoad) {
-    long long slot = slot_of(c);
+    long long slot[kSlots];
+    slots_of(c, slot);
     while (c.u < units) {
       uint4 raw[R][2];
 #pragma unroll
@@ -225,7 +262,8 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
       }
       const Cursor now = c;
       advance(c);
-      const long long slot_next = slot_of(c);
+      long long slot_next[kSlots];
+      slots_of(c, slot_next);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         uint32_t word[2], sc;
@@ -236,12 +274,14 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
         *reinterpret_cast<uint2*>(code) = make_uint2(word[0], word[1]);
         if (part % 2 == 0) *reinterpret_cast<unsigned short*>(scale) = (unsigned short)sc;
       }
-      slot = slot_next;
+#pragma unroll
+      for (int r = 0; r < kSlots; ++r) slot[r] = slot_next[r];
     }
   } else {
-    // the codes of the next unit, and the slot of the one after it, are on
+    // the codes of the next unit, and the slots of the one after it, are on
     // their way while a unit is written
-    auto fetch = [&](const Cursor& k, long long slot, uint2 (&word)[R], uint32_t (&sc)[R]) {
+    auto fetch = [&](const Cursor& k, const long long (&slot)[kSlots], uint2 (&word)[R],
+                     uint32_t (&sc)[R]) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         uint8_t* scale;
@@ -252,17 +292,19 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
     };
     uint2 word[R];
     uint32_t sc[R];
-    fetch(c, slot_of(c), word, sc);
+    long long slot[kSlots];
+    slots_of(c, slot);
+    fetch(c, slot, word, sc);
     Cursor ahead = c;
     advance(ahead);
-    long long slot = slot_of(ahead);
+    slots_of(ahead, slot);
     while (c.u < units) {
       uint2 word_next[R];
       uint32_t sc_next[R];
       const Cursor next = ahead;
       if (next.u < units) fetch(next, slot, word_next, sc_next);
       advance(ahead);
-      slot = slot_of(ahead);
+      slots_of(ahead, slot);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         uint4* x = bf16_row(c, r);
@@ -282,11 +324,21 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
 template <int D, bool kLoad>
 cudaError_t launch_cache(CacheArgs& a, cudaStream_t stream) {
   constexpr int kBatch = 32 / (D / 16) * kCacheRows;
-  a.batches = (2 * a.Hkv + kBatch - 1) / kBatch;
-  const long long units = (long long)a.B * a.S * a.batches;
+  const long long rows = 2LL * a.Hkv, tokens = (long long)a.B * a.S;
+  const long long batches = (rows + kBatch - 1) / kBatch;
+  // Packed where a token's rows leave more than a quarter of its batches empty: its
+  // rows cost more to find, but no lane waits. Write and read, in place of batches of
+  // one token's: 91993 tokens x 1 head of 64: 23 us against 185; 16384 x 4 of 128: 24
+  // against 33, x 6 (12 of 16 rows): 35 against 33, x 8: 43 against 34.
+  const bool packed = 4 * rows < 3 * batches * kBatch;
+  const long long units = packed ? (tokens * rows + kBatch - 1) / kBatch : tokens * batches;
+  a.period = (int)(packed ? rows : batches);
+  a.per_row = (uint32_t)((0xffffffffull + rows) / rows);
+  a.per_s = a.S > 1 ? (uint32_t)((0xffffffffull + a.S) / a.S) : 0;
   const int blocks = (int)std::min<long long>(kCachePerSm * sm_count(),
                                               (units + kCacheWarps - 1) / kCacheWarps);
-  return launch_early(cache_q4_kernel<D, kLoad>, blocks, kCacheThreads, 0, stream, a);
+  return packed ? launch_early(cache_q4_kernel<D, kLoad, true>, blocks, kCacheThreads, 0, stream, a)
+                : launch_early(cache_q4_kernel<D, kLoad, false>, blocks, kCacheThreads, 0, stream, a);
 }
 
 attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const long long* slots,
@@ -322,10 +374,15 @@ attn_status run_cache(bool load, const attn_view* k, const attn_view* v, const l
   a.slots = slots;
   a.Hkv = Hkv;
   a.S = S;
+  a.B = B;
+  if (S == 1) {  // the batch is the sequence
+    for (int t = 0; t < 2; ++t) a.ss[t] = a.sb[t];
+    a.S = B;
+    a.B = 1;
+  }
   a.num_pages = num_pages;
   a.shift = 4;
   while ((1 << a.shift) != page_size) ++a.shift;
-  a.B = B;
   if (load) return cuda_status(D == 64 ? launch_cache<64, true>(a, stream) : launch_cache<128, true>(a, stream));
   return cuda_status(D == 64 ? launch_cache<64, false>(a, stream) : launch_cache<128, false>(a, stream));
 }

@@ -69,6 +69,16 @@ def test_store_and_load(D, page, B, H, S):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,S", [(2, 8, 9), (1, 16, 40), (5, 1, 18), (3, 1, 17), (3, 5, 16),
+                                   (40, 2, 3), (33, 1, 2), (2, 17, 6), (70, 4, 1), (1, 1, 700)])
+def test_rows_that_fill_batches_and_that_do_not(D, B, H, S):
+    """Tokens whose rows take whole batches, fractions of one, and batches that
+    begin inside one token or sequence and end in another."""
+    test_store_and_load(D, 16, B, H, S)
+
+
+@pytest.mark.gpu
 def test_half_aligned_rows():
     """Rows that start on 16 but not on 32 bytes (slices of an odd projection)."""
     import masked_attention_gb300 as M
