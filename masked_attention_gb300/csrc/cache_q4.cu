@@ -220,7 +220,6 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
   auto bf16_row = [&](const Cursor& k, int r) -> uint4* {
     int row;
     const int ahead = place(k, r, row);
-    if (ahead < 0) return nullptr;
     int b = k.b, s = k.s;
     if constexpr (kPacked) {  // over the sequence's end; a unit has at most 16 tokens
       s += ahead;
@@ -231,7 +230,7 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
     const int v = row >= a.Hkv ? 1 : 0, h = row - v * a.Hkv;
     const long long at = v ? b * a.sb[1] + s * a.ss[1] + h * a.sh[1]
                            : b * a.sb[0] + s * a.ss[0] + h * a.sh[0];
-    if (!MATTN_IN_BOUNDS(kSiteCacheRow, at + part * 32, a.span[v] - 31)) return nullptr;
+    if (ahead < 0 || !MATTN_IN_BOUNDS(kSiteCacheRow, at + part * 32, a.span[v] - 31)) return nullptr;
     return reinterpret_cast<uint4*>((v ? a.x[1] : a.x[0]) + at + part * 32);
   };
   // its codes and scale in the record, for a slot of the pool; nullptr: none
