@@ -792,16 +792,19 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
   }
 }
 
+constexpr int merge_warps(int W) { return W > kQ4Warps ? W : kQ4Warps; }  // of a block
+
 // Joins the partial results of the pairs that several CTAs share: W warps per
 // row of o take its parts in turn (a fixed order), each lane D / 32 channels.
 // Bound by latency: two dependent loads, then the parts' rows from the L2.
 template <int D, int W>
-__global__ void __launch_bounds__(kQ4Threads) q4_merge_kernel(const Q4Problem p) {
+__global__ void __launch_bounds__(32 * merge_warps(W)) q4_merge_kernel(const Q4Problem p) {
   constexpr int V = D / 32;
-  __shared__ float sh[kQ4Warps][D + 2];
+  constexpr int kWarps = merge_warps(W);
+  __shared__ float sh[kWarps][D + 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long rows = (long long)p.B * p.Hq * p.Sq;
-  const long long row = (long long)blockIdx.x * (kQ4Warps / W) + warp / W;
+  const long long row = (long long)blockIdx.x * (kWarps / W) + warp / W;
   early_start();
   float M = -INFINITY, L = 0.0f, acc[V];
 #pragma unroll
@@ -882,12 +885,18 @@ __global__ void __launch_bounds__(kQ4Threads) q4_merge_kernel(const Q4Problem p)
 template <int D>
 cudaError_t launch_merge(const Q4Problem& p, int ctas, cudaStream_t stream) {
   const long long rows = (long long)p.B * p.Hq * p.Sq;
-  // One warp per row where a pair is cut into few parts; a whole block where
-  // the CTAs are at least eight times the pairs.
-  const bool wide = ctas >= 8LL * p.B * p.Hkv;
-  const unsigned grid = (unsigned)(wide ? rows : (rows + kQ4Warps - 1) / kQ4Warps);
-  return wide ? launch_early(q4_merge_kernel<D, kQ4Warps>, grid, kQ4Threads, 0, stream, p)
-              : launch_early(q4_merge_kernel<D, 1>, grid, kQ4Threads, 0, stream, p);
+  // One warp per row where a pair is cut into few parts, a block of 4 or 16 warps
+  // where the CTAs are at least 8 or 32 times the pairs: parts in turn are what a
+  // row waits for (1 sequence x 1 head, 60000 keys, 456 parts: 18 us with 16 warps,
+  // 24 with 8, 29 with 4), but 16 warps for 8 parts cost more than they save (7
+  // sequences x 8 heads of 64, 16 rows: 68 us against 65).
+  const long long pairs = (long long)p.B * p.Hkv;
+  if (ctas >= 32 * pairs)
+    return launch_early(q4_merge_kernel<D, 16>, (unsigned)rows, 32 * merge_warps(16), 0, stream, p);
+  if (ctas >= 8 * pairs)
+    return launch_early(q4_merge_kernel<D, 4>, (unsigned)rows, 32 * merge_warps(4), 0, stream, p);
+  return launch_early(q4_merge_kernel<D, 1>, (unsigned)((rows + kQ4Warps - 1) / kQ4Warps),
+                      32 * merge_warps(1), 0, stream, p);
 }
 
 // Up to this many tiles a pair is one CTA's, whatever the workspace: sharing it out

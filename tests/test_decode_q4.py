@@ -140,6 +140,17 @@ def test_long_and_split(D, heads, ws):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,heads", [(64, (4, 1, 1)), (128, (5, 1, 3))])
+@pytest.mark.parametrize("lens", [[4800], [5003, 3], [1700], [0, 1700, 40]])
+def test_one_long_sequence(D, heads, lens):
+    """Few pairs cut into many parts."""
+    Hq, Hkv, Sq = heads
+    c = Cache(lens, Hkv, D, 32, seed=4)
+    check(c, queries(len(lens), Hq, Sq, D))
+    check(c, queries(len(lens), Hq, Sq, D), window=4500, sink=40)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D,heads,seed", [(64, (2, 1, 1), 0), (128, (4, 2, 2), 1), (64, (9, 1, 1), 2)])
 def test_large_ragged_batches(D, heads, seed):
     """Hundreds of sequences, many of them empty or short, one long: the dealing
