@@ -13,7 +13,7 @@
 // shared memory (8 bytes per request), so blocks need nothing from one
 // another, one launch does it all, and the rest is two binary searches in
 // shared memory (GPU time: 64 requests with a token each 5 us, 500 prompts in 65536
-// places 10). The entries a block reads (below need(cached)) and the
+// places 9). The entries a block reads (below need(cached)) and the
 // entries any block writes (from there on) are disjoint.
 #include <cuda_runtime.h>
 
@@ -30,7 +30,9 @@ namespace mattn {
 namespace {
 
 constexpr int kPlanThreads = 256;
-constexpr int kPlanTokens = 1024;  // tokens per block and pass
+// Tokens that a block more is worth: it scans the lengths once more. 65536 places for 4000
+// requests: 512: 13.0 us, 1024: 14.2, 256: 19.4; 16000 with a token each: 16.3, 19.1, 14.9.
+constexpr int kPlanTokens = 512;
 constexpr int kPlanMaxB = 16384;   // 8 (B + 1) bytes of shared memory
 
 struct PlanArgs {
