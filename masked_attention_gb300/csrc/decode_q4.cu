@@ -127,17 +127,25 @@ __device__ __forceinline__ Q4Range q4_range(const Q4Problem& p, int b) {
   return r;
 }
 
-// cap tanh(s / cap), s and cap in log2 units, inv = 2 / cap (natural), as
-// cap - 2 cap / (1 + e^(2 s / cap)): off by at most 2^-22 cap. Where |s / cap| < 1/8
-// that would be many times the score's own rounding (a cap of 10^6: 0.2), so there it
-// is s (1 - x^2/3 + 2 x^4/15 - 17 x^6/315), x = s / cap, off by 2^-29 s.
+// Soft-cap: cap tanh(s / cap), s and cap in log2 units, inv = 2 / cap (natural).
+// Where |s / cap| < 1/4: s (1 - x^2/3 + 2 x^4/15 - 17 x^6/315 + 62 x^8/2835), x = s / cap,
+// off by 2^-26 s.
+constexpr float kCapNear = 0.25f * 2.0f / 0.69314718f;  // that bound on s inv
+__device__ __forceinline__ float soft_cap_near(float s, float inv) {
+  constexpr float kX2 = 0.25f * 0.69314718f * 0.69314718f;  // x = s inv ln 2 / 2
+  const float y = s * inv, y2 = y * y;
+  float p = fmaf(y2, 62.0f / 2835.0f * kX2 * kX2 * kX2 * kX2, -17.0f / 315.0f * kX2 * kX2 * kX2);
+  p = fmaf(y2, p, 2.0f / 15.0f * kX2 * kX2);
+  p = fmaf(y2, p, -1.0f / 3.0f * kX2);
+  return fmaf(s * y2, p, s);
+}
+
+// Anywhere: beyond that bound cap - 2 cap / (1 + e^(2 s / cap)), off by at most 2^-22 cap
+// (below it that would be many times the score's own rounding: 0.2 for a cap of 10^6).
 __device__ __forceinline__ float soft_cap(float s, float cap2, float inv) {
-  const float y = s * inv;  // x = y ln 2 / 2
+  const float y = s * inv;
   const float far = fmaf(-cap2, __fdividef(2.0f, 1.0f + ex2_approx(y)), cap2);
-  constexpr float kX2 = 0.25f * 0.69314718f * 0.69314718f;
-  const float x2 = kX2 * y * y;
-  const float near = s + s * x2 * fmaf(x2, fmaf(x2, -17.0f / 315.0f, 2.0f / 15.0f), -1.0f / 3.0f);
-  return x2 < 1.0f / 64.0f ? near : far;
+  return fabsf(y) < kCapNear ? soft_cap_near(s, inv) : far;
 }
 
 template <int D, int NT>
@@ -255,7 +263,7 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) {  // i = 0 or 1
 struct Q4Segment {
   int b, hkv;
   int len, win_tile, sink_tiles;
-  int v_first, n_tiles;  // this warp's first tile and its count (every kQ4Warps-th)
+  int v_last, n_tiles;   // this warp's last tile and its count (every kQ4Warps-th)
   long long slot;        // partial result, or -1: all of the pair's tiles
 };
 
@@ -374,8 +382,9 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
         sg.len = rg.len;
         sg.win_tile = rg.win_tile;
         sg.sink_tiles = rg.sink_tiles;
-        sg.v_first = v_begin + warp;
-        sg.n_tiles = sg.v_first < v_end ? (v_end - sg.v_first + kQ4Warps - 1) / kQ4Warps : 0;
+        const int v_first = v_begin + warp;
+        sg.n_tiles = v_first < v_end ? (v_end - v_first + kQ4Warps - 1) / kQ4Warps : 0;
+        sg.v_last = v_first + (sg.n_tiles - 1) * kQ4Warps;
         sg.slot = cut ? (long long)blockIdx.x + pair : -1;
         ++hkv;
         if (!p.ws_meta) b = p.B;  // one pair per CTA
@@ -396,8 +405,11 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
   uint4* qs = reinterpret_cast<uint4*>(smem + kQ4Warps * (C::kWarp + C::kState));  // [NT][G][32 lanes]
   float4* offs = reinterpret_cast<float4*>(qs + C::kQ / 16);                        // [NT][G][4]
   float* units = reinterpret_cast<float*>(offs + C::kOff / 16);                     // [NT * 8]
-  auto key_of = [&](const Q4Segment& sg, int i) {  // first key of the warp's tile i
-    const int v = sg.v_first + i * kQ4Warps;
+  // First key of the warp's tile i: the last keys come first, where scores that fall
+  // with the distance are largest, so that the reference stays (64 sequences x 8000 keys
+  // with ALiBi: 119 us, ascending 137; without: 116 and 119).
+  auto key_of = [&](const Q4Segment& sg, int i) {
+    const int v = sg.v_last - i * kQ4Warps;
     return (v < sg.sink_tiles ? v : v - sg.sink_tiles + sg.win_tile) * kQ4Tile;
   };
   auto look_up = [&](const Q4Segment& sg, int i0) -> int {
@@ -601,25 +613,43 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
         load_scales<G>(scales + C::kScales + (8 * i + g) * 2 * G, sv[i >> 1][i & 1]);
       // score modification and mask. Without a modification the scores stay in
       // the products' units and `unit` enters with the exponent.
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      auto each_score = [&](auto f) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = key0 + 16 * mt + 8 * (e >> 1) + g, i = pos[nt][e & 1];
-            float s = x[mt][nt][e];
-            if constexpr (SCORE != 0) s *= unit[nt][e & 1];
-            if constexpr ((SCORE & 1) != 0) s -= slope2[nt][e & 1] * float(i - j);
-            if constexpr ((SCORE & 2) != 0) s = soft_cap(s, p.softcap2, p.softcap_e);
-            if constexpr (kMask) {
-              bool keep = j < len && i >= 0;
-              if (causal) keep = keep && j <= i;
-              if (windowed) keep = keep && (i - j < p.window || j < p.sink);
-              s = keep ? s : -INFINITY;
-            }
-            x[mt][nt][e] = s;
-          }
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) f(x[mt][nt][e], nt, e, 16 * mt + 8 * (e >> 1));
+      };
+      if constexpr (SCORE != 0)
+        each_score([&](float& s, int nt, int e, int) { s *= unit[nt][e & 1]; });
+      if constexpr ((SCORE & 1) != 0) {
+        float dist[NT][2];  // to the lane's first key; conversions are slow, so one per row
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) dist[nt][e] = float(pos[nt][e] - key0 - g);
+        each_score([&](float& s, int nt, int e, int key) {
+          s = fmaf(-slope2[nt][e & 1], dist[nt][e & 1] - float(key), s);
+        });
+      }
+      if constexpr ((SCORE & 2) != 0) {
+        float big = 0.0f;
+        each_score([&](float& s, int, int, int) { big = fmaxf(big, fabsf(s)); });
+        // scores are mostly well below their cap
+        if (__all_sync(0xffffffffu, big * p.softcap_e < kCapNear))
+          each_score([&](float& s, int, int, int) { s = soft_cap_near(s, p.softcap_e); });
+        else
+          each_score([&](float& s, int, int, int) { s = soft_cap(s, p.softcap2, p.softcap_e); });
+      }
+      if constexpr (kMask)
+        each_score([&](float& s, int nt, int e, int key) {
+          const int j = key0 + key + g, i = pos[nt][e & 1];
+          bool keep = j < len && i >= 0;
+          if (causal) keep = keep && j <= i;
+          if (windowed) keep = keep && (i - j < p.window || j < p.sink);
+          s = keep ? s : -INFINITY;
+        });
       auto log2_of = [&](float s, int nt, int e) { return SCORE ? s : s * unit[nt][e]; };
       // The reference follows keys that pass its bound. First a quick bound: the
       // lane's largest score with its largest V scale, rounded up to a power of
