@@ -109,12 +109,19 @@ __device__ __forceinline__ uint4 pack(const float2 (&f)[P]) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The two chunks of a row that a lane holds: partners of the rotation where
-// they lie below rot_dim.
-template <int N>
+// they lie below rot_dim, else one in each half of what is left. Neighbouring lanes'
+// chunks are neighbours, so an access covers whole sectors (two neighbouring chunks
+// per lane: 165 against 124 us, interleaved, 15795 tokens x 88 heads of 64 fp32 channels).
+template <int N, int LANES>
 __device__ __forceinline__ void lane_chunks(const RopeArgs& a, bool inter, int part, int (&ch)[2]) {
   const int pairs = a.table && !inter ? a.rot / (2 * N) : 0;  // lanes with partners
-  ch[0] = part < pairs ? part * N : (2 * part) * N;
-  ch[1] = part < pairs ? part * N + a.rot / 2 : (2 * part + 1) * N;
+  if (part < pairs) {
+    ch[0] = part * N;
+    ch[1] = part * N + a.rot / 2;
+  } else {
+    ch[0] = (part + pairs) * N;
+    ch[1] = (part + LANES) * N;
+  }
 }
 
 // A token's rotation as the lane's channels see it:
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
   const int apart = warp / a.together;       // head item within the group
   const int spread = kRopeWarps / a.together;
   int ch[2];
-  lane_chunks<N>(a, kInter, lane % LANES, ch);
+  lane_chunks<N, LANES>(a, kInter, lane % LANES, ch);
   const int c0 = ch[0] * (16 / N), c1 = ch[1] * (16 / N);  // bytes
 
   for (int t = 0; t < 2; ++t) {
