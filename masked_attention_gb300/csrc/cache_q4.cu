@@ -39,8 +39,8 @@ constexpr int kCacheThreads = 256;
 constexpr int kCacheWarps = kCacheThreads / 32;
 constexpr int kCacheRows = 4;   // rows in flight per lane group
 constexpr int kCachePerSm = 3;  // blocks per SM. 16384 tokens x 8 heads of 128 channels, write and
-                                // read: 38 us; 2 rows at 4 blocks 42 us, 1 row at 6 blocks 46 us
-                                // (before their starts were programmatic: 33 us)
+                                // read: 33.7 us; 4 blocks 36.2; 2 rows at 4 blocks 35.5, 1 row
+                                // at 6 blocks 42.9
 
 struct CacheArgs {
   char* x[2];            // K and V rows (store: read, load: written)

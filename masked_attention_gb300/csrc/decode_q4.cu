@@ -47,13 +47,13 @@
 // With a window the tiles are those of the first `sink` keys, then those of the
 // window.
 //
-// 16 sequences of 32768 keys, 32 query and 8 key/value heads of 128: 119.6 us for the
-// call, 604 MB at 0.74 of a plain copy's rate. What bounds it is issue: 641 instructions
+// 16 sequences of 32768 keys, 32 query and 8 key/value heads of 128: 116.7 us for the
+// call, 604 MB at 0.76 of a plain copy's rate. What bounds it is issue: 635 instructions
 // per warp and tile, of which the tensor products hold the issue port about 8 slots each
-// (the products cut out, the same loads take 99.6 us; out of the L2 the whole takes 121).
-// Q K^T on tcgen05 instead (K's values unpacked into tensor memory as the 128-row
-// operand, q as the 16-wide one) took 139 us: the unpacking stays, and a block barrier
-// and a round trip through tensor memory per tile come on top.
+// (with the products cut out the same loads take 99.6 us, and the whole takes no less out
+// of the L2). Q K^T on tcgen05 instead (K's values unpacked into tensor memory as the
+// 128-row operand, q as the 16-wide one) took 139 us: the unpacking stays, and a block
+// barrier and a round trip through tensor memory per tile come on top.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -76,7 +76,7 @@ constexpr int kQ4Tile = 32;    // keys per warp step
 constexpr int kQ4Stages = 2;   // per-warp tile buffers
 constexpr int kQ4MaxRows = 16;
 // What a segment's start and end cost beside its tiles (61 ragged sequences of up to 15001
-// keys: 0: 151 us, 4: 140, 8: 131, 16: 124, 24: 127)
+// keys and a soft-cap: 10: 126 us, 12: 123, 16: 121, 24: 124; 0, before other steps, 27 more)
 constexpr int kQ4SegmentCost = 16;
 constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
@@ -168,9 +168,9 @@ struct Q4Cfg {
 };
 
 // CTAs per SM that the registers are cut to. What is measured is issue, not
-// latency: one more CTA at fewer registers spills and is slower (16 x 32768 keys,
-// D = 128: 123 us, with four 134; one product of 16 query rows: 102 with two, 106 with three;
-// D = 64: 80 with four, 86 with five).
+// latency: one more CTA at fewer registers spills and is slower (16 x 32768 keys, 8
+// key/value heads of 128: 117 us, with two 126, with four 123; with 16 query rows each
+// 173, with three 184; 32 x 32768 keys, heads of 64: 143, with three 147, with five 155).
 template <int D, int NT>
 constexpr int q4_per_sm() {
   return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);

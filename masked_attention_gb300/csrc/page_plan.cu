@@ -13,7 +13,7 @@
 // shared memory (8 bytes per request), so blocks need nothing from one
 // another, one launch does it all, and the rest is two binary searches in
 // shared memory (GPU time: 64 requests with a token each 5 us, 500 prompts in 65536
-// places 9). The entries a block reads (below need(cached)) and the
+// places 8). The entries a block reads (below need(cached)) and the
 // entries any block writes (from there on) are disjoint.
 #include <cuda_runtime.h>
 
