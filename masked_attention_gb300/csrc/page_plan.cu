@@ -218,7 +218,8 @@ MATTN_API attn_status attn_page_plan(const int* cached_lens, const int* new_lens
     for (int j = i + 1; j < kRanges; ++j) {
       const uintptr_t a = reinterpret_cast<uintptr_t>(ranges[i].at);
       const uintptr_t b = reinterpret_cast<uintptr_t>(ranges[j].at);
-      if (a < b + ranges[j].bytes && b < a + ranges[i].bytes) return ATTN_ERR_INVALID_ARG;
+      if (ranges[i].bytes && ranges[j].bytes && a < b + ranges[j].bytes && b < a + ranges[i].bytes)
+        return ATTN_ERR_INVALID_ARG;
     }
   static DeviceOnce ready;
   const cudaError_t err = ready.allow_smem(page_plan_kernel, 2 * (kPlanMaxB + 1) * (int)sizeof(int));

@@ -326,6 +326,23 @@ def test_infinities_and_nan_in_queries(D, ws):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,Hkv", [(64, 8), (128, 4)])
+def test_pool_past_32_bits(D, Hkv):
+    """The same records beyond 4 GiB of a larger pool: the same bits."""
+    import masked_attention_gb300 as M
+    c = Cache([1500, 70], Hkv, D, 128, seed=31)
+    q = queries(2, 2 * Hkv, 1, D)
+    o, lse = check(c, q)
+    small = c.pool
+    first = (1 << 32) // small[0].size + 3
+    pool = torch.zeros(first + len(small), *small.shape[1:], dtype=torch.uint8, device="cuda")
+    pool[first:] = torch.from_numpy(small).cuda()
+    c.table = np.where(c.table < 0, -1, c.table + first).astype(np.int32)
+    o2, lse2 = run(c, q, M.MASK_CAUSAL, "full", pool=pool)
+    assert np.array_equal(o, o2) and np.array_equal(lse, lse2)
+
+
+@pytest.mark.gpu
 def test_pages_outside_the_pool_read_zeros():
     """Bad table entries: their keys have K = V = 0 (as attn_decode reads them)."""
     c = Cache([100, 64], 2, 64, 16, seed=18)

@@ -175,6 +175,30 @@ def test_without_parts(dtype, kw):
 
 
 @pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Batch elements 4 GiB apart, in and out: the bits of a compact call."""
+    import masked_attention_gb300 as M
+    B, H, S, D = 2, 3, 5, 128
+    c = Case(B, S, H, H, D, fused=False)
+
+    def far(x=None):
+        t = torch.empty((1 << 31) + H * S * D, dtype=c.dtype, device="cuda").as_strided(
+            (B, H, S, D), (1 << 31, S * D, D, 1))
+        return t if x is None else t.copy_(x)
+
+    outs = check_forward(c)
+    o = far()
+    M.attn_qk_norm_rope(far(c.dq), None, o, None, **c.kwargs())
+    assert torch.equal(o, outs[0])
+    (gq, _), _ = check_backward(c)
+    dx, dw = far(), torch.empty(D, device="cuda")
+    ws = torch.empty(M.attn_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8, device="cuda")
+    M.attn_qk_norm_rope_bwd(far(c.dq), None, far(c.gq.cuda()), None, dx, None, dq_weight=dw,
+                            workspace=ws, **c.kwargs())
+    assert torch.equal(dx, gq)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_rows_outside_the_table(dtype):
     """Padded places (position -1 or past the table): not written, no share in

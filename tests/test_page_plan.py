@@ -148,6 +148,24 @@ def test_oracle_plan_by_hand():
     assert tab.tolist() == [[8, 2, -7], [5, 6, 9]] and info.tolist() == [5, 2, 0, 0]
 
 
+@pytest.mark.gpu
+def test_empty_arguments_overlap_nothing():
+    """An empty free list may begin anywhere, inside an output too."""
+    import masked_attention_gb300 as M
+    d = {n: torch.zeros(64, dtype=torch.int32, device="cuda")
+         for n in ("cached", "new", "table", "lens", "cu", "slots", "pos", "ids", "info")}
+    d["cached"][:2] = torch.tensor([3, 5])
+    d["new"][:2] = 1
+    d["table"][[0, 4]] = torch.tensor([7, 2], dtype=torch.int32, device="cuda")
+    a = {n: t.data_ptr() for n, t in d.items()}
+    stream = torch.cuda.current_stream().cuda_stream
+    assert M.lib().attn_page_plan(a["cached"], a["new"], 2, a["table"], 4, 16, a["lens"] + 4, 0,
+                                  a["lens"], a["cu"], a["slots"], a["pos"], a["ids"], 2, a["info"],
+                                  stream) == M.ATTN_OK
+    assert d["lens"][:2].tolist() == [4, 6] and d["info"][:4].tolist() == [2, 0, 0, 0]
+    assert d["slots"].view(torch.int64)[:2].tolist() == [7 * 16 + 3, 2 * 16 + 5]
+
+
 def test_overlapping_arguments_are_refused():
     """The lengths in place, the natural mistake, and neighbours that run into
     one another."""
