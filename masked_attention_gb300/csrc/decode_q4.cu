@@ -483,19 +483,18 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     const int len = cur.len, first_pos = len - p.Sq;  // absolute position of query row 0
     const size_t row0 = (size_t)(cur.b * p.Hq + cur.hkv * group) * p.Sq;
 
-    // Meanwhile warp 0 prepares q^T's fragments (B operand) in shared memory, in
-    // fp16: a row is scaled by a power of two that brings its largest channel to
-    // [2^14, 2^15), so bf16's 8 bits are exact (channels 2^28 times smaller lose
-    // bits below 2^-39 of the largest). Channel order of a lane's 8 per group: pairs
-    // (0, 4), (1, 5) | (2, 6), (3, 7). Rows past R are 0.
-    if (warp == 0) {
+    // Meanwhile q^T's fragments (B operand) are prepared in shared memory, in fp16,
+    // each warp a fourth of them: a row is scaled by a power of two that brings its
+    // largest channel to [2^14, 2^15), so bf16's 8 bits are exact (channels 2^28 times
+    // smaller lose bits below 2^-39 of the largest). Channel order of a lane's 8 per
+    // group: pairs (0, 4), (1, 5) | (2, 6), (3, 7). Rows past R are 0.
+    {
       const __nv_bfloat16* Q = static_cast<const __nv_bfloat16*>(p.q) + row0 * D;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g;
         uint4 x[G];
-        float big = 0.0f;
-        bool odd = false;  // a NaN, which fmaxf passes over
+        uint32_t m2 = 0;  // largest |q| as bits, two at a time: ordered like the values, NaN last
 #pragma unroll
         for (int a = 0; a < G; ++a) {
           x[a] = make_uint4(0, 0, 0, 0);
@@ -503,22 +502,19 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
             x[a] = *reinterpret_cast<const uint4*>(Q + (size_t)r * D + 32 * a + 8 * t);
           const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            for (int e = 0; e < 2; ++e) {
-              big = fmaxf(big, fabsf(scale_of(u[i], e)));
-              odd = odd || isnan(scale_of(u[i], e));
-            }
+          for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, u[i] & 0x7fff7fffu);
         }
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        odd = __ballot_sync(0xffffffffu, odd) & (0xfu << (lane & 28));
-        const bool fine = big < INFINITY && !odd;
-        const int ex = max((int)(__float_as_uint(big) >> 23) - 127, -100);  // floor(log2 big)
+        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+        m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 2));
+        const uint32_t big = max(m2 & 0xffff0000u, m2 << 16);
+        const bool fine = big < 0x7f800000u;
+        const int ex = max((int)(big >> 23) - 127, -100);  // floor(log2)
         const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
         // scores per product, log2; a row with an infinity or NaN scores NaN
-        if (t == 0) units[r] = fine ? exp2f((float)(ex - 14)) * p.scale2 : NAN;
+        if (warp == 0 && t == 0) units[r] = fine ? exp2f((float)(ex - 14)) * p.scale2 : NAN;
 #pragma unroll
         for (int a = 0; a < G; ++a) {
+          if ((nt * G + a) % kQ4Warps != warp) continue;
           const uint32_t u[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
           float c[8], sum = 0.0f;
 #pragma unroll
@@ -799,29 +795,34 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
                 make_float2(o[a][jp][nt][e], o[a][jp][nt][e + 2]);
     }
     __syncthreads();
-    for (int idx = threadIdx.x; idx < R * D; idx += kQ4Threads) {
-      const int r = idx / D, c = idx % D;
+    for (int idx = threadIdx.x; idx < R * (D / 4); idx += kQ4Threads) {
+      const int r = idx / (D / 4), c = idx % (D / 4) * 4;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kQ4Warps; ++w)
         M = fmaxf(M, states[w * (C::kState / 4) + r]);
-      float Ls = 0.0f, acc = 0.0f;
+      float Ls = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kQ4Warps; ++w) {
         const float* st = states + w * (C::kState / 4);
         const float wt = M != -INFINITY ? ex2_approx(st[r] - M) : 1.0f;  // -inf -> 0
+        const float4 x = *reinterpret_cast<const float4*>(st + 2 * kR + r * D + c);
         Ls += wt * st[kR + r];
-        acc += wt * st[2 * kR + r * D + c];
+        acc = make_float4(acc.x + wt * x.x, acc.y + wt * x.y, acc.z + wt * x.z, acc.w + wt * x.w);
       }
       // a row without a key: O = 0, LSE = -inf. NaN sums pass through.
-      const float out = Ls == 0.0f ? 0.0f : acc / Ls;
-      const float lse2 = Ls == 0.0f ? -INFINITY : M + __log2f(Ls);
+      const bool none = Ls == 0.0f;
+      const float lse2 = none ? -INFINITY : M + __log2f(Ls);
+      acc = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                 : make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
       if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
       if (cur.slot >= 0) {
-        p.ws_o[((size_t)cur.slot * R + r) * D + c] = out;
+        *reinterpret_cast<float4*>(p.ws_o + ((size_t)cur.slot * R + r) * D + c) = acc;
         if (c == 0) p.ws_lse[(size_t)cur.slot * R + r] = lse2;
       } else {
-        static_cast<__nv_bfloat16*>(p.o)[(row0 + r) * D + c] = __float2bfloat16_rn(out);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (row0 + r) * D + c) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
         if (c == 0) p.lse[row0 + r] = lse2 * kLn2;
       }
     }
