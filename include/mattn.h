@@ -336,8 +336,8 @@ attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view* k, const 
  *   V codes  [page_size][D / 2]   b, channel 2b + 1 in the high one
  *   K scales [page_size][D / 32]  bf16, one per 32 consecutive channels
  *   V scales [page_size][D / 32]  bf16
- * and a code n stands for (n - 8) * scale (4.5 bits an element). D is 64 or
- * 128, page_size 16, 32, 64 or 128. The pool is 16-byte aligned. */
+ * and a code n stands for (n - 8) * scale (4.5 bits an element). Scales are
+ * not negative. D is 64 or 128, page_size 16, 32, 64 or 128. The pool is 16-byte aligned. */
 size_t attn_cache_q4_bytes(int num_pages, int Hkv, int page_size, int D);
 
 /* Writes K and V rows (bf16 [B, Hkv, S, D], strides of their own) to slots
@@ -374,7 +374,12 @@ attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
  *   keep(i, j) = j < seq_len AND i >= 0 AND (CAUSAL: j <= i)
  *                AND (WINDOW: i - j < window OR j < sink)
  * Keys that no row sees are not read, and what a masked key's record holds,
- * NaN included, changes nothing. A row without a key (an empty place of the
+ * NaN included, changes nothing. Products run on the codes, exact in fp16, and
+ * sums are fp32. A query row is scaled by a power of two and rounded to fp16:
+ * exact but for channels 2^28 and more below its largest, whose bits below 2^-38
+ * of that are lost. A probability times its V scale is rounded to 11 bits, and
+ * sums of a group of 32 channels drop what lies 2^-25 below its largest such
+ * product; the groups may differ in size by up to 2^100. A row without a key (an empty place of the
  * batch) gets O = 0, LSE = -inf. A page index outside [0, num_pages) reads as
  * zeros. With a workspace the keys of all sequences are shared out evenly over
  * the SMs, and results of sequences that several CTAs share are joined from it:

@@ -30,9 +30,15 @@
 // P is rounded to fp16 after the V scale multiplied it: with y = score +
 // log2(scale of the key's largest V group), the running reference m keeps
 // 2^(y - m) <= 2^15 and at 2^8 for the largest key when m last moved, so fp16's
-// 11 bits hold over 22 binades below the largest weight. m moves (and O and l
-// are rescaled) only when a key passes that bound, which one vote per 32 keys
-// decides. Sums are fp32.
+// 11 bits hold over 22 binades below the largest weighted scale of all groups, and
+// 14 below that of each group while no key's V scales lie 2^8 or more apart. From the first
+// tile on where a visible key's do (or are zero in a group that has values in other keys,
+// or below 2^-98), a warp rounds P to two bf16 parts instead, which have 16 bits and
+// fp32's range for every group by itself (16 sequences x 32768 keys: 163 us against 117;
+// the test, a window of 8 binades that scales stay in, is not seen there and costs up to
+// 2 % with a soft-cap). Groups that are zero in every key stay with fp16.
+// m moves (and O and l are rescaled) only when a key passes its bound, which one vote per
+// 32 keys decides. Sums are fp32.
 //
 // The tiles of 32 keys of all (sequence, key/value head) pairs, one after the
 // other, are dealt out evenly: CTA c of C takes tiles [c N / C, (c + 1) N / C), so
@@ -82,6 +88,12 @@ constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
 constexpr uint32_t kQ4Tiny = 0x12801280u;  // bf16 2^-90, twice: smaller V scales count as this,
                                            // so that unscaled weights stay within fp32
+constexpr uint32_t kQ4Spread = 8u << 7;    // a key's V scales may lie this far apart, as bf16
+                                           // bits (2^8), for weights in fp16
+constexpr uint32_t kQ4Outside = 0xfc00fc00u;  // bits of a distance of kQ4Spread or more, twice
+// Lower ends of such windows that hold, of scales >= 0 (NaN aside), 0 alone (and
+// 2^-133, where the lower half borrows) and none.
+constexpr uint32_t kQ4NoValues = 0xfc01u, kQ4Apart = 0xfc00fc00u;
 
 struct Q4Problem {
   const void* q;
@@ -210,6 +222,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 // (x & mask) | bits in one instruction.
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
   uint32_t y;
@@ -234,6 +255,18 @@ __device__ __forceinline__ void nibble_pairs(uint32_t w, uint32_t (&f)[4]) {
     const uint32_t off = j & 1 ? 0x54805480u : 0x64086408u;         // 72, 1032
     const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&raw),
                               *reinterpret_cast<const __half2*>(&off));
+    f[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Nibbles 0 to 3 of both halves of w as exact bf16 pairs (n - 8, n' - 8): the
+// nibble's bits in the mantissa of 128, less 136.
+__device__ __forceinline__ void nibble_pairs_bf16(uint32_t w, uint32_t (&f)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t raw = and_or(w >> (4 * j), 0x000f000fu, 0x43004300u), off = 0x43084308u;
+    const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&raw),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&off));
     f[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
@@ -563,6 +596,12 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
       m[nt][0] = m[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.0f;
     }
+    // The 8 binades that the V scales of the warp's keys lie in: the bf16 bits of their lower
+    // end (kQ4NoValues: the group is zero), of two groups to a word, and log2 of their upper
+    // end. Where a tile's do not, they are looked at key by key. 0: no key yet; kQ4Apart: a
+    // key's scales lay too far apart for weights in fp16.
+    uint32_t low[G / 2] = {};
+    float lsm = 0.0f;
 
     // One tile of 32 keys. kMask: some (key, row) pair of it is masked.
     auto process = [&](const uint32_t stage_off, const int key0, auto mask_tag) {
@@ -648,18 +687,13 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
         });
       auto log2_of = [&](float s, int nt, int e) { return SCORE ? s : s * unit[nt][e]; };
       // The reference follows keys that pass its bound. First a quick bound: the
-      // lane's largest score with its largest V scale, rounded up to a power of
-      // two (a negative or NaN scale counts as huge).
-      uint32_t sm = kQ4Tiny;
+      // lane's largest score with the upper end of the window that V scales lie in. Whether
+      // the tile's do, each lane tests for one key.
+      uint32_t out = 0, mine[G / 2];
+      load_scales<G>(scales + C::kScales + lane * 2 * G, mine);
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < G / 2; ++i) sm = __vmaxu2(sm, sv[mt][e][i]);
-      sm = max(sm, sm << 16);
-      const float lsm = (float)(int)(sm >> 23) - 126.0f;
-      bool over = false;
+      for (int i = 0; i < G / 2; ++i) out |= mine[i] - low[i];
+      bool over = (out & kQ4Outside) != 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -667,7 +701,56 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
           const float y = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
           over = over || log2_of(y, nt, e) + lsm > m[nt][e] + kQ4Head;
         }
+      auto weights = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float& s = x[k >> 1][nt][e + 2 * (k & 1)];
+              s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
+              l[nt][e] += s;
+            }
+          }
+      };
       if (__any_sync(0xffffffffu, over)) {
+        if (low[0] != kQ4Apart) {
+          uint32_t hi = kQ4Tiny >> 16, lo = 0xffffu, held = 0;  // of the lane's key
+#pragma unroll
+          for (int a = 0; a < G; ++a) {
+            const uint32_t s = mine[a / 2] >> (a & 1 ? 16 : 0) & 0x7fffu;
+            hi = max(hi, s);
+            lo = min(lo, s - 1);  // a zero is the largest here
+            held |= s ? 1u << a : 0u;
+          }
+          bool seen = true;  // by some row
+          if constexpr (kMask) {
+            const int j = key0 + lane, i = max(max(first_pos, 0), causal ? j : 0);
+            seen = j < len && (!windowed || i - j < p.window || j < p.sink);
+          }
+          const bool far = seen && (!held || hi - lo > kQ4Spread);
+          const uint32_t top = __reduce_max_sync(0xffffffffu, seen ? hi : 0u) >> 7;  // 0: no key
+          const uint32_t some = __reduce_or_sync(0xffffffffu, seen ? held : 0u);
+          const uint32_t every = __reduce_and_sync(0xffffffffu, seen ? held : ~0u);
+          uint32_t before = some;  // the groups that had values, if a key was there
+          if (low[0]) {
+            before = 0;
+#pragma unroll
+            for (int a = 0; a < G; ++a)
+              before |= (low[a / 2] >> (a & 1 ? 16 : 0) & 0xffffu) != kQ4NoValues ? 1u << a : 0u;
+          }
+          if (__any_sync(0xffffffffu, far) || (top && (some != every || some != before))) {
+            low[0] = kQ4Apart;
+          } else if (top) {
+            lsm = (float)(int)top - 126.0f;
+#pragma unroll
+            for (int i = 0; i < G / 2; ++i)
+              low[i] = (some >> (2 * i) & 1 ? (top - 7) << 7 : kQ4NoValues) |
+                       (some >> (2 * i + 1) & 1 ? (top - 7) << 7 : kQ4NoValues) << 16;
+          }
+        }
         float lsv[2][2];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -702,19 +785,45 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
                 o[a][jp][nt][e + 2] *= c;
               }
           }
-      }
+        if (low[0] == kQ4Apart) {  // O^T += V^T P^T, P as the sum of two bf16 halves
+          weights();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int a = 0; a < G; ++a) {
+            uint32_t w[4];
+            ldsm4_t((rows ^ (a * 16)) + C::kCodes, w);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
+            for (int mt = 0; mt < 2; ++mt) {
+              uint32_t f[2][4];
+              nibble_pairs_bf16(w[2 * mt], f[0]);
+              nibble_pairs_bf16(w[2 * mt + 1], f[1]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float& s = x[k >> 1][nt][e + 2 * (k & 1)];
-            s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
-            l[nt][e] += s;
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t b[2][2];  // [keys' half][the larger part, what it leaves]
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float s = scale_of(sv[mt][e][a / 2], a & 1);
+                  float p0 = x[mt][nt][2 * e] * s, p1 = x[mt][nt][2 * e + 1] * s;
+                  if constexpr (kMask) {
+                    p0 = x[mt][nt][2 * e] > 0.0f ? p0 : 0.0f;
+                    p1 = x[mt][nt][2 * e + 1] > 0.0f ? p1 : 0.0f;
+                  }
+                  const uint32_t big = pack_bf16x2(p0, p1);
+                  b[e][0] = transpose8(big);
+                  b[e][1] = transpose8(pack_bf16x2(p0 - scale_of(big, 0), p1 - scale_of(big, 1)));
+                }
+#pragma unroll
+                for (int jp = 0; jp < 2; ++jp)
+#pragma unroll
+                  for (int part = 0; part < 2; ++part)
+                    mma_bf16(o[a][jp][nt], f[0][2 * jp], f[0][2 * jp + 1], f[1][2 * jp],
+                             f[1][2 * jp + 1], b[0][part], b[1][part]);
+              }
+            }
           }
+          return;
         }
+      }
+      weights();
       // O^T += V^T P^T
 #pragma unroll
       for (int a = 0; a < G; ++a) {

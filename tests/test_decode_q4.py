@@ -476,3 +476,87 @@ def test_refusals():
     assert dec(q=0x1008) == dec(ws=0x100010, n=4096) == dec(alibi_slopes=0x5001) == mis
     assert dec(B=0) == dec(Sq=0) == M.ATTN_OK
     assert M.attn_decode_q4_workspace_bytes(1, 4, 2, 1, 0, 64) == 0
+
+
+def group_factors(pattern, j, n, G):
+    """Sizes of the G channel groups of value row j of n."""
+    f = np.ones(G)
+    if pattern == "steady":
+        f = np.array([1.0, 2.0 ** -24, 2.0 ** -60, 2.0 ** 6])[:G]
+    elif pattern == "far":
+        f = np.array([2.0 ** -50, 2.0 ** 40, 1.0, 2.0 ** 10])[:G]
+    elif pattern == "first half":      # keys are processed from the last one
+        f[1] = 2.0 ** 30 if j < n // 2 else 1.0
+    elif pattern == "second half":
+        f[1] = 2.0 ** 30 if j >= n // 2 else 1.0
+    elif pattern == "in turn":
+        f[j % G] = 2.0 ** 24
+    elif pattern == "a zero group":
+        f[1] = 0.0
+    elif pattern == "zero in most keys":
+        f[1] = 2.0 ** -30 if j % 7 == 0 else 0.0
+    elif pattern == "zero in late keys":
+        f[0] = 2.0 ** -30 if j < n // 2 else 0.0
+    elif pattern == "tiny":
+        f[:] = 2.0 ** -112
+    elif pattern == "tiny in late keys":
+        f[:] = 1.0 if j < n // 2 else 2.0 ** -112
+    return f
+
+
+GROUP_PATTERNS = ["steady", "far", "first half", "second half", "in turn", "a zero group",
+                  "zero in most keys", "zero in late keys", "tiny", "tiny in late keys"]
+
+
+def check_groups(c, q, ws="full", window=0, sink=0):
+    """Like check(), each channel group held to its own size. A weight is rounded to fp16 times
+    its group's scale, which is at least 2^-8 of the key's largest, and 2^8 is the largest such
+    product of a row: what a subnormal loses, half a step of 2^-24, is at most 2^-25 of the
+    group's largest product for each key (a quantised group's largest code is 7 of at most 8)."""
+    import masked_attention_gb300 as M
+    o, lse = run(c, q, M.MASK_CAUSAL | (M.MASK_WINDOW if window else 0), ws, window=window, sink=sink)
+    B, Hq, Sq, D = q.shape
+    qn = q.double().numpy()
+    O, L, A = decode_q4(qn, c.pool, c.table, c.lens, c.page, window=window, sink=sink)
+    w = D // 32 * 2
+    sk = bf16_value(np.ascontiguousarray(c.pool[:, :, c.page * D:c.page * (D + w)]).view(np.uint16))
+    top = float(np.abs(sk[np.isfinite(sk)]).max())
+    eps = (2.0 ** -18 * 144 + 2.0 ** -20 * 8) * np.abs(qn).sum(-1) * top * D ** -0.5
+    f = (np.expm1(2 * eps) + 2.0 ** -11 + 2.0 ** -18)[..., None]
+    size = np.repeat(A.reshape(B, Hq, Sq, D // 32, 32).max(-1), 32, -1)
+    tol = (2.0 ** -8 * np.abs(O) + f * A * (1 + 2.0 ** -8) + c.lens.max() * 2.0 ** -25 * 8 / 7 * size
+           + 2.0 ** -134)   # and half of bf16's smallest step
+    assert (np.abs(lse - L) <= 2 * eps + 2.0 ** -20 * (1 + np.abs(L))).all()
+    with np.errstate(invalid="ignore", divide="ignore"):
+        assert (np.abs(o - O) <= tol).all(), float(np.nanmax(np.abs(o - O) / tol))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pattern", GROUP_PATTERNS)
+@pytest.mark.parametrize("D,heads,n", [(64, (4, 1, 1), 150), (128, (4, 1, 1), 150),
+                                       (128, (6, 1, 2), 97), (64, (4, 1, 1), 1500)])
+def test_groups_keep_their_own_precision(pattern, D, heads, n):
+    """Channel groups of unlike size, in all keys, in some, and without values: each one's
+    outputs are as precise as if it were alone."""
+    Hq, Hkv, Sq = heads
+    page = 16
+    c = Cache([n], Hkv, D, page, seed=33)
+    rng = np.random.default_rng(7)
+    for j in range(n):
+        k, v = rng.normal(size=(2, D))
+        v = v * np.repeat(group_factors(pattern, j, n, D // 32), 32)
+        q4_write(c.pool, c.table[0, j // page] * page + j % page, 0, k, v, page)
+    check_groups(c, queries(1, Hq, Sq, D))
+    check_groups(c, queries(1, Hq, Sq, D), window=70, sink=5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", [3, 60, 99])
+def test_a_heavy_key_without_values(where):
+    """A key that takes nearly all of the weight (it scores 85, the others about 0) and whose
+    values are zero: the others' share of about 2^-122 is what O is."""
+    D, n, page = 64, 100, 16
+    c = Cache([n], 1, D, page, seed=34)
+    q4_write(c.pool, c.table[0, where // page] * page + where % page, 0, np.full(D, 10.6),
+             np.zeros(D), page)
+    check_groups(c, bf16(np.full((1, 2, 1, D), 1.0)))
