@@ -376,18 +376,18 @@ attn_status attn_cache_load_q4(const void* pool, int num_pages, int page_size,
  * Keys that no row sees are not read, and what a masked key's record holds,
  * NaN included, changes nothing. Products run on the codes, exact in fp16, and
  * sums are fp32. A query row is scaled by a power of two and rounded to fp16:
- * exact but for channels 2^28 and more below its largest, whose bits below 2^-38
- * of that are lost. A probability times its V scale is rounded to 11 bits, and
- * sums of a group of 32 channels drop what lies 2^-25 below its largest such
- * product; the groups may differ in size by up to 2^100. A row without a key (an empty place of the
- * batch) gets O = 0, LSE = -inf. A page index outside [0, num_pages) reads as
- * zeros. With a workspace the keys of all sequences are shared out evenly over
- * the SMs, and results of sequences that several CTAs share are joined from it:
- * 256-byte aligned device memory, attn_decode_q4_workspace_bytes() for the full
- * spread, less or NULL means fewer CTAs (one per sequence and key/value head
- * with NULL); its contents need not be kept between calls, and calls that may
- * run at the same time need one each. ATTN_ERR_UNSUPPORTED for B * Hkv > 65535 or
- * max_len > INT_MAX - 255. */
+ * exact but for channels 2^28 and more below its largest, whose bits below 2^-38 of
+ * that are lost. A probability times its V scale is rounded to 11 bits, and sums of
+ * a group of 32 channels drop what lies 2^-25 below its largest such product; the
+ * groups may differ in size by up to 2^100. A row without a key (an empty place of
+ * the batch) gets O = 0, LSE = -inf. A page index outside [0, num_pages) reads as
+ * zeros. With a workspace the keys of all sequences are shared out evenly over the
+ * SMs, and results of sequences that several CTAs share are joined from it: 256-byte
+ * aligned device memory, attn_decode_q4_workspace_bytes() for the full spread, less
+ * or NULL means fewer CTAs (one per sequence and key/value head with NULL); its
+ * contents need not be kept between calls, and calls that may run at the same time
+ * need one each. ATTN_ERR_UNSUPPORTED for B * Hkv > 65535 or max_len > INT_MAX -
+ * 255. */
 attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse, int B, int Hq,
                            int Hkv, int Sq, int max_len, int D, unsigned variant,
                            const attn_params* p, const int* seq_lens, int sink, void* workspace,

@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
           const float y = fmaxf(fmaxf(x[0][nt][e], x[0][nt][e + 2]), fmaxf(x[1][nt][e], x[1][nt][e + 2]));
           over = over || log2_of(y, nt, e) + lsm > m[nt][e] + kQ4Head;
         }
-      auto weights = [&]() {
+      auto weights = [&]() {  // a masked key's is -0, one too small for fp32 +0
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -710,8 +710,10 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float& s = x[k >> 1][nt][e + 2 * (k & 1)];
+              const bool masked = kMask && s == -INFINITY;
               s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
               l[nt][e] += s;
+              if (masked) s = -0.0f;
             }
           }
       };
@@ -804,8 +806,8 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
                   const float s = scale_of(sv[mt][e][a / 2], a & 1);
                   float p0 = x[mt][nt][2 * e] * s, p1 = x[mt][nt][2 * e + 1] * s;
                   if constexpr (kMask) {
-                    p0 = x[mt][nt][2 * e] > 0.0f ? p0 : 0.0f;
-                    p1 = x[mt][nt][2 * e + 1] > 0.0f ? p1 : 0.0f;
+                    p0 = signbit(x[mt][nt][2 * e]) ? 0.0f : p0;
+                    p1 = signbit(x[mt][nt][2 * e + 1]) ? 0.0f : p1;
                   }
                   const uint32_t big = pack_bf16x2(p0, p1);
                   b[e][0] = transpose8(big);
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
             for (int e = 0; e < 4; ++e) {
               pv[e] = x[mt][nt][e] * scale_of(sv[mt][e >> 1][a / 2], a & 1);
               // a masked key adds nothing, whatever its scale holds
-              if constexpr (kMask) pv[e] = x[mt][nt][e] > 0.0f ? pv[e] : 0.0f;
+              if constexpr (kMask) pv[e] = signbit(x[mt][nt][e]) ? 0.0f : pv[e];
             }
             const uint32_t b0 = transpose8(pack_f16x2(pv[0], pv[1]));
             const uint32_t b1 = transpose8(pack_f16x2(pv[2], pv[3]));

@@ -560,3 +560,19 @@ def test_a_heavy_key_without_values(where):
     q4_write(c.pool, c.table[0, where // page] * page + where % page, 0, np.full(D, 10.6),
              np.zeros(D), page)
     check_groups(c, bf16(np.full((1, 2, 1, D), 1.0)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heavy,j", [(20, 5), (36, 33), (36, 5), (20, 38)])
+def test_nan_values_of_a_visible_key_without_weight(heavy, j):
+    """The weight of a key that scores 1600 below the largest is 0, and NaN times it is NaN,
+    in a tile whose keys are all visible (keys 0 to 31) as in one that ends the sequence."""
+    import masked_attention_gb300 as M
+    D, n, page = 64, 40, 16
+    c = Cache([n], 1, D, page, seed=35)
+    for at in range(n):
+        q4_write(c.pool, c.table[0, at // page] * page + at % page, 0,
+                 np.full(D, 100.0 if at == heavy else -100.0), np.ones(D), page)
+    c.set_scales(0, j, 1, 0x7fff)
+    o, lse = run(c, bf16(np.full((1, 2, 1, D), 1.0)), M.MASK_CAUSAL, "none")
+    assert np.isnan(o).all() and np.isfinite(lse).all()
