@@ -209,7 +209,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
   const int c0 = ch[0] * (16 / N), c1 = ch[1] * (16 / N);  // bytes
 
   for (int t = 0; t < 2; ++t) {
-    if (a.H[t] == 0) continue;
+    if (a.H[t] == 0) {  // no rows: their share of a weight gradient is 0
+      if constexpr (kBwd)
+        for (int c = threadIdx.x; c < D; c += kRopeThreads)
+          a.part[(size_t)blockIdx.x * 2 * D + t * D + c] = 0.0f;
+      continue;
+    }
     const bool norm = a.w[t] != nullptr;
     auto weight = [&](int k, int i) {
       return norm ? make_float2(a.w[t][ch[k] + 2 * i], a.w[t][ch[k] + 2 * i + 1]) : both(1.0f);

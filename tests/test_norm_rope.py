@@ -390,3 +390,32 @@ def test_refusals():
         M.attn_qk_norm_rope(t, t, t, t)                   # not on a GPU
     with pytest.raises(ValueError):
         M.attn_qk_norm_rope(t.half(), t, t, t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("without", ["keys", "queries"])
+def test_weight_gradient_of_a_side_without_heads(without, dtype, D):
+    """A sum over no rows is 0, whatever the workspace held."""
+    import masked_attention_gb300 as M
+    c = Case(B=2, S=70, Hq=3, Hkv=3, D=D, dtype=dtype)
+    (dq, dk), (dwq, dwk) = check_backward(c)
+    ws = torch.full((M.attn_qk_norm_rope_bwd_workspace_bytes(D),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    dws = [torch.full((D,), 5.0, device="cuda") for _ in (0, 1)]
+    gq, gk, kw = c.gq.cuda(), c.gk.cuda(), c.kwargs()
+    kw.update(dq_weight=dws[0], dk_weight=dws[1], workspace=ws)
+    if without == "keys":
+        out = torch.empty_like(dq)
+        M.attn_qk_norm_rope_bwd(c.dq, None, gq, None, out, None, **kw)
+        assert torch.equal(out, dq) and (dws[1] == 0).all()
+        size = turned_size(f64(c.gq), c) * np.abs(f64(c.q)) / np.sqrt(
+            (f64(c.q) ** 2).mean(-1, keepdims=True))
+        # another order of the sum than with the keys' rows: twice the sum's own bound
+        tol = 2 * (size[..., 0].size + 16) * 2.0 ** -24 * size.sum((0, 1, 2))
+        assert (np.abs(f64(dws[0].cpu()) - f64(dwq.cpu())) <= tol).all()
+    else:
+        none, out = c.dq[:, :0], torch.empty_like(dk)
+        M.attn_qk_norm_rope_bwd(none, c.dk, gq[:, :0], gk, none, out, **kw)
+        assert torch.equal(out, dk) and (dws[0] == 0).all() and torch.isfinite(dws[1]).all()
