@@ -127,17 +127,23 @@ __device__ __forceinline__ void lane_chunks(const RopeArgs& a, bool inter, int p
 // A token's rotation as the lane's channels see it:
 //   z0 = c0 y0 + e0 y0',  z1 = c1 y1 + e1 y1'
 // with y' the other chunk or, interleaved, the neighbouring channel. The transpose
-// is the same with e negated.
+// is the same with e negated. A chunk past rot_dim does not turn: its y' is left out, which
+// may be an infinity (0 times it is NaN).
 template <int N, bool kInter>
 struct Rotation {
   float2 c[2][N / 2], e[2][N / 2];
+
+  // Worked out where it is used: kept for the rows, it cost the gradient 2 us of 146.
+  static __device__ __forceinline__ bool turns(const RopeArgs& a, const int (&ch)[2], int k) {
+    return a.table && ch[kInter ? k : 0] < a.rot;
+  }
 
   __device__ __forceinline__ void load(const RopeArgs& a, int pos, const int (&ch)[2]) {
     const float* row = a.table + (size_t)pos * a.rot;
     const int half = a.rot / 2;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (!a.table || ch[k] >= a.rot) {
+      if (!turns(a, ch, k)) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
           c[k][i] = both(1.0f);
@@ -166,9 +172,10 @@ struct Rotation {
   }
 
   // c y + e y'
-  __device__ __forceinline__ float2 turn(const float2 (&y)[2][N / 2], int k, int i) const {
+  __device__ __forceinline__ float2 turn(const RopeArgs& a, const int (&ch)[2],
+                                         const float2 (&y)[2][N / 2], int k, int i) const {
     const float2 other = kInter ? make_float2(y[k][i].y, y[k][i].x) : y[1 - k][i];
-    return ffma2(y[k][i], c[k][i], fmul2(other, e[k][i]));
+    return ffma2(y[k][i], c[k][i], turns(a, ch, k) ? fmul2(other, e[k][i]) : both(0.0f));
   }
 };
 
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < P; ++j) y[k][j] = fmul2(both(ri), rot.turn(x, k, j));
+            for (int j = 0; j < P; ++j) y[k][j] = fmul2(both(ri), rot.turn(a, ch, x, k, j));
         } else {
           float2 g[2][P];
           unpack<kBf16>(place(i & 1, r, 2), g[0]);
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < P; ++j) y[k][j] = rot.turn(g, k, j);  // dy
+            for (int j = 0; j < P; ++j) y[k][j] = rot.turn(a, ch, g, k, j);  // dy
           if (norm) {
             float2 q = both(0.0f);
 #pragma unroll

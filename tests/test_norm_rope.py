@@ -419,3 +419,58 @@ def test_weight_gradient_of_a_side_without_heads(without, dtype, D):
         none, out = c.dq[:, :0], torch.empty_like(dk)
         M.attn_qk_norm_rope_bwd(none, c.dk, gq[:, :0], gk, none, out, **kw)
         assert torch.equal(out, dk) and (dws[0] == 0).all() and torch.isfinite(dws[1]).all()
+
+
+def same_kind(got, ref, tol):
+    """Equal infinities and NaN; elsewhere within tol."""
+    f = np.isfinite(ref)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.array_equal(np.isposinf(got), np.isposinf(ref))
+    assert np.array_equal(np.isneginf(got), np.isneginf(ref))
+    assert (np.abs(got - ref)[f] <= np.broadcast_to(tol, ref.shape)[f]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [0, 16, 48])
+@pytest.mark.parametrize("norm", [False, True])
+def test_infinities_and_nan_stay_in_their_channels(norm, rot, inter, dtype, D):
+    """A channel that is not rotated passes by itself: what a neighbour of it holds, in the
+    input or the gradient, does not reach it. With a norm an infinite channel makes the row's
+    others 0, a NaN all of them NaN."""
+    import masked_attention_gb300 as M
+    c = Case(B=1, S=12, Hq=3, Hkv=1, D=D, dtype=dtype, norm=norm, rot=rot, inter=inter, fused=False,
+             pos=list(range(1, 13)))
+    tab = None if c.table is None else c.table.astype(np.float64)
+    bad = [float("inf"), -float("inf"), float("nan")]
+    places = [(s, (7 * s + 5 * h) % D, bad[(s + h) % 3]) for h in range(3) for s in range(12)]
+    q, g = c.q.clone(), c.gq.clone()
+    for i, (s, ch, x) in enumerate(places):
+        if s % 4:    # some rows stay finite
+            q[0, i // 12, s, ch] = x
+            g[0, i // 12, s, (ch + 3) % D] = x
+    o = torch.empty(q.shape, dtype=dtype, device="cuda")
+    kw = c.kwargs()
+    w = None if c.w[0] is None else f64(c.w[0])
+    with np.errstate(invalid="ignore", over="ignore"):
+        M.attn_qk_norm_rope(q.cuda(), None, o, None, **kw)
+        ref = norm_rope(f64(q), w, c.eps, tab, c.ref_pos(), inter)
+        y = np.nan_to_num(norm_rope(f64(q), w, c.eps, None, None, inter), nan=0, posinf=0, neginf=0)
+        size = 2.0 ** -19 * np.abs(y).max(-1, keepdims=True)
+        same_kind(f64(o.cpu()), ref, HALF[dtype] * np.abs(ref) + size)
+        if norm:    # finite inputs, gradients that are not: which outputs stay finite
+            q = c.q
+        dx, dw = torch.empty_like(o), torch.empty(D, device="cuda")
+        ws = torch.empty(M.attn_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8, device="cuda")
+        M.attn_qk_norm_rope_bwd(q.cuda(), None, g.cuda(), None, dx, None, workspace=ws,
+                                dq_weight=dw if norm else None, **kw)
+        ref, dw_ref = norm_rope_backward(f64(q), f64(g), w, c.eps, tab, c.ref_pos(), inter)
+        if norm:
+            assert np.array_equal(np.isfinite(f64(dx.cpu())), np.isfinite(ref))
+            assert np.array_equal(np.isfinite(f64(dw.cpu())), np.isfinite(dw_ref))
+        else:
+            size = 2.0 ** -19 * np.abs(np.nan_to_num(f64(g), nan=0, posinf=0, neginf=0)).max(
+                -1, keepdims=True)
+            same_kind(f64(dx.cpu()), ref, HALF[dtype] * np.abs(ref) + size)
