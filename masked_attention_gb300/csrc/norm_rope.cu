@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
   const int spread = kRopeWarps / a.together;
   int ch[2];
   lane_chunks<N, LANES>(a, kInter, lane % LANES, ch);
-  const int c0 = ch[0] * (16 / N), c1 = ch[1] * (16 / N);  // bytes
+  const int c0 = ch[0] * (16 / N), c1 = ch[1] * (16 / N);  // bytes, c0 < c1
 
   for (int t = 0; t < 2; ++t) {
     if (a.H[t] == 0) {  // no rows: their share of a weight gradient is 0
@@ -268,11 +268,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           if (r * SUBS < heads) {
-            if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, x - xv.p, xv.bytes)) {
+            if ((!kBwd || norm) && MATTN_IN_BOUNDS(kSiteRope, x + c1 + 15 - xv.p, xv.bytes)) {
               cp_async16(&place(buf, r, 0), x + c0);
               cp_async16(&place(buf, r, 1), x + c1);
             }
-            if (kBwd && MATTN_IN_BOUNDS(kSiteRope, z - zv.p, zv.bytes)) {
+            if (kBwd && MATTN_IN_BOUNDS(kSiteRope, z + c1 + 15 - zv.p, zv.bytes)) {
               cp_async16(&place(buf, r, 2), z + c0);
               cp_async16(&place(buf, r, 3), z + c1);
             }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
                 y[k][j] = fmul2(both(ri), ffma2(x[k][j], m, fmul2(y[k][j], w[k][j])));
           }
         }
-        if (here && MATTN_IN_BOUNDS(kSiteRope, out - ov.p, ov.bytes)) {
+        if (here && MATTN_IN_BOUNDS(kSiteRope, out + c1 + 15 - ov.p, ov.bytes)) {
           *reinterpret_cast<uint4*>(out + c0) = pack<kBf16>(y[0]);
           *reinterpret_cast<uint4*>(out + c1) = pack<kBf16>(y[1]);
         }
