@@ -637,6 +637,7 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSitePlan: return "page plan: page-table or free-list entry";
     case kSiteRope: return "norm and rotation: row";
     case kSiteCacheRow: return "4-bit cache: bf16 row";
+    case kSiteCacheRec: return "4-bit cache: record row";
     case kSiteQ4Q: return "4-bit decode: query row";
     case kSiteQ4Out: return "4-bit decode: output or split partial store";
   }

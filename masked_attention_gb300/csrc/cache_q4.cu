@@ -246,7 +246,12 @@ __global__ void __launch_bounds__(kCacheThreads, kCachePerSm)
     uint8_t* rec = a.pool + page * page_bytes + (long long)h * L.bytes();
     const int in_page = (int)(slot & (L.page - 1));
     scale = rec + (v ? L.v_scales() : L.k_scales()) + in_page * L.scale_row() + part / 2 * 2;
-    return rec + (v ? L.v_codes() : 0) + in_page * L.code_row() + part * 8;
+    uint8_t* code = rec + (v ? L.v_codes() : 0) + in_page * L.code_row() + part * 8;
+    [[maybe_unused]] const long long pool_bytes = a.num_pages * page_bytes;
+    if (!MATTN_IN_BOUNDS(kSiteCacheRec, code + 7 - a.pool, pool_bytes) ||
+        !MATTN_IN_BOUNDS(kSiteCacheRec, scale + 1 - a.pool, pool_bytes))
+      return nullptr;
+    return code;
   };
 
   if constexpr (!kLoad) {

@@ -42,6 +42,7 @@ enum DebugSite : int {
   kSiteCacheRow = 22,     // bf16 row of the 4-bit cache's write or read
   kSiteQ4Q = 23,          // query row of the 4-bit decode
   kSiteQ4Out = 24,        // output or split partial of the 4-bit decode
+  kSiteCacheRec = 25,     // record row of the 4-bit cache's write or read
   kSiteCount
 };
 

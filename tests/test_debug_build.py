@@ -94,3 +94,16 @@ def test_gpu_suite_leaves_debug_record_clean(debug_lib):
     tail = "\n".join((r.stdout + r.stderr).splitlines()[-30:])
     print(tail)
     assert r.returncode == 0, tail
+
+
+def test_sites_have_names(debug_lib):
+    """Every check site that debug.cuh lists is named by the library, each its own way."""
+    path = os.path.join(ROOT, "masked_attention_gb300", "csrc", "debug.cuh")
+    with open(path) as f:
+        sites = dict(re.findall(r"^  (kSite\w+) = (\d+),", f.read(), flags=re.M))
+    L = ctypes.CDLL(debug_lib)
+    L.attn_debug_site_name.restype = ctypes.c_char_p
+    names = {s: L.attn_debug_site_name(int(n)) for s, n in sites.items() if s != "kSiteNone"}
+    assert b"unknown" not in names.values() and len(set(names.values())) == len(names)
+    for site in ("kSiteCacheRow", "kSiteCacheRec"):
+        assert b"4-bit cache" in names[site]
