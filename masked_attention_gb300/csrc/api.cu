@@ -639,6 +639,8 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSiteCacheRow: return "4-bit cache: bf16 row";
     case kSiteCacheRec: return "4-bit cache: record row";
     case kSiteQ4Q: return "4-bit decode: query row";
+    case kSiteQ4Pool: return "4-bit decode: record chunk";
+    case kSiteQ4Table: return "4-bit decode: page-table entry";
     case kSiteQ4Out: return "4-bit decode: output or split partial store";
   }
   return "unknown";

@@ -43,6 +43,8 @@ enum DebugSite : int {
   kSiteQ4Q = 23,          // query row of the 4-bit decode
   kSiteQ4Out = 24,        // output or split partial of the 4-bit decode
   kSiteCacheRec = 25,     // record row of the 4-bit cache's write or read
+  kSiteQ4Pool = 26,       // record chunk read by the 4-bit decode
+  kSiteQ4Table = 27,      // page-table entry read by the 4-bit decode
   kSiteCount
 };
 

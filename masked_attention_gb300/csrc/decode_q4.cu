@@ -115,6 +115,7 @@ struct Q4Problem {
   int2* ws_meta;   // [pairs]: first and last CTA of a cut pair; first = -1: done
   float* ws_lse;   // [slots][R], log2
   float* ws_o;     // [slots][R][D]
+  long long slots;
 };
 
 // A sequence's tiles: those of the sinks, then those from win_tile on.
@@ -450,11 +451,19 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     if (i >= sg.n_tiles) return -1;
     const int lp = (key_of(sg, i) + 16 * (lane & 1)) >> p.shift;
     if (lp >= p.pages_per_seq) return -1;
-    const int pg = p.table[(size_t)sg.b * p.pages_per_seq + lp];
+    const long long at = (long long)sg.b * p.pages_per_seq + lp;
+    if (!MATTN_IN_BOUNDS(kSiteQ4Table, at, (long long)p.B * p.pages_per_seq)) return -1;
+    const int pg = p.table[at];
     return pg >= 0 && pg < p.num_pages ? pg : -1;
   };
   int pages = -1, pages_next = -1;
   const uint32_t page_stride = (uint32_t)p.Hkv * L.bytes();
+  [[maybe_unused]] const long long pool_bytes = (long long)p.num_pages * page_stride;
+  // Whether the 16 bytes at x lie in the pool (true in the release build).
+  [[maybe_unused]] auto in_pool = [&](const uint8_t* x) {
+    return MATTN_IN_BOUNDS(kSiteQ4Pool, x - p.pool, pool_bytes) &&
+           MATTN_IN_BOUNDS(kSiteQ4Pool, x + 15 - p.pool, pool_bytes);
+  };
   constexpr int kScaleChunks = C::kScales / 32;  // 16-byte chunks of K (or V) scales per half
   // lane's chunk of the scales: half, K or V, place
   const bool sc_half = lane / kScaleChunks & 1;
@@ -473,6 +482,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
     const uint32_t lane_dst = dst + lane / G * C::kRow + (lane % G ^ C::swz(lane / G)) * 16;
     auto half_codes = [&](int h, const uint8_t* k, uint32_t bytes) {  // 16 keys, K and V
       const uint8_t* v = k + L.v_codes();
+      if (bytes && !(in_pool(k) && in_pool(v + (D / 64 - 1) * 512))) bytes = 0;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
         const uint32_t d = lane_dst + (16 * h + c * (32 / G)) * C::kRow;
@@ -500,7 +510,10 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
         sc_bytes = pg1 >= 0 ? 16u : 0u;
       }
     }
-    if (lane < 4 * kScaleChunks) cp_async16z(dst + sc_dst, sc, sc_bytes);
+    if (lane < 4 * kScaleChunks) {
+      if (sc_bytes && !in_pool(sc)) sc_bytes = 0;
+      cp_async16z(dst + sc_dst, sc, sc_bytes);
+    }
     cp_async_commit();
   };
   auto start_loads = [&](const Q4Segment& sg) {
@@ -929,6 +942,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
                  : make_float4(acc.x / Ls, acc.y / Ls, acc.z / Ls, acc.w / Ls);
       if (!MATTN_IN_BOUNDS(kSiteQ4Out, row0 + r, total_rows)) continue;
       if (cur.slot >= 0) {
+        if (!MATTN_IN_BOUNDS(kSiteQ4Out, cur.slot, p.slots)) continue;
         *reinterpret_cast<float4*>(p.ws_o + ((size_t)cur.slot * R + r) * D + c) = acc;
         if (c == 0) p.ws_lse[(size_t)cur.slot * R + r] = lse2;
       } else {
@@ -971,7 +985,9 @@ __global__ void __launch_bounds__(32 * merge_warps(W)) q4_merge_kernel(const Q4P
     if (mine) {
       for (int c0 = ctas.x + warp % W; c0 <= ctas.y; c0 += 32 * W) {  // 32 parts at a time
         const int c = c0 + lane * W;
-        const float lse = c <= ctas.y ? p.ws_lse[(c + pair) * R + r] : -INFINITY;
+        float lse = -INFINITY;
+        if (c <= ctas.y && MATTN_IN_BOUNDS(kSiteQ4Out, c + pair, p.slots))
+          lse = p.ws_lse[(c + pair) * R + r];
         float m = lse;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -986,7 +1002,9 @@ __global__ void __launch_bounds__(32 * merge_warps(W)) q4_merge_kernel(const Q4P
 #pragma unroll 4
         for (int k = 0; k < n; ++k) {
           const float wk = __shfl_sync(0xffffffffu, w, k);
-          const float* part = p.ws_o + ((c0 + (long long)k * W + pair) * R + r) * D + lane * V;
+          const long long slot = c0 + (long long)k * W + pair;
+          if (!MATTN_IN_BOUNDS(kSiteQ4Out, slot, p.slots)) continue;
+          const float* part = p.ws_o + (slot * R + r) * D + lane * V;
           float x[V];
           if constexpr (V == 4) {
             const float4 f = *reinterpret_cast<const float4*>(part);
@@ -1101,6 +1119,7 @@ cudaError_t launch_typed(Q4Problem& p, long long tiles, void* ws, size_t ws_byte
     return launch_early(decode_q4_kernel<D, NT, SCORE>, (unsigned)pairs, kQ4Threads, C::kSmem, stream, p);
   }
   const Q4Workspace w = q4_workspace(pairs, ctas, R, D);
+  p.slots = pairs + ctas;
   p.ws_meta = static_cast<int2*>(ws);
   p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + w.lse);
   p.ws_o = reinterpret_cast<float*>(static_cast<char*>(ws) + w.o);

@@ -107,3 +107,5 @@ def test_sites_have_names(debug_lib):
     assert b"unknown" not in names.values() and len(set(names.values())) == len(names)
     for site in ("kSiteCacheRow", "kSiteCacheRec"):
         assert b"4-bit cache" in names[site]
+    for site in ("kSiteQ4Q", "kSiteQ4Pool", "kSiteQ4Table", "kSiteQ4Out"):
+        assert b"4-bit decode" in names[site]
