@@ -247,3 +247,43 @@ def test_refusals():
     with pytest.raises(ValueError):
         M.attn_cache_store_q4(t, t, torch.zeros(1, 3, dtype=torch.int64),
                               torch.zeros(1, 2, q4_bytes(16, 64), dtype=torch.uint8), page_size=16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,S,D", [(3, 8, 4001, 128), (1, 16, 12007, 64), (2, 40, 1301, 128),
+                                     (2, 3, 15001, 128), (7, 1, 25003, 64), (3001, 5, 11, 128),
+                                     (3201, 19, 3, 64), (14003, 8, 1, 128), (90001, 2, 1, 64),
+                                     (2, 7, 6001, 128)])
+def test_warps_with_many_batches(B, H, S, D):
+    """Enough tokens that every warp goes through three batches of rows and more, whole
+    tokens' and packed ones, over the sequences' ends, with skipped places on its way."""
+    import masked_attention_gb300 as M
+    page, T = 32, B * S
+    pages = T // page + 3
+    g = torch.Generator().manual_seed(T)
+    k, v = (torch.randn(B, H, S, D, generator=g).to(torch.bfloat16) for _ in (0, 1))
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    slots[torch.randperm(T, generator=g)[:T // 11]] = -1
+    slots[torch.randperm(T, generator=g)[:T // 50]] = pages * page + 4
+    there = ((slots >= 0) & (slots < pages * page)).numpy()
+    at = slots.numpy()[there]
+    ref = np.full((pages, H, q4_bytes(page, D)), 0xCC, np.uint8)
+    codes = ref[:, :, :page * D].reshape(pages, H, 2, page, D // 2)
+    scales = ref[:, :, page * D:].reshape(pages, H, 2, page, D // 16)
+    rows, values = [], []
+    for i, x in enumerate((k, v)):
+        n, bits = q4_quantise(x.transpose(1, 2).reshape(T, H, D).double().numpy())
+        values.append((n.astype(np.float32) - 8) * np.repeat(bf16_value(bits), 32, -1).astype(np.float32))
+        codes[at // page, :, i, at % page] = (n[..., 0::2] | (n[..., 1::2] << 4))[there]
+        scales[at // page, :, i, at % page] = bits.view(np.uint8).reshape(T, H, D // 16)[there]
+    ref[:, :, :page * D] = codes.reshape(pages, H, -1)
+    ref[:, :, page * D:] = scales.reshape(pages, H, -1)
+    ds = slots.view(B, S).cuda()
+    pool = store(k, v, slots.view(B, S), pages, page, strided=B % 2 == 1)
+    assert np.array_equal(pool.cpu().numpy(), ref)
+    out = [guarded_empty((B, S, H, D), torch.bfloat16).transpose(1, 2) for _ in (0, 1)]
+    M.attn_cache_load_q4(pool, ds, *out, page_size=page)
+    check_canaries()
+    for o, x in zip(out, values):
+        x[~there] = 0.0
+        assert torch.equal(o.transpose(1, 2).reshape(T, H, D).cpu(), torch.from_numpy(x).to(torch.bfloat16))

@@ -576,3 +576,78 @@ def test_nan_values_of_a_visible_key_without_weight(heavy, j):
     c.set_scales(0, j, 1, 0x7fff)
     o, lse = run(c, bf16(np.full((1, 2, 1, D), 1.0)), M.MASK_CAUSAL, "none")
     assert np.isnan(o).all() and np.isfinite(lse).all()
+
+
+def shared(lens, Hkv, D, page=16, **kw):
+    """A cache whose table is wide enough that the keys are shared out over CTAs."""
+    return Cache(lens, Hkv, D, page, per=max(-(-max(lens) // page), 1300 // page + 1), **kw)
+
+
+def shares_out(c, q):
+    import masked_attention_gb300 as M
+    B, Hq, Sq, D = q.shape
+    return M.attn_decode_q4_workspace_bytes(B, Hq, c.Hkv, Sq, c.table.shape[1] * c.page, D) > 0
+
+
+SHARED_SCORES = [dict(softcap=30.0), dict(softcap=1.5), dict(alibi=True),
+                 dict(alibi=True, softcap=20.0), dict(alibi=True, softcap=20.0, window=1450, sink=5),
+                 dict(scale=0.5, causal=False), dict(softcap=1e6)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", SHARED_SCORES)
+@pytest.mark.parametrize("D,heads", [(64, (4, 1, 2)), (128, (12, 1, 1))])
+def test_scores_of_shared_keys(D, heads, kw):
+    """Score modifications where a pair's keys are cut over many CTAs."""
+    Hq, Hkv, Sq = heads
+    c = shared([1700, 3, 0, 260], Hkv, D, seed=41)
+    q = queries(4, Hq, Sq, D)
+    assert shares_out(c, q)
+    check(c, q, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,heads", [(64, (4, 1, 3)), (128, (16, 1, 1))])
+def test_edges_of_shared_keys(D, heads):
+    """NaN and infinite queries, NaN in visible and in masked records, pages outside the pool
+    and lengths outside the bound, with the results of cut pairs joined from the workspace."""
+    import masked_attention_gb300 as M
+    Hq, Hkv, Sq = heads
+    lens = [1600, 90, 1300]
+    c = shared(lens, Hkv, D, seed=42)
+    q = queries(3, Hq, Sq, D)
+    assert shares_out(c, q)
+    ref = check(c, q)
+    bad = q.clone()   # such rows are NaN, the others keep their bits
+    bad[0, 1, 0, 5] = float("inf")
+    bad[2, Hq - 1, Sq - 1, D - 1] = float("nan")
+    hit = np.zeros((3, Hq, Sq), bool)
+    hit[0, 1, 0] = hit[2, Hq - 1, Sq - 1] = True
+    got = run(c, bad, M.MASK_CAUSAL, "full")
+    for x, y in zip(got, ref):
+        assert np.isnan(x[hit]).all() and np.array_equal(x[~hit], y[~hit])
+    if Sq > 1:        # the last key is masked for the first rows
+        for bits in (0x7fff, 0xff80):
+            d = shared(lens, Hkv, D, seed=42)
+            d.set_scales(0, 1599, 0, bits)
+            d.set_scales(2, 1299, 1, bits)
+            for x, y in zip(run(d, q, M.MASK_CAUSAL, "full"), ref):
+                assert np.array_equal(x[:, :, :Sq - 1], y[:, :, :Sq - 1])
+    d = shared(lens, Hkv, D, seed=42)      # a NaN key in a part of its own
+    d.set_scales(0, 40, 0, 0x7fff)
+    o, lse = run(d, q, M.MASK_CAUSAL, "full")
+    assert np.isnan(o[0]).all() and np.isnan(lse[0]).all()
+    assert np.array_equal(o[1:], ref[0][1:]) and np.array_equal(lse[1:], ref[1][1:])
+    d = shared(lens, Hkv, D, seed=42)      # pages that are not there read as zeros
+    d.table[0, 2:60] = -5
+    d.table[2, 7] = len(d.pool)
+    t = np.where((d.table >= 0) & (d.table < len(d.pool)), d.table, -1)
+    o, lse = run(d, q, M.MASK_CAUSAL, "full")
+    O, L, _ = decode_q4(q.double().numpy(), d.pool, t, d.lens, 16)
+    assert np.abs(lse - L).max() < 1e-3 and np.abs(o - O).max() < 2e-2
+    d = shared(lens, Hkv, D, seed=42)      # lengths count as the nearest bound
+    d.lens = np.array([2 ** 31 - 1, 90, -7], np.int32)
+    got = run(d, q, M.MASK_CAUSAL, "full", max_len=1600)
+    d.lens = np.array([1600, 90, 0], np.int32)
+    for x, y in zip(got, run(d, q, M.MASK_CAUSAL, "full", max_len=1600)):
+        assert np.array_equal(x, y)

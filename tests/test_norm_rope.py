@@ -474,3 +474,21 @@ def test_infinities_and_nan_stay_in_their_channels(norm, rot, inter, dtype, D):
             size = 2.0 ** -19 * np.abs(np.nan_to_num(f64(g), nan=0, posinf=0, neginf=0)).max(
                 -1, keepdims=True)
             same_kind(f64(dx.cpu()), ref, HALF[dtype] * np.abs(ref) + size)
+
+
+LONG = [dict(B=3, S=1667, Hq=20, Hkv=7, D=128), dict(B=1667, S=3, Hq=9, Hkv=2, D=64, rot=32),
+        dict(B=2, S=2501, Hq=5, Hkv=5, D=64, inter=True), dict(B=2, S=2499, Hq=1, Hkv=14, D=128, rot=48),
+        dict(B=5, S=1001, Hq=6, Hkv=1, D=128, dtype=torch.float32),
+        dict(B=411, S=13, Hq=10, Hkv=3, D=64, dtype=torch.float32, inter=True, rot=16)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", LONG)
+def test_blocks_with_many_items(kw):
+    """Thousands of tokens: a block goes through several items of several tokens, over the
+    sequences' ends, with rows outside the table on its way."""
+    c = Case(seed=9, **kw)
+    gone = torch.rand(c.pos.shape, generator=torch.Generator().manual_seed(1)) < 0.2
+    c.pos[gone] = torch.where(torch.arange(int(gone.sum())) % 2 == 0, -1, len(c.table)).to(torch.int32)
+    check_forward(c)
+    check_backward(c)
