@@ -723,10 +723,9 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               float& s = x[k >> 1][nt][e + 2 * (k & 1)];
-              const bool masked = kMask && s == -INFINITY;
-              s = ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
+              const bool masked = kMask && s == -INFINITY;  // in any row, one of NaN too
+              s = masked ? -0.0f : ex2_approx(SCORE ? s - ref : fmaf(s, unit[nt][e], -ref));
               l[nt][e] += s;
-              if (masked) s = -0.0f;
             }
           }
       };

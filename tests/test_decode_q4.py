@@ -651,3 +651,26 @@ def test_edges_of_shared_keys(D, heads):
     d.lens = np.array([1600, 90, 0], np.int32)
     for x, y in zip(got, run(d, q, M.MASK_CAUSAL, "full", max_len=1600)):
         assert np.array_equal(x, y)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,heads", [(64, (2, 1, 3)), (128, (12, 3, 4))])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(alibi=True), dict(window=2)])
+def test_rows_without_a_key_take_any_query(D, heads, kw):
+    """Rows before a sequence's first token (places of a padded batch) are 0 with LSE -inf
+    whatever their queries hold, alone and where keys are shared out."""
+    import masked_attention_gb300 as M
+    Hq, Hkv, Sq = heads
+    for make in (Cache, shared):
+        c = make([1, 0, 2, 1400 if make is shared else 40], Hkv, D, 16, seed=51)
+        q = queries(4, Hq, Sq, D)
+        ref = check(c, q, **kw)
+        bad = q.clone()
+        for b, n in enumerate(c.lens):
+            for r in range(max(0, Sq - int(n))):
+                bad[b, :, r, r::3] = float("nan") if r % 2 == 0 else float("inf")
+        variant = (M.MASK_CAUSAL | (M.MASK_WINDOW if "window" in kw else 0) |
+                   (M.SCORE_SOFTCAP if "softcap" in kw else 0) | (M.SCORE_ALIBI if "alibi" in kw else 0))
+        kw2 = {k: v for k, v in kw.items() if k != "alibi"}
+        for x, y in zip(run(c, bad, variant, "full", **kw2), ref):
+            assert np.array_equal(x, y)
