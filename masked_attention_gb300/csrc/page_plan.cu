@@ -226,8 +226,8 @@ MATTN_API attn_status attn_page_plan(const int* cached_lens, const int* new_lens
   if (err != cudaSuccess) return cuda_status(err);
   const PlanArgs args{cached_lens, new_lens, B, page_table, pages_per_seq, free_pages, num_free,
                    shift, seq_lens, cu_new, slots, positions, seq_ids, max_tokens, info};
-  const int blocks = std::max(1, std::min(2 * sm_count(),
-                                          (max_tokens + kPlanTokens - 1) / kPlanTokens));
+  const int blocks =
+      std::max(1, std::min(2 * sm_count(), max_tokens / kPlanTokens + (max_tokens % kPlanTokens != 0)));
   return cuda_status(launch_early(page_plan_kernel, blocks, kPlanThreads, 2 * (B + 1) * sizeof(int),
                                   reinterpret_cast<cudaStream_t>(stream), args));
 }

@@ -215,3 +215,37 @@ def test_refusals():
         M.attn_page_plan(i, i, torch.zeros(4, 2, dtype=torch.int32), i, i,
                          torch.zeros(5, dtype=torch.int32), torch.zeros(3, dtype=torch.int64),
                          i[:3], i[:3], i, page_size=16)
+
+
+@pytest.mark.gpu
+def test_the_largest_token_budget():
+    """2^31 - 1 token places: the last ones are -1, and the work is spread over the GPU as it
+    is for a few places less (the count of blocks must not overflow)."""
+    import masked_attention_gb300 as M
+    most = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 60 * 2 ** 30:
+        pytest.skip("needs 34 GB for the outputs")
+    cached, new, table, free = (torch.from_numpy(np.ascontiguousarray(x)).cuda()
+                                for x in make([3, 40], [5, 700], 16, 50))
+    outs = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (2, 3)]
+    slots = torch.zeros(most, dtype=torch.int64, device="cuda")
+    pos, ids = (torch.zeros(most, dtype=torch.int32, device="cuda") for _ in (0, 1))
+    info = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ref = page_plan([3, 40], [5, 700], table.cpu().numpy(), free.cpu().numpy(), 16, 800)
+
+    def call(n):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in (0, 1))
+        a.record()
+        M.attn_page_plan(cached, new, table, free, *outs, slots[:n], pos[:n], ids[:n], info,
+                         page_size=16)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b)
+
+    few = min(call(most - 1000) for _ in range(3))
+    slots[-1000:] = 7
+    assert min(call(most) for _ in range(2)) < 8 * few
+    for got, r in zip((slots, pos, ids), ref[2:5]):
+        assert np.array_equal(got[:800].cpu().numpy(), r)
+        assert (got[-2000:] == -1).all()
+    assert np.array_equal(info.cpu().numpy(), ref[6])
