@@ -273,7 +273,9 @@ typedef struct attn_view {
  * calls skip them, so a captured graph may keep max_tokens fixed); new tokens
  * past max_tokens are dropped. A page that free_pages cannot give is entered
  * as -1, and tokens without a page (that one, or past pages_per_seq) get slot
- * -1: info tells. page_size 16, 32, 64 or 128; B <= 16384 (else
+ * -1: info tells. free_pages itself is not changed: the caller moves its front
+ * past the info[1] pages taken before the next call, between replays of a graph
+ * too. page_size 16, 32, 64 or 128; B <= 16384 (else
  * ATTN_ERR_UNSUPPORTED). What is written (page_table and the outputs) may
  * overlap no other argument (ATTN_ERR_INVALID_ARG): seq_lens is not
  * cached_lens. Asynchronous on `stream`, one launch. */
@@ -306,7 +308,9 @@ typedef struct attn_rope_params {
  * (its tensors are then not used). q_out may be q itself with the same strides
  * (k likewise); no other overlap. With cos_sin, a row whose position lies
  * outside [0, max_pos) is not written (places of a padded batch). D is 64 or
- * 128. Sums are fp32; each output is rounded once. Asynchronous on `stream`. */
+ * 128. Sums are fp32, squares among them (they stay finite up to |x| = 2^60);
+ * each output is rounded once. Infinities and NaN act as the formulas say: what
+ * is not rotated does not see its neighbours'. Asynchronous on `stream`. */
 attn_status attn_qk_norm_rope(const attn_view* q, const attn_view* k, const attn_view* q_out,
                               const attn_view* k_out, int B, int Hq, int Hkv, int S, int D,
                               const attn_rope_params* p, struct CUstream_st* stream);
@@ -315,10 +319,12 @@ attn_status attn_qk_norm_rope(const attn_view* q, const attn_view* k, const attn
 size_t attn_qk_norm_rope_bwd_workspace_bytes(int D);
 
 /* Gradient of attn_qk_norm_rope: from its inputs q, k and the gradients
- * dq_out, dk_out of its outputs computes dq, dk (rows that the forward did not
- * write are not written and add nothing) and dq_weight, dk_weight (device fp32
- * [D], summed over every row; NULL: not wanted, and invalid for a weight that
- * is NULL). q (k) is not read and may be NULL when its weight is NULL. dq may
+ * dq_out, dk_out of its outputs computes dq, dk and dq_weight, dk_weight (device
+ * fp32 [D], summed over every row, 0 without rows; NULL: not wanted, and invalid
+ * for a weight that is NULL). Rows that the forward did not write are not
+ * written either and add nothing: where dq and dk are parts of a gradient that
+ * goes on (a projection's), zero it before its first use, as what stands in
+ * those rows is what the next product reads. q (k) is not read and may be NULL when its weight is NULL. dq may
  * be dq_out itself with the same strides. No atomics: results are bitwise
  * reproducible. The workspace is 256-byte aligned device memory whose contents
  * need not be kept between calls; calls that may run at the same time need

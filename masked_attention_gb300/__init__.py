@@ -576,7 +576,8 @@ def attn_page_plan(cached_lens, new_lens, page_table, free_pages, seq_lens, cu_n
     [B], ``cu_new`` [B + 1], per new token ``slots`` (int64), ``positions`` and
     ``seq_ids`` [max_tokens] (-1 past the last one), and ``info`` [4]: new
     tokens, pages taken, pages lacking, requests longer than their table. All
-    int32 but ``slots``. See include/mattn.h."""
+    int32 but ``slots``. ``free_pages`` is not changed: move its front past the
+    pages taken before the next call. See include/mattn.h."""
     w = "attn_page_plan"
     dev = _device(w, "cached_lens", cached_lens)
     i32 = _torch.int32
@@ -652,7 +653,9 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, *, dq_weight=None, dk_we
     """Gradient of ``attn_qk_norm_rope``: from its inputs ``q``, ``k`` (not
     read, and may be None, without a norm) and the gradients ``dq_out``,
     ``dk_out`` of its outputs writes ``dq``, ``dk`` and the weights' gradients
-    ``dq_weight``, ``dk_weight`` (fp32 [D]; None: not wanted). ``workspace``:
+    ``dq_weight``, ``dk_weight`` (fp32 [D]; None: not wanted). Rows whose position
+    is outside the table are not written in ``dq``, ``dk``: zero them beforehand
+    where something reads those rows. ``workspace``:
     a CUDA tensor of ``attn_qk_norm_rope_bwd_workspace_bytes(D)`` bytes."""
     w = "attn_qk_norm_rope_bwd"
     dev = _device(w, "dq_out", dq_out)

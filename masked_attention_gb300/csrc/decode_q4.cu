@@ -34,9 +34,10 @@
 // 14 below that of each group while no key's V scales lie 2^8 or more apart. From the first
 // tile on where a visible key's do (or are zero in a group that has values in other keys,
 // or below 2^-98), a warp rounds P to two bf16 parts instead, which have 16 bits and
-// fp32's range for every group by itself (16 sequences x 32768 keys: 163 us against 117;
-// the test, a window of 8 binades that scales stay in, is not seen there and costs up to
-// 2 % with a soft-cap). Groups that are zero in every key stay with fp16.
+// fp32's range for every group by itself (16 sequences x 32768 keys: 164 us against 117;
+// the test, a window of 8 binades that scales stay in, costs 1 % there, 3 % with a soft-cap
+// and 6 % for short sequences: 80 x 16 heads x 1300 keys 64 -> 68). Groups that are zero in
+// every key stay with fp16.
 // m moves (and O and l are rescaled) only when a key passes its bound, which one vote per
 // 32 keys decides. Sums are fp32.
 //
@@ -53,7 +54,7 @@
 // With a window the tiles are those of the first `sink` keys, then those of the
 // window.
 //
-// 16 sequences of 32768 keys, 32 query and 8 key/value heads of 128: 116.7 us for the
+// 16 sequences of 32768 keys, 32 query and 8 key/value heads of 128: 117.4 us for the
 // call, 604 MB at 0.76 of a plain copy's rate. What bounds it is issue: 635 instructions
 // per warp and tile, of which the tensor products hold the issue port about 8 slots each
 // (with the products cut out the same loads take 99.6 us, and the whole takes no less out
@@ -82,7 +83,8 @@ constexpr int kQ4Tile = 32;    // keys per warp step
 constexpr int kQ4Stages = 2;   // per-warp tile buffers
 constexpr int kQ4MaxRows = 16;
 // What a segment's start and end cost beside its tiles (61 ragged sequences of up to 15001
-// keys and a soft-cap: 10: 126 us, 12: 123, 16: 121, 24: 124; 0, before other steps, 27 more)
+// keys and a soft-cap: 10: 124.6 us, 12: 124.9, 16: 125.3, 24: 127.7; 7 of 40000, 8 heads of
+// 64, 16 rows: 64.8, 64.8, 64.1, 63.5; 0, before other steps, 27 more on the former)
 constexpr int kQ4SegmentCost = 16;
 constexpr float kQ4Head = 15.0f;   // log2 bound of a scaled weight
 constexpr float kQ4Start = 8.0f;   // log2 of the largest one when the reference moves
@@ -182,8 +184,8 @@ struct Q4Cfg {
 
 // CTAs per SM that the registers are cut to. What is measured is issue, not
 // latency: one more CTA at fewer registers spills and is slower (16 x 32768 keys, 8
-// key/value heads of 128: 117 us, with two 126, with four 123; with 16 query rows each
-// 173, with three 184; 32 x 32768 keys, heads of 64: 143, with three 147, with five 155).
+// key/value heads of 128: 118 us, with two 126, with four 127; with 16 query rows each
+// 176, with three 180; 32 x 32768 keys, heads of 64: 145, with three the same, with five 160).
 template <int D, int NT>
 constexpr int q4_per_sm() {
   return D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kQ4Threads, q4_per_sm<D, NT>())
   float* units = reinterpret_cast<float*>(offs + C::kOff / 16);                     // [NT * 8]
   // First key of the warp's tile i: the last keys come first, where scores that fall
   // with the distance are largest, so that the reference stays (64 sequences x 8000 keys
-  // with ALiBi: 119 us, ascending 137; without: 116 and 119).
+  // with ALiBi: 122 us, ascending 155; without: 118 and 119).
   auto key_of = [&](const Q4Segment& sg, int i) {
     const int v = sg.v_last - i * kQ4Warps;
     return (v < sg.sink_tiles ? v : v - sg.sink_tiles + sg.win_tile) * kQ4Tile;

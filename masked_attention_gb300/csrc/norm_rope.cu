@@ -24,7 +24,7 @@
 // registers from one item to the next. Queries and keys are two passes over the
 // tokens, so that one set of weights is held at a time. All arithmetic is fp32;
 // each output is rounded once. 16384 tokens x 40 heads of 128 bf16 channels: 60 us, 0.84
-// of a plain copy's rate; the gradient of 32768 x 32 heads: 145 us, 0.82.
+// of a plain copy's rate; the gradient of 32768 x 32 heads: 144 us, 0.83.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,7 +45,7 @@ constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopePerSm = 2;  // blocks per SM: 3, with 80 registers, spilled (66 against 60 us
                                // on 16384 tokens x 40 heads of 128 bf16 channels)
 // Row steps (a row of each lane group) per item. The gradient needs more rows in
-// flight at its 128 registers: 3 against 1 is 145 against 153 us on the training
+// flight at its 128 registers: 3 against 1 is 144 against 153 us on the training
 // shape (B 8, 16 + 16 heads, S 4096, D 128); the forward: 2: 60 us, 1: 67, 3: 62.
 template <bool kBwd>
 constexpr int rope_rows() { return kBwd ? 3 : 2; }
