@@ -336,6 +336,28 @@ attn_status attn_qk_norm_rope_bwd(const attn_view* q, const attn_view* k, const 
                                   int S, int D, const attn_rope_params* p,
                                   struct CUstream_st* stream);
 
+/* attn_qk_norm_rope with positions on several axes (tokens of images and video: time, height,
+ * width): channel pair i (of rot_dim / 2) turns by the angle of the token's position on axis
+ * pair_axis[i], row `position` and column i of cos_sin. `axes` is 1 to 4 and pair_axis a host
+ * array of rot_dim / 2 entries below it, read before the call returns; p->positions is then
+ * device int32 [axes][B][S], and neither it nor p->cos_sin may be NULL. A row is not written
+ * where a position on any axis lies outside [0, max_pos). Everything else is as for
+ * attn_qk_norm_rope, which gives the same bits for equal positions on every axis. */
+attn_status attn_qk_norm_rope_axes(const attn_view* q, const attn_view* k, const attn_view* q_out,
+                                   const attn_view* k_out, int B, int Hq, int Hkv, int S, int D,
+                                   const attn_rope_params* p, int axes,
+                                   const unsigned char* pair_axis, struct CUstream_st* stream);
+
+/* Gradient of attn_qk_norm_rope_axes, as attn_qk_norm_rope_bwd is of attn_qk_norm_rope (the
+ * workspace is attn_qk_norm_rope_bwd_workspace_bytes() too). */
+attn_status attn_qk_norm_rope_axes_bwd(const attn_view* q, const attn_view* k,
+                                       const attn_view* dq_out, const attn_view* dk_out,
+                                       const attn_view* dq, const attn_view* dk, float* dq_weight,
+                                       float* dk_weight, void* workspace, size_t workspace_bytes,
+                                       int B, int Hq, int Hkv, int S, int D,
+                                       const attn_rope_params* p, int axes,
+                                       const unsigned char* pair_axis, struct CUstream_st* stream);
+
 /* The 4-bit paged key/value cache. A pool is num_pages * Hkv records, record
  * (page, head) being
  *   K codes  [page_size][D / 2]   bytes: channel 2b in the low nibble of byte

@@ -29,7 +29,8 @@ __all__ = [
     "attn_check_status", "attn_status_str", "attn_last_cuda_error", "attn_combine", "lib",
     "LIB_PATH", "LIB_DEBUG_PATH", "debug_record", "debug_selftest",
     "attn_page_plan", "attn_qk_norm_rope", "attn_qk_norm_rope_bwd",
-    "attn_qk_norm_rope_bwd_workspace_bytes", "attn_cache_q4_bytes", "attn_cache_store_q4",
+    "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_axes",
+    "attn_qk_norm_rope_axes_bwd", "attn_cache_q4_bytes", "attn_cache_store_q4",
     "attn_cache_load_q4", "attn_decode_q4", "attn_decode_q4_workspace_bytes",
 ]
 
@@ -138,6 +139,12 @@ def lib() -> ctypes.CDLL:
         L.attn_qk_norm_rope_bwd_workspace_bytes.restype = sz
         L.attn_qk_norm_rope_bwd.argtypes = [V, V, V, V, V, V, vp, vp, vp, sz, i, i, i, i, i, R, vp]
         L.attn_qk_norm_rope_bwd.restype = i
+        cp = ctypes.c_char_p
+        L.attn_qk_norm_rope_axes.argtypes = [V, V, V, V, i, i, i, i, i, R, i, cp, vp]
+        L.attn_qk_norm_rope_axes.restype = i
+        L.attn_qk_norm_rope_axes_bwd.argtypes = [V, V, V, V, V, V, vp, vp, vp, sz, i, i, i, i, i,
+                                                 R, i, cp, vp]
+        L.attn_qk_norm_rope_axes_bwd.restype = i
         L.attn_cache_q4_bytes.argtypes = [i, i, i, i]
         L.attn_cache_q4_bytes.restype = sz
         L.attn_cache_store_q4.argtypes = [V, V, vp, vp, i, i, i, i, i, i, vp]
@@ -673,6 +680,70 @@ def attn_qk_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, *, dq_weight=None, dk_we
          None if dq_weight is None else _tensor(w, "dq_weight", dq_weight, f32, dev, (D,)),
          None if dk_weight is None else _tensor(w, "dk_weight", dk_weight, f32, dev, (D,)),
          *_workspace(w, workspace, dev), B, Hq, Hkv, S, D, p)
+
+
+def _rope_axes(w: str, positions, axes, cos_sin) -> tuple:
+    """(number of axes, axis of each channel pair as bytes), checked."""
+    if cos_sin is None or positions is None:
+        raise ValueError(f"{w}: cos_sin and positions are needed")
+    if positions.dim() != 3:
+        raise ValueError(f"{w}: positions must have shape [axes, B, S]")
+    pairs = axes if isinstance(axes, bytes) else bytes([int(a) for a in axes])
+    if 2 * len(pairs) != cos_sin.shape[1]:
+        raise ValueError(f"{w}: axes must have an entry for each of the {cos_sin.shape[1] // 2} "
+                         f"channel pairs, not {len(pairs)}")
+    return positions.shape[0], pairs
+
+
+def attn_qk_norm_rope_axes(q, k, q_out, k_out, *, cos_sin, positions, axes, q_weight=None,
+                           k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                           stream=None) -> None:
+    """``attn_qk_norm_rope`` with positions on several axes (time, height and
+    width of images and video): ``positions`` int32 [A, B, S], A up to 4, and
+    ``axes`` the axis of each of the rot_dim / 2 channel pairs (a sequence of
+    whole numbers, e.g. ``bytes([0] * 16 + [1] * 24 + [2] * 24)``). A row with a
+    position outside the table on any axis is not written."""
+    w = "attn_qk_norm_rope_axes"
+    dev = _device(w, "q", q)
+    B, Hq, S, D = shape = q.shape
+    dt = q.dtype
+    A, pairs = _rope_axes(w, positions, axes, cos_sin)
+    p = _rope_params(w, dt, dev, A * B * S, D, q_weight, k_weight, eps, cos_sin, positions,
+                     interleaved)
+    kv = ko = None
+    Hkv = 0
+    if k is not None:
+        Hkv = k.shape[1]
+        kv = _view(w, "k", k, dt, dev, (B, Hkv, S, D))
+        ko = _view(w, "k_out", k_out, dt, dev, (B, Hkv, S, D))
+    _run(w, lib().attn_qk_norm_rope_axes, dev, stream, _view(w, "q", q, dt, dev, shape), kv,
+         _view(w, "q_out", q_out, dt, dev, shape), ko, B, Hq, Hkv, S, D, p, A, pairs)
+
+
+def attn_qk_norm_rope_axes_bwd(q, k, dq_out, dk_out, dq, dk, *, cos_sin, positions, axes,
+                               workspace, dq_weight=None, dk_weight=None, q_weight=None,
+                               k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                               stream=None) -> None:
+    """Gradient of ``attn_qk_norm_rope_axes``, with the arguments of
+    ``attn_qk_norm_rope_bwd`` beside ``positions`` [A, B, S] and ``axes``."""
+    w = "attn_qk_norm_rope_axes_bwd"
+    dev = _device(w, "dq_out", dq_out)
+    B, Hq, S, D = qs = dq_out.shape
+    Hkv = dk_out.shape[1] if dk_out is not None else 0
+    ks = (B, Hkv, S, D)
+    dt, f32 = dq_out.dtype, _torch.float32
+    A, pairs = _rope_axes(w, positions, axes, cos_sin)
+    p = _rope_params(w, dt, dev, A * B * S, D, q_weight, k_weight, eps, cos_sin, positions,
+                     interleaved)
+    _run(w, lib().attn_qk_norm_rope_axes_bwd, dev, stream,
+         _view(w, "q", q, dt, dev, qs) if q is not None else None,
+         _view(w, "k", k, dt, dev, ks) if Hkv and k is not None else None,
+         _view(w, "dq_out", dq_out, dt, dev, qs),
+         _view(w, "dk_out", dk_out, dt, dev, ks) if Hkv else None,
+         _view(w, "dq", dq, dt, dev, qs), _view(w, "dk", dk, dt, dev, ks) if Hkv else None,
+         None if dq_weight is None else _tensor(w, "dq_weight", dq_weight, f32, dev, (D,)),
+         None if dk_weight is None else _tensor(w, "dk_weight", dk_weight, f32, dev, (D,)),
+         *_workspace(w, workspace, dev), B, Hq, Hkv, S, D, p, A, pairs)
 
 
 def _workspace(w: str, x, dev: int) -> tuple:

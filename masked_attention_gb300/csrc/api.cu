@@ -580,6 +580,7 @@ const DebugTu kDebugTus[] = {
     {debug_fetch_mask_build, debug_clear_mask_build},
     {debug_fetch_page_plan, debug_clear_page_plan},
     {debug_fetch_norm_rope, debug_clear_norm_rope},
+    {debug_fetch_norm_rope_axes, debug_clear_norm_rope_axes},
     {debug_fetch_cache_q4, debug_clear_cache_q4},
     {debug_fetch_decode_q4, debug_clear_decode_q4},
 };

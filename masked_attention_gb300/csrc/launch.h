@@ -79,6 +79,7 @@ MATTN_DECLARE_DEBUG_RECORD(combine)
 MATTN_DECLARE_DEBUG_RECORD(mask_build)
 MATTN_DECLARE_DEBUG_RECORD(page_plan)
 MATTN_DECLARE_DEBUG_RECORD(norm_rope)
+MATTN_DECLARE_DEBUG_RECORD(norm_rope_axes)
 MATTN_DECLARE_DEBUG_RECORD(cache_q4)
 MATTN_DECLARE_DEBUG_RECORD(decode_q4)
 #undef MATTN_DECLARE_DEBUG_RECORD
