@@ -425,6 +425,29 @@ attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse,
  * device (0 when a sequence's keys are too few to share out). */
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D);
 
+/* The attention weight that each cached key received, e.g. to decide which keys a cache
+ * gives up (attn_cache_evict):
+ *   weights[b][hk][j] = decay * previous[b][hk][j]
+ *                       + sum over the query rows (h, r) of key/value head hk that see key j
+ *                         of exp(s'[b,h,r,j] - lse[b,h,r])
+ * for j < seq_lens[b]; entries from there on are left as they were. q [B, Hq, Sq, D] bf16 and
+ * lse fp32 [B, Hq, Sq] are those of an attention call over the same keys (Sq >= 1: the token of
+ * a decode step, or the last tokens of a prompt), k its bf16 keys: page pools and
+ * p->page_table, or NULL and contiguous [B, Hkv, max_len, D]. Row r sits at absolute position
+ * i = seq_lens[b] - Sq + r and key j at j; seq_lens (device int32 [B]) counts each sequence's
+ * keys, the rows' own tokens included, NULL: max_len each. max_len bounds seq_lens on the host
+ * (a length outside [0, max_len] counts as the nearest bound). Variant and p as for
+ * attn_decode_q4 (no sinks). weights and previous are device fp32 [B][Hkv][weights_stride],
+ * weights_stride >= max_len; previous may be weights itself (weights added up step by step),
+ * or NULL (0), and is not read where decay is 0; no other overlap. A row whose LSE is -inf adds
+ * nothing, and what a key that no row sees holds, NaN included, changes nothing. A page index
+ * outside [0, num_pages) reads as zeros. Sums are fp32 in a fixed order: bitwise reproducible.
+ * Asynchronous on `stream`; ATTN_ERR_UNSUPPORTED for B * Hkv > 65535. */
+attn_status attn_key_weights(const void* q, const void* k, const float* lse, const float* previous,
+                             float decay, float* weights, int B, int Hq, int Hkv, int Sq,
+                             int max_len, int D, int weights_stride, unsigned variant,
+                             const attn_params* p, const int* seq_lens, struct CUstream_st* stream);
+
 /* Bytes of device buffer build_block_mask() needs (256-byte aligned pieces). */
 size_t attn_block_mask_bytes(int B, int Sq, int Skv, int transposed);
 

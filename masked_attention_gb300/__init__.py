@@ -32,6 +32,7 @@ __all__ = [
     "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_axes",
     "attn_qk_norm_rope_axes_bwd", "attn_cache_q4_bytes", "attn_cache_store_q4",
     "attn_cache_load_q4", "attn_decode_q4", "attn_decode_q4_workspace_bytes",
+    "attn_key_weights",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmattn.so")
@@ -155,6 +156,9 @@ def lib() -> ctypes.CDLL:
         L.attn_decode_q4.restype = i
         L.attn_decode_q4_workspace_bytes.argtypes = [i, i, i, i, i, i]
         L.attn_decode_q4_workspace_bytes.restype = sz
+        f = ctypes.c_float
+        L.attn_key_weights.argtypes = [vp, vp, vp, vp, f, vp, i, i, i, i, i, i, i, u, P, vp, vp]
+        L.attn_key_weights.restype = i
         L.attn_check_status.argtypes = [vp, vp]
         L.attn_check_status.restype = i
         L.attn_status_str.argtypes = [i]
@@ -829,6 +833,58 @@ def attn_decode_q4(q, pool, o, lse, variant: int = 0, *, page_table, page_size: 
          _tensor(w, "o", o, bf16, dev, shape), _tensor(w, "lse", lse, f32, dev, (B, Hq, Sq)),
          B, Hq, Hkv, Sq, per * page_size if max_len is None else max_len, D, variant,
          ctypes.byref(p), _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)), sink, ws, ws_bytes)
+
+
+def _paged_params(w: str, dev: int, B: int, Hq: int, scale, window, softcap, alibi_slopes,
+                  page_table, page_size: int, pages: int, status, timeout_ns: int,
+                  fault_inject: int) -> attn_params:
+    """Parameters of the calls over the bf16 cache with sequences of their own lengths."""
+    i32 = _torch.int32
+    p = attn_params(BF16, scale, window, softcap)
+    if alibi_slopes is not None:
+        p.alibi_slopes = _tensor(w, "alibi_slopes", alibi_slopes, _torch.float32, dev, (Hq,))
+    if page_table is not None:
+        per = page_table.shape[1]
+        p.page_table = _tensor(w, "page_table", page_table, i32, dev, (B, per))
+        p.page_size = page_size
+        p.pages_per_seq = per
+        p.num_pages = pages
+    if status is not None:
+        p.status = _tensor(w, "status", status, i32, dev, status.shape)
+    p.timeout_ns = timeout_ns
+    p.fault_inject = fault_inject
+    return p
+
+
+def attn_key_weights(q, k, lse, weights, variant: int = 0, *, previous=None, decay: float = 1.0,
+                     page_table=None, page_size: int = 0, seq_lens=None, scale: float = 0.0,
+                     window: int = 0, softcap: float = 0.0, alibi_slopes=None, status=None,
+                     timeout_ns: int = 0, fault_inject: int = 0, stream=None) -> None:
+    """The attention weight that each cached key received: writes ``weights`` (fp32 [B, Hkv,
+    L]) = ``decay`` * ``previous`` + the sum over the query rows of each key/value head of
+    exp(score - LSE). ``q`` [B, Hq, Sq, D] bf16 and ``lse`` fp32 [B, Hq, Sq] are those of an
+    attention call over the same keys; ``k``: bf16 page pool [num_pages, Hkv, page, D] with
+    ``page_table`` [B, pages_per_seq], or contiguous [B, Hkv, Skv, D]. ``seq_lens`` int32 [B]
+    counts each sequence's keys (its Sq rows are the last ones; None: all of L or Skv);
+    entries of ``weights`` past them are left as they were. ``previous`` (like ``weights``, or
+    ``weights`` itself; None: 0). See include/mattn.h."""
+    w = "attn_key_weights"
+    dev = _device(w, "q", q)
+    bf16, f32 = _torch.bfloat16, _torch.float32
+    B, Hq, Sq, D = shape = q.shape
+    Hkv, L = k.shape[1], weights.shape[-1]
+    paged = page_table is not None
+    p = _paged_params(w, dev, B, Hq, scale, window, softcap, alibi_slopes, page_table, page_size,
+                      k.shape[0], status, timeout_ns, fault_inject)
+    max_len = min(L, p.pages_per_seq * page_size) if paged else k.shape[2]
+    _run(w, lib().attn_key_weights, dev, stream, _tensor(w, "q", q, bf16, dev, shape),
+         _tensor(w, "k", k, bf16, dev, (k.shape[0], Hkv, page_size, D) if paged
+                 else (B, Hkv, max_len, D)),
+         _tensor(w, "lse", lse, f32, dev, (B, Hq, Sq)),
+         None if previous is None else _tensor(w, "previous", previous, f32, dev, (B, Hkv, L)),
+         decay, _tensor(w, "weights", weights, f32, dev, (B, Hkv, L)), B, Hq, Hkv, Sq, max_len, D,
+         L, variant, ctypes.byref(p),
+         None if seq_lens is None else _tensor(w, "seq_lens", seq_lens, _torch.int32, dev, (B,)))
 
 
 def attn_check_status(status=None, stream=None) -> int:

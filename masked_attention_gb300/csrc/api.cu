@@ -542,6 +542,26 @@ MATTN_API const char* attn_last_cuda_error(void) {
 }
 
 namespace mattn {
+
+int* library_status() { return default_status(); }
+
+attn_status paged_args(unsigned variant, const attn_params* p, int D) {
+  if ((D != 64 && D != 128) || p->dtype != ATTN_BF16) return ATTN_ERR_UNSUPPORTED;
+  if (variant & ~kKnownBits) return ATTN_ERR_INVALID_ARG;
+  if (variant & ~(unsigned)(ATTN_MASK_CAUSAL | ATTN_MASK_WINDOW | ATTN_SCORE_ALIBI | ATTN_SCORE_SOFTCAP))
+    return ATTN_ERR_UNSUPPORTED;
+  if ((variant & ATTN_MASK_WINDOW) && p->window < 1) return ATTN_ERR_INVALID_ARG;
+  if ((variant & ATTN_SCORE_SOFTCAP) &&
+      !(p->softcap > 0.0f && std::isfinite(p->softcap) && std::isfinite(2.0f / p->softcap)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || p->scale < 0.0f) return ATTN_ERR_INVALID_ARG;
+  if (p->q_offset || p->kv_offset) return ATTN_ERR_UNSUPPORTED;
+  if (!p->page_table) return ATTN_OK;
+  const int ps = p->page_size;
+  if (ps != 16 && ps != 32 && ps != 64 && ps != 128) return ATTN_ERR_UNSUPPORTED;
+  return p->num_pages < 1 || p->pages_per_seq < 1 ? ATTN_ERR_INVALID_ARG : ATTN_OK;
+}
+
 MATTN_DEBUG_RECORD_ACCESSORS(api)
 }  // namespace mattn
 
@@ -583,6 +603,7 @@ const DebugTu kDebugTus[] = {
     {debug_fetch_norm_rope_axes, debug_clear_norm_rope_axes},
     {debug_fetch_cache_q4, debug_clear_cache_q4},
     {debug_fetch_decode_q4, debug_clear_decode_q4},
+    {debug_fetch_key_weights, debug_clear_key_weights},
 };
 
 }  // namespace
@@ -643,6 +664,9 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSiteQ4Pool: return "4-bit decode: record chunk";
     case kSiteQ4Table: return "4-bit decode: page-table entry";
     case kSiteQ4Out: return "4-bit decode: output or split partial store";
+    case kSiteKwTable: return "key weights: page-table entry";
+    case kSiteKwLse: return "key weights: LSE";
+    case kSiteKwOut: return "key weights: weight";
   }
   return "unknown";
 }

@@ -45,6 +45,9 @@ enum DebugSite : int {
   kSiteCacheRec = 25,     // record row of the 4-bit cache's write or read
   kSiteQ4Pool = 26,       // record chunk read by the 4-bit decode
   kSiteQ4Table = 27,      // page-table entry read by the 4-bit decode
+  kSiteKwTable = 28,      // page-table entry read by the key weights
+  kSiteKwLse = 29,        // LSE read by the key weights
+  kSiteKwOut = 30,        // weight read or written by the key weights
   kSiteCount
 };
 

@@ -1,0 +1,646 @@
+// The attention weight that each cached key received:
+//
+//   w[b][hk][j] = decay * previous[b][hk][j]
+//                 + sum over the query rows (h, r) of key/value head hk that see key j of
+//                   exp(score_mod(scale <q[b,h,r], k[b,hk,j]>) - LSE[b,h,r])
+//
+// from the queries and the LSE of an attention call that has run (one decode step, or the last
+// tokens of a prompt); the sum over a head's keys of its new part is its number of rows.
+//
+// Every key row is read once for all query rows of its head: 2 D bytes against 2 D products a
+// row, so HBM is the bound up to about 256 rows (group * Sq) and the tensor cores and the
+// special-function units, one exponential a score, behind that.
+//
+// Scores are computed transposed, S^T = K Q^T, on tcgen05: 128 keys are the M of a product (TMEM
+// lanes), up to 256 query rows its N. A key is then one thread's: its weight is a sum over that
+// thread's own columns, in a fixed order, without a shuffle or an atomic, and bitwise
+// reproducible whatever CTA has the tile.
+//
+// The tiles of 128 keys of all (sequence, key/value head) pairs, one after the other, are dealt
+// out evenly to one CTA per SM. Warp 8 streams them by TMA (and the query rows, per pair or,
+// with more than 256 of them, block by block for two tiles at a time), warp 9 issues the
+// products, and two warpgroups take turns with the tiles, so that one's exponentials run under
+// the other's product.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host_util.h"
+#include "launch.h"
+#include "soft_cap.cuh"
+
+#define MATTN_API extern "C" __attribute__((visibility("default")))
+
+namespace mattn {
+namespace {
+
+constexpr int kKwThreads = 320;
+constexpr int kKwProducer = 8, kKwMma = 9;  // warps; 0 to 7: two warpgroups
+constexpr int kKwMaxN = 256;                // query rows of one product
+constexpr int kKwMaxSlots = 8;
+
+struct KwProblem {
+  const float* lse;
+  const float* previous;  // or nullptr
+  float* weights;
+  const int* seq_lens;  // or nullptr: max_len each
+  const int* table;     // or nullptr: contiguous keys
+  const float* slopes;
+  int B, Hq, Hkv, Sq, D, max_len, stride;  // stride: row length of the weights
+  int shift, pages_per_seq, num_pages;
+  unsigned variant;
+  int window;
+  float decay, scale2, softcap2, softcap_e;  // scale and cap in log2 units
+  int n_cols, blocks;                        // query rows per product, products per tile
+  int q_slots, k_slots;
+  int* status;
+  uint64_t timeout_ns;
+  unsigned fault_inject;
+};
+
+struct KwRange {
+  int len, first, tiles;  // keys, first visible tile, tiles from there on
+};
+
+__device__ __forceinline__ KwRange kw_range(const KwProblem& p, int b) {
+  KwRange r;
+  r.len = p.max_len;
+  if (p.seq_lens) r.len = max(0, min(p.seq_lens[b], p.max_len));
+  r.first = 0;
+  if (p.variant & ATTN_MASK_WINDOW)
+    r.first = (int)(max(0ll, (long long)r.len - p.Sq - p.window + 1) / kTile);
+  r.tiles = max(0, (r.len + kTile - 1) / kTile - r.first);
+  return r;
+}
+
+// A CTA's walk over its tiles; every role walks alike.
+struct KwWalk {
+  int b, hk, tile;    // tile counts from the sequence's first visible one
+  long long left;     // tiles still to go, this one included
+  KwRange r;
+  __device__ __forceinline__ void advance(const KwProblem& p) {
+    --left;
+    if (++tile < r.tiles || left <= 0) return;
+    tile = 0;
+    if (++hk < p.Hkv) return;
+    hk = 0;
+    do r = kw_range(p, ++b);
+    while (r.tiles == 0 && b + 1 < p.B);  // left > 0: a later sequence has tiles
+  }
+};
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+// The wait, naming the registers so that no use moves above it.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ bool kw_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  return __all_sync(0xffffffffu, wait_bounded(bar, parity, wd));
+}
+
+// What a warpgroup keeps of a block's query rows (columns of the product), in shared memory.
+struct KwColumns {
+  float nlse[kKwMaxN];   // -LSE in log2 units; -inf: the column adds nothing
+  float slope[kKwMaxN];  // ALiBi slope in log2 units
+  int pos[kKwMaxN];      // the row's position; -1: none
+};
+
+// Sum over COLS columns of exp2(score - lse) for the thread's key j.
+template <int SCORE, bool kMask, int COLS>
+__device__ __forceinline__ void kw_add(const KwProblem& p, const KwColumns& col, int c0, int j,
+                                       int len, const uint32_t* v, float2 (&sum)[4]) {
+  const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+  const float2 sl = make_float2(p.scale2, p.scale2);
+#pragma unroll
+  for (int c = 0; c < COLS; c += 4) {
+    const float4 nl = *reinterpret_cast<const float4*>(col.nlse + c0 + c);
+    int4 pos;
+    float4 slope;
+    if constexpr (kMask || (SCORE & 1)) pos = *reinterpret_cast<const int4*>(col.pos + c0 + c);
+    if constexpr (SCORE & 1) slope = *reinterpret_cast<const float4*>(col.slope + c0 + c);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float2 s = make_float2(__uint_as_float(v[c + 2 * h]), __uint_as_float(v[c + 2 * h + 1]));
+      const float2 n = h ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
+      float2 x;
+      if constexpr (SCORE == 0) {
+        x = ffma2(s, sl, n);
+      } else {
+        x = fmul2(s, sl);
+        if constexpr (SCORE & 1) {
+          const float2 m = h ? make_float2(slope.z, slope.w) : make_float2(slope.x, slope.y);
+          x.x -= m.x * float((h ? pos.z : pos.x) - j);
+          x.y -= m.y * float((h ? pos.w : pos.y) - j);
+        }
+        if constexpr (SCORE & 2) {
+          x.x = soft_cap(x.x, p.softcap2, p.softcap_e);
+          x.y = soft_cap(x.y, p.softcap2, p.softcap_e);
+        }
+        x = fadd2(x, n);
+      }
+      float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      if constexpr (kMask) {
+        auto keep = [&](int i) {
+          return i >= 0 && (causal ? j <= i : j < len) && (!windowed || i - j < p.window);
+        };
+        e.x = keep(h ? pos.z : pos.x) ? e.x : 0.0f;
+        e.y = keep(h ? pos.w : pos.y) ? e.y : 0.0f;
+      }
+      const int a = (c / 2 + h) & 3;
+      sum[a] = fadd2(sum[a], e);
+    }
+  }
+}
+
+template <int D, int SCORE>
+__global__ void __launch_bounds__(kKwThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k, const KwProblem p) {
+  constexpr int kBoxes = D / 64;
+  constexpr int kBoxBytes = kTile * 128;
+  constexpr int kTileBytes = kBoxes * kBoxBytes;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int q_box = p.n_cols * 128, q_bytes = kBoxes * q_box;  // n_cols % 16 == 0: 2048 | q_box
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + p.q_slots * q_bytes;
+  __shared__ __align__(16) KwColumns columns[2];
+  __shared__ uint64_t bars[11 + 2 * kKwMaxSlots];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_word;
+  __shared__ long long run_sum[kKwThreads];
+  __shared__ long long first_tile, total_tiles;
+  __shared__ int first_b;
+  uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_free = bars + 6,
+           *drain = bars + 8, *wg_bar = bars + 9, *k_full = bars + 11,
+           *k_empty = k_full + kKwMaxSlots;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &abort_word;
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(s_free + i, 4);
+      mbar_init(wg_bar + i, 4);
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < p.k_slots; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(k_empty + i, 1);
+    }
+    abort_word = 0;
+    first_tile = 0;
+    first_b = p.B;
+    fence_barrier_init();
+  }
+  if (warp == kKwMma) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (warp == kKwProducer && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+  }
+  early_start();
+
+  // This CTA's tiles [lo, hi) of all: a thread adds up a run of sequences.
+  const int run = (p.B + kKwThreads - 1) / kKwThreads;
+  const int r0 = min((int)threadIdx.x * run, p.B), r1 = min(r0 + run, p.B);
+  long long own = 0;
+  for (int b = r0; b < r1; ++b) own += (long long)kw_range(p, b).tiles * p.Hkv;
+  run_sum[threadIdx.x] = own;
+  __syncthreads();
+  if (warp == 0) {  // exclusive sums of the runs, 10 threads' at a time
+    constexpr int per = kKwThreads / 32;
+    long long s = 0;
+#pragma unroll
+    for (int i = 0; i < per; ++i) s += run_sum[lane * per + i];
+    long long before = s;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, before, d);
+      if (lane >= d) before += o;
+    }
+    if (lane == 31) total_tiles = before;
+    before -= s;
+#pragma unroll
+    for (int i = 0; i < per; ++i) {
+      const long long mine = run_sum[lane * per + i];
+      run_sum[lane * per + i] = before;
+      before += mine;
+    }
+  }
+  __syncthreads();
+  const long long total = total_tiles;
+  const long long share = (total + gridDim.x - 1) / gridDim.x;
+  const long long lo = min(total, blockIdx.x * share), hi = min(total, lo + share);
+  {
+    long long at = run_sum[threadIdx.x];
+    for (int b = r0; b < r1 && at <= lo; ++b) {
+      const long long n = (long long)kw_range(p, b).tiles * p.Hkv;
+      if (lo < at + n) {
+        first_b = b;
+        first_tile = lo - at;
+      }
+      at += n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  KwWalk walk{};
+  walk.left = hi - lo;
+  if (walk.left > 0) {
+    walk.b = first_b;
+    walk.r = kw_range(p, walk.b);
+    walk.hk = (int)(first_tile / walk.r.tiles);
+    walk.tile = (int)(first_tile % walk.r.tiles);
+  }
+  const int R = p.Hq / p.Hkv * p.Sq;
+  // Tiles that share a pass over the query blocks: two of one pair with several blocks.
+  auto group_of = [&](const KwWalk& w) {
+    return p.blocks > 1 && w.left > 1 && w.tile + 1 < w.r.tiles ? 2 : 1;
+  };
+
+  if (warp == kKwProducer) {
+    const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
+    uint32_t k_it = 0, q_it = 0;
+    bool ok = true, fresh = true;  // fresh: the pair's query rows are not loaded
+    while (walk.left > 0 && ok) {
+      const int g = group_of(walk);
+      const int pair = walk.b * p.Hkv + walk.hk;
+      for (int nb = 0; nb < p.blocks && ok; ++nb) {
+        if (nb > 0 || fresh || p.blocks > 1) {
+          const int slot = q_it % p.q_slots;
+          ok = kw_wait(q_empty + slot, ((q_it / p.q_slots) & 1) ^ 1, wd);
+          if (!ok) break;
+          if (lane == 0 && issue) {
+            mbar_arrive_expect_tx(q_full + slot, q_bytes);
+#pragma unroll
+            for (int bx = 0; bx < kBoxes; ++bx)
+              tma_load_3d(sQ + slot * q_bytes + bx * q_box, &tm_q, q_full + slot, bx * 64,
+                          nb * p.n_cols, pair);
+          }
+          __syncwarp();
+          ++q_it;
+        }
+        if (nb > 0) continue;
+        for (int m = 0; m < g && ok; ++m) {
+          const int slot = k_it % p.k_slots;
+          ok = kw_wait(k_empty + slot, ((k_it / p.k_slots) & 1) ^ 1, wd);
+          if (!ok) break;
+          const int kt = walk.r.first + walk.tile + m;
+          uint8_t* dst = sK + slot * kTileBytes;
+          if (lane == 0 && issue) mbar_arrive_expect_tx(k_full + slot, kTileBytes);
+          __syncwarp();
+          if (!p.table) {
+            if (lane == 0 && issue)
+#pragma unroll
+              for (int bx = 0; bx < kBoxes; ++bx)
+                tma_load_3d(dst + bx * kBoxBytes, &tm_k, k_full + slot, bx * 64, kt * kTile, pair);
+          } else if (issue && lane < (kTile >> p.shift)) {
+            // a lane per page: pages past the last one with keys repeat it (their keys are
+            // masked), and a page outside the pool reads as zeros (past the map's end)
+            const int lp = min((kt * kTile >> p.shift) + lane, (walk.r.len - 1) >> p.shift);
+            int phys = -1;
+            if (MATTN_IN_BOUNDS(kSiteKwTable, lp, p.pages_per_seq))
+              phys = p.table[(size_t)walk.b * p.pages_per_seq + lp];
+            if (phys < 0 || phys >= p.num_pages) phys = p.num_pages;
+#pragma unroll
+            for (int bx = 0; bx < kBoxes; ++bx)
+              tma_load_3d(dst + bx * kBoxBytes + (lane << p.shift) * 128, &tm_k, k_full + slot,
+                          bx * 64, 0, phys * p.Hkv + walk.hk);
+          }
+          __syncwarp();
+          ++k_it;
+        }
+      }
+      for (int m = 0; m < g; ++m) walk.advance(p);
+      fresh = walk.left > 0 && walk.b * p.Hkv + walk.hk != pair;
+    }
+    if (!ok && issue) {  // let copies in flight land
+      for (uint32_t i = 0; i < (uint32_t)p.k_slots && i < k_it; ++i) {
+        const uint32_t it = k_it - 1 - i;
+        wait_drain(k_full + it % p.k_slots, (it / p.k_slots) & 1);
+      }
+      for (uint32_t i = 0; i < (uint32_t)p.q_slots && i < q_it; ++i) {
+        const uint32_t it = q_it - 1 - i;
+        wait_drain(q_full + it % p.q_slots, (it / p.q_slots) & 1);
+      }
+    }
+  } else if (warp == kKwMma) {
+    const uint32_t idesc = idesc_bf16(128, p.n_cols, false);
+    uint32_t k_it = 0, q_it = 0, parity = 0;
+    uint32_t s_it0 = 0, s_it1 = 0;
+    bool ok = true, fresh = true;
+    while (walk.left > 0 && ok) {
+      const int g = group_of(walk);
+      const int pair = walk.b * p.Hkv + walk.hk;
+      KwWalk next = walk;
+      for (int m = 0; m < g; ++m) next.advance(p);
+      const bool leaves = next.left <= 0 || next.b * p.Hkv + next.hk != pair;
+      const uint32_t x0 = p.blocks > 1 ? 0 : parity;
+      for (int nb = 0; nb < p.blocks && ok; ++nb) {
+        if (nb > 0 || fresh || p.blocks > 1) {
+          ok = kw_wait(q_full + q_it % p.q_slots, (q_it / p.q_slots) & 1, wd);
+          if (!ok) break;
+          ++q_it;
+        }
+        const uint32_t q_slot = (q_it - 1) % p.q_slots;
+        for (int m = 0; m < g && ok; ++m) {
+          const uint32_t x = (x0 + m) & 1, seq = k_it + m, slot = seq % p.k_slots;
+          if (nb == 0) {
+            ok = kw_wait(k_full + slot, (seq / p.k_slots) & 1, wd);
+            if (!ok) break;
+          }
+          const uint32_t it = x ? s_it1 : s_it0;
+          ok = kw_wait(s_free + x, (it & 1) ^ 1, wd);
+          if (!ok) break;
+          if (x) ++s_it1; else ++s_it0;
+          tc_fence_after();
+          const uint64_t a0 = sdesc_sw128(smem_u32(sK + slot * kTileBytes), 16, 1024);
+          const uint64_t b0 = sdesc_sw128(smem_u32(sQ + q_slot * q_bytes), 16, 1024);
+          uint64_t a[D / 16], b[D / 16];
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            a[kk] = a0 + (uint64_t)(((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4);
+            b[kk] = b0 + (uint64_t)(((kk / 4) * q_box + (kk % 4) * 32) >> 4);
+          }
+          mma_ss_warp<D / 16>(tmem + kKwMaxN * x, a, b, idesc, 0u);
+          mma_commit_warp(s_full + x);
+          if (nb == p.blocks - 1) mma_commit_warp(k_empty + slot);
+          if (m == g - 1 && (p.blocks > 1 || leaves)) mma_commit_warp(q_empty + q_slot);
+          __syncwarp();
+        }
+      }
+      k_it += g;
+      parity ^= 1;
+      walk = next;
+      fresh = leaves;
+    }
+    mma_commit_warp(drain);
+    __syncwarp();
+    wait_drain(drain, 0);
+  } else {
+    const uint32_t x = warp >> 2;     // warpgroup
+    const int t = threadIdx.x & 127;  // key of the tile, TMEM lane
+    const uint32_t cols = tmem + (uint32_t((warp & 3) * 32) << 16) + kKwMaxN * x;
+    KwColumns& col = columns[x];
+    // Keys before the first visible tile only decay.
+    if (p.variant & ATTN_MASK_WINDOW) {
+      for (long long pr = blockIdx.x; pr < (long long)p.B * p.Hkv; pr += gridDim.x) {
+        const KwRange r = kw_range(p, (int)(pr / p.Hkv));
+        const int n = min(r.first * kTile, r.len);
+        for (int j = threadIdx.x; j < n; j += 256) {
+          const size_t at = (size_t)pr * p.stride + j;
+          if (MATTN_IN_BOUNDS(kSiteKwOut, at, (size_t)p.B * p.Hkv * p.stride))
+            p.weights[at] = p.previous ? p.decay * p.previous[at] : 0.0f;
+        }
+      }
+    }
+    uint32_t parity = 0, s_it = 0, wg_it = 0;
+    bool ok = true;
+    // The warpgroup meets (a bounded wait, so that no warp is left behind in one).
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wg_bar + x);
+      return kw_wait(wg_bar + x, wg_it++ & 1, wd);
+    };
+    // The columns of a (pair, block) are read one use ahead, two by each thread.
+    auto read_lse = [&](const KwWalk& w, int nb, float (&out)[2]) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = t + 128 * i, row = nb * p.n_cols + c;
+        out[i] = INFINITY;  // adds nothing
+        if (c < p.n_cols && row < R) {
+          const size_t at = ((size_t)w.b * p.Hq + (size_t)w.hk * (p.Hq / p.Hkv)) * p.Sq + row;
+          if (MATTN_IN_BOUNDS(kSiteKwLse, at, (size_t)p.B * p.Hq * p.Sq)) out[i] = p.lse[at];
+        }
+      }
+    };
+    float ahead[2];
+    int have_pair = -1, have_block = -1;  // the columns in shared memory
+    if (walk.left > 0) read_lse(walk, 0, ahead);
+    while (walk.left > 0 && ok) {
+      const int g = group_of(walk);
+      const int pair = walk.b * p.Hkv + walk.hk;
+      KwWalk next = walk;
+      for (int m = 0; m < g; ++m) next.advance(p);
+      const uint32_t x0 = p.blocks > 1 ? 0 : parity;
+      const int m = (int)(x ^ x0);  // this warpgroup's tile of the group
+      const bool mine = m < g;
+      const int len = walk.r.len;
+      const int j0 = (walk.r.first + walk.tile + m) * kTile, j = j0 + t;
+      const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+      const bool whole = j0 + kTile <= len && len >= p.Sq &&
+                         (!causal || j0 + kTile - 1 <= len - p.Sq) &&
+                         (!windowed || len - 1 - j0 < p.window);
+      const size_t at = (size_t)pair * p.stride + j;
+      const bool store = mine && j < len &&
+                         MATTN_IN_BOUNDS(kSiteKwOut, at, (size_t)p.B * p.Hkv * p.stride);
+      float old = 0.0f;
+      if (store && p.previous) old = p.previous[at];
+      float2 sum[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
+      for (int nb = 0; nb < p.blocks && ok; ++nb) {
+        if (have_pair != pair || have_block != nb) {
+          have_pair = pair;
+          have_block = nb;
+          ok = meet();  // the block before has been used by all
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = t + 128 * i, row = nb * p.n_cols + c;
+            if (c < p.n_cols) {
+              // a row without keys (LSE -inf) adds nothing
+              col.nlse[c] = ahead[i] == -INFINITY ? -INFINITY : -ahead[i] * kLog2e;
+              const bool there = row < R;
+              col.pos[c] = there ? len - p.Sq + row % p.Sq : -1;
+              if constexpr (SCORE & 1) {
+                const int h = walk.hk * (p.Hq / p.Hkv) + (there ? row / p.Sq : 0);
+                const float slope = p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq));
+                col.slope[c] = slope * kLog2e;
+              }
+            }
+          }
+          ok = meet();
+          if (!ok) break;
+        }
+        // the next block, or the next pair's first
+        if (nb + 1 < p.blocks) read_lse(walk, nb + 1, ahead);
+        else if (next.left > 0 && (p.blocks > 1 || next.b * p.Hkv + next.hk != pair))
+          read_lse(next, 0, ahead);
+        if (!mine) continue;
+        ok = kw_wait(s_full + x, s_it & 1, wd);
+        if (!ok) break;
+        ++s_it;
+        tc_fence_after();
+        auto columns_sum = [&](auto mask) {
+          constexpr bool kMask = decltype(mask)::value;
+          int c = 0;
+          for (; c + 32 <= p.n_cols; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(cols + c, v);
+            tmem_ld_wait_regs(v);
+            kw_add<SCORE, kMask, 32>(p, col, c, j, len, v, sum);
+          }
+          if (c < p.n_cols) {
+            uint32_t v[16];
+            tmem_ld16(cols + c, v);
+            tmem_ld16_wait(v);
+            kw_add<SCORE, kMask, 16>(p, col, c, j, len, v, sum);
+          }
+        };
+        if (whole) columns_sum(std::false_type{});
+        else columns_sum(std::true_type{});
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free + x);
+      }
+      if (store && ok) {
+        const float2 s = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+        p.weights[at] = p.previous ? fmaf(p.decay, old, s.x + s.y) : s.x + s.y;
+      }
+      parity ^= 1;
+      walk = next;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kKwMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kKwSmem = 232448 - 12 * 1024;  // per CTA, less the static part
+
+template <int D, int SCORE>
+cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const KwProblem& p,
+                         unsigned grid, size_t smem, cudaStream_t s) {
+  static DeviceOnce ready;
+  const cudaError_t e = ready.allow_smem(key_weights_kernel<D, SCORE>, kKwSmem);
+  return e != cudaSuccess
+             ? e
+             : launch_early(key_weights_kernel<D, SCORE>, grid, kKwThreads, smem, s, mq, mk, p);
+}
+
+template <int D>
+cudaError_t launch_key_weights(const void* q, const void* k, KwProblem& p, cudaStream_t s) {
+  const int R = p.Hq / p.Hkv * p.Sq;
+  // Query rows of a product: all, up to 256; more of them in blocks of like size.
+  p.blocks = (R + kKwMaxN - 1) / kKwMaxN;
+  p.n_cols = ((R + p.blocks - 1) / p.blocks + 15) / 16 * 16;
+  const int q_bytes = p.n_cols * D * 2, k_bytes = kTile * D * 2;
+  // Two places for query rows where blocks stream or where it leaves four tiles of keys.
+  p.q_slots = p.blocks > 1 || 2 * q_bytes + 4 * k_bytes + 1024 <= kKwSmem ? 2 : 1;
+  p.k_slots = std::min(kKwMaxSlots, (kKwSmem - 1024 - p.q_slots * q_bytes) / k_bytes);
+  CUtensorMap mq, mk;
+  const bool paged = p.table != nullptr;
+  if (!make_map_bf16_3d(&mq, q, (long long)p.B * p.Hkv, R, D, p.n_cols) ||
+      !make_map_bf16_3d(&mk, k, paged ? (long long)p.num_pages * p.Hkv : (long long)p.B * p.Hkv,
+                        paged ? 1 << p.shift : p.max_len, D, paged ? 1 << p.shift : kTile))
+    return cudaErrorInvalidValue;
+  const size_t smem = 1024 + p.q_slots * q_bytes + p.k_slots * k_bytes;
+  const long long tiles = (long long)p.B * p.Hkv * ((p.max_len + kTile - 1) / kTile);
+  const unsigned grid = (unsigned)std::min<long long>(sm_count(), tiles);
+  switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
+    case 0: return launch_typed<D, 0>(mq, mk, p, grid, smem, s);
+    case 1: return launch_typed<D, 1>(mq, mk, p, grid, smem, s);
+    case 2: return launch_typed<D, 2>(mq, mk, p, grid, smem, s);
+    default: return launch_typed<D, 3>(mq, mk, p, grid, smem, s);
+  }
+}
+
+}  // namespace
+}  // namespace mattn
+
+MATTN_API attn_status attn_key_weights(const void* q, const void* k, const float* lse,
+                                       const float* previous, float decay, float* weights, int B,
+                                       int Hq, int Hkv, int Sq, int max_len, int D,
+                                       int weights_stride, unsigned variant, const attn_params* p,
+                                       const int* seq_lens, struct CUstream_st* stream) {
+  using namespace mattn;
+  if (!p || B < 0 || Hq < 1 || Hkv < 1 || Sq < 1 || max_len < 0 || Hq % Hkv ||
+      weights_stride < max_len || !std::isfinite(decay))
+    return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(variant, p, D);
+  if (st != ATTN_OK) return st;
+  if ((long long)B * Hkv > 65535 || max_len > INT_MAX - 255 ||
+      (long long)Hq / Hkv * Sq > INT_MAX / 256)
+    return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || max_len == 0) return ATTN_OK;
+  if (p->page_table && (long long)p->pages_per_seq * p->page_size < (long long)max_len)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->page_table && (long long)p->num_pages * Hkv + Hkv > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  if (!k || !weights || !q || !lse) return ATTN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 15u)
+    return ATTN_ERR_MISALIGNED;
+  const void* words[] = {lse, previous, weights, seq_lens, p->page_table, p->alibi_slopes};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return ATTN_ERR_MISALIGNED;
+  // the previous weights are read where they are written, or apart
+  const size_t bytes = (size_t)B * Hkv * weights_stride * sizeof(float);
+  const char *a = reinterpret_cast<const char*>(previous), *w = reinterpret_cast<char*>(weights);
+  if (a && a != w && a < w + bytes && w < a + bytes) return ATTN_ERR_INVALID_ARG;
+
+  KwProblem f{};
+  f.lse = lse;
+  f.previous = decay != 0.0f ? previous : nullptr;
+  f.weights = weights;
+  f.seq_lens = seq_lens;
+  f.table = p->page_table;
+  f.slopes = p->alibi_slopes;
+  f.B = B;
+  f.Hq = Hq;
+  f.Hkv = Hkv;
+  f.Sq = Sq;
+  f.D = D;
+  f.max_len = max_len;
+  f.stride = weights_stride;
+  f.shift = 7;
+  if (p->page_table)
+    while ((1 << f.shift) != p->page_size) --f.shift;
+  f.pages_per_seq = p->pages_per_seq;
+  f.num_pages = p->num_pages;
+  f.variant = variant;
+  f.window = p->window;
+  f.decay = decay;
+  f.scale2 = (p->scale != 0.0f ? p->scale : 1.0f / std::sqrt((float)D)) * kLog2e;
+  f.softcap2 = p->softcap * kLog2e;
+  f.softcap_e = 2.0f / p->softcap;
+  f.status = p->status ? p->status : library_status();
+  if (!f.status) return ATTN_ERR_CUDA;
+  f.timeout_ns = p->timeout_ns ? p->timeout_ns : 4000000000ull;
+  f.fault_inject = p->fault_inject;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(D == 64 ? launch_key_weights<64>(q, k, f, s)
+                             : launch_key_weights<128>(q, k, f, s));
+}
+
+namespace mattn {
+MATTN_DEBUG_RECORD_ACCESSORS(key_weights)
+}  // namespace mattn

@@ -82,6 +82,7 @@ MATTN_DECLARE_DEBUG_RECORD(norm_rope)
 MATTN_DECLARE_DEBUG_RECORD(norm_rope_axes)
 MATTN_DECLARE_DEBUG_RECORD(cache_q4)
 MATTN_DECLARE_DEBUG_RECORD(decode_q4)
+MATTN_DECLARE_DEBUG_RECORD(key_weights)
 #undef MATTN_DECLARE_DEBUG_RECORD
 #endif
 
@@ -109,6 +110,13 @@ cudaError_t launch_bwd_tc_ragged(const BwdProblem& p, cudaStream_t stream);
 // convert Q, K, V, dO to the fp16 copies; one fp16 kernel (mode: 0 dQ, 1 dK/dV)
 cudaError_t launch_bwd_f16_prepare(const BwdProblem& p, cudaStream_t stream);
 cudaError_t launch_bwd_f16_mode(const BwdProblem& p, int mode, cudaStream_t stream);
+
+// The library's own status word on the current device (nullptr: a CUDA call failed).
+int* library_status();
+
+// The checks that the calls over the bf16 cache with sequences of their own lengths share:
+// variant, scale, D and the page size (with a page table).
+attn_status paged_args(unsigned variant, const attn_params* p, int D);
 
 // The checks attn_bwd makes on everything but its workspace (no CUDA call);
 // fills bp.f when they pass.
