@@ -110,8 +110,25 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
 }
 
 __device__ __forceinline__ bool kw_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
-  return __all_sync(0xffffffffu, wait_bounded(bar, parity, wd));
+  // a sleeping try first: the timer that bounds the wait takes long to read
+  const uint32_t hint = wd.timeout_ns < 1000000ull ? (uint32_t)wd.timeout_ns : 1000000u;
+  const bool done = mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, hint) ||
+                    wait_bounded(bar, parity, wd);
+  return __all_sync(0xffffffffu, done);
 }
+
+// A place in a ring of `n` buffers and the parity of its pass. (Counted, not divided out: a
+// division by the ring's length takes a lone warp some 150 cycles, and four of them a tile
+// were what bounded one decode step.)
+struct KwRing {
+  uint32_t slot = 0, pass = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      pass ^= 1;
+    }
+  }
+};
 
 // What a warpgroup keeps of a block's query rows (columns of the product), in shared memory.
 struct KwColumns {
@@ -128,6 +145,8 @@ __device__ __forceinline__ void kw_add(const KwProblem& p, const KwColumns& col,
   const float2 sl = make_float2(p.scale2, p.scale2);
 #pragma unroll
   for (int c = 0; c < COLS; c += 4) {
+    // keeps the reads of later columns' constants behind (they would fill the registers)
+    if (c % 16 == 0) asm volatile("" ::: "memory");
     const float4 nl = *reinterpret_cast<const float4*>(col.nlse + c0 + c);
     int4 pos;
     float4 slope;
@@ -284,124 +303,132 @@ __global__ void __launch_bounds__(kKwThreads, 1)
 
   if (warp == kKwProducer) {
     const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
-    uint32_t k_it = 0, q_it = 0;
+    KwRing kr, qr;
     bool ok = true, fresh = true;  // fresh: the pair's query rows are not loaded
+    // A lane per page of a tile, its table entry read one tile ahead. Pages past the last one
+    // with keys repeat it (their keys are masked); one outside the pool reads as zeros (past
+    // the map's end).
+    auto page_of = [&](const KwWalk& w) {
+      if (!p.table || w.left <= 0 || lane >= (kTile >> p.shift)) return 0;
+      const int lp = min(((w.r.first + w.tile) * kTile >> p.shift) + lane, (w.r.len - 1) >> p.shift);
+      int phys = -1;
+      if (MATTN_IN_BOUNDS(kSiteKwTable, lp, p.pages_per_seq))
+        phys = p.table[(size_t)w.b * p.pages_per_seq + lp];
+      return phys;
+    };
+    int page = page_of(walk);
     while (walk.left > 0 && ok) {
       const int g = group_of(walk);
       const int pair = walk.b * p.Hkv + walk.hk;
+      KwWalk at = walk;  // goes on to each tile that is loaded
       for (int nb = 0; nb < p.blocks && ok; ++nb) {
         if (nb > 0 || fresh || p.blocks > 1) {
-          const int slot = q_it % p.q_slots;
-          ok = kw_wait(q_empty + slot, ((q_it / p.q_slots) & 1) ^ 1, wd);
+          ok = kw_wait(q_empty + qr.slot, qr.pass ^ 1, wd);
           if (!ok) break;
           if (lane == 0 && issue) {
-            mbar_arrive_expect_tx(q_full + slot, q_bytes);
+            mbar_arrive_expect_tx(q_full + qr.slot, q_bytes);
 #pragma unroll
             for (int bx = 0; bx < kBoxes; ++bx)
-              tma_load_3d(sQ + slot * q_bytes + bx * q_box, &tm_q, q_full + slot, bx * 64,
+              tma_load_3d(sQ + qr.slot * q_bytes + bx * q_box, &tm_q, q_full + qr.slot, bx * 64,
                           nb * p.n_cols, pair);
           }
           __syncwarp();
-          ++q_it;
+          qr.next(p.q_slots);
         }
         if (nb > 0) continue;
         for (int m = 0; m < g && ok; ++m) {
-          const int slot = k_it % p.k_slots;
-          ok = kw_wait(k_empty + slot, ((k_it / p.k_slots) & 1) ^ 1, wd);
+          ok = kw_wait(k_empty + kr.slot, kr.pass ^ 1, wd);
           if (!ok) break;
-          const int kt = walk.r.first + walk.tile + m;
-          uint8_t* dst = sK + slot * kTileBytes;
-          if (lane == 0 && issue) mbar_arrive_expect_tx(k_full + slot, kTileBytes);
+          uint64_t* full = k_full + kr.slot;
+          uint8_t* dst = sK + kr.slot * kTileBytes;
+          if (lane == 0 && issue) mbar_arrive_expect_tx(full, kTileBytes);
           __syncwarp();
           if (!p.table) {
             if (lane == 0 && issue)
 #pragma unroll
               for (int bx = 0; bx < kBoxes; ++bx)
-                tma_load_3d(dst + bx * kBoxBytes, &tm_k, k_full + slot, bx * 64, kt * kTile, pair);
+                tma_load_3d(dst + bx * kBoxBytes, &tm_k, full, bx * 64,
+                            (at.r.first + at.tile) * kTile, pair);
           } else if (issue && lane < (kTile >> p.shift)) {
-            // a lane per page: pages past the last one with keys repeat it (their keys are
-            // masked), and a page outside the pool reads as zeros (past the map's end)
-            const int lp = min((kt * kTile >> p.shift) + lane, (walk.r.len - 1) >> p.shift);
-            int phys = -1;
-            if (MATTN_IN_BOUNDS(kSiteKwTable, lp, p.pages_per_seq))
-              phys = p.table[(size_t)walk.b * p.pages_per_seq + lp];
-            if (phys < 0 || phys >= p.num_pages) phys = p.num_pages;
+            const int phys = page < 0 || page >= p.num_pages ? p.num_pages : page;
 #pragma unroll
             for (int bx = 0; bx < kBoxes; ++bx)
-              tma_load_3d(dst + bx * kBoxBytes + (lane << p.shift) * 128, &tm_k, k_full + slot,
-                          bx * 64, 0, phys * p.Hkv + walk.hk);
+              tma_load_3d(dst + bx * kBoxBytes + (lane << p.shift) * 128, &tm_k, full, bx * 64, 0,
+                          phys * p.Hkv + walk.hk);
           }
+          at.advance(p);
+          page = page_of(at);
           __syncwarp();
-          ++k_it;
+          kr.next(p.k_slots);
         }
       }
       for (int m = 0; m < g; ++m) walk.advance(p);
       fresh = walk.left > 0 && walk.b * p.Hkv + walk.hk != pair;
     }
-    if (!ok && issue) {  // let copies in flight land
-      for (uint32_t i = 0; i < (uint32_t)p.k_slots && i < k_it; ++i) {
-        const uint32_t it = k_it - 1 - i;
-        wait_drain(k_full + it % p.k_slots, (it / p.k_slots) & 1);
-      }
-      for (uint32_t i = 0; i < (uint32_t)p.q_slots && i < q_it; ++i) {
-        const uint32_t it = q_it - 1 - i;
-        wait_drain(q_full + it % p.q_slots, (it / p.q_slots) & 1);
-      }
+    // On the way out of a failed wait copies in flight land first. The next pass of a slot not
+    // begun, its latest copy is that of the pass before: parity pass ^ 1, which a slot that
+    // was never used has too.
+    if (!ok && issue) {
+      for (int i = 0; i < p.k_slots; ++i, kr.next(p.k_slots))
+        wait_drain(k_full + kr.slot, kr.pass ^ 1);
+      for (int i = 0; i < p.q_slots; ++i, qr.next(p.q_slots))
+        wait_drain(q_full + qr.slot, qr.pass ^ 1);
     }
   } else if (warp == kKwMma) {
     const uint32_t idesc = idesc_bf16(128, p.n_cols, false);
-    uint32_t k_it = 0, q_it = 0, parity = 0;
-    uint32_t s_it0 = 0, s_it1 = 0;
+    const uint64_t a0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+    const uint64_t b0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    KwRing kr, qr;
+    uint32_t q_slot = 0, parity = 0, s_pass0 = 0, s_pass1 = 0;
     bool ok = true, fresh = true;
     while (walk.left > 0 && ok) {
       const int g = group_of(walk);
       const int pair = walk.b * p.Hkv + walk.hk;
-      KwWalk next = walk;
-      for (int m = 0; m < g; ++m) next.advance(p);
-      const bool leaves = next.left <= 0 || next.b * p.Hkv + next.hk != pair;
+      for (int m = 0; m < g; ++m) walk.advance(p);
+      const bool leaves = walk.left <= 0 || walk.b * p.Hkv + walk.hk != pair;
       const uint32_t x0 = p.blocks > 1 ? 0 : parity;
       for (int nb = 0; nb < p.blocks && ok; ++nb) {
         if (nb > 0 || fresh || p.blocks > 1) {
-          ok = kw_wait(q_full + q_it % p.q_slots, (q_it / p.q_slots) & 1, wd);
+          ok = kw_wait(q_full + qr.slot, qr.pass, wd);
           if (!ok) break;
-          ++q_it;
+          q_slot = qr.slot;
+          qr.next(p.q_slots);
         }
-        const uint32_t q_slot = (q_it - 1) % p.q_slots;
-        for (int m = 0; m < g && ok; ++m) {
-          const uint32_t x = (x0 + m) & 1, seq = k_it + m, slot = seq % p.k_slots;
+        KwRing kn = kr;
+        for (int m = 0; m < g && ok; ++m, kn.next(p.k_slots)) {
+          const uint32_t x = (x0 + m) & 1;
           if (nb == 0) {
-            ok = kw_wait(k_full + slot, (seq / p.k_slots) & 1, wd);
+            ok = kw_wait(k_full + kn.slot, kn.pass, wd);
             if (!ok) break;
           }
-          const uint32_t it = x ? s_it1 : s_it0;
-          ok = kw_wait(s_free + x, (it & 1) ^ 1, wd);
+          ok = kw_wait(s_free + x, (x ? s_pass1 : s_pass0) ^ 1, wd);
           if (!ok) break;
-          if (x) ++s_it1; else ++s_it0;
+          if (x) s_pass1 ^= 1;
+          else s_pass0 ^= 1;
           tc_fence_after();
-          const uint64_t a0 = sdesc_sw128(smem_u32(sK + slot * kTileBytes), 16, 1024);
-          const uint64_t b0 = sdesc_sw128(smem_u32(sQ + q_slot * q_bytes), 16, 1024);
+          const uint64_t ak = a0 + (uint64_t)((kn.slot * kTileBytes) >> 4);
+          const uint64_t bq = b0 + (uint64_t)((q_slot * q_bytes) >> 4);
           uint64_t a[D / 16], b[D / 16];
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            a[kk] = a0 + (uint64_t)(((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4);
-            b[kk] = b0 + (uint64_t)(((kk / 4) * q_box + (kk % 4) * 32) >> 4);
+            a[kk] = ak + (uint64_t)(((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4);
+            b[kk] = bq + (uint64_t)(((kk / 4) * q_box + (kk % 4) * 32) >> 4);
           }
           mma_ss_warp<D / 16>(tmem + kKwMaxN * x, a, b, idesc, 0u);
           mma_commit_warp(s_full + x);
-          if (nb == p.blocks - 1) mma_commit_warp(k_empty + slot);
+          if (nb == p.blocks - 1) mma_commit_warp(k_empty + kn.slot);
           if (m == g - 1 && (p.blocks > 1 || leaves)) mma_commit_warp(q_empty + q_slot);
           __syncwarp();
         }
       }
-      k_it += g;
+      for (int m = 0; m < g; ++m) kr.next(p.k_slots);
       parity ^= 1;
-      walk = next;
       fresh = leaves;
     }
     mma_commit_warp(drain);
     __syncwarp();
     wait_drain(drain, 0);
-  } else {
+  } else if (warp < kKwProducer) {
     const uint32_t x = warp >> 2;     // warpgroup
     const int t = threadIdx.x & 127;  // key of the tile, TMEM lane
     const uint32_t cols = tmem + (uint32_t((warp & 3) * 32) << 16) + kKwMaxN * x;
@@ -459,7 +486,13 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       const bool store = mine && j < len &&
                          MATTN_IN_BOUNDS(kSiteKwOut, at, (size_t)p.B * p.Hkv * p.stride);
       float old = 0.0f;
-      if (store && p.previous) old = p.previous[at];
+      if (store && p.previous) {
+        old = p.previous[at];
+        // a line per warp, to be in the L2 when its tile comes
+        constexpr int kAhead = 8 * kTile;
+        if (lane == 0 && j + kAhead < len)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.previous + at + kAhead));
+      }
       float2 sum[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
@@ -498,19 +531,29 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         tc_fence_after();
         auto columns_sum = [&](auto mask) {
           constexpr bool kMask = decltype(mask)::value;
-          int c = 0;
-          for (; c + 32 <= p.n_cols; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(cols + c, v);
-            tmem_ld_wait_regs(v);
-            kw_add<SCORE, kMask, 32>(p, col, c, j, len, v, sum);
-          }
-          if (c < p.n_cols) {
+          if (p.n_cols == 16) {
             uint32_t v[16];
-            tmem_ld16(cols + c, v);
+            tmem_ld16(cols, v);
             tmem_ld16_wait(v);
-            kw_add<SCORE, kMask, 16>(p, col, c, j, len, v, sum);
+            kw_add<SCORE, kMask, 16>(p, col, 0, j, len, v, sum);
+            return;
           }
+          // The next 32 columns are on their way while 32 are worked on (16 at a time, the
+          // loads' latency bounded it: 3600 cycles for 256 columns). The last load of an even
+          // number repeats the last columns: a load under a condition would cost registers.
+          uint32_t v0[32], v1[32];
+          tmem_ld32(cols, v0);
+          int c = 0;
+          for (; c + 64 <= p.n_cols; c += 64) {
+            tmem_ld_wait_regs(v0);
+            tmem_ld32(cols + c + 32, v1);
+            kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
+            tmem_ld_wait_regs(v1);
+            tmem_ld32(cols + min(c + 64, p.n_cols - 32), v0);
+            kw_add<SCORE, kMask, 32>(p, col, c + 32, j, len, v1, sum);
+          }
+          tmem_ld_wait_regs(v0);
+          if (c < p.n_cols) kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
         };
         if (whole) columns_sum(std::false_type{});
         else columns_sum(std::true_type{});
@@ -543,9 +586,8 @@ cudaError_t launch_typed(const CUtensorMap& mq, const CUtensorMap& mk, const KwP
                          unsigned grid, size_t smem, cudaStream_t s) {
   static DeviceOnce ready;
   const cudaError_t e = ready.allow_smem(key_weights_kernel<D, SCORE>, kKwSmem);
-  return e != cudaSuccess
-             ? e
-             : launch_early(key_weights_kernel<D, SCORE>, grid, kKwThreads, smem, s, mq, mk, p);
+  if (e != cudaSuccess) return e;
+  return launch_early(key_weights_kernel<D, SCORE>, grid, kKwThreads, smem, s, mq, mk, p);
 }
 
 template <int D>
@@ -553,7 +595,8 @@ cudaError_t launch_key_weights(const void* q, const void* k, KwProblem& p, cudaS
   const int R = p.Hq / p.Hkv * p.Sq;
   // Query rows of a product: all, up to 256; more of them in blocks of like size.
   p.blocks = (R + kKwMaxN - 1) / kKwMaxN;
-  p.n_cols = ((R + p.blocks - 1) / p.blocks + 15) / 16 * 16;
+  p.n_cols = (R + p.blocks - 1) / p.blocks;
+  p.n_cols = p.n_cols <= 16 ? 16 : (p.n_cols + 31) / 32 * 32;
   const int q_bytes = p.n_cols * D * 2, k_bytes = kTile * D * 2;
   // Two places for query rows where blocks stream or where it leaves four tiles of keys.
   p.q_slots = p.blocks > 1 || 2 * q_bytes + 4 * k_bytes + 1024 <= kKwSmem ? 2 : 1;
