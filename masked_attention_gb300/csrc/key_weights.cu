@@ -73,16 +73,19 @@ __device__ __forceinline__ KwRange kw_range(const KwProblem& p, int b) {
   return r;
 }
 
-// A CTA's walk over its tiles; every role walks alike.
+// A CTA's walk over its tiles, the CTA's share of one pair after the other; every role walks
+// alike. (Tile by tile a walk's bookkeeping cost the MMA warp 900 cycles each.)
 struct KwWalk {
-  int b, hk, tile;    // tile counts from the sequence's first visible one
-  long long left;     // tiles still to go, this one included
+  int b, hk, tile;  // tile counts from the sequence's first visible one
+  long long left;   // tiles still to go
   KwRange r;
-  __device__ __forceinline__ void advance(const KwProblem& p) {
-    --left;
-    if (++tile < r.tiles || left <= 0) return;
+  __device__ __forceinline__ int run() const {  // tiles of this pair
+    return (int)min(left, (long long)(r.tiles - tile));
+  }
+  __device__ __forceinline__ void next_pair(const KwProblem& p) {
+    left -= run();
     tile = 0;
-    if (++hk < p.Hkv) return;
+    if (left <= 0 || ++hk < p.Hkv) return;
     hk = 0;
     do r = kw_range(p, ++b);
     while (r.tiles == 0 && b + 1 < p.B);  // left > 0: a later sequence has tiles
@@ -296,74 +299,68 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     walk.tile = (int)(first_tile % walk.r.tiles);
   }
   const int R = p.Hq / p.Hkv * p.Sq;
-  // Tiles that share a pass over the query blocks: two of one pair with several blocks.
-  auto group_of = [&](const KwWalk& w) {
-    return p.blocks > 1 && w.left > 1 && w.tile + 1 < w.r.tiles ? 2 : 1;
-  };
 
   if (warp == kKwProducer) {
     const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
     KwRing kr, qr;
-    bool ok = true, fresh = true;  // fresh: the pair's query rows are not loaded
+    bool ok = true;
     // A lane per page of a tile, its table entry read one tile ahead. Pages past the last one
     // with keys repeat it (their keys are masked); one outside the pool reads as zeros (past
     // the map's end).
-    auto page_of = [&](const KwWalk& w) {
-      if (!p.table || w.left <= 0 || lane >= (kTile >> p.shift)) return 0;
-      const int lp = min(((w.r.first + w.tile) * kTile >> p.shift) + lane, (w.r.len - 1) >> p.shift);
+    auto page_of = [&](const KwWalk& w, int i) {
+      if (!p.table || lane >= (kTile >> p.shift)) return 0;
+      const int lp = min(((w.r.first + w.tile + i) * kTile >> p.shift) + lane,
+                         (w.r.len - 1) >> p.shift);
       int phys = -1;
       if (MATTN_IN_BOUNDS(kSiteKwTable, lp, p.pages_per_seq))
         phys = p.table[(size_t)w.b * p.pages_per_seq + lp];
       return phys;
     };
-    int page = page_of(walk);
-    while (walk.left > 0 && ok) {
-      const int g = group_of(walk);
-      const int pair = walk.b * p.Hkv + walk.hk;
-      KwWalk at = walk;  // goes on to each tile that is loaded
-      for (int nb = 0; nb < p.blocks && ok; ++nb) {
-        if (nb > 0 || fresh || p.blocks > 1) {
-          ok = kw_wait(q_empty + qr.slot, qr.pass ^ 1, wd);
-          if (!ok) break;
-          if (lane == 0 && issue) {
-            mbar_arrive_expect_tx(q_full + qr.slot, q_bytes);
+    auto load_rows = [&](int nb, int pair) {
+      if (!kw_wait(q_empty + qr.slot, qr.pass ^ 1, wd)) return false;
+      if (lane == 0 && issue) {
+        mbar_arrive_expect_tx(q_full + qr.slot, q_bytes);
 #pragma unroll
-            for (int bx = 0; bx < kBoxes; ++bx)
-              tma_load_3d(sQ + qr.slot * q_bytes + bx * q_box, &tm_q, q_full + qr.slot, bx * 64,
-                          nb * p.n_cols, pair);
-          }
-          __syncwarp();
-          qr.next(p.q_slots);
-        }
-        if (nb > 0) continue;
-        for (int m = 0; m < g && ok; ++m) {
-          ok = kw_wait(k_empty + kr.slot, kr.pass ^ 1, wd);
-          if (!ok) break;
-          uint64_t* full = k_full + kr.slot;
-          uint8_t* dst = sK + kr.slot * kTileBytes;
-          if (lane == 0 && issue) mbar_arrive_expect_tx(full, kTileBytes);
-          __syncwarp();
-          if (!p.table) {
-            if (lane == 0 && issue)
-#pragma unroll
-              for (int bx = 0; bx < kBoxes; ++bx)
-                tma_load_3d(dst + bx * kBoxBytes, &tm_k, full, bx * 64,
-                            (at.r.first + at.tile) * kTile, pair);
-          } else if (issue && lane < (kTile >> p.shift)) {
-            const int phys = page < 0 || page >= p.num_pages ? p.num_pages : page;
-#pragma unroll
-            for (int bx = 0; bx < kBoxes; ++bx)
-              tma_load_3d(dst + bx * kBoxBytes + (lane << p.shift) * 128, &tm_k, full, bx * 64, 0,
-                          phys * p.Hkv + walk.hk);
-          }
-          at.advance(p);
-          page = page_of(at);
-          __syncwarp();
-          kr.next(p.k_slots);
-        }
+        for (int bx = 0; bx < kBoxes; ++bx)
+          tma_load_3d(sQ + qr.slot * q_bytes + bx * q_box, &tm_q, q_full + qr.slot, bx * 64,
+                      nb * p.n_cols, pair);
       }
-      for (int m = 0; m < g; ++m) walk.advance(p);
-      fresh = walk.left > 0 && walk.b * p.Hkv + walk.hk != pair;
+      __syncwarp();
+      qr.next(p.q_slots);
+      return true;
+    };
+    while (walk.left > 0 && ok) {
+      const int run = walk.run(), pair = walk.b * p.Hkv + walk.hk;
+      int page = page_of(walk, 0);
+      for (int i = 0; i < run && ok; ++i) {
+        // blocks of rows go before every group of tiles, their first one before the tiles
+        if (p.blocks > 1 ? (i & 1) == 0 : i == 0) ok = load_rows(0, pair);
+        ok = ok && kw_wait(k_empty + kr.slot, kr.pass ^ 1, wd);
+        if (!ok) break;
+        uint64_t* full = k_full + kr.slot;
+        uint8_t* dst = sK + kr.slot * kTileBytes;
+        if (lane == 0 && issue) mbar_arrive_expect_tx(full, kTileBytes);
+        __syncwarp();
+        if (!p.table) {
+          if (lane == 0 && issue)
+#pragma unroll
+            for (int bx = 0; bx < kBoxes; ++bx)
+              tma_load_3d(dst + bx * kBoxBytes, &tm_k, full, bx * 64,
+                          (walk.r.first + walk.tile + i) * kTile, pair);
+        } else if (issue && lane < (kTile >> p.shift)) {
+          const int phys = page < 0 || page >= p.num_pages ? p.num_pages : page;
+#pragma unroll
+          for (int bx = 0; bx < kBoxes; ++bx)
+            tma_load_3d(dst + bx * kBoxBytes + (lane << p.shift) * 128, &tm_k, full, bx * 64, 0,
+                        phys * p.Hkv + walk.hk);
+        }
+        if (i + 1 < run) page = page_of(walk, i + 1);
+        __syncwarp();
+        kr.next(p.k_slots);
+        if (p.blocks > 1 && ((i & 1) || i + 1 == run))
+          for (int nb = 1; nb < p.blocks && ok; ++nb) ok = load_rows(nb, pair);
+      }
+      walk.next_pair(p);
     }
     // On the way out of a failed wait copies in flight land first. The next pass of a slot not
     // begun, its latest copy is that of the pass before: parity pass ^ 1, which a slot that
@@ -379,51 +376,57 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     const uint64_t a0 = sdesc_sw128(smem_u32(sK), 16, 1024);
     const uint64_t b0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
     KwRing kr, qr;
-    uint32_t q_slot = 0, parity = 0, s_pass0 = 0, s_pass1 = 0;
-    bool ok = true, fresh = true;
-    while (walk.left > 0 && ok) {
-      const int g = group_of(walk);
-      const int pair = walk.b * p.Hkv + walk.hk;
-      for (int m = 0; m < g; ++m) walk.advance(p);
-      const bool leaves = walk.left <= 0 || walk.b * p.Hkv + walk.hk != pair;
-      const uint32_t x0 = p.blocks > 1 ? 0 : parity;
-      for (int nb = 0; nb < p.blocks && ok; ++nb) {
-        if (nb > 0 || fresh || p.blocks > 1) {
-          ok = kw_wait(q_full + qr.slot, qr.pass, wd);
-          if (!ok) break;
-          q_slot = qr.slot;
-          qr.next(p.q_slots);
-        }
-        KwRing kn = kr;
-        for (int m = 0; m < g && ok; ++m, kn.next(p.k_slots)) {
-          const uint32_t x = (x0 + m) & 1;
-          if (nb == 0) {
-            ok = kw_wait(k_full + kn.slot, kn.pass, wd);
-            if (!ok) break;
-          }
-          ok = kw_wait(s_free + x, (x ? s_pass1 : s_pass0) ^ 1, wd);
-          if (!ok) break;
-          if (x) s_pass1 ^= 1;
-          else s_pass0 ^= 1;
-          tc_fence_after();
-          const uint64_t ak = a0 + (uint64_t)((kn.slot * kTileBytes) >> 4);
-          const uint64_t bq = b0 + (uint64_t)((q_slot * q_bytes) >> 4);
-          uint64_t a[D / 16], b[D / 16];
+    uint32_t x = 0, s_pass = 0;  // s_pass: bit x is the parity of that warpgroup's buffer
+    bool ok = true;
+    // S^T of the tile in K slot `slot` and the query rows in use, for warpgroup x
+    auto product = [&](uint32_t slot) {
+      if (!kw_wait(s_free + x, ((s_pass >> x) & 1) ^ 1, wd)) return false;
+      s_pass ^= 1u << x;
+      tc_fence_after();
+      const uint64_t ak = a0 + (uint64_t)((slot * kTileBytes) >> 4);
+      const uint64_t bq = b0 + (uint64_t)((qr.slot * q_bytes) >> 4);
+      uint64_t a[D / 16], b[D / 16];
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            a[kk] = ak + (uint64_t)(((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4);
-            b[kk] = bq + (uint64_t)(((kk / 4) * q_box + (kk % 4) * 32) >> 4);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        a[kk] = ak + (uint64_t)(((kk / 4) * kBoxBytes + (kk % 4) * 32) >> 4);
+        b[kk] = bq + (uint64_t)(((kk / 4) * q_box + (kk % 4) * 32) >> 4);
+      }
+      mma_ss_warp<D / 16>(tmem + kKwMaxN * x, a, b, idesc, 0u);
+      mma_commit_warp(s_full + x);
+      x ^= 1;
+      return true;
+    };
+    while (walk.left > 0 && ok) {
+      const int run = walk.run();
+      if (p.blocks == 1) {
+        ok = kw_wait(q_full + qr.slot, qr.pass, wd);
+        for (int i = 0; i < run && ok; ++i) {
+          ok = kw_wait(k_full + kr.slot, kr.pass, wd) && product(kr.slot);
+          if (ok) mma_commit_warp(k_empty + kr.slot);
+          kr.next(p.k_slots);
+        }
+        if (ok) mma_commit_warp(q_empty + qr.slot);
+        qr.next(p.q_slots);
+      } else {
+        for (int i = 0; i < run && ok; i += 2) {
+          const int g = min(2, run - i);
+          KwRing kn = kr;
+          for (int nb = 0; nb < p.blocks && ok; ++nb) {
+            ok = kw_wait(q_full + qr.slot, qr.pass, wd);
+            kn = kr;
+            x = 0;
+            for (int m = 0; m < g && ok; ++m) {
+              ok = (nb > 0 || kw_wait(k_full + kn.slot, kn.pass, wd)) && product(kn.slot);
+              if (ok && nb == p.blocks - 1) mma_commit_warp(k_empty + kn.slot);
+              kn.next(p.k_slots);
+            }
+            if (ok) mma_commit_warp(q_empty + qr.slot);
+            qr.next(p.q_slots);
           }
-          mma_ss_warp<D / 16>(tmem + kKwMaxN * x, a, b, idesc, 0u);
-          mma_commit_warp(s_full + x);
-          if (nb == p.blocks - 1) mma_commit_warp(k_empty + kn.slot);
-          if (m == g - 1 && (p.blocks > 1 || leaves)) mma_commit_warp(q_empty + q_slot);
-          __syncwarp();
+          kr = kn;
         }
       }
-      for (int m = 0; m < g; ++m) kr.next(p.k_slots);
-      parity ^= 1;
-      fresh = leaves;
+      walk.next_pair(p);
     }
     mma_commit_warp(drain);
     __syncwarp();
@@ -445,7 +448,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         }
       }
     }
-    uint32_t parity = 0, s_it = 0, wg_it = 0;
+    uint32_t turn = 0, s_it = 0, wg_it = 0;  // turn: the warpgroup of the pair's first tile
     bool ok = true;
     // The warpgroup meets (a bounded wait, so that no warp is left behind in one).
     auto meet = [&]() {
@@ -454,118 +457,121 @@ __global__ void __launch_bounds__(kKwThreads, 1)
       return kw_wait(wg_bar + x, wg_it++ & 1, wd);
     };
     // The columns of a (pair, block) are read one use ahead, two by each thread.
-    auto read_lse = [&](const KwWalk& w, int nb, float (&out)[2]) {
+    float ahead[2];
+    auto read_lse = [&](const KwWalk& w, int nb) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int c = t + 128 * i, row = nb * p.n_cols + c;
-        out[i] = INFINITY;  // adds nothing
+        ahead[i] = INFINITY;  // adds nothing
         if (c < p.n_cols && row < R) {
           const size_t at = ((size_t)w.b * p.Hq + (size_t)w.hk * (p.Hq / p.Hkv)) * p.Sq + row;
-          if (MATTN_IN_BOUNDS(kSiteKwLse, at, (size_t)p.B * p.Hq * p.Sq)) out[i] = p.lse[at];
+          if (MATTN_IN_BOUNDS(kSiteKwLse, at, (size_t)p.B * p.Hq * p.Sq)) ahead[i] = p.lse[at];
         }
       }
     };
-    float ahead[2];
-    int have_pair = -1, have_block = -1;  // the columns in shared memory
-    if (walk.left > 0) read_lse(walk, 0, ahead);
-    while (walk.left > 0 && ok) {
-      const int g = group_of(walk);
-      const int pair = walk.b * p.Hkv + walk.hk;
-      KwWalk next = walk;
-      for (int m = 0; m < g; ++m) next.advance(p);
-      const uint32_t x0 = p.blocks > 1 ? 0 : parity;
-      const int m = (int)(x ^ x0);  // this warpgroup's tile of the group
-      const bool mine = m < g;
-      const int len = walk.r.len;
-      const int j0 = (walk.r.first + walk.tile + m) * kTile, j = j0 + t;
-      const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
-      const bool whole = j0 + kTile <= len && len >= p.Sq &&
-                         (!causal || j0 + kTile - 1 <= len - p.Sq) &&
-                         (!windowed || len - 1 - j0 < p.window);
-      const size_t at = (size_t)pair * p.stride + j;
-      const bool store = mine && j < len &&
-                         MATTN_IN_BOUNDS(kSiteKwOut, at, (size_t)p.B * p.Hkv * p.stride);
-      float old = 0.0f;
-      if (store && p.previous) {
-        old = p.previous[at];
-        // a line per warp, to be in the L2 when its tile comes
-        constexpr int kAhead = 8 * kTile;
-        if (lane == 0 && j + kAhead < len)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.previous + at + kAhead));
-      }
-      float2 sum[4];
+    auto set_columns = [&](const KwWalk& w, int nb) {
+      if (!meet()) return false;  // the block before has been used by all
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
-      for (int nb = 0; nb < p.blocks && ok; ++nb) {
-        if (have_pair != pair || have_block != nb) {
-          have_pair = pair;
-          have_block = nb;
-          ok = meet();  // the block before has been used by all
-          if (!ok) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = t + 128 * i, row = nb * p.n_cols + c;
-            if (c < p.n_cols) {
-              // a row without keys (LSE -inf) adds nothing
-              col.nlse[c] = ahead[i] == -INFINITY ? -INFINITY : -ahead[i] * kLog2e;
-              const bool there = row < R;
-              col.pos[c] = there ? len - p.Sq + row % p.Sq : -1;
-              if constexpr (SCORE & 1) {
-                const int h = walk.hk * (p.Hq / p.Hkv) + (there ? row / p.Sq : 0);
-                const float slope = p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq));
-                col.slope[c] = slope * kLog2e;
-              }
-            }
+      for (int i = 0; i < 2; ++i) {
+        const int c = t + 128 * i, row = nb * p.n_cols + c;
+        if (c < p.n_cols) {
+          // a row without keys (LSE -inf) adds nothing
+          col.nlse[c] = ahead[i] == -INFINITY ? -INFINITY : -ahead[i] * kLog2e;
+          const bool there = row < R;
+          col.pos[c] = there ? w.r.len - p.Sq + row % p.Sq : -1;
+          if constexpr (SCORE & 1) {
+            const int h = w.hk * (p.Hq / p.Hkv) + (there ? row / p.Sq : 0);
+            const float slope = p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq));
+            col.slope[c] = slope * kLog2e;
           }
-          ok = meet();
-          if (!ok) break;
         }
-        // the next block, or the next pair's first
-        if (nb + 1 < p.blocks) read_lse(walk, nb + 1, ahead);
-        else if (next.left > 0 && (p.blocks > 1 || next.b * p.Hkv + next.hk != pair))
-          read_lse(next, 0, ahead);
-        if (!mine) continue;
-        ok = kw_wait(s_full + x, s_it & 1, wd);
+      }
+      return meet();
+    };
+    const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+    if (walk.left > 0) read_lse(walk, 0);
+    while (walk.left > 0 && ok) {
+      const int run = walk.run(), len = walk.r.len;
+      const size_t row0 = (size_t)(walk.b * p.Hkv + walk.hk) * p.stride;
+      KwWalk next = walk;
+      next.next_pair(p);
+      if (p.blocks == 1) {
+        ok = set_columns(walk, 0);
         if (!ok) break;
-        ++s_it;
-        tc_fence_after();
-        auto columns_sum = [&](auto mask) {
-          constexpr bool kMask = decltype(mask)::value;
-          if (p.n_cols == 16) {
-            uint32_t v[16];
-            tmem_ld16(cols, v);
-            tmem_ld16_wait(v);
-            kw_add<SCORE, kMask, 16>(p, col, 0, j, len, v, sum);
-            return;
+        if (next.left > 0) read_lse(next, 0);
+      }
+      for (int i0 = 0; i0 < run && ok; i0 += 2) {
+        const int i = i0 + (int)(p.blocks > 1 ? x : x ^ turn);  // this warpgroup's tile
+        const bool mine = i < run;
+        const int j0 = (walk.r.first + walk.tile + i) * kTile, j = j0 + t;
+        const bool whole = j0 + kTile <= len && len >= p.Sq &&
+                           (!causal || j0 + kTile - 1 <= len - p.Sq) &&
+                           (!windowed || len - 1 - j0 < p.window);
+        const size_t at = row0 + j;
+        const bool store = mine && j < len &&
+                           MATTN_IN_BOUNDS(kSiteKwOut, at, (size_t)p.B * p.Hkv * p.stride);
+        float old = 0.0f;
+        if (store && p.previous) {
+          old = p.previous[at];
+          // a line per warp, to be in the L2 when its tile comes
+          constexpr int kAhead = 8 * kTile;
+          if (lane == 0 && j + kAhead < len)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.previous + at + kAhead));
+        }
+        float2 sum[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[k] = make_float2(0.0f, 0.0f);
+        for (int nb = 0; nb < p.blocks && ok; ++nb) {
+          if (p.blocks > 1) {
+            ok = set_columns(walk, nb);
+            if (!ok) break;
+            if (nb + 1 < p.blocks) read_lse(walk, nb + 1);
+            else if (i0 + 2 < run) read_lse(walk, 0);
+            else if (next.left > 0) read_lse(next, 0);
           }
-          // The next 32 columns are on their way while 32 are worked on (16 at a time, the
-          // loads' latency bounded it: 3600 cycles for 256 columns). The last load of an even
-          // number repeats the last columns: a load under a condition would cost registers.
-          uint32_t v0[32], v1[32];
-          tmem_ld32(cols, v0);
-          int c = 0;
-          for (; c + 64 <= p.n_cols; c += 64) {
+          if (!mine) continue;
+          ok = kw_wait(s_full + x, s_it & 1, wd);
+          if (!ok) break;
+          ++s_it;
+          tc_fence_after();
+          auto columns_sum = [&](auto mask) {
+            constexpr bool kMask = decltype(mask)::value;
+            if (p.n_cols == 16) {
+              uint32_t v[16];
+              tmem_ld16(cols, v);
+              tmem_ld16_wait(v);
+              kw_add<SCORE, kMask, 16>(p, col, 0, j, len, v, sum);
+              return;
+            }
+            // The next 32 columns are on their way while 32 are worked on (16 at a time, the
+            // loads' latency bounded it: 3600 cycles for 256 columns). The last load of an even
+            // number repeats the last columns: a load under a condition would cost registers.
+            uint32_t v0[32], v1[32];
+            tmem_ld32(cols, v0);
+            int c = 0;
+            for (; c + 64 <= p.n_cols; c += 64) {
+              tmem_ld_wait_regs(v0);
+              tmem_ld32(cols + c + 32, v1);
+              kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
+              tmem_ld_wait_regs(v1);
+              tmem_ld32(cols + min(c + 64, p.n_cols - 32), v0);
+              kw_add<SCORE, kMask, 32>(p, col, c + 32, j, len, v1, sum);
+            }
             tmem_ld_wait_regs(v0);
-            tmem_ld32(cols + c + 32, v1);
-            kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
-            tmem_ld_wait_regs(v1);
-            tmem_ld32(cols + min(c + 64, p.n_cols - 32), v0);
-            kw_add<SCORE, kMask, 32>(p, col, c + 32, j, len, v1, sum);
-          }
-          tmem_ld_wait_regs(v0);
-          if (c < p.n_cols) kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
-        };
-        if (whole) columns_sum(std::false_type{});
-        else columns_sum(std::true_type{});
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + x);
+            if (c < p.n_cols) kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
+          };
+          if (whole) columns_sum(std::false_type{});
+          else columns_sum(std::true_type{});
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + x);
+        }
+        if (store && ok) {
+          const float2 s = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+          p.weights[at] = p.previous ? fmaf(p.decay, old, s.x + s.y) : s.x + s.y;
+        }
       }
-      if (store && ok) {
-        const float2 s = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
-        p.weights[at] = p.previous ? fmaf(p.decay, old, s.x + s.y) : s.x + s.y;
-      }
-      parity ^= 1;
+      turn = (turn + run) & 1;
       walk = next;
     }
   }
