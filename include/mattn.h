@@ -448,6 +448,47 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
                              int max_len, int D, int weights_stride, unsigned variant,
                              const attn_params* p, const int* seq_lens, struct CUstream_st* stream);
 
+/* Eviction from the bf16 paged cache by accumulated attention weight (attn_key_weights), per
+ * sequence and key/value head. With first = starts[b], or sink where starts is NULL (both cut to
+ * seq_lens[b]), the first `first` keys stay; of the n = seq_lens[b] - first others, where they
+ * are more than `keep`, the last `recent` (<= keep) stay and the keep - recent of the largest
+ * weights (equal ones: the lowest index; NaN counts as the largest), else all. The held keys move
+ * together in their order: held key m behind the first ones to position first + m. Each head
+ * keeps keys of its own, as many as the others, so positions count places of the cache from then
+ * on, not tokens: rotations that the rows hold stay true, positions of new tokens
+ * (attn_qk_norm_rope) are the caller's to count, and window and ALiBi terms see places.
+ *   weights      fp32 [B][Hkv][weights_stride]
+ *   weights_out  the same, the held keys' weights at their new positions and 0 from there to
+ *                seq_lens[b]; entries past seq_lens[b] stay. May be weights itself
+ *   k, v         bf16 page pools [num_pages][Hkv][page_size][D], D 64 or 128
+ *   page_table   int32 [B][pages_per_seq]
+ *   new_table    int32 [B][new_pages_per_seq], or NULL: the rows move in place. Otherwise held
+ *                rows are copied to the pages that it names, from position first rounded down
+ *                to whole pages on (pages before that, e.g. a shared prefix, stay in both tables,
+ *                and a row whose place is the same in both is left alone), and the old pages
+ *                keep what they hold. Rows past its end are not written
+ *   kept         int32 [B][Hkv][keep]  old positions of the held keys behind the first ones,
+ *                ascending, then -1
+ *   new_lens     int32 [B]   first + min(n, keep)
+ *   freed        int32 [max_freed]  the pages that the sequences no longer use, one sequence
+ *                after the other: entries of page_table from ceil(new_lens / page_size) on in
+ *                place, from first / page_size on with new_table, up to ceil(seq_lens /
+ *                page_size). Those past max_freed are dropped; other entries stay
+ *   info         int32 [2]   pages freed, sequences that gave up keys
+ * A page outside the pool reads as zeros and is not written. In place, a page that several
+ * sequences hold must lie among their first keys (whole pages before `first`); with new_table,
+ * its pages must hold no row that the call reads, other than in its own place. Lengths outside
+ * [0, max_len] count as the nearest bound. What is written overlaps nothing else
+ * (ATTN_ERR_INVALID_ARG). page_size 16, 32, 64 or 128; B <= 16384 and B * Hkv <= 65535
+ * (ATTN_ERR_UNSUPPORTED). Asynchronous on `stream`, two launches. */
+attn_status attn_cache_evict(const float* weights, float* weights_out, int weights_stride,
+                             const int* seq_lens, const int* starts, int sink, int keep,
+                             int recent, void* k, void* v, int num_pages, int page_size,
+                             const int* page_table, int pages_per_seq, const int* new_table,
+                             int new_pages_per_seq, int B, int Hkv, int max_len, int D, int* kept,
+                             int* new_lens, int* freed, int max_freed, int* info,
+                             struct CUstream_st* stream);
+
 /* Bytes of device buffer build_block_mask() needs (256-byte aligned pieces). */
 size_t attn_block_mask_bytes(int B, int Sq, int Skv, int transposed);
 

@@ -32,7 +32,7 @@ __all__ = [
     "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_axes",
     "attn_qk_norm_rope_axes_bwd", "attn_cache_q4_bytes", "attn_cache_store_q4",
     "attn_cache_load_q4", "attn_decode_q4", "attn_decode_q4_workspace_bytes",
-    "attn_key_weights",
+    "attn_key_weights", "attn_cache_evict",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmattn.so")
@@ -159,6 +159,9 @@ def lib() -> ctypes.CDLL:
         f = ctypes.c_float
         L.attn_key_weights.argtypes = [vp, vp, vp, vp, f, vp, i, i, i, i, i, i, i, u, P, vp, vp]
         L.attn_key_weights.restype = i
+        L.attn_cache_evict.argtypes = [vp, vp, i, vp, vp, i, i, i, vp, vp, i, i, vp, i, vp, i, i,
+                                       i, i, i, vp, vp, vp, i, vp, vp]
+        L.attn_cache_evict.restype = i
         L.attn_check_status.argtypes = [vp, vp]
         L.attn_check_status.restype = i
         L.attn_status_str.argtypes = [i]
@@ -885,6 +888,38 @@ def attn_key_weights(q, k, lse, weights, variant: int = 0, *, previous=None, dec
          decay, _tensor(w, "weights", weights, f32, dev, (B, Hkv, L)), B, Hq, Hkv, Sq, max_len, D,
          L, variant, ctypes.byref(p),
          None if seq_lens is None else _tensor(w, "seq_lens", seq_lens, _torch.int32, dev, (B,)))
+
+
+def attn_cache_evict(weights, seq_lens, k, v, page_table, weights_out, kept, new_lens, freed, info,
+                     *, page_size: int, recent: int, sink: int = 0, starts=None, new_table=None,
+                     stream=None) -> None:
+    """Eviction from the bf16 paged cache by attention weight: of every (sequence, key/value
+    head)'s keys the first ``sink`` (or ``starts`` [B] int32) stay, and of the others, where
+    they are more than ``kept.shape[2]``, the last ``recent`` and the heaviest by ``weights``
+    (fp32 [B, Hkv, L]), that many in all. Their rows in the pools ``k``, ``v`` (bf16 [num_pages,
+    Hkv, page, D]) move together in order, in place or, with ``new_table`` [B, pages], into its
+    pages. Writes ``weights_out`` (may be ``weights``), ``kept`` [B, Hkv, keep] (old positions,
+    -1 past the last), ``new_lens`` [B], ``freed`` (page ids no longer used) and ``info`` [2]:
+    pages freed, sequences cut. All int32. See include/mattn.h."""
+    w = "attn_cache_evict"
+    dev = _device(w, "weights", weights)
+    i32, f32, bf16 = _torch.int32, _torch.float32, _torch.bfloat16
+    B, Hkv, L = ws = weights.shape
+    pages, D = k.shape[0], k.shape[-1]
+    pool, per, keep = (pages, Hkv, page_size, D), page_table.shape[1], kept.shape[-1]
+    new = None if new_table is None else _tensor(w, "new_table", new_table, i32, dev,
+                                                 (B, new_table.shape[1]))
+    _run(w, lib().attn_cache_evict, dev, stream, _tensor(w, "weights", weights, f32, dev, ws),
+         _tensor(w, "weights_out", weights_out, f32, dev, ws), L,
+         _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)),
+         None if starts is None else _tensor(w, "starts", starts, i32, dev, (B,)), sink, keep,
+         recent, _tensor(w, "k", k, bf16, dev, pool), _tensor(w, "v", v, bf16, dev, pool), pages,
+         page_size, _tensor(w, "page_table", page_table, i32, dev, (B, per)), per, new,
+         0 if new is None else new_table.shape[1], B, Hkv, min(L, per * page_size), D,
+         _tensor(w, "kept", kept, i32, dev, (B, Hkv, keep)),
+         _tensor(w, "new_lens", new_lens, i32, dev, (B,)),
+         _tensor(w, "freed", freed, i32, dev, (freed.numel(),)), freed.numel(),
+         _tensor(w, "info", info, i32, dev, (2,)))
 
 
 def attn_check_status(status=None, stream=None) -> int:

@@ -604,6 +604,7 @@ const DebugTu kDebugTus[] = {
     {debug_fetch_cache_q4, debug_clear_cache_q4},
     {debug_fetch_decode_q4, debug_clear_decode_q4},
     {debug_fetch_key_weights, debug_clear_key_weights},
+    {debug_fetch_evict, debug_clear_evict},
 };
 
 }  // namespace
@@ -667,6 +668,8 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSiteKwTable: return "key weights: page-table entry";
     case kSiteKwLse: return "key weights: LSE";
     case kSiteKwOut: return "key weights: weight";
+    case kSiteEvict: return "eviction: page-table, kept-key or freed-page entry";
+    case kSiteEvictRow: return "eviction: row";
   }
   return "unknown";
 }

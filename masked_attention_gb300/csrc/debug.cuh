@@ -48,6 +48,8 @@ enum DebugSite : int {
   kSiteKwTable = 28,      // page-table entry read by the key weights
   kSiteKwLse = 29,        // LSE read by the key weights
   kSiteKwOut = 30,        // weight read or written by the key weights
+  kSiteEvict = 31,        // page-table, kept-key or freed-page entry of the eviction
+  kSiteEvictRow = 32,     // row read or written by the eviction
   kSiteCount
 };
 

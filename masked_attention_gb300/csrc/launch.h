@@ -83,6 +83,7 @@ MATTN_DECLARE_DEBUG_RECORD(norm_rope_axes)
 MATTN_DECLARE_DEBUG_RECORD(cache_q4)
 MATTN_DECLARE_DEBUG_RECORD(decode_q4)
 MATTN_DECLARE_DEBUG_RECORD(key_weights)
+MATTN_DECLARE_DEBUG_RECORD(evict)
 #undef MATTN_DECLARE_DEBUG_RECORD
 #endif
 

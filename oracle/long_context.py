@@ -83,3 +83,50 @@ def key_weights(q, rows, lse, previous, decay, lens, weights, *, causal=True, wi
             old = 0 if previous is None else decay * previous[b, hk, :n]
             out[b, hk, :n] = old + new
     return out, size
+
+
+def evict(weights, lens, starts, keep, recent, k, v, table, page, new_table, weights_out, freed):
+    """(weights_out, kept, new_lens, freed, info, k, v) after the eviction, key by key."""
+    B, Hkv, L = weights.shape
+    k, v, out, freed = k.copy(), v.copy(), weights_out.copy(), freed.copy()
+    kept = np.full((B, Hkv, keep), -1, np.int32)
+    new_lens, cut, gone = np.zeros(B, np.int32), 0, []
+    old = k.copy(), v.copy()
+    most = min(L, table.shape[1] * page)
+    for b in range(B):
+        n = min(max(int(lens[b]), 0), most)
+        first = min(max(int(starts[b]), 0), n)
+        fits = n - first <= keep
+        cut += not fits
+        new_lens[b] = n if fits else first + keep
+        dest = table if new_table is None else new_table
+        begin = first if new_table is None else first // page * page
+        have = -(-n // page)
+        stay = -(-int(new_lens[b]) // page) if new_table is None else first // page
+        gone += [int(x) for x in table[b, stay:have]]
+        for h in range(Hkv):
+            hold = list(range(first, n))
+            if not fits:
+                # NaN above all; equal weights by index
+                order = sorted(range(first, n - recent), key=lambda j: (
+                    -np.inf if np.isnan(weights[b, h, j]) else -weights[b, h, j],
+                    not np.isnan(weights[b, h, j]), j))
+                hold = sorted(order[:keep - recent]) + list(range(n - recent, n))
+            kept[b, h, :len(hold)] = hold
+            hold = list(range(first)) + hold
+            w = [weights[b, h, j] for j in hold]
+            out[b, h, :n] = 0
+            out[b, h, :len(w)] = w
+            for m, j in enumerate(hold):
+                if m < begin or (new_table is None and m == j):
+                    continue
+                src = int(table[b, j // page])
+                dst = int(dest[b, m // page]) if m // page < dest.shape[1] else -1
+                if not 0 <= dst < len(k) or (dst == src and m % page == j % page):
+                    continue
+                for pool, was in zip((k, v), old):
+                    row = was[src, h, j % page] if 0 <= src < len(k) else 0
+                    pool[dst, h, m % page] = row
+    n = min(len(gone), len(freed))
+    freed[:n] = gone[:n]
+    return out, kept, new_lens, freed, np.array([len(gone), cut], np.int32), k, v
