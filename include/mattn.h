@@ -425,6 +425,41 @@ attn_status attn_decode_q4(const void* q, const void* pool, void* o, float* lse,
  * device (0 when a sequence's keys are too few to share out). */
 size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_len, int D);
 
+/* Decode over a bf16 paged cache for sequences of their own lengths, groups of which share
+ * their first keys (a prompt behind many requests): O and LSE of every sequence over its own
+ * keys and, with one read for all, over those that its group shares. Arguments as for
+ * attn_decode_q4 (no sinks), with k and v bf16 page pools [num_pages][Hkv][page_size][D] (p:
+ * page_table, page_size, pages_per_seq, num_pages) and
+ *   group_starts  device int32 [G + 1], ascending: group g is sequences group_starts[g] to
+ *                 group_starts[g + 1] - 1 (entries are cut to [0, B], and one below an earlier
+ *                 one counts as that); sequences in no group share nothing
+ *   shared_lens   device int32 [G]: the first shared_lens[g] keys of the group's sequences are
+ *                 the same, in the same pages; the first sequence's table row may stand for all
+ *                 there, so each row of page_table must hold them
+ * G may be 0 (then both may be NULL): a decode of ragged lengths. A shared key past a
+ * sequence's own length is not seen by it. Row r of sequence b sits at absolute position
+ * i = seq_lens[b] - Sq + r and sees key j where
+ *   keep(i, j) = j < seq_len AND i >= 0 AND (CAUSAL: j <= i) AND (WINDOW: i - j < window).
+ * A row without a key gets O = 0, LSE = -inf. Products are of bf16 pairs and sums fp32;
+ * a probability is rounded to bf16 before it multiplies its value row. What a key that no row of
+ * its sequence (a shared one: of its group) sees holds, NaN included, changes nothing; of the
+ * seen ones, values must be finite for the rows that do not see them. A page index outside
+ * [0, num_pages) reads as zeros. `workspace`: device memory, 256-byte aligned, of
+ * attn_decode_shared_workspace_bytes() bytes (less: ATTN_ERR_WORKSPACE_TOO_SMALL); its contents
+ * need not be kept between calls, and calls that may run at the same time need one each.
+ * Results are bitwise reproducible. Asynchronous on `stream`, three launches.
+ * ATTN_ERR_UNSUPPORTED for (Hq / Hkv) * Sq > 16, B or G > 4096, B * Hkv > 65535. */
+attn_status attn_decode_shared(const void* q, const void* k, const void* v, void* o, float* lse,
+                               int B, int Hq, int Hkv, int Sq, int max_len, int D,
+                               unsigned variant, const attn_params* p, const int* seq_lens,
+                               const int* group_starts, const int* shared_lens, int G,
+                               void* workspace, size_t workspace_bytes,
+                               struct CUstream_st* stream);
+
+/* Bytes of workspace that attn_decode_shared() needs on the current device. */
+size_t attn_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Sq, int G, int max_len,
+                                          int D);
+
 /* The attention weight that each cached key received, e.g. to decide which keys a cache
  * gives up (attn_cache_evict):
  *   weights[b][hk][j] = decay * previous[b][hk][j]

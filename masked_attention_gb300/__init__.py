@@ -32,7 +32,8 @@ __all__ = [
     "attn_qk_norm_rope_bwd_workspace_bytes", "attn_qk_norm_rope_axes",
     "attn_qk_norm_rope_axes_bwd", "attn_cache_q4_bytes", "attn_cache_store_q4",
     "attn_cache_load_q4", "attn_decode_q4", "attn_decode_q4_workspace_bytes",
-    "attn_key_weights", "attn_cache_evict",
+    "attn_decode_shared", "attn_decode_shared_workspace_bytes", "attn_key_weights",
+    "attn_cache_evict",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmattn.so")
@@ -159,6 +160,11 @@ def lib() -> ctypes.CDLL:
         f = ctypes.c_float
         L.attn_key_weights.argtypes = [vp, vp, vp, vp, f, vp, i, i, i, i, i, i, i, u, P, vp, vp]
         L.attn_key_weights.restype = i
+        L.attn_decode_shared.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, u, P, vp, vp, vp, i,
+                                         vp, sz, vp]
+        L.attn_decode_shared.restype = i
+        L.attn_decode_shared_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
+        L.attn_decode_shared_workspace_bytes.restype = sz
         L.attn_cache_evict.argtypes = [vp, vp, i, vp, vp, i, i, i, vp, vp, i, i, vp, i, vp, i, i,
                                        i, i, i, vp, vp, vp, i, vp, vp]
         L.attn_cache_evict.restype = i
@@ -857,6 +863,46 @@ def _paged_params(w: str, dev: int, B: int, Hq: int, scale, window, softcap, ali
     p.timeout_ns = timeout_ns
     p.fault_inject = fault_inject
     return p
+
+
+def attn_decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, Sq: int, G: int, max_len: int,
+                                       D: int) -> int:
+    return int(lib().attn_decode_shared_workspace_bytes(B, Hq, Hkv, Sq, G, max_len, D))
+
+
+def attn_decode_shared(q, k, v, o, lse, variant: int = 0, *, page_table, page_size: int, seq_lens,
+                       workspace, group_starts=None, shared_lens=None,
+                       max_len: Optional[int] = None, scale: float = 0.0, window: int = 0,
+                       softcap: float = 0.0, alibi_slopes=None, status=None, timeout_ns: int = 0,
+                       fault_inject: int = 0, stream=None) -> None:
+    """Decode over a bf16 paged cache for sequences of their own lengths, groups of which share
+    their first keys: ``q`` [B, Hq, Sq, D] (the last Sq tokens of each, (Hq/Hkv) * Sq <= 16)
+    against the ``seq_lens`` [B] int32 tokens that ``page_table`` [B, pages_per_seq] places in
+    the pools ``k``, ``v`` [num_pages, Hkv, page, D]. Sequences ``group_starts[g]`` to
+    ``group_starts[g + 1] - 1`` (int32 [G + 1]) hold the same first ``shared_lens[g]`` (int32
+    [G]) keys in the same pages, which are read once for all of them. ``max_len`` (default: all
+    the table holds) bounds seq_lens. Writes ``o`` (bf16, like q) and ``lse`` fp32 [B, Hq, Sq].
+    ``workspace``: a CUDA tensor of ``attn_decode_shared_workspace_bytes`` bytes."""
+    w = "attn_decode_shared"
+    dev = _device(w, "q", q)
+    bf16, i32 = _torch.bfloat16, _torch.int32
+    B, Hq, Sq, D = shape = q.shape
+    pages, Hkv = k.shape[:2]
+    pool = (pages, Hkv, page_size, D)
+    p = _paged_params(w, dev, B, Hq, scale, window, softcap, alibi_slopes, page_table, page_size,
+                      pages, status, timeout_ns, fault_inject)
+    G, gs, sl = 0, None, None
+    if group_starts is not None or shared_lens is not None:
+        G = shared_lens.numel() if shared_lens is not None else 0
+        sl = _tensor(w, "shared_lens", shared_lens, i32, dev, (G,))
+        gs = _tensor(w, "group_starts", group_starts, i32, dev, (G + 1,))
+    _run(w, lib().attn_decode_shared, dev, stream, _tensor(w, "q", q, bf16, dev, shape),
+         _tensor(w, "k", k, bf16, dev, pool), _tensor(w, "v", v, bf16, dev, pool),
+         _tensor(w, "o", o, bf16, dev, shape), _tensor(w, "lse", lse, _torch.float32, dev,
+                                                       (B, Hq, Sq)),
+         B, Hq, Hkv, Sq, p.pages_per_seq * page_size if max_len is None else max_len, D, variant,
+         ctypes.byref(p), _tensor(w, "seq_lens", seq_lens, i32, dev, (B,)), gs, sl, G,
+         *_workspace(w, workspace, dev))
 
 
 def attn_key_weights(q, k, lse, weights, variant: int = 0, *, previous=None, decay: float = 1.0,

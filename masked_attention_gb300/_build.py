@@ -23,7 +23,8 @@ LIB_DEBUG_PATH = os.path.join(HERE, "libmattn_debug.so")
 SOURCES = ["api.cu", "mask_build.cu", "fwd_f32.cu", "fwd_tc.cu", "fwd_tc_rb.cu",
            "fwd_tc_paged.cu", "bwd_tc.cu", "bwd_tc_ragged.cu", "bwd_tc_f16.cu",
            "bwd_noalloc.cu", "varlen.cu", "combine.cu", "decode.cu", "page_plan.cu",
-           "norm_rope.cu", "norm_rope_axes.cu", "cache_q4.cu", "decode_q4.cu", "key_weights.cu", "evict.cu"]
+           "norm_rope.cu", "norm_rope_axes.cu", "cache_q4.cu", "decode_q4.cu", "key_weights.cu", "evict.cu",
+           "decode_shared.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", INCLUDE]

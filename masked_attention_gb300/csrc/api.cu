@@ -605,6 +605,7 @@ const DebugTu kDebugTus[] = {
     {debug_fetch_decode_q4, debug_clear_decode_q4},
     {debug_fetch_key_weights, debug_clear_key_weights},
     {debug_fetch_evict, debug_clear_evict},
+    {debug_fetch_decode_shared, debug_clear_decode_shared},
 };
 
 }  // namespace
@@ -670,6 +671,10 @@ MATTN_API const char* attn_debug_site_name(int site) {
     case kSiteKwOut: return "key weights: weight";
     case kSiteEvict: return "eviction: page-table, kept-key or freed-page entry";
     case kSiteEvictRow: return "eviction: row";
+    case kSiteShPlan: return "shared-prefix decode: piece of the plan";
+    case kSiteShTable: return "shared-prefix decode: page-table entry";
+    case kSiteShPart: return "shared-prefix decode: partial result";
+    case kSiteShOut: return "shared-prefix decode: output row";
   }
   return "unknown";
 }

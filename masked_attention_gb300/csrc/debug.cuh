@@ -50,6 +50,10 @@ enum DebugSite : int {
   kSiteKwOut = 30,        // weight read or written by the key weights
   kSiteEvict = 31,        // page-table, kept-key or freed-page entry of the eviction
   kSiteEvictRow = 32,     // row read or written by the eviction
+  kSiteShPlan = 33,       // piece of the shared-prefix decode's plan
+  kSiteShTable = 34,      // page-table entry read by the shared-prefix decode
+  kSiteShPart = 35,       // partial result of the shared-prefix decode
+  kSiteShOut = 36,        // output row of the shared-prefix decode
   kSiteCount
 };
 

@@ -1,0 +1,1047 @@
+// Decode attention over a bf16 paged cache for sequences of their own lengths, groups of which
+// share their first keys (a long prompt behind many requests):
+//
+//   O = softmax(mask(mod(scale q K^T))) V  over the shared keys and the sequence's own, merged:
+//   with parts (O_p, LSE_p) over disjoint keys, LSE = ln sum e^LSE_p, O = sum e^(LSE_p - LSE) O_p.
+//
+// A shared key row is read once for all query rows of the group's sequences (as long as they
+// are no more than 128 of a key/value head, else once per 128), so HBM's part is
+// (shared + sum of own keys) * 4 D bytes per key/value head, against sequences * shared without.
+// With 128 rows a tile of 128 keys is 64 KB and 2 x 2 * 128^3 operations, so the tensor cores,
+// the exponentials and HBM all matter, and the product runs on tcgen05 with 128-row tiles.
+//
+// Work. A piece is a run of 128-key tiles of one key/value head for one 128-row block: of a
+// group's shared keys with up to 128 / R of its sequences (R query rows each: the heads of the
+// key/value head times Sq), or of one sequence's own keys with its R rows (the tile's other rows
+// idle: HBM bounds these). All pieces' tiles, one after the other, each with a constant for its
+// start and end, are dealt out evenly to two CTAs per SM (one's softmax runs under the other's
+// products). Shared keys with several row blocks are cut into chunks of one CTA's share first,
+// all blocks of a chunk side by side, so that CTAs that read the same keys do so at the same time
+// and the second reads them from the L2. A small first kernel lays the pieces out from the lengths on
+// the device, CTAs leave fp32 partial results in the workspace, a third kernel joins them.
+//
+// Within a CTA: warps 0 to 3 softmax, a thread per query row (TMEM lane); warp 4 TMA; warp 5
+// products: S = Q K^T (both from shared memory), P (bf16, over S in tensor memory, rounded to 8
+// bits as in the other bf16 calls; its sum is of the unrounded values), O += P V.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "host_util.h"
+#include "launch.h"
+#include "soft_cap.cuh"
+
+#define MATTN_API extern "C" __attribute__((visibility("default")))
+
+namespace mattn {
+namespace {
+
+constexpr int kShThreads = 192;
+constexpr int kShProducer = 4, kShMma = 5;  // warps; 0 to 3: softmax
+constexpr int kShPerSm = 2;
+constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memory
+constexpr int kShMaxRows = 16;
+constexpr int kShCost = 1;        // what a piece's start and end count for, in tiles
+constexpr int kShPlanThreads = 1024;
+constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
+
+struct ShDesc {  // a piece for every key/value head
+  long long start;  // of the first head's piece in the dealing out; each takes tiles + kShCost
+  int tiles;
+  int key0;      // first key of the first tile, a multiple of the page size
+  int klo, khi;  // keys of the piece
+  int seq, nseq;  // sequences of its rows
+  int lead;       // sequence whose table row is read
+  int shared;     // 1: shared keys
+};
+
+struct ShSeq {  // how to find a sequence's parts
+  int pdesc, step, chunks;  // pieces of its group's shared keys: pdesc + c * step
+  int row0;                 // its first row in their block
+  int sdesc;                // piece of its own keys, or -1
+};
+
+struct ShHead {
+  long long total, share;  // positions dealt out, and per CTA
+  int n_prefix;            // pieces (per head) of shared keys come first
+};
+
+struct ShProblem {
+  const int* seq_lens;
+  const int* starts;  // [G + 1]
+  const int* shared_lens;
+  const int* table;
+  const float* slopes;
+  void* o;
+  float* lse;
+  int B, Hq, Hkv, Sq, R, G, max_len;
+  int seqs_per_block;  // 128 / R
+  int shift, pages_per_seq, num_pages;
+  unsigned variant;
+  int window;
+  float scale2, softcap2, softcap_e;
+  int ctas, max_desc, max_prefix;
+  ShHead* head;
+  int* first;     // [ctas]: piece that a CTA begins in
+  ShDesc* desc;   // [max_desc]
+  ShSeq* seqs;    // [B]
+  float *p_lse, *p_o, *s_lse, *s_o;  // partial results: shared [slots][128], own [slots][R]
+  long long p_slots, s_slots;
+  int* status;
+  uint64_t timeout_ns;
+  unsigned fault_inject;
+};
+
+// ------------------------------------------------------------------------- the plan
+struct ShGroup {
+  int blocks, tiles;        // row blocks, tiles of its shared keys
+  int key0, low, shared;    // first key of the first tile, first one that is seen, their end
+  int chunks, piece;        // runs of tiles, its first piece
+  long long start;          // and that one's position
+};
+
+__device__ __forceinline__ int sh_len(const ShProblem& p, int b) {
+  return max(0, min(p.seq_lens[b], p.max_len));
+}
+// First key that some row of a sequence sees.
+__device__ __forceinline__ int sh_low(const ShProblem& p, int len) {
+  return p.variant & ATTN_MASK_WINDOW ? (int)max(0ll, (long long)len - p.Sq - p.window + 1) : 0;
+}
+__device__ __forceinline__ int sh_down(const ShProblem& p, int key) {
+  return key >> p.shift << p.shift;
+}
+
+// Block-wide scan: sum (or maximum) of the threads before, and of all.
+template <bool kMax, typename T>
+__device__ __forceinline__ T plan_scan(T mine, T* warps, T& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto join = [](T a, T b) { return kMax ? (a > b ? a : b) : a + b; };
+  T x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x = join(x, o);
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  T w = warps[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xffffffffu, w, d);
+    if (lane >= d) w = join(w, o);
+  }
+  all = __shfl_sync(0xffffffffu, w, 31);
+  const T before_warp = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  T before = __shfl_up_sync(0xffffffffu, x, 1);
+  if (lane == 0) before = 0;  // neutral: values are not negative
+  return warp ? join(before, before_warp) : before;
+}
+
+__global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShProblem p) {
+  extern __shared__ __align__(16) int plan_smem[];
+  int* group_of = plan_smem;                     // [B]: its group, or -1
+  int* begin = group_of + ((p.B + 3) & ~3);      // [G + 1]
+  ShGroup* groups = reinterpret_cast<ShGroup*>(begin + ((p.G + 4) & ~3));  // [G]
+  __shared__ long long warps[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  early_start();
+  for (int b = tid; b < p.B; b += kShPlanThreads) group_of[b] = -1;
+  // the groups' first sequences, ascending whatever they hold
+  long long carry = 0, all;
+  for (int g0 = 0; p.G > 0 && g0 <= p.G; g0 += kShPlanThreads) {
+    const int g = g0 + tid;
+    const long long x = g <= p.G ? max(0, min(p.starts[g], p.B)) : 0;
+    const long long before = plan_scan<true>(x, warps, all);
+    if (g <= p.G) begin[g] = (int)max(carry, max(before, x));
+    carry = max(carry, all);
+  }
+  __syncthreads();
+  // shared keys of the groups that have two sequences or more, a warp each
+  long long work = 0;
+  for (int g = warp; g < p.G; g += 32) {
+    const int b0 = begin[g], n = begin[g + 1] - b0;
+    ShGroup gr{};
+    if (n > 1) {
+      int longest = 0, low = INT_MAX;
+      for (int b = b0 + lane; b < b0 + n; b += 32) {
+        const int len = sh_len(p, b);
+        longest = max(longest, len);
+        if (len > 0) low = min(low, sh_low(p, len));
+      }
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      low = __reduce_min_sync(0xffffffffu, low);
+      const int end = min(p.shared_lens[g], longest);
+      if (end >= kShMinShared) {
+        gr.shared = end;
+        gr.blocks = (n + p.seqs_per_block - 1) / p.seqs_per_block;
+        gr.low = min(low, end);
+        gr.key0 = sh_down(p, gr.low);
+        gr.tiles = low < end ? (end - gr.key0 + kTile - 1) / kTile : 0;
+        for (int b = b0 + lane; b < b0 + n; b += 32) group_of[b] = g;
+      }
+    }
+    if (lane == 0) {
+      groups[g] = gr;
+      work += (long long)gr.tiles * gr.blocks;
+    }
+  }
+  __syncthreads();
+  // a sequence's own keys
+  struct Own {
+    int klo, len, key0, tiles;
+  };
+  auto own_of = [&](int b) {
+    Own w;
+    w.len = sh_len(p, b);
+    const int g = group_of[b];
+    w.klo = max(g >= 0 ? groups[g].shared : 0, sh_low(p, w.len));
+    w.key0 = sh_down(p, w.klo);
+    w.tiles = w.len > w.klo ? (w.len - w.key0 + kTile - 1) / kTile : 0;
+    return w;
+  };
+  for (int b = tid; b < p.B; b += kShPlanThreads) work += own_of(b).tiles;
+  plan_scan<false>(work, warps, all);
+  const long long chunk = max(1ll, (all * p.Hkv + p.ctas - 1) / p.ctas);
+  // Pieces and positions: of the shared keys, group by group, then of the sequences' own keys,
+  // counted in a first pass and, with the CTAs' share known, written in a second.
+  __shared__ long long share_smem;
+  long long at = 0, share = 1;
+  int n_prefix = 0;
+  auto begins = [&](long long c) { return c * share; };  // position of a CTA's first tile
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      if (tid == 0) {
+        share_smem = max(1ll, (at + p.ctas - 1) / p.ctas);
+        p.head->total = at;
+        p.head->share = share_smem;
+        p.head->n_prefix = n_prefix;
+      }
+      __syncthreads();
+      share = share_smem;
+    }
+    at = 0;
+    n_prefix = 0;
+    for (int g0 = 0; g0 < p.G; g0 += kShPlanThreads) {
+      const int g = g0 + tid;
+      long long n = 0, len = 0, all_n, all_len;
+      if (g < p.G && groups[g].tiles) {
+        ShGroup& gr = groups[g];
+        // one block of rows needs no chunks
+        gr.chunks = gr.blocks > 1 ? (int)((gr.tiles + chunk - 1) / chunk) : 1;
+        n = (long long)gr.chunks * gr.blocks;
+        len = (long long)p.Hkv * gr.blocks * (gr.tiles + gr.chunks * kShCost);
+      }
+      const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
+      const long long a0 = at + plan_scan<false>(len, warps, all_len);
+      if (n) {
+        groups[g].piece = (int)n0;
+        groups[g].start = a0;
+      }
+      n_prefix += (int)all_n;
+      at += all_len;
+    }
+    __syncthreads();
+    for (int g = warp; pass == 1 && g < p.G; g += 32) {  // a lane per piece
+      const ShGroup gr = groups[g];
+      const int n = gr.chunks * gr.blocks;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane, c = i / max(gr.blocks, 1), k = i - c * gr.blocks;
+        long long start = 0, end = 0;
+        if (i < n) {
+          const int t0 = (int)((long long)gr.tiles * c / gr.chunks);
+          const int t1 = (int)((long long)gr.tiles * (c + 1) / gr.chunks);
+          ShDesc x;
+          x.tiles = t1 - t0;
+          start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
+                                                 k * (long long)(x.tiles + kShCost));
+          end = start + (long long)p.Hkv * (x.tiles + kShCost);
+          x.start = start;
+          x.key0 = gr.key0 + t0 * kTile;
+          x.klo = max(x.key0, gr.low);
+          x.khi = min(gr.shared, gr.key0 + t1 * kTile);
+          x.seq = begin[g] + k * p.seqs_per_block;
+          x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
+          x.lead = begin[g];
+          x.shared = 1;
+          if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
+        }
+        for (int j = 0; j < min(32, n - i0); ++j) {  // the CTAs that begin in piece i0 + j
+          const long long s0 = __shfl_sync(0xffffffffu, start, j);
+          const long long s1 = __shfl_sync(0xffffffffu, end, j);
+          for (long long c0 = (s0 + share - 1) / share + lane; begins(c0) < s1; c0 += 32)
+            if (MATTN_IN_BOUNDS(kSiteShPlan, c0, p.ctas)) p.first[c0] = gr.piece + i0 + j;
+        }
+      }
+    }
+    for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
+      const int b = b0 + tid;
+      Own w{0, 0, 0, 0};
+      if (b < p.B) w = own_of(b);
+      const long long len = w.tiles ? (long long)p.Hkv * (w.tiles + kShCost) : 0;
+      long long all_len;
+      const long long a0 = at + plan_scan<false>(len, warps, all_len);
+      at += all_len;
+      if (pass == 0 || b >= p.B) continue;
+      ShDesc x;
+      x.start = a0;
+      x.tiles = w.tiles;  // 0: a piece that is passed over
+      x.key0 = w.key0;
+      x.klo = w.klo;
+      x.khi = w.len;
+      x.seq = x.lead = b;
+      x.nseq = 1;
+      x.shared = 0;
+      if (MATTN_IN_BOUNDS(kSiteShPlan, n_prefix + b, p.max_desc)) p.desc[n_prefix + b] = x;
+      for (long long c = (a0 + share - 1) / share; len && begins(c) < a0 + len; ++c)
+        if (MATTN_IN_BOUNDS(kSiteShPlan, c, p.ctas)) p.first[c] = n_prefix + b;
+      ShSeq q{0, 0, 0, 0, w.tiles ? n_prefix + b : -1};
+      const int g = group_of[b];
+      if (g >= 0 && groups[g].tiles) {
+        const int k = (b - begin[g]) / p.seqs_per_block;
+        q.pdesc = groups[g].piece + k;
+        q.step = groups[g].blocks;
+        q.chunks = groups[g].chunks;
+        q.row0 = (b - begin[g] - k * p.seqs_per_block) * p.R;
+      }
+      p.seqs[b] = q;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------- the pieces
+template <int D>
+struct ShCfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBoxBytes = kTile * 128;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kSlots = D == 128 ? 2 : 5;  // K and V tiles in turn
+  static constexpr int kSmem = (1 + kSlots) * kTileBytes + 1024;
+  static constexpr uint32_t kColO = 128;
+  static_assert(kSmem + 512 <= 113 * 1024, "two CTAs per SM");
+};
+
+__device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
+  const uint32_t hint = wd.timeout_ns < 1000000ull ? (uint32_t)wd.timeout_ns : 1000000u;
+  const bool done = mbar_try_wait(bar, parity) || mbar_try_wait_sleep(bar, parity, hint) ||
+                    wait_bounded(bar, parity, wd);
+  return __all_sync(0xffffffffu, done);
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+struct ShRing {
+  uint32_t slot = 0, pass = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      pass ^= 1;
+    }
+  }
+};
+
+// A CTA's walk over its share of the pieces: a run of tiles [t0, t1) of one after the other.
+struct ShWalk {
+  ShDesc d;
+  int at, h;        // piece and its head
+  int t0, t1;
+  long long lo, hi;  // positions still to go
+  // From position lo: the run that begins there (false: none left).
+  __device__ __forceinline__ bool find(const ShProblem& p) {
+    while (lo < hi) {
+      const long long len = d.tiles + kShCost;
+      const long long start = d.start + h * len;  // of this head's piece
+      const long long off = lo - start;
+      const long long end = min(hi, start + len);
+      if (d.tiles > 0 && end - start > kShCost) {
+        t0 = (int)max(0ll, off - kShCost);
+        t1 = (int)(end - start) - kShCost;
+        if (t0 < t1) return true;
+      }
+      lo = end;
+      if (lo < start + len || lo >= hi) return false;  // the share ends inside the piece
+      step(p);
+    }
+    return false;
+  }
+  __device__ __forceinline__ void step(const ShProblem& p) {
+    if (++h < p.Hkv) return;
+    h = 0;
+    do d = p.desc[++at];
+    while (d.tiles == 0);
+  }
+  __device__ __forceinline__ bool next(const ShProblem& p) {
+    const long long len = d.tiles + kShCost, start = d.start + h * len;
+    lo = start + kShCost + t1;
+    if (lo >= hi) return false;
+    step(p);
+    return find(p);
+  }
+};
+
+// What a softmax thread keeps of its row.
+struct ShRow {
+  int lo, hi;    // keys that it sees, relative to the tile's first
+  float slope2;  // ALiBi slope in log2 units
+  int pos;       // i - (first key of the tile)
+};
+
+// 32 columns from c0 on: the linear part of the score in log2 units, masked ones -inf.
+template <int SCORE, bool kMask>
+__device__ __forceinline__ float sh_linear(const ShProblem& p, const ShRow& r, float s, int c) {
+  float x = s * p.scale2;
+  if constexpr (SCORE & 1) x -= r.slope2 * float(r.pos - c);
+  if constexpr (kMask) x = c >= r.lo && c < r.hi ? x : -INFINITY;
+  return x;
+}
+
+template <int SCORE, bool kMask>
+__device__ __forceinline__ float sh_max32(const ShProblem& p, const ShRow& r, const uint32_t* v,
+                                          int c0) {
+  float x[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    const float s = __uint_as_float(v[c]);
+    x[c] = SCORE & 1 || kMask ? sh_linear<SCORE, kMask>(p, r, s, c0 + c) : s;
+  }
+  const float m = row_max<32>(x);
+  return SCORE & 1 || kMask ? m : m * p.scale2;
+}
+
+// P of 32 columns as packed bf16, and their sum.
+template <int SCORE, bool kMask>
+__device__ __forceinline__ float sh_exp32(const ShProblem& p, const ShRow& r, const uint32_t* v,
+                                          int c0, float m, uint32_t* pk) {
+  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  const float2 sl = make_float2(p.scale2, p.scale2), mm = make_float2(-m, -m);
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    const float s0 = __uint_as_float(v[c]), s1 = __uint_as_float(v[c + 1]);
+    float2 x;
+    if constexpr (SCORE == 0 && !kMask) {
+      x = ffma2(make_float2(s0, s1), sl, mm);
+    } else {
+      x.x = sh_linear<SCORE, false>(p, r, s0, c0 + c);
+      x.y = sh_linear<SCORE, false>(p, r, s1, c0 + c + 1);
+      if constexpr (SCORE & 2) {
+        x.x = soft_cap(x.x, p.softcap2, p.softcap_e);
+        x.y = soft_cap(x.y, p.softcap2, p.softcap_e);
+      }
+      x = fadd2(x, mm);
+    }
+    float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    if constexpr (kMask) {
+      e.x = c0 + c >= r.lo && c0 + c < r.hi ? e.x : 0.0f;
+      e.y = c0 + c + 1 >= r.lo && c0 + c + 1 < r.hi ? e.y : 0.0f;
+    }
+    sum[(c / 2) & 1] = fadd2(sum[(c / 2) & 1], e);
+    pk[c / 2] = pack_bf16x2(e.x, e.y);
+  }
+  const float2 t = fadd2(sum[0], sum[1]);
+  return t.x + t.y;
+}
+
+template <int D, int SCORE>
+__global__ void __launch_bounds__(kShThreads, kShPerSm)
+    decode_shared_kernel(const __grid_constant__ CUtensorMap tm_qs,
+                         const __grid_constant__ CUtensorMap tm_q1,
+                         const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const ShProblem p) {
+  using C = ShCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + C::kTileBytes;
+  __shared__ uint64_t bars[8 + 2 * C::kSlots];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_word;
+  uint64_t *q_full = bars, *q_empty = bars + 1, *s_full = bars + 2, *p_full = bars + 3,
+           *o_full = bars + 4, *o_free = bars + 5, *drain = bars + 6, *full = bars + 8,
+           *empty = full + C::kSlots;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &abort_word;
+  const Watchdog wd{abort_flag, p.status, p.timeout_ns};
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_full, 1);
+    mbar_init(o_free, 4);
+    mbar_init(drain, 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == kShMma) {
+    tmem_alloc(&tmem_base, 256);
+    tmem_relinquish();
+  }
+  if (warp == kShProducer && lane == 0) {
+    prefetch_tmap(&tm_qs);
+    prefetch_tmap(&tm_q1);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  early_start();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+
+  ShWalk walk;
+  const long long share = p.head->share, total = p.head->total;
+  walk.lo = min(total, blockIdx.x * share);
+  walk.hi = min(total, walk.lo + share);
+  bool more = walk.lo < walk.hi;
+  if (more) {
+    walk.at = p.first[blockIdx.x];
+    walk.d = p.desc[walk.at];
+    walk.h = (int)((walk.lo - walk.d.start) / (walk.d.tiles + kShCost));
+    more = walk.find(p);
+  }
+
+  if (warp == kShProducer) {
+    const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
+    ShRing kv;
+    uint32_t q_pass = 0;
+    bool ok = true;
+    const int per_tile = kTile >> p.shift;  // pages of a tile
+    while (more && ok) {
+      // A lane per page of a tile, its entry read one tile ahead. Pages past the last one with
+      // keys repeat it; one outside the pool reads as zeros (past the map's end).
+      const int last = (walk.d.khi - 1) >> p.shift, page0 = walk.d.key0 >> p.shift;
+      const int* row = p.table + (size_t)walk.d.lead * p.pages_per_seq;
+      auto page_of = [&](int t) {
+        if (lane >= per_tile) return 0;
+        const int lp = min(page0 + t * per_tile + lane, last);
+        return MATTN_IN_BOUNDS(kSiteShTable, lp, p.pages_per_seq) ? row[lp] : -1;
+      };
+      int page = page_of(walk.t0);
+      ok = sh_wait(q_empty, q_pass ^ 1, wd);
+      if (!ok) break;
+      q_pass ^= 1;
+      if (lane == 0 && issue) {
+        const int rows = walk.d.shared ? p.seqs_per_block * p.R : p.R;
+        mbar_arrive_expect_tx(q_full, rows * D * 2);
+#pragma unroll
+        for (int bx = 0; bx < C::kBoxes; ++bx)
+          tma_load_4d(sQ + bx * C::kBoxBytes, walk.d.shared ? &tm_qs : &tm_q1, q_full, bx * 64, 0,
+                      walk.h, walk.d.seq);
+      }
+      __syncwarp();
+      for (int t = walk.t0; t < walk.t1 && ok; ++t) {
+        const int z = (page < 0 || page >= p.num_pages ? p.num_pages : page) * p.Hkv + walk.h;
+        if (t + 1 < walk.t1) page = page_of(t + 1);
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          ok = ok && sh_wait(empty + kv.slot, kv.pass ^ 1, wd);
+          if (!ok) break;
+          uint8_t* dst = sKV + kv.slot * C::kTileBytes;
+          if (lane == 0 && issue) mbar_arrive_expect_tx(full + kv.slot, C::kTileBytes);
+          __syncwarp();
+          if (issue && lane < per_tile) {
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+              tma_load_3d(dst + bx * C::kBoxBytes + (lane << p.shift) * 128, which ? &tm_v : &tm_k,
+                          full + kv.slot, bx * 64, 0, z);
+          }
+          __syncwarp();
+          kv.next(C::kSlots);
+        }
+      }
+      more = ok && walk.next(p);
+    }
+    // On the way out of a failed wait copies in flight land first (an unused slot's wait ends
+    // at once).
+    if (!ok && issue) {
+      for (int i = 0; i < C::kSlots; ++i, kv.next(C::kSlots)) wait_drain(full + kv.slot, kv.pass ^ 1);
+      wait_drain(q_full, q_pass ^ 1);
+    }
+  } else if (warp == kShMma) {
+    constexpr uint32_t kIdescQK = idesc_bf16(128, 128, false);
+    constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
+    const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+    const uint64_t dK = sdesc_sw128(smem_u32(sKV), 16, 1024);
+    const uint64_t dV = sdesc_sw128(smem_u32(sKV), C::kBoxBytes, 1024);
+    ShRing kv;
+    uint32_t q_pass = 0, p_pass = 0, o_pass = 0;
+    bool ok = true;
+    while (more && ok) {
+      const int n = walk.t1 - walk.t0;
+      ok = sh_wait(q_full, q_pass, wd);
+      q_pass ^= 1;
+      for (int t = 0; t < n && ok; ++t) {
+        // S = Q K^T over the P of the tile before, which its product (issued before) has read
+        ok = sh_wait(full + kv.slot, kv.pass, wd);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          const uint64_t k0 = dK + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
+          uint64_t a[D / 16], b[D / 16];
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4);
+            a[kk] = dQ + off;
+            b[kk] = k0 + off;
+          }
+          mma_ss_warp<D / 16>(tmem, a, b, kIdescQK, 0u);
+        }
+        mma_commit_warp(s_full);
+        mma_commit_warp(empty + kv.slot);
+        if (t == n - 1) mma_commit_warp(q_empty);
+        __syncwarp();
+        kv.next(C::kSlots);
+        // O (+)= P V
+        ok = sh_wait(full + kv.slot, kv.pass, wd);
+        if (ok && t == 0) {
+          ok = sh_wait(o_free, o_pass ^ 1, wd);
+          o_pass ^= 1;
+        }
+        ok = ok && sh_wait(p_full, p_pass, wd);
+        if (!ok) break;
+        p_pass ^= 1;
+        tc_fence_after();
+        {
+          const uint64_t v0 = dV + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
+          uint32_t a[8];
+          uint64_t b[8];
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            a[kk] = tmem + kk * 8;
+            b[kk] = v0 + (uint64_t)((kk * 16 * 128) >> 4);
+          }
+          mma_ts_warp<8>(tmem + C::kColO, a, b, kIdescPV, t > 0 ? 1u : 0u);
+        }
+        mma_commit_warp(empty + kv.slot);
+        if (t == n - 1) mma_commit_warp(o_full);
+        __syncwarp();
+        kv.next(C::kSlots);
+      }
+      more = ok && walk.next(p);
+    }
+    mma_commit_warp(drain);
+    __syncwarp();
+    wait_drain(drain, 0);
+  } else {
+    const int t = threadIdx.x;  // row of the block, TMEM lane, and key of a tile
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    const uint32_t colS = tmem + lanes, colO = tmem + lanes + C::kColO;
+    const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+    ShRing kv;
+    uint32_t s_pass = 0, o_pass = 0;
+    bool ok = true;
+    int known = -1;  // piece whose rows these are
+    int lo = 0, hi = 0, pos = 0, head = 0;
+    while (more && ok) {
+      const ShDesc& d = walk.d;
+      if (known != walk.at) {  // the same rows for every head
+        known = walk.at;
+        const int q = t / p.R, r = t - q * p.R, g = r / p.Sq;
+        lo = hi = 0;
+        if (q < d.nseq) {
+          const int len = sh_len(p, d.seq + q);
+          pos = len - p.Sq + (r - g * p.Sq);
+          head = g;
+          hi = pos < 0 ? 0 : min(d.khi, causal ? pos + 1 : len);
+          lo = max(d.klo, windowed ? pos - p.window + 1 : 0);
+        }
+      }
+      const int rows = d.nseq * p.R;
+      const bool active = warp * 32 < rows;  // a warp without rows only keeps step
+      // keys that some row of the piece sees: values of others are zeroed before their product
+      int vlo = d.klo, vhi = d.khi;
+      if (windowed && !d.shared) vlo = max(vlo, sh_low(p, d.khi));
+      ShRow row{};
+      if constexpr (SCORE & 1) {
+        const int hq = walk.h * (p.Hq / p.Hkv) + head;
+        row.slope2 = (p.slopes ? p.slopes[hq] : exp2f(-8.0f * float(hq + 1) / float(p.Hq))) * kLog2e;
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int i = walk.t0; i < walk.t1; ++i) {
+        const int j0 = d.key0 + i * kTile;
+        row.lo = lo - j0;
+        row.hi = hi - j0;
+        row.pos = pos - j0;
+        const bool whole = __all_sync(0xffffffffu, t >= rows || (row.lo <= 0 && row.hi >= kTile));
+        ok = sh_wait(s_full, s_pass, wd);
+        if (!ok) break;
+        s_pass ^= 1;
+        tc_fence_after();
+        kv.next(C::kSlots);  // the value tile's slot
+        if (j0 < vlo || j0 + kTile > vhi) {
+          ok = sh_wait(full + kv.slot, kv.pass, wd);
+          if (!ok) break;
+          if (j0 + t < vlo || j0 + t >= vhi) {
+            uint8_t* v = sKV + kv.slot * C::kTileBytes + t * 128;
+#pragma unroll
+            for (int bx = 0; bx < C::kBoxes; ++bx)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                reinterpret_cast<uint4*>(v + bx * C::kBoxBytes)[c] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        kv.next(C::kSlots);
+        if (active) {
+          auto tile = [&](auto mask) {
+            constexpr bool kMask = decltype(mask)::value;
+            // the tile's maximum, then the weights; 32 columns ahead each time
+            uint32_t v0[32], v1[32];
+            tmem_ld32(colS, v0);
+            tmem_ld_wait_regs(v0);
+            tmem_ld32(colS + 32, v1);
+            float mt = sh_max32<SCORE, kMask>(p, row, v0, 0);
+            tmem_ld_wait_regs(v1);
+            tmem_ld32(colS + 64, v0);
+            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v1, 32));
+            tmem_ld_wait_regs(v0);
+            tmem_ld32(colS + 96, v1);
+            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v0, 64));
+            tmem_ld_wait_regs(v1);
+            tmem_ld32(colS, v0);
+            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v1, 96));
+            if constexpr (SCORE & 2) mt = mt == -INFINITY ? mt : soft_cap(mt, p.softcap2, p.softcap_e);
+            // The reference moves when a row's scores pass it by 2^8, or when it has none.
+            const bool move = mt > m + 8.0f;
+            if (__any_sync(0xffffffffu, move)) {
+              const float m_new = move ? mt : m;
+              const float fix = move ? ex2_approx(m - m_new) : 1.0f;  // from -inf: 0
+              if (i > walk.t0) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(colO + c, o);
+                  tmem_ld_wait_regs(o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                  tmem_st32(colO + c, o);
+                }
+              }
+              l *= fix;
+              m = m_new;
+            }
+            const float ref = m == -INFINITY ? 0.0f : m;
+            uint32_t pk[16];
+            tmem_ld_wait_regs(v0);
+            tmem_ld32(colS + 32, v1);
+            l += sh_exp32<SCORE, kMask>(p, row, v0, 0, ref, pk);
+            tmem_ld_wait_regs(v1);
+            tmem_st16(colS, pk);
+            tmem_ld32(colS + 64, v0);
+            l += sh_exp32<SCORE, kMask>(p, row, v1, 32, ref, pk);
+            tmem_ld_wait_regs(v0);
+            tmem_st16(colS + 16, pk);
+            tmem_ld32(colS + 96, v1);
+            l += sh_exp32<SCORE, kMask>(p, row, v0, 64, ref, pk);
+            tmem_ld_wait_regs(v1);
+            tmem_st16(colS + 32, pk);
+            l += sh_exp32<SCORE, kMask>(p, row, v1, 96, ref, pk);
+            tmem_st16(colS + 48, pk);
+          };
+          if (whole) tile(std::false_type{});
+          else tile(std::true_type{});
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+      ok = ok && sh_wait(o_full, o_pass, wd);
+      if (!ok) break;
+      o_pass ^= 1;
+      tc_fence_after();
+      if (active) {
+        // the part's O / l and LSE (log2); rows of a column chunk side by side
+        const long long piece = (long long)walk.at * p.Hkv + walk.h;
+        const int stride = d.shared ? kTile : p.R;
+        const long long slot =
+            blockIdx.x + piece - (d.shared ? 0 : (long long)p.head->n_prefix * p.Hkv);
+        const bool there = t < rows && MATTN_IN_BOUNDS(kSiteShPart, slot, d.shared ? p.p_slots : p.s_slots);
+        float* po = (d.shared ? p.p_o : p.s_o) + slot * stride * D;
+        const bool none = l == 0.0f;  // no key: O = 0, LSE = -inf. NaN passes through
+        const float inv = none ? 0.0f : 1.0f / l;
+        if (there)
+          ((d.shared ? p.p_lse : p.s_lse) + slot * stride)[t] = none ? -INFINITY : m + __log2f(l);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(colO + c, o);
+          tmem_ld_wait_regs(o);
+          if (there) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                                     __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              if (none) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              reinterpret_cast<float4*>(po)[((c + e) / 4) * stride + t] = x;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      more = walk.next(p);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kShMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ------------------------------------------------------------------------- the join
+// A thread joins 4 channels of one query row over its parts, in the order of the keys.
+constexpr int kShJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShProblem p) {
+  const long long id = (long long)blockIdx.x * kShJoinThreads + threadIdx.x;
+  early_start();
+  const int per = p.R * (D / 4);
+  const long long pair = id / per;
+  if (pair >= (long long)p.B * p.Hkv) return;
+  const int rest = (int)(id - pair * per);
+  const int r = rest % p.R, c4 = rest / p.R;
+  const int b = (int)(pair / p.Hkv), h = (int)(pair % p.Hkv);
+  const ShSeq s = p.seqs[b];
+  const ShHead head = *p.head;
+  float M = -INFINITY, L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](int at, int row, int stride, const float* lse, const float* o, long long slots) {
+    const ShDesc& d = p.desc[at];
+    const long long len = d.tiles + kShCost, start = d.start + h * len + kShCost;
+    const long long base = (long long)(at - (stride == kTile ? 0 : head.n_prefix)) * p.Hkv + h;
+    const long long c0 = start / head.share, c1 = (start + d.tiles - 1) / head.share;
+    for (long long c = c0; c <= c1; ++c) {
+      const long long slot = base + c;
+      if (!MATTN_IN_BOUNDS(kSiteShPart, slot, slots)) continue;
+      const float e = lse[slot * stride + row];
+      const float4 x = reinterpret_cast<const float4*>(o + slot * stride * D)[c4 * stride + row];
+      const float m = fmaxf(M, e), ref = m == -INFINITY ? 0.0f : m;
+      const float fix = ex2_approx(M - ref), w = ex2_approx(e - ref);  // -inf -> 0
+      L = L * fix + w;
+      acc = make_float4(acc.x * fix + w * x.x, acc.y * fix + w * x.y, acc.z * fix + w * x.z,
+                        acc.w * fix + w * x.w);
+      M = m;
+    }
+  };
+  for (int c = 0; c < s.chunks; ++c)
+    add(s.pdesc + c * s.step, s.row0 + r, kTile, p.p_lse, p.p_o, p.p_slots);
+  if (s.sdesc >= 0) add(s.sdesc, r, p.R, p.s_lse, p.s_o, p.s_slots);
+  const long long row = ((long long)b * p.Hq + (long long)h * (p.Hq / p.Hkv)) * p.Sq + r;
+  if (!MATTN_IN_BOUNDS(kSiteShOut, row, (long long)p.B * p.Hq * p.Sq)) return;
+  const bool any = !(L == 0.0f);
+  const float inv = any ? 1.0f / L : 0.0f;
+  const uint2 out = any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                     pack_bf16x2(acc.z * inv, acc.w * inv))
+                        : make_uint2(0u, 0u);
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[c4] = out;
+  if (c4 == 0) p.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
+}
+
+// ------------------------------------------------------------------------- host side
+size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+struct ShLayout {
+  int ctas, max_desc, max_prefix;
+  long long p_slots, s_slots;
+  size_t first, desc, seqs, p_lse, p_o, s_lse, s_o, total;
+};
+
+ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
+  ShLayout w;
+  const long long R = (long long)Hq / Hkv * Sq, per_block = std::max(1LL, kTile / R);
+  // two CTAs per SM, or one per tile where there are fewer (a sequence's own keys may begin
+  // inside a tile)
+  const long long tiles = (long long)B * Hkv * (((long long)max_len + kTile - 1) / kTile + 1);
+  w.ctas = (int)std::max(1LL, std::min<long long>(kShPerSm * sm_count(), tiles));
+  // Pieces of shared keys: the chunks of a group hold a CTA's share each, but for one; so
+  // chunks * blocks of all groups are at most ctas / Hkv and the blocks themselves.
+  const long long shared = std::min(G, B / 2);
+  w.max_prefix = shared ? (int)(w.ctas / Hkv + B / per_block + shared + 1) : 0;
+  w.max_desc = w.max_prefix + B;
+  w.p_slots = shared ? w.ctas + (long long)w.max_prefix * Hkv : 0;
+  w.s_slots = w.ctas + (long long)B * Hkv;
+  size_t at = up256(sizeof(ShHead));
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += up256(n);
+    return x;
+  };
+  w.first = take(sizeof(int) * w.ctas);
+  w.desc = take(sizeof(ShDesc) * w.max_desc);
+  w.seqs = take(sizeof(ShSeq) * B);
+  w.p_lse = take(sizeof(float) * w.p_slots * kTile);
+  w.s_lse = take(sizeof(float) * w.s_slots * R);
+  w.p_o = take(sizeof(float) * w.p_slots * kTile * D);
+  w.s_o = take(sizeof(float) * w.s_slots * R * D);
+  w.total = at;
+  return w;
+}
+
+// 4-D view [B][Hkv][R][D] of the queries; box: `seqs` sequences' rows of one key/value head.
+bool make_map_rows(CUtensorMap* map, const void* q, int B, int Hkv, int R, int D, int seqs) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)R, (cuuint64_t)Hkv, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)R * D * 2, (cuuint64_t)Hkv * R * D * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)R, 1, (cuuint32_t)seqs};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct ShMaps {
+  CUtensorMap qs, q1, k, v;
+};
+
+template <int D, int SCORE>
+cudaError_t launch_main(const ShMaps& m, const ShProblem& p, cudaStream_t s) {
+  using C = ShCfg<D>;
+  static DeviceOnce ready;
+  const cudaError_t e = ready.allow_smem(decode_shared_kernel<D, SCORE>, C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_early(decode_shared_kernel<D, SCORE>, (unsigned)p.ctas, kShThreads, C::kSmem, s,
+                      m.qs, m.q1, m.k, m.v, p);
+}
+
+template <int D>
+cudaError_t launch_shared(const void* q, const void* k, const void* v, ShProblem& p,
+                          cudaStream_t s) {
+  ShMaps m;
+  const long long slices = (long long)p.num_pages * p.Hkv;
+  if (!make_map_rows(&m.qs, q, p.B, p.Hkv, p.R, D, p.seqs_per_block) ||
+      !make_map_rows(&m.q1, q, p.B, p.Hkv, p.R, D, 1) ||
+      !make_map_bf16_3d(&m.k, k, slices, 1 << p.shift, D, 1 << p.shift) ||
+      !make_map_bf16_3d(&m.v, v, slices, 1 << p.shift, D, 1 << p.shift))
+    return cudaErrorInvalidValue;
+  const size_t plan_smem = sizeof(int) * (((p.B + 3) & ~3) + ((p.G + 4) & ~3)) + sizeof(ShGroup) * p.G;
+  static DeviceOnce ready;
+  cudaError_t e = ready.allow_smem(shared_plan_kernel, 226 * 1024 - 1024);
+  if (e != cudaSuccess) return e;
+  e = launch_early(shared_plan_kernel, 1u, kShPlanThreads, plan_smem, s, p);
+  if (e != cudaSuccess) return e;
+  switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
+    case 0: e = launch_main<D, 0>(m, p, s); break;
+    case 1: e = launch_main<D, 1>(m, p, s); break;
+    case 2: e = launch_main<D, 2>(m, p, s); break;
+    default: e = launch_main<D, 3>(m, p, s);
+  }
+  if (e != cudaSuccess) return e;
+  const long long threads = (long long)p.B * p.Hkv * p.R * (D / 4);
+  return launch_early(shared_join_kernel<D>,
+                      (unsigned)((threads + kShJoinThreads - 1) / kShJoinThreads), kShJoinThreads,
+                      0, s, p);
+}
+
+}  // namespace
+}  // namespace mattn
+
+MATTN_API size_t attn_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int Sq, int G,
+                                                    int max_len, int D) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || G < 0 || max_len < 0 || (D != 64 && D != 128) ||
+      Hq % Hkv || (long long)Hq / Hkv * Sq > mattn::kShMaxRows)
+    return 0;
+  return mattn::sh_layout(B, Hq, Hkv, Sq, G, max_len, D).total;
+}
+
+MATTN_API attn_status attn_decode_shared(const void* q, const void* k, const void* v, void* o,
+                                         float* lse, int B, int Hq, int Hkv, int Sq, int max_len,
+                                         int D, unsigned variant, const attn_params* p,
+                                         const int* seq_lens, const int* group_starts,
+                                         const int* shared_lens, int G, void* workspace,
+                                         size_t workspace_bytes, struct CUstream_st* stream) {
+  using namespace mattn;
+  if (!p || B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || max_len < 0 || G < 0 || Hq % Hkv)
+    return ATTN_ERR_INVALID_ARG;
+  if (!p->page_table) return ATTN_ERR_INVALID_ARG;
+  attn_status st = paged_args(variant, p, D);
+  if (st != ATTN_OK) return st;
+  if ((long long)(Hq / Hkv) * Sq > kShMaxRows || (long long)B * Hkv > 65535 || B > kShMaxB ||
+      G > kShMaxB || max_len > INT_MAX - 65536 ||
+      (long long)p->num_pages * Hkv + Hkv > INT_MAX)
+    return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Sq == 0) return ATTN_OK;
+  if ((long long)p->pages_per_seq * p->page_size < (long long)max_len) return ATTN_ERR_INVALID_ARG;
+  if (!q || !k || !v || !o || !lse || !seq_lens || !workspace ||
+      (G > 0 && (!group_starts || !shared_lens)))
+    return ATTN_ERR_INVALID_ARG;
+  const void* vecs[] = {q, k, v, o};
+  for (const void* x : vecs)
+    if (reinterpret_cast<uintptr_t>(x) & 15u) return ATTN_ERR_MISALIGNED;
+  const void* words[] = {lse, seq_lens, group_starts, shared_lens, p->page_table, p->alibi_slopes};
+  for (const void* x : words)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return ATTN_ERR_MISALIGNED;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return ATTN_ERR_MISALIGNED;
+  const ShLayout w = sh_layout(B, Hq, Hkv, Sq, G, max_len, D);
+  if (workspace_bytes < w.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+
+  ShProblem f{};
+  f.seq_lens = seq_lens;
+  f.starts = group_starts;
+  f.shared_lens = shared_lens;
+  f.table = p->page_table;
+  f.slopes = p->alibi_slopes;
+  f.o = o;
+  f.lse = lse;
+  f.B = B;
+  f.Hq = Hq;
+  f.Hkv = Hkv;
+  f.Sq = Sq;
+  f.R = Hq / Hkv * Sq;
+  f.G = G;
+  f.max_len = max_len;
+  f.seqs_per_block = kTile / f.R;
+  f.shift = 4;
+  while ((1 << f.shift) != p->page_size) ++f.shift;
+  f.pages_per_seq = p->pages_per_seq;
+  f.num_pages = p->num_pages;
+  f.variant = variant;
+  f.window = p->window;
+  f.scale2 = (p->scale != 0.0f ? p->scale : 1.0f / std::sqrt((float)D)) * kLog2e;
+  f.softcap2 = p->softcap * kLog2e;
+  f.softcap_e = 2.0f / p->softcap;
+  f.ctas = w.ctas;
+  f.max_desc = w.max_desc;
+  f.max_prefix = w.max_prefix;
+  char* ws = static_cast<char*>(workspace);
+  f.head = reinterpret_cast<ShHead*>(ws);
+  f.first = reinterpret_cast<int*>(ws + w.first);
+  f.desc = reinterpret_cast<ShDesc*>(ws + w.desc);
+  f.seqs = reinterpret_cast<ShSeq*>(ws + w.seqs);
+  f.p_lse = reinterpret_cast<float*>(ws + w.p_lse);
+  f.p_o = reinterpret_cast<float*>(ws + w.p_o);
+  f.s_lse = reinterpret_cast<float*>(ws + w.s_lse);
+  f.s_o = reinterpret_cast<float*>(ws + w.s_o);
+  f.p_slots = w.p_slots;
+  f.s_slots = w.s_slots;
+  f.status = p->status ? p->status : library_status();
+  if (!f.status) return ATTN_ERR_CUDA;
+  f.timeout_ns = p->timeout_ns ? p->timeout_ns : 4000000000ull;
+  f.fault_inject = p->fault_inject;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(D == 64 ? launch_shared<64>(q, k, v, f, s) : launch_shared<128>(q, k, v, f, s));
+}
+
+namespace mattn {
+MATTN_DEBUG_RECORD_ACCESSORS(decode_shared)
+}  // namespace mattn

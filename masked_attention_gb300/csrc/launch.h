@@ -84,6 +84,7 @@ MATTN_DECLARE_DEBUG_RECORD(cache_q4)
 MATTN_DECLARE_DEBUG_RECORD(decode_q4)
 MATTN_DECLARE_DEBUG_RECORD(key_weights)
 MATTN_DECLARE_DEBUG_RECORD(evict)
+MATTN_DECLARE_DEBUG_RECORD(decode_shared)
 #undef MATTN_DECLARE_DEBUG_RECORD
 #endif
 

@@ -130,3 +130,36 @@ def evict(weights, lens, starts, keep, recent, k, v, table, page, new_table, wei
     n = min(len(gone), len(freed))
     freed[:n] = gone[:n]
     return out, kept, new_lens, freed, np.array([len(gone), cut], np.int32), k, v
+
+
+def decode_rows(q, rows, lens, *, causal=True, window=0, softcap=0.0, alibi=None, scale=None):
+    """O [B, Hq, Sq, D], LSE [B, Hq, Sq], per row sum_j p_j |v_j| [.., D] and the size of what
+    the scores were made of, which a tolerance needs. rows(b, h): keys and values [n, D] as
+    head h of sequence b sees them."""
+    B, Hq, Sq, D = q.shape
+    O, A = np.zeros(q.shape), np.zeros(q.shape)
+    L, size = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
+    scale = D ** -0.5 if scale is None else scale
+    for b in range(B):
+        n = int(lens[b])
+        if not n:
+            continue
+        for h in range(Hq):
+            K, V = rows(b, h)
+            for r in range(Sq):
+                i = n - Sq + r
+                see = visible(n, i, causal, window)
+                if not see.any():
+                    continue
+                slope = None if alibi is None else alibi[h]
+                s = row_scores(q[b, h, r], K, i, scale, slope, softcap)[see]
+                m = s.max()
+                p = np.exp(s - m)
+                L[b, h, r] = m + np.log(p.sum())
+                p /= p.sum()
+                O[b, h, r], A[b, h, r] = p @ V[see], p @ np.abs(V[see])
+                parts = np.abs(K[see]) @ np.abs(q[b, h, r]) * scale
+                if slope is not None:
+                    parts = parts + slope * np.abs(i - np.arange(n))[see]
+                size[b, h, r] = parts.max() * (5 if softcap else 1)
+    return O, L, A, size
