@@ -340,7 +340,8 @@ template <int K>
 __device__ __forceinline__ void mma_ts_warp(uint32_t d, const uint32_t (&a)[K],
                                             const uint64_t (&b)[K], uint32_t idesc,
                                             uint32_t first) {
-  static_assert(K == 8, "8 K-steps");
+  static_assert(K == 4 || K == 8, "4 or 8 K-steps");
+  if constexpr (K == 8) {
   asm volatile(
       "{\n\t.reg .pred pl, pa, pt;\n\t.reg .b32 ln;\n\t"
       "mov.u32 ln, %laneid;\n\t"
@@ -356,6 +357,19 @@ __device__ __forceinline__ void mma_ts_warp(uint32_t d, const uint32_t (&a)[K],
       "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%15], %16, %1, pt;\n\t"
       "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%17], %18, %1, pt;\n\t"
       "}" ::"r"(d), "r"(idesc), "r"(first), "r"(a[0]), "l"(b[0]), "r"(a[1]), "l"(b[1]), "r"(a[2]), "l"(b[2]), "r"(a[3]), "l"(b[3]), "r"(a[4]), "l"(b[4]), "r"(a[5]), "l"(b[5]), "r"(a[6]), "l"(b[6]), "r"(a[7]), "l"(b[7]));
+  } else {
+    asm volatile(
+      "{\n\t.reg .pred pl, pa, pt;\n\t.reg .b32 ln;\n\t"
+      "mov.u32 ln, %laneid;\n\t"
+      "setp.eq.u32 pl, ln, 0;\n\t"
+      "setp.ne.b32 pa, %2, 0;\n\t"
+      "setp.eq.b32 pt, 0, 0;\n\t"
+      "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %4, %1, pa;\n\t"
+      "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %1, pt;\n\t"
+      "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %1, pt;\n\t"
+      "@pl tcgen05.mma.cta_group::1.kind::f16 [%0], [%9], %10, %1, pt;\n\t"
+      "}" ::"r"(d), "r"(idesc), "r"(first), "r"(a[0]), "l"(b[0]), "r"(a[1]), "l"(b[1]), "r"(a[2]), "l"(b[2]), "r"(a[3]), "l"(b[3]));
+  }
 }
 
 // tcgen05.commit from a converged warp (issued by lane 0, the lane that

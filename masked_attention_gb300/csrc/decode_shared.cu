@@ -10,19 +10,23 @@
 // With 128 rows a tile of 128 keys is 64 KB and 2 x 2 * 128^3 operations, so the tensor cores,
 // the exponentials and HBM all matter, and the product runs on tcgen05 with 128-row tiles.
 //
-// Work. A piece is a run of 128-key tiles of one key/value head for one 128-row block: of a
+// Work. A piece is a run of 64-key tiles of one key/value head for one 128-row block: of a
 // group's shared keys with up to 128 / R of its sequences (R query rows each: the heads of the
 // key/value head times Sq), or of one sequence's own keys with its R rows (the tile's other rows
 // idle: HBM bounds these). All pieces' tiles, one after the other, each with a constant for its
 // start and end, are dealt out evenly to two CTAs per SM (one's softmax runs under the other's
 // products). Shared keys with several row blocks are cut into chunks of one CTA's share first,
 // all blocks of a chunk side by side, so that CTAs that read the same keys do so at the same time
-// and the second reads them from the L2. A small first kernel lays the pieces out from the lengths on
-// the device, CTAs leave fp32 partial results in the workspace, a third kernel joins them.
+// and the second reads them from the L2. A small first kernel lays the pieces out from the
+// lengths on the device, CTAs leave fp32 partial results in the workspace, a third kernel joins
+// them.
 //
-// Within a CTA: warps 0 to 3 softmax, a thread per query row (TMEM lane); warp 4 TMA; warp 5
-// products: S = Q K^T (both from shared memory), P (bf16, over S in tensor memory, rounded to 8
-// bits as in the other bf16 calls; its sum is of the unrounded values), O += P V.
+// Within a CTA: warps 0 to 3 softmax, a thread per query row (TMEM lane); warp 4 finds the pieces,
+// tells the others through shared memory and copies (TMA); warp 5 issues the products, S = Q K^T
+// of the next tile under the softmax of this one (two S buffers), then O += P V (P: bf16, over S
+// in tensor memory, rounded to 8 bits as in the other bf16 calls; its sum is of the unrounded
+// values). Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
+// two, so that the next ones arrive while this one is worked on.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -41,8 +45,10 @@ constexpr int kShProducer = 4, kShMma = 5;  // warps; 0 to 3: softmax
 constexpr int kShPerSm = 2;
 constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memory
 constexpr int kShMaxRows = 16;
-constexpr int kShCost = 1;        // what a piece's start and end count for, in tiles
-constexpr int kShPlanThreads = 1024;
+constexpr int kShKeys = 64;       // keys of a tile
+constexpr int kShCost = 2;        // what a piece's start and end count for, in tiles
+constexpr int kShPlanThreads = 256;
+constexpr int kShPlanWarps = kShPlanThreads / 32;
 constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
 
 struct ShDesc {  // a piece for every key/value head
@@ -64,7 +70,14 @@ struct ShSeq {  // how to find a sequence's parts
 struct ShHead {
   long long total, share;  // positions dealt out, and per CTA
   int n_prefix;            // pieces (per head) of shared keys come first
+  int n_desc;
 };
+
+// Quotient of positions: 64-bit divisions take several hundred cycles, and positions past 32
+// bits need tens of millions of keys.
+__device__ __forceinline__ long long sh_div(long long a, long long b) {
+  return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 
 struct ShProblem {
   const int* seq_lens;
@@ -107,9 +120,12 @@ __device__ __forceinline__ int sh_len(const ShProblem& p, int b) {
 __device__ __forceinline__ int sh_low(const ShProblem& p, int len) {
   return p.variant & ATTN_MASK_WINDOW ? (int)max(0ll, (long long)len - p.Sq - p.window + 1) : 0;
 }
+// A tile begins with a page, or in the middle of one of 128 keys.
 __device__ __forceinline__ int sh_down(const ShProblem& p, int key) {
-  return key >> p.shift << p.shift;
+  const int s = min(p.shift, 6);
+  return key >> s << s;
 }
+__device__ __forceinline__ int sh_tiles(int keys) { return (keys + kShKeys - 1) / kShKeys; }
 
 // Block-wide scan: sum (or maximum) of the threads before, and of all.
 template <bool kMax, typename T>
@@ -125,17 +141,28 @@ __device__ __forceinline__ T plan_scan(T mine, T* warps, T& all) {
   __syncthreads();
   if (lane == 31) warps[warp] = x;
   __syncthreads();
-  T w = warps[lane];
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const T o = __shfl_up_sync(0xffffffffu, w, d);
-    if (lane >= d) w = join(w, o);
-  }
-  all = __shfl_sync(0xffffffffu, w, 31);
-  const T before_warp = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   T before = __shfl_up_sync(0xffffffffu, x, 1);
   if (lane == 0) before = 0;  // neutral: values are not negative
-  return warp ? join(before, before_warp) : before;
+  all = 0;
+#pragma unroll
+  for (int i = 0; i < kShPlanWarps; ++i) {
+    if (i < warp) before = join(before, warps[i]);
+    all = join(all, warps[i]);
+  }
+  return before;
+}
+
+// Sum over the block.
+__device__ __forceinline__ long long plan_sum(long long mine, long long* warps) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  long long all = 0;
+#pragma unroll
+  for (int i = 0; i < kShPlanWarps; ++i) all += warps[i];
+  return all;
 }
 
 __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShProblem p) {
@@ -143,7 +170,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
   int* group_of = plan_smem;                     // [B]: its group, or -1
   int* begin = group_of + ((p.B + 3) & ~3);      // [G + 1]
   ShGroup* groups = reinterpret_cast<ShGroup*>(begin + ((p.G + 4) & ~3));  // [G]
-  __shared__ long long warps[32];
+  __shared__ long long warps[kShPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   early_start();
   for (int b = tid; b < p.B; b += kShPlanThreads) group_of[b] = -1;
@@ -159,7 +186,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
   __syncthreads();
   // shared keys of the groups that have two sequences or more, a warp each
   long long work = 0;
-  for (int g = warp; g < p.G; g += 32) {
+  for (int g = warp; g < p.G; g += kShPlanWarps) {
     const int b0 = begin[g], n = begin[g + 1] - b0;
     ShGroup gr{};
     if (n > 1) {
@@ -177,7 +204,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
         gr.blocks = (n + p.seqs_per_block - 1) / p.seqs_per_block;
         gr.low = min(low, end);
         gr.key0 = sh_down(p, gr.low);
-        gr.tiles = low < end ? (end - gr.key0 + kTile - 1) / kTile : 0;
+        gr.tiles = low < end ? sh_tiles(end - gr.key0) : 0;
         for (int b = b0 + lane; b < b0 + n; b += 32) group_of[b] = g;
       }
     }
@@ -197,116 +224,115 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     const int g = group_of[b];
     w.klo = max(g >= 0 ? groups[g].shared : 0, sh_low(p, w.len));
     w.key0 = sh_down(p, w.klo);
-    w.tiles = w.len > w.klo ? (w.len - w.key0 + kTile - 1) / kTile : 0;
+    w.tiles = w.len > w.klo ? sh_tiles(w.len - w.key0) : 0;
     return w;
   };
-  for (int b = tid; b < p.B; b += kShPlanThreads) work += own_of(b).tiles;
-  plan_scan<false>(work, warps, all);
-  const long long chunk = max(1ll, (all * p.Hkv + p.ctas - 1) / p.ctas);
-  // Pieces and positions: of the shared keys, group by group, then of the sequences' own keys,
-  // counted in a first pass and, with the CTAs' share known, written in a second.
-  __shared__ long long share_smem;
-  long long at = 0, share = 1;
+  // the CTAs' share of the tiles alone, as the length of the chunks; then with what pieces cost
+  int own_pieces = 0;
+  for (int b = tid; b < p.B; b += kShPlanThreads) {
+    const int n = own_of(b).tiles;
+    work += n;
+    own_pieces += n > 0;
+  }
+  const long long tiles = plan_sum(work, warps);
+  const long long chunk = max(1ll, sh_div(tiles * p.Hkv + p.ctas - 1, p.ctas));
+  long long pieces = own_pieces;
+  for (int g = tid; g < p.G; g += kShPlanThreads) {
+    ShGroup& gr = groups[g];
+    if (!gr.tiles) continue;
+    // one block of rows needs no chunks
+    gr.chunks = gr.blocks > 1 ? (int)sh_div(gr.tiles + chunk - 1, chunk) : 1;
+    pieces += (long long)gr.chunks * gr.blocks;
+  }
+  const long long total = (tiles + plan_sum(pieces, warps) * kShCost) * p.Hkv;
+  const long long share = max(1ll, sh_div(total + p.ctas - 1, p.ctas));
+  // positions: of the shared keys, group by group, then of the sequences' own keys
+  long long at = 0;
   int n_prefix = 0;
-  auto begins = [&](long long c) { return c * share; };  // position of a CTA's first tile
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
-      if (tid == 0) {
-        share_smem = max(1ll, (at + p.ctas - 1) / p.ctas);
-        p.head->total = at;
-        p.head->share = share_smem;
-        p.head->n_prefix = n_prefix;
-      }
-      __syncthreads();
-      share = share_smem;
+  for (int g0 = 0; g0 < p.G; g0 += kShPlanThreads) {
+    const int g = g0 + tid;
+    long long n = 0, len = 0, all_n, all_len;
+    if (g < p.G && groups[g].tiles) {
+      n = (long long)groups[g].chunks * groups[g].blocks;
+      len = (long long)p.Hkv * groups[g].blocks * (groups[g].tiles + groups[g].chunks * kShCost);
     }
-    at = 0;
-    n_prefix = 0;
-    for (int g0 = 0; g0 < p.G; g0 += kShPlanThreads) {
-      const int g = g0 + tid;
-      long long n = 0, len = 0, all_n, all_len;
-      if (g < p.G && groups[g].tiles) {
-        ShGroup& gr = groups[g];
-        // one block of rows needs no chunks
-        gr.chunks = gr.blocks > 1 ? (int)((gr.tiles + chunk - 1) / chunk) : 1;
-        n = (long long)gr.chunks * gr.blocks;
-        len = (long long)p.Hkv * gr.blocks * (gr.tiles + gr.chunks * kShCost);
-      }
-      const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
-      const long long a0 = at + plan_scan<false>(len, warps, all_len);
-      if (n) {
-        groups[g].piece = (int)n0;
-        groups[g].start = a0;
-      }
-      n_prefix += (int)all_n;
-      at += all_len;
+    const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
+    const long long a0 = at + plan_scan<false>(len, warps, all_len);
+    if (n) {
+      groups[g].piece = (int)n0;
+      groups[g].start = a0;
     }
-    __syncthreads();
-    for (int g = warp; pass == 1 && g < p.G; g += 32) {  // a lane per piece
-      const ShGroup gr = groups[g];
-      const int n = gr.chunks * gr.blocks;
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane, c = i / max(gr.blocks, 1), k = i - c * gr.blocks;
-        long long start = 0, end = 0;
-        if (i < n) {
-          const int t0 = (int)((long long)gr.tiles * c / gr.chunks);
-          const int t1 = (int)((long long)gr.tiles * (c + 1) / gr.chunks);
-          ShDesc x;
-          x.tiles = t1 - t0;
-          start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
+    n_prefix += (int)all_n;
+    at += all_len;
+  }
+  if (tid == 0) *p.head = ShHead{total, share, n_prefix, n_prefix + p.B};
+  __syncthreads();
+  for (int g = warp; g < p.G; g += kShPlanWarps) {  // a lane per piece
+    const ShGroup gr = groups[g];
+    const int n = gr.tiles ? gr.chunks * gr.blocks : 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane, c = i / gr.blocks, k = i - c * gr.blocks;
+      long long c0 = 0, c1 = 0;  // CTAs that begin in the piece
+      if (i < n) {
+        // chunk c: the first `more` ones are a tile longer
+        const int len = gr.tiles / gr.chunks, more = gr.tiles - len * gr.chunks;
+        const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
+        ShDesc x;
+        x.tiles = t1 - t0;
+        x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
                                                  k * (long long)(x.tiles + kShCost));
-          end = start + (long long)p.Hkv * (x.tiles + kShCost);
-          x.start = start;
-          x.key0 = gr.key0 + t0 * kTile;
-          x.klo = max(x.key0, gr.low);
-          x.khi = min(gr.shared, gr.key0 + t1 * kTile);
-          x.seq = begin[g] + k * p.seqs_per_block;
-          x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
-          x.lead = begin[g];
-          x.shared = 1;
-          if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
-        }
-        for (int j = 0; j < min(32, n - i0); ++j) {  // the CTAs that begin in piece i0 + j
-          const long long s0 = __shfl_sync(0xffffffffu, start, j);
-          const long long s1 = __shfl_sync(0xffffffffu, end, j);
-          for (long long c0 = (s0 + share - 1) / share + lane; begins(c0) < s1; c0 += 32)
-            if (MATTN_IN_BOUNDS(kSiteShPlan, c0, p.ctas)) p.first[c0] = gr.piece + i0 + j;
-        }
+        x.key0 = gr.key0 + t0 * kShKeys;
+        x.klo = max(x.key0, gr.low);
+        x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
+        x.seq = begin[g] + k * p.seqs_per_block;
+        x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
+        x.lead = begin[g];
+        x.shared = 1;
+        if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
+        c0 = sh_div(x.start + share - 1, share);
+        c1 = sh_div(x.start + (long long)p.Hkv * (x.tiles + kShCost) + share - 1, share);
+      }
+      for (int j = 0; j < min(32, n - i0); ++j) {
+        const int from = __shfl_sync(0xffffffffu, (int)c0, j), to = __shfl_sync(0xffffffffu, (int)c1, j);
+        for (int c = from + lane; c < to; c += 32)
+          if (MATTN_IN_BOUNDS(kSiteShPlan, c, p.ctas)) p.first[c] = gr.piece + i0 + j;
       }
     }
-    for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
-      const int b = b0 + tid;
-      Own w{0, 0, 0, 0};
-      if (b < p.B) w = own_of(b);
-      const long long len = w.tiles ? (long long)p.Hkv * (w.tiles + kShCost) : 0;
-      long long all_len;
-      const long long a0 = at + plan_scan<false>(len, warps, all_len);
-      at += all_len;
-      if (pass == 0 || b >= p.B) continue;
-      ShDesc x;
-      x.start = a0;
-      x.tiles = w.tiles;  // 0: a piece that is passed over
-      x.key0 = w.key0;
-      x.klo = w.klo;
-      x.khi = w.len;
-      x.seq = x.lead = b;
-      x.nseq = 1;
-      x.shared = 0;
-      if (MATTN_IN_BOUNDS(kSiteShPlan, n_prefix + b, p.max_desc)) p.desc[n_prefix + b] = x;
-      for (long long c = (a0 + share - 1) / share; len && begins(c) < a0 + len; ++c)
+  }
+  for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
+    const int b = b0 + tid;
+    Own w{0, 0, 0, 0};
+    if (b < p.B) w = own_of(b);
+    const long long len = w.tiles ? (long long)p.Hkv * (w.tiles + kShCost) : 0;
+    long long all_len;
+    const long long a0 = at + plan_scan<false>(len, warps, all_len);
+    at += all_len;
+    if (b >= p.B) continue;
+    ShDesc x;
+    x.start = a0;
+    x.tiles = w.tiles;  // 0: a piece that is passed over
+    x.key0 = w.key0;
+    x.klo = w.klo;
+    x.khi = w.len;
+    x.seq = x.lead = b;
+    x.nseq = 1;
+    x.shared = 0;
+    if (MATTN_IN_BOUNDS(kSiteShPlan, n_prefix + b, p.max_desc)) p.desc[n_prefix + b] = x;
+    if (len) {
+      const int c0 = (int)sh_div(a0 + share - 1, share), c1 = (int)sh_div(a0 + len + share - 1, share);
+      for (int c = c0; c < c1; ++c)
         if (MATTN_IN_BOUNDS(kSiteShPlan, c, p.ctas)) p.first[c] = n_prefix + b;
-      ShSeq q{0, 0, 0, 0, w.tiles ? n_prefix + b : -1};
-      const int g = group_of[b];
-      if (g >= 0 && groups[g].tiles) {
-        const int k = (b - begin[g]) / p.seqs_per_block;
-        q.pdesc = groups[g].piece + k;
-        q.step = groups[g].blocks;
-        q.chunks = groups[g].chunks;
-        q.row0 = (b - begin[g] - k * p.seqs_per_block) * p.R;
-      }
-      p.seqs[b] = q;
     }
-    __syncthreads();
+    ShSeq q{0, 0, 0, 0, w.tiles ? n_prefix + b : -1};
+    const int g = group_of[b];
+    if (g >= 0 && groups[g].tiles) {
+      const int k = (b - begin[g]) / p.seqs_per_block;
+      q.pdesc = groups[g].piece + k;
+      q.step = groups[g].blocks;
+      q.chunks = groups[g].chunks;
+      q.row0 = (b - begin[g] - k * p.seqs_per_block) * p.R;
+    }
+    p.seqs[b] = q;
   }
 }
 
@@ -314,12 +340,24 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
 template <int D>
 struct ShCfg {
   static constexpr int kBoxes = D / 64;
-  static constexpr int kBoxBytes = kTile * 128;
-  static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  static constexpr int kSlots = D == 128 ? 2 : 5;  // K and V tiles in turn
-  static constexpr int kSmem = (1 + kSlots) * kTileBytes + 1024;
-  static constexpr uint32_t kColO = 128;
-  static_assert(kSmem + 512 <= 113 * 1024, "two CTAs per SM");
+  static constexpr int kQBox = kTile * 128;        // 128 query rows x 64 channels
+  static constexpr int kQBytes = kBoxes * kQBox;
+  static constexpr int kBox = kShKeys * 128;       // 64 keys x 64 channels
+  static constexpr int kTileBytes = kBoxes * kBox;
+  static constexpr int kSlots = D == 128 ? 5 : 10;  // K and V tiles in turn
+  static constexpr int kSmem = kQBytes + kSlots * kTileBytes;
+  static constexpr uint32_t kColO = 2 * kShKeys;    // S twice, then O
+  // A sequence's rows alone (at most 16) stand in one half of the Q tile or the other, row 0 or
+  // row 64 of it, so that the next piece's are there early.
+  static constexpr int kHalf = 64 * 128;
+  static_assert(kSmem + 1024 <= 113 * 1024 + 512, "two CTAs per SM");
+};
+
+constexpr int kShMsgs = 4;
+struct ShMsg {  // a run of tiles, as the producer tells it
+  int tiles;    // 0: no more
+  int key0, klo, khi, seq, nseq, shared, h;
+  long long slot;  // of its partial result
 };
 
 __device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
@@ -348,21 +386,23 @@ struct ShRing {
   }
 };
 
-// A CTA's walk over its share of the pieces: a run of tiles [t0, t1) of one after the other.
+// The producer's walk over the CTA's share of the pieces: runs of tiles [t0, t1).
 struct ShWalk {
-  ShDesc d;
-  int at, h;        // piece and its head
+  ShDesc d, ahead;   // this piece and, read early, the one behind it
+  int at, h, n_desc;  // piece and head
   int t0, t1;
   long long lo, hi;  // positions still to go
+  __device__ __forceinline__ void enter(const ShProblem& p) {
+    ahead = p.desc[min(at + 1, n_desc - 1)];
+  }
   // From position lo: the run that begins there (false: none left).
   __device__ __forceinline__ bool find(const ShProblem& p) {
     while (lo < hi) {
       const long long len = d.tiles + kShCost;
       const long long start = d.start + h * len;  // of this head's piece
-      const long long off = lo - start;
       const long long end = min(hi, start + len);
       if (d.tiles > 0 && end - start > kShCost) {
-        t0 = (int)max(0ll, off - kShCost);
+        t0 = (int)max(0ll, lo - start - kShCost);
         t1 = (int)(end - start) - kShCost;
         if (t0 < t1) return true;
       }
@@ -375,8 +415,10 @@ struct ShWalk {
   __device__ __forceinline__ void step(const ShProblem& p) {
     if (++h < p.Hkv) return;
     h = 0;
-    do d = p.desc[++at];
-    while (d.tiles == 0);
+    ++at;
+    d = ahead;
+    while (d.tiles == 0 && at + 1 < n_desc) d = p.desc[++at];
+    enter(p);
   }
   __device__ __forceinline__ bool next(const ShProblem& p) {
     const long long len = d.tiles + kShCost, start = d.start + h * len;
@@ -403,35 +445,61 @@ __device__ __forceinline__ float sh_linear(const ShProblem& p, const ShRow& r, f
   return x;
 }
 
+// The largest of 32 columns' linear scores (log2 units) and the largest magnitude, which a
+// soft-cap asks for.
 template <int SCORE, bool kMask>
-__device__ __forceinline__ float sh_max32(const ShProblem& p, const ShRow& r, const uint32_t* v,
-                                          int c0) {
+__device__ __forceinline__ float sh_max32(const ShProblem& p, const ShRow& r, const uint32_t (&v)[32],
+                                          int c0, float& size) {
   float x[32];
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
     const float s = __uint_as_float(v[c]);
     x[c] = SCORE & 1 || kMask ? sh_linear<SCORE, kMask>(p, r, s, c0 + c) : s;
   }
-  const float m = row_max<32>(x);
-  return SCORE & 1 || kMask ? m : m * p.scale2;
+  float m = row_max<32>(x);
+  if (!(SCORE & 1 || kMask)) m *= p.scale2;
+  if constexpr (SCORE & 2) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const float s = __uint_as_float(v[c]);
+      size = fmaxf(size, fabsf(SCORE & 1 ? sh_linear<SCORE, false>(p, r, s, c0 + c) : s * p.scale2));
+    }
+  }
+  return m;
 }
 
-// P of 32 columns as packed bf16, and their sum.
-template <int SCORE, bool kMask>
-__device__ __forceinline__ float sh_exp32(const ShProblem& p, const ShRow& r, const uint32_t* v,
+// The soft-cap's series alone, for two scores below a quarter of the cap (soft_cap_near).
+__device__ __forceinline__ float2 cap_near2(float2 s, float inv) {
+  constexpr float kX2 = 0.25f * 0.69314718f * 0.69314718f;
+  auto two = [](float x) { return make_float2(x, x); };
+  const float2 y = fmul2(s, two(inv)), y2 = fmul2(y, y);
+  float2 q = ffma2(y2, two(62.0f / 2835.0f * kX2 * kX2 * kX2 * kX2), two(-17.0f / 315.0f * kX2 * kX2 * kX2));
+  q = ffma2(y2, q, two(2.0f / 15.0f * kX2 * kX2));
+  q = ffma2(y2, q, two(-1.0f / 3.0f * kX2));
+  return ffma2(fmul2(s, y2), q, s);
+}
+
+// P of 32 columns as packed bf16, and their sum. kNear: every score is below a quarter of the cap.
+template <int SCORE, bool kMask, bool kNear>
+__device__ __forceinline__ float sh_exp32(const ShProblem& p, const ShRow& r, const uint32_t (&v)[32],
                                           int c0, float m, uint32_t* pk) {
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   const float2 sl = make_float2(p.scale2, p.scale2), mm = make_float2(-m, -m);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    const float s0 = __uint_as_float(v[c]), s1 = __uint_as_float(v[c + 1]);
+    const float2 s = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
     float2 x;
-    if constexpr (SCORE == 0 && !kMask) {
-      x = ffma2(make_float2(s0, s1), sl, mm);
+    if constexpr (SCORE == 0) {
+      x = ffma2(s, sl, mm);
     } else {
-      x.x = sh_linear<SCORE, false>(p, r, s0, c0 + c);
-      x.y = sh_linear<SCORE, false>(p, r, s1, c0 + c + 1);
-      if constexpr (SCORE & 2) {
+      x = fmul2(s, sl);
+      if constexpr (SCORE & 1) {
+        x.x -= r.slope2 * float(r.pos - (c0 + c));
+        x.y -= r.slope2 * float(r.pos - (c0 + c + 1));
+      }
+      if constexpr ((SCORE & 2) && kNear) {
+        x = cap_near2(x, p.softcap_e);
+      } else if constexpr (SCORE & 2) {
         x.x = soft_cap(x.x, p.softcap2, p.softcap_e);
         x.y = soft_cap(x.y, p.softcap2, p.softcap_e);
       }
@@ -456,28 +524,33 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const ShProblem p) {
   using C = ShCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + C::kTileBytes;
-  __shared__ uint64_t bars[8 + 2 * C::kSlots];
+  uint8_t* sKV = smem + C::kQBytes;
+  __shared__ uint64_t bars[11 + 2 * kShMsgs + 2 * C::kSlots];
+  __shared__ ShMsg msgs[kShMsgs];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
-  uint64_t *q_full = bars, *q_empty = bars + 1, *s_full = bars + 2, *p_full = bars + 3,
-           *o_full = bars + 4, *o_free = bars + 5, *drain = bars + 6, *full = bars + 8,
-           *empty = full + C::kSlots;
+  uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6,
+           *pv_done = bars + 8, *o_free = bars + 9, *drain = bars + 10, *msg_full = bars + 11,
+           *msg_empty = msg_full + kShMsgs, *full = msg_empty + kShMsgs, *empty = full + C::kSlots;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &abort_word;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
-    mbar_init(o_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + i, 1);
+      mbar_init(q_empty + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_full + i, 4);
+    }
+    mbar_init(pv_done, 1);
     mbar_init(o_free, 4);
     mbar_init(drain, 1);
+    for (int i = 0; i < kShMsgs; ++i) {
+      mbar_init(msg_full + i, 1);
+      mbar_init(msg_empty + i, 5);  // the products' warp and four of the softmax
+    }
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(full + i, 1);
       mbar_init(empty + i, 1);
@@ -495,55 +568,102 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  early_start();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-
-  ShWalk walk;
-  const long long share = p.head->share, total = p.head->total;
-  walk.lo = min(total, blockIdx.x * share);
-  walk.hi = min(total, walk.lo + share);
-  bool more = walk.lo < walk.hi;
-  if (more) {
-    walk.at = p.first[blockIdx.x];
-    walk.d = p.desc[walk.at];
-    walk.h = (int)((walk.lo - walk.d.start) / (walk.d.tiles + kShCost));
-    more = walk.find(p);
-  }
+  early_start();
+  // The next message, or false (and ok = false where the wait ran out).
+  ShRing mr;
+  auto next_msg = [&](ShMsg& m, bool& ok) {
+    ok = sh_wait(msg_full + mr.slot, mr.pass, wd);
+    if (!ok) return false;
+    m = msgs[mr.slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(msg_empty + mr.slot);
+    mr.next(kShMsgs);
+    return m.tiles > 0;
+  };
 
   if (warp == kShProducer) {
     const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
     ShRing kv;
-    uint32_t q_pass = 0;
-    bool ok = true;
-    const int per_tile = kTile >> p.shift;  // pages of a tile
-    while (more && ok) {
+    uint32_t q_pass[2] = {0, 0}, half = 0;  // parity of the halves' release, half in turn
+    uint32_t q_armed = 0, q_seen = 0;       // halves with a copy, parity of their latest
+    const int per_tile = max(1, kShKeys >> p.shift), page_rows = min(kShKeys, 1 << p.shift);
+    ShWalk walk;
+    const ShHead head = *p.head;
+    walk.lo = min(head.total, blockIdx.x * head.share);
+    walk.hi = min(head.total, walk.lo + head.share);
+    bool ok = true, more = walk.lo < walk.hi;
+    if (more) {
+      walk.n_desc = head.n_desc;
+      walk.at = p.first[blockIdx.x];
+      walk.d = p.desc[walk.at];
+      walk.enter(p);
+      walk.h = (int)sh_div(walk.lo - walk.d.start, walk.d.tiles + kShCost);
+      more = walk.find(p);
+    }
+    while (ok) {
+      ok = sh_wait(msg_empty + mr.slot, mr.pass ^ 1, wd);
+      if (!ok) break;
+      if (lane == 0) {
+        ShMsg m{};
+        if (more) {
+          const ShDesc& d = walk.d;
+          m.tiles = walk.t1 - walk.t0;
+          m.key0 = d.key0 + walk.t0 * kShKeys;
+          m.klo = d.klo;
+          m.khi = d.khi;
+          m.seq = d.seq;
+          m.nseq = d.nseq;
+          m.shared = d.shared;
+          m.h = walk.h;
+          m.slot = blockIdx.x + walk.h +
+                   (long long)(walk.at - (d.shared ? 0 : head.n_prefix)) * p.Hkv;
+        }
+        msgs[mr.slot] = m;
+        mbar_arrive(msg_full + mr.slot);
+      }
+      __syncwarp();
+      mr.next(kShMsgs);
+      if (!more) break;
       // A lane per page of a tile, its entry read one tile ahead. Pages past the last one with
       // keys repeat it; one outside the pool reads as zeros (past the map's end).
-      const int last = (walk.d.khi - 1) >> p.shift, page0 = walk.d.key0 >> p.shift;
+      const int last = (walk.d.khi - 1) >> p.shift;
       const int* row = p.table + (size_t)walk.d.lead * p.pages_per_seq;
       auto page_of = [&](int t) {
         if (lane >= per_tile) return 0;
-        const int lp = min(page0 + t * per_tile + lane, last);
+        const int lp = min(((walk.d.key0 + t * kShKeys) >> p.shift) + lane, last);
         return MATTN_IN_BOUNDS(kSiteShTable, lp, p.pages_per_seq) ? row[lp] : -1;
       };
       int page = page_of(walk.t0);
-      ok = sh_wait(q_empty, q_pass ^ 1, wd);
+      // the rows: both halves for a block of sequences, one for a sequence alone
+      const bool block = walk.d.shared;
+      if (block) half = 0;
+      for (int i = 0; i < 2 && ok; ++i)
+        if (block || i == (int)half) {
+          ok = sh_wait(q_empty + i, (i ? q_pass[1] : q_pass[0]) ^ 1, wd);
+          if (i) q_pass[1] ^= 1;
+          else q_pass[0] ^= 1;
+        }
       if (!ok) break;
-      q_pass ^= 1;
-      if (lane == 0 && issue) {
-        const int rows = walk.d.shared ? p.seqs_per_block * p.R : p.R;
-        mbar_arrive_expect_tx(q_full, rows * D * 2);
+      if (issue) {
+        q_armed |= 1u << half;
+        q_seen ^= 1u << half;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full + half, (block ? p.seqs_per_block * p.R : p.R) * D * 2);
 #pragma unroll
-        for (int bx = 0; bx < C::kBoxes; ++bx)
-          tma_load_4d(sQ + bx * C::kBoxBytes, walk.d.shared ? &tm_qs : &tm_q1, q_full, bx * 64, 0,
-                      walk.h, walk.d.seq);
+          for (int bx = 0; bx < C::kBoxes; ++bx)
+            tma_load_4d(sQ + bx * C::kQBox + half * C::kHalf, block ? &tm_qs : &tm_q1, q_full + half,
+                        bx * 64, 0, walk.h, walk.d.seq);
+        }
       }
       __syncwarp();
+      half = block ? 0 : half ^ 1;
       for (int t = walk.t0; t < walk.t1 && ok; ++t) {
         const int z = (page < 0 || page >= p.num_pages ? p.num_pages : page) * p.Hkv + walk.h;
+        const int y = (walk.d.key0 + t * kShKeys) & ((1 << p.shift) - 1);  // pages of 128: 0 or 64
         if (t + 1 < walk.t1) page = page_of(t + 1);
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
@@ -555,8 +675,8 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           if (issue && lane < per_tile) {
 #pragma unroll
             for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_3d(dst + bx * C::kBoxBytes + (lane << p.shift) * 128, which ? &tm_v : &tm_k,
-                          full + kv.slot, bx * 64, 0, z);
+              tma_load_3d(dst + bx * C::kBox + lane * page_rows * 128, which ? &tm_v : &tm_k,
+                          full + kv.slot, bx * 64, y, z);
           }
           __syncwarp();
           kv.next(C::kSlots);
@@ -568,213 +688,250 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     // at once).
     if (!ok && issue) {
       for (int i = 0; i < C::kSlots; ++i, kv.next(C::kSlots)) wait_drain(full + kv.slot, kv.pass ^ 1);
-      wait_drain(q_full, q_pass ^ 1);
+      for (int i = 0; i < 2; ++i)
+        if (q_armed >> i & 1) wait_drain(q_full + i, (q_seen >> i & 1) ^ 1);
     }
   } else if (warp == kShMma) {
-    constexpr uint32_t kIdescQK = idesc_bf16(128, 128, false);
+    constexpr uint32_t kIdescQK = idesc_bf16(128, kShKeys, false);
     constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
     const uint64_t dK = sdesc_sw128(smem_u32(sKV), 16, 1024);
-    const uint64_t dV = sdesc_sw128(smem_u32(sKV), C::kBoxBytes, 1024);
-    ShRing kv;
-    uint32_t q_pass = 0, p_pass = 0, o_pass = 0;
+    const uint64_t dV = sdesc_sw128(smem_u32(sKV), C::kBox, 1024);
+    ShRing kv;  // the next key tile's slot; its value tile's is the one behind
+    uint32_t q_pass = 0, p_pass = 0, o_pass = 0, half = 0;  // bit per half, per buffer
+    uint32_t buf = 0;  // S buffer of the next key tile
+    uint32_t pv_count = 0;  // products P V issued
     bool ok = true;
-    while (more && ok) {
-      const int n = walk.t1 - walk.t0;
-      ok = sh_wait(q_full, q_pass, wd);
-      q_pass ^= 1;
-      for (int t = 0; t < n && ok; ++t) {
-        // S = Q K^T over the P of the tile before, which its product (issued before) has read
-        ok = sh_wait(full + kv.slot, kv.pass, wd);
-        if (!ok) break;
-        tc_fence_after();
-        {
-          const uint64_t k0 = dK + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
-          uint64_t a[D / 16], b[D / 16];
+    ShMsg m;
+    // A tile's scores go over the P of two tiles before, whose product must be done: nothing
+    // orders products of unlike shapes (N 64 and N 128).
+    auto buffer_free = [&]() { return sh_wait(pv_done, (pv_count & 1) ^ 1, wd); };
+    auto scores = [&]() {  // S = Q K^T of the tile in slot kv (whose copy has landed)
+      tc_fence_after();
+      const uint64_t q0 = dQ + (uint64_t)((half * C::kHalf) >> 4);
+      const uint64_t k0 = dK + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
+      uint64_t a[D / 16], b[D / 16];
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk / 4) * C::kBoxBytes + (kk % 4) * 32) >> 4);
-            a[kk] = dQ + off;
-            b[kk] = k0 + off;
-          }
-          mma_ss_warp<D / 16>(tmem, a, b, kIdescQK, 0u);
-        }
-        mma_commit_warp(s_full);
-        mma_commit_warp(empty + kv.slot);
-        if (t == n - 1) mma_commit_warp(q_empty);
-        __syncwarp();
+      for (int kk = 0; kk < D / 16; ++kk) {
+        a[kk] = q0 + (uint64_t)(((kk / 4) * C::kQBox + (kk % 4) * 32) >> 4);
+        b[kk] = k0 + (uint64_t)(((kk / 4) * C::kBox + (kk % 4) * 32) >> 4);
+      }
+      mma_ss_warp<D / 16>(tmem + kShKeys * buf, a, b, kIdescQK, 0u);
+      mma_commit_warp(s_full + buf);
+      mma_commit_warp(empty + kv.slot);
+      buf ^= 1;
+    };
+    while (ok && next_msg(m, ok)) {
+      if (m.shared) half = 0;
+      ok = sh_wait(q_full + half, q_pass >> half & 1, wd) && sh_wait(full + kv.slot, kv.pass, wd) &&
+           buffer_free();
+      if (!ok) break;
+      q_pass ^= 1u << half;
+      scores();
+      ShRing v = kv;
+      for (int t = 0; t < m.tiles && ok; ++t) {
+        v = kv;
+        v.next(C::kSlots);
+        kv = v;
         kv.next(C::kSlots);
+        const uint32_t pb = buf ^ 1;  // the buffer of this tile
+        // The next tile's scores before this one's product where its keys are there, so that they
+        // are ready when the softmax is; else behind it.
+        const bool last = t == m.tiles - 1;
+        bool early = !last && __all_sync(0xffffffffu, mbar_try_wait(full + kv.slot, kv.pass));
+        if (early) {
+          ok = buffer_free();
+          if (!ok) break;
+          scores();
+        }
+        if (last) {
+          mma_commit_warp(q_empty + half);
+          if (m.shared) mma_commit_warp(q_empty + 1);
+        }
+        __syncwarp();
         // O (+)= P V
-        ok = sh_wait(full + kv.slot, kv.pass, wd);
+        ok = sh_wait(full + v.slot, v.pass, wd);
         if (ok && t == 0) {
           ok = sh_wait(o_free, o_pass ^ 1, wd);
           o_pass ^= 1;
         }
-        ok = ok && sh_wait(p_full, p_pass, wd);
+        ok = ok && sh_wait(p_full + pb, p_pass >> pb & 1, wd);
         if (!ok) break;
-        p_pass ^= 1;
+        p_pass ^= 1u << pb;
         tc_fence_after();
         {
-          const uint64_t v0 = dV + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
-          uint32_t a[8];
-          uint64_t b[8];
+          const uint64_t v0 = dV + (uint64_t)((v.slot * C::kTileBytes) >> 4);
+          uint32_t a[kShKeys / 16];
+          uint64_t b[kShKeys / 16];
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            a[kk] = tmem + kk * 8;
+          for (int kk = 0; kk < kShKeys / 16; ++kk) {
+            a[kk] = tmem + kShKeys * pb + kk * 8;
             b[kk] = v0 + (uint64_t)((kk * 16 * 128) >> 4);
           }
-          mma_ts_warp<8>(tmem + C::kColO, a, b, kIdescPV, t > 0 ? 1u : 0u);
+          mma_ts_warp<kShKeys / 16>(tmem + C::kColO, a, b, kIdescPV, t > 0 ? 1u : 0u);
         }
-        mma_commit_warp(empty + kv.slot);
-        if (t == n - 1) mma_commit_warp(o_full);
+        mma_commit_warp(empty + v.slot);
+        mma_commit_warp(pv_done);
+        ++pv_count;
         __syncwarp();
-        kv.next(C::kSlots);
+        if (!last && !early) {
+          ok = sh_wait(full + kv.slot, kv.pass, wd) && buffer_free();
+          if (!ok) break;
+          scores();
+          __syncwarp();
+        }
       }
-      more = ok && walk.next(p);
+      half = m.shared ? 0 : half ^ 1;
     }
     mma_commit_warp(drain);
     __syncwarp();
     wait_drain(drain, 0);
   } else {
-    const int t = threadIdx.x;  // row of the block, TMEM lane, and key of a tile
+    const int t = threadIdx.x;  // row of the block, TMEM lane
     const uint32_t lanes = uint32_t(warp * 32) << 16;
-    const uint32_t colS = tmem + lanes, colO = tmem + lanes + C::kColO;
+    const uint32_t colO = tmem + lanes + C::kColO;
     const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
+    // the row's sequence of the block, its head of the group and its token
+    const int rq = t / p.R, rr = t - rq * p.R, rg = rr / p.Sq, rs = rr - rg * p.Sq;
     ShRing kv;
-    uint32_t s_pass = 0, o_pass = 0;
+    uint32_t s_pass = 0, buf = 0, pv_count = 0;  // pv_count: tiles before this one
     bool ok = true;
-    int known = -1;  // piece whose rows these are
-    int lo = 0, hi = 0, pos = 0, head = 0;
-    while (more && ok) {
-      const ShDesc& d = walk.d;
-      if (known != walk.at) {  // the same rows for every head
-        known = walk.at;
-        const int q = t / p.R, r = t - q * p.R, g = r / p.Sq;
-        lo = hi = 0;
-        if (q < d.nseq) {
-          const int len = sh_len(p, d.seq + q);
-          pos = len - p.Sq + (r - g * p.Sq);
-          head = g;
-          hi = pos < 0 ? 0 : min(d.khi, causal ? pos + 1 : len);
-          lo = max(d.klo, windowed ? pos - p.window + 1 : 0);
-        }
+    ShMsg msg;
+    int known = -1;  // first sequence of the rows that `len` was read for
+    int len = 0;
+    while (ok && next_msg(msg, ok)) {
+      const int rows = msg.nseq * p.R;
+      const bool mine = t < rows, active = warp * 32 < rows;  // a warp without rows keeps step
+      if (!msg.shared) {
+        len = msg.khi;
+        known = -1;
+      } else if (known != msg.seq) {
+        known = msg.seq;
+        len = mine ? sh_len(p, msg.seq + rq) : 0;
       }
-      const int rows = d.nseq * p.R;
-      const bool active = warp * 32 < rows;  // a warp without rows only keeps step
-      // keys that some row of the piece sees: values of others are zeroed before their product
-      int vlo = d.klo, vhi = d.khi;
-      if (windowed && !d.shared) vlo = max(vlo, sh_low(p, d.khi));
+      const int pos = len - p.Sq + rs;
+      int lo = 0, hi = 0;  // keys that the row sees
+      if (mine && pos >= 0) {
+        hi = min(msg.khi, causal ? pos + 1 : len);
+        lo = max(msg.klo, windowed ? pos - p.window + 1 : 0);
+      }
       ShRow row{};
       if constexpr (SCORE & 1) {
-        const int hq = walk.h * (p.Hq / p.Hkv) + head;
+        const int hq = msg.h * (p.Hq / p.Hkv) + (mine ? rg : 0);
         row.slope2 = (p.slopes ? p.slopes[hq] : exp2f(-8.0f * float(hq + 1) / float(p.Hq))) * kLog2e;
       }
       float m = -INFINITY, l = 0.0f;
-      for (int i = walk.t0; i < walk.t1; ++i) {
-        const int j0 = d.key0 + i * kTile;
+      for (int i = 0; i < msg.tiles; ++i) {
+        const int j0 = msg.key0 + i * kShKeys;
         row.lo = lo - j0;
         row.hi = hi - j0;
         row.pos = pos - j0;
-        const bool whole = __all_sync(0xffffffffu, t >= rows || (row.lo <= 0 && row.hi >= kTile));
-        ok = sh_wait(s_full, s_pass, wd);
-        if (!ok) break;
-        s_pass ^= 1;
-        tc_fence_after();
+        const bool whole = __all_sync(0xffffffffu, !mine || (row.lo <= 0 && row.hi >= kShKeys));
         kv.next(C::kSlots);  // the value tile's slot
-        if (j0 < vlo || j0 + kTile > vhi) {
+        ok = sh_wait(s_full + buf, s_pass >> buf & 1, wd);
+        if (!ok) break;
+        s_pass ^= 1u << buf;
+        tc_fence_after();
+        if (j0 < msg.klo || j0 + kShKeys > msg.khi) {
+          // values of keys that no row sees are zeroed before their product (P is 0 there, and
+          // they may be anything)
           ok = sh_wait(full + kv.slot, kv.pass, wd);
           if (!ok) break;
-          if (j0 + t < vlo || j0 + t >= vhi) {
-            uint8_t* v = sKV + kv.slot * C::kTileBytes + t * 128;
+          const int key = j0 + (t & 63), bx = t >> 6;
+          if ((key < msg.klo || key >= msg.khi) && bx < C::kBoxes) {
+            uint4* v = reinterpret_cast<uint4*>(sKV + kv.slot * C::kTileBytes + bx * C::kBox +
+                                                (t & 63) * 128);
 #pragma unroll
-            for (int bx = 0; bx < C::kBoxes; ++bx)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                reinterpret_cast<uint4*>(v + bx * C::kBoxBytes)[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         kv.next(C::kSlots);
         if (active) {
-          auto tile = [&](auto mask) {
-            constexpr bool kMask = decltype(mask)::value;
-            // the tile's maximum, then the weights; 32 columns ahead each time
-            uint32_t v0[32], v1[32];
-            tmem_ld32(colS, v0);
-            tmem_ld_wait_regs(v0);
-            tmem_ld32(colS + 32, v1);
-            float mt = sh_max32<SCORE, kMask>(p, row, v0, 0);
-            tmem_ld_wait_regs(v1);
-            tmem_ld32(colS + 64, v0);
-            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v1, 32));
-            tmem_ld_wait_regs(v0);
-            tmem_ld32(colS + 96, v1);
-            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v0, 64));
-            tmem_ld_wait_regs(v1);
-            tmem_ld32(colS, v0);
-            mt = fmaxf(mt, sh_max32<SCORE, kMask>(p, row, v1, 96));
-            if constexpr (SCORE & 2) mt = mt == -INFINITY ? mt : soft_cap(mt, p.softcap2, p.softcap_e);
-            // The reference moves when a row's scores pass it by 2^8, or when it has none.
-            const bool move = mt > m + 8.0f;
-            if (__any_sync(0xffffffffu, move)) {
-              const float m_new = move ? mt : m;
-              const float fix = move ? ex2_approx(m - m_new) : 1.0f;  // from -inf: 0
-              if (i > walk.t0) {
+          const uint32_t colS = tmem + lanes + kShKeys * buf;
+          uint32_t v0[32], v1[32];
+          tmem_ld32(colS, v0);
+          tmem_ld32(colS + 32, v1);
+          tmem_ld_wait_regs(v0);
+          tmem_ld_wait_regs(v1);
+          float mt, size = 0.0f;
+          if (whole) {
+            mt = sh_max32<SCORE, false>(p, row, v0, 0, size);
+            mt = fmaxf(mt, sh_max32<SCORE, false>(p, row, v1, 32, size));
+          } else {
+            mt = sh_max32<SCORE, true>(p, row, v0, 0, size);
+            mt = fmaxf(mt, sh_max32<SCORE, true>(p, row, v1, 32, size));
+          }
+          bool near = true;
+          if constexpr (SCORE & 2) {
+            near = __all_sync(0xffffffffu, size * p.softcap_e < kCapNear);
+            if (mt != -INFINITY) mt = soft_cap(mt, p.softcap2, p.softcap_e);
+          }
+          // The reference moves when a row's scores pass it by 2^8, or when it has none.
+          const bool move = mt > m + 8.0f;
+          if (__any_sync(0xffffffffu, move)) {
+            const float m_new = move ? mt : m;
+            const float fix = move ? ex2_approx(m - m_new) : 1.0f;  // from -inf: 0
+            if (i > 0) {  // O as the tile before left it
+              ok = sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(colO + c, o);
-                  tmem_ld_wait_regs(o);
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(colO + c, o);
+                tmem_ld_wait_regs(o);
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
-                  tmem_st32(colO + c, o);
-                }
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fix);
+                tmem_st32(colO + c, o);
               }
-              l *= fix;
-              m = m_new;
             }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            uint32_t pk[16];
-            tmem_ld_wait_regs(v0);
-            tmem_ld32(colS + 32, v1);
-            l += sh_exp32<SCORE, kMask>(p, row, v0, 0, ref, pk);
-            tmem_ld_wait_regs(v1);
-            tmem_st16(colS, pk);
-            tmem_ld32(colS + 64, v0);
-            l += sh_exp32<SCORE, kMask>(p, row, v1, 32, ref, pk);
-            tmem_ld_wait_regs(v0);
-            tmem_st16(colS + 16, pk);
-            tmem_ld32(colS + 96, v1);
-            l += sh_exp32<SCORE, kMask>(p, row, v0, 64, ref, pk);
-            tmem_ld_wait_regs(v1);
-            tmem_st16(colS + 32, pk);
-            l += sh_exp32<SCORE, kMask>(p, row, v1, 96, ref, pk);
-            tmem_st16(colS + 48, pk);
+            l *= fix;
+            m = m_new;
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+          uint32_t pk[32];
+          auto weights = [&](auto mask, auto series) {
+            constexpr bool kMask = decltype(mask)::value, kNear = decltype(series)::value;
+            l += sh_exp32<SCORE, kMask, kNear>(p, row, v0, 0, ref, pk);
+            l += sh_exp32<SCORE, kMask, kNear>(p, row, v1, 32, ref, pk + 16);
           };
-          if (whole) tile(std::false_type{});
-          else tile(std::true_type{});
+          if constexpr (SCORE & 2) {
+            if (whole && near) weights(std::false_type{}, std::true_type{});
+            else if (whole) weights(std::false_type{}, std::false_type{});
+            else weights(std::true_type{}, std::false_type{});
+          } else {
+            if (whole) weights(std::false_type{}, std::false_type{});
+            else weights(std::true_type{}, std::false_type{});
+          }
+          tmem_st32(colS, pk);
           tmem_st_wait();
+        }
+        // Every phase of pv_done is seen in turn: two that end unseen would look like none. (This
+        // tile's scores may have come before the product of the one before.)
+        if (i > 0) {
+          ok = sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
+          if (!ok) break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full);
+        if (lane == 0) mbar_arrive(p_full + buf);
+        buf ^= 1;
+        ++pv_count;
       }
-      ok = ok && sh_wait(o_full, o_pass, wd);
+      ok = ok && sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
       if (!ok) break;
-      o_pass ^= 1;
       tc_fence_after();
       if (active) {
         // the part's O / l and LSE (log2); rows of a column chunk side by side
-        const long long piece = (long long)walk.at * p.Hkv + walk.h;
-        const int stride = d.shared ? kTile : p.R;
-        const long long slot =
-            blockIdx.x + piece - (d.shared ? 0 : (long long)p.head->n_prefix * p.Hkv);
-        const bool there = t < rows && MATTN_IN_BOUNDS(kSiteShPart, slot, d.shared ? p.p_slots : p.s_slots);
-        float* po = (d.shared ? p.p_o : p.s_o) + slot * stride * D;
+        const int stride = msg.shared ? kTile : p.R;
+        const bool there =
+            mine && MATTN_IN_BOUNDS(kSiteShPart, msg.slot, msg.shared ? p.p_slots : p.s_slots);
+        float* po = (msg.shared ? p.p_o : p.s_o) + msg.slot * stride * D;
         const bool none = l == 0.0f;  // no key: O = 0, LSE = -inf. NaN passes through
         const float inv = none ? 0.0f : 1.0f / l;
         if (there)
-          ((d.shared ? p.p_lse : p.s_lse) + slot * stride)[t] = none ? -INFINITY : m + __log2f(l);
+          ((msg.shared ? p.p_lse : p.s_lse) + msg.slot * stride)[t] = none ? -INFINITY : m + __log2f(l);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -794,7 +951,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      more = walk.next(p);
     }
   }
 
@@ -829,7 +985,7 @@ __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShPro
     const ShDesc& d = p.desc[at];
     const long long len = d.tiles + kShCost, start = d.start + h * len + kShCost;
     const long long base = (long long)(at - (stride == kTile ? 0 : head.n_prefix)) * p.Hkv + h;
-    const long long c0 = start / head.share, c1 = (start + d.tiles - 1) / head.share;
+    const long long c0 = sh_div(start, head.share), c1 = sh_div(start + d.tiles - 1, head.share);
     for (long long c = c0; c <= c1; ++c) {
       const long long slot = base + c;
       if (!MATTN_IN_BOUNDS(kSiteShPart, slot, slots)) continue;
@@ -871,7 +1027,7 @@ ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
   const long long R = (long long)Hq / Hkv * Sq, per_block = std::max(1LL, kTile / R);
   // two CTAs per SM, or one per tile where there are fewer (a sequence's own keys may begin
   // inside a tile)
-  const long long tiles = (long long)B * Hkv * (((long long)max_len + kTile - 1) / kTile + 1);
+  const long long tiles = (long long)B * Hkv * (((long long)max_len + kShKeys - 1) / kShKeys + 1);
   w.ctas = (int)std::max(1LL, std::min<long long>(kShPerSm * sm_count(), tiles));
   // Pieces of shared keys: the chunks of a group hold a CTA's share each, but for one; so
   // chunks * blocks of all groups are at most ctas / Hkv and the blocks themselves.
@@ -931,8 +1087,8 @@ cudaError_t launch_shared(const void* q, const void* k, const void* v, ShProblem
   const long long slices = (long long)p.num_pages * p.Hkv;
   if (!make_map_rows(&m.qs, q, p.B, p.Hkv, p.R, D, p.seqs_per_block) ||
       !make_map_rows(&m.q1, q, p.B, p.Hkv, p.R, D, 1) ||
-      !make_map_bf16_3d(&m.k, k, slices, 1 << p.shift, D, 1 << p.shift) ||
-      !make_map_bf16_3d(&m.v, v, slices, 1 << p.shift, D, 1 << p.shift))
+      !make_map_bf16_3d(&m.k, k, slices, 1 << p.shift, D, std::min(kShKeys, 1 << p.shift)) ||
+      !make_map_bf16_3d(&m.v, v, slices, 1 << p.shift, D, std::min(kShKeys, 1 << p.shift)))
     return cudaErrorInvalidValue;
   const size_t plan_smem = sizeof(int) * (((p.B + 3) & ~3) + ((p.G + 4) & ~3)) + sizeof(ShGroup) * p.G;
   static DeviceOnce ready;
