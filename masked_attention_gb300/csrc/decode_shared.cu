@@ -23,9 +23,9 @@
 //
 // Within a CTA: warps 0 to 3 softmax, a thread per query row (TMEM lane); warp 4 finds the pieces,
 // tells the others through shared memory and copies (TMA); warp 5 issues the products, S = Q K^T
-// of the next tile under the softmax of this one (two S buffers), then O += P V (P: bf16, over S
-// in tensor memory, rounded to 8 bits as in the other bf16 calls; its sum is of the unrounded
-// values). Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
+// of the next tile as soon as the softmax has this one's scores in registers, then O += P V (P:
+// bf16 in tensor memory, in two places of its own, rounded to 8 bits as in the other bf16 calls;
+// its sum is of the unrounded values). Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
 // two, so that the next ones arrive while this one is worked on.
 #include <algorithm>
 #include <climits>
@@ -346,7 +346,8 @@ struct ShCfg {
   static constexpr int kTileBytes = kBoxes * kBox;
   static constexpr int kSlots = D == 128 ? 5 : 10;  // K and V tiles in turn
   static constexpr int kSmem = kQBytes + kSlots * kTileBytes;
-  static constexpr uint32_t kColO = 2 * kShKeys;    // S twice, then O
+  // Tensor memory: S (64 columns), P twice (32 each), O.
+  static constexpr uint32_t kColP = kShKeys, kColO = 2 * kShKeys;
   // A sequence's rows alone (at most 16) stand in one half of the Q tile or the other, row 0 or
   // row 64 of it, so that the next piece's are there early.
   static constexpr int kHalf = 64 * 128;
@@ -527,12 +528,13 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + C::kQBytes;
-  __shared__ uint64_t bars[11 + 2 * kShMsgs + 2 * C::kSlots];
+  __shared__ uint64_t bars[10 + 2 * kShMsgs + 2 * C::kSlots];
   __shared__ ShMsg msgs[kShMsgs];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_word;
-  uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *p_full = bars + 6,
-           *pv_done = bars + 8, *o_free = bars + 9, *drain = bars + 10, *msg_full = bars + 11,
+  uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_free = bars + 5,
+           *p_full = bars + 6, *pv_done = bars + 7, *o_free = bars + 8, *drain = bars + 9,
+           *msg_full = bars + 10,
            *msg_empty = msg_full + kShMsgs, *full = msg_empty + kShMsgs, *empty = full + C::kSlots;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &abort_word;
@@ -541,9 +543,10 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
     }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     mbar_init(o_free, 4);
     mbar_init(drain, 1);
@@ -698,15 +701,14 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     const uint64_t dK = sdesc_sw128(smem_u32(sKV), 16, 1024);
     const uint64_t dV = sdesc_sw128(smem_u32(sKV), C::kBox, 1024);
     ShRing kv;  // the next key tile's slot; its value tile's is the one behind
-    uint32_t q_pass = 0, p_pass = 0, o_pass = 0, half = 0;  // bit per half, per buffer
-    uint32_t buf = 0;  // S buffer of the next key tile
-    uint32_t pv_count = 0;  // products P V issued
+    uint32_t q_pass = 0, half = 0;  // q_pass: a bit per half of the rows
+    uint32_t s_pass = 0, p_pass = 0, o_pass = 0, pb = 0;  // pb: place of the next P
     bool ok = true;
     ShMsg m;
-    // A tile's scores go over the P of two tiles before, whose product must be done: nothing
-    // orders products of unlike shapes (N 64 and N 128).
-    auto buffer_free = [&]() { return sh_wait(pv_done, (pv_count & 1) ^ 1, wd); };
-    auto scores = [&]() {  // S = Q K^T of the tile in slot kv (whose copy has landed)
+    // S = Q K^T of the tile in slot kv, whose copy has landed, once the tile before has been read
+    auto scores = [&]() {
+      if (!sh_wait(s_free, s_pass ^ 1, wd)) return false;
+      s_pass ^= 1;
       tc_fence_after();
       const uint64_t q0 = dQ + (uint64_t)((half * C::kHalf) >> 4);
       const uint64_t k0 = dK + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
@@ -716,48 +718,39 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         a[kk] = q0 + (uint64_t)(((kk / 4) * C::kQBox + (kk % 4) * 32) >> 4);
         b[kk] = k0 + (uint64_t)(((kk / 4) * C::kBox + (kk % 4) * 32) >> 4);
       }
-      mma_ss_warp<D / 16>(tmem + kShKeys * buf, a, b, kIdescQK, 0u);
-      mma_commit_warp(s_full + buf);
+      mma_ss_warp<D / 16>(tmem, a, b, kIdescQK, 0u);
+      mma_commit_warp(s_full);
       mma_commit_warp(empty + kv.slot);
-      buf ^= 1;
+      return true;
     };
     while (ok && next_msg(m, ok)) {
       if (m.shared) half = 0;
       ok = sh_wait(q_full + half, q_pass >> half & 1, wd) && sh_wait(full + kv.slot, kv.pass, wd) &&
-           buffer_free();
-      if (!ok) break;
+           scores();
       q_pass ^= 1u << half;
-      scores();
-      ShRing v = kv;
       for (int t = 0; t < m.tiles && ok; ++t) {
-        v = kv;
+        ShRing v = kv;
         v.next(C::kSlots);
         kv = v;
         kv.next(C::kSlots);
-        const uint32_t pb = buf ^ 1;  // the buffer of this tile
         // The next tile's scores before this one's product where its keys are there, so that they
         // are ready when the softmax is; else behind it.
         const bool last = t == m.tiles - 1;
-        bool early = !last && __all_sync(0xffffffffu, mbar_try_wait(full + kv.slot, kv.pass));
-        if (early) {
-          ok = buffer_free();
-          if (!ok) break;
-          scores();
-        }
+        const bool early = !last && __all_sync(0xffffffffu, mbar_try_wait(full + kv.slot, kv.pass));
+        if (early) ok = scores();
         if (last) {
           mma_commit_warp(q_empty + half);
           if (m.shared) mma_commit_warp(q_empty + 1);
         }
-        __syncwarp();
         // O (+)= P V
-        ok = sh_wait(full + v.slot, v.pass, wd);
+        ok = ok && sh_wait(full + v.slot, v.pass, wd);
         if (ok && t == 0) {
           ok = sh_wait(o_free, o_pass ^ 1, wd);
           o_pass ^= 1;
         }
-        ok = ok && sh_wait(p_full + pb, p_pass >> pb & 1, wd);
+        ok = ok && sh_wait(p_full, p_pass, wd);
         if (!ok) break;
-        p_pass ^= 1u << pb;
+        p_pass ^= 1;
         tc_fence_after();
         {
           const uint64_t v0 = dV + (uint64_t)((v.slot * C::kTileBytes) >> 4);
@@ -765,21 +758,15 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           uint64_t b[kShKeys / 16];
 #pragma unroll
           for (int kk = 0; kk < kShKeys / 16; ++kk) {
-            a[kk] = tmem + kShKeys * pb + kk * 8;
+            a[kk] = tmem + C::kColP + kShKeys / 2 * pb + kk * 8;
             b[kk] = v0 + (uint64_t)((kk * 16 * 128) >> 4);
           }
           mma_ts_warp<kShKeys / 16>(tmem + C::kColO, a, b, kIdescPV, t > 0 ? 1u : 0u);
         }
-        mma_commit_warp(empty + v.slot);
         mma_commit_warp(pv_done);
-        ++pv_count;
-        __syncwarp();
-        if (!last && !early) {
-          ok = sh_wait(full + kv.slot, kv.pass, wd) && buffer_free();
-          if (!ok) break;
-          scores();
-          __syncwarp();
-        }
+        mma_commit_warp(empty + v.slot);
+        pb ^= 1;
+        if (!last && !early) ok = sh_wait(full + kv.slot, kv.pass, wd) && scores();
       }
       half = m.shared ? 0 : half ^ 1;
     }
@@ -794,7 +781,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     // the row's sequence of the block, its head of the group and its token
     const int rq = t / p.R, rr = t - rq * p.R, rg = rr / p.Sq, rs = rr - rg * p.Sq;
     ShRing kv;
-    uint32_t s_pass = 0, buf = 0, pv_count = 0;  // pv_count: tiles before this one
+    uint32_t s_pass = 0, pv_count = 0;  // pv_count: tiles before this one
     bool ok = true;
     ShMsg msg;
     int known = -1;  // first sequence of the rows that `len` was read for
@@ -828,10 +815,18 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         row.pos = pos - j0;
         const bool whole = __all_sync(0xffffffffu, !mine || (row.lo <= 0 && row.hi >= kShKeys));
         kv.next(C::kSlots);  // the value tile's slot
-        ok = sh_wait(s_full + buf, s_pass >> buf & 1, wd);
+        ok = sh_wait(s_full, s_pass, wd);
         if (!ok) break;
-        s_pass ^= 1u << buf;
+        s_pass ^= 1;
         tc_fence_after();
+        uint32_t v0[32], v1[32];
+        tmem_ld32(tmem + lanes, v0);
+        tmem_ld32(tmem + lanes + 32, v1);
+        tmem_ld_wait_regs(v0);
+        tmem_ld_wait_regs(v1);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         if (j0 < msg.klo || j0 + kShKeys > msg.khi) {
           // values of keys that no row sees are zeroed before their product (P is 0 there, and
           // they may be anything)
@@ -848,12 +843,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         }
         kv.next(C::kSlots);
         if (active) {
-          const uint32_t colS = tmem + lanes + kShKeys * buf;
-          uint32_t v0[32], v1[32];
-          tmem_ld32(colS, v0);
-          tmem_ld32(colS + 32, v1);
-          tmem_ld_wait_regs(v0);
-          tmem_ld_wait_regs(v1);
           float mt, size = 0.0f;
           if (whole) {
             mt = sh_max32<SCORE, false>(p, row, v0, 0, size);
@@ -904,19 +893,19 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
             if (whole) weights(std::false_type{}, std::false_type{});
             else weights(std::true_type{}, std::false_type{});
           }
-          tmem_st32(colS, pk);
+          // (the place of the tile two before, whose product was waited for below)
+          tmem_st32(tmem + lanes + C::kColP + kShKeys / 2 * (pv_count & 1), pk);
           tmem_st_wait();
         }
-        // Every phase of pv_done is seen in turn: two that end unseen would look like none. (This
-        // tile's scores may have come before the product of the one before.)
+        // Every phase of pv_done is seen in turn: two that end unseen would look like none. (The
+        // scores of a tile may come before the product of the one before.)
         if (i > 0) {
           ok = sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
           if (!ok) break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + buf);
-        buf ^= 1;
+        if (lane == 0) mbar_arrive(p_full);
         ++pv_count;
       }
       ok = ok && sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
