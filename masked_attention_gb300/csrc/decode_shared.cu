@@ -22,10 +22,11 @@
 // them.
 //
 // Within a CTA: warps 0 to 3 softmax, a thread per query row (TMEM lane); warp 4 finds the pieces,
-// tells the others through shared memory and copies (TMA); warp 5 issues the products, S = Q K^T
-// of the next tile as soon as the softmax has this one's scores in registers, then O += P V (P:
-// bf16 in tensor memory, in two places of its own, rounded to 8 bits as in the other bf16 calls;
-// its sum is of the unrounded values). Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
+// tells the others through shared memory and copies (TMA); warp 5 issues S = Q K^T, of the next
+// tile as soon as the softmax has this one's scores in registers; warp 6 O += P V (P: bf16 in
+// tensor memory, in two places of its own, rounded to 8 bits as in the other bf16 calls; its sum
+// is of the unrounded values). (One warp for both products was what a tile waited for: 1900
+// cycles, of which 900 its waits.) Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
 // two, so that the next ones arrive while this one is worked on.
 #include <algorithm>
 #include <climits>
@@ -40,8 +41,9 @@
 namespace mattn {
 namespace {
 
-constexpr int kShThreads = 192;
-constexpr int kShProducer = 4, kShMma = 5;  // warps; 0 to 3: softmax
+constexpr int kShThreads = 256;
+constexpr int kShProducer = 4, kShQK = 5, kShPV = 6;  // warps; 0 to 3: softmax
+constexpr int kShRegsSoftmax = 176, kShRegsOther = 80;  // 128 x 176 + 128 x 80 = 256 x 128
 constexpr int kShPerSm = 2;
 constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memory
 constexpr int kShMaxRows = 16;
@@ -344,7 +346,11 @@ struct ShCfg {
   static constexpr int kQBytes = kBoxes * kQBox;
   static constexpr int kBox = kShKeys * 128;       // 64 keys x 64 channels
   static constexpr int kTileBytes = kBoxes * kBox;
-  static constexpr int kSlots = D == 128 ? 5 : 10;  // K and V tiles in turn
+  // Places of K and of V tiles. Rings of their own: each has one warp that sees every pass of it
+  // (a warp that waited for every other pass of a shared place would take one for the next).
+  // Values stay longer, from before their scores to the end of their product.
+  static constexpr int kKSlots = D == 128 ? 2 : 5, kVSlots = D == 128 ? 3 : 5;
+  static constexpr int kSlots = kKSlots + kVSlots;
   static constexpr int kSmem = kQBytes + kSlots * kTileBytes;
   // Tensor memory: S (64 columns), P twice (32 each), O.
   static constexpr uint32_t kColP = kShKeys, kColO = 2 * kShKeys;
@@ -527,7 +533,8 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
   using C = ShCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
-  uint8_t* sKV = smem + C::kQBytes;
+  uint8_t* sK = smem + C::kQBytes;
+  uint8_t* sV = sK + C::kKSlots * C::kTileBytes;
   __shared__ uint64_t bars[10 + 2 * kShMsgs + 2 * C::kSlots];
   __shared__ ShMsg msgs[kShMsgs];
   __shared__ uint32_t tmem_base;
@@ -535,7 +542,9 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
   uint64_t *q_full = bars, *q_empty = bars + 2, *s_full = bars + 4, *s_free = bars + 5,
            *p_full = bars + 6, *pv_done = bars + 7, *o_free = bars + 8, *drain = bars + 9,
            *msg_full = bars + 10,
-           *msg_empty = msg_full + kShMsgs, *full = msg_empty + kShMsgs, *empty = full + C::kSlots;
+           *msg_empty = msg_full + kShMsgs, *k_full = msg_empty + kShMsgs,
+           *k_empty = k_full + C::kKSlots, *v_full = k_empty + C::kKSlots,
+           *v_empty = v_full + C::kVSlots;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &abort_word;
   const Watchdog wd{abort_flag, p.status, p.timeout_ns};
@@ -549,19 +558,16 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     mbar_init(p_full, 4);
     mbar_init(pv_done, 1);
     mbar_init(o_free, 4);
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     for (int i = 0; i < kShMsgs; ++i) {
       mbar_init(msg_full + i, 1);
-      mbar_init(msg_empty + i, 5);  // the products' warp and four of the softmax
+      mbar_init(msg_empty + i, 6);  // the products' two warps and four of the softmax
     }
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
-    }
+    for (int i = 0; i < 2 * C::kSlots; ++i) mbar_init(k_full + i, 1);
     abort_word = 0;
     fence_barrier_init();
   }
-  if (warp == kShMma) {
+  if (warp == kShQK) {
     tmem_alloc(&tmem_base, 256);
     tmem_relinquish();
   }
@@ -588,9 +594,10 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     return m.tiles > 0;
   };
 
+  if (warp >= kShProducer) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kShRegsOther));
   if (warp == kShProducer) {
     const bool issue = !(p.fault_inject & ATTN_FAULT_NO_LOADS);
-    ShRing kv;
+    ShRing kr, vr;
     uint32_t q_pass[2] = {0, 0}, half = 0;  // parity of the halves' release, half in turn
     uint32_t q_armed = 0, q_seen = 0;       // halves with a copy, parity of their latest
     const int per_tile = max(1, kShKeys >> p.shift), page_rows = min(kShKeys, 1 << p.shift);
@@ -668,83 +675,86 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         const int z = (page < 0 || page >= p.num_pages ? p.num_pages : page) * p.Hkv + walk.h;
         const int y = (walk.d.key0 + t * kShKeys) & ((1 << p.shift) - 1);  // pages of 128: 0 or 64
         if (t + 1 < walk.t1) page = page_of(t + 1);
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          ok = ok && sh_wait(empty + kv.slot, kv.pass ^ 1, wd);
-          if (!ok) break;
-          uint8_t* dst = sKV + kv.slot * C::kTileBytes;
-          if (lane == 0 && issue) mbar_arrive_expect_tx(full + kv.slot, C::kTileBytes);
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* full, uint64_t* empty,
+                        uint32_t pass) {
+          if (!sh_wait(empty, pass ^ 1, wd)) return false;
+          if (lane == 0 && issue) mbar_arrive_expect_tx(full, C::kTileBytes);
           __syncwarp();
           if (issue && lane < per_tile) {
 #pragma unroll
             for (int bx = 0; bx < C::kBoxes; ++bx)
-              tma_load_3d(dst + bx * C::kBox + lane * page_rows * 128, which ? &tm_v : &tm_k,
-                          full + kv.slot, bx * 64, y, z);
+              tma_load_3d(dst + bx * C::kBox + lane * page_rows * 128, map, full, bx * 64, y, z);
           }
           __syncwarp();
-          kv.next(C::kSlots);
-        }
+          return true;
+        };
+        ok = load(sK + kr.slot * C::kTileBytes, &tm_k, k_full + kr.slot, k_empty + kr.slot, kr.pass);
+        if (!ok) break;
+        kr.next(C::kKSlots);
+        ok = load(sV + vr.slot * C::kTileBytes, &tm_v, v_full + vr.slot, v_empty + vr.slot, vr.pass);
+        if (!ok) break;
+        vr.next(C::kVSlots);
       }
       more = ok && walk.next(p);
     }
     // On the way out of a failed wait copies in flight land first (an unused slot's wait ends
     // at once).
     if (!ok && issue) {
-      for (int i = 0; i < C::kSlots; ++i, kv.next(C::kSlots)) wait_drain(full + kv.slot, kv.pass ^ 1);
+      for (int i = 0; i < C::kKSlots; ++i, kr.next(C::kKSlots)) wait_drain(k_full + kr.slot, kr.pass ^ 1);
+      for (int i = 0; i < C::kVSlots; ++i, vr.next(C::kVSlots)) wait_drain(v_full + vr.slot, vr.pass ^ 1);
       for (int i = 0; i < 2; ++i)
         if (q_armed >> i & 1) wait_drain(q_full + i, (q_seen >> i & 1) ^ 1);
     }
-  } else if (warp == kShMma) {
-    constexpr uint32_t kIdescQK = idesc_bf16(128, kShKeys, false);
-    constexpr uint32_t kIdescPV = idesc_bf16(128, D, true);
+  } else if (warp == kShQK) {
+    constexpr uint32_t kIdesc = idesc_bf16(128, kShKeys, false);
     const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
-    const uint64_t dK = sdesc_sw128(smem_u32(sKV), 16, 1024);
-    const uint64_t dV = sdesc_sw128(smem_u32(sKV), C::kBox, 1024);
-    ShRing kv;  // the next key tile's slot; its value tile's is the one behind
-    uint32_t q_pass = 0, half = 0;  // q_pass: a bit per half of the rows
-    uint32_t s_pass = 0, p_pass = 0, o_pass = 0, pb = 0;  // pb: place of the next P
+    const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+    ShRing kr;
+    uint32_t q_pass = 0, half = 0, s_pass = 0;  // q_pass: a bit per half of the rows
     bool ok = true;
     ShMsg m;
-    // S = Q K^T of the tile in slot kv, whose copy has landed, once the tile before has been read
-    auto scores = [&]() {
-      if (!sh_wait(s_free, s_pass ^ 1, wd)) return false;
-      s_pass ^= 1;
-      tc_fence_after();
-      const uint64_t q0 = dQ + (uint64_t)((half * C::kHalf) >> 4);
-      const uint64_t k0 = dK + (uint64_t)((kv.slot * C::kTileBytes) >> 4);
-      uint64_t a[D / 16], b[D / 16];
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        a[kk] = q0 + (uint64_t)(((kk / 4) * C::kQBox + (kk % 4) * 32) >> 4);
-        b[kk] = k0 + (uint64_t)(((kk / 4) * C::kBox + (kk % 4) * 32) >> 4);
-      }
-      mma_ss_warp<D / 16>(tmem, a, b, kIdescQK, 0u);
-      mma_commit_warp(s_full);
-      mma_commit_warp(empty + kv.slot);
-      return true;
-    };
     while (ok && next_msg(m, ok)) {
       if (m.shared) half = 0;
-      ok = sh_wait(q_full + half, q_pass >> half & 1, wd) && sh_wait(full + kv.slot, kv.pass, wd) &&
-           scores();
+      ok = sh_wait(q_full + half, q_pass >> half & 1, wd);
       q_pass ^= 1u << half;
       for (int t = 0; t < m.tiles && ok; ++t) {
-        ShRing v = kv;
-        v.next(C::kSlots);
-        kv = v;
-        kv.next(C::kSlots);
-        // The next tile's scores before this one's product where its keys are there, so that they
-        // are ready when the softmax is; else behind it.
-        const bool last = t == m.tiles - 1;
-        const bool early = !last && __all_sync(0xffffffffu, mbar_try_wait(full + kv.slot, kv.pass));
-        if (early) ok = scores();
-        if (last) {
-          mma_commit_warp(q_empty + half);
-          if (m.shared) mma_commit_warp(q_empty + 1);
+        // once the tile is there and the scores before it have been read
+        ok = sh_wait(k_full + kr.slot, kr.pass, wd) && sh_wait(s_free, s_pass ^ 1, wd);
+        if (!ok) break;
+        s_pass ^= 1;
+        tc_fence_after();
+        const uint64_t q0 = dQ + (uint64_t)((half * C::kHalf) >> 4);
+        const uint64_t k0 = dK + (uint64_t)((kr.slot * C::kTileBytes) >> 4);
+        uint64_t a[D / 16], b[D / 16];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          a[kk] = q0 + (uint64_t)(((kk / 4) * C::kQBox + (kk % 4) * 32) >> 4);
+          b[kk] = k0 + (uint64_t)(((kk / 4) * C::kBox + (kk % 4) * 32) >> 4);
         }
-        // O (+)= P V
-        ok = ok && sh_wait(full + v.slot, v.pass, wd);
-        if (ok && t == 0) {
+        mma_ss_warp<D / 16>(tmem, a, b, kIdesc, 0u);
+        mma_commit_warp(s_full);
+        mma_commit_warp(k_empty + kr.slot);
+        kr.next(C::kKSlots);
+      }
+      if (!ok) break;
+      mma_commit_warp(q_empty + half);
+      if (m.shared) mma_commit_warp(q_empty + 1);
+      half = m.shared ? 0 : half ^ 1;
+    }
+    mma_commit_warp(drain);
+    __syncwarp();
+    wait_drain(drain, 0);
+  } else if (warp == kShPV) {
+    constexpr uint32_t kIdesc = idesc_bf16(128, D, true);
+    const uint64_t dV = sdesc_sw128(smem_u32(sV), C::kBox, 1024);
+    ShRing vr;
+    uint32_t p_pass = 0, o_pass = 0, place = 0;  // place: of the next P
+    bool ok = true;
+    ShMsg m;
+    while (ok && next_msg(m, ok)) {
+      for (int t = 0; t < m.tiles && ok; ++t) {
+        ok = sh_wait(v_full + vr.slot, vr.pass, wd);
+        if (ok && t == 0) {  // O of the piece before has been read
           ok = sh_wait(o_free, o_pass ^ 1, wd);
           o_pass ^= 1;
         }
@@ -752,35 +762,33 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         if (!ok) break;
         p_pass ^= 1;
         tc_fence_after();
-        {
-          const uint64_t v0 = dV + (uint64_t)((v.slot * C::kTileBytes) >> 4);
-          uint32_t a[kShKeys / 16];
-          uint64_t b[kShKeys / 16];
+        const uint64_t v0 = dV + (uint64_t)((vr.slot * C::kTileBytes) >> 4);
+        uint32_t a[kShKeys / 16];
+        uint64_t b[kShKeys / 16];
 #pragma unroll
-          for (int kk = 0; kk < kShKeys / 16; ++kk) {
-            a[kk] = tmem + C::kColP + kShKeys / 2 * pb + kk * 8;
-            b[kk] = v0 + (uint64_t)((kk * 16 * 128) >> 4);
-          }
-          mma_ts_warp<kShKeys / 16>(tmem + C::kColO, a, b, kIdescPV, t > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kShKeys / 16; ++kk) {
+          a[kk] = tmem + C::kColP + kShKeys / 2 * place + kk * 8;
+          b[kk] = v0 + (uint64_t)((kk * 16 * 128) >> 4);
         }
+        mma_ts_warp<kShKeys / 16>(tmem + C::kColO, a, b, kIdesc, t > 0 ? 1u : 0u);
         mma_commit_warp(pv_done);
-        mma_commit_warp(empty + v.slot);
-        pb ^= 1;
-        if (!last && !early) ok = sh_wait(full + kv.slot, kv.pass, wd) && scores();
+        mma_commit_warp(v_empty + vr.slot);
+        place ^= 1;
+        vr.next(C::kVSlots);
       }
-      half = m.shared ? 0 : half ^ 1;
     }
     mma_commit_warp(drain);
     __syncwarp();
     wait_drain(drain, 0);
-  } else {
+  } else if (warp < kShProducer) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kShRegsSoftmax));
     const int t = threadIdx.x;  // row of the block, TMEM lane
     const uint32_t lanes = uint32_t(warp * 32) << 16;
     const uint32_t colO = tmem + lanes + C::kColO;
     const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
     // the row's sequence of the block, its head of the group and its token
     const int rq = t / p.R, rr = t - rq * p.R, rg = rr / p.Sq, rs = rr - rg * p.Sq;
-    ShRing kv;
+    ShRing vr;
     uint32_t s_pass = 0, pv_count = 0;  // pv_count: tiles before this one
     bool ok = true;
     ShMsg msg;
@@ -814,7 +822,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         row.hi = hi - j0;
         row.pos = pos - j0;
         const bool whole = __all_sync(0xffffffffu, !mine || (row.lo <= 0 && row.hi >= kShKeys));
-        kv.next(C::kSlots);  // the value tile's slot
         ok = sh_wait(s_full, s_pass, wd);
         if (!ok) break;
         s_pass ^= 1;
@@ -830,18 +837,18 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         if (j0 < msg.klo || j0 + kShKeys > msg.khi) {
           // values of keys that no row sees are zeroed before their product (P is 0 there, and
           // they may be anything)
-          ok = sh_wait(full + kv.slot, kv.pass, wd);
+          ok = sh_wait(v_full + vr.slot, vr.pass, wd);
           if (!ok) break;
           const int key = j0 + (t & 63), bx = t >> 6;
           if ((key < msg.klo || key >= msg.khi) && bx < C::kBoxes) {
-            uint4* v = reinterpret_cast<uint4*>(sKV + kv.slot * C::kTileBytes + bx * C::kBox +
+            uint4* v = reinterpret_cast<uint4*>(sV + vr.slot * C::kTileBytes + bx * C::kBox +
                                                 (t & 63) * 128);
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-        kv.next(C::kSlots);
+        vr.next(C::kVSlots);
         if (active) {
           float mt, size = 0.0f;
           if (whole) {
@@ -945,7 +952,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kShMma) {
+  if (warp == kShQK) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 256);
@@ -1065,6 +1072,13 @@ cudaError_t launch_main(const ShMaps& m, const ShProblem& p, cudaStream_t s) {
   static DeviceOnce ready;
   const cudaError_t e = ready.allow_smem(decode_shared_kernel<D, SCORE>, C::kSmem);
   if (e != cudaSuccess) return e;
+  // setmaxnreg.inc draws on the registers that the block holds: refuse where they do not cover
+  // the split (the increase would wait for ever)
+  static const int regs = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, decode_shared_kernel<D, SCORE>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (128 * (kShRegsSoftmax + kShRegsOther) > regs * kShThreads) return cudaErrorInvalidConfiguration;
   return launch_early(decode_shared_kernel<D, SCORE>, (unsigned)p.ctas, kShThreads, C::kSmem, s,
                       m.qs, m.q1, m.k, m.v, p);
 }
