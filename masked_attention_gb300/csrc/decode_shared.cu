@@ -436,44 +436,10 @@ struct ShWalk {
   }
 };
 
-// What a softmax thread keeps of its row.
-struct ShRow {
-  int lo, hi;    // keys that it sees, relative to the tile's first
-  float slope2;  // ALiBi slope in log2 units
-  int pos;       // i - (first key of the tile)
-};
-
-// 32 columns from c0 on: the linear part of the score in log2 units, masked ones -inf.
-template <int SCORE, bool kMask>
-__device__ __forceinline__ float sh_linear(const ShProblem& p, const ShRow& r, float s, int c) {
-  float x = s * p.scale2;
-  if constexpr (SCORE & 1) x -= r.slope2 * float(r.pos - c);
-  if constexpr (kMask) x = c >= r.lo && c < r.hi ? x : -INFINITY;
-  return x;
-}
-
-// The largest of 32 columns' linear scores (log2 units) and the largest magnitude, which a
-// soft-cap asks for.
-template <int SCORE, bool kMask>
-__device__ __forceinline__ float sh_max32(const ShProblem& p, const ShRow& r, const uint32_t (&v)[32],
-                                          int c0, float& size) {
-  float x[32];
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const float s = __uint_as_float(v[c]);
-    x[c] = SCORE & 1 || kMask ? sh_linear<SCORE, kMask>(p, r, s, c0 + c) : s;
-  }
-  float m = row_max<32>(x);
-  if (!(SCORE & 1 || kMask)) m *= p.scale2;
-  if constexpr (SCORE & 2) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const float s = __uint_as_float(v[c]);
-      size = fmaxf(size, fabsf(SCORE & 1 ? sh_linear<SCORE, false>(p, r, s, c0 + c) : s * p.scale2));
-    }
-  }
-  return m;
-}
+// The steps of a tile's softmax, on the thread's 64 scores in registers. They are kept apart,
+// each once in the code: a piece's first and last tiles run all of them, and with masked copies
+// of each step their instructions did not stay in the cache (a piece of one tile took 10000
+// cycles).
 
 // The soft-cap's series alone, for two scores below a quarter of the cap (soft_cap_near).
 __device__ __forceinline__ float2 cap_near2(float2 s, float inv) {
@@ -486,37 +452,48 @@ __device__ __forceinline__ float2 cap_near2(float2 s, float inv) {
   return ffma2(fmul2(s, y2), q, s);
 }
 
-// P of 32 columns as packed bf16, and their sum. kNear: every score is below a quarter of the cap.
-template <int SCORE, bool kMask, bool kNear>
-__device__ __forceinline__ float sh_exp32(const ShProblem& p, const ShRow& r, const uint32_t (&v)[32],
-                                          int c0, float m, uint32_t* pk) {
+// Score modifications: x becomes the modified score in log2 units (SCORE 0: stays the product).
+// pos: the row's position less the tile's first key.
+template <int SCORE>
+__device__ __forceinline__ void sh_modify(const ShProblem& p, float slope2, int pos, float (&x)[64]) {
+  if constexpr (SCORE == 0) return;
+  const float2 sl = make_float2(p.scale2, p.scale2);
+  float size = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 64; c += 2) {
+    float2 y = fmul2(make_float2(x[c], x[c + 1]), sl);
+    if constexpr (SCORE & 1) {
+      y.x -= slope2 * float(pos - c);
+      y.y -= slope2 * float(pos - c - 1);
+    }
+    x[c] = y.x;
+    x[c + 1] = y.y;
+    if constexpr (SCORE & 2) size = fmax3(size, fabsf(y.x), fabsf(y.y));
+  }
+  if constexpr (SCORE & 2) {
+    // (a NaN leaves `size` as it is and passes through the series too)
+    if (__all_sync(0xffffffffu, size * p.softcap_e < kCapNear)) {
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        const float2 y = cap_near2(make_float2(x[c], x[c + 1]), p.softcap_e);
+        x[c] = y.x;
+        x[c + 1] = y.y;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 64; ++c) x[c] = soft_cap(x[c], p.softcap2, p.softcap_e);
+    }
+  }
+}
+
+// P of 32 scores as packed bf16, and their sum. scale: what is left to multiply them with.
+__device__ __forceinline__ float sh_exp32(const float* x, float scale, float m, uint32_t* pk) {
   float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-  const float2 sl = make_float2(p.scale2, p.scale2), mm = make_float2(-m, -m);
+  const float2 sl = make_float2(scale, scale), mm = make_float2(-m, -m);
 #pragma unroll
   for (int c = 0; c < 32; c += 2) {
-    const float2 s = make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-    float2 x;
-    if constexpr (SCORE == 0) {
-      x = ffma2(s, sl, mm);
-    } else {
-      x = fmul2(s, sl);
-      if constexpr (SCORE & 1) {
-        x.x -= r.slope2 * float(r.pos - (c0 + c));
-        x.y -= r.slope2 * float(r.pos - (c0 + c + 1));
-      }
-      if constexpr ((SCORE & 2) && kNear) {
-        x = cap_near2(x, p.softcap_e);
-      } else if constexpr (SCORE & 2) {
-        x.x = soft_cap(x.x, p.softcap2, p.softcap_e);
-        x.y = soft_cap(x.y, p.softcap2, p.softcap_e);
-      }
-      x = fadd2(x, mm);
-    }
-    float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-    if constexpr (kMask) {
-      e.x = c0 + c >= r.lo && c0 + c < r.hi ? e.x : 0.0f;
-      e.y = c0 + c + 1 >= r.lo && c0 + c + 1 < r.hi ? e.y : 0.0f;
-    }
+    const float2 y = ffma2(make_float2(x[c], x[c + 1]), sl, mm);
+    const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
     sum[(c / 2) & 1] = fadd2(sum[(c / 2) & 1], e);
     pk[c / 2] = pack_bf16x2(e.x, e.y);
   }
@@ -810,23 +787,23 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         hi = min(msg.khi, causal ? pos + 1 : len);
         lo = max(msg.klo, windowed ? pos - p.window + 1 : 0);
       }
-      ShRow row{};
+      float slope2 = 0.0f;
       if constexpr (SCORE & 1) {
         const int hq = msg.h * (p.Hq / p.Hkv) + (mine ? rg : 0);
-        row.slope2 = (p.slopes ? p.slopes[hq] : exp2f(-8.0f * float(hq + 1) / float(p.Hq))) * kLog2e;
+        slope2 = (p.slopes ? p.slopes[hq] : exp2f(-8.0f * float(hq + 1) / float(p.Hq))) * kLog2e;
       }
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < msg.tiles; ++i) {
         const int j0 = msg.key0 + i * kShKeys;
-        row.lo = lo - j0;
-        row.hi = hi - j0;
-        row.pos = pos - j0;
-        const bool whole = __all_sync(0xffffffffu, !mine || (row.lo <= 0 && row.hi >= kShKeys));
+        const int from = lo - j0, to = hi - j0;  // columns that the row sees
+        const bool whole = __all_sync(0xffffffffu, !mine || (from <= 0 && to >= kShKeys));
         ok = sh_wait(s_full, s_pass, wd);
         if (!ok) break;
         s_pass ^= 1;
         tc_fence_after();
-        uint32_t v0[32], v1[32];
+        float x[64];
+        uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(x);
+        uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(x + 32);
         tmem_ld32(tmem + lanes, v0);
         tmem_ld32(tmem + lanes + 32, v1);
         tmem_ld_wait_regs(v0);
@@ -850,19 +827,13 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         }
         vr.next(C::kVSlots);
         if (active) {
-          float mt, size = 0.0f;
-          if (whole) {
-            mt = sh_max32<SCORE, false>(p, row, v0, 0, size);
-            mt = fmaxf(mt, sh_max32<SCORE, false>(p, row, v1, 32, size));
-          } else {
-            mt = sh_max32<SCORE, true>(p, row, v0, 0, size);
-            mt = fmaxf(mt, sh_max32<SCORE, true>(p, row, v1, 32, size));
+          sh_modify<SCORE>(p, slope2, pos - j0, x);
+          if (!whole) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = c >= from && c < to ? x[c] : -INFINITY;
           }
-          bool near = true;
-          if constexpr (SCORE & 2) {
-            near = __all_sync(0xffffffffu, size * p.softcap_e < kCapNear);
-            if (mt != -INFINITY) mt = soft_cap(mt, p.softcap2, p.softcap_e);
-          }
+          const float scale = SCORE == 0 ? p.scale2 : 1.0f;
+          const float mt = row_max<64>(x) * scale;
           // The reference moves when a row's scores pass it by 2^8, or when it has none.
           const bool move = mt > m + 8.0f;
           if (__any_sync(0xffffffffu, move)) {
@@ -872,7 +843,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
               ok = sh_wait(pv_done, (pv_count & 1) ^ 1, wd);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(colO + c, o);
@@ -887,19 +858,8 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           }
           const float ref = m == -INFINITY ? 0.0f : m;
           uint32_t pk[32];
-          auto weights = [&](auto mask, auto series) {
-            constexpr bool kMask = decltype(mask)::value, kNear = decltype(series)::value;
-            l += sh_exp32<SCORE, kMask, kNear>(p, row, v0, 0, ref, pk);
-            l += sh_exp32<SCORE, kMask, kNear>(p, row, v1, 32, ref, pk + 16);
-          };
-          if constexpr (SCORE & 2) {
-            if (whole && near) weights(std::false_type{}, std::true_type{});
-            else if (whole) weights(std::false_type{}, std::false_type{});
-            else weights(std::true_type{}, std::false_type{});
-          } else {
-            if (whole) weights(std::false_type{}, std::false_type{});
-            else weights(std::true_type{}, std::false_type{});
-          }
+          l += sh_exp32(x, scale, ref, pk);
+          l += sh_exp32(x + 32, scale, ref, pk + 16);
           // (the place of the tile two before, whose product was waited for below)
           tmem_st32(tmem + lanes + C::kColP + kShKeys / 2 * (pv_count & 1), pk);
           tmem_st_wait();
@@ -928,18 +888,21 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         const float inv = none ? 0.0f : 1.0f / l;
         if (there)
           ((msg.shared ? p.p_lse : p.s_lse) + msg.slot * stride)[t] = none ? -INFINITY : m + __log2f(l);
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(colO + c, o);
-          tmem_ld_wait_regs(o);
+        float4* out = reinterpret_cast<float4*>(po) + t;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 64) {
+          uint32_t o[2][32];
+          tmem_ld32(colO + c, o[0]);
+          tmem_ld32(colO + c + 32, o[1]);
+          tmem_ld_wait_regs(o[0]);
+          tmem_ld_wait_regs(o[1]);
           if (there) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              float4 x = make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                     __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-              if (none) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              reinterpret_cast<float4*>(po)[((c + e) / 4) * stride + t] = x;
+            for (int e = 0; e < 64; e += 4, out += stride) {
+              const uint32_t* v = o[e / 32] + e % 32;
+              *out = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                          : make_float4(__uint_as_float(v[0]) * inv, __uint_as_float(v[1]) * inv,
+                                        __uint_as_float(v[2]) * inv, __uint_as_float(v[3]) * inv);
             }
           }
         }
