@@ -95,9 +95,8 @@ struct ShProblem {
   unsigned variant;
   int window;
   float scale2, softcap2, softcap_e;
-  int ctas, max_desc, max_prefix;
+  int ctas, max_desc, max_prefix, max_parts;
   ShHead* head;
-  int* first;     // [ctas]: piece that a CTA begins in
   ShDesc* desc;   // [max_desc]
   ShSeq* seqs;    // [B]
   float *p_lse, *p_o, *s_lse, *s_o;  // partial results: shared [slots][128], own [slots][R]
@@ -272,33 +271,23 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
   for (int g = warp; g < p.G; g += kShPlanWarps) {  // a lane per piece
     const ShGroup gr = groups[g];
     const int n = gr.tiles ? gr.chunks * gr.blocks : 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const int i = i0 + lane, c = i / gr.blocks, k = i - c * gr.blocks;
-      long long c0 = 0, c1 = 0;  // CTAs that begin in the piece
-      if (i < n) {
-        // chunk c: the first `more` ones are a tile longer
-        const int len = gr.tiles / gr.chunks, more = gr.tiles - len * gr.chunks;
-        const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
-        ShDesc x;
-        x.tiles = t1 - t0;
-        x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
-                                                 k * (long long)(x.tiles + kShCost));
-        x.key0 = gr.key0 + t0 * kShKeys;
-        x.klo = max(x.key0, gr.low);
-        x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
-        x.seq = begin[g] + k * p.seqs_per_block;
-        x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
-        x.lead = begin[g];
-        x.shared = 1;
-        if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
-        c0 = sh_div(x.start + share - 1, share);
-        c1 = sh_div(x.start + (long long)p.Hkv * (x.tiles + kShCost) + share - 1, share);
-      }
-      for (int j = 0; j < min(32, n - i0); ++j) {
-        const int from = __shfl_sync(0xffffffffu, (int)c0, j), to = __shfl_sync(0xffffffffu, (int)c1, j);
-        for (int c = from + lane; c < to; c += 32)
-          if (MATTN_IN_BOUNDS(kSiteShPlan, c, p.ctas)) p.first[c] = gr.piece + i0 + j;
-      }
+    for (int i = lane; i < n; i += 32) {
+      const int c = i / gr.blocks, k = i - c * gr.blocks;
+      // chunk c: the first `more` ones are a tile longer
+      const int len = gr.tiles / gr.chunks, more = gr.tiles - len * gr.chunks;
+      const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
+      ShDesc x;
+      x.tiles = t1 - t0;
+      x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
+                                               k * (long long)(x.tiles + kShCost));
+      x.key0 = gr.key0 + t0 * kShKeys;
+      x.klo = max(x.key0, gr.low);
+      x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
+      x.seq = begin[g] + k * p.seqs_per_block;
+      x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
+      x.lead = begin[g];
+      x.shared = 1;
+      if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
     }
   }
   for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
@@ -320,11 +309,6 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     x.nseq = 1;
     x.shared = 0;
     if (MATTN_IN_BOUNDS(kSiteShPlan, n_prefix + b, p.max_desc)) p.desc[n_prefix + b] = x;
-    if (len) {
-      const int c0 = (int)sh_div(a0 + share - 1, share), c1 = (int)sh_div(a0 + len + share - 1, share);
-      for (int c = c0; c < c1; ++c)
-        if (MATTN_IN_BOUNDS(kSiteShPlan, c, p.ctas)) p.first[c] = n_prefix + b;
-    }
     ShSeq q{0, 0, 0, 0, w.tiles ? n_prefix + b : -1};
     const int g = group_of[b];
     if (g >= 0 && groups[g].tiles) {
@@ -585,7 +569,17 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     bool ok = true, more = walk.lo < walk.hi;
     if (more) {
       walk.n_desc = head.n_desc;
-      walk.at = p.first[blockIdx.x];
+      // The last piece that starts at or before lo, 32 probes at a time (pieces without tiles
+      // start where the next one does).
+      int from = 0, to = head.n_desc;
+      while (to - from > 1) {
+        const int step = (to - from + 31) / 32, at = from + lane * step;
+        const bool below = at < to && p.desc[at].start <= walk.lo;
+        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0's always is
+        to = min(to, from + (hit + 1) * step);
+        from += hit * step;
+      }
+      walk.at = from;
       walk.d = p.desc[walk.at];
       walk.enter(p);
       walk.h = (int)sh_div(walk.lo - walk.d.start, walk.d.tiles + kShCost);
@@ -923,53 +917,123 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
 }
 
 // ------------------------------------------------------------------------- the join
-// A thread joins 4 channels of one query row over its parts, in the order of the keys.
-constexpr int kShJoinThreads = 128;
+// A block joins the rows of one sequence and key/value head. A warp lists their parts; then a
+// thread takes 4 channels of a row, and where rows are few the parts are spread over groups of
+// threads, whose results meet in shared memory. Bound by latency: the sequence, its pieces, then
+// the parts, four loads of them at a time. Everything in a fixed order.
+constexpr int kShJoinThreads = 256;
+
+struct ShAcc {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float e, float w, const float4& x) {  // w: weight of part e
+    const float to = fmaxf(m, e), ref = to == -INFINITY ? 0.0f : to;
+    const float fix = ex2_approx(m - ref), k = w * ex2_approx(e - ref);  // -inf -> 0
+    l = l * fix + k;
+    o = make_float4(o.x * fix + k * x.x, o.y * fix + k * x.y, o.z * fix + k * x.z, o.w * fix + k * x.w);
+    m = to;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShProblem p) {
-  const long long id = (long long)blockIdx.x * kShJoinThreads + threadIdx.x;
+  extern __shared__ int parts[];  // slots of the partial results, ~slot for the own keys'
+  __shared__ float4 other_o[kShJoinThreads];
+  __shared__ float other_m[kShJoinThreads], other_l[kShJoinThreads];
+  __shared__ int n_parts;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   early_start();
-  const int per = p.R * (D / 4);
-  const long long pair = id / per;
-  if (pair >= (long long)p.B * p.Hkv) return;
-  const int rest = (int)(id - pair * per);
-  const int r = rest % p.R, c4 = rest / p.R;
-  const int b = (int)(pair / p.Hkv), h = (int)(pair % p.Hkv);
   const ShSeq s = p.seqs[b];
-  const ShHead head = *p.head;
-  float M = -INFINITY, L = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  auto add = [&](int at, int row, int stride, const float* lse, const float* o, long long slots) {
-    const ShDesc& d = p.desc[at];
-    const long long len = d.tiles + kShCost, start = d.start + h * len + kShCost;
-    const long long base = (long long)(at - (stride == kTile ? 0 : head.n_prefix)) * p.Hkv + h;
-    const long long c0 = sh_div(start, head.share), c1 = sh_div(start + d.tiles - 1, head.share);
-    for (long long c = c0; c <= c1; ++c) {
-      const long long slot = base + c;
-      if (!MATTN_IN_BOUNDS(kSiteShPart, slot, slots)) continue;
-      const float e = lse[slot * stride + row];
-      const float4 x = reinterpret_cast<const float4*>(o + slot * stride * D)[c4 * stride + row];
-      const float m = fmaxf(M, e), ref = m == -INFINITY ? 0.0f : m;
-      const float fix = ex2_approx(M - ref), w = ex2_approx(e - ref);  // -inf -> 0
-      L = L * fix + w;
-      acc = make_float4(acc.x * fix + w * x.x, acc.y * fix + w * x.y, acc.z * fix + w * x.z,
-                        acc.w * fix + w * x.w);
-      M = m;
+  if (tid < 32) {
+    const ShHead head = *p.head;
+    const int pieces = s.chunks + (s.sdesc >= 0);
+    int n = 0;
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+      const int i = i0 + lane;
+      int first = 0, count = 0;
+      if (i < pieces) {
+        const bool own = i == s.chunks;
+        const int at = own ? s.sdesc : s.pdesc + i * s.step;
+        const ShDesc& d = p.desc[at];
+        const long long start = d.start + h * (long long)(d.tiles + kShCost) + kShCost;
+        const int c0 = (int)sh_div(start, head.share);
+        count = (int)sh_div(start + d.tiles - 1, head.share) - c0 + 1;
+        first = (at - (own ? head.n_prefix : 0)) * p.Hkv + h + c0;
+        if (own) first = ~first;
+      }
+      int before = count;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
+      }
+      const int total = __shfl_sync(0xffffffffu, before, 31);
+      before += n - count;
+      for (int k = 0; k < count; ++k)
+        if (MATTN_IN_BOUNDS(kSiteShPart, before + k, p.max_parts))
+          parts[before + k] = first < 0 ? first - k : first + k;
+      n += total;
     }
-  };
-  for (int c = 0; c < s.chunks; ++c)
-    add(s.pdesc + c * s.step, s.row0 + r, kTile, p.p_lse, p.p_o, p.p_slots);
-  if (s.sdesc >= 0) add(s.sdesc, r, p.R, p.s_lse, p.s_o, p.s_slots);
-  const long long row = ((long long)b * p.Hq + (long long)h * (p.Hq / p.Hkv)) * p.Sq + r;
-  if (!MATTN_IN_BOUNDS(kSiteShOut, row, (long long)p.B * p.Hq * p.Sq)) return;
-  const bool any = !(L == 0.0f);
-  const float inv = any ? 1.0f / L : 0.0f;
-  const uint2 out = any ? make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                     pack_bf16x2(acc.z * inv, acc.w * inv))
-                        : make_uint2(0u, 0u);
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[c4] = out;
-  if (c4 == 0) p.lse[row] = any ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    if (lane == 0) n_parts = n;
+  }
+  __syncthreads();
+  const int n = n_parts, per = p.R * (D / 4);
+  const bool wide = per >= kShJoinThreads;  // several items per thread; else one, and groups
+  const int groups = wide ? 1 : kShJoinThreads / per, group = wide ? 0 : tid / per;
+  for (int item = wide ? tid : tid - group * per; item < per; item += wide ? kShJoinThreads : per) {
+    const int r = item % p.R, c4 = item / p.R;
+    ShAcc a{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    if (group < groups) {
+      for (int k0 = group; k0 < n; k0 += 4 * groups) {
+        float e[4];
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + i * groups;
+          e[i] = -INFINITY;
+          x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (k < n) {
+            const int part = parts[k];
+            const bool own = part < 0;
+            const long long slot = own ? ~part : part;
+            const int stride = own ? p.R : kTile, row = own ? r : s.row0 + r;
+            if (MATTN_IN_BOUNDS(kSiteShPart, slot, own ? p.s_slots : p.p_slots)) {
+              e[i] = (own ? p.s_lse : p.p_lse)[slot * stride + row];
+              x[i] = reinterpret_cast<const float4*>((own ? p.s_o : p.p_o) +
+                                                     slot * stride * D)[c4 * stride + row];
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a.add(e[i], 1.0f, x[i]);
+      }
+    }
+    if (groups > 1) {
+      other_m[tid] = a.m;
+      other_l[tid] = a.l;
+      other_o[tid] = a.o;
+      __syncthreads();
+      if (group > 0) return;
+      for (int g = 1; g < groups; ++g) {
+        const int at = g * per + item;
+        const float l = other_l[at], inv = l != 0.0f ? 1.0f / l : 0.0f;
+        const float4 x = other_o[at];
+        a.add(other_m[at], l, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+      }
+    } else if (group > 0) {
+      return;  // a thread left over
+    }
+    const long long row = ((long long)b * p.Hq + (long long)h * (p.Hq / p.Hkv)) * p.Sq + r;
+    if (!MATTN_IN_BOUNDS(kSiteShOut, row, (long long)p.B * p.Hq * p.Sq)) continue;
+    const bool any = !(a.l == 0.0f);
+    const float inv = any ? 1.0f / a.l : 0.0f;
+    const uint2 out = any ? make_uint2(pack_bf16x2(a.o.x * inv, a.o.y * inv),
+                                       pack_bf16x2(a.o.z * inv, a.o.w * inv))
+                          : make_uint2(0u, 0u);
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * D)[c4] = out;
+    if (c4 == 0) p.lse[row] = any ? (a.m + __log2f(a.l)) * kLn2 : -INFINITY;
+  }
 }
 
 // ------------------------------------------------------------------------- host side
@@ -978,7 +1042,7 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 struct ShLayout {
   int ctas, max_desc, max_prefix;
   long long p_slots, s_slots;
-  size_t first, desc, seqs, p_lse, p_o, s_lse, s_o, total;
+  size_t desc, seqs, p_lse, p_o, s_lse, s_o, total;
 };
 
 ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
@@ -1001,7 +1065,6 @@ ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
     at += up256(n);
     return x;
   };
-  w.first = take(sizeof(int) * w.ctas);
   w.desc = take(sizeof(ShDesc) * w.max_desc);
   w.seqs = take(sizeof(ShSeq) * B);
   w.p_lse = take(sizeof(float) * w.p_slots * kTile);
@@ -1069,10 +1132,8 @@ cudaError_t launch_shared(const void* q, const void* k, const void* v, ShProblem
     default: e = launch_main<D, 3>(m, p, s);
   }
   if (e != cudaSuccess) return e;
-  const long long threads = (long long)p.B * p.Hkv * p.R * (D / 4);
-  return launch_early(shared_join_kernel<D>,
-                      (unsigned)((threads + kShJoinThreads - 1) / kShJoinThreads), kShJoinThreads,
-                      0, s, p);
+  return launch_early(shared_join_kernel<D>, (unsigned)(p.B * p.Hkv), kShJoinThreads,
+                      sizeof(int) * p.max_parts, s, p);
 }
 
 }  // namespace
@@ -1145,9 +1206,10 @@ MATTN_API attn_status attn_decode_shared(const void* q, const void* k, const voi
   f.ctas = w.ctas;
   f.max_desc = w.max_desc;
   f.max_prefix = w.max_prefix;
+  // a part per CTA and piece that meet, and a sequence's pieces lie one behind the other
+  f.max_parts = w.ctas + w.max_prefix + 1;
   char* ws = static_cast<char*>(workspace);
   f.head = reinterpret_cast<ShHead*>(ws);
-  f.first = reinterpret_cast<int*>(ws + w.first);
   f.desc = reinterpret_cast<ShDesc*>(ws + w.desc);
   f.seqs = reinterpret_cast<ShSeq*>(ws + w.seqs);
   f.p_lse = reinterpret_cast<float*>(ws + w.p_lse);
