@@ -48,13 +48,15 @@ constexpr int kShPerSm = 2;
 constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memory
 constexpr int kShMaxRows = 16;
 constexpr int kShKeys = 64;       // keys of a tile
-constexpr int kShCost = 2;        // what a piece's start and end count for, in tiles
+// What counts in the dealing out: a tile of a sequence's own keys, of shared ones (whose rows keep
+// all warps busy), and a piece's start and end.
+constexpr int kShOwn = 8, kShShared = 8, kShCost = 16;
 constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
 constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
 
 struct ShDesc {  // a piece for every key/value head
-  long long start;  // of the first head's piece in the dealing out; each takes tiles + kShCost
+  long long start;  // of the first head's piece in the dealing out, of length sh_length() each
   int tiles;
   int key0;      // first key of the first tile, a multiple of the page size
   int klo, khi;  // keys of the piece
@@ -74,6 +76,13 @@ struct ShHead {
   int n_prefix;            // pieces (per head) of shared keys come first
   int n_desc;
 };
+
+// A piece's tile t begins at kShCost + t * w behind the piece's start, w by its kind, and is the
+// CTA's that has that position.
+__host__ __device__ __forceinline__ int sh_weight(int shared) { return shared ? kShShared : kShOwn; }
+__device__ __forceinline__ long long sh_length(int shared, int tiles) {
+  return kShCost + (long long)tiles * sh_weight(shared);
+}
 
 // Quotient of positions: 64-bit divisions take several hundred cycles, and positions past 32
 // bits need tens of millions of keys.
@@ -229,6 +238,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     return w;
   };
   // the CTAs' share of the tiles alone, as the length of the chunks; then with what pieces cost
+  const long long shared_work = work;
   int own_pieces = 0;
   for (int b = tid; b < p.B; b += kShPlanThreads) {
     const int n = own_of(b).tiles;
@@ -237,16 +247,18 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
   }
   const long long tiles = plan_sum(work, warps);
   const long long chunk = max(1ll, sh_div(tiles * p.Hkv + p.ctas - 1, p.ctas));
-  long long pieces = own_pieces;
+  long long length = (work - shared_work) * kShOwn + shared_work * kShShared +
+                     (long long)own_pieces * kShCost;
   for (int g = tid; g < p.G; g += kShPlanThreads) {
     ShGroup& gr = groups[g];
     if (!gr.tiles) continue;
     // one block of rows needs no chunks
     gr.chunks = gr.blocks > 1 ? (int)sh_div(gr.tiles + chunk - 1, chunk) : 1;
-    pieces += (long long)gr.chunks * gr.blocks;
+    length += (long long)gr.chunks * gr.blocks * kShCost;
   }
-  const long long total = (tiles + plan_sum(pieces, warps) * kShCost) * p.Hkv;
-  const long long share = max(1ll, sh_div(total + p.ctas - 1, p.ctas));
+  const long long total = plan_sum(length, warps) * p.Hkv;
+  // no less than a tile, so that every CTA within a piece has one of it
+  const long long share = max((long long)max(kShOwn, kShShared), sh_div(total + p.ctas - 1, p.ctas));
   // positions: of the shared keys, group by group, then of the sequences' own keys
   long long at = 0;
   int n_prefix = 0;
@@ -255,7 +267,8 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     long long n = 0, len = 0, all_n, all_len;
     if (g < p.G && groups[g].tiles) {
       n = (long long)groups[g].chunks * groups[g].blocks;
-      len = (long long)p.Hkv * groups[g].blocks * (groups[g].tiles + groups[g].chunks * kShCost);
+      len = (long long)p.Hkv * groups[g].blocks *
+            ((long long)groups[g].tiles * kShShared + groups[g].chunks * kShCost);
     }
     const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
     const long long a0 = at + plan_scan<false>(len, warps, all_len);
@@ -278,8 +291,8 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
       const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
       ShDesc x;
       x.tiles = t1 - t0;
-      x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 + (long long)c * kShCost) +
-                                               k * (long long)(x.tiles + kShCost));
+      x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 * kShShared + c * kShCost) +
+                                               k * sh_length(1, x.tiles));
       x.key0 = gr.key0 + t0 * kShKeys;
       x.klo = max(x.key0, gr.low);
       x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
@@ -294,7 +307,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     const int b = b0 + tid;
     Own w{0, 0, 0, 0};
     if (b < p.B) w = own_of(b);
-    const long long len = w.tiles ? (long long)p.Hkv * (w.tiles + kShCost) : 0;
+    const long long len = w.tiles ? p.Hkv * sh_length(0, w.tiles) : 0;
     long long all_len;
     const long long a0 = at + plan_scan<false>(len, warps, all_len);
     at += all_len;
@@ -389,14 +402,13 @@ struct ShWalk {
   // From position lo: the run that begins there (false: none left).
   __device__ __forceinline__ bool find(const ShProblem& p) {
     while (lo < hi) {
-      const long long len = d.tiles + kShCost;
+      const long long len = sh_length(d.shared, d.tiles);
       const long long start = d.start + h * len;  // of this head's piece
       const long long end = min(hi, start + len);
-      if (d.tiles > 0 && end - start > kShCost) {
-        t0 = (int)max(0ll, lo - start - kShCost);
-        t1 = (int)(end - start) - kShCost;
-        if (t0 < t1) return true;
-      }
+      const int w = sh_weight(d.shared);
+      t0 = (int)sh_div(max(0ll, lo - start - kShCost) + w - 1, w);
+      t1 = min(d.tiles, (int)sh_div(max(0ll, end - start - kShCost) + w - 1, w));
+      if (t0 < t1) return true;
       lo = end;
       if (lo < start + len || lo >= hi) return false;  // the share ends inside the piece
       step(p);
@@ -412,8 +424,8 @@ struct ShWalk {
     enter(p);
   }
   __device__ __forceinline__ bool next(const ShProblem& p) {
-    const long long len = d.tiles + kShCost, start = d.start + h * len;
-    lo = start + kShCost + t1;
+    const long long len = sh_length(d.shared, d.tiles);
+    lo = d.start + (h + 1) * len;
     if (lo >= hi) return false;
     step(p);
     return find(p);
@@ -582,7 +594,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
       walk.at = from;
       walk.d = p.desc[walk.at];
       walk.enter(p);
-      walk.h = (int)sh_div(walk.lo - walk.d.start, walk.d.tiles + kShCost);
+      walk.h = (int)sh_div(walk.lo - walk.d.start, sh_length(walk.d.shared, walk.d.tiles));
       more = walk.find(p);
     }
     while (ok) {
@@ -956,9 +968,10 @@ __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShPro
         const bool own = i == s.chunks;
         const int at = own ? s.sdesc : s.pdesc + i * s.step;
         const ShDesc& d = p.desc[at];
-        const long long start = d.start + h * (long long)(d.tiles + kShCost) + kShCost;
+        const long long start = d.start + h * sh_length(d.shared, d.tiles) + kShCost;
         const int c0 = (int)sh_div(start, head.share);
-        count = (int)sh_div(start + d.tiles - 1, head.share) - c0 + 1;
+        const long long last = start + (long long)(d.tiles - 1) * sh_weight(d.shared);
+        count = (int)sh_div(last, head.share) - c0 + 1;
         first = (at - (own ? head.n_prefix : 0)) * p.Hkv + h + c0;
         if (own) first = ~first;
       }
