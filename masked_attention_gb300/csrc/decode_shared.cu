@@ -55,25 +55,25 @@ constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
 constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
 
-struct ShDesc {  // a piece for every key/value head
-  long long start;  // of the first head's piece in the dealing out, of length sh_length() each
+struct ShDesc {  // pieces of the same keys: one per key/value head and, of shared keys, row block
+  long long start;  // of the first one in the dealing out, of length sh_length() each
   int tiles;
   int key0;      // first key of the first tile, a multiple of the page size
   int klo, khi;  // keys of the piece
-  int seq, nseq;  // sequences of its rows
-  int lead;       // sequence whose table row is read
-  int shared;     // 1: shared keys
+  int seq, nseq;  // sequences of its rows, in blocks; the first one's table row is read
+  int blocks;     // row blocks of shared keys (a head's pieces side by side); 0: own keys
+  int base;       // number of its first piece among those of its kind
 };
 
 struct ShSeq {  // how to find a sequence's parts
-  int pdesc, step, chunks;  // pieces of its group's shared keys: pdesc + c * step
-  int row0;                 // its first row in their block
-  int sdesc;                // piece of its own keys, or -1
+  int pdesc, chunks;  // pieces of its group's shared keys: from pdesc on
+  int block, row0;    // its block there, its first row in it
+  int sdesc;          // pieces of its own keys, or -1
 };
 
 struct ShHead {
   long long total, share;  // positions dealt out, and per CTA
-  int n_prefix;            // pieces (per head) of shared keys come first
+  int n_prefix;            // descriptions of shared keys come first
   int n_desc;
 };
 
@@ -119,7 +119,7 @@ struct ShProblem {
 struct ShGroup {
   int blocks, tiles;        // row blocks, tiles of its shared keys
   int key0, low, shared;    // first key of the first tile, first one that is seen, their end
-  int chunks, piece;        // runs of tiles, its first piece
+  int chunks, desc, base;   // runs of tiles, first description, first piece's number
   long long start;          // and that one's position
 };
 
@@ -237,70 +237,75 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     w.tiles = w.len > w.klo ? sh_tiles(w.len - w.key0) : 0;
     return w;
   };
-  // the CTAs' share of the tiles alone, as the length of the chunks; then with what pieces cost
-  const long long shared_work = work;
-  int own_pieces = 0;
+  // Keys of several row blocks are cut into chunks, each a CTA's share: what all tiles and the
+  // pieces of whole groups take, then with that many chunks' starts and ends once more.
+  long long length = work * kShShared;
   for (int b = tid; b < p.B; b += kShPlanThreads) {
     const int n = own_of(b).tiles;
     work += n;
-    own_pieces += n > 0;
+    length += n ? sh_length(0, n) : 0;
   }
-  const long long tiles = plan_sum(work, warps);
-  const long long chunk = max(1ll, sh_div(tiles * p.Hkv + p.ctas - 1, p.ctas));
-  long long length = (work - shared_work) * kShOwn + shared_work * kShShared +
-                     (long long)own_pieces * kShCost;
-  for (int g = tid; g < p.G; g += kShPlanThreads) {
-    ShGroup& gr = groups[g];
-    if (!gr.tiles) continue;
-    // one block of rows needs no chunks
-    gr.chunks = gr.blocks > 1 ? (int)sh_div(gr.tiles + chunk - 1, chunk) : 1;
-    length += (long long)gr.chunks * gr.blocks * kShCost;
+  const long long least = sh_div(plan_sum(work, warps) * p.Hkv + p.ctas - 1, p.ctas);  // tiles
+  const long long plain = plan_sum(length, warps);
+  auto share_of = [&](long long n) { return sh_div(n * p.Hkv + p.ctas - 1, p.ctas); };
+  long long chunk = 1, pieces = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const long long cut = pass ? plan_sum(pieces, warps) * kShCost : 0;
+    chunk = max(max(1ll, (least + 1) / 2), sh_div(max(0ll, share_of(plain + cut) - kShCost), kShShared));
+    pieces = 0;
+    for (int g = tid; g < p.G; g += kShPlanThreads) {
+      ShGroup& gr = groups[g];
+      if (!gr.tiles) continue;
+      gr.chunks = gr.blocks > 1 ? (int)sh_div(gr.tiles + chunk - 1, chunk) : 1;
+      pieces += (long long)gr.chunks * gr.blocks;
+    }
   }
-  const long long total = plan_sum(length, warps) * p.Hkv;
+  const long long total = (plain + plan_sum(pieces, warps) * kShCost) * p.Hkv;
   // no less than a tile, so that every CTA within a piece has one of it
   const long long share = max((long long)max(kShOwn, kShShared), sh_div(total + p.ctas - 1, p.ctas));
   // positions: of the shared keys, group by group, then of the sequences' own keys
-  long long at = 0;
+  long long at = 0, base = 0;
   int n_prefix = 0;
   for (int g0 = 0; g0 < p.G; g0 += kShPlanThreads) {
     const int g = g0 + tid;
-    long long n = 0, len = 0, all_n, all_len;
+    long long n = 0, count = 0, len = 0, all_n, all_count, all_len;
     if (g < p.G && groups[g].tiles) {
-      n = (long long)groups[g].chunks * groups[g].blocks;
+      n = groups[g].chunks;
+      count = n * groups[g].blocks * p.Hkv;
       len = (long long)p.Hkv * groups[g].blocks *
             ((long long)groups[g].tiles * kShShared + groups[g].chunks * kShCost);
     }
     const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
+    const long long b0 = base + plan_scan<false>(count, warps, all_count);
     const long long a0 = at + plan_scan<false>(len, warps, all_len);
     if (n) {
-      groups[g].piece = (int)n0;
+      groups[g].desc = (int)n0;
+      groups[g].base = (int)b0;
       groups[g].start = a0;
     }
     n_prefix += (int)all_n;
+    base += all_count;
     at += all_len;
   }
   if (tid == 0) *p.head = ShHead{total, share, n_prefix, n_prefix + p.B};
   __syncthreads();
-  for (int g = warp; g < p.G; g += kShPlanWarps) {  // a lane per piece
+  for (int g = warp; g < p.G; g += kShPlanWarps) {  // a lane per chunk
     const ShGroup gr = groups[g];
-    const int n = gr.tiles ? gr.chunks * gr.blocks : 0;
-    for (int i = lane; i < n; i += 32) {
-      const int c = i / gr.blocks, k = i - c * gr.blocks;
-      // chunk c: the first `more` ones are a tile longer
+    for (int c = lane; gr.tiles && c < gr.chunks; c += 32) {
+      // the first `more` ones are a tile longer
       const int len = gr.tiles / gr.chunks, more = gr.tiles - len * gr.chunks;
       const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
       ShDesc x;
       x.tiles = t1 - t0;
-      x.start = gr.start + (long long)p.Hkv * (gr.blocks * ((long long)t0 * kShShared + c * kShCost) +
-                                               k * sh_length(1, x.tiles));
+      x.start = gr.start + (long long)p.Hkv * gr.blocks * ((long long)t0 * kShShared + c * kShCost);
       x.key0 = gr.key0 + t0 * kShKeys;
       x.klo = max(x.key0, gr.low);
       x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
-      x.seq = begin[g] + k * p.seqs_per_block;
-      x.nseq = min(p.seqs_per_block, begin[g + 1] - x.seq);
-      x.lead = begin[g];
-      x.shared = 1;
-      if (MATTN_IN_BOUNDS(kSiteShPlan, gr.piece + i, p.max_prefix)) p.desc[gr.piece + i] = x;
+      x.seq = begin[g];
+      x.nseq = begin[g + 1] - begin[g];
+      x.blocks = gr.blocks;
+      x.base = gr.base + c * gr.blocks * p.Hkv;
+      if (MATTN_IN_BOUNDS(kSiteShPlan, gr.desc + c, p.max_prefix)) p.desc[gr.desc + c] = x;
     }
   }
   for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
@@ -318,18 +323,18 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     x.key0 = w.key0;
     x.klo = w.klo;
     x.khi = w.len;
-    x.seq = x.lead = b;
+    x.seq = b;
     x.nseq = 1;
-    x.shared = 0;
+    x.blocks = 0;
+    x.base = b * p.Hkv;
     if (MATTN_IN_BOUNDS(kSiteShPlan, n_prefix + b, p.max_desc)) p.desc[n_prefix + b] = x;
     ShSeq q{0, 0, 0, 0, w.tiles ? n_prefix + b : -1};
     const int g = group_of[b];
     if (g >= 0 && groups[g].tiles) {
-      const int k = (b - begin[g]) / p.seqs_per_block;
-      q.pdesc = groups[g].piece + k;
-      q.step = groups[g].blocks;
+      q.pdesc = groups[g].desc;
       q.chunks = groups[g].chunks;
-      q.row0 = (b - begin[g] - k * p.seqs_per_block) * p.R;
+      q.block = (b - begin[g]) / p.seqs_per_block;
+      q.row0 = (b - begin[g] - q.block * p.seqs_per_block) * p.R;
     }
     p.seqs[b] = q;
   }
@@ -393,7 +398,8 @@ struct ShRing {
 // The producer's walk over the CTA's share of the pieces: runs of tiles [t0, t1).
 struct ShWalk {
   ShDesc d, ahead;   // this piece and, read early, the one behind it
-  int at, h, n_desc;  // piece and head
+  int at, n_desc;     // the piece's description
+  int h, block;       // its head and row block
   int t0, t1;
   long long lo, hi;  // positions still to go
   __device__ __forceinline__ void enter(const ShProblem& p) {
@@ -402,10 +408,10 @@ struct ShWalk {
   // From position lo: the run that begins there (false: none left).
   __device__ __forceinline__ bool find(const ShProblem& p) {
     while (lo < hi) {
-      const long long len = sh_length(d.shared, d.tiles);
-      const long long start = d.start + h * len;  // of this head's piece
+      const long long len = sh_length(d.blocks, d.tiles);
+      const long long start = d.start + piece() * len;
       const long long end = min(hi, start + len);
-      const int w = sh_weight(d.shared);
+      const int w = sh_weight(d.blocks);
       t0 = (int)sh_div(max(0ll, lo - start - kShCost) + w - 1, w);
       t1 = min(d.tiles, (int)sh_div(max(0ll, end - start - kShCost) + w - 1, w));
       if (t0 < t1) return true;
@@ -415,7 +421,10 @@ struct ShWalk {
     }
     return false;
   }
+  __device__ __forceinline__ int piece() const { return h * max(1, d.blocks) + block; }
   __device__ __forceinline__ void step(const ShProblem& p) {
+    if (++block < d.blocks) return;
+    block = 0;
     if (++h < p.Hkv) return;
     h = 0;
     ++at;
@@ -424,8 +433,8 @@ struct ShWalk {
     enter(p);
   }
   __device__ __forceinline__ bool next(const ShProblem& p) {
-    const long long len = sh_length(d.shared, d.tiles);
-    lo = d.start + (h + 1) * len;
+    const long long len = sh_length(d.blocks, d.tiles);
+    lo = d.start + (piece() + 1) * len;
     if (lo >= hi) return false;
     step(p);
     return find(p);
@@ -594,7 +603,10 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
       walk.at = from;
       walk.d = p.desc[walk.at];
       walk.enter(p);
-      walk.h = (int)sh_div(walk.lo - walk.d.start, sh_length(walk.d.shared, walk.d.tiles));
+      const int n = max(1, walk.d.blocks);
+      walk.block = (int)sh_div(walk.lo - walk.d.start, sh_length(walk.d.blocks, walk.d.tiles));
+      walk.h = walk.block / n;
+      walk.block -= walk.h * n;
       more = walk.find(p);
     }
     while (ok) {
@@ -608,12 +620,11 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           m.key0 = d.key0 + walk.t0 * kShKeys;
           m.klo = d.klo;
           m.khi = d.khi;
-          m.seq = d.seq;
-          m.nseq = d.nseq;
-          m.shared = d.shared;
+          m.seq = d.seq + walk.block * p.seqs_per_block;
+          m.nseq = min(d.nseq - walk.block * p.seqs_per_block, p.seqs_per_block);
+          m.shared = d.blocks;
           m.h = walk.h;
-          m.slot = blockIdx.x + walk.h +
-                   (long long)(walk.at - (d.shared ? 0 : head.n_prefix)) * p.Hkv;
+          m.slot = (long long)blockIdx.x + d.base + walk.piece();
         }
         msgs[mr.slot] = m;
         mbar_arrive(msg_full + mr.slot);
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
       // A lane per page of a tile, its entry read one tile ahead. Pages past the last one with
       // keys repeat it; one outside the pool reads as zeros (past the map's end).
       const int last = (walk.d.khi - 1) >> p.shift;
-      const int* row = p.table + (size_t)walk.d.lead * p.pages_per_seq;
+      const int* row = p.table + (size_t)walk.d.seq * p.pages_per_seq;
       auto page_of = [&](int t) {
         if (lane >= per_tile) return 0;
         const int lp = min(((walk.d.key0 + t * kShKeys) >> p.shift) + lane, last);
@@ -632,7 +643,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
       };
       int page = page_of(walk.t0);
       // the rows: both halves for a block of sequences, one for a sequence alone
-      const bool block = walk.d.shared;
+      const bool block = walk.d.blocks;
       if (block) half = 0;
       for (int i = 0; i < 2 && ok; ++i)
         if (block || i == (int)half) {
@@ -649,7 +660,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
 #pragma unroll
           for (int bx = 0; bx < C::kBoxes; ++bx)
             tma_load_4d(sQ + bx * C::kQBox + half * C::kHalf, block ? &tm_qs : &tm_q1, q_full + half,
-                        bx * 64, 0, walk.h, walk.d.seq);
+                        bx * 64, 0, walk.h, walk.d.seq + walk.block * p.seqs_per_block);
         }
       }
       __syncwarp();
@@ -966,13 +977,13 @@ __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShPro
       int first = 0, count = 0;
       if (i < pieces) {
         const bool own = i == s.chunks;
-        const int at = own ? s.sdesc : s.pdesc + i * s.step;
-        const ShDesc& d = p.desc[at];
-        const long long start = d.start + h * sh_length(d.shared, d.tiles) + kShCost;
+        const ShDesc d = p.desc[own ? s.sdesc : s.pdesc + i];
+        const int piece = own ? h : h * d.blocks + s.block;
+        const long long start = d.start + piece * sh_length(d.blocks, d.tiles) + kShCost;
         const int c0 = (int)sh_div(start, head.share);
-        const long long last = start + (long long)(d.tiles - 1) * sh_weight(d.shared);
+        const long long last = start + (long long)(d.tiles - 1) * sh_weight(d.blocks);
         count = (int)sh_div(last, head.share) - c0 + 1;
-        first = (at - (own ? head.n_prefix : 0)) * p.Hkv + h + c0;
+        first = d.base + piece + c0;
         if (own) first = ~first;
       }
       int before = count;
@@ -1065,10 +1076,11 @@ ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
   // inside a tile)
   const long long tiles = (long long)B * Hkv * (((long long)max_len + kShKeys - 1) / kShKeys + 1);
   w.ctas = (int)std::max(1LL, std::min<long long>(kShPerSm * sm_count(), tiles));
-  // Pieces of shared keys: the chunks of a group hold a CTA's share each, but for one; so
-  // chunks * blocks of all groups are at most ctas / Hkv and the blocks themselves.
+  // Chunks of shared keys: each holds half of a CTA's share of the tiles or more, but for one of
+  // each group; so chunks * blocks of all groups are at most 2 ctas / Hkv and the blocks
+  // themselves, the chunks no more than that.
   const long long shared = std::min(G, B / 2);
-  w.max_prefix = shared ? (int)(w.ctas / Hkv + B / per_block + shared + 1) : 0;
+  w.max_prefix = shared ? (int)(2 * w.ctas / Hkv + B / per_block + shared + 1) : 0;
   w.max_desc = w.max_prefix + B;
   w.p_slots = shared ? w.ctas + (long long)w.max_prefix * Hkv : 0;
   w.s_slots = w.ctas + (long long)B * Hkv;
