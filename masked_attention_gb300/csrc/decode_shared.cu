@@ -49,8 +49,9 @@ constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memo
 constexpr int kShMaxRows = 16;
 constexpr int kShKeys = 64;       // keys of a tile
 // What counts in the dealing out: a tile of a sequence's own keys, of shared ones (whose rows keep
-// all warps busy), and a piece's start and end.
-constexpr int kShOwn = 8, kShShared = 8, kShCost = 16;
+// all warps busy), and a piece's start and end. (64 sequences behind 32768 keys, 1 key each, with
+// kShCost 12, 16, 24, 32: 70, 68, 61, 61 us; kShShared 7 to 9 makes no difference, 13 costs 15 %.)
+constexpr int kShOwn = 8, kShShared = 8, kShCost = 24;
 constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
 constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
