@@ -15,7 +15,7 @@
 // key/value head times Sq), or of one sequence's own keys with its R rows (the tile's other rows
 // idle: HBM bounds these). All pieces' tiles, one after the other, each with a constant for its
 // start and end, are dealt out evenly to two CTAs per SM (one's softmax runs under the other's
-// products), shared and own keys apart, so that every CTA has its part of both. Shared keys with several row blocks are cut into chunks of one CTA's share first,
+// products). Shared keys with several row blocks are cut into chunks of one CTA's share first,
 // all blocks of a chunk side by side, so that CTAs that read the same keys do so at the same time
 // and the second reads them from the L2. A small first kernel lays the pieces out from the
 // lengths on the device, CTAs leave fp32 partial results in the workspace, a third kernel joins
@@ -45,16 +45,19 @@ constexpr int kShThreads = 256;
 constexpr int kShProducer = 4, kShQK = 5, kShPV = 6;  // warps; 0 to 3: softmax
 constexpr int kShRegsSoftmax = 176, kShRegsOther = 80;  // 128 x 176 + 128 x 80 = 256 x 128
 constexpr int kShPerSm = 2;
-constexpr int kShMaxB = 4096;  // the plan holds 56 bytes of each in shared memory
+constexpr int kShMaxB = 4096;  // the plan holds 48 bytes of each in shared memory
 constexpr int kShMaxRows = 16;
 constexpr int kShKeys = 64;       // keys of a tile
-constexpr int kShCost = 3;        // what a piece's start and end count for, in tiles
+// What counts in the dealing out: a tile of a sequence's own keys, of shared ones (whose rows keep
+// all warps busy), and a piece's start and end. (64 sequences behind 32768 keys, 1 key each, with
+// kShCost 12, 16, 24, 32: 70, 68, 61, 61 us; kShShared 7 to 9 makes no difference, 13 costs 15 %.)
+constexpr int kShOwn = 8, kShShared = 8, kShCost = 24;
 constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
 constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
 
 struct ShDesc {  // pieces of the same keys: one per key/value head and, of shared keys, row block
-  long long start;  // of the first one in the dealing out; each takes kShCost + tiles
+  long long start;  // of the first one in the dealing out, of length sh_length() each
   int tiles;
   int key0;      // first key of the first tile, a multiple of the page size
   int klo, khi;  // keys of the piece
@@ -69,12 +72,18 @@ struct ShSeq {  // how to find a sequence's parts
   int sdesc;          // pieces of its own keys, or -1
 };
 
-// The dealing out of the shared keys' pieces and of the own keys': positions, CTA's share of them,
-// descriptions [from, to). Shared keys first; rank r of `ctas` has positions [r share, (r + 1) share).
-struct ShDeal {
-  long long total, share;
-  int from, to;
+struct ShHead {
+  long long total, share;  // positions dealt out, and per CTA
+  int n_prefix;            // descriptions of shared keys come first
+  int n_desc;
 };
+
+// A piece's tile t begins at kShCost + t * w behind the piece's start, w by its kind, and is the
+// CTA's that has that position.
+__host__ __device__ __forceinline__ int sh_weight(int shared) { return shared ? kShShared : kShOwn; }
+__device__ __forceinline__ long long sh_length(int shared, int tiles) {
+  return kShCost + (long long)tiles * sh_weight(shared);
+}
 
 // Quotient of positions: 64-bit divisions take several hundred cycles, and positions past 32
 // bits need tens of millions of keys.
@@ -97,7 +106,7 @@ struct ShProblem {
   int window;
   float scale2, softcap2, softcap_e;
   int ctas, max_desc, max_prefix, max_parts;
-  ShDeal* deal;   // [2]
+  ShHead* head;
   ShDesc* desc;   // [max_desc]
   ShSeq* seqs;    // [B]
   float *p_lse, *p_o, *s_lse, *s_o;  // partial results: shared [slots][128], own [slots][R]
@@ -117,11 +126,6 @@ struct ShGroup {
 
 __device__ __forceinline__ int sh_len(const ShProblem& p, int b) {
   return max(0, min(p.seq_lens[b], p.max_len));
-}
-// Lets the stream's next kernel be set up while this one runs (it waits for its end). Here that
-// takes nothing from running blocks: the plan is one, and the pieces' CTAs are all resident.
-__device__ __forceinline__ void next_kernel_in() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 // First key that some row of a sequence sees.
 __device__ __forceinline__ int sh_low(const ShProblem& p, int len) {
@@ -175,18 +179,12 @@ __device__ __forceinline__ long long plan_sum(long long mine, long long* warps) 
 __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShProblem p) {
   extern __shared__ __align__(16) int plan_smem[];
   int* group_of = plan_smem;                     // [B]: its group, or -1
-  int* lens = group_of + ((p.B + 3) & ~3);       // [B]
-  int* begin = lens + ((p.B + 3) & ~3);          // [G + 1]
+  int* begin = group_of + ((p.B + 3) & ~3);      // [G + 1]
   ShGroup* groups = reinterpret_cast<ShGroup*>(begin + ((p.G + 4) & ~3));  // [G]
   __shared__ long long warps[kShPlanWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   early_start();
-  next_kernel_in();
-  for (int b = tid; b < p.B; b += kShPlanThreads) {
-    group_of[b] = -1;
-    lens[b] = sh_len(p, b);
-  }
-  for (int g = tid; g < p.G; g += kShPlanThreads) groups[g].shared = p.shared_lens[g];
+  for (int b = tid; b < p.B; b += kShPlanThreads) group_of[b] = -1;
   // the groups' first sequences, ascending whatever they hold
   long long carry = 0, all;
   for (int g0 = 0; p.G > 0 && g0 <= p.G; g0 += kShPlanThreads) {
@@ -205,13 +203,13 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     if (n > 1) {
       int longest = 0, low = INT_MAX;
       for (int b = b0 + lane; b < b0 + n; b += 32) {
-        const int len = lens[b];
+        const int len = sh_len(p, b);
         longest = max(longest, len);
         if (len > 0) low = min(low, sh_low(p, len));
       }
       longest = __reduce_max_sync(0xffffffffu, longest);
       low = __reduce_min_sync(0xffffffffu, low);
-      const int end = min(groups[g].shared, longest);
+      const int end = min(p.shared_lens[g], longest);
       if (end >= kShMinShared) {
         gr.shared = end;
         gr.blocks = (n + p.seqs_per_block - 1) / p.seqs_per_block;
@@ -221,7 +219,6 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
         for (int b = b0 + lane; b < b0 + n; b += 32) group_of[b] = g;
       }
     }
-    __syncwarp();
     if (lane == 0) {
       groups[g] = gr;
       work += (long long)gr.tiles * gr.blocks;
@@ -234,21 +231,28 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
   };
   auto own_of = [&](int b) {
     Own w;
-    w.len = lens[b];
+    w.len = sh_len(p, b);
     const int g = group_of[b];
     w.klo = max(g >= 0 ? groups[g].shared : 0, sh_low(p, w.len));
     w.key0 = sh_down(p, w.klo);
     w.tiles = w.len > w.klo ? sh_tiles(w.len - w.key0) : 0;
     return w;
   };
-  // Keys of several row blocks are cut into chunks, each a CTA's share: of the tiles and one start
-  // and end per group, then with that many chunks' starts and ends.
-  auto share_of = [&](long long n) { return max(1ll, sh_div(n * p.Hkv + p.ctas - 1, p.ctas)); };
-  const long long tiles = plan_sum(work, warps), least = share_of(tiles);
-  long long pieces = 0;
+  // Keys of several row blocks are cut into chunks, each a CTA's share: what all tiles and the
+  // pieces of whole groups take, then with that many chunks' starts and ends once more.
+  long long length = work * kShShared;
+  for (int b = tid; b < p.B; b += kShPlanThreads) {
+    const int n = own_of(b).tiles;
+    work += n;
+    length += n ? sh_length(0, n) : 0;
+  }
+  const long long least = sh_div(plan_sum(work, warps) * p.Hkv + p.ctas - 1, p.ctas);  // tiles
+  const long long plain = plan_sum(length, warps);
+  auto share_of = [&](long long n) { return sh_div(n * p.Hkv + p.ctas - 1, p.ctas); };
+  long long chunk = 1, pieces = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    const long long cut = plan_sum(pieces, warps) * kShCost;
-    const long long chunk = max((least + 1) / 2, share_of(tiles + cut) - kShCost);
+    const long long cut = pass ? plan_sum(pieces, warps) * kShCost : 0;
+    chunk = max(max(1ll, (least + 1) / 2), sh_div(max(0ll, share_of(plain + cut) - kShCost), kShShared));
     pieces = 0;
     for (int g = tid; g < p.G; g += kShPlanThreads) {
       ShGroup& gr = groups[g];
@@ -257,7 +261,10 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
       pieces += (long long)gr.chunks * gr.blocks;
     }
   }
-  // positions of the shared keys, group by group
+  const long long total = (plain + plan_sum(pieces, warps) * kShCost) * p.Hkv;
+  // no less than a tile, so that every CTA within a piece has one of it
+  const long long share = max((long long)max(kShOwn, kShShared), sh_div(total + p.ctas - 1, p.ctas));
+  // positions: of the shared keys, group by group, then of the sequences' own keys
   long long at = 0, base = 0;
   int n_prefix = 0;
   for (int g0 = 0; g0 < p.G; g0 += kShPlanThreads) {
@@ -267,7 +274,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
       n = groups[g].chunks;
       count = n * groups[g].blocks * p.Hkv;
       len = (long long)p.Hkv * groups[g].blocks *
-            ((long long)groups[g].tiles + groups[g].chunks * kShCost);
+            ((long long)groups[g].tiles * kShShared + groups[g].chunks * kShCost);
     }
     const long long n0 = n_prefix + plan_scan<false>(n, warps, all_n);
     const long long b0 = base + plan_scan<false>(count, warps, all_count);
@@ -281,8 +288,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     base += all_count;
     at += all_len;
   }
-  if (tid == 0)
-    p.deal[0] = ShDeal{at, max(1ll, sh_div(at + p.ctas - 1, p.ctas)), 0, n_prefix};
+  if (tid == 0) *p.head = ShHead{total, share, n_prefix, n_prefix + p.B};
   __syncthreads();
   for (int g = warp; g < p.G; g += kShPlanWarps) {  // a lane per chunk
     const ShGroup gr = groups[g];
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
       const int t0 = c * len + min(c, more), t1 = t0 + len + (c < more);
       ShDesc x;
       x.tiles = t1 - t0;
-      x.start = gr.start + (long long)p.Hkv * gr.blocks * ((long long)t0 + c * kShCost);
+      x.start = gr.start + (long long)p.Hkv * gr.blocks * ((long long)t0 * kShShared + c * kShCost);
       x.key0 = gr.key0 + t0 * kShKeys;
       x.klo = max(x.key0, gr.low);
       x.khi = min(gr.shared, gr.key0 + t1 * kShKeys);
@@ -303,13 +309,11 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
       if (MATTN_IN_BOUNDS(kSiteShPlan, gr.desc + c, p.max_prefix)) p.desc[gr.desc + c] = x;
     }
   }
-  // and of the own keys
-  at = 0;
   for (int b0 = 0; b0 < p.B; b0 += kShPlanThreads) {
     const int b = b0 + tid;
     Own w{0, 0, 0, 0};
     if (b < p.B) w = own_of(b);
-    const long long len = w.tiles ? (long long)p.Hkv * (kShCost + w.tiles) : 0;
+    const long long len = w.tiles ? p.Hkv * sh_length(0, w.tiles) : 0;
     long long all_len;
     const long long a0 = at + plan_scan<false>(len, warps, all_len);
     at += all_len;
@@ -335,8 +339,6 @@ __global__ void __launch_bounds__(kShPlanThreads) shared_plan_kernel(const ShPro
     }
     p.seqs[b] = q;
   }
-  if (tid == 0)
-    p.deal[1] = ShDeal{at, max(1ll, sh_div(at + p.ctas - 1, p.ctas)), n_prefix, n_prefix + p.B};
 }
 
 // ------------------------------------------------------------------------- the pieces
@@ -394,59 +396,33 @@ struct ShRing {
   }
 };
 
-// The producer's walk over a CTA's share of one kind of pieces: runs of tiles [t0, t1).
+// The producer's walk over the CTA's share of the pieces: runs of tiles [t0, t1).
 struct ShWalk {
   ShDesc d, ahead;   // this piece and, read early, the one behind it
-  int at, end;       // the piece's description; those of the kind end here
-  int h, block;      // its head and row block
-  int rank;          // the CTA's among those that share the kind
+  int at, n_desc;     // the piece's description
+  int h, block;       // its head and row block
   int t0, t1;
   long long lo, hi;  // positions still to go
-  __device__ __forceinline__ int piece() const { return h * max(1, d.blocks) + block; }
   __device__ __forceinline__ void enter(const ShProblem& p) {
-    ahead = p.desc[min(at + 1, end - 1)];
-  }
-  __device__ __forceinline__ bool begin(const ShProblem& p, int kind, int r) {
-    const ShDeal deal = p.deal[kind];
-    rank = r;
-    lo = min(deal.total, r * deal.share);
-    hi = min(deal.total, lo + deal.share);
-    if (lo >= hi) return false;
-    // The last piece that starts at or before lo, 32 probes at a time (pieces without tiles start
-    // where the next one does).
-    const int lane = threadIdx.x & 31;
-    int to = deal.to;
-    at = deal.from;
-    end = deal.to;
-    while (to - at > 1) {
-      const int step = (to - at + 31) / 32, i = at + lane * step;
-      const bool below = i < to && p.desc[i].start <= lo;
-      const int hit = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0's always is
-      to = min(to, at + (hit + 1) * step);
-      at += hit * step;
-    }
-    d = p.desc[at];
-    enter(p);
-    block = (int)sh_div(lo - d.start, kShCost + d.tiles);
-    const int n = max(1, d.blocks);
-    h = block / n;
-    block -= h * n;
-    return find(p);
+    ahead = p.desc[min(at + 1, n_desc - 1)];
   }
   // From position lo: the run that begins there (false: none left).
   __device__ __forceinline__ bool find(const ShProblem& p) {
     while (lo < hi) {
-      const long long len = kShCost + d.tiles, start = d.start + piece() * len;
-      const long long stop = min(hi, start + len);
-      t0 = (int)max(0ll, lo - start - kShCost);
-      t1 = (int)max(0ll, stop - start - kShCost);
+      const long long len = sh_length(d.blocks, d.tiles);
+      const long long start = d.start + piece() * len;
+      const long long end = min(hi, start + len);
+      const int w = sh_weight(d.blocks);
+      t0 = (int)sh_div(max(0ll, lo - start - kShCost) + w - 1, w);
+      t1 = min(d.tiles, (int)sh_div(max(0ll, end - start - kShCost) + w - 1, w));
       if (t0 < t1) return true;
-      lo = stop;
+      lo = end;
       if (lo < start + len || lo >= hi) return false;  // the share ends inside the piece
       step(p);
     }
     return false;
   }
+  __device__ __forceinline__ int piece() const { return h * max(1, d.blocks) + block; }
   __device__ __forceinline__ void step(const ShProblem& p) {
     if (++block < d.blocks) return;
     block = 0;
@@ -454,11 +430,12 @@ struct ShWalk {
     h = 0;
     ++at;
     d = ahead;
-    while (d.tiles == 0 && at + 1 < end) d = p.desc[++at];
+    while (d.tiles == 0 && at + 1 < n_desc) d = p.desc[++at];
     enter(p);
   }
   __device__ __forceinline__ bool next(const ShProblem& p) {
-    lo = d.start + (piece() + 1) * (long long)(kShCost + d.tiles);
+    const long long len = sh_length(d.blocks, d.tiles);
+    lo = d.start + (piece() + 1) * len;
     if (lo >= hi) return false;
     step(p);
     return find(p);
@@ -588,7 +565,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   early_start();
-  next_kernel_in();
   // The next message, or false (and ok = false where the wait ran out).
   ShRing mr;
   auto next_msg = [&](ShMsg& m, bool& ok) {
@@ -608,23 +584,32 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     uint32_t q_pass[2] = {0, 0}, half = 0;  // parity of the halves' release, half in turn
     uint32_t q_armed = 0, q_seen = 0;       // halves with a copy, parity of their latest
     const int per_tile = max(1, kShKeys >> p.shift), page_rows = min(kShKeys, 1 << p.shift);
-    // Each CTA takes of both kinds, one half of the CTAs shared keys first (with many rows they ask
-    // more of the SM) and the other half own keys (they ask more of HBM); own keys in the other
-    // order of CTAs, so that few pieces of either kind meet in none.
     ShWalk walk;
-    int kind = (int)blockIdx.x < p.ctas / 2 ? 0 : 1, kinds = 2;  // kinds: still to begin
-    bool ok = true, more = false;
-    auto begin_kind = [&]() {
-      while (kinds > 0) {
-        const bool any =
-            walk.begin(p, kind, kind ? p.ctas - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        kind ^= 1;
-        --kinds;
-        if (any) return true;
+    const ShHead head = *p.head;
+    walk.lo = min(head.total, blockIdx.x * head.share);
+    walk.hi = min(head.total, walk.lo + head.share);
+    bool ok = true, more = walk.lo < walk.hi;
+    if (more) {
+      walk.n_desc = head.n_desc;
+      // The last piece that starts at or before lo, 32 probes at a time (pieces without tiles
+      // start where the next one does).
+      int from = 0, to = head.n_desc;
+      while (to - from > 1) {
+        const int step = (to - from + 31) / 32, at = from + lane * step;
+        const bool below = at < to && p.desc[at].start <= walk.lo;
+        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0's always is
+        to = min(to, from + (hit + 1) * step);
+        from += hit * step;
       }
-      return false;
-    };
-    more = begin_kind();
+      walk.at = from;
+      walk.d = p.desc[walk.at];
+      walk.enter(p);
+      const int n = max(1, walk.d.blocks);
+      walk.block = (int)sh_div(walk.lo - walk.d.start, sh_length(walk.d.blocks, walk.d.tiles));
+      walk.h = walk.block / n;
+      walk.block -= walk.h * n;
+      more = walk.find(p);
+    }
     while (ok) {
       ok = sh_wait(msg_empty + mr.slot, mr.pass ^ 1, wd);
       if (!ok) break;
@@ -640,7 +625,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           m.nseq = min(d.nseq - walk.block * p.seqs_per_block, p.seqs_per_block);
           m.shared = d.blocks;
           m.h = walk.h;
-          m.slot = (long long)walk.rank + d.base + walk.piece();
+          m.slot = (long long)blockIdx.x + d.base + walk.piece();
         }
         msgs[mr.slot] = m;
         mbar_arrive(msg_full + mr.slot);
@@ -705,7 +690,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         if (!ok) break;
         vr.next(C::kVSlots);
       }
-      more = ok && (walk.next(p) || begin_kind());
+      more = ok && walk.next(p);
     }
     // On the way out of a failed wait copies in flight land first (an unused slot's wait ends
     // at once).
@@ -960,7 +945,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
 // thread takes 4 channels of a row, and where rows are few the parts are spread over groups of
 // threads, whose results meet in shared memory. Bound by latency: the sequence, its pieces, then
 // the parts, four loads of them at a time. Everything in a fixed order.
-constexpr int kShJoinThreads = 512;
+constexpr int kShJoinThreads = 256;
 
 struct ShAcc {
   float m, l;
@@ -984,8 +969,8 @@ __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShPro
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   early_start();
   const ShSeq s = p.seqs[b];
-  const long long shares[2] = {p.deal[0].share, p.deal[1].share};
   if (tid < 32) {
+    const ShHead head = *p.head;
     const int pieces = s.chunks + (s.sdesc >= 0);
     int n = 0;
     for (int i0 = 0; i0 < pieces; i0 += 32) {
@@ -995,10 +980,10 @@ __global__ void __launch_bounds__(kShJoinThreads) shared_join_kernel(const ShPro
         const bool own = i == s.chunks;
         const ShDesc d = p.desc[own ? s.sdesc : s.pdesc + i];
         const int piece = own ? h : h * d.blocks + s.block;
-        const long long start = d.start + piece * (long long)(kShCost + d.tiles) + kShCost;
-        const long long share = own ? shares[1] : shares[0];
-        const int c0 = (int)sh_div(start, share);
-        count = (int)sh_div(start + d.tiles - 1, share) - c0 + 1;
+        const long long start = d.start + piece * sh_length(d.blocks, d.tiles) + kShCost;
+        const int c0 = (int)sh_div(start, head.share);
+        const long long last = start + (long long)(d.tiles - 1) * sh_weight(d.blocks);
+        count = (int)sh_div(last, head.share) - c0 + 1;
         first = d.base + piece + c0;
         if (own) first = ~first;
       }
@@ -1100,7 +1085,7 @@ ShLayout sh_layout(int B, int Hq, int Hkv, int Sq, int G, int max_len, int D) {
   w.max_desc = w.max_prefix + B;
   w.p_slots = shared ? w.ctas + (long long)w.max_prefix * Hkv : 0;
   w.s_slots = w.ctas + (long long)B * Hkv;
-  size_t at = up256(2 * sizeof(ShDeal));
+  size_t at = up256(sizeof(ShHead));
   auto take = [&](size_t n) {
     const size_t x = at;
     at += up256(n);
@@ -1160,8 +1145,7 @@ cudaError_t launch_shared(const void* q, const void* k, const void* v, ShProblem
       !make_map_bf16_3d(&m.k, k, slices, 1 << p.shift, D, std::min(kShKeys, 1 << p.shift)) ||
       !make_map_bf16_3d(&m.v, v, slices, 1 << p.shift, D, std::min(kShKeys, 1 << p.shift)))
     return cudaErrorInvalidValue;
-  const size_t plan_smem =
-      sizeof(int) * (2 * ((p.B + 3) & ~3) + ((p.G + 4) & ~3)) + sizeof(ShGroup) * p.G;
+  const size_t plan_smem = sizeof(int) * (((p.B + 3) & ~3) + ((p.G + 4) & ~3)) + sizeof(ShGroup) * p.G;
   static DeviceOnce ready;
   cudaError_t e = ready.allow_smem(shared_plan_kernel, 226 * 1024 - 1024);
   if (e != cudaSuccess) return e;
@@ -1248,10 +1232,10 @@ MATTN_API attn_status attn_decode_shared(const void* q, const void* k, const voi
   f.ctas = w.ctas;
   f.max_desc = w.max_desc;
   f.max_prefix = w.max_prefix;
-  // a part per CTA and piece that meet: no more than CTAs and pieces, of each kind
-  f.max_parts = 2 * w.ctas + w.max_prefix + 1;
+  // a part per CTA and piece that meet, and a sequence's pieces lie one behind the other
+  f.max_parts = w.ctas + w.max_prefix + 1;
   char* ws = static_cast<char*>(workspace);
-  f.deal = reinterpret_cast<ShDeal*>(ws);
+  f.head = reinterpret_cast<ShHead*>(ws);
   f.desc = reinterpret_cast<ShDesc*>(ws + w.desc);
   f.seqs = reinterpret_cast<ShSeq*>(ws + w.seqs);
   f.p_lse = reinterpret_cast<float*>(ws + w.p_lse);
