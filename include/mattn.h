@@ -514,8 +514,9 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
  * sequences hold must lie among their first keys (whole pages before `first`); with new_table,
  * its pages must hold no row that the call reads, other than in its own place. Lengths outside
  * [0, max_len] count as the nearest bound. What is written overlaps nothing else
- * (ATTN_ERR_INVALID_ARG). page_size 16, 32, 64 or 128; B <= 16384 and B * Hkv <= 65535
- * (ATTN_ERR_UNSUPPORTED). Asynchronous on `stream`, two launches. */
+ * (ATTN_ERR_INVALID_ARG). page_size 16, 32, 64 or 128; B <= 16384, B * Hkv <= 65535 and
+ * num_pages * Hkv * page_size < 2^32 (ATTN_ERR_UNSUPPORTED). Asynchronous on `stream`, two
+ * launches. */
 attn_status attn_cache_evict(const float* weights, float* weights_out, int weights_stride,
                              const int* seq_lens, const int* starts, int sink, int keep,
                              int recent, void* k, void* v, int num_pages, int page_size,

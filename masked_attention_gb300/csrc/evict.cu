@@ -4,22 +4,30 @@
 //
 // Two kernels. The first finds, per pair, the kept keys: the key of rank keep - recent in the
 // order (weight descending, index ascending) by a radix selection on the weights' bits (ordered
-// as unsigned numbers; 11, 11 and 10 bits, so that three histograms of the block's weights,
-// staged in shared memory, give it exactly), then an ascending list of those above it. Bound by
-// latency: one block per pair, six passes over weights in shared memory.
+// as unsigned numbers; 11, 11 and 10 bits, so that three histograms of the weights, staged in
+// shared memory, give it exactly), then an ascending list of those above it. Bound by latency: a
+// pair's candidates are dealt out to a cluster of up to eight blocks, each of which adds up the
+// histograms of all by 16-byte reads of their shared memory.
 //
 // The second moves the rows. HBM is the bound: every kept row is read and written once. In
 // place, kept key m's row goes from kept[m] to first + m <= kept[m], so in ascending batches
 // no write reaches a later batch's source; inside a batch all rows are read before one is
 // written (a barrier). A block therefore owns some channels of one pair's K or V rows from the
-// first batch to the last, and pairs x channels give the parallelism. Into other pages no order
-// is needed and batches are dealt out too.
+// first batch to the last, alone or with the others of its cluster, behind the cluster's barrier.
+// The next batch's rows are read while the last one's are written, and the places of the one
+// after it are looked up meanwhile, one row per thread. Into other pages no order is needed and
+// batches are dealt out too.
+//
+// 8 sequences of 32768 keys, 8 heads of 128 channels, 8192 kept: 126 us, 4.3 TB/s of the 545 MB
+// that must move. 32 of 8000, 4000 kept: 200 us, 5.3 TB/s. Rows in flight are the bound: with half
+// of them per block (2 pieces per thread, or 128 threads) 158 and 250 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <climits>
 #include <cstdint>
 
+#include "common.cuh"
 #include "host_util.h"
 #include "launch.h"
 
@@ -28,12 +36,15 @@
 namespace mattn {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelStaged = 48 * 1024;  // weights of a pair that are staged (4 bytes each)
+constexpr int kSelStaged = 48 * 1024;  // weights of a block that are staged (4 bytes each)
 constexpr int kSelBins = 2048;
-constexpr int kMoveThreads = 512;
+constexpr int kSelOwnBins = kSelBins / kSelThreads;
+constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // 16-byte pieces of a thread in flight
+constexpr int kMoveBlocks = 4;  // blocks per SM
+constexpr int kMaxCluster = 8;  // blocks of a cluster, on any device
 
 struct EvictArgs {
   const float* weights;
@@ -53,8 +64,10 @@ struct EvictArgs {
   int* freed;
   int max_freed;
   int* info;
-  int splits, piece;  // the move: parts of a row of `piece` bytes
-  int chunks;         // the move into other pages: runs of positions
+  int select_cluster;  // blocks of a pair in the selection
+  int move_cluster;    // blocks that share the batches of a move in place
+  int splits, piece;   // the move: parts of a row of `piece` bytes
+  int chunks;          // the move into other pages: runs of positions
 };
 
 struct EvictSeq {
@@ -87,6 +100,40 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+// All threads of the cluster: what they read and wrote before lies before what any does after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile(
+      "barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
+          : "memory");
+}
+
+// The int at the same place in the shared memory of the cluster's block `rank`.
+__device__ __forceinline__ void ranks_sync(int ranks) {
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
+__device__ __forceinline__ int cluster_read(const int* p, int rank) {
+  uint32_t at;
+  int x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+__device__ __forceinline__ int4 cluster_read4(const int* p, int rank) {
+  uint32_t at;
+  int4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(at)
+               : "memory");
+  return x;
+}
+
 // Sum over the block of `mine`, and of those of the threads before: by a scan of warp sums.
 __device__ __forceinline__ int block_before(int mine, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -112,14 +159,15 @@ __device__ __forceinline__ int block_before(int mine, int* warp_sums, int& total
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
   extern __shared__ uint32_t staged[];
-  __shared__ int hist[kSelBins];
+  __shared__ alignas(16) int hist[3][kSelBins];
   __shared__ int sums[kSelWarps], equals[kSelWarps];
-  __shared__ int found_bin, found_above;
+  __shared__ int found_bin, found_above, count[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.Hkv, h = blockIdx.x % a.Hkv;
+  const int ranks = a.select_cluster, pair = blockIdx.x / ranks, rank = blockIdx.x % ranks;
+  const int b = pair / a.Hkv, h = pair % a.Hkv;
   early_start();
   const EvictSeq s = evict_seq(a, b);
-  if (h == 0) {  // the sequence's length and its pages that go
+  if (h == 0 && rank == 0) {  // the sequence's length and its pages that go
     int gone = 0, cuts = 0, total, all_cuts;
     const int upto = b == a.B - 1 ? a.B : b;
     for (int i = tid; i < upto; i += kSelThreads) {
@@ -143,20 +191,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       }
     }
   }
-  int* kept = a.kept + (size_t)blockIdx.x * a.keep;
+  int* kept = a.kept + (size_t)pair * a.keep;
+  const int each = rank * kSelThreads + tid, all = ranks * kSelThreads;
   if (!s.cut) {
-    for (int m = tid; m < a.keep; m += kSelThreads) kept[m] = m < s.held ? s.first + m : -1;
+    for (int m = each; m < a.keep; m += all) kept[m] = m < s.held ? s.first + m : -1;
     return;
   }
-  const int c = s.len - s.first - a.recent, k = a.keep - a.recent;  // k of c candidates stay
-  for (int m = tid; m < a.recent; m += kSelThreads) kept[k + m] = s.len - a.recent + m;
+  const int cands = s.len - s.first - a.recent, k = a.keep - a.recent;  // k of them stay
+  for (int m = each; m < a.recent; m += all) kept[k + m] = s.len - a.recent + m;
   if (k == 0) return;
+  // this block's candidates
+  const int begin = (int)((long long)cands * rank / ranks);
+  const int c = (int)((long long)cands * (rank + 1) / ranks) - begin;
   const uint32_t* w =
-      reinterpret_cast<const uint32_t*>(a.weights + (size_t)blockIdx.x * a.stride + s.first);
+      reinterpret_cast<const uint32_t*>(a.weights + (size_t)pair * a.stride + s.first + begin);
   const bool stage = c <= kSelStaged;
   if (stage)
     for (int i = tid; i < c; i += kSelThreads) staged[i] = weight_key(w[i]);
   auto key_at = [&](int i) { return stage ? staged[i] : weight_key(w[i]); };
+  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
 
   // The threshold: the largest key that at least k candidates reach, digit by digit.
   uint32_t prefix = 0, mask = 0;
@@ -165,8 +219,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
     for (int i0 = warp * 32; i0 < c; i0 += kSelThreads) {
       const int i = i0 + lane;
       int bin = -1;
@@ -178,21 +230,34 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       int same;
       __match_all_sync(0xffffffffu, bin, &same);
       if (same) {
-        if (lane == 0 && bin >= 0) atomicAdd(&hist[bin], 32);
+        if (lane == 0 && bin >= 0) atomicAdd(&hist[pass][bin], 32);
       } else if (bin >= 0) {
-        atomicAdd(&hist[bin], 1);
+        atomicAdd(&hist[pass][bin], 1);
       }
     }
-    __syncthreads();
-    // from the largest digit down: thread t holds the bins 2047 - 2t and 2046 - 2t
-    const int hi = kSelBins - 1 - 2 * tid;
-    const int n0 = hist[hi], n1 = hist[hi - 1];
+    cluster_sync();
+    // from the largest digit down: thread t holds the four bins down from hi
+    static_assert(kSelOwnBins == 4, "one 16-byte word of bins per thread");
+    const int hi = kSelBins - 1 - kSelOwnBins * tid;
+    int n[kSelOwnBins] = {};
+#pragma unroll 4
+    for (int r = 0; r < ranks; ++r) {
+      // (every block begins with its own bins, so that they do not all ask the same one)
+      const int4 x = cluster_read4(&hist[pass][hi - 3], (rank + r) & (ranks - 1));
+      n[0] += x.w;
+      n[1] += x.z;
+      n[2] += x.y;
+      n[3] += x.x;
+    }
     int total;
-    const int above = block_before(n0 + n1, sums, total);
-    if (above < left && left <= above + n0 + n1) {
-      const bool second = left > above + n0;
-      found_bin = second ? hi - 1 : hi;
-      found_above = second ? above + n0 : above;
+    int above = block_before(n[0] + n[1] + n[2] + n[3], sums, total);
+#pragma unroll
+    for (int e = 0; e < kSelOwnBins; ++e) {
+      if (above < left && left <= above + n[e]) {
+        found_bin = hi - e;
+        found_above = above;
+      }
+      above += n[e];
     }
     __syncthreads();
     left -= found_above;
@@ -221,6 +286,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     above += sums[i];
     equal += equals[i];
   }
+  if (tid == kSelThreads - 1) {  // the block's, for those of the blocks behind it
+    count[0] = above + sums[warp];
+    count[1] = equal + equals[warp];
+  }
+  cluster_sync();
+  for (int r = 0; r < rank; ++r) {
+    above += cluster_read(&count[0], r);
+    equal += cluster_read(&count[1], r);
+  }
   const uint32_t below = (1u << lane) - 1u;
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const int i = i0 + lane;
@@ -230,50 +304,67 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     const int g = above + __popc(gt & below), e = equal + __popc(eq & below);
     const bool take = (gt >> lane & 1) || ((eq >> lane & 1) && e < left);
     const int m = g + min(e, left);
-    if (take && MATTN_IN_BOUNDS(kSiteEvict, m, a.keep)) kept[m] = s.first + i;
+    if (take && MATTN_IN_BOUNDS(kSiteEvict, m, a.keep)) kept[m] = s.first + begin + i;
     above += __popc(gt);
     equal += __popc(eq);
   }
+  cluster_sync();  // no block ends while others read its shared memory
 }
 
-// Byte offset of a head's row at a position of sequence b, or -1 outside the pool.
-__device__ __forceinline__ long long evict_row(const EvictArgs& a, const int* table, int per,
-                                               int b, int h, int pos) {
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+// Row of the pool (counted over all pages and heads) that a head's key at a position of sequence
+// b has, or kNoRow outside the pool.
+__device__ __forceinline__ uint32_t evict_row(const EvictArgs& a, const int* table, int per, int b,
+                                              int h, int pos) {
   const int lp = pos >> a.shift;
-  if (lp >= per || !MATTN_IN_BOUNDS(kSiteEvict, lp, per)) return -1;
+  if (lp >= per || !MATTN_IN_BOUNDS(kSiteEvict, lp, per)) return kNoRow;
   const int page = table[(size_t)b * per + lp];
-  if (page < 0 || page >= a.num_pages) return -1;
-  return ((((long long)page * a.Hkv + h) << a.shift) + (pos & ((1 << a.shift) - 1))) * a.row_bytes;
+  if (page < 0 || page >= a.num_pages) return kNoRow;
+  return (((uint32_t)page * a.Hkv + h) << a.shift) + (pos & ((1 << a.shift) - 1));
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// Where a key's row comes from and goes to; equal: it stays.
+__device__ __forceinline__ uint2 evict_way(const EvictArgs& a, const EvictSeq& s, const int* kept,
+                                           int b, int h, int n, int to) {
+  if (n >= to) return make_uint2(kNoRow, kNoRow);
+  const int src = n < s.first || !s.cut ? n : kept[n - s.first];
+  if (!a.new_table && src == n) return make_uint2(kNoRow, kNoRow);
+  const uint32_t dst = evict_row(a, a.new_table ? a.new_table : a.table,
+                                 a.new_table ? a.new_per : a.per, b, h, n);
+  return make_uint2(evict_row(a, a.table, a.per, b, h, src), dst);
+}
+
+__global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) evict_move_kernel(const EvictArgs a) {
+  __shared__ uint2 ways[2][kMoveThreads];  // of a batch's rows: at most kMoveThreads
   early_start();
+  const int ranks = a.move_cluster, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks;
   const int parts = 2 * a.splits * a.chunks + 1;
-  const int pair = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int pair = unit / parts, part = unit % parts;
   const int b = pair / a.Hkv, h = pair % a.Hkv;
   const EvictSeq s = evict_seq(a, b);
   const int* kept = a.kept + (size_t)pair * a.keep;
-  auto source = [&](int n) { return n < s.first || !s.cut ? n : kept[n - s.first]; };
   const int end = s.new_len();
+  const int tid = threadIdx.x;
   if (part == parts - 1) {  // the weights; where they went from is 0
     const float* in = a.weights + (size_t)pair * a.stride;
     float* out = a.weights_out + (size_t)pair * a.stride;
-    for (int n0 = 0; n0 < end; n0 += kMoveThreads * kMoveUnroll) {
+    const int each = rank * kMoveThreads + tid, all = ranks * kMoveThreads;
+    for (int n0 = 0; n0 < end; n0 += all * kMoveUnroll) {
       float x[kMoveUnroll];
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        const int n = n0 + u * kMoveThreads + threadIdx.x;
-        x[u] = n < end ? in[source(n)] : 0.0f;
+        const int n = n0 + u * all + each;
+        x[u] = n < end ? in[n < s.first || !s.cut ? n : kept[n - s.first]] : 0.0f;
       }
-      __syncthreads();
+      ranks_sync(ranks);
 #pragma unroll
       for (int u = 0; u < kMoveUnroll; ++u) {
-        const int n = n0 + u * kMoveThreads + threadIdx.x;
+        const int n = n0 + u * all + each;
         if (n < end) out[n] = x[u];
       }
     }
-    __syncthreads();
-    for (int n = end + threadIdx.x; n < s.len; n += kMoveThreads) out[n] = 0.0f;
+    for (int n = end + each; n < s.len; n += all) out[n] = 0.0f;
     return;
   }
   const bool in_place = a.new_table == nullptr;
@@ -281,43 +372,57 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
   char* pool = part & 1 ? a.v : a.k;
   const int split = (part >> 1) % a.splits, chunk = (part >> 1) / a.splits;
   const int lanes = a.piece / 16;  // threads of a row
-  const int row = threadIdx.x / lanes, rows = kMoveThreads / lanes;
-  const int col = split * a.piece + threadIdx.x % lanes * 16;
+  const int row = tid / lanes, rows = kMoveThreads / lanes, own = rows * kMoveUnroll;
+  const int col = split * a.piece + tid % lanes * 16;
+  const int batch = own * ranks;
   int from = s.first, to = end;
   if (!in_place) {  // all pages from the first that holds a key that may go, in runs
     from = s.first >> a.shift << a.shift;
-    const int batch = rows * kMoveUnroll;
     const int batches = (end - from + batch - 1) / batch;
     const int lo = from + (int)((long long)batches * chunk / a.chunks) * batch;
     to = min(end, from + (int)((long long)batches * (chunk + 1) / a.chunks) * batch);
     from = lo;
   }
   [[maybe_unused]] const long long bytes = ((long long)a.num_pages * a.Hkv << a.shift) * a.row_bytes;
-  for (int n0 = from; n0 < to; n0 += rows * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    long long dst[kMoveUnroll];
+  const int mine = from + rank * own + tid;  // thread t < own looks up row t of the block's
+  auto way = [&](int n0) {
+    return tid < own ? evict_way(a, s, kept, b, h, n0 + mine - from, to) : make_uint2(kNoRow, kNoRow);
+  };
+  uint4 x[kMoveUnroll];
+  uint32_t dst[kMoveUnroll];
+  auto load = [&](const uint2* ways, uint4 (&x)[kMoveUnroll], uint32_t (&dst)[kMoveUnroll]) {
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
-      const int n = n0 + u * rows + row;
-      dst[u] = -1;
+      const uint2 way = ways[u * rows + row];
       x[u] = make_uint4(0, 0, 0, 0);
-      if (n < to) {
-        const int src = source(n);
-        if (!in_place || src != n) {
-          dst[u] = evict_row(a, in_place ? a.table : a.new_table, in_place ? a.per : a.new_per, b,
-                             h, n);
-          const long long at = evict_row(a, a.table, a.per, b, h, src);
-          if (at >= 0 && MATTN_IN_BOUNDS(kSiteEvictRow, at + col + 15, bytes))
-            x[u] = *reinterpret_cast<const uint4*>(pool + at + col);
-          if (at == dst[u]) dst[u] = -1;
-        }
+      dst[u] = way.x == way.y ? kNoRow : way.y;
+      if (dst[u] != kNoRow && way.x != kNoRow) {
+        const size_t at = (size_t)way.x * a.row_bytes + col;
+        if (MATTN_IN_BOUNDS(kSiteEvictRow, at + 15, bytes))
+          x[u] = *reinterpret_cast<const uint4*>(pool + at);
       }
     }
-    if (in_place) __syncthreads();  // every row of the batch is read before one is written
+  };
+  ways[0][tid] = way(from);
+  ways[1][tid] = way(from + batch);
+  __syncthreads();
+  load(ways[0], x, dst);
+  int turn = 0;
+  for (int n0 = from; n0 < to; n0 += batch, turn ^= 1) {
+    const uint2 later = way(n0 + 2 * batch);
+    ranks_sync(ranks);  // every row of the batch is read before one is written
+    uint4 next[kMoveUnroll];
+    uint32_t next_dst[kMoveUnroll];
+    load(ways[turn ^ 1], next, next_dst);
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (dst[u] >= 0 && MATTN_IN_BOUNDS(kSiteEvictRow, dst[u] + col + 15, bytes))
-        *reinterpret_cast<uint4*>(pool + dst[u] + col) = x[u];
+    for (int u = 0; u < kMoveUnroll; ++u) {
+      const size_t at = (size_t)dst[u] * a.row_bytes + col;
+      if (dst[u] != kNoRow && MATTN_IN_BOUNDS(kSiteEvictRow, at + 15, bytes))
+        *reinterpret_cast<uint4*>(pool + at) = x[u];
+      x[u] = next[u];
+      dst[u] = next_dst[u];
+    }
+    ways[turn][tid] = later;
   }
 }
 
@@ -351,6 +456,8 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
     return ATTN_ERR_UNSUPPORTED;
   // the freed pages are counted in an int
   if ((long long)B * pages_per_seq > INT_MAX) return ATTN_ERR_UNSUPPORTED;
+  // rows of a pool are counted in 32 bits, the largest number meaning none
+  if ((long long)num_pages * Hkv * page_size > 0xffffffffLL) return ATTN_ERR_UNSUPPORTED;
   if (B == 0) return ATTN_OK;
   if (!weights || !weights_out || !seq_lens || !k || !v || !page_table || !kept || !new_lens ||
       !info || (max_freed > 0 && !freed))
@@ -414,16 +521,30 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
   a.freed = freed;
   a.max_freed = max_freed;
   a.info = info;
-  // Blocks of the move: about eight per SM. In place by splitting the rows, down to 64 bytes;
-  // into other pages by runs of whole rows.
-  const long long want = 8LL * sm_count();
-  a.splits = a.chunks = 1;
+  const long long sms = sm_count();
+  // Blocks of a pair in the selection: as long as each has 2048 keys or more and all run at once,
+  // two per SM. (8 x 32768 keys of 8 heads: 1, 2, 4, 8 blocks 152, 136, 132, 146 us for the call;
+  // 60000 keys of 8 heads 255, 113, 95, 90 us: both with a move of 512 threads, no clusters.)
+  a.select_cluster = 1;
+  while (a.select_cluster < kMaxCluster && max_len >= 2 * 2048LL * a.select_cluster &&
+         2 * pairs * a.select_cluster <= 2 * sms)
+    a.select_cluster *= 2;
+  // The move: three blocks or more per SM. Into other pages by runs of whole rows. In place first
+  // by the channels, down to 64 bytes, then by clusters. (8 x 32768 keys of 8 heads, 8192 kept:
+  // four parts of a row 126 us, two parts and clusters of two 148 us: their barrier costs more
+  // than a block's. 60000 keys of 8 heads, 16000 kept, four parts: clusters of four 70 us, of
+  // eight 60 us.)
+  const long long want = 3 * sms;
+  a.move_cluster = a.splits = a.chunks = 1;
+  const int batch = kMoveThreads * 16 / a.row_bytes * kMoveUnroll;
+  const long long most = ((long long)std::min(max_len, keep) + page_size + batch - 1) / batch;
   if (new_table) {
-    const int batch = kMoveThreads * 16 / a.row_bytes * kMoveUnroll;
-    const long long most = ((long long)std::min(max_len, keep) + page_size + batch - 1) / batch;
     a.chunks = (int)std::max(1LL, std::min(most, (want + 2 * pairs - 1) / (2 * pairs)));
   } else {
     while (2 * pairs * a.splits < want && a.row_bytes / a.splits > 64) a.splits *= 2;
+    while (a.move_cluster < kMaxCluster && 2 * pairs * a.splits * a.move_cluster < want &&
+           a.move_cluster < most)
+      a.move_cluster *= 2;
   }
   a.piece = a.row_bytes / a.splits;
 
@@ -431,11 +552,15 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
   attn_status st = cuda_status(ready.allow_smem(evict_select_kernel, kSelStaged * 4));
   if (st != ATTN_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const size_t smem = (size_t)std::min(max_len, kSelStaged) * 4;
-  st = cuda_status(launch_early(evict_select_kernel, (unsigned)pairs, kSelThreads, smem, s, a));
+  const int slice = max_len / a.select_cluster + 1;
+  const size_t smem = (size_t)std::min(slice, kSelStaged) * 4;
+  st = cuda_status(launch_early_clusters(evict_select_kernel, (unsigned)(pairs * a.select_cluster),
+                                         a.select_cluster, kSelThreads, smem, s, a));
   if (st != ATTN_OK) return st;
-  const unsigned blocks = (unsigned)(pairs * (2 * a.splits * a.chunks + 1));
-  return cuda_status(launch_early(evict_move_kernel, blocks, kMoveThreads, 0, s, a));
+  const unsigned blocks =
+      (unsigned)(pairs * (2 * a.splits * a.chunks + 1) * a.move_cluster);
+  return cuda_status(launch_early_clusters(evict_move_kernel, blocks, a.move_cluster, kMoveThreads, 0,
+                                           s, a));
 }
 
 namespace mattn {

@@ -83,21 +83,31 @@ class DeviceOnce {
 };
 
 // Launches a kernel that begins with early_start(): it may be set up before the
-// stream's previous kernel has ended, and waits for that end.
+// stream's previous kernel has ended, and waits for that end. Blocks in clusters of
+// `cluster` (a divisor of `grid`, at most 8).
 template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, dim3 block, size_t smem,
-                         cudaStream_t stream, Args&&... args) {
+cudaError_t launch_early_clusters(void (*kernel)(Params...), unsigned grid, unsigned cluster,
+                                  dim3 block, size_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, dim3 block, size_t smem,
+                         cudaStream_t stream, Args&&... args) {
+  return launch_early_clusters(kernel, grid, 1, block, smem, stream, args...);
 }
 
 inline int sm_count() {

@@ -293,3 +293,29 @@ def test_refusals():
     t = torch.zeros(1, 1, 4)
     with pytest.raises(ValueError):
         M.attn_cache_evict(t, t, t, t, t, t, t, t, t, t, page_size=16, recent=0)
+
+
+def test_refuses_more_rows_than_are_counted():
+    """Pool rows are numbered in 32 bits; empty batches show the check alone."""
+    import masked_attention_gb300 as M
+
+    def call(pages, Hkv=2, ps=128):
+        return M.lib().attn_cache_evict(None, None, 100, None, None, 4, 50, 8, None, None, pages, ps,
+                                        None, 7, None, 0, 0, Hkv, 100, 64, None, None, None, 0, None,
+                                        None)
+
+    assert call(2 ** 24 - 1) == M.ATTN_OK                      # 2^32 - 256 rows
+    assert call(2 ** 24) == call(2 ** 31 - 1) == M.ATTN_ERR_UNSUPPORTED
+    assert call(2 ** 27 - 1, 2, 16) == M.ATTN_OK and call(2 ** 27, 2, 16) == M.ATTN_ERR_UNSUPPORTED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("copy", [False, True])
+@pytest.mark.parametrize("Hkv,D", [(1, 64), (3, 128), (40, 64)])
+def test_blocks_that_share_a_pair(Hkv, D, copy):
+    """From one pair, whose keys several blocks select from and move, to 120; a sequence that is cut
+    beside one that is not, and slices of unlike lengths."""
+    c = Case([17001, 30, 8193], 4097, 33, 5, Hkv=Hkv, D=D, page=32, copy=copy, seed=Hkv)
+    c.check(in_place_weights=not copy)
+    c = Case([20011], 6000, 6000, 0, Hkv=Hkv, D=D, kind="few", copy=copy, seed=Hkv)
+    c.check()
