@@ -459,9 +459,11 @@ __device__ __forceinline__ float2 cap_near2(float2 s, float inv) {
 }
 
 // Score modifications: x becomes the modified score in log2 units (SCORE 0: stays the product).
-// pos: the row's position less the tile's first key.
+// pos: the row's position less the tile's first key. mine: the thread has a row; the others hold
+// products with what earlier rows or kernels left in the Q tile, and have no say in the branch.
 template <int SCORE>
-__device__ __forceinline__ void sh_modify(const ShProblem& p, float slope2, int pos, float (&x)[64]) {
+__device__ __forceinline__ void sh_modify(const ShProblem& p, float slope2, int pos, bool mine,
+                                          float (&x)[64]) {
   if constexpr (SCORE == 0) return;
   const float2 sl = make_float2(p.scale2, p.scale2);
   float size = 0.0f;
@@ -478,7 +480,7 @@ __device__ __forceinline__ void sh_modify(const ShProblem& p, float slope2, int 
   }
   if constexpr (SCORE & 2) {
     // (a NaN leaves `size` as it is and passes through the series too)
-    if (__all_sync(0xffffffffu, size * p.softcap_e < kCapNear)) {
+    if (__all_sync(0xffffffffu, !mine || size * p.softcap_e < kCapNear)) {
 #pragma unroll
       for (int c = 0; c < 64; c += 2) {
         const float2 y = cap_near2(make_float2(x[c], x[c + 1]), p.softcap_e);
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         }
         vr.next(C::kVSlots);
         if (active) {
-          sh_modify<SCORE>(p, slope2, pos - j0, x);
+          sh_modify<SCORE>(p, slope2, pos - j0, mine, x);
           if (!whole) {
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] = c >= from && c < to ? x[c] : -INFINITY;
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
           const float scale = SCORE == 0 ? p.scale2 : 1.0f;
           const float mt = row_max<64>(x) * scale;
           // The reference moves when a row's scores pass it by 2^8, or when it has none.
-          const bool move = mt > m + 8.0f;
+          const bool move = mine && mt > m + 8.0f;
           if (__any_sync(0xffffffffu, move)) {
             const float m_new = move ? mt : m;
             const float fix = move ? ex2_approx(m - m_new) : 1.0f;  // from -inf: 0
