@@ -26,8 +26,15 @@
 // tile as soon as the softmax has this one's scores in registers; warp 6 O += P V (P: bf16 in
 // tensor memory, in two places of its own, rounded to 8 bits as in the other bf16 calls; its sum
 // is of the unrounded values). (One warp for both products was what a tile waited for: 1900
-// cycles, of which 900 its waits.) Tiles of 64 keys, not 128: five K or V tiles then fit beside Q twice per SM instead of
-// two, so that the next ones arrive while this one is worked on.
+// cycles, of which 900 its waits.) Tiles of 64 keys, not 128: five K or V tiles then fit beside Q
+// twice per SM instead of two, so that the next ones arrive while this one is worked on.
+//
+// 32 heads on 8 of 128 channels, bf16. 16 sequences of 32768 own keys: 313 us, 6.8 TB/s, the rate
+// of a copy. 64 of 4000: 168 us, 6.3 TB/s. 64 sequences behind 32768 shared keys, 700 own keys
+// each: 80 us, 4.0 TB/s and 440 TFLOP/s. There the pieces' starts and ends, and the two small
+// kernels (about 10 us), are what it takes beyond the 47 us of its bytes. A soft-cap adds 8 us to
+// the 80 of 61 ragged sequences: 16 packed operations per pair of scores, in the warps that hold
+// rows.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -54,7 +61,11 @@ constexpr int kShKeys = 64;       // keys of a tile
 constexpr int kShOwn = 8, kShShared = 8, kShCost = 24;
 constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
-constexpr int kShMinShared = 128;  // shared keys below this are read by each sequence itself
+// Shared keys below this are read by each sequence itself: all but the first find them in the L2,
+// and a shared run is one more part to join. (64 sequences with 700 own keys behind 128, 256 and
+// 512 shared ones, in groups of 2: shared 52.8, 55.0, 59.0 us, by each itself 50.9, 54.3, 59.8 us;
+// in one group 48.0, 47.5, 47.8 and 46.1, 46.7, 48.5 us.)
+constexpr int kShMinShared = 512;
 
 struct ShDesc {  // pieces of the same keys: one per key/value head and, of shared keys, row block
   long long start;  // of the first one in the dealing out, of length sh_length() each

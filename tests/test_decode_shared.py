@@ -279,6 +279,99 @@ def test_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(1, 1, 1), (14, 2, 2), (16, 1, 1), (5, 1, 3)])
+def test_long_shared_runs(Hq, Hkv, Sq, page, D):
+    """Runs long enough to be read once, beside one that each sequence reads itself."""
+    Case([(3, 640), (2, 512), (2, 200), (3, 1100)], [1, 17, 300, 5, 60, 128, 129, 1, 127, -50],
+         Hq, Hkv, Sq, D, page, seed=6).check()
+
+
+@pytest.mark.gpu
+def test_ends_of_long_shared_runs():
+    """Shared lengths around the tile and page sizes and around what is read once; sequences that
+    end inside the shared keys, and empty ones."""
+    for s in (511, 512, 513, 527, 528, 575, 576, 577, 639, 641):
+        Case([(3, s), (2, 0), (1, 300)], [1, -s, 40, 0, 1, 3], seed=s).check()
+        Case([(4, s)], [-1, -100, 2, -s + 1], page=32, seed=s, Sq=2).check()
+    Case([(2, 600)], [-600, -600]).check()       # nobody is there
+    Case([(3, 600)], [-100, -90, -520]).check()  # the longest ends at 510: below what is read once
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(), dict(window=40), dict(window=400), dict(Sq=3),
+                                dict(softcap=20.0)])
+def test_what_no_row_sees_changes_nothing_behind_a_long_run(kw):
+    """NaN and infinities behind the sequences' ends, before the window, in other pages."""
+    c = Case([(3, 600), (2, 0)], [30, 100, -60, 70, 5], page=32, seed=5, **kw)
+    a, la = c.check()
+    Sq, window = c.shape[3], c.kw["window"]
+    low = [max(0, int(n) - Sq - window + 1) if window else 0 for n in c.lens]
+    seen = {(int(c.table[b, j // 32]), j % 32) for b in range(5) for j in range(low[b], int(c.lens[b]))}
+    # keys that some row of the group sees stay finite
+    seen |= {(int(c.table[0, j // 32]), j % 32) for j in range(min(low[:3]), 600)}
+    for at in range(len(c.k)):
+        for r in range(32):
+            if (at, r) not in seen:
+                c.k[at, :, r] = float("nan") if r % 2 else float("inf")
+                c.v[at, :, r] = float("inf") if r % 3 else float("nan")
+    o, lse = c.run()
+    assert np.array_equal(o.double().cpu().numpy(), a)
+    assert np.array_equal(lse.double().cpu().numpy(), la)
+
+
+@pytest.mark.gpu
+def test_nan_of_a_key_that_is_read_once_shows():
+    c = Case([(3, 576)], [10, 20, 30])
+    c.k[int(c.table[0, 3]), 1, 2] = float("nan")         # a shared key of head pair 1
+    o, lse = c.run()
+    assert torch.isnan(lse.cpu())[:, 2:].all() and not torch.isnan(lse.cpu())[:, :2].any()
+    assert torch.isnan(o.cpu())[:, 2:].all() and not torch.isnan(o.cpu())[:, :2].any()
+    c = Case([(3, 576)], [10, 20, 30])
+    c.v[int(c.table[0, 3]), 0, 5, 7] = float("nan")      # a shared value channel
+    o, lse = c.run()
+    bad = torch.isnan(o.cpu())
+    assert bad[:, :2, :, 7].all() and int(bad.sum()) == 6 and not torch.isnan(lse.cpu()).any()
+
+
+@pytest.mark.gpu
+def test_bad_pages_and_groups_of_long_runs():
+    c = Case([(3, 600), (2, 700)], [30, 100, 7, 70, 5], page=32, spare=1)
+    for b in range(3):
+        c.table[b, 2] = -3                               # the group's third page: zeros
+    c.table[1, 20], c.table[3, 23] = len(c.k), 2 ** 31 - 1
+    c.check()
+    c = Case([(3, 600), (2, 700)], [30, 100, 7, 70, 5], page=32)
+    ref = c.run()
+    o, lse = c.run(group_starts=torch.tensor([-7, 3, 99], dtype=torch.int32).cuda())
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    for starts, shared in (([3, 0, 5], [0, 700]), ([0, 0, 0], [600, 600]), ([0, 3, 1], [600, 9])):
+        c.check(group_starts=torch.tensor(starts, dtype=torch.int32).cuda(),
+                shared_lens=torch.tensor(shared, dtype=torch.int32).cuda())
+
+
+@pytest.mark.gpu
+def test_far_pages_of_a_long_run():
+    """Shared keys in pages past 4 GiB."""
+    import masked_attention_gb300 as M
+    c = Case([(3, 640)], [90, 33, 5], Hkv=2, D=128, page=128)
+    o, lse = c.run()
+    pages = (1 << 32) // (2 * 2 * 128 * 128) + len(c.k)
+    pools = [torch.empty(pages, 2, 128, 128, dtype=torch.bfloat16, device="cuda") for _ in (0, 1)]
+    for pool, x in zip(pools, (c.k, c.v)):
+        pool[-len(c.k):] = x.cuda()
+    table = torch.where(c.table >= 0, c.table + pages - len(c.k), -1).to(torch.int32).cuda()
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    ws = torch.empty(M.attn_decode_shared_workspace_bytes(3, 4, 2, 1, 1, table.shape[1] * 128, 128),
+                     dtype=torch.uint8, device="cuda")
+    M.attn_decode_shared(c.q.cuda(), *pools, o2, lse2, c.variant(), page_table=table, page_size=128,
+                         seq_lens=c.lens.cuda(), group_starts=c.starts.cuda(),
+                         shared_lens=c.shared.cuda(), workspace=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.gpu
 def test_reproducible_captured_and_on_another_stream():
     """Equal bits again, on a side stream and in two graphs that share a workspace; a graph
     follows lengths and groups that change under it."""

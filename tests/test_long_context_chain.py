@@ -12,9 +12,9 @@ from oracle.long_context import (axes_rows, cached_rows, decode_rows, evict, key
 from oracle.serving import norm_rope, page_plan
 
 HQ, HKV, D, PAGE = 4, 2, 64, 16
-SHARED, KEEP, RECENT, DECAY = 48, 20, 6, 0.75     # three whole pages are shared
+SHARED, KEEP, RECENT, DECAY = 528, 20, 6, 0.75    # 33 whole pages, read once
 AXES = bytes([0] * 10 + [1] * 12 + [2] * 10)
-FAR = 400
+FAR = 1000
 
 
 def table():
@@ -28,9 +28,9 @@ def f64(t):
 
 
 class Server:
-    """Four requests, the first three behind one prompt; 64 tokens a step at most."""
+    """Four requests, the first three behind one prompt; 560 tokens a step at most."""
 
-    B, CAP, PAGES, PER = 4, 64, 40, 8
+    B, CAP, PAGES, PER = 4, 560, 64, 38
 
     def __init__(self):
         import masked_attention_gb300 as M
@@ -207,9 +207,9 @@ def test_prompt_tokens_eviction_tokens(captured):
     s.write(feed(s, 2, lens, [at] * 3))
     check_write(s, b, lens)
     s.advance(s.lens)
-    assert s.cached.tolist() == [78, 65, 51, 20]
+    assert s.cached.tolist() == [SHARED + 30, SHARED + 17, SHARED + 3, 20]
 
-    clock = 100     # positions of new tokens are the caller's to count, past what is evicted too
+    clock = 600     # positions of new tokens are the caller's to count, past what is evicted too
     graphs = {}
 
     def run(name, work):
