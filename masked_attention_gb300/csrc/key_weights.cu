@@ -138,6 +138,7 @@ struct KwColumns {
   float nlse[kKwMaxN];   // -LSE in log2 units; -inf: the column adds nothing
   float slope[kKwMaxN];  // ALiBi slope in log2 units
   int pos[kKwMaxN];      // the row's position; -1: none
+  int skip[4];           // per warp: a row without an LSE is among its columns
 };
 
 // Sum over COLS columns of exp2(score - lse) for the thread's key j.
@@ -469,16 +470,20 @@ __global__ void __launch_bounds__(kKwThreads, 1)
         }
       }
     };
+    // A row whose LSE is -inf adds nothing, whatever its query holds: it has no position, and
+    // the masked form of the sum, which leaves NaN out too, is taken for its block.
+    bool skip = false;
     auto set_columns = [&](const KwWalk& w, int nb) {
       if (!meet()) return false;  // the block before has been used by all
+      bool none = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int c = t + 128 * i, row = nb * p.n_cols + c;
         if (c < p.n_cols) {
-          // a row without keys (LSE -inf) adds nothing
-          col.nlse[c] = ahead[i] == -INFINITY ? -INFINITY : -ahead[i] * kLog2e;
-          const bool there = row < R;
-          col.pos[c] = there ? w.r.len - p.Sq + row % p.Sq : -1;
+          const bool empty = ahead[i] == -INFINITY, there = row < R;
+          none |= empty;
+          col.nlse[c] = empty ? -INFINITY : -ahead[i] * kLog2e;
+          col.pos[c] = there && !empty ? w.r.len - p.Sq + row % p.Sq : -1;
           if constexpr (SCORE & 1) {
             const int h = w.hk * (p.Hq / p.Hkv) + (there ? row / p.Sq : 0);
             const float slope = p.slopes ? p.slopes[h] : exp2f(-8.0f * float(h + 1) / float(p.Hq));
@@ -486,7 +491,12 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           }
         }
       }
-      return meet();
+      none = __any_sync(0xffffffffu, none);
+      if (lane == 0) col.skip[warp & 3] = none;
+      if (!meet()) return false;
+      const int4 all = *reinterpret_cast<const int4*>(col.skip);
+      skip = all.x | all.y | all.z | all.w;
+      return true;
     };
     const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
     if (walk.left > 0) read_lse(walk, 0);
@@ -515,7 +525,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           old = p.previous[at];
           // a line per warp, to be in the L2 when its tile comes
           constexpr int kAhead = 8 * kTile;
-          if (lane == 0 && j + kAhead < len)
+          if (lane == 0 && j < len - kAhead)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.previous + at + kAhead));
         }
         float2 sum[4];
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
             tmem_ld_wait_regs(v0);
             if (c < p.n_cols) kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
           };
-          if (whole) columns_sum(std::false_type{});
+          if (whole && !skip) columns_sum(std::false_type{});
           else columns_sum(std::true_type{});
           tc_fence_before();
           __syncwarp();

@@ -187,6 +187,19 @@ def test_what_no_row_sees_changes_nothing():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Sq,Hq,Hkv", [(1, 4, 2), (3, 4, 2), (16, 8, 2), (40, 16, 2)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(alibi=True), dict(window=100)])
+def test_rows_without_an_lse_add_nothing(kw, Sq, Hq, Hkv):
+    """Places of a batch that hold no row: LSE -inf, and whatever their queries were left with."""
+    c = Case([700, 300, 129], Hq, Hkv, Sq, seed=8, **kw)
+    gone = torch.zeros(c.lse.shape, dtype=torch.bool)
+    gone[0, 1], gone[0, 0, -1], gone[1] = True, True, True
+    c.lse[gone] = -float("inf")
+    c.q[gone] = float("nan")
+    c.q[0, 1, 0, 3], c.q[1, 0] = float("inf"), -float("inf")
+    c.check()
+
+@pytest.mark.gpu
 def test_nan_of_a_visible_key_shows_there():
     c = Case([40, 150], Hq=4, Hkv=2)
     at = int(c.table[1, 5])
