@@ -21,6 +21,10 @@
 // with more than 256 of them, block by block for two tiles at a time), warp 9 issues the
 // products, and two warpgroups take turns with the tiles, so that one's exponentials run under
 // the other's product.
+//
+// 16 x 32768 keys of 8 heads of 128 channels, 4 rows each: 176 us, 6.3 TB/s of keys and weights,
+// 0.92 of a copy's rate. 8 x 40960 keys, 256 rows: 156 us, 1.1 PFLOP/s; there the exponentials
+// (144 us at 16 per clock and SM) are the bound.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -37,7 +41,8 @@ namespace {
 constexpr int kKwThreads = 320;
 constexpr int kKwProducer = 8, kKwMma = 9;  // warps; 0 to 7: two warpgroups
 constexpr int kKwMaxN = 256;                // query rows of one product
-constexpr int kKwMaxSlots = 8;
+constexpr int kKwMaxSlots = 8;  // tiles of keys
+constexpr int kKwQSlots = 2;    // blocks of query rows
 
 struct KwProblem {
   const float* lse;
@@ -52,7 +57,7 @@ struct KwProblem {
   int window;
   float decay, scale2, softcap2, softcap_e;  // scale and cap in log2 units
   int n_cols, blocks;                        // query rows per product, products per tile
-  int q_slots, k_slots;
+  int k_slots;
   int* status;
   uint64_t timeout_ns;
   unsigned fault_inject;
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
                                              ~uintptr_t(1023));
   const int q_box = p.n_cols * 128, q_bytes = kBoxes * q_box;  // n_cols % 16 == 0: 2048 | q_box
   uint8_t* sQ = smem;
-  uint8_t* sK = smem + p.q_slots * q_bytes;
+  uint8_t* sK = smem + kKwQSlots * q_bytes;
   __shared__ __align__(16) KwColumns columns[2];
   __shared__ uint64_t bars[11 + 2 * kKwMaxSlots];
   __shared__ uint32_t tmem_base;
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
                       nb * p.n_cols, pair);
       }
       __syncwarp();
-      qr.next(p.q_slots);
+      qr.next(kKwQSlots);
       return true;
     };
     while (walk.left > 0 && ok) {
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
     if (!ok && issue) {
       for (int i = 0; i < p.k_slots; ++i, kr.next(p.k_slots))
         wait_drain(k_full + kr.slot, kr.pass ^ 1);
-      for (int i = 0; i < p.q_slots; ++i, qr.next(p.q_slots))
+      for (int i = 0; i < kKwQSlots; ++i, qr.next(kKwQSlots))
         wait_drain(q_full + qr.slot, qr.pass ^ 1);
     }
   } else if (warp == kKwMma) {
@@ -407,7 +412,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
           kr.next(p.k_slots);
         }
         if (ok) mma_commit_warp(q_empty + qr.slot);
-        qr.next(p.q_slots);
+        qr.next(kKwQSlots);
       } else {
         for (int i = 0; i < run && ok; i += 2) {
           const int g = min(2, run - i);
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(kKwThreads, 1)
               kn.next(p.k_slots);
             }
             if (ok) mma_commit_warp(q_empty + qr.slot);
-            qr.next(p.q_slots);
+            qr.next(kKwQSlots);
           }
           kr = kn;
         }
@@ -614,16 +619,17 @@ cudaError_t launch_key_weights(const void* q, const void* k, KwProblem& p, cudaS
   p.n_cols = (R + p.blocks - 1) / p.blocks;
   p.n_cols = p.n_cols <= 16 ? 16 : (p.n_cols + 31) / 32 * 32;
   const int q_bytes = p.n_cols * D * 2, k_bytes = kTile * D * 2;
-  // Two places for query rows where blocks stream or where it leaves four tiles of keys.
-  p.q_slots = p.blocks > 1 || 2 * q_bytes + 4 * k_bytes + 1024 <= kKwSmem ? 2 : 1;
-  p.k_slots = std::min(kKwMaxSlots, (kKwSmem - 1024 - p.q_slots * q_bytes) / k_bytes);
+  // Two places for query rows leave two tiles of keys or more. (One place and four tiles for 256
+  // rows of 128 channels: 8 x 40960 keys 160 us for 156, 64 x 704 keys 56 for 54; one place for
+  // all: 64 x 704 keys and 4 rows 19.6 for 18.0.)
+  p.k_slots = std::min(kKwMaxSlots, (kKwSmem - 1024 - kKwQSlots * q_bytes) / k_bytes);
   CUtensorMap mq, mk;
   const bool paged = p.table != nullptr;
   if (!make_map_bf16_3d(&mq, q, (long long)p.B * p.Hkv, R, D, p.n_cols) ||
       !make_map_bf16_3d(&mk, k, paged ? (long long)p.num_pages * p.Hkv : (long long)p.B * p.Hkv,
                         paged ? 1 << p.shift : p.max_len, D, paged ? 1 << p.shift : kTile))
     return cudaErrorInvalidValue;
-  const size_t smem = 1024 + p.q_slots * q_bytes + p.k_slots * k_bytes;
+  const size_t smem = 1024 + kKwQSlots * q_bytes + p.k_slots * k_bytes;
   const long long tiles = (long long)p.B * p.Hkv * ((p.max_len + kTile - 1) / kTile);
   const unsigned grid = (unsigned)std::min<long long>(sm_count(), tiles);
   switch (((p.variant & ATTN_SCORE_ALIBI) ? 1 : 0) | ((p.variant & ATTN_SCORE_SOFTCAP) ? 2 : 0)) {
