@@ -372,6 +372,59 @@ def test_far_pages_of_a_long_run():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G", [0, 2048, 4096])
+def test_most_sequences_and_groups(G):
+    """As many sequences and groups as a call takes, one of them with keys that are read once; the
+    reference gathers the rows and computes in fp64 on the device."""
+    import masked_attention_gb300 as M
+    B, Hq, Hkv, D, page, n, long = 4096, 4, 2, 64, 16, 48, 640
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lens = torch.randint(0, n + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    table = torch.full((B, long // page + 3), -1, dtype=torch.int32, device="cuda")
+    table[:, :3] = torch.randperm(3 * B, generator=g, device="cuda").view(B, 3).to(torch.int32)
+    # the last two sequences share `long` keys, in pages of their own, and have 40 more each
+    shared_pages = 3 * B + torch.arange(long // page, device="cuda", dtype=torch.int32)
+    table[-2:, long // page:] = table[-2:, :3].clone()
+    table[-2:, :long // page] = shared_pages
+    lens[-2:] = long + 40
+    k, v = (torch.randn(3 * B + long // page, Hkv, page, D, generator=g, device="cuda")
+            .to(torch.bfloat16) for _ in (0, 1))
+    q = torch.randn(B, Hq, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    starts = torch.arange(G + 1, device="cuda", dtype=torch.int32) * (B // max(G, 1))
+    if G == 4096:                                # groups of one, and the last of two
+        starts[-2] = B - 2
+        starts[-3] = B - 2
+    shared = torch.zeros(G, device="cuda", dtype=torch.int32)
+    shared[-1:] = long
+    o, lse = guarded_empty((B, Hq, 1, D), torch.bfloat16), guarded_empty((B, Hq, 1), torch.float32)
+    ws = guarded_empty((M.attn_decode_shared_workspace_bytes(B, Hq, Hkv, 1, G, table.shape[1] * page,
+                                                             D),), torch.uint8)
+    groups = dict(group_starts=starts, shared_lens=shared) if G else {}
+    M.attn_decode_shared(q, k, v, o, lse, M.MASK_CAUSAL, page_table=table, page_size=page,
+                         seq_lens=lens, workspace=ws, **groups)
+    assert M.attn_check_status() == M.ATTN_OK
+    check_canaries()
+    for part, most in ((slice(0, B - 2), n), (slice(B - 2, B), long + 40)):
+        at = table[part, :-(-most // page)].long().clamp(min=0)
+        K, V = (x[at].transpose(1, 2).reshape(at.shape[0], Hkv, -1, D).double()
+                .repeat_interleave(Hq // Hkv, 1) for x in (k, v))
+        there = torch.arange(K.shape[2], device="cuda")[None] < lens[part, None]
+        s = torch.einsum("bhd,bhjd->bhj", q[part, :, 0].double(), K) * D ** -0.5
+        size = torch.einsum("bhd,bhjd->bhj", q[part, :, 0].double().abs(), K.abs()) * D ** -0.5
+        s = s.masked_fill(~there[:, None], -np.inf)
+        L = torch.logsumexp(s, -1)
+        p = torch.exp(s - torch.where(torch.isinf(L), 0, L)[..., None])
+        O, A = (torch.einsum("bhj,bhjd->bhd", p, x) for x in (V, V.abs()))
+        E = 2.0 ** -17 * size.masked_fill(~there[:, None], 0).amax(-1)
+        none = torch.isinf(L)
+        got_o, got_l = o[part, :, 0].double(), lse[part, :, 0].double()
+        assert torch.equal(torch.isinf(got_l), none) and (got_o[none] == 0).all()
+        assert (none | ((got_l - L).abs() <= E + 2.0 ** -20 * (1 + L.abs()))).all()
+        tol = 2.0 ** -8 * O.abs() + (2.0 ** -8 + 2.0 ** -18 + 4 * E[..., None]) * A
+        assert ((got_o - O).abs() <= tol).all()
+
+
+@pytest.mark.gpu
 def test_reproducible_captured_and_on_another_stream():
     """Equal bits again, on a side stream and in two graphs that share a workspace; a graph
     follows lengths and groups that change under it."""

@@ -319,3 +319,11 @@ def test_blocks_that_share_a_pair(Hkv, D, copy):
     c.check(in_place_weights=not copy)
     c = Case([20011], 6000, 6000, 0, Hkv=Hkv, D=D, kind="few", copy=copy, seed=Hkv)
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("copy", [False, True])
+def test_most_sequences(copy):
+    """As many sequences as a call takes."""
+    lens = np.random.default_rng(5).integers(0, 40, 16384)
+    Case(lens.tolist(), 12, 3, 2, Hkv=1, copy=copy, kind="few").check()

@@ -200,6 +200,14 @@ def test_rows_without_an_lse_add_nothing(kw, Sq, Hq, Hkv):
     c.check()
 
 @pytest.mark.gpu
+def test_many_sequences():
+    """More sequences than threads, most of a tile or less, empty ones among them."""
+    lens = np.random.default_rng(6).integers(0, 30, 3000)
+    lens[[5, 1500, 2999]] = 300, 129, 128
+    Case(lens.tolist(), Hq=2, Hkv=1, Sq=2).check()
+
+
+@pytest.mark.gpu
 def test_nan_of_a_visible_key_shows_there():
     c = Case([40, 150], Hq=4, Hkv=2)
     at = int(c.table[1, 5])

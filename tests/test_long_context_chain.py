@@ -252,6 +252,52 @@ def test_prompt_tokens_eviction_tokens(captured):
         tokens(range(20 + 10 * turn, 24 + 10 * turn))
 
 
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Two caches of their own on two streams: equal bits to the same calls one after the other."""
+    import masked_attention_gb300 as M
+
+    def made(seed):
+        from tests.test_decode_shared import Case
+        c = Case([(6, 900), (3, 0)], [9 * b + 1 + seed for b in range(9)], Hq=8, Hkv=2, D=128, page=64,
+                 seed=seed)
+        t = {n: getattr(c, n).cuda() for n in ("q", "k", "v", "table", "lens", "starts", "shared")}
+        n = c.table.shape[1] * 64
+        t["ws"] = torch.empty(M.attn_decode_shared_workspace_bytes(9, 8, 2, 1, 2, n, 128),
+                              dtype=torch.uint8, device="cuda")
+        t["first"] = torch.tensor([896] * 6 + [0] * 3, dtype=torch.int32, device="cuda")
+        return t, n
+
+    def run(t, n, turns=1):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        for _ in range(turns):
+            k, v = t["k"].clone(), t["v"].clone()
+            o, lse = torch.empty_like(t["q"]), torch.empty(9, 8, 1, device="cuda")
+            w = torch.zeros(9, 2, n, device="cuda")
+            kept, held = torch.zeros(9, 2, 20, **i32), torch.zeros(9, **i32)
+            freed, info = torch.full((99,), -1, **i32), torch.zeros(2, **i32)
+            cache = dict(page_table=t["table"], page_size=64, seq_lens=t["lens"])
+            M.attn_decode_shared(t["q"], k, v, o, lse, M.MASK_CAUSAL, group_starts=t["starts"],
+                                 shared_lens=t["shared"], workspace=t["ws"], **cache)
+            M.attn_key_weights(t["q"], k, lse, w, M.MASK_CAUSAL, previous=w, **cache)
+            M.attn_cache_evict(w, t["lens"], k, v, t["table"], w, kept, held, freed, info, page_size=64,
+                               recent=3, starts=t["first"])
+        return o, lse, w, kept, held, freed, info, k, v
+
+    both = [made(1), made(2)]
+    refs = [run(*x) for x in both]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in both], []
+    for s, x in zip(streams, both):
+        with torch.cuda.stream(s):
+            outs.append(run(*x, turns=8))
+    torch.cuda.synchronize()
+    assert M.attn_check_status() == M.ATTN_OK
+    for ref, out in zip(refs, outs):
+        for a, b in zip(ref, out):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_chain_sizes():
     """Whole pages are shared, and own keys pass what eviction keeps: a page is given up."""
     own = [30 + 3, 17 + 3, 3 + 3]
