@@ -57,7 +57,9 @@ constexpr int kShMaxRows = 16;
 constexpr int kShKeys = 64;       // keys of a tile
 // What counts in the dealing out: a tile of a sequence's own keys, of shared ones (whose rows keep
 // all warps busy), and a piece's start and end. (64 sequences behind 32768 keys, 1 key each, with
-// kShCost 12, 16, 24, 32: 70, 68, 61, 61 us; kShShared 7 to 9 makes no difference, 13 costs 15 %.)
+// kShCost 12, 16, 24, 32: 70, 68, 61, 61 us; kShShared 7 to 9 makes no difference, 13 costs 15 %.
+// Six ragged batches with a soft-cap, 100 to 130 us: kShCost 16 takes 2 % less, 48 3 % more,
+// kShShared 12 5 % more.)
 constexpr int kShOwn = 8, kShShared = 8, kShCost = 24;
 constexpr int kShPlanThreads = 256;
 constexpr int kShPlanWarps = kShPlanThreads / 32;
