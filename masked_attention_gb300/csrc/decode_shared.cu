@@ -25,7 +25,8 @@
 // tells the others through shared memory and copies (TMA); warp 5 issues S = Q K^T, of the next
 // tile as soon as the softmax has this one's scores in registers; warp 6 O += P V (P: bf16 in
 // tensor memory, in two places of its own, rounded to 8 bits as in the other bf16 calls; its sum
-// is of the unrounded values). (One warp for both products was what a tile waited for: 1900
+// is of the unrounded values) and, while it waits for P, zeroes the values of keys that no row
+// sees. (One warp for both products was what a tile waited for: 1900
 // cycles, of which 900 its waits.) Tiles of 64 keys, not 128: five K or V tiles then fit beside Q
 // twice per SM instead of two, so that the next ones arrive while this one is worked on.
 //
@@ -382,6 +383,43 @@ struct ShMsg {  // a run of tiles, as the producer tells it
   int key0, klo, khi, seq, nseq, shared, h;
   long long slot;  // of its partial result
 };
+
+// Of 32 keys those from `from` to `to` - 1, a bit each.
+__device__ __forceinline__ unsigned sh_span(int from, int to) {
+  from = max(from, 0);
+  to = min(to, 32);
+  return from < to ? (~0u >> (32 - (to - from))) << from : 0u;
+}
+
+// Of the 32 keys from j0 on those that some row of a block of sequences sees. (A sequence's rows
+// see one run of keys, all of them together.)
+__device__ __forceinline__ unsigned sh_seen(const ShProblem& p, int seq, int nseq, int j0) {
+  unsigned mine = 0;
+  for (int i = threadIdx.x & 31; i < nseq; i += 32) {
+    const int len = sh_len(p, seq + i);
+    mine |= sh_span(sh_low(p, len) - j0, len - j0);
+  }
+  return __reduce_or_sync(0xffffffffu, mine);
+}
+
+// Whether a block's sequences may leave some of the keys [from, to) to nobody: they end apart, so
+// with a window their runs of keys may lie apart, too. (Runs that all meet at one place do not.
+// Asked once per piece: with sh_seen() for every tile 64 sequences behind 8192 keys, window 4096,
+// took 34 to 37 us instead of 32.)
+__device__ __forceinline__ bool sh_apart(const ShProblem& p, int seq, int nseq, int from, int to) {
+  int low = INT_MAX, high = 0, near = INT_MAX, far = 0;  // least and largest start and end
+  for (int i = threadIdx.x & 31; i < nseq; i += 32) {
+    const int len = sh_len(p, seq + i), at = sh_low(p, len);
+    if (len == 0) continue;
+    low = min(low, at);
+    high = max(high, at);
+    near = min(near, len);
+    far = max(far, len);
+  }
+  constexpr unsigned all = 0xffffffffu;
+  return __reduce_max_sync(all, high) > __reduce_min_sync(all, near) ||
+         __reduce_min_sync(all, low) > from || __reduce_max_sync(all, far) < to;
+}
 
 __device__ __forceinline__ bool sh_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
   const uint32_t hint = wd.timeout_ns < 1000000ull ? (uint32_t)wd.timeout_ns : 1000000u;
@@ -762,8 +800,31 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     bool ok = true;
     ShMsg m;
     while (ok && next_msg(m, ok)) {
+      const bool apart = m.shared && (p.variant & ATTN_MASK_WINDOW) &&
+                         sh_apart(p, m.seq, m.nseq, max(m.klo, m.key0),
+                                  min(m.khi, m.key0 + m.tiles * kShKeys));
       for (int t = 0; t < m.tiles && ok; ++t) {
         ok = sh_wait(v_full + vr.slot, vr.pass, wd);
+        // Values of keys that no row of the block sees are zeroed before their product (P is 0
+        // there, and they may be anything).
+        const int j0 = m.key0 + t * kShKeys;
+        if (ok && (apart || j0 < m.klo || j0 + kShKeys > m.khi)) {
+#pragma unroll 1
+          for (int at = 0; at < kShKeys; at += 32) {
+            unsigned seen = sh_span(m.klo - j0 - at, m.khi - j0 - at);
+            if (apart) seen &= sh_seen(p, m.seq, m.nseq, j0 + at);
+            if (seen == ~0u) continue;
+            uint8_t* rows = sV + vr.slot * C::kTileBytes + at * 128 + lane * 16;
+#pragma unroll
+            for (int r = 0; r < 32; r += 4)  // four rows of 128 bytes
+              if (!(seen >> (r + lane / 8) & 1))
+#pragma unroll
+                for (int bx = 0; bx < C::kBoxes; ++bx)
+                  *reinterpret_cast<uint4*>(rows + bx * C::kBox + r * 128) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         if (ok && t == 0) {  // O of the piece before has been read
           ok = sh_wait(o_free, o_pass ^ 1, wd);
           o_pass ^= 1;
@@ -798,7 +859,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
     const bool causal = p.variant & ATTN_MASK_CAUSAL, windowed = p.variant & ATTN_MASK_WINDOW;
     // the row's sequence of the block, its head of the group and its token
     const int rq = t / p.R, rr = t - rq * p.R, rg = rr / p.Sq, rs = rr - rg * p.Sq;
-    ShRing vr;
     uint32_t s_pass = 0, pv_count = 0;  // pv_count: tiles before this one
     bool ok = true;
     ShMsg msg;
@@ -844,21 +904,6 @@ __global__ void __launch_bounds__(kShThreads, kShPerSm)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_free);
-        if (j0 < msg.klo || j0 + kShKeys > msg.khi) {
-          // values of keys that no row sees are zeroed before their product (P is 0 there, and
-          // they may be anything)
-          ok = sh_wait(v_full + vr.slot, vr.pass, wd);
-          if (!ok) break;
-          const int key = j0 + (t & 63), bx = t >> 6;
-          if ((key < msg.klo || key >= msg.khi) && bx < C::kBoxes) {
-            uint4* v = reinterpret_cast<uint4*>(sV + vr.slot * C::kTileBytes + bx * C::kBox +
-                                                (t & 63) * 128);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
-        vr.next(C::kVSlots);
         if (active) {
           sh_modify<SCORE>(p, slope2, pos - j0, mine, x);
           if (!whole) {

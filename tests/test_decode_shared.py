@@ -322,6 +322,45 @@ def test_what_no_row_sees_changes_nothing_behind_a_long_run(kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("groups,own,kw", [
+    ([(3, 600), (2, 0)], [30, 100, -60, 70, 5], dict(window=40)),
+    ([(3, 600)], [30, 100, -60], dict(window=40, Sq=3, causal=False)),
+    # holes of whole tiles, one of them from a tile's start; a sequence that is empty
+    ([(4, 1216)], [-576, 5, -100, -1216], dict(window=64)),
+    ([(4, 1216)], [-577, 40, -130, -300], dict(window=1, softcap=20.0)),
+    # several row blocks: what one of them sees the other does not
+    ([(1, 100), (21, 900)], [9] + [-40 * b for b in range(21)], dict(window=7, Hq=16, Hkv=1)),
+    ([(40, 700)], [3 * b - 90 for b in range(40)], dict(window=2, Hq=8, Hkv=2, alibi=True)),
+    # the sequences of each row block see one run, the blocks' runs lie apart
+    ([(16, 900)], [-400 - b for b in range(8)] + [5 - 5 * b for b in range(8)],
+     dict(window=40, Hq=16, Hkv=1)),
+])
+def test_shared_keys_between_the_windows_change_nothing(groups, own, kw, page, D):
+    """Sequences of a group that end apart, each with a window: NaN and infinities in every key
+    that none of them sees, between their windows too."""
+    c = Case(groups, own, page=page, D=D, seed=7, **kw)
+    a, la = c.check()
+    Sq, window = c.shape[3], c.kw["window"]
+    seen = set()
+    for b, n in enumerate(c.lens.tolist()):
+        g = int(c.group[b])
+        for j in range(max(0, n - Sq - window + 1), n):
+            # a shared key is read from the first sequence's pages
+            of = {b, int(c.starts[g])} if j < int(c.shared[g]) else {b}
+            seen |= {(int(c.table[x, j // page]), j % page) for x in of}
+    for at in range(len(c.k)):
+        for r in range(page):
+            if (at, r) not in seen:
+                c.k[at, :, r] = float("nan") if r % 2 else float("inf")
+                c.v[at, :, r] = float("inf") if r % 3 else float("nan")
+    o, lse = c.run()
+    assert np.array_equal(o.double().cpu().numpy(), a)
+    assert np.array_equal(lse.double().cpu().numpy(), la)
+
+
+@pytest.mark.gpu
 def test_nan_of_a_key_that_is_read_once_shows():
     c = Case([(3, 576)], [10, 20, 30])
     c.k[int(c.table[0, 3]), 1, 2] = float("nan")         # a shared key of head pair 1
