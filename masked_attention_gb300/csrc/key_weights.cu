@@ -117,6 +117,14 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// One column, read and waited for.
+__device__ __forceinline__ float tmem_column(uint32_t taddr) {
+  uint32_t x;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
+  return __uint_as_float(x);
+}
+
 __device__ __forceinline__ bool kw_wait(uint64_t* bar, uint32_t parity, const Watchdog& wd) {
   // a sleeping try first: the timer that bounds the wait takes long to read
   const uint32_t hint = wd.timeout_ns < 1000000ull ? (uint32_t)wd.timeout_ns : 1000000u;
@@ -575,7 +583,12 @@ __global__ void __launch_bounds__(kKwThreads, 1)
             tmem_ld_wait_regs(v0);
             if (c < p.n_cols) kw_add<SCORE, kMask, 32>(p, col, c, j, len, v0, sum);
           };
-          if (whole && !skip) columns_sum(std::false_type{});
+          bool plain = whole && !skip;
+          // Columns behind the head's rows hold zeros times the key: NaN where it has an infinity,
+          // which the masked form leaves out (they have no position). The last one tells.
+          if (plain && (nb + 1) * p.n_cols > R)
+            plain = !__any_sync(0xffffffffu, isnan(tmem_column(cols + p.n_cols - 1)));
+          if (plain) columns_sum(std::false_type{});
           else columns_sum(std::true_type{});
           tc_fence_before();
           __syncwarp();

@@ -221,6 +221,55 @@ def test_nan_of_a_visible_key_shows_there():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("paged", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(alibi=True), dict(window=690)])
+@pytest.mark.parametrize("Sq,Hq,Hkv", [(1, 1, 1), (1, 8, 2), (5, 8, 2), (37, 7, 1), (16, 16, 1)])
+def test_infinite_visible_keys(Sq, Hq, Hkv, kw, D, paged):
+    """Keys with a channel of -infinity or +infinity, all queries positive there, in whole tiles and
+    in the last one: their score is that infinity (with a soft-cap -cap or cap), so their weight is
+    0 or infinity (sum of exp(+-cap - LSE)), wherever they lie and however many rows a head has;
+    other keys keep their bits."""
+    c = Case([700, 640], Hq, Hkv, Sq, D, 32, seed=9, paged=paged, **kw)
+    c.q[..., 3] = 0.25 + c.q[..., 3].abs()
+    c.lse = c.oracle_lse()
+    ref = c.run("same", 0.5)
+    low, high = (12, 300, 530, 645), (77, 310, 650)
+    for j in low + high:
+        x = -np.inf if j in low else np.inf
+        for b, n in enumerate(c.lens.tolist()):
+            if j >= n:
+                continue
+            if paged:
+                c.k[int(c.table[b, j // 32]), :, j % 32, 3] = x
+            else:
+                c.k[b, :, j, 3] = x
+    w = c.run("same", 0.5)
+    lse = c.lse.double().numpy()
+    old = 0.5 * c.previous.double().numpy()
+    hit = torch.zeros(w.shape, dtype=torch.bool, device="cuda")
+    for j in low + high:
+        for b, n in enumerate(c.lens.tolist()):
+            for h in range(Hkv if j < n else 0):
+                hit[b, h, j] = True
+                got = float(w[b, h, j])
+                # rows of the head that see the key: positions i with j <= i, i - j < window
+                i = n - Sq + np.arange(Sq)
+                see = (j <= i) & ((i - j < c.kw["window"]) | (c.kw["window"] == 0))
+                L = lse[b, h * (Hq // Hkv):(h + 1) * (Hq // Hkv)][:, see]
+                if c.kw["softcap"]:
+                    s = -20.0 if j in low else 20.0
+                    # E of the module's tolerance without the product, which the cap swallows
+                    tol = np.exp(s - L).sum() * 2.0 ** -16 * (1 + 5 * 20 + np.abs(L).max(initial=0))
+                    assert abs(got - old[b, h, j] - np.exp(s - L).sum()) <= tol + 2.0 ** -23 * got, (b, h, j)
+                elif j in low or not L.size:
+                    assert got == np.float32(old[b, h, j]), (b, h, j, got)
+                else:
+                    assert got == np.inf, (b, h, j, got)
+    assert torch.equal(w[~hit], ref[~hit])
+
+
+@pytest.mark.gpu
 def test_pages_outside_the_pool_and_lengths_outside_the_bound():
     c = Case([100, 90, 30])
     c.table[0, 2], c.table[1, 0], c.table[2, 1] = -5, len(c.k), 2 ** 31 - 1
