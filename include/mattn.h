@@ -506,9 +506,11 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
  *                ascending, then -1
  *   new_lens     int32 [B]   first + min(n, keep)
  *   freed        int32 [max_freed]  the pages that the sequences no longer use, one sequence
- *                after the other: entries of page_table from ceil(new_lens / page_size) on in
+ *                after the other (a page that several gave up, once for each): entries of page_table from ceil(new_lens / page_size) on in
  *                place, from first / page_size on with new_table, up to ceil(seq_lens /
- *                page_size). Those past max_freed are dropped; other entries stay
+ *                page_size). An entry that new_table has in the same place, below
+ *                ceil(new_lens / page_size), is in use and not listed. Those past max_freed are
+ *                dropped; other entries stay
  *   info         int32 [2]   pages freed, sequences that gave up keys
  * A page outside the pool reads as zeros and is not written. In place, a page that several
  * sequences hold must lie among their first keys (whole pages before `first`); with new_table,

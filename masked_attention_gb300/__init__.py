@@ -945,8 +945,8 @@ def attn_cache_evict(weights, seq_lens, k, v, page_table, weights_out, kept, new
     (fp32 [B, Hkv, L]), that many in all. Their rows in the pools ``k``, ``v`` (bf16 [num_pages,
     Hkv, page, D]) move together in order, in place or, with ``new_table`` [B, pages], into its
     pages. Writes ``weights_out`` (may be ``weights``), ``kept`` [B, Hkv, keep] (old positions,
-    -1 past the last), ``new_lens`` [B], ``freed`` (page ids no longer used) and ``info`` [2]:
-    pages freed, sequences cut. All int32. See include/mattn.h."""
+    -1 past the last), ``new_lens`` [B], ``freed`` (page ids no longer used: not those that
+    ``new_table`` has in the same place) and ``info`` [2]: pages freed, sequences cut. All int32. See include/mattn.h."""
     w = "attn_cache_evict"
     dev = _device(w, "weights", weights)
     i32, f32, bf16 = _torch.int32, _torch.float32, _torch.bfloat16

@@ -16,7 +16,8 @@
 // first batch to the last, alone or with the others of its cluster, behind the cluster's barrier.
 // The next batch's rows are read while the last one's are written, and the places of the one
 // after it are looked up meanwhile, one row per thread. Into other pages no order is needed and
-// batches are dealt out too.
+// batches are dealt out too; there this kernel's first blocks list the pages that go, which takes
+// the tables' entries.
 //
 // 8 sequences of 32768 keys, 8 heads of 128 channels, 8192 kept: 126 us, 4.3 TB/s of the 545 MB
 // that must move. 32 of 8000, 4000 kept: 200 us, 5.3 TB/s. Rows in flight are the bound: with half
@@ -68,6 +69,7 @@ struct EvictArgs {
   int move_cluster;    // blocks that share the batches of a move in place
   int splits, piece;   // the move: parts of a row of `piece` bytes
   int chunks;          // the move into other pages: runs of positions
+  int lists, list_run; // blocks that list the freed pages first, sequences of each
 };
 
 struct EvictSeq {
@@ -85,7 +87,8 @@ __device__ __forceinline__ EvictSeq evict_seq(const EvictArgs& a, int b) {
   return s;
 }
 
-// Pages of a sequence that it no longer uses: entries [stay, have) of its table row.
+// Pages of a sequence that it no longer uses: entries [stay, have) of its table row, but for those
+// that a new table keeps (evict_list).
 __device__ __forceinline__ int2 evict_pages(const EvictArgs& a, const EvictSeq& s) {
   const int up = (1 << a.shift) - 1;
   const int have = (s.len + up) >> a.shift;
@@ -135,6 +138,7 @@ __device__ __forceinline__ int4 cluster_read4(const int* p, int rank) {
 }
 
 // Sum over the block of `mine`, and of those of the threads before: by a scan of warp sums.
+template <int WARPS = kSelWarps>
 __device__ __forceinline__ int block_before(int mine, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = mine;
@@ -146,7 +150,7 @@ __device__ __forceinline__ int block_before(int mine, int* warp_sums, int& total
   __syncthreads();  // warp_sums of an earlier call have been read
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  int w = lane < kSelWarps ? warp_sums[lane] : 0;
+  int w = lane < WARPS ? warp_sums[lane] : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, w, d);
@@ -167,7 +171,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int b = pair / a.Hkv, h = pair % a.Hkv;
   early_start();
   const EvictSeq s = evict_seq(a, b);
-  if (h == 0 && rank == 0) {  // the sequence's length and its pages that go
+  if (h == 0 && rank == 0) {  // the sequence's length and, in place, its pages that go
+    if (tid == 0) a.new_lens[b] = s.new_len();
+  }
+  if (h == 0 && rank == 0 && !a.new_table) {
     int gone = 0, cuts = 0, total, all_cuts;
     const int upto = b == a.B - 1 ? a.B : b;
     for (int i = tid; i < upto; i += kSelThreads) {
@@ -183,12 +190,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     for (int i = tid; i < n; i += kSelThreads)
       if (total + i < a.max_freed && MATTN_IN_BOUNDS(kSiteEvict, pages.x + i, a.per))
         a.freed[total + i] = a.table[(size_t)b * a.per + pages.x + i];
-    if (tid == 0) {
-      a.new_lens[b] = s.new_len();
-      if (b == a.B - 1) {
-        a.info[0] = total + n;
-        a.info[1] = all_cuts;
-      }
+    if (tid == 0 && b == a.B - 1) {
+      a.info[0] = total + n;
+      a.info[1] = all_cuts;
     }
   }
   int* kept = a.kept + (size_t)pair * a.keep;
@@ -335,10 +339,62 @@ __device__ __forceinline__ uint2 evict_way(const EvictArgs& a, const EvictSeq& s
   return make_uint2(evict_row(a, a.table, a.per, b, h, src), dst);
 }
 
+// With a new table: the pages that go, of list_run sequences from b on. An entry that the new table
+// has in the same place, among those that it still uses, stays; so those of the sequences before
+// are counted entry by entry.
+__device__ __noinline__ void evict_list(const EvictArgs& a, int b) {
+  constexpr int kWarps = kMoveThreads / 32;
+  __shared__ int sums[kWarps];
+  const int tid = threadIdx.x;
+  auto named = [&](const EvictSeq& s) {
+    return min(a.new_per, (s.new_len() + (1 << a.shift) - 1) >> a.shift);
+  };
+  auto same = [&](int i, int page) {
+    return MATTN_IN_BOUNDS(kSiteEvict, page, a.per) &&
+           a.new_table[(size_t)i * a.new_per + page] == a.table[(size_t)i * a.per + page];
+  };
+  const int end = min(b + a.list_run, a.B), upto = end == a.B ? a.B : b;
+  int team = 1;  // threads of a sequence: as many as there are, up to a warp
+  while (team < 32 && 2 * team * upto <= kMoveThreads) team *= 2;
+  int gone = 0, cuts = 0, at, all_cuts;
+  for (int i = tid / team; i < upto; i += kMoveThreads / team) {
+    const EvictSeq s = evict_seq(a, i);
+    const int2 pages = evict_pages(a, s);
+    if (tid % team == 0) cuts += s.cut;
+    if (i >= b) continue;
+    if (tid % team == 0) gone += pages.y - pages.x;
+    const int to = named(s);
+#pragma unroll 4
+    for (int p = pages.x + tid % team; p < to; p += team) gone -= same(i, p);
+  }
+  block_before<kWarps>(gone, sums, at);
+  block_before<kWarps>(cuts, sums, all_cuts);
+  for (int i = b; i < end; ++i) {
+    const EvictSeq s = evict_seq(a, i);
+    const int2 pages = evict_pages(a, s);
+    const int to = named(s);
+    for (int p0 = pages.x; p0 < pages.y; p0 += kMoveThreads) {
+      const int p = p0 + tid;
+      const bool goes = p < pages.y && !(p < to && same(i, p));
+      int n;
+      const int place = at + block_before<kWarps>(goes, sums, n);
+      if (goes && place < a.max_freed && MATTN_IN_BOUNDS(kSiteEvict, p, a.per))
+        a.freed[place] = a.table[(size_t)i * a.per + p];
+      at += n;
+    }
+  }
+  if (tid == 0 && end == a.B) {
+    a.info[0] = at;
+    a.info[1] = all_cuts;
+  }
+}
+
 __global__ void __launch_bounds__(kMoveThreads, kMoveBlocks) evict_move_kernel(const EvictArgs a) {
   __shared__ uint2 ways[2][kMoveThreads];  // of a batch's rows: at most kMoveThreads
   early_start();
-  const int ranks = a.move_cluster, rank = blockIdx.x % ranks, unit = blockIdx.x / ranks;
+  if ((int)blockIdx.x < a.lists) return evict_list(a, blockIdx.x * a.list_run);
+  const int ranks = a.move_cluster, block = blockIdx.x - a.lists;
+  const int rank = block % ranks, unit = block / ranks;
   const int parts = 2 * a.splits * a.chunks + 1;
   const int pair = unit / parts, part = unit % parts;
   const int b = pair / a.Hkv, h = pair % a.Hkv;
@@ -536,6 +592,11 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
   // eight 60 us.)
   const long long want = 3 * sms;
   a.move_cluster = a.splits = a.chunks = 1;
+  // Every block that lists freed pages counts those of all sequences before its own, so up to 128
+  // of them. (1024 sequences of 500 keys, one head, pages of 16: 64, 128, 256 blocks 58, 54, 58 us;
+  // 8192 of 200 keys 313, 271, 277 us.)
+  a.list_run = (B + 127) / 128;
+  a.lists = new_table ? (B + a.list_run - 1) / a.list_run : 0;
   const int batch = kMoveThreads * 16 / a.row_bytes * kMoveUnroll;
   const long long most = ((long long)std::min(max_len, keep) + page_size + batch - 1) / batch;
   if (new_table) {
@@ -558,7 +619,7 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
                                          a.select_cluster, kSelThreads, smem, s, a));
   if (st != ATTN_OK) return st;
   const unsigned blocks =
-      (unsigned)(pairs * (2 * a.splits * a.chunks + 1) * a.move_cluster);
+      (unsigned)(a.lists + pairs * (2 * a.splits * a.chunks + 1) * a.move_cluster);
   return cuda_status(launch_early_clusters(evict_move_kernel, blocks, a.move_cluster, kMoveThreads, 0,
                                            s, a));
 }

@@ -102,8 +102,11 @@ def evict(weights, lens, starts, keep, recent, k, v, table, page, new_table, wei
         dest = table if new_table is None else new_table
         begin = first if new_table is None else first // page * page
         have = -(-n // page)
-        stay = -(-int(new_lens[b]) // page) if new_table is None else first // page
-        gone += [int(x) for x in table[b, stay:have]]
+        used = -(-int(new_lens[b]) // page)
+        for p in range(used if new_table is None else first // page, have):
+            # a page that the new table names in the same place, among those it uses, is kept
+            if new_table is None or p >= min(used, new_table.shape[1]) or new_table[b, p] != table[b, p]:
+                gone.append(int(table[b, p]))
         for h in range(Hkv):
             hold = list(range(first, n))
             if not fits:

@@ -327,3 +327,76 @@ def test_most_sequences(copy):
     """As many sequences as a call takes."""
     lens = np.random.default_rng(5).integers(0, 40, 16384)
     Case(lens.tolist(), 12, 3, 2, Hkv=1, copy=copy, kind="few").check()
+
+
+def pages_of(c, b, n):
+    """Entries of sequence b's table row that hold its first n keys."""
+    return -(-n // c.page)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_pages_that_the_new_table_keeps_are_not_freed(page):
+    """A sequence that is not cut and keeps its pages, one whose first held keys stay where they
+    are, and one whose new table names an old page that it no longer reaches."""
+    c = Case([300, 1000, 900, 0, 700], 500, 40, 3, page=page, copy=True, seed=11)
+    c.weights[1] = c.weights[2] = c.weights[4] = -np.arange(c.L)  # the first keys are the heaviest
+    # 0: not cut, every page is kept. 1: pages of the keys that stay in front are kept
+    c.new_table[0, :pages_of(c, 0, 300)] = c.table[0, :pages_of(c, 0, 300)]
+    same = (3 + 500 - 40) // page
+    c.new_table[1, :same] = c.table[1, :same]
+    # 2: names the page behind the last one that its 503 keys reach
+    at = pages_of(c, 2, 503)
+    c.new_table[2, at] = c.table[2, at]
+    out = c.check()
+    gone = set(out["freed"].cpu().tolist()[:int(out["info"][0])])
+    assert not gone & set(c.table[0, :pages_of(c, 0, 300)].tolist() + c.table[1, :same].tolist())
+    assert c.table[2, at] in gone and set(c.table[4, :pages_of(c, 4, 700)].tolist()) <= gone
+    c.check(in_place_weights=True)
+    # all of it in a short list, and a new table that ends before its sequences do
+    c.max_freed = 7
+    c.check()
+    c.new_table = np.ascontiguousarray(c.new_table[:, :2])
+    c.check()
+
+
+@pytest.mark.gpu
+def test_old_table_as_the_new_one():
+    """Nothing is cut and both tables are equal: nothing moves, nothing is freed, also where
+    entries name no page."""
+    c = Case([100, 31, 0, 64], 200, 10, 2, copy=True)
+    c.new_table = c.table.copy()
+    c.new_table[0, 3] = c.table[0, 3] = -1
+    out = c.check()
+    assert out["info"].tolist() == [0, 0] and (out["freed"] == -3).all()
+    assert torch.equal(out["k"].cpu(), c.k) and torch.equal(out["v"].cpu(), c.v)
+
+
+@pytest.mark.gpu
+def test_kept_pages_of_many_sequences():
+    """More sequences than threads: some keep all, some a part, some no page."""
+    rng = np.random.default_rng(12)
+    c = Case(rng.integers(0, 150, 1500).tolist(), 60, 9, 20, Hkv=1, copy=True, kind="few", seed=12)
+    c.weights[:] = -np.arange(c.L)
+    for b, n in enumerate(c.lens.tolist()):
+        held = min(n, 20 + 60)
+        stay = pages_of(c, b, n) if n <= 80 else (20 + 60 - 9) // 16
+        same = int(rng.integers(0, stay + 1)) if b % 3 else stay
+        c.new_table[b, :same] = c.table[b, :same]
+        assert pages_of(c, b, held) <= c.new_table.shape[1]
+    out = c.check()
+    assert 0 < int(out["info"][0]) < int((-(-c.lens // 16)).sum())
+
+
+def test_oracle_keeps_pages_that_the_new_table_names():
+    w = np.arange(48, 0, -1, dtype=np.float32).reshape(1, 1, 48)
+    k = np.arange(6 * 16).reshape(6, 1, 16, 1).astype(np.int16)
+    args = w, [40], [0], 20, 2, k, k, np.array([[1, 2, 3]]), 16
+    free = np.full(4, -1, np.int32)
+    # the first page stays: keys 0 to 15 are held and do not move
+    _, _, lens, freed, info, k2, _ = evict(*args, np.array([[1, 4]]), w, free)
+    assert lens.tolist() == [20] and freed.tolist() == [2, 3, -1, -1] and info.tolist() == [2, 1]
+    assert k2[4, 0, :4, 0].tolist() == [32, 33, 54, 55] and np.array_equal(k2[1], k[1])
+    # an old page behind the last one in use is freed wherever it is named
+    _, _, _, freed, info, _, _ = evict(*args, np.array([[4, 5, 3]]), w, free)
+    assert freed.tolist() == [1, 2, 3, -1] and info.tolist() == [3, 1]
