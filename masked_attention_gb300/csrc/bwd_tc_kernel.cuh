@@ -1126,14 +1126,11 @@ cudaError_t launch_one(const BwdArgs& a, const CUtensorMap& mq, const CUtensorMa
   // setmaxnreg.inc draws on the registers the launch holds: refuse to launch
   // if the compiled register count cannot cover the split (the increase
   // would wait forever)
-  static int regs = -1;
-  static std::once_flag regs_once;
-  std::call_once(regs_once, [] {
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, bwd_kernel<D, SCORE, MODE, GENERAL, F16>) == cudaSuccess)
-      regs = fa.numRegs;
-  });
-  if (regs < 0 || 256LL * kRegsCompute + 128LL * kRegsOther > (long long)regs * kThreads)
+  static KernelRegs known;
+  int regs = 0;
+  const cudaError_t e = known.get(bwd_kernel<D, SCORE, MODE, GENERAL, F16>, regs);
+  if (e != cudaSuccess) return e;
+  if (256LL * kRegsCompute + 128LL * kRegsOther > (long long)regs * kThreads)
     return cudaErrorInvalidConfiguration;
   const int grid = units < sm_count() ? units : sm_count();
   if (grid == 0) return cudaSuccess;

@@ -1182,14 +1182,13 @@ template <int D, int SCORE>
 cudaError_t launch_main(const ShMaps& m, const ShProblem& p, cudaStream_t s) {
   using C = ShCfg<D>;
   static DeviceOnce ready;
-  const cudaError_t e = ready.allow_smem(decode_shared_kernel<D, SCORE>, C::kSmem);
+  cudaError_t e = ready.allow_smem(decode_shared_kernel<D, SCORE>, C::kSmem);
   if (e != cudaSuccess) return e;
   // setmaxnreg.inc draws on the registers that the block holds: refuse where they do not cover
   // the split (the increase would wait for ever)
-  static const int regs = [] {
-    cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, decode_shared_kernel<D, SCORE>) == cudaSuccess ? fa.numRegs : 0;
-  }();
+  static KernelRegs known;
+  int regs = 0;
+  if ((e = known.get(decode_shared_kernel<D, SCORE>, regs)) != cudaSuccess) return e;
   if (128 * (kShRegsSoftmax + kShRegsOther) > regs * kShThreads) return cudaErrorInvalidConfiguration;
   return launch_early(decode_shared_kernel<D, SCORE>, (unsigned)p.ctas, kShThreads, C::kSmem, s,
                       m.qs, m.q1, m.k, m.v, p);

@@ -1229,15 +1229,11 @@ cudaError_t launch_typed(const FwdProblem& p, cudaStream_t stream) {
   // setmaxnreg.inc draws on the registers the launch holds: refuse to launch
   // if the compiled register count cannot cover the split (the increase
   // would wait forever)
-  static int regs = -1;
-  static std::once_flag regs_once;
-  std::call_once(regs_once, [] {
-    cudaFuncAttributes fa{};
-    if (cudaFuncGetAttributes(&fa, fwd_tc_kernel<D, SCORE, PAGED>) == cudaSuccess)
-      regs = fa.numRegs;
-  });
-  if (regs < 0 || 2LL * kSoftmaxThreads * kRegsSoftmax + 128LL * kRegsOther >
-                      (long long)regs * kThreads)
+  static KernelRegs known;
+  int regs = 0;
+  const cudaError_t e = known.get(fwd_tc_kernel<D, SCORE, PAGED>, regs);
+  if (e != cudaSuccess) return e;
+  if (2LL * kSoftmaxThreads * kRegsSoftmax + 128LL * kRegsOther > (long long)regs * kThreads)
     return cudaErrorInvalidConfiguration;
   const int units = count_units<D, PAGED>(p);
   const int grid = units < sm_count() ? units : sm_count();

@@ -82,6 +82,23 @@ class DeviceOnce {
   std::atomic<unsigned long long> done_{0};
 };
 
+// Registers per thread of a kernel, asked once. A question that fails is asked again by the next
+// call: its error is that call's.
+class KernelRegs {
+ public:
+  template <typename Kernel>
+  cudaError_t get(Kernel* kernel, int& regs) {
+    if ((regs = known_.load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    cudaFuncAttributes fa{};
+    const cudaError_t e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel));
+    if (e == cudaSuccess) known_.store(regs = fa.numRegs, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  std::atomic<int> known_{0};
+};
+
 // Launches a kernel that begins with early_start(): it may be set up before the
 // stream's previous kernel has ended, and waits for that end. Blocks in clusters of
 // `cluster` (a divisor of `grid`, at most 8).
