@@ -427,9 +427,10 @@ size_t attn_decode_q4_workspace_bytes(int B, int Hq, int Hkv, int Sq, int max_le
 
 /* Decode over a bf16 paged cache for sequences of their own lengths, groups of which share
  * their first keys (a prompt behind many requests): O and LSE of every sequence over its own
- * keys and, with one read for all, over those that its group shares. Arguments as for
- * attn_decode_q4 (no sinks), with k and v bf16 page pools [num_pages][Hkv][page_size][D] (p:
- * page_table, page_size, pages_per_seq, num_pages) and
+ * keys and those that its group shares, which (512 of them or more) are read once for up to 128
+ * query rows of a key/value head. Arguments as for attn_decode_q4 (no sinks), with k and v bf16
+ * page pools [num_pages][Hkv][page_size][D] (p: page_table, page_size, pages_per_seq, num_pages)
+ * and
  *   group_starts  device int32 [G + 1], ascending: group g is sequences group_starts[g] to
  *                 group_starts[g + 1] - 1 (entries are cut to [0, B], and one below an earlier
  *                 one counts as that); sequences in no group share nothing
@@ -506,11 +507,11 @@ attn_status attn_key_weights(const void* q, const void* k, const float* lse, con
  *                ascending, then -1
  *   new_lens     int32 [B]   first + min(n, keep)
  *   freed        int32 [max_freed]  the pages that the sequences no longer use, one sequence
- *                after the other (a page that several gave up, once for each): entries of page_table from ceil(new_lens / page_size) on in
- *                place, from first / page_size on with new_table, up to ceil(seq_lens /
- *                page_size). An entry that new_table has in the same place, below
- *                ceil(new_lens / page_size), is in use and not listed. Those past max_freed are
- *                dropped; other entries stay
+ *                after the other (a page that several gave up, once for each): entries of
+ *                page_table from ceil(new_lens / page_size) on in place, from first / page_size
+ *                on with new_table, up to ceil(seq_lens / page_size). An entry that new_table has
+ *                in the same place, below ceil(new_lens / page_size), is in use and not listed.
+ *                Those past max_freed are dropped; other entries stay
  *   info         int32 [2]   pages freed, sequences that gave up keys
  * A page outside the pool reads as zeros and is not written. In place, a page that several
  * sequences hold must lie among their first keys (whole pages before `first`); with new_table,

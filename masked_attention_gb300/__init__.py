@@ -880,8 +880,9 @@ def attn_decode_shared(q, k, v, o, lse, variant: int = 0, *, page_table, page_si
     against the ``seq_lens`` [B] int32 tokens that ``page_table`` [B, pages_per_seq] places in
     the pools ``k``, ``v`` [num_pages, Hkv, page, D]. Sequences ``group_starts[g]`` to
     ``group_starts[g + 1] - 1`` (int32 [G + 1]) hold the same first ``shared_lens[g]`` (int32
-    [G]) keys in the same pages, which are read once for all of them. ``max_len`` (default: all
-    the table holds) bounds seq_lens. Writes ``o`` (bf16, like q) and ``lse`` fp32 [B, Hq, Sq].
+    [G]) keys in the same pages: 512 or more of them are read once for all, fewer by each
+    sequence. ``max_len`` (default: all the table holds) bounds seq_lens. Writes ``o`` (bf16,
+    like q) and ``lse`` fp32 [B, Hq, Sq].
     ``workspace``: a CUDA tensor of ``attn_decode_shared_workspace_bytes`` bytes."""
     w = "attn_decode_shared"
     dev = _device(w, "q", q)

@@ -32,10 +32,13 @@
 //
 // 32 heads on 8 of 128 channels, bf16. 16 sequences of 32768 own keys: 313 us, 6.8 TB/s, the rate
 // of a copy. 64 of 4000: 168 us, 6.3 TB/s. 64 sequences behind 32768 shared keys, 700 own keys
-// each: 80 us, 4.0 TB/s and 440 TFLOP/s. There the pieces' starts and ends, and the two small
-// kernels (about 10 us), are what it takes beyond the 47 us of its bytes. A soft-cap adds 8 us to
-// the 80 of 61 ragged sequences: 16 packed operations per pair of scores, in the warps that hold
-// rows.
+// each: 80 us, 4.0 TB/s and 440 TFLOP/s, for 47 us of bytes. What it takes beyond them: three
+// dependent kernels, 14 us in a captured graph for one sequence of one key (the plan is one block,
+// the join reads every part back: with half of these keys 8 and 14 us, cold); a second reading of
+// each shared tile, out of the L2, by the second block of 128 rows (one own key each: 32 sequences
+// 49 us, 64 60); and the pieces' starts and ends. A soft-cap adds 6 us to the 80 of 61 ragged sequences of
+// fixed lengths: 16 packed operations per pair of scores, in the warps that hold rows. With a
+// window the tiles between the sequences' windows are read and multiplied, too.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -67,7 +70,9 @@ constexpr int kShPlanWarps = kShPlanThreads / 32;
 // Shared keys below this are read by each sequence itself: all but the first find them in the L2,
 // and a shared run is one more part to join. (64 sequences with 700 own keys behind 128, 256 and
 // 512 shared ones, in groups of 2: shared 52.8, 55.0, 59.0 us, by each itself 50.9, 54.3, 59.8 us;
-// in one group 48.0, 47.5, 47.8 and 46.1, 46.7, 48.5 us.)
+// in one group 48.0, 47.5, 47.8 and 46.1, 46.7, 48.5 us.) The bound knows nothing of the group's
+// size: with 50 own keys each large groups lose by it (64, 256 and 1024 sequences behind 448 keys
+// 33, 83, 258 us, with a bound of 64 24.6, 50, 163; behind 128 keys 25, 55, 168 and 23, 46, 152).
 constexpr int kShMinShared = 512;
 
 struct ShDesc {  // pieces of the same keys: one per key/value head and, of shared keys, row block

@@ -19,8 +19,8 @@
 // batches are dealt out too; there this kernel's first blocks list the pages that go, which takes
 // the tables' entries.
 //
-// 8 sequences of 32768 keys, 8 heads of 128 channels, 8192 kept: 126 us, 4.3 TB/s of the 545 MB
-// that must move. 32 of 8000, 4000 kept: 200 us, 5.3 TB/s. Rows in flight are the bound: with half
+// 8 sequences of 32768 keys, 8 heads of 128 channels, 8192 kept: 125 us, 4.4 TB/s of the 545 MB
+// that must move; into other pages 116. 32 of 8000, 4000 kept: 200 us, 5.3 TB/s. Rows in flight are the bound: with half
 // of them per block (2 pieces per thread, or 128 threads) 158 and 250 us.
 #include <cuda_runtime.h>
 
@@ -110,7 +110,7 @@ __device__ __forceinline__ void cluster_sync() {
           : "memory");
 }
 
-// The int at the same place in the shared memory of the cluster's block `rank`.
+// The same for the blocks that share a pair's batches, or the threads of the one that has them.
 __device__ __forceinline__ void ranks_sync(int ranks) {
   if (ranks > 1)
     cluster_sync();
@@ -118,6 +118,7 @@ __device__ __forceinline__ void ranks_sync(int ranks) {
     __syncthreads();
 }
 
+// The int at the same place in the shared memory of the cluster's block `rank`, and four of them.
 __device__ __forceinline__ int cluster_read(const int* p, int rank) {
   uint32_t at;
   int x;
@@ -579,8 +580,8 @@ MATTN_API attn_status attn_cache_evict(const float* weights, float* weights_out,
   a.info = info;
   const long long sms = sm_count();
   // Blocks of a pair in the selection: as long as each has 2048 keys or more and all run at once,
-  // two per SM. (8 x 32768 keys of 8 heads: 1, 2, 4, 8 blocks 152, 136, 132, 146 us for the call;
-  // 60000 keys of 8 heads 255, 113, 95, 90 us: both with a move of 512 threads, no clusters.)
+  // two per SM. (8 x 32768 keys of 8 heads: 1, 2, 4, 8 blocks 146, 129, 125, 140 us for the call;
+  // 60000 keys of 8 heads 223, 82, 65, 59 us.)
   a.select_cluster = 1;
   while (a.select_cluster < kMaxCluster && max_len >= 2 * 2048LL * a.select_cluster &&
          2 * pairs * a.select_cluster <= 2 * sms)

@@ -8,8 +8,8 @@
 // tokens of a prompt); the sum over a head's keys of its new part is its number of rows.
 //
 // Every key row is read once for all query rows of its head: 2 D bytes against 2 D products a
-// row, so HBM is the bound up to about 256 rows (group * Sq) and the tensor cores and the
-// special-function units, one exponential a score, behind that.
+// row, so HBM is the bound up to about 290 rows (group * Sq) and the tensor cores behind that; the
+// special-function units, one exponential a score, would take 390 rows in a key's time.
 //
 // Scores are computed transposed, S^T = K Q^T, on tcgen05: 128 keys are the M of a product (TMEM
 // lanes), up to 256 query rows its N. A key is then one thread's: its weight is a sum over that
@@ -22,9 +22,12 @@
 // products, and two warpgroups take turns with the tiles, so that one's exponentials run under
 // the other's product.
 //
-// 16 x 32768 keys of 8 heads of 128 channels, 4 rows each: 176 us, 6.3 TB/s of keys and weights,
-// 0.92 of a copy's rate. 8 x 40960 keys, 256 rows: 156 us, 1.1 PFLOP/s; there the exponentials
-// (144 us at 16 per clock and SM) are the bound.
+// 16 x 32768 keys of 8 heads of 128 channels, 4 rows each: 174 us, 6.4 TB/s of keys and weights,
+// 0.93 of a copy's rate. 8 x 40960 keys, 256 rows: 158 us, 1.1 PFLOP/s, for 102 us of bytes; 512
+// rows 323 us. There latency is the bound: tensor cores and special-function units are busy for a
+// third of the time each and HBM little longer (2 x 40960 keys, 59 us), while the two warps of a
+// scheduler that add the columns up wait, most of all on loads. Tiles in the masked form take
+// about three times as long (240 rows, every tile masked: 459 us).
 #include <algorithm>
 #include <climits>
 #include <cmath>
